@@ -6,8 +6,10 @@ in the library's gfx950 kernels.  There is no CPU or PyTorch fallback: if the
 library is missing or the device is not gfx950, calls raise.
 
 Names follow the C ABI: ``quantize_nf4``, ``dequant``, ``linear_fwd``,
-``linear_bwd``, ``linear_fwd_dropout``, ``linear_bwd_dropout``, ``linear_fwd_multi``, ``adamw_step``, ``adamw8_step``, ``merge``, plus ``QLoRALinearFn`` (a torch.autograd.Function whose backward
-returns gradients for X, A and B and none for the frozen NF4 weight).
+``linear_bwd``, ``linear_fwd_dropout``, ``linear_bwd_dropout``, ``linear_fwd_multi``, ``adamw_step``,
+``adamw8_step``, ``merge``, ``head_ce``, ``head_distill``, plus ``QLoRALinearFn`` (a torch.autograd.Function whose backward
+returns gradients for X, A and B and none for the frozen NF4 weight), ``HeadCEFn`` and ``HeadDistillFn``
+(the output layer's losses with their gradients).
 """
 from __future__ import annotations
 
@@ -31,6 +33,7 @@ OP_BWD = 1
 OP_FWD_DROPOUT = 2
 OP_FWD_MULTI = 3
 MAX_RANK = 128
+MAX_TARGETS = 256
 
 EXPORTED = (
     "qlora_nf4_storage",
@@ -47,6 +50,9 @@ EXPORTED = (
     "qlora_adamw_step",
     "qlora_adamw8_step",
     "qlora_merge",
+    "qlora_head_ce",
+    "qlora_head_distill",
+    "qlora_head_workspace_bytes",
     "qlora_strerror",
     "qlora_last_error",
     "qlora_timing_enable",
@@ -128,6 +134,10 @@ def load_library() -> ctypes.CDLL:
                                    ctypes.c_int),
         "qlora_adamw8_step": ([ctypes.POINTER(_Adam8Tensor), i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                ctypes.c_double, ctypes.c_double, i64, P], ctypes.c_int),
+        "qlora_head_ce": ([P, i64, P, i64, i64, P, P, P, P, P, P, sz, P], ctypes.c_int),
+        "qlora_head_distill": ([P, i64, P, i64, i64, P, P, i32, ctypes.c_float, P, P, P, P, P, sz, P], ctypes.c_int),
+        "qlora_head_workspace_bytes": ([i64, i64, i64, i32, ctypes.c_int, ctypes.c_int, ctypes.POINTER(sz)],
+                                       ctypes.c_int),
         "qlora_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "qlora_last_error": ([], ctypes.c_char_p),
         "qlora_timing_enable": ([ctypes.c_char_p, ctypes.c_int], ctypes.c_int),
@@ -558,6 +568,84 @@ def adamw8_step(params, grads, states, lr: float, step: int, beta1: float = 0.9,
            "qlora_adamw8_step")
 
 
+@functools.lru_cache(maxsize=256)
+def head_workspace_bytes(T: int, n_vocab: int, n_in: int, k: int = 0, need_dx: bool = True,
+                         need_dw: bool = False) -> int:
+    """Workspace bytes of ``head_ce`` (k = 0) and ``head_distill`` (k teacher logits per row)."""
+    b = ctypes.c_size_t()
+    _check(load_library().qlora_head_workspace_bytes(T, n_vocab, n_in, k, int(need_dx), int(need_dw), ctypes.byref(b)),
+           "qlora_head_workspace_bytes")
+    return b.value
+
+
+def _head_args(X, W, weight, k, need_dx, need_dw, ws, outs):
+    """Checked operands and outputs of the two losses: (X, W, loss, dX or None, dW or None, ws, ws bytes)."""
+    X, W = _bits(X), _bits(W)
+    _inputs(X, W, weight)
+    if W.dim() != 2 or W.shape[1] != X.shape[1]:
+        raise ValueError(f"W must be [n_vocab, {X.shape[1]}], got {tuple(W.shape)}")
+    T, dev, bf = X.shape[0], X.device, torch.bfloat16
+    if weight is not None:
+        _want(weight, (T,), torch.float32, dev, "weight")
+    if outs is None:
+        loss = torch.empty((T,), dtype=torch.float32, device=dev)
+        dX = torch.empty_like(X) if need_dx else None
+        dW = torch.empty_like(W) if need_dw else None
+    else:
+        loss, dX, dW = outs
+        _want(loss, (T,), torch.float32, dev, "loss")
+        if dX is not None:
+            _want(dX, tuple(X.shape), bf, dev, "dX")
+        if dW is not None:
+            _want(dW, tuple(W.shape), bf, dev, "dW")
+    if ws is None:
+        nb = head_workspace_bytes(T, W.shape[0], W.shape[1], k, dX is not None, dW is not None)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    else:
+        nb = _ws_bytes(ws, dev)
+    _on_gpu(X)
+    return X, W, loss, dX, dW, ws, nb
+
+
+def head_ce(X: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, weight: torch.Tensor | None = None,
+            need_dx: bool = True, need_dw: bool = False, ws: torch.Tensor | None = None, outs: tuple | None = None):
+    """Softmax cross entropy of z = X W^T (output layer W, bf16 [n_vocab, n_in]) without storing the logits.
+
+    labels int64 [T]; a label outside the vocabulary ignores its row. Returns (loss float32 [T], dX or None, dW or
+    None), the gradients of sum(weight * loss) (weight float32 [T], default 1). ``outs`` are optional preallocated
+    (loss, dX or None, dW or None), which then say which gradients are formed."""
+    if not isinstance(labels, torch.Tensor) or labels.dtype != torch.int64:
+        raise TypeError("labels must be an int64 tensor")
+    X, W, loss, dX, dW, ws, nb = _head_args(X, W, weight, 0, need_dx, need_dw, ws, outs)
+    _want(labels, (X.shape[0],), torch.int64, X.device, "labels")
+    _check(load_library().qlora_head_ce(_ptr(X), X.shape[0], _ptr(W), W.shape[0], W.shape[1], _ptr(labels),
+                                        _ptr(weight), _ptr(loss), _ptr(dX), _ptr(dW), _ptr(ws), nb,
+                                        _stream(X.device)), "qlora_head_ce")
+    return loss, dX, dW
+
+
+def head_distill(X: torch.Tensor, W: torch.Tensor, index: torch.Tensor, logit: torch.Tensor, tau: float = 1.0,
+                 weight: torch.Tensor | None = None, need_dx: bool = True, need_dw: bool = False,
+                 ws: torch.Tensor | None = None, outs: tuple | None = None):
+    """tau^2 KL(teacher's softmax over its top logits || softmax(X W^T / tau)) without storing the logits.
+
+    index int32 [T, k] and logit float32 [T, k] are the teacher's; entries outside the vocabulary (-1) or at -inf have
+    no part. Returns (loss, dX or None, dW or None) as ``head_ce`` does."""
+    for t, dt, name in ((index, torch.int32, "index"), (logit, torch.float32, "logit")):
+        if not isinstance(t, torch.Tensor) or t.dtype != dt or t.dim() != 2:
+            raise TypeError(f"{name} must be a 2-D {dt} tensor")
+    k = index.shape[1]
+    if not 1 <= k <= MAX_TARGETS:
+        raise ValueError(f"1 to {MAX_TARGETS} teacher logits per row, got {k}")
+    X, W, loss, dX, dW, ws, nb = _head_args(X, W, weight, k, need_dx, need_dw, ws, outs)
+    _want(index, (X.shape[0], k), torch.int32, X.device, "index")
+    _want(logit, (X.shape[0], k), torch.float32, X.device, "logit")
+    _check(load_library().qlora_head_distill(_ptr(X), X.shape[0], _ptr(W), W.shape[0], W.shape[1], _ptr(index),
+                                             _ptr(logit), k, float(tau), _ptr(weight), _ptr(loss), _ptr(dX), _ptr(dW),
+                                             _ptr(ws), nb, _stream(X.device)), "qlora_head_distill")
+    return loss, dX, dW
+
+
 class QLoRALinearFn(torch.autograd.Function):
     """Autograd wrapper: forward(X, w, A, B, alpha) -> Y; gradients for X, A, B only."""
 
@@ -573,6 +661,50 @@ class QLoRALinearFn(torch.autograd.Function):
         X, A, B, U = ctx.saved_tensors
         dX, dA, dB = linear_bwd(X, dY.contiguous(), ctx.w, A, B, ctx.alpha, U=U, need_dx=ctx.needs_input_grad[0])
         return dX, None, dA, dB, None
+
+
+def _head_total(ctx, loss, weight, dX, dW):
+    ctx.save_for_backward(*(t for t in (dX, dW) if t is not None))
+    ctx.have = (dX is not None, dW is not None)
+    ctx.mark_non_differentiable(loss)
+    return (loss if weight is None else loss * weight).sum(), loss
+
+
+def _head_grads(ctx, g):
+    saved = list(ctx.saved_tensors)
+    return tuple(saved.pop(0) * g if have else None for have in ctx.have)
+
+
+class HeadCEFn(torch.autograd.Function):
+    """Autograd wrapper of ``head_ce``: forward(X, W, labels, weight) -> (sum(weight * loss), loss [T]).
+
+    The gradients are formed with the losses, in one call, for those of X and W that need them; the backward
+    multiplies them by the incoming scalar. The per-token losses carry no gradient."""
+
+    @staticmethod
+    def forward(ctx, X, W, labels, weight=None):
+        loss, dX, dW = head_ce(X, W, labels, weight, need_dx=ctx.needs_input_grad[0], need_dw=ctx.needs_input_grad[1])
+        return _head_total(ctx, loss, weight, dX, dW)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g, _):
+        return *_head_grads(ctx, g), None, None
+
+
+class HeadDistillFn(torch.autograd.Function):
+    """Autograd wrapper of ``head_distill``: forward(X, W, index, logit, tau, weight) -> (sum(weight * loss), loss)."""
+
+    @staticmethod
+    def forward(ctx, X, W, index, logit, tau=1.0, weight=None):
+        loss, dX, dW = head_distill(X, W, index, logit, tau, weight, need_dx=ctx.needs_input_grad[0],
+                                    need_dw=ctx.needs_input_grad[1])
+        return _head_total(ctx, loss, weight, dX, dW)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g, _):
+        return *_head_grads(ctx, g), None, None, None, None
 
 
 def timing_enable(kernel: str, enable: bool = True):

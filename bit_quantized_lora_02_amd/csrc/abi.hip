@@ -18,6 +18,7 @@
 
 #include "adamw.h"
 #include "device.h"
+#include "head.h"
 #include "launch.h"
 #include "recip_div.h"
 #include "qlora.h"
@@ -411,6 +412,131 @@ int check_ws(int op, int64_t T, int64_t N, int64_t K, int32_t r, const void *ws,
     return fail(QLORA_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, p->total);
   if (p->total > 0 && (!ws || ((uintptr_t)ws & (kAlign - 1))))
     return fail(QLORA_EINVAL, "workspace must be non-NULL and 256-byte aligned");
+  return QLORA_OK;
+}
+
+// -------------------------------------------------- the output layer's losses
+// Rows of E (binary16-wide entries, one per vocabulary column) and their tile statistics are held for a block of
+// rows at a time, of at most this many bytes: at 4096 rows of a 131072-wide vocabulary the products run at full
+// size (256 tiles of dX), so larger blocks gain nothing and smaller ones would leave compute units idle.
+constexpr size_t kHeadBlockBytes = (size_t)1 << 30;
+
+struct HeadPlan {
+  int64_t tb = 0, blocks = 0, ntile = 0, lde = 0;
+  size_t off_n = 0, off_zero = 0, off_list = 0, off_ref = 0, off_col = 0, off_h = 0, off_zt = 0, off_pt = 0,
+         off_stat = 0, off_scale = 0, off_e = 0, off_part = 0, off_xs = 0, off_sums = 0, total = 0;
+  bool split = false;  // dX may come as partial sums
+};
+
+HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw) {
+  HeadPlan p;
+  const bool grad = dx || dw;
+  p.ntile = ceil_div(V, kHeadTile);
+  p.lde = ceil_div(V, kHeadPad) * kHeadPad;
+  const size_t row = (size_t)p.ntile * sizeof(float2) + (grad ? (size_t)p.lde * 2 : 0);
+  int64_t most = (int64_t)(kHeadBlockBytes / row) / 256 * 256;
+  most = most < 256 ? 256 : most;
+  p.blocks = T <= most ? 1 : ceil_div(T, most);
+  p.tb = p.blocks == 1 ? (T < 1 ? 1 : T) : (int64_t)up((size_t)ceil_div(T, p.blocks), 256);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = up(off + bytes, kAlign);
+    return at;
+  };
+  p.off_n = take(4);
+  p.off_zero = take(256);
+  p.off_list = take((size_t)T * 4);
+  p.off_ref = take((size_t)T * 4);
+  p.off_col = take((size_t)T * 4);
+  p.off_h = take((size_t)T * 4);
+  if (k > 0) {
+    p.off_zt = take((size_t)T * k * 4);
+    p.off_pt = take((size_t)T * k * 4);
+  }
+  p.off_stat = take((size_t)p.tb * p.ntile * sizeof(float2));
+  p.off_scale = take((size_t)p.tb * 4);
+  if (grad) p.off_e = take((size_t)p.tb * p.lde * 2);
+  if (dx) {
+    const size_t part = head_part_floats(p.tb, K, p.lde) * 4;
+    p.split = part > 0;
+    p.off_part = take(part);
+  }
+  if (dw) {
+    p.off_xs = take((size_t)p.tb * K * 2);
+    if (p.blocks > 1) p.off_sums = take((size_t)V * K * 4);
+  }
+  p.total = off;
+  return p;
+}
+
+int check_head_sizes(int64_t T, int64_t V, int64_t K) {
+  if (T < 0 || T > kMaxDim) return fail(QLORA_EINVAL, "T must be in [0, 2^22] (got %lld)", (long long)T);
+  if (V < 1 || V > kMaxDim || K < 8 || K > kMaxDim || K % 8 != 0)
+    return fail(QLORA_EINVAL, "need n_vocab >= 1 and n_in a positive multiple of 8, each at most 2^22 (got %lld x %lld)",
+                (long long)V, (long long)K);
+  if (V * K > kMaxWeights || T * K > kMaxActs)
+    return fail(QLORA_EINVAL, "n_vocab x n_in must be at most 2^34 and T x n_in below 2^32 (got T=%lld, %lld x %lld)",
+                (long long)T, (long long)V, (long long)K);
+  return QLORA_OK;
+}
+
+bool aligned_to(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// Either labels (k = 0) or index and logit (k >= 1 teacher logits per row).
+int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, int64_t K, const int64_t *labels,
+              const int32_t *index, const float *logit, int32_t k, float tau, const float *weight, float *loss,
+              qlora_bf16 *dX, qlora_bf16 *dW, void *ws, size_t ws_bytes, void *stream) {
+  int rc = check_head_sizes(T, V, K);
+  if (rc) return rc;
+  if (!W || !aligned16(W)) return fail(QLORA_EINVAL, "W must be non-NULL and 16-byte aligned");
+  if (T > 0 && (!X || !loss)) return fail(QLORA_EINVAL, "X and loss must not be NULL");
+  if (!aligned16(X) || !aligned16(dX) || !aligned16(dW))
+    return fail(QLORA_EINVAL, "X, dX and dW must be 16-byte aligned");
+  if (!aligned_to(loss, 4) || !aligned_to(weight, 4))
+    return fail(QLORA_EINVAL, "loss and weight must be 4-byte aligned");
+  const HeadPlan p = head_plan(T, V, K, k, dX != nullptr, dW != nullptr);
+  if (ws_bytes < p.total) return fail(QLORA_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, p.total);
+  if (!ws || !aligned_to(ws, kAlign)) return fail(QLORA_EINVAL, "workspace must be non-NULL and 256-byte aligned");
+  if ((rc = check_device(nullptr))) return rc;
+  if (T == 0 && !dW) return QLORA_OK;
+  hipStream_t s = (hipStream_t)stream;
+  char *w = (char *)ws;
+  int32_t *n = (int32_t *)(w + p.off_n), *list = (int32_t *)(w + p.off_list);
+  HeadRows rows;
+  rows.n = n;
+  rows.list = list;
+  rows.ref = (float *)(w + p.off_ref);
+  rows.refcol = (int32_t *)(w + p.off_col);
+  rows.h = (float *)(w + p.off_h);
+  rows.zt = k > 0 ? (float *)(w + p.off_zt) : nullptr;
+  rows.pt = k > 0 ? (float *)(w + p.off_pt) : nullptr;
+  const bool grad = dX || dW;
+  float2 *stat = (float2 *)(w + p.off_stat);
+  float *scale = (float *)(w + p.off_scale);
+  bf16_t *E = grad ? (bf16_t *)(w + p.off_e) : nullptr;
+  float *part = p.split ? (float *)(w + p.off_part) : nullptr;
+  bf16_t *Xs = dW ? (bf16_t *)(w + p.off_xs) : nullptr;
+  float *sums = p.off_sums ? (float *)(w + p.off_sums) : nullptr;
+  const bf16_t *zero = (const bf16_t *)(w + p.off_zero);
+  const float c = 1.44269504f / tau;
+  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, rows, loss, dX,
+                                       (uint32_t *)(w + p.off_zero), s));
+  for (int64_t b = 0; b < p.blocks; ++b) {
+    const int64_t row0 = b * p.tb, tb = T - row0 < p.tb ? T - row0 : p.tb;
+    if (tb > 0) {
+      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, X, W, V, K, c, stat, p.ntile, E, p.lde, zero, s));
+      LAUNCH("head_combine", launch_head_combine(rows, row0, tb, stat, p.ntile, V, labels, index, k, tau, weight, loss,
+                                                 scale, E, p.lde, X, K, Xs, s));
+      if (dX) {
+        LAUNCH("head_dx", launch_head_dx(rows, row0, tb, E, p.lde, W, V, K, scale, part, dX, s));
+        if (part) LAUNCH("head_dx_reduce", launch_head_reduce(rows, row0, tb, part, V, K, p.lde, scale, dX, s));
+      }
+    }
+    if (dW)
+      LAUNCH("head_dw",
+             launch_head_dw(rows, row0, tb, E, p.lde, Xs, V, K, zero, sums, b == 0, b + 1 == p.blocks, dW, s));
+  }
   return QLORA_OK;
 }
 
@@ -886,6 +1012,34 @@ int qlora_adamw8_step(const qlora_adamw8_tensor *tensors, int32_t count, double 
     LAUNCH("adamw8", launch_adamw8(a, blocks, s));
   }
   return QLORA_OK;
+}
+
+int qlora_head_workspace_bytes(int64_t T, int64_t n_vocab, int64_t n_in, int32_t k, int need_dx, int need_dw,
+                               size_t *bytes) {
+  if (!bytes) return fail(QLORA_EINVAL, "bytes is NULL");
+  if (int rc = check_head_sizes(T, n_vocab, n_in)) return rc;
+  if (k < 0 || k > QLORA_MAX_TARGETS) return fail(QLORA_EINVAL, "k must be in [0, %d] (got %d)", QLORA_MAX_TARGETS, (int)k);
+  *bytes = head_plan(T, n_vocab, n_in, k, need_dx != 0, need_dw != 0).total;
+  return QLORA_OK;
+}
+
+int qlora_head_ce(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t n_vocab, int64_t n_in,
+                  const int64_t *labels, const float *weight, float *loss, qlora_bf16 *dX, qlora_bf16 *dW, void *ws,
+                  size_t ws_bytes, void *stream) {
+  if (T > 0 && !labels) return fail(QLORA_EINVAL, "labels must not be NULL");
+  if (!aligned_to(labels, 8)) return fail(QLORA_EINVAL, "labels must be 8-byte aligned");
+  return head_loss(X, T, W, n_vocab, n_in, labels, nullptr, nullptr, 0, 1.f, weight, loss, dX, dW, ws, ws_bytes,
+                   stream);
+}
+
+int qlora_head_distill(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t n_vocab, int64_t n_in,
+                       const int32_t *index, const float *logit, int32_t k, float tau, const float *weight,
+                       float *loss, qlora_bf16 *dX, qlora_bf16 *dW, void *ws, size_t ws_bytes, void *stream) {
+  if (k < 1 || k > QLORA_MAX_TARGETS) return fail(QLORA_EINVAL, "k must be in [1, %d] (got %d)", QLORA_MAX_TARGETS, (int)k);
+  if (!(tau > 0.f) || !isfinite(tau)) return fail(QLORA_EINVAL, "tau must be positive and finite (got %g)", (double)tau);
+  if (T > 0 && (!index || !logit)) return fail(QLORA_EINVAL, "index and logit must not be NULL");
+  if (!aligned_to(index, 4) || !aligned_to(logit, 4)) return fail(QLORA_EINVAL, "index and logit must be 4-byte aligned");
+  return head_loss(X, T, W, n_vocab, n_in, nullptr, index, logit, k, tau, weight, loss, dX, dW, ws, ws_bytes, stream);
 }
 
 int qlora_timing_enable(const char *kernel, int enable) {

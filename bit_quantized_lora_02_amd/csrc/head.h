@@ -1,0 +1,82 @@
+// head.h -- sizes and tables shared by the output layer's loss kernels (head_gemm.hip, head_loss.hip) and the
+// C ABI (internal to the library).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qlora {
+
+typedef uint16_t bf16_t;
+
+// One loss over the output layer z = X W^T: the rows that count, their targets, and what the kernels hand on.
+//
+// The rows of X that count (a target inside the vocabulary) are numbered 0 .. n-1 in the order of X; `list` gives
+// row i's place in X.  Work goes by blocks of `tb` such rows.  With c = log2(e) / tau, a row's unit u is its first
+// target's logit ref = z[refcol] (or, where some logit is so far above it that bf16 would overflow, a larger one),
+// and E[v] = exp2((z[v] - u) c) is what is kept of logit v.
+struct HeadRows {
+  const int32_t *n;     // rows that count
+  const int32_t *list;  // [T] their rows in X
+  float *ref;           // [T] by row of X: the logit of the row's first target
+  int32_t *refcol;      // [T] by row of X: that target's column
+  float *h;             // [T] by row of X: sum_i p_i (log p_i - (z_i - ref) / tau); 0 for a one-hot target
+  float *zt;            // [T][k] logits of the k targets (NULL: one target)
+  float *pt;            // [T][k] their probabilities (NULL: one target)
+};
+
+// Columns of W (rows of the output layer) per tile of the logit product, and the row statistics' unit.
+constexpr int kHeadTile = 256;
+// Rows of E are padded with zero columns to a multiple of this.
+constexpr int kHeadPad = 64;
+// A logit may exceed the row's reference by 2^kHeadRange before the tile takes a unit of its own.
+constexpr float kHeadRange = 40.f;
+
+// Reduction ranges of the dX product: `tiles` output tiles of `steps` 64-deep steps on `slots` workgroups that run
+// at once.  A round of workgroups costs its steps plus about 10 (first loads, output); more than one range also
+// costs the binary32 partial sums, written and read once: about 33 steps' time for 256 tiles of 256 x 256.
+__host__ __device__ inline int head_split(int64_t tiles, int64_t steps, int slots, int tile_elems) {
+  int best = 1;
+  float best_cost = 3.4e38f;
+  for (int s = 1; s <= 16 && (s == 1 || steps / s >= 8); ++s) {
+    const float rounds = (float)((tiles * s + slots - 1) / slots);
+    const float cost = rounds * (float)((steps + s - 1) / s + 10) +
+                       (s > 1 ? 33.f * (float)(tiles * s) * (float)tile_elems / (256.f * 65536.f) : 0.f);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t V, int64_t K, const int64_t *labels,
+                            const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
+                            const HeadRows &rows, float *loss, bf16_t *dX, uint32_t *zero, hipStream_t s);
+hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
+                               int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
+                               const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde,
+                               const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s);
+hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t V, int64_t K,
+                              int64_t lde, const float *scale, bf16_t *dX, hipStream_t s);
+
+// Rows of X per tile of the three products for blocks of at most `tb` rows.
+int head_tile_rows(int64_t tb);
+// Largest size in floats of the dX product's partial sums over all row counts up to tb (0: never split).
+size_t head_part_floats(int64_t tb, int64_t K, int64_t lde);
+// Ranges of the dX product of n rows.
+__host__ __device__ inline int head_dx_ranges(int64_t n, int64_t K, int64_t lde, int tile_rows) {
+  const int64_t tiles = ((n + tile_rows - 1) / tile_rows) * ((K + 255) / 256);
+  return head_split(tiles, lde / 64, tile_rows == 64 ? 512 : 256, 256 * tile_rows);
+}
+
+hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *X, const bf16_t *W,
+                              int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E, int64_t lde,
+                              const bf16_t *zero, hipStream_t s);
+hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde,
+                          const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
+                          hipStream_t s);
+hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde,
+                          const bf16_t *Xs, int64_t V, int64_t K, const bf16_t *zero, float *acc, bool first,
+                          bool last, bf16_t *dW, hipStream_t s);
+
+}  // namespace qlora

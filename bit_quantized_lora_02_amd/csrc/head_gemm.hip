@@ -1,0 +1,483 @@
+// head_gemm.hip -- the three products of the output layer's losses on bf16 MFMAs:
+//
+//   logits   z = X W^T       per tile: softmax statistics, and E = exp2((z - u) c) in bf16 (never z itself)
+//   dX       dX = f o (E W)  reduction over the vocabulary, f the rows' factors
+//   dW       dW = E^T (f o X)  reduction over the rows
+//
+// (E with its targets' entries put in by k_head_combine; see head_loss.hip for the mathematics.)
+//
+// One kernel body serves all three: C[n][m] = sum_r A(m, r) B(n, r), the operands read from global memory either
+// along the reduction ("rows": [m][r]) or across it ("transposed": [r][m]).  A workgroup of 8 waves computes a
+// 256 x BN tile with v_mfma_f32_32x32x16_bf16; m is the MFMA's row index, so a lane holds four consecutive m of
+// one n, which makes the softmax statistics of a row of X (n) a reduction inside the lane.  The reduction runs in
+// 64-deep steps: both tiles of step s + 2 are copied global -> LDS by the load unit (16 bytes per lane) while
+// step s + 1 is multiplied, two buffers, one barrier per step.  The barrier sits before the last quarter of a
+// step's MFMAs, whose operands are in registers by then, and the first operands of the next step are read under
+// them, so that the matrix unit has work while the waves meet.
+//
+// LDS tiles: "rows" [row][64] with the 16-byte chunk index XOR-swizzled by (row / 2) % 8; "transposed" [64][cols]
+// with the 64-byte groups of a row XOR-swizzled by row % 4 (a transposing read takes four rows at once), both
+// conflict-free; the direct copies write lane-consecutive LDS, so the swizzle is applied to the source address.
+#include <type_traits>
+
+#include "device.h"
+#include "head.h"
+#include "launch.h"
+
+namespace qlora {
+
+namespace {
+
+constexpr int BK = 64;
+constexpr int BM = kHeadTile;
+
+template <int WAVES_M_, int WAVES_N_, int WM_, int WN_>
+struct HeadCfg {
+  static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WM = WM_, WN = WN_;
+  static constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
+  static constexpr int BN = WAVES_N * WN * 32;
+  static_assert(WAVES_M * WM * 32 == BM, "tiles are 256 wide");
+};
+using H256 = HeadCfg<2, 4, 4, 2>;  // 128 x 64 per wave
+using H128 = HeadCfg<4, 2, 2, 2>;  // 64 x 64 per wave
+using H64 = HeadCfg<8, 1, 1, 2>;   // 32 x 64 per wave
+
+__device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0); }
+
+// Where an operand's tile comes from: ROWS rows (or columns, transposed) of a row-major matrix.
+//  rows:       element (i, r) at base + row(i) ld + r; row(i) gathered through `list` or first + i, clamped to the
+//              last one; r >= red reads `zero`.
+//  transposed: element (i, r) at base + r ld + first + i; columns clamped to the last chunk; r >= red reads `zero`
+//              if there is one, else the last row (the other operand is zero there).
+template <int ROWS, int NT, bool TR>
+struct Tile {
+  static constexpr int LD = ROWS * 8 / NT;  // 16-byte copies per thread and step
+  static_assert(ROWS * 8 % NT == 0 && LD >= 1, "unsupported tile");
+  const bf16_t *src[TR ? 1 : LD];
+  int col[LD], row[LD];
+  int64_t ld, red;
+  const bf16_t *zero;
+  int wave;
+
+  __device__ __forceinline__ void init(const bf16_t *base, int64_t ld_, int64_t first, int64_t count, int64_t red_,
+                                       const int32_t *list, const bf16_t *zero_, int w, int lane) {
+    ld = ld_, red = red_, zero = zero_, wave = w;
+    if constexpr (TR) src[0] = base;
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int g = i * (NT / 64) + w;  // 1 KB piece of the tile
+      if constexpr (!TR) {
+        const int rr = 8 * g + (lane >> 3);
+        int64_t at = first + rr < count ? first + rr : count - 1;
+        if (list) at = list[at];
+        src[i] = base + at * ld;
+        col[i] = 8 * ((lane & 7) ^ ((rr >> 1) & 7));
+        row[i] = 0;
+      } else {
+        constexpr int CH = ROWS / 8;  // 16-byte chunks per LDS row
+        const int rr = g * (64 / CH) + lane / CH;
+        const int chunk = (lane % CH) ^ (swz(rr) << 2);
+        int64_t c = first + 8 * chunk;
+        if (c > count - 8) c = count - 8;  // count % 8 == 0
+        col[i] = (int)c;
+        row[i] = rr;
+      }
+    }
+  }
+  // XOR of the 64-byte group index of LDS row r: rows r .. r + 3 then start in different quarters of the 64 banks
+  static __device__ __forceinline__ int swz(int r) { return ROWS >= 128 ? (r & 3) : ((r >> 1) & 1); }
+
+  __device__ __forceinline__ void issue(int64_t step, bf16_t *s) const {
+    const int64_t r0 = step * BK;
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const bf16_t *p;
+      if constexpr (!TR) {
+        const int64_t c = r0 + col[i];
+        p = c < red ? src[i] + c : zero;
+      } else {
+        const int64_t r = r0 + row[i];
+        p = r < red ? src[0] + r * ld + col[i] : (zero ? zero : src[0] + (red - 1) * ld + col[i]);
+      }
+      __builtin_amdgcn_global_load_lds((const void *)p,
+                                       (__attribute__((address_space(3))) void *)(s + (i * (NT / 64) + wave) * 512),
+                                       16, 0, 0);
+    }
+  }
+  // MFMA operand of the 32 rows from `at`, reduction 16 kk .. 16 kk + 15 of the step
+  static __device__ __forceinline__ u32x4_t read(const bf16_t *s, int at, int kk, int lane) {
+    if constexpr (!TR) {
+      const int r = at + (lane & 31), chunk = kk * 2 + (lane >> 5);
+      return *reinterpret_cast<const u32x4_t *>(s + r * BK + ((chunk ^ ((r >> 1) & 7)) << 3));
+    } else {
+      // In each 16-lane group, lane i of a transposing read gets element (i & 3) of the 8 bytes addressed by lane
+      // 4 m + (i >> 2): lane a points at row base + (a >> 2), columns 4 (a & 3) .. + 3, and the reads of rows + 0..3
+      // and + 4..7 give its 8 reduction values.
+      typedef short s4_t __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s4_t lds_s4;
+      const int grp = lane >> 4, ai = lane & 15;
+      const int r = kk * 16 + 8 * (grp >> 1) + (ai >> 2);
+      const int c = at + 16 * (grp & 1) + 4 * (ai & 3);
+      const int off = r * ROWS + (c ^ (swz(r) << 5));  // r and r + 4 have the same swizzle
+      const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(s + off));
+      const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(s + off + 4 * ROWS));
+      const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+      return u32x4_t{l2.x, l2.y, h2.x, h2.y};
+    }
+  }
+};
+
+template <class C>
+using Acc = f32x16_t[C::WM][C::WN];
+
+// The reduction over steps [s0, s1) into acc.
+template <class C, bool TA, bool TB>
+__device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, TA> &ta, const Tile<C::BN, C::NT, TB> &tb, int64_t s0,
+                                             int64_t s1, bf16_t *a0, bf16_t *a1, bf16_t *b0, bf16_t *b1, int wm, int wn,
+                                             int lane, Acc<C> &acc) {
+  typedef Tile<BM, C::NT, TA> TileA;
+  typedef Tile<C::BN, C::NT, TB> TileB;
+#pragma unroll
+  for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::WN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  if (s0 >= s1) return;
+  bf16_t *const sa[2] = {a0, a1};
+  bf16_t *const sb[2] = {b0, b1};
+  u32x4_t a[2][C::WM], b[2][C::WN];
+  auto read = [&](const bf16_t *pa, const bf16_t *pb, int kk, u32x4_t(&av)[C::WM], u32x4_t(&bv)[C::WN]) {
+#pragma unroll
+    for (int i = 0; i < C::WM; ++i) av[i] = TileA::read(pa, (wm * C::WM + i) * 32, kk, lane);
+#pragma unroll
+    for (int j = 0; j < C::WN; ++j) bv[j] = TileB::read(pb, (wn * C::WN + j) * 32, kk, lane);
+  };
+  auto mma = [&](const u32x4_t(&av)[C::WM], const u32x4_t(&bv)[C::WN]) {
+#pragma unroll
+    for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::WN; ++j) acc[i][j] = mfma_32x32x16(av[i], bv[j], acc[i][j]);
+  };
+  ta.issue(s0, sa[0]);
+  tb.issue(s0, sb[0]);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+  __syncthreads();
+  if (s0 + 1 < s1) {
+    ta.issue(s0 + 1, sa[1]);
+    tb.issue(s0 + 1, sb[1]);
+  }
+  read(sa[0], sb[0], 0, a[0], b[0]);
+  auto step = [&](auto pc, int64_t s) {
+    constexpr int P = decltype(pc)::value;
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      read(sa[P], sb[P], kk + 1, a[(kk + 1) & 1], b[(kk + 1) & 1]);
+      fence_sched();
+      mma(a[kk & 1], b[kk & 1]);
+      fence_sched();
+    }
+    // every wave holds the step's last operands; the next step's tiles have landed
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __syncthreads();
+    if (s + 2 < s1) {
+      ta.issue(s + 2, sa[P]);
+      tb.issue(s + 2, sb[P]);
+    }
+    if (s + 1 < s1) read(sa[P ^ 1], sb[P ^ 1], 0, a[0], b[0]);
+    fence_sched();
+    mma(a[1], b[1]);
+    fence_sched();
+  };
+  int64_t s = s0;
+  for (; s + 1 < s1; s += 2) {
+    step(std::integral_constant<int, 0>(), s);
+    step(std::integral_constant<int, 1>(), s + 1);
+  }
+  if (s < s1) step(std::integral_constant<int, 0>(), s);
+  __syncthreads();  // the buffers may be reused
+}
+
+// Work item of this workgroup: items are numbered so that each XCD (workgroups go round the 8 XCDs) takes a run of
+// consecutive ones, and consecutive ones are blocks of 4 m-tiles x all n-tiles: the 32 workgroups of an XCD then
+// share 4 + 8 operand tiles.
+struct Item {
+  int64_t m, n;
+  int range;
+};
+__device__ __forceinline__ bool item_of(int64_t tiles_m, int64_t tiles_n, int ranges, Item *it) {
+  const int64_t total = tiles_m * tiles_n * ranges, per = (total + 7) / 8;
+  const int64_t lin = blockIdx.x, id = (lin & 7) * per + (lin >> 3);
+  if ((lin >> 3) >= per || id >= total) return false;
+  const int64_t in = id % (tiles_m * tiles_n);
+  it->range = (int)(id / (tiles_m * tiles_n));
+  const int64_t band = in / (4 * tiles_n), left = in % (4 * tiles_n);
+  const int64_t wide = tiles_m - band * 4 < 4 ? tiles_m - band * 4 : 4;
+  it->m = band * 4 + left % wide;
+  it->n = left / wide;
+  return true;
+}
+
+__device__ __forceinline__ int64_t block_rows(const HeadRows &rows, int64_t row0, int64_t tb) {
+  const int64_t n = *rows.n - row0;
+  return n < tb ? n : tb;
+}
+
+// ------------------------------------------------------------------ logits
+// m: columns of the vocabulary, n: counted rows of the block.
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t row0, int64_t tb,
+                                                       const bf16_t *__restrict__ X, const bf16_t *__restrict__ W,
+                                                       int64_t V, int64_t K, float c, float2 *__restrict__ stat,
+                                                       int64_t ntile, bf16_t *__restrict__ E, int64_t lde,
+                                                       const bf16_t *__restrict__ zero) {
+  __shared__ __attribute__((aligned(16))) bf16_t a0[BM * BK], a1[BM * BK], b0[C::BN * BK], b1[C::BN * BK];
+  __shared__ float s_max[C::WAVES_M][C::BN], s_sum[C::WAVES_M][C::BN];
+  const int64_t n = block_rows(rows, row0, tb);
+  if (n <= 0) return;
+  Item it;
+  if (!item_of(ntile, (n + C::BN - 1) / C::BN, 1, &it)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
+  Tile<BM, C::NT, false> ta;
+  Tile<C::BN, C::NT, false> tbl;
+  ta.init(W, K, m0, V, K, nullptr, zero, wave, lane);
+  tbl.init(X, K, n0, n, K, rows.list + row0, zero, wave, lane);
+  f32x16_t acc[C::WM][C::WN];
+  reduce_steps<C, false, false>(ta, tbl, 0, (K + BK - 1) / BK, a0, a1, b0, b1, wm, wn, lane, acc);
+
+  // element e of acc[i][j]: column m0 + mi + 8 (e / 4) + e % 4, row n0 + nj (nj per lane)
+  const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
+  float ref[C::WN];
+#pragma unroll
+  for (int j = 0; j < C::WN; ++j) {
+    const int nj = (wn * C::WN + j) * 32 + (lane & 31);
+    const int64_t row = n0 + nj < n ? n0 + nj : n - 1;
+    const int64_t t = rows.list[row0 + row];
+    ref[j] = rows.ref[t];
+    const int64_t rc = rows.refcol[t] - m0;  // the reference's own column stays out of the sums
+    if (__any((rc >= 0 && rc < BM) || m0 + BM > V)) {
+#pragma unroll
+      for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int m = mlane + 32 * i + 8 * (e >> 2) + (e & 3);
+          if (m == rc || m0 + m >= V) acc[i][j][e] = -INFINITY;
+        }
+    }
+    float top = acc[0][j][0];
+#pragma unroll
+    for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (lane < 32) s_max[wm][nj] = top;
+  }
+  __syncthreads();
+  // 64 rows of 256 columns each (the narrow tiles use the first ones)
+  auto stage = [&](int i) { return i == 0 ? a0 : i == 1 ? a1 : i == 2 ? b0 : b1; };
+#pragma unroll
+  for (int j = 0; j < C::WN; ++j) {
+    const int nj = (wn * C::WN + j) * 32 + (lane & 31);
+    float top = s_max[0][nj];
+#pragma unroll
+    for (int w = 1; w < C::WAVES_M; ++w) top = fmaxf(top, s_max[w][nj]);
+    const float u = (top - ref[j]) * c > kHeadRange ? top : ref[j];
+    float sum = 0.f;
+    bf16_t *const srow = stage(nj >> 6) + (nj & 63) * BM;
+#pragma unroll
+    for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = __builtin_amdgcn_exp2f((acc[i][j][4 * q + e] - u) * c);
+          sum += p[e];
+        }
+        if (E) {  // 16-byte chunk index swizzled by the row: conflict-free here and in the row-wise reads below
+          const int m = mlane + 32 * i + 8 * q;
+          *reinterpret_cast<u32x2_t *>(srow + ((((m >> 3) ^ nj) & 31) << 3) + (m & 7)) =
+              u32x2_t{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
+        }
+      }
+    sum += __shfl_xor(sum, 32);
+    if (lane < 32) s_sum[wm][nj] = sum;
+  }
+  __syncthreads();
+  if (tid < C::BN && n0 + tid < n) {
+    float top = s_max[0][tid], sum = s_sum[0][tid];
+#pragma unroll
+    for (int w = 1; w < C::WAVES_M; ++w) top = fmaxf(top, s_max[w][tid]), sum += s_sum[w][tid];
+    const float r = rows.ref[rows.list[row0 + n0 + tid]];
+    stat[(n0 + tid) * ntile + it.m] = make_float2((top - r) * c > kHeadRange ? top : r, sum);
+  }
+  if (!E) return;
+  for (int at = tid; at < C::BN * 32; at += C::NT) {
+    const int nj = at >> 5, chunk = at & 31;
+    if (n0 + nj >= n || m0 + chunk * 8 >= lde) continue;
+    *reinterpret_cast<u32x4_t *>(E + (n0 + nj) * lde + m0 + chunk * 8) =
+        *reinterpret_cast<const u32x4_t *>(stage(nj >> 6) + (nj & 63) * BM + (((chunk ^ nj) & 31) << 3));
+  }
+}
+
+// ---------------------------------------------------------------------- dX
+// m: columns of X, n: counted rows of the block; reduction over the vocabulary (lde of it: E is zero past V).
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, int64_t tb,
+                                                   const bf16_t *__restrict__ E, int64_t lde,
+                                                   const bf16_t *__restrict__ W, int64_t V, int64_t K,
+                                                   const float *__restrict__ scale, float *__restrict__ part,
+                                                   bf16_t *__restrict__ dX) {
+  __shared__ __attribute__((aligned(16))) bf16_t a0[BM * BK], a1[BM * BK], b0[C::BN * BK], b1[C::BN * BK];
+  const int64_t n = block_rows(rows, row0, tb);
+  if (n <= 0) return;
+  const int ranges = head_dx_ranges(n, K, lde, C::BN);
+  Item it;
+  if (!item_of((K + BM - 1) / BM, (n + C::BN - 1) / C::BN, ranges, &it)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
+  const int64_t steps = lde / BK, per = (steps + ranges - 1) / ranges;
+  const int64_t s0 = it.range * per, s1 = s0 + per < steps ? s0 + per : steps;
+  Tile<BM, C::NT, true> ta;
+  Tile<C::BN, C::NT, false> tbl;
+  ta.init(W, K, m0, K, V, nullptr, nullptr, wave, lane);
+  tbl.init(E, lde, n0, n, lde, nullptr, nullptr, wave, lane);
+  f32x16_t acc[C::WM][C::WN];
+  reduce_steps<C, true, false>(ta, tbl, s0, s1, a0, a1, b0, b1, wm, wn, lane, acc);
+#pragma unroll
+  for (int j = 0; j < C::WN; ++j) {
+    const int64_t i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
+    if (i >= n) continue;
+    const float f = ranges > 1 ? 1.f : scale[i];
+    bf16_t *const out = dX + (int64_t)rows.list[row0 + i] * K;
+    float *const psum = part + (it.range * n + i) * K;
+#pragma unroll
+    for (int mi = 0; mi < C::WM; ++mi)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t m = m0 + (wm * C::WM + mi) * 32 + 8 * q + 4 * (lane >> 5);
+        if (m >= K) continue;  // K % 8 == 0: four columns are all in or all out
+        const f32x16_t &v = acc[mi][j];
+        if (ranges > 1)
+          *reinterpret_cast<float4 *>(psum + m) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        else
+          *reinterpret_cast<u32x2_t *>(out + m) =
+              u32x2_t{pack_bf16x2(v[4 * q] * f, v[4 * q + 1] * f), pack_bf16x2(v[4 * q + 2] * f, v[4 * q + 3] * f)};
+      }
+  }
+}
+
+// ---------------------------------------------------------------------- dW
+// m: columns of X, n: columns of the vocabulary; reduction over the block's counted rows.  With `sums` (several
+// blocks) the binary32 sums are carried in it from block to block and rounded to dW after the last.
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, int64_t tb,
+                                                   const bf16_t *__restrict__ E, int64_t lde,
+                                                   const bf16_t *__restrict__ Xs, int64_t V, int64_t K,
+                                                   const bf16_t *__restrict__ zero, float *__restrict__ sums,
+                                                   int first, int last, bf16_t *__restrict__ dW) {
+  __shared__ __attribute__((aligned(16))) bf16_t a0[BM * BK], a1[BM * BK], b0[C::BN * BK], b1[C::BN * BK];
+  const int64_t n = block_rows(rows, row0, tb) < 0 ? 0 : block_rows(rows, row0, tb);
+  Item it;
+  if (!item_of((K + BM - 1) / BM, (V + C::BN - 1) / C::BN, 1, &it)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
+  Tile<BM, C::NT, true> ta;
+  Tile<C::BN, C::NT, true> tbl;
+  ta.init(Xs, K, m0, K, n, nullptr, zero, wave, lane);
+  tbl.init(E, lde, n0, lde, n, nullptr, zero, wave, lane);
+  f32x16_t acc[C::WM][C::WN];
+  reduce_steps<C, true, true>(ta, tbl, 0, (n + BK - 1) / BK, a0, a1, b0, b1, wm, wn, lane, acc);
+#pragma unroll
+  for (int j = 0; j < C::WN; ++j) {
+    const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 31);
+    if (v >= V) continue;
+#pragma unroll
+    for (int mi = 0; mi < C::WM; ++mi)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t m = m0 + (wm * C::WM + mi) * 32 + 8 * q + 4 * (lane >> 5);
+        if (m >= K) continue;
+        float4 o = make_float4(acc[mi][j][4 * q], acc[mi][j][4 * q + 1], acc[mi][j][4 * q + 2], acc[mi][j][4 * q + 3]);
+        if (sums) {
+          float4 *const p = reinterpret_cast<float4 *>(sums + v * K + m);
+          if (!first) {
+            const float4 was = *p;
+            o = make_float4(o.x + was.x, o.y + was.y, o.z + was.z, o.w + was.w);
+          }
+          if (!last) {
+            *p = o;
+            continue;
+          }
+        }
+        *reinterpret_cast<u32x2_t *>(dW + v * K + m) = u32x2_t{pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w)};
+      }
+  }
+}
+
+int64_t items8(int64_t items) { return (items + 7) / 8 * 8; }  // every XCD's run has the same length
+
+}  // namespace
+
+// Few rows take narrow tiles: the padding rows' MFMA work would cost more than the wider tile's operand reuse gains.
+int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
+
+size_t head_part_floats(int64_t tb, int64_t K, int64_t lde) {
+  const int bn = head_tile_rows(tb);
+  size_t most = 0;
+  for (int64_t n = tb;; n = (n - 1) / bn * bn) {  // the largest row count of each number of tiles
+    const int s = head_dx_ranges(n, K, lde, bn);
+    const size_t need = s > 1 ? (size_t)s * n * K : 0;
+    most = need > most ? need : most;
+    if (n <= bn) return most;
+  }
+}
+
+#define QLORA_HEAD_TILES(rows_, CALL)   \
+  switch (head_tile_rows(rows_)) {      \
+    case 64: CALL(H64); break;          \
+    case 128: CALL(H128); break;        \
+    default: CALL(H256); break;         \
+  }
+
+hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *X, const bf16_t *W,
+                              int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E, int64_t lde,
+                              const bf16_t *zero, hipStream_t s) {
+#define QLORA_CALL(CFG)                                                                                             \
+  launch(k_head_logits<CFG>, dim3((unsigned)items8(ntile * ((tb + CFG::BN - 1) / CFG::BN))), dim3(CFG::NT), 0, s, rows, row0, \
+         tb, X, W, V, K, c, stat, ntile, E, lde, zero)
+  QLORA_HEAD_TILES(tb, QLORA_CALL)
+#undef QLORA_CALL
+  return hipGetLastError();
+}
+
+hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde,
+                          const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
+                          hipStream_t s) {
+  const int bn = head_tile_rows(tb);
+  int64_t most = 0;  // workgroups over all row counts of the block (the kernel takes as many as the count needs)
+  for (int64_t t = 1; t <= (tb + bn - 1) / bn; ++t) {
+    const int64_t items = t * ((K + BM - 1) / BM) * head_dx_ranges(t * bn, K, lde, bn);
+    most = items > most ? items : most;
+  }
+#define QLORA_CALL(CFG)                                                                                          \
+  launch(k_head_dx<CFG>, dim3((unsigned)items8(most)), dim3(CFG::NT), 0, s, rows, row0, tb, E, lde, W, V, K, scale, part, \
+         dX)
+  QLORA_HEAD_TILES(tb, QLORA_CALL)
+#undef QLORA_CALL
+  return hipGetLastError();
+}
+
+hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde,
+                          const bf16_t *Xs, int64_t V, int64_t K, const bf16_t *zero, float *sums, bool first,
+                          bool last, bf16_t *dW, hipStream_t s) {
+  launch(k_head_dw<H256>, dim3((unsigned)items8(((K + BM - 1) / BM) * ((V + 255) / 256))), dim3(H256::NT), 0, s, rows,
+         row0, tb, E, lde, Xs, V, K, zero, sums, first ? 1 : 0, last ? 1 : 0, dW);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

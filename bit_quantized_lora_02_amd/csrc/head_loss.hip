@@ -1,0 +1,327 @@
+// head_loss.hip -- the row-wise kernels of the output layer's losses: which rows count and their targets' logits
+// (k_head_prep), the loss, the row's factor and the targets' gradient (k_head_combine), and the sum of the dX
+// product's partial sums (k_head_reduce).
+//
+// For a row with logits z, targets v_i with probabilities p_i (one target with p = 1: cross entropy), temperature
+// tau and c = log2(e) / tau, everything is taken against the first target r (the most probable one):
+//   -log q_r = log(sum_v exp((z_v - z_r) / tau)) = log1p(rest),  rest = sum over v != r
+//   loss = tau^2 (sum_i p_i (log p_i - (z_i - z_r) / tau) + log1p(rest)),
+// which keeps the digits of a loss near zero, where log-sum-exp minus z_r would cancel.  With the row's unit u = z_r,
+// E_v = exp2((z_v - u) c) and S = 1 + rest, the gradient by the logits is
+//   G_v = w tau (q_v - P_v) = (w tau / S) (E_v - S P_v),   P_v = sum of the p_i whose target is v,
+// so the product kernels take E with only the targets' entries replaced by E_v - S P_v (at r: (1 - P_r) - P_r rest,
+// again without cancellation), and the row factor w tau / S is applied in binary32 afterwards.
+#include "device.h"
+#include "head.h"
+#include "launch.h"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kPrepThreads = 256;
+constexpr int kScanRows = 16;  // consecutive rows per thread and pass of the numbering
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
+  return x;
+}
+
+__device__ __forceinline__ bool target_ok(int64_t v, int64_t V) { return v >= 0 && v < V; }
+
+// A row of a distillation batch counts if one of its targets is inside the vocabulary with a logit above -inf.
+__device__ __forceinline__ bool row_counts(const int64_t *__restrict__ labels, const int32_t *__restrict__ index,
+                                           const float *__restrict__ logit, int k, int64_t V, int64_t t) {
+  if (labels) return target_ok(labels[t], V);
+  for (int i = 0; i < k; ++i)
+    if (target_ok(index[t * k + i], V) && logit[t * k + i] > -INFINITY) return true;
+  return false;
+}
+
+// Sum over this lane's share of x . w (16-byte pieces lane, lane + 64, ...) for N rows w at once.
+template <int N>
+__device__ __forceinline__ void dots(const bf16_t *__restrict__ x, const bf16_t *const (&w)[N], int64_t K, int lane,
+                                     float (&out)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) out[j] = 0.f;
+  for (int64_t at = 8 * lane; at < K; at += 512) {
+    const u32x4_t xv = *reinterpret_cast<const u32x4_t *>(x + at);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const u32x4_t wv = *reinterpret_cast<const u32x4_t *>(w[j] + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        out[j] = fmaf(bf16_lo_to_f32(xv[e]), bf16_lo_to_f32(wv[e]), out[j]);
+        out[j] = fmaf(bf16_hi_to_f32(xv[e]), bf16_hi_to_f32(wv[e]), out[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) out[j] = wave_sum(out[j]);
+}
+
+// Workgroup 0 numbers the rows that count, in order; the others take rows of X (cross entropy: one per wave,
+// distillation: one per workgroup): the targets' logits by dot products (binary32 FMA), the teacher's softmax, or,
+// for a row that does not count, its zeros.
+__global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__restrict__ X, int64_t T,
+                                                            const bf16_t *__restrict__ W, int64_t V, int64_t K,
+                                                            const int64_t *__restrict__ labels,
+                                                            const int32_t *__restrict__ index,
+                                                            const float *__restrict__ logit, int k, float tau,
+                                                            int32_t *__restrict__ n, int32_t *__restrict__ list,
+                                                            HeadRows rows, float *__restrict__ loss,
+                                                            bf16_t *__restrict__ dX, uint32_t *__restrict__ zero) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (blockIdx.x == 0) {
+    __shared__ int s_wave[kPrepThreads / 64];
+    if (tid < 64) zero[tid] = 0u;
+    int base = 0;
+    for (int64_t t0 = 0; t0 < T; t0 += kPrepThreads * kScanRows) {
+      const int64_t mine = t0 + (int64_t)tid * kScanRows;
+      uint32_t bits = 0;
+#pragma unroll
+      for (int j = 0; j < kScanRows; ++j)
+        if (mine + j < T && row_counts(labels, index, logit, k, V, mine + j)) bits |= 1u << j;
+      int before = __popc(bits);  // inclusive sum over the wave, then over the waves
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(before, o);
+        if (lane >= o) before += up;
+      }
+      if (lane == 63) s_wave[wave] = before;
+      __syncthreads();
+      int total = 0;
+#pragma unroll
+      for (int w = 0; w < kPrepThreads / 64; ++w) {
+        if (w < wave) before += s_wave[w];
+        total += s_wave[w];
+      }
+      int at = base + before - __popc(bits);
+#pragma unroll
+      for (int j = 0; j < kScanRows; ++j)
+        if (bits >> j & 1) list[at++] = (int32_t)(mine + j);
+      base += total;
+      __syncthreads();
+    }
+    if (tid == 0) *n = base;
+    return;
+  }
+  if (labels) {
+    const int64_t t = (int64_t)(blockIdx.x - 1) * (kPrepThreads / 64) + wave;
+    if (t >= T) return;
+    const int64_t y = labels[t];
+    if (target_ok(y, V)) {
+      const bf16_t *const w[1] = {W + y * K};
+      float z[1];
+      dots<1>(X + t * K, w, K, lane, z);
+      if (lane == 0) {
+        rows.ref[t] = z[0];
+        rows.refcol[t] = (int32_t)y;
+        rows.h[t] = 0.f;
+      }
+    } else {
+      if (lane == 0) loss[t] = 0.f;
+      if (dX)
+        for (int64_t at = 8 * lane; at < K; at += 512)
+          *reinterpret_cast<u32x4_t *>(dX + t * K + at) = u32x4_t{0u, 0u, 0u, 0u};
+    }
+    return;
+  }
+  __shared__ float s_z[256];
+  const int64_t t = blockIdx.x - 1;
+  const int32_t *idx = index + t * k;
+  for (int i0 = 4 * wave; i0 < k; i0 += 4 * (kPrepThreads / 64)) {
+    const bf16_t *w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t v = i0 + j < k ? idx[i0 + j] : 0;
+      w[j] = W + (target_ok(v, V) ? v : 0) * K;
+    }
+    const bf16_t *const wc[4] = {w[0], w[1], w[2], w[3]};
+    float z[4];
+    dots<4>(X + t * K, wc, K, lane, z);
+    if (lane == 0)
+      for (int j = 0; j < 4 && i0 + j < k; ++j) s_z[i0 + j] = z[j];
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  // the teacher's softmax over the row's targets, up to four per lane
+  float tl[4], top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = lane + 64 * j;
+    tl[j] = i < k && target_ok(idx[i], V) ? logit[t * k + i] : -INFINITY;
+    top = fmaxf(top, tl[j]);
+  }
+  top = wave_max(top);
+  if (top == -INFINITY) {  // nothing to learn from in this row
+    if (lane == 0) loss[t] = 0.f;
+    if (dX)
+      for (int64_t at = 8 * lane; at < K; at += 512)
+        *reinterpret_cast<u32x4_t *>(dX + t * K + at) = u32x4_t{0u, 0u, 0u, 0u};
+    return;
+  }
+  int first = 1 << 20;
+  float e[4], sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    e[j] = expf((tl[j] - top) / tau);
+    sum += e[j];
+    if (tl[j] == top) first = min(first, lane + 64 * j);
+  }
+  sum = wave_sum(sum);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) first = min(first, __shfl_xor(first, o));
+  const float ref = s_z[first], lsum = logf(sum);
+  float h = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = lane + 64 * j;
+    const float p = e[j] / sum;
+    if (i < k) {
+      rows.pt[t * k + i] = p;
+      rows.zt[t * k + i] = s_z[i];
+      if (p > 0.f) h += p * ((tl[j] - top) / tau - lsum - (s_z[i] - ref) / tau);
+    }
+  }
+  h = wave_sum(h);
+  if (lane == 0) {
+    rows.ref[t] = ref;
+    rows.refcol[t] = idx[first];
+    rows.h[t] = h;
+  }
+}
+
+// One wave per counted row of the block.
+__global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, const float2 *__restrict__ stat,
+                                                      int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
+                                                      const int32_t *__restrict__ index, int k, float tau,
+                                                      const float *__restrict__ weight, float *__restrict__ loss,
+                                                      float *__restrict__ scale, bf16_t *__restrict__ E, int64_t lde,
+                                                      const bf16_t *__restrict__ X, int64_t K,
+                                                      bf16_t *__restrict__ Xs) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // row of the block
+  if (row0 + i >= *rows.n) return;
+  const int64_t t = rows.list[row0 + i];
+  const float ref = rows.ref[t], c = 1.44269504f / tau;
+  const float2 *st = stat + i * ntile;
+  float u = ref, sum = 0.f;
+  for (int64_t j = lane; j < ntile; j += 64) {
+    const float2 v = st[j];
+    u = fmaxf(u, v.x);
+    sum += v.x == ref ? v.y : 0.f;
+  }
+  u = wave_max(u);
+  float S, eref = 1.f, rest, nlogq;
+  const bool wide = u != ref;  // some tile's logits are far above the reference: the row takes the largest unit
+  if (!wide) {
+    rest = wave_sum(sum);
+    nlogq = log1pf(rest);
+  } else {
+    sum = 0.f;
+    for (int64_t j = lane; j < ntile; j += 64) sum += st[j].y * exp2f((st[j].x - u) * c);
+    rest = wave_sum(sum);
+    eref = exp2f((ref - u) * c);
+    nlogq = logf(rest + eref) + (u - ref) / tau;
+  }
+  S = rest + eref;
+  if (lane == 0) loss[t] = tau * tau * (rows.h[t] + nlogq);
+  if (!E) return;
+  bf16_t *e = E + i * lde;
+  if (wide) {  // bring the row's tiles to one unit (a factor below binary32's range is applied in two halves)
+    for (int64_t at = 8 * lane; at < lde; at += 512) {
+      const float d = exp2f(0.5f * (st[at / kHeadTile].x - u) * c);
+      u32x4_t v = *reinterpret_cast<u32x4_t *>(e + at);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v[w] = pack_bf16x2(bf16_lo_to_f32(v[w]) * d * d, bf16_hi_to_f32(v[w]) * d * d);
+      *reinterpret_cast<u32x4_t *>(e + at) = v;
+    }
+    __threadfence_block();  // the targets' entries below follow these stores
+  }
+  const float f = (weight ? weight[t] : 1.f) * tau / S;
+  if (lane == 0) scale[i] = f;
+  const int32_t rc = rows.refcol[t];
+  if (labels) {
+    if (lane == 0) e[rc] = f32_to_bf16(-rest);
+  } else {
+    for (int i0 = 0; i0 < k; i0 += 64) {
+      const int me = i0 + lane;
+      const int32_t v = me < k ? index[t * k + me] : -1;
+      float P = 0.f;  // all of the row's probability at this column
+      for (int j = 0; j < k; ++j) P += index[t * k + j] == v ? rows.pt[t * k + j] : 0.f;
+      if (target_ok(v, V))
+        e[v] = f32_to_bf16(v == rc ? eref * (1.f - P) - P * rest : exp2f((rows.zt[t * k + me] - u) * c) - P * S);
+    }
+  }
+  if (Xs)  // rows of X times the row factor: the dW product's second operand, rounded to bf16 for the matrix unit
+    for (int64_t at = 8 * lane; at < K; at += 512) {
+      u32x4_t v = *reinterpret_cast<const u32x4_t *>(X + t * K + at);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v[w] = pack_bf16x2(bf16_lo_to_f32(v[w]) * f, bf16_hi_to_f32(v[w]) * f);
+      *reinterpret_cast<u32x4_t *>(Xs + i * K + at) = v;
+    }
+}
+
+// dX rows of the block from the ranges' partial sums part[range][row of the block][K], added in range order.
+__global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0, int64_t tb, int tile_rows,
+                                                     const float *__restrict__ part, int64_t K, int64_t lde,
+                                                     const float *__restrict__ scale, bf16_t *__restrict__ dX) {
+  int64_t n = *rows.n - row0;
+  n = n < tb ? n : tb;
+  if (n <= 0) return;
+  const int ranges = head_dx_ranges(n, K, lde, tile_rows);
+  if (ranges == 1) return;  // the product wrote dX itself
+  const int64_t per = K / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= n * per) return;
+  const int64_t i = at / per, col = (at % per) * 8;
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = 0.f;
+  for (int r = 0; r < ranges; ++r) {
+    const float4 a = *reinterpret_cast<const float4 *>(part + (r * n + i) * K + col);
+    const float4 b = *reinterpret_cast<const float4 *>(part + (r * n + i) * K + col + 4);
+    s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
+    s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+  }
+  const float f = scale[i];
+  u32x4_t o;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) o[w] = pack_bf16x2(s[2 * w] * f, s[2 * w + 1] * f);
+  *reinterpret_cast<u32x4_t *>(dX + (int64_t)rows.list[row0 + i] * K + col) = o;
+}
+
+}  // namespace
+
+hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t V, int64_t K, const int64_t *labels,
+                            const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
+                            const HeadRows &rows, float *loss, bf16_t *dX, uint32_t *zero, hipStream_t s) {
+  const int64_t wgs = labels ? (T + 3) / 4 : T;
+  launch(k_head_prep, dim3((unsigned)(1 + wgs)), dim3(kPrepThreads), 0, s, X, T, W, V, K, labels, index, logit, k, tau,
+         n, list, rows, loss, dX, zero);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
+                               int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
+                               const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde,
+                               const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s) {
+  launch(k_head_combine, dim3((unsigned)((tb + 3) / 4)), dim3(256), 0, s, rows, row0, stat, ntile, V, labels, index, k,
+         tau, weight, loss, scale, E, lde, X, K, Xs);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t V, int64_t K,
+                              int64_t lde, const float *scale, bf16_t *dX, hipStream_t s) {
+  launch(k_head_reduce, dim3((unsigned)((tb * (K / 8) + 255) / 256)), dim3(256), 0, s, rows, row0, tb,
+         head_tile_rows(tb), part, K, lde, scale, dX);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

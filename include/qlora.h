@@ -58,6 +58,7 @@ typedef uint16_t qlora_bf16; /* bf16 bit pattern */
 #define QLORA_OP_FWD_MULTI 3   /* qlora_linear_fwd_multi */
 
 #define QLORA_MAX_RANK 128
+#define QLORA_MAX_TARGETS 256 /* teacher logits per row of qlora_head_distill */
 
 /*
  * An NF4 weight of logical shape [n_out, n_in] (katajob, "NF4" and "Double
@@ -326,6 +327,72 @@ typedef struct qlora_adamw8_tensor {
 
 int qlora_adamw8_step(const qlora_adamw8_tensor *tensors, int32_t count, double lr, double beta1, double beta2,
                       double eps, double weight_decay, int64_t step, void *stream);
+
+/*
+ * The losses at the end of a training step.  The output layer stays in bf16
+ * beside the quantized linears ("What stays in full precision", katajob); the
+ * step is forward -> loss -> backward into the adapters (glossary, steps 3 and
+ * 4).  With X [T, n_in] the last hidden states and W [n_vocab, n_in] the output
+ * layer (bf16, device), z = X . W^T.  The logits are never stored: the losses
+ * come from softmax statistics of pieces of the vocabulary, and the gradients
+ * from bf16 values exp(z - reference) of a bounded block of rows in the
+ * workspace (at most about 1 GiB however many tokens there are; 256 rows at
+ * least).
+ *
+ * Cross entropy, y_t = labels[t] (device int64):
+ *   loss[t] = log(sum_v exp(z_tv)) - z_t,y        [T] binary32
+ *   G_tv    = weight[t] (softmax(z_t)_v - [v = y_t])
+ *   dX = G . W   [T, n_in] bf16,   dW = G^T . X   [n_vocab, n_in] bf16
+ * A row whose label is outside [0, n_vocab) (-100, say) is ignored: its loss
+ * is 0, its dX row 0, its X row is not read (it may hold anything), and no
+ * work is spent on it.
+ * weight: [T] binary32, finite, the rows' factors in the gradients (1 / number
+ * of counted tokens for a mean), or NULL for 1; the losses are not multiplied.
+ * dX and dW are overwritten; either may be NULL (a frozen output layer needs
+ * no dW; with both NULL the call only scores).
+ *
+ * Arithmetic: logits accumulate in binary32 and are never rounded to fewer
+ * bits; the sums of the softmax, the losses and the rows' factors are
+ * binary32.  The loss is formed against the target's logit, log1p of the other
+ * terms, so a loss near 0 keeps its digits.  The gradient's entries are rounded
+ * to bf16 once for the matrix unit (for dW, X times the row factor once more);
+ * the products accumulate in binary32 and are rounded to bf16 once.  Reductions
+ * run in a fixed order: results are bitwise repeatable.
+ *
+ * X, W, dX, dW 16-byte aligned, labels 8-byte, loss and weight 4-byte; none
+ * may overlap an output.  n_in % 8 == 0, n_vocab >= 1, both at most 2^22,
+ * n_vocab * n_in <= 2^34, T <= 2^22, T * n_in < 2^32.  ws: at least
+ * qlora_head_workspace_bytes(T, n_vocab, n_in, 0, dX != NULL, dW != NULL),
+ * 256-byte aligned; nothing in it needs to start at zero, and calls that
+ * overlap in time need workspaces of their own.  The call can be captured into
+ * a HIP graph.
+ */
+int qlora_head_ce(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t n_vocab, int64_t n_in,
+                  const int64_t *labels, const float *weight, float *loss, qlora_bf16 *dX, qlora_bf16 *dW, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/*
+ * Distillation from a teacher's top logits, with the conventions and the
+ * arithmetic of qlora_head_ce.  Each row has k stored teacher logits:
+ * index [T, k] int32 columns of the vocabulary, logit [T, k] binary32 (device).
+ *   p_i     = exp(logit_i / tau) / sum_j exp(logit_j / tau)    over the row's entries
+ *   q_v     = softmax(z_t / tau)_v                             over the vocabulary
+ *   loss[t] = tau^2 sum_i p_i (log p_i - log q_index_i)
+ *   G_tv    = weight[t] tau (q_v - P_v),   P_v = sum of p_i over the entries with index_i = v
+ * (the gradient of weight[t] loss[t] by z).  An entry whose index is outside
+ * [0, n_vocab) or whose logit is -inf has no part (fill short lists with -1); a
+ * row without any other entry is ignored as in qlora_head_ce.  The same index
+ * twice in a row adds its probabilities.  Logits are otherwise finite.
+ * 1 <= k <= QLORA_MAX_TARGETS, tau > 0.  index and logit are 4-byte aligned.
+ * ws: qlora_head_workspace_bytes(T, n_vocab, n_in, k, dX != NULL, dW != NULL).
+ */
+int qlora_head_distill(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t n_vocab, int64_t n_in,
+                       const int32_t *index, const float *logit, int32_t k, float tau, const float *weight,
+                       float *loss, qlora_bf16 *dX, qlora_bf16 *dW, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of qlora_head_ce (k = 0) and qlora_head_distill (its k) into host *bytes (no HIP call). */
+int qlora_head_workspace_bytes(int64_t T, int64_t n_vocab, int64_t n_in, int32_t k, int need_dx, int need_dw,
+                               size_t *bytes);
 
 /* Static text for a QLORA_E* code. */
 const char *qlora_strerror(int code);
