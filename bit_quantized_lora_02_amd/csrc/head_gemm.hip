@@ -46,62 +46,69 @@ __device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0
 
 // Where an operand's tile comes from: ROWS rows (or columns, transposed) of a row-major matrix.
 //  rows:       element (i, r) at base + row(i) ld + r; row(i) gathered through `list` or first + i, clamped to the
-//              last one; r >= red reads `zero`.
-//  transposed: element (i, r) at base + r ld + first + i; columns clamped to the last chunk; r >= red reads `zero`
-//              if there is one, else the last row (the other operand is zero there).
+//              last one.
+//  transposed: element (i, r) at base + r ld + first + i; columns clamped to the last chunk.
+// Reduction indices from `red` on are zero.  A step's addresses are a wave-uniform base plus 32-bit lane offsets
+// that do not change from step to step.
 template <int ROWS, int NT, bool TR>
 struct Tile {
   static constexpr int LD = ROWS * 8 / NT;  // 16-byte copies per thread and step
+  static constexpr int NW = NT / 64;
+  static constexpr int CH = ROWS / 8;  // transposed: 16-byte chunks per LDS row, and LDS rows from copy to copy
+  static constexpr int RSTEP = NW * 64 / CH;
   static_assert(ROWS * 8 % NT == 0 && LD >= 1, "unsupported tile");
-  const bf16_t *src[TR ? 1 : LD];
-  int col[LD], row[LD];
-  int64_t ld, red;
-  const bf16_t *zero;
+  static_assert(!TR || (64 % CH == 0 && RSTEP % 4 == 0), "the copies of a thread share one swizzle");
+  const char *base;  // reduction index 0 of the tile
+  uint32_t off[TR ? 1 : LD];
+  int64_t ld;
   int wave;
 
-  __device__ __forceinline__ void init(const bf16_t *base, int64_t ld_, int64_t first, int64_t count, int64_t red_,
-                                       const int32_t *list, const bf16_t *zero_, int w, int lane) {
-    ld = ld_, red = red_, zero = zero_, wave = w;
-    if constexpr (TR) src[0] = base;
+  __device__ __forceinline__ void init(const bf16_t *src, int64_t ld_, int64_t first, int64_t count,
+                                       const int32_t *list, int w, int lane) {
+    ld = ld_, wave = w;
+    const int k0 = first_index(w, lane);
+    if constexpr (!TR) {
+      base = (const char *)(list ? src : src + first * ld);
 #pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int g = i * (NT / 64) + w;  // 1 KB piece of the tile
-      if constexpr (!TR) {
-        const int rr = 8 * g + (lane >> 3);
-        int64_t at = first + rr < count ? first + rr : count - 1;
-        if (list) at = list[at];
-        src[i] = base + at * ld;
-        col[i] = 8 * ((lane & 7) ^ ((rr >> 1) & 7));
-        row[i] = 0;
-      } else {
-        constexpr int CH = ROWS / 8;  // 16-byte chunks per LDS row
-        const int rr = g * (64 / CH) + lane / CH;
-        const int chunk = (lane % CH) ^ (swz(rr) << 2);
-        int64_t c = first + 8 * chunk;
-        if (c > count - 8) c = count - 8;  // count % 8 == 0
-        col[i] = (int)c;
-        row[i] = rr;
+      for (int i = 0; i < LD; ++i) {
+        const int rr = 8 * (i * NW + w) + (lane >> 3);
+        const int64_t at = first + rr < count ? rr : count - 1 - first;
+        off[i] = (uint32_t)(((list ? list[first + at] : at) * ld + k0) * 2);
       }
+    } else {
+      int64_t c = first + 8 * ((lane % CH) ^ (swz(k0) << 2));
+      if (c > count - 8) c = count - 8;  // count % 8 == 0
+      base = (const char *)src;
+      off[0] = (uint32_t)((k0 * ld + c) * 2);
     }
   }
   // XOR of the 64-byte group index of LDS row r: rows r .. r + 3 then start in different quarters of the 64 banks
   static __device__ __forceinline__ int swz(int r) { return ROWS >= 128 ? (r & 3) : ((r >> 1) & 1); }
-
+  // Reduction index within a step of this thread's first copy (rows: of all, their rows / 2 are equal modulo 8).
+  static __device__ __forceinline__ int first_index(int w, int lane) {
+    return TR ? w * (64 / CH) + lane / CH : 8 * ((lane & 7) ^ (((8 * w + (lane >> 3)) >> 1) & 7));
+  }
+  __device__ __forceinline__ const char *at(int64_t step) const {
+    return base + step * (TR ? ld * (2 * BK) : 2 * BK);
+  }
+  // (buffer loads take the uniform part in scalar registers; the descriptor spans all of memory behind the base,
+  // every address is inside the operand by construction)
   __device__ __forceinline__ void issue(int64_t step, bf16_t *s) const {
-    const int64_t r0 = step * BK;
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)at(step), 0, -1, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < LD; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void *)(s + (i * NW + wave) * 512), 16, off[TR ? 0 : i],
+          TR ? (int)(i * (ld * (2 * RSTEP))) : 0, 0, 0);
+  }
+  // The last step of a reduction that is no multiple of 64 deep: through registers, `left` < 64 indices remain.
+  __device__ __forceinline__ void issue_part(int64_t step, int left, bf16_t *s) const {
+    const int lane = threadIdx.x & 63, k0 = first_index(wave, lane);
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const bf16_t *p;
-      if constexpr (!TR) {
-        const int64_t c = r0 + col[i];
-        p = c < red ? src[i] + c : zero;
-      } else {
-        const int64_t r = r0 + row[i];
-        p = r < red ? src[0] + r * ld + col[i] : (zero ? zero : src[0] + (red - 1) * ld + col[i]);
-      }
-      __builtin_amdgcn_global_load_lds((const void *)p,
-                                       (__attribute__((address_space(3))) void *)(s + (i * (NT / 64) + wave) * 512),
-                                       16, 0, 0);
+      u32x4_t v = u32x4_t{0u, 0u, 0u, 0u};
+      if (k0 + (TR ? i * RSTEP : 0) < left) v = *reinterpret_cast<const u32x4_t *>(at(step) + (TR ? off[0] + i * (ld * (2 * RSTEP)) : off[TR ? 0 : i]));
+      *reinterpret_cast<u32x4_t *>(s + (i * NW + wave) * 512 + lane * 8) = v;
     }
   }
   // MFMA operand of the 32 rows from `at`, reduction 16 kk .. 16 kk + 15 of the step
@@ -130,10 +137,10 @@ struct Tile {
 template <class C>
 using Acc = f32x16_t[C::WM][C::WN];
 
-// The reduction over steps [s0, s1) into acc.
+// The reduction over steps [s0, s1) into acc; `red` is the reduction's length.
 template <class C, bool TA, bool TB>
-__device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, TA> &ta, const Tile<C::BN, C::NT, TB> &tb, int64_t s0,
-                                             int64_t s1, bf16_t *a0, bf16_t *a1, bf16_t *b0, bf16_t *b1, int wm, int wn,
+__device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, TA> &ta, const Tile<C::BN, C::NT, TB> &tb, int64_t red,
+                                             int64_t s0, int64_t s1, bf16_t *a0, bf16_t *a1, bf16_t *b0, bf16_t *b1, int wm, int wn,
                                              int lane, Acc<C> &acc) {
   typedef Tile<BM, C::NT, TA> TileA;
   typedef Tile<C::BN, C::NT, TB> TileB;
@@ -159,14 +166,19 @@ __device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, TA> &ta, cons
 #pragma unroll
       for (int j = 0; j < C::WN; ++j) acc[i][j] = mfma_32x32x16(av[i], bv[j], acc[i][j]);
   };
-  ta.issue(s0, sa[0]);
-  tb.issue(s0, sb[0]);
+  auto issue = [&](int64_t s, bf16_t *pa, bf16_t *pb) {
+    if ((s + 1) * BK <= red) {
+      ta.issue(s, pa);
+      tb.issue(s, pb);
+    } else {
+      ta.issue_part(s, (int)(red - s * BK), pa);
+      tb.issue_part(s, (int)(red - s * BK), pb);
+    }
+  };
+  issue(s0, sa[0], sb[0]);
   __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
   __syncthreads();
-  if (s0 + 1 < s1) {
-    ta.issue(s0 + 1, sa[1]);
-    tb.issue(s0 + 1, sb[1]);
-  }
+  if (s0 + 1 < s1) issue(s0 + 1, sa[1], sb[1]);
   read(sa[0], sb[0], 0, a[0], b[0]);
   auto step = [&](auto pc, int64_t s) {
     constexpr int P = decltype(pc)::value;
@@ -180,10 +192,7 @@ __device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, TA> &ta, cons
     // every wave holds the step's last operands; the next step's tiles have landed
     __builtin_amdgcn_s_waitcnt(0x0070);
     __syncthreads();
-    if (s + 2 < s1) {
-      ta.issue(s + 2, sa[P]);
-      tb.issue(s + 2, sb[P]);
-    }
+    if (s + 2 < s1) issue(s + 2, sa[P], sb[P]);
     if (s + 1 < s1) read(sa[P ^ 1], sb[P ^ 1], 0, a[0], b[0]);
     fence_sched();
     mma(a[1], b[1]);
@@ -237,15 +246,15 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
   if (n <= 0) return;
   Item it;
   if (!item_of(ntile, (n + C::BN - 1) / C::BN, 1, &it)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
   Tile<BM, C::NT, false> ta;
   Tile<C::BN, C::NT, false> tbl;
-  ta.init(W, K, m0, V, K, nullptr, zero, wave, lane);
-  tbl.init(X, K, n0, n, K, rows.list + row0, zero, wave, lane);
+  ta.init(W, K, m0, V, nullptr, wave, lane);
+  tbl.init(X, K, n0, n, rows.list + row0, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, false, false>(ta, tbl, 0, (K + BK - 1) / BK, a0, a1, b0, b1, wm, wn, lane, acc);
+  reduce_steps<C, false, false>(ta, tbl, K, 0, (K + BK - 1) / BK, a0, a1, b0, b1, wm, wn, lane, acc);
 
   // element e of acc[i][j]: column m0 + mi + 8 (e / 4) + e % 4, row n0 + nj (nj per lane)
   const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
@@ -336,17 +345,17 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
   const int ranges = head_dx_ranges(n, K, lde, C::BN);
   Item it;
   if (!item_of((K + BM - 1) / BM, (n + C::BN - 1) / C::BN, ranges, &it)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
   const int64_t steps = lde / BK, per = (steps + ranges - 1) / ranges;
   const int64_t s0 = it.range * per, s1 = s0 + per < steps ? s0 + per : steps;
   Tile<BM, C::NT, true> ta;
   Tile<C::BN, C::NT, false> tbl;
-  ta.init(W, K, m0, K, V, nullptr, nullptr, wave, lane);
-  tbl.init(E, lde, n0, n, lde, nullptr, nullptr, wave, lane);
+  ta.init(W, K, m0, K, nullptr, wave, lane);
+  tbl.init(E, lde, n0, n, nullptr, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, true, false>(ta, tbl, s0, s1, a0, a1, b0, b1, wm, wn, lane, acc);
+  reduce_steps<C, true, false>(ta, tbl, V, s0, s1, a0, a1, b0, b1, wm, wn, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::WN; ++j) {
     const int64_t i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
@@ -383,15 +392,15 @@ __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, 
   const int64_t n = block_rows(rows, row0, tb) < 0 ? 0 : block_rows(rows, row0, tb);
   Item it;
   if (!item_of((K + BM - 1) / BM, (V + C::BN - 1) / C::BN, 1, &it)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
   Tile<BM, C::NT, true> ta;
   Tile<C::BN, C::NT, true> tbl;
-  ta.init(Xs, K, m0, K, n, nullptr, zero, wave, lane);
-  tbl.init(E, lde, n0, lde, n, nullptr, zero, wave, lane);
+  ta.init(Xs, K, m0, K, nullptr, wave, lane);
+  tbl.init(E, lde, n0, lde, nullptr, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, true, true>(ta, tbl, 0, (n + BK - 1) / BK, a0, a1, b0, b1, wm, wn, lane, acc);
+  reduce_steps<C, true, true>(ta, tbl, n, 0, (n + BK - 1) / BK, a0, a1, b0, b1, wm, wn, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::WN; ++j) {
     const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 31);
