@@ -7,15 +7,13 @@
 // (E with its targets' entries put in by k_head_combine; see head_loss.hip for the mathematics.)
 //
 // One kernel body serves all three: C[n][m] = sum_r A(m, r) B(n, r), the operands read from global memory either
-// along the reduction ("rows": [m][r]) or across it ("transposed": [r][m]).  A workgroup of 8 waves computes a
+// along the reduction ("rows": [m][r]) or across it ("transposed": [r][m]).  A workgroup of 4 or 8 waves computes a
 // 256 x BN tile with v_mfma_f32_32x32x16_bf16; m is the MFMA's row index, so a lane holds four consecutive m of
 // one n, which makes the softmax statistics of a row of X (n) a reduction inside the lane.  The reduction runs in
-// 64-deep steps: both tiles of step s + 2 are copied global -> LDS by the load unit (16 bytes per lane) while
-// step s + 1 is multiplied, two buffers, one barrier per step.  The barrier sits before the last quarter of a
-// step's MFMAs, whose operands are in registers by then, and the first operands of the next step are read under
-// them, so that the matrix unit has work while the waves meet.
+// 32-deep steps over a ring of four LDS tiles that the load unit fills directly (16 bytes per lane, see
+// reduce_steps).
 //
-// LDS tiles: "rows" [row][64] with the 16-byte chunk index XOR-swizzled by (row / 2) % 8; "transposed" [64][cols]
+// LDS tiles: "rows" [row][32] with the 16-byte chunk index XOR-swizzled by (row / 4) % 4; "transposed" [32][cols]
 // with the 64-byte groups of a row XOR-swizzled by row % 4 (a transposing read takes four rows at once), both
 // conflict-free; the direct copies write lane-consecutive LDS, so the swizzle is applied to the source address.
 #include <type_traits>
@@ -28,7 +26,8 @@ namespace qlora {
 
 namespace {
 
-constexpr int BK = 64;
+constexpr int BK = 32;      // reduction depth of a step
+constexpr int STAGES = 4;   // tiles in LDS: one being multiplied, three on their way
 constexpr int BM = kHeadTile;
 
 template <int WAVES_M_, int WAVES_N_, int WM_, int WN_>
@@ -40,7 +39,7 @@ struct HeadCfg {
 };
 using H256 = HeadCfg<2, 4, 4, 2>;  // 128 x 64 per wave
 using H128 = HeadCfg<4, 2, 2, 2>;  // 64 x 64 per wave
-using H64 = HeadCfg<8, 1, 1, 2>;   // 32 x 64 per wave
+using H64 = HeadCfg<4, 1, 2, 2>;   // 64 x 64 per wave, two workgroups per CU
 
 __device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0); }
 
@@ -52,11 +51,11 @@ __device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0
 // that do not change from step to step.
 template <int ROWS, int NT, bool TR>
 struct Tile {
-  static constexpr int LD = ROWS * 8 / NT;  // 16-byte copies per thread and step
+  static constexpr int LD = ROWS * BK / 8 / NT;  // 16-byte copies per thread and step
   static constexpr int NW = NT / 64;
   static constexpr int CH = ROWS / 8;  // transposed: 16-byte chunks per LDS row, and LDS rows from copy to copy
   static constexpr int RSTEP = NW * 64 / CH;
-  static_assert(ROWS * 8 % NT == 0 && LD >= 1, "unsupported tile");
+  static_assert(ROWS * BK / 8 % NT == 0 && LD >= 1, "unsupported tile");
   static_assert(!TR || (64 % CH == 0 && RSTEP % 4 == 0), "the copies of a thread share one swizzle");
   const char *base;  // reduction index 0 of the tile
   uint32_t off[TR ? 1 : LD];
@@ -71,7 +70,7 @@ struct Tile {
       base = (const char *)(list ? src : src + first * ld);
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int rr = 8 * (i * NW + w) + (lane >> 3);
+        const int rr = 16 * (i * NW + w) + (lane >> 2);
         const int64_t at = first + rr < count ? rr : count - 1 - first;
         off[i] = (uint32_t)(((list ? list[first + at] : at) * ld + k0) * 2);
       }
@@ -84,24 +83,22 @@ struct Tile {
   }
   // XOR of the 64-byte group index of LDS row r: rows r .. r + 3 then start in different quarters of the 64 banks
   static __device__ __forceinline__ int swz(int r) { return ROWS >= 128 ? (r & 3) : ((r >> 1) & 1); }
-  // Reduction index within a step of this thread's first copy (rows: of all, their rows / 2 are equal modulo 8).
+  // Reduction index within a step of this thread's first copy (rows: of all, their rows / 4 are equal modulo 4).
   static __device__ __forceinline__ int first_index(int w, int lane) {
-    return TR ? w * (64 / CH) + lane / CH : 8 * ((lane & 7) ^ (((8 * w + (lane >> 3)) >> 1) & 7));
+    return TR ? w * (64 / CH) + lane / CH : 8 * ((lane & 3) ^ ((lane >> 4) & 3));
   }
   __device__ __forceinline__ const char *at(int64_t step) const {
     return base + step * (TR ? ld * (2 * BK) : 2 * BK);
   }
-  // (buffer loads take the uniform part in scalar registers; the descriptor spans all of memory behind the base,
-  // every address is inside the operand by construction)
-  __device__ __forceinline__ void issue(int64_t step, bf16_t *s) const {
+  // Copy i of this thread.  (Buffer loads take the uniform part of the address in scalar registers; the descriptor
+  // spans all of memory behind the base, every address is inside the operand by construction.)
+  __device__ __forceinline__ void issue(int64_t step, int i, bf16_t *s) const {
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)at(step), 0, -1, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < LD; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (__attribute__((address_space(3))) void *)(s + (i * NW + wave) * 512), 16, off[TR ? 0 : i],
-          TR ? (int)(i * (ld * (2 * RSTEP))) : 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, (__attribute__((address_space(3))) void *)(s + (i * NW + wave) * 512), 16, off[TR ? 0 : i],
+        TR ? (int)(i * (ld * (2 * RSTEP))) : 0, 0, 0);
   }
-  // The last step of a reduction that is no multiple of 64 deep: through registers, `left` < 64 indices remain.
+  // The last step of a reduction that is no multiple of 32 deep: through registers, `left` < 32 indices remain.
   __device__ __forceinline__ void issue_part(int64_t step, int left, bf16_t *s) const {
     const int lane = threadIdx.x & 63, k0 = first_index(wave, lane);
 #pragma unroll
@@ -115,7 +112,7 @@ struct Tile {
   static __device__ __forceinline__ u32x4_t read(const bf16_t *s, int at, int kk, int lane) {
     if constexpr (!TR) {
       const int r = at + (lane & 31), chunk = kk * 2 + (lane >> 5);
-      return *reinterpret_cast<const u32x4_t *>(s + r * BK + ((chunk ^ ((r >> 1) & 7)) << 3));
+      return *reinterpret_cast<const u32x4_t *>(s + r * BK + ((chunk ^ ((r >> 2) & 3)) << 3));
     } else {
       // In each 16-lane group, lane i of a transposing read gets element (i & 3) of the 8 bytes addressed by lane
       // 4 m + (i >> 2): lane a points at row base + (a >> 2), columns 4 (a & 3) .. + 3, and the reads of rows + 0..3
@@ -137,13 +134,42 @@ struct Tile {
 template <class C>
 using Acc = f32x16_t[C::WM][C::WN];
 
+// The LDS tiles of one workgroup.  Each is an array of its own, so that the compiler can tell reads of one from the
+// direct copies into another and adds no waits.
+template <class C>
+struct Ring {
+  bf16_t *a[STAGES], *b[STAGES];
+};
+#define QLORA_RING(C, ring)                                                                            \
+  __shared__ __attribute__((aligned(16))) bf16_t ra0[BM * BK], ra1[BM * BK], ra2[BM * BK], ra3[BM * BK];   \
+  __shared__ __attribute__((aligned(16))) bf16_t rb0[C::BN * BK], rb1[C::BN * BK], rb2[C::BN * BK], rb3[C::BN * BK]; \
+  const Ring<C> ring = {{ra0, ra1, ra2, ra3}, {rb0, rb1, rb2, rb3}}
+
+// Wait until at most VM vector-memory operations are in flight and all LDS operations are done, then meet the
+// workgroup's other waves (without the full memory fence of __syncthreads, which would wait for every copy).
+// s_waitcnt fields: vmcnt[3:0] and [15:14], expcnt[6:4] (7 = no wait), lgkmcnt[11:8].
+template <int VM>
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (VM >> 4 << 14) | 0x0070);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // The reduction over steps [s0, s1) into acc; `red` is the reduction's length.
+//
+// Step s multiplies the tiles of slot s % 4 while the copies of steps s + 1 .. s + 3 are in flight.  Its first MFMAs'
+// operands are in registers; the second half's are read under them; then the waves meet (every wave holds the last
+// operands of slot s, and step s + 1 has landed), read the first operands of step s + 1 and run the second half's
+// MFMAs.  The copies of step s + 3 (into the slot of step s - 1, which all waves have left) are issued one at a time
+// between the MFMAs: issued together they would hold the waves up for as long as the load unit takes to accept them.
 template <class C, bool TA, bool TB>
 __device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, TA> &ta, const Tile<C::BN, C::NT, TB> &tb, int64_t red,
-                                             int64_t s0, int64_t s1, bf16_t *a0, bf16_t *a1, bf16_t *b0, bf16_t *b1, int wm, int wn,
-                                             int lane, Acc<C> &acc) {
+                                             int64_t s0, int64_t s1, const Ring<C> &ring, int wm, int wn, int lane,
+                                             Acc<C> &acc) {
   typedef Tile<BM, C::NT, TA> TileA;
   typedef Tile<C::BN, C::NT, TB> TileB;
+  constexpr int L = TileA::LD + TileB::LD, L1 = L / 2;  // copies per thread and step, those before the meeting
 #pragma unroll
   for (int i = 0; i < C::WM; ++i)
 #pragma unroll
@@ -151,60 +177,88 @@ __device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, TA> &ta, cons
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   if (s0 >= s1) return;
-  bf16_t *const sa[2] = {a0, a1};
-  bf16_t *const sb[2] = {b0, b1};
   u32x4_t a[2][C::WM], b[2][C::WN];
-  auto read = [&](const bf16_t *pa, const bf16_t *pb, int kk, u32x4_t(&av)[C::WM], u32x4_t(&bv)[C::WN]) {
+  auto read = [&](int slot, int kk) {
 #pragma unroll
-    for (int i = 0; i < C::WM; ++i) av[i] = TileA::read(pa, (wm * C::WM + i) * 32, kk, lane);
+    for (int i = 0; i < C::WM; ++i) a[kk][i] = TileA::read(ring.a[slot], (wm * C::WM + i) * 32, kk, lane);
 #pragma unroll
-    for (int j = 0; j < C::WN; ++j) bv[j] = TileB::read(pb, (wn * C::WN + j) * 32, kk, lane);
+    for (int j = 0; j < C::WN; ++j) b[kk][j] = TileB::read(ring.b[slot], (wn * C::WN + j) * 32, kk, lane);
   };
-  auto mma = [&](const u32x4_t(&av)[C::WM], const u32x4_t(&bv)[C::WN]) {
-#pragma unroll
-    for (int i = 0; i < C::WM; ++i)
-#pragma unroll
-      for (int j = 0; j < C::WN; ++j) acc[i][j] = mfma_32x32x16(av[i], bv[j], acc[i][j]);
+  auto copy = [&](int64_t s, int slot, int q) {
+    if (q < TileA::LD)
+      ta.issue(s, q, ring.a[slot]);
+    else
+      tb.issue(s, q - TileA::LD, ring.b[slot]);
   };
-  auto issue = [&](int64_t s, bf16_t *pa, bf16_t *pb) {
+  auto copy_all = [&](int64_t s, int slot) {
     if ((s + 1) * BK <= red) {
-      ta.issue(s, pa);
-      tb.issue(s, pb);
+#pragma unroll
+      for (int q = 0; q < L; ++q) copy(s, slot, q);
     } else {
-      ta.issue_part(s, (int)(red - s * BK), pa);
-      tb.issue_part(s, (int)(red - s * BK), pb);
+      ta.issue_part(s, (int)(red - s * BK), ring.a[slot]);
+      tb.issue_part(s, (int)(red - s * BK), ring.b[slot]);
     }
   };
-  issue(s0, sa[0], sb[0]);
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
-  __syncthreads();
-  if (s0 + 1 < s1) issue(s0 + 1, sa[1], sb[1]);
-  read(sa[0], sb[0], 0, a[0], b[0]);
+  // the MFMAs of half kk with copies [q0, q1) of step s spread among them
+  auto mma = [&](int kk, int64_t s, int slot, int q0, int q1) {
+#pragma unroll
+    for (int i = 0; i < C::WM; ++i) {
+#pragma unroll
+      for (int j = 0; j < C::WN; ++j) acc[i][j] = mfma_32x32x16(a[kk][i], b[kk][j], acc[i][j]);
+      fence_sched();
+#pragma unroll
+      for (int q = q0 + (q1 - q0) * i / C::WM; q < q0 + (q1 - q0) * (i + 1) / C::WM; ++q) {
+        copy(s, slot, q);
+        fence_sched();
+      }
+    }
+  };
+  const int64_t whole = red / BK < s1 ? red / BK : s1;  // steps before this one are full
+#pragma unroll
+  for (int q = 0; q < STAGES - 1; ++q)
+    if (s0 + q < s1) copy_all(s0 + q, q);
+  if (s0 + STAGES - 1 <= whole)
+    meet<2 * L>();
+  else
+    meet<0>();
+  read(0, 0);
+  // steady state: copies of step s + 3 are issued, those of s + 2 and the first ones of s + 3 stay in flight
   auto step = [&](auto pc, int64_t s) {
     constexpr int P = decltype(pc)::value;
-#pragma unroll
-    for (int kk = 0; kk < 3; ++kk) {
-      read(sa[P], sb[P], kk + 1, a[(kk + 1) & 1], b[(kk + 1) & 1]);
-      fence_sched();
-      mma(a[kk & 1], b[kk & 1]);
-      fence_sched();
-    }
-    // every wave holds the step's last operands; the next step's tiles have landed
-    __builtin_amdgcn_s_waitcnt(0x0070);
-    __syncthreads();
-    if (s + 2 < s1) issue(s + 2, sa[P], sb[P]);
-    if (s + 1 < s1) read(sa[P ^ 1], sb[P ^ 1], 0, a[0], b[0]);
+    read(P, 1);
     fence_sched();
-    mma(a[1], b[1]);
+    mma(0, s + 3, (P + 3) % STAGES, 0, L1);
+    meet<L + L1>();
+    read((P + 1) % STAGES, 0);
     fence_sched();
+    mma(1, s + 3, (P + 3) % STAGES, L1, L);
+  };
+  // the last steps: at most a part step is still to be copied; everything is waited for
+  auto last = [&](auto pc, int64_t s) {
+    constexpr int P = decltype(pc)::value;
+    read(P, 1);
+    if (s + 3 < s1) copy_all(s + 3, (P + 3) % STAGES);
+    fence_sched();
+    mma(0, 0, 0, 0, 0);
+    meet<0>();
+    if (s + 1 < s1) read((P + 1) % STAGES, 0);
+    fence_sched();
+    mma(1, 0, 0, 0, 0);
   };
   int64_t s = s0;
-  for (; s + 1 < s1; s += 2) {
+  for (; s + STAGES + 2 < whole; s += STAGES) {  // s + 3 + 3 < whole: four steady steps
     step(std::integral_constant<int, 0>(), s);
     step(std::integral_constant<int, 1>(), s + 1);
+    step(std::integral_constant<int, 2>(), s + 2);
+    step(std::integral_constant<int, 3>(), s + 3);
   }
-  if (s < s1) step(std::integral_constant<int, 0>(), s);
-  __syncthreads();  // the buffers may be reused
+  for (; s < s1; s += STAGES) {
+    last(std::integral_constant<int, 0>(), s);
+    if (s + 1 < s1) last(std::integral_constant<int, 1>(), s + 1);
+    if (s + 2 < s1) last(std::integral_constant<int, 2>(), s + 2);
+    if (s + 3 < s1) last(std::integral_constant<int, 3>(), s + 3);
+  }
+  meet<0>();  // the tiles may be reused
 }
 
 // Work item of this workgroup: items are numbered so that each XCD (workgroups go round the 8 XCDs) takes a run of
@@ -240,7 +294,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
                                                        int64_t V, int64_t K, float c, float2 *__restrict__ stat,
                                                        int64_t ntile, bf16_t *__restrict__ E, int64_t lde,
                                                        const bf16_t *__restrict__ zero) {
-  __shared__ __attribute__((aligned(16))) bf16_t a0[BM * BK], a1[BM * BK], b0[C::BN * BK], b1[C::BN * BK];
+  QLORA_RING(C, ring);
   __shared__ float s_max[C::WAVES_M][C::BN], s_sum[C::WAVES_M][C::BN];
   const int64_t n = block_rows(rows, row0, tb);
   if (n <= 0) return;
@@ -254,7 +308,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
   ta.init(W, K, m0, V, nullptr, wave, lane);
   tbl.init(X, K, n0, n, rows.list + row0, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, false, false>(ta, tbl, K, 0, (K + BK - 1) / BK, a0, a1, b0, b1, wm, wn, lane, acc);
+  reduce_steps<C, false, false>(ta, tbl, K, 0, (K + BK - 1) / BK, ring, wm, wn, lane, acc);
 
   // element e of acc[i][j]: column m0 + mi + 8 (e / 4) + e % 4, row n0 + nj (nj per lane)
   const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
@@ -284,8 +338,10 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
     if (lane < 32) s_max[wm][nj] = top;
   }
   __syncthreads();
-  // 64 rows of 256 columns each (the narrow tiles use the first ones)
-  auto stage = [&](int i) { return i == 0 ? a0 : i == 1 ? a1 : i == 2 ? b0 : b1; };
+  // E's tile is turned through the ring's arrays, 32 rows of 256 columns in each (the narrow tiles use the first ones)
+  auto stage = [&](int i) {
+    return i == 0 ? ra0 : i == 1 ? ra1 : i == 2 ? ra2 : i == 3 ? ra3 : i == 4 ? rb0 : i == 5 ? rb1 : i == 6 ? rb2 : rb3;
+  };
 #pragma unroll
   for (int j = 0; j < C::WN; ++j) {
     const int nj = (wn * C::WN + j) * 32 + (lane & 31);
@@ -294,7 +350,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
     for (int w = 1; w < C::WAVES_M; ++w) top = fmaxf(top, s_max[w][nj]);
     const float u = (top - ref[j]) * c > kHeadRange ? top : ref[j];
     float sum = 0.f;
-    bf16_t *const srow = stage(nj >> 6) + (nj & 63) * BM;
+    bf16_t *const srow = stage(nj >> 5) + (nj & 31) * BM;
 #pragma unroll
     for (int i = 0; i < C::WM; ++i)
 #pragma unroll
@@ -327,7 +383,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
     const int nj = at >> 5, chunk = at & 31;
     if (n0 + nj >= n || m0 + chunk * 8 >= lde) continue;
     *reinterpret_cast<u32x4_t *>(E + (n0 + nj) * lde + m0 + chunk * 8) =
-        *reinterpret_cast<const u32x4_t *>(stage(nj >> 6) + (nj & 63) * BM + (((chunk ^ nj) & 31) << 3));
+        *reinterpret_cast<const u32x4_t *>(stage(nj >> 5) + (nj & 31) * BM + (((chunk ^ nj) & 31) << 3));
   }
 }
 
@@ -339,7 +395,7 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
                                                    const bf16_t *__restrict__ W, int64_t V, int64_t K,
                                                    const float *__restrict__ scale, float *__restrict__ part,
                                                    bf16_t *__restrict__ dX) {
-  __shared__ __attribute__((aligned(16))) bf16_t a0[BM * BK], a1[BM * BK], b0[C::BN * BK], b1[C::BN * BK];
+  QLORA_RING(C, ring);
   const int64_t n = block_rows(rows, row0, tb);
   if (n <= 0) return;
   const int ranges = head_dx_ranges(n, K, lde, C::BN);
@@ -355,7 +411,7 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
   ta.init(W, K, m0, K, nullptr, wave, lane);
   tbl.init(E, lde, n0, n, nullptr, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, true, false>(ta, tbl, V, s0, s1, a0, a1, b0, b1, wm, wn, lane, acc);
+  reduce_steps<C, true, false>(ta, tbl, V, s0, s1, ring, wm, wn, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::WN; ++j) {
     const int64_t i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
@@ -388,7 +444,7 @@ __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, 
                                                    const bf16_t *__restrict__ Xs, int64_t V, int64_t K,
                                                    const bf16_t *__restrict__ zero, float *__restrict__ sums,
                                                    int first, int last, bf16_t *__restrict__ dW) {
-  __shared__ __attribute__((aligned(16))) bf16_t a0[BM * BK], a1[BM * BK], b0[C::BN * BK], b1[C::BN * BK];
+  QLORA_RING(C, ring);
   const int64_t n = block_rows(rows, row0, tb) < 0 ? 0 : block_rows(rows, row0, tb);
   Item it;
   if (!item_of((K + BM - 1) / BM, (V + C::BN - 1) / C::BN, 1, &it)) return;
@@ -400,7 +456,7 @@ __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, 
   ta.init(Xs, K, m0, K, nullptr, wave, lane);
   tbl.init(E, lde, n0, lde, nullptr, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, true, true>(ta, tbl, n, 0, (n + BK - 1) / BK, a0, a1, b0, b1, wm, wn, lane, acc);
+  reduce_steps<C, true, true>(ta, tbl, n, 0, (n + BK - 1) / BK, ring, wm, wn, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::WN; ++j) {
     const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 31);
