@@ -422,8 +422,10 @@ int check_ws(int op, int64_t T, int64_t N, int64_t K, int32_t r, const void *ws,
 constexpr size_t kHeadBlockBytes = (size_t)1 << 30;
 
 struct HeadPlan {
-  int64_t tb = 0, blocks = 0, ntile = 0, lde = 0;
-  size_t off_n = 0, off_zero = 0, off_list = 0, off_ref = 0, off_col = 0, off_h = 0, off_zt = 0, off_pt = 0,
+  HeadBlocks b = {};
+  int64_t ntile = 0;
+  int64_t ldx = 0;  // rows per block of the laid out X (0: it is read as it is)
+  size_t off_n = 0, off_ranges = 0, off_xt = 0, off_list = 0, off_ref = 0, off_col = 0, off_h = 0, off_zt = 0, off_pt = 0,
          off_stat = 0, off_scale = 0, off_e = 0, off_part = 0, off_xs = 0, off_sums = 0, total = 0;
   bool split = false;  // dX may come as partial sums
 };
@@ -432,12 +434,16 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   HeadPlan p;
   const bool grad = dx || dw;
   p.ntile = ceil_div(V, kHeadTile);
-  p.lde = ceil_div(V, kHeadPad) * kHeadPad;
-  const size_t row = (size_t)p.ntile * sizeof(float2) + (grad ? (size_t)p.lde * 2 : 0);
+  p.b.lde = ceil_div(V, kHeadPad) * kHeadPad;
+  const size_t row = (size_t)p.ntile * sizeof(float2) + (grad ? (size_t)p.b.lde * 2 : 0);
   int64_t most = (int64_t)(kHeadBlockBytes / row) / 256 * 256;
   most = most < 256 ? 256 : most;
-  p.blocks = T <= most ? 1 : ceil_div(T, most);
-  p.tb = p.blocks == 1 ? (T < 1 ? 1 : T) : (int64_t)up((size_t)ceil_div(T, p.blocks), 256);
+  p.b.count = T <= most ? 1 : ceil_div(T, most);
+  p.b.tb = p.b.count == 1 ? (T < 1 ? 1 : T) : (int64_t)up((size_t)ceil_div(T, p.b.count), 256);
+  p.b.count = T < 1 ? 1 : ceil_div(T, p.b.tb);
+  p.b.te = (int64_t)up((size_t)p.b.tb, 16);
+  // up to 64 rows the logits are bound by the stream of W and take X as it is
+  p.ldx = head_tile_rows(p.b.tb) > 64 ? (int64_t)up((size_t)T, 16) : 0;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -445,7 +451,8 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
     return at;
   };
   p.off_n = take(4);
-  p.off_zero = take(256);
+  p.off_ranges = take((size_t)p.b.count * 4);
+  if (p.ldx) p.off_xt = take((size_t)ceil_div(K, 32) * p.ldx * 64);
   p.off_list = take((size_t)T * 4);
   p.off_ref = take((size_t)T * 4);
   p.off_col = take((size_t)T * 4);
@@ -454,17 +461,17 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
     p.off_zt = take((size_t)T * k * 4);
     p.off_pt = take((size_t)T * k * 4);
   }
-  p.off_stat = take((size_t)p.tb * p.ntile * sizeof(float2));
-  p.off_scale = take((size_t)p.tb * 4);
-  if (grad) p.off_e = take((size_t)p.tb * p.lde * 2);
+  p.off_stat = take((size_t)p.b.tb * p.ntile * sizeof(float2));
+  p.off_scale = take((size_t)p.b.tb * 4);
+  if (grad) p.off_e = take((size_t)p.b.te * p.b.lde * 2);
   if (dx) {
-    const size_t part = head_part_floats(p.tb, K, p.lde) * 4;
+    const size_t part = head_part_floats(p.b.tb, K, p.b.lde) * 4;
     p.split = part > 0;
     p.off_part = take(part);
   }
   if (dw) {
-    p.off_xs = take((size_t)p.tb * K * 2);
-    if (p.blocks > 1) p.off_sums = take((size_t)V * K * 4);
+    p.off_xs = take((size_t)p.b.tb * K * 2);
+    if (p.b.count > 1) p.off_sums = take((size_t)V * K * 4);
   }
   p.total = off;
   return p;
@@ -475,8 +482,9 @@ int check_head_sizes(int64_t T, int64_t V, int64_t K) {
   if (V < 1 || V > kMaxDim || K < 8 || K > kMaxDim || K % 8 != 0)
     return fail(QLORA_EINVAL, "need n_vocab >= 1 and n_in a positive multiple of 8, each at most 2^22 (got %lld x %lld)",
                 (long long)V, (long long)K);
-  if (V * K > kMaxWeights || T * K > kMaxActs)
-    return fail(QLORA_EINVAL, "n_vocab x n_in must be at most 2^34 and T x n_in below 2^32 (got T=%lld, %lld x %lld)",
+  // (rows of X are addressed by 32-bit byte offsets)
+  if (V * K > kMaxWeights || T * K >= (int64_t)1 << 31)
+    return fail(QLORA_EINVAL, "n_vocab x n_in must be at most 2^34 and T x n_in below 2^31 (got T=%lld, %lld x %lld)",
                 (long long)T, (long long)V, (long long)K);
   return QLORA_OK;
 }
@@ -505,6 +513,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   int32_t *n = (int32_t *)(w + p.off_n), *list = (int32_t *)(w + p.off_list);
   HeadRows rows;
   rows.n = n;
+  rows.ranges = nullptr;
   rows.list = list;
   rows.ref = (float *)(w + p.off_ref);
   rows.refcol = (int32_t *)(w + p.off_col);
@@ -518,24 +527,27 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   float *part = p.split ? (float *)(w + p.off_part) : nullptr;
   bf16_t *Xs = dW ? (bf16_t *)(w + p.off_xs) : nullptr;
   float *sums = p.off_sums ? (float *)(w + p.off_sums) : nullptr;
-  const bf16_t *zero = (const bf16_t *)(w + p.off_zero);
+  bf16_t *Xt = p.ldx ? (bf16_t *)(w + p.off_xt) : nullptr;
+  int32_t *ranges = (int32_t *)(w + p.off_ranges);
   const float c = 1.44269504f / tau;
-  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, rows, loss, dX,
-                                       (uint32_t *)(w + p.off_zero), s));
-  for (int64_t b = 0; b < p.blocks; ++b) {
-    const int64_t row0 = b * p.tb, tb = T - row0 < p.tb ? T - row0 : p.tb;
+  const int64_t lde = p.b.lde, te = p.b.te;
+  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, ranges, p.b, rows, loss, dX,
+                                       Xt, p.ldx, s));
+  for (int64_t b = 0; b < p.b.count; ++b) {
+    const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
+    rows.ranges = ranges + b;
     if (tb > 0) {
-      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, X, W, V, K, c, stat, p.ntile, E, p.lde, zero, s));
+      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, X, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, s));
       LAUNCH("head_combine", launch_head_combine(rows, row0, tb, stat, p.ntile, V, labels, index, k, tau, weight, loss,
-                                                 scale, E, p.lde, X, K, Xs, s));
+                                                 scale, E, lde, te, X, K, Xs, s));
       if (dX) {
-        LAUNCH("head_dx", launch_head_dx(rows, row0, tb, E, p.lde, W, V, K, scale, part, dX, s));
-        if (part) LAUNCH("head_dx_reduce", launch_head_reduce(rows, row0, tb, part, V, K, p.lde, scale, dX, s));
+        LAUNCH("head_dx", launch_head_dx(rows, row0, tb, E, lde, te, W, V, K, scale, part, dX, s));
+        if (part) LAUNCH("head_dx_reduce", launch_head_reduce(rows, row0, tb, part, K, scale, dX, s));
       }
     }
     if (dW)
       LAUNCH("head_dw",
-             launch_head_dw(rows, row0, tb, E, p.lde, Xs, V, K, zero, sums, b == 0, b + 1 == p.blocks, dW, s));
+             launch_head_dw(rows, row0, tb, E, lde, te, Xs, V, K, sums, b == 0, b + 1 == p.b.count, dW, s));
   }
   return QLORA_OK;
 }

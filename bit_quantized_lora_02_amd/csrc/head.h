@@ -15,7 +15,8 @@ typedef uint16_t bf16_t;
 // target's logit ref = z[refcol] (or, where some logit is so far above it that bf16 would overflow, a larger one),
 // and E[v] = exp2((z[v] - u) c) is what is kept of logit v.
 struct HeadRows {
-  const int32_t *n;     // rows that count
+  const int32_t *n;       // rows that count
+  const int32_t *ranges;  // the dX product's ranges for the block at hand
   const int32_t *list;  // [T] their rows in X
   float *ref;           // [T] by row of X: the logit of the row's first target
   int32_t *refcol;      // [T] by row of X: that target's column
@@ -49,18 +50,27 @@ __host__ __device__ inline int head_split(int64_t tiles, int64_t steps, int slot
   return best;
 }
 
+// How the counted rows are taken in blocks.
+struct HeadBlocks {
+  int64_t tb, count;  // rows per block (the last: what is left of T), blocks
+  int64_t lde;        // columns of E: V rounded up to kHeadPad
+  int64_t te;         // rows of E's blocks of columns (E is [lde / 32][te][32])
+};
+
 hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t V, int64_t K, const int64_t *labels,
                             const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
-                            const HeadRows &rows, float *loss, bf16_t *dX, uint32_t *zero, hipStream_t s);
+                            int32_t *ranges, const HeadBlocks &blocks, const HeadRows &rows, float *loss, bf16_t *dX,
+                            bf16_t *Xt, int64_t ldx, hipStream_t s);
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
-                               const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde,
+                               const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde, int64_t te,
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s);
-hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t V, int64_t K,
-                              int64_t lde, const float *scale, bf16_t *dX, hipStream_t s);
+hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t K,
+                              const float *scale, bf16_t *dX, hipStream_t s);
 
 // Rows of X per tile of the three products for blocks of at most `tb` rows.
-int head_tile_rows(int64_t tb);
+// Few rows take narrow tiles: the padding rows' MFMA work would cost more than the wider tile's operand reuse gains.
+__host__ __device__ inline int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
 // Largest size in floats of the dX product's partial sums over all row counts up to tb (0: never split).
 size_t head_part_floats(int64_t tb, int64_t K, int64_t lde);
 // Ranges of the dX product of n rows.
@@ -69,14 +79,15 @@ __host__ __device__ inline int head_dx_ranges(int64_t n, int64_t K, int64_t lde,
   return head_split(tiles, lde / 64, tile_rows == 64 ? 512 : 256, 256 * tile_rows);
 }
 
-hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *X, const bf16_t *W,
-                              int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E, int64_t lde,
-                              const bf16_t *zero, hipStream_t s);
-hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde,
+// The logits take X as it is (Xt NULL) or as k_head_prep lays it out: Xt [K / 32 rounded up][ldx][32], zero past K.
+hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *X, const bf16_t *Xt,
+                              int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
+                              bf16_t *E, int64_t lde, int64_t te, hipStream_t s);
+hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
                           hipStream_t s);
-hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde,
-                          const bf16_t *Xs, int64_t V, int64_t K, const bf16_t *zero, float *acc, bool first,
-                          bool last, bf16_t *dW, hipStream_t s);
+hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
+                          const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,
+                          hipStream_t s);
 
 }  // namespace qlora

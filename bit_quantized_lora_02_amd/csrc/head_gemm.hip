@@ -43,17 +43,24 @@ using H64 = HeadCfg<4, 1, 2, 2>;   // 64 x 64 per wave, two workgroups per CU
 
 __device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0); }
 
-// Where an operand's tile comes from: ROWS rows (or columns, transposed) of a row-major matrix.
-//  rows:       element (i, r) at base + row(i) ld + r; row(i) gathered through `list` or first + i, clamped to the
-//              last one.
-//  transposed: element (i, r) at base + r ld + first + i; columns clamped to the last chunk.
-// Reduction indices from `red` on are zero.  A step's addresses are a wave-uniform base plus 32-bit lane offsets
-// that do not change from step to step.
-template <int ROWS, int NT, bool TR>
+// How an operand lies in memory (element (i, r): row or column i of the tile's side, reduction index r):
+//  LINES:   row-major [i][r].
+//  BLOCKS:  32 reduction indices at a time, [r / 32][i][32]: a step's tile is one contiguous piece, where LINES
+//           would fetch half of every 128-byte line it touches in one step and the other half in the next.
+//  ACROSS:  row-major [r][i].
+//  BLOCKS_ACROSS: [i / 32][r][32], what BLOCKS is seen from its other side.
+enum { LINES, BLOCKS, ACROSS, BLOCKS_ACROSS };
+
+// One operand's tile of ROWS rows (columns for the ACROSS ones).  `ld` is the row length of a row-major matrix, the
+// number of rows in a block otherwise.  Rows may be gathered through `list`; those past the last one repeat it.
+// Reduction indices from the reduction's length on read as zero (BLOCKS are zero there in memory).  A step's
+// addresses are a wave-uniform base plus 32-bit lane offsets that do not change from step to step.
+template <int ROWS, int NT, int KIND>
 struct Tile {
+  static constexpr bool TR = KIND == ACROSS || KIND == BLOCKS_ACROSS;
   static constexpr int LD = ROWS * BK / 8 / NT;  // 16-byte copies per thread and step
   static constexpr int NW = NT / 64;
-  static constexpr int CH = ROWS / 8;  // transposed: 16-byte chunks per LDS row, and LDS rows from copy to copy
+  static constexpr int CH = ROWS / 8;  // across: 16-byte chunks per LDS row, and LDS rows from copy to copy
   static constexpr int RSTEP = NW * 64 / CH;
   static_assert(ROWS * BK / 8 % NT == 0 && LD >= 1, "unsupported tile");
   static_assert(!TR || (64 % CH == 0 && RSTEP % 4 == 0), "the copies of a thread share one swizzle");
@@ -67,18 +74,24 @@ struct Tile {
     ld = ld_, wave = w;
     const int k0 = first_index(w, lane);
     if constexpr (!TR) {
-      base = (const char *)(list ? src : src + first * ld);
+      const int64_t row = KIND == BLOCKS ? BK : ld;
+      base = (const char *)(list ? src : src + first * row);
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
         const int rr = 16 * (i * NW + w) + (lane >> 2);
         const int64_t at = first + rr < count ? rr : count - 1 - first;
-        off[i] = (uint32_t)(((list ? list[first + at] : at) * ld + k0) * 2);
+        off[i] = (uint32_t)(((list ? list[first + at] : at) * row + k0) * 2);
       }
     } else {
       int64_t c = first + 8 * ((lane % CH) ^ (swz(k0) << 2));
       if (c > count - 8) c = count - 8;  // count % 8 == 0
-      base = (const char *)src;
-      off[0] = (uint32_t)((k0 * ld + c) * 2);
+      if constexpr (KIND == ACROSS) {
+        base = (const char *)src;
+        off[0] = (uint32_t)((k0 * ld + c) * 2);
+      } else {
+        base = (const char *)(src + first / 32 * ld * 32);
+        off[0] = (uint32_t)((((c - first) / 32 * ld + k0) * 32 + c % 32) * 2);
+      }
     }
   }
   // XOR of the 64-byte group index of LDS row r: rows r .. r + 3 then start in different quarters of the 64 banks
@@ -88,15 +101,18 @@ struct Tile {
     return TR ? w * (64 / CH) + lane / CH : 8 * ((lane & 3) ^ ((lane >> 4) & 3));
   }
   __device__ __forceinline__ const char *at(int64_t step) const {
-    return base + step * (TR ? ld * (2 * BK) : 2 * BK);
+    return base + step * (KIND == ACROSS || KIND == BLOCKS ? ld * (2 * BK) : KIND == LINES ? 2 * BK : 64 * BK);
+  }
+  __device__ __forceinline__ int64_t next(int i) const {  // bytes from an across operand's first copy to copy i
+    return KIND == ACROSS ? i * (ld * (2 * RSTEP)) : KIND == BLOCKS_ACROSS ? i * 64 * RSTEP : 0;
   }
   // Copy i of this thread.  (Buffer loads take the uniform part of the address in scalar registers; the descriptor
   // spans all of memory behind the base, every address is inside the operand by construction.)
   __device__ __forceinline__ void issue(int64_t step, int i, bf16_t *s) const {
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)at(step), 0, -1, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rsrc, (__attribute__((address_space(3))) void *)(s + (i * NW + wave) * 512), 16, off[TR ? 0 : i],
-        TR ? (int)(i * (ld * (2 * RSTEP))) : 0, 0, 0);
+        rsrc, (__attribute__((address_space(3))) void *)(s + (i * NW + wave) * 512), 16, off[TR ? 0 : i], (int)next(i),
+        0, 0);
   }
   // The last step of a reduction that is no multiple of 32 deep: through registers, `left` < 32 indices remain.
   __device__ __forceinline__ void issue_part(int64_t step, int left, bf16_t *s) const {
@@ -104,7 +120,8 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
       u32x4_t v = u32x4_t{0u, 0u, 0u, 0u};
-      if (k0 + (TR ? i * RSTEP : 0) < left) v = *reinterpret_cast<const u32x4_t *>(at(step) + (TR ? off[0] + i * (ld * (2 * RSTEP)) : off[TR ? 0 : i]));
+      if (KIND == BLOCKS || k0 + (TR ? i * RSTEP : 0) < left)
+        v = *reinterpret_cast<const u32x4_t *>(at(step) + off[TR ? 0 : i] + next(i));
       *reinterpret_cast<u32x4_t *>(s + (i * NW + wave) * 512 + lane * 8) = v;
     }
   }
@@ -163,12 +180,12 @@ __device__ __forceinline__ void meet() {
 // operands of slot s, and step s + 1 has landed), read the first operands of step s + 1 and run the second half's
 // MFMAs.  The copies of step s + 3 (into the slot of step s - 1, which all waves have left) are issued one at a time
 // between the MFMAs: issued together they would hold the waves up for as long as the load unit takes to accept them.
-template <class C, bool TA, bool TB>
-__device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, TA> &ta, const Tile<C::BN, C::NT, TB> &tb, int64_t red,
-                                             int64_t s0, int64_t s1, const Ring<C> &ring, int wm, int wn, int lane,
+template <class C, int KA, int KB>
+__device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, KA> &ta, const Tile<C::BN, C::NT, KB> &tb,
+                                             int64_t red, int64_t s0, int64_t s1, const Ring<C> &ring, int wm, int wn, int lane,
                                              Acc<C> &acc) {
-  typedef Tile<BM, C::NT, TA> TileA;
-  typedef Tile<C::BN, C::NT, TB> TileB;
+  typedef Tile<BM, C::NT, KA> TileA;
+  typedef Tile<C::BN, C::NT, KB> TileB;
   constexpr int L = TileA::LD + TileB::LD, L1 = L / 2;  // copies per thread and step, those before the meeting
 #pragma unroll
   for (int i = 0; i < C::WM; ++i)
@@ -288,12 +305,13 @@ __device__ __forceinline__ int64_t block_rows(const HeadRows &rows, int64_t row0
 
 // ------------------------------------------------------------------ logits
 // m: columns of the vocabulary, n: counted rows of the block.
-template <class C>
+// X row-major (LINES) or as k_head_prep lays it out (BLOCKS, ldx rows per block).
+template <class C, int KX>
 __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t row0, int64_t tb,
-                                                       const bf16_t *__restrict__ X, const bf16_t *__restrict__ W,
-                                                       int64_t V, int64_t K, float c, float2 *__restrict__ stat,
-                                                       int64_t ntile, bf16_t *__restrict__ E, int64_t lde,
-                                                       const bf16_t *__restrict__ zero) {
+                                                       const bf16_t *__restrict__ X, int64_t ldx,
+                                                       const bf16_t *__restrict__ W, int64_t V, int64_t K, float c,
+                                                       float2 *__restrict__ stat, int64_t ntile,
+                                                       bf16_t *__restrict__ E, int64_t lde, int64_t te) {
   QLORA_RING(C, ring);
   __shared__ float s_max[C::WAVES_M][C::BN], s_sum[C::WAVES_M][C::BN];
   const int64_t n = block_rows(rows, row0, tb);
@@ -303,12 +321,12 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
-  Tile<BM, C::NT, false> ta;
-  Tile<C::BN, C::NT, false> tbl;
+  Tile<BM, C::NT, LINES> ta;
+  Tile<C::BN, C::NT, KX> tbl;
   ta.init(W, K, m0, V, nullptr, wave, lane);
-  tbl.init(X, K, n0, n, rows.list + row0, wave, lane);
+  tbl.init(X, ldx, n0, n, rows.list + row0, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, false, false>(ta, tbl, K, 0, (K + BK - 1) / BK, ring, wm, wn, lane, acc);
+  reduce_steps<C, LINES, KX>(ta, tbl, K, 0, (K + BK - 1) / BK, ring, wm, wn, lane, acc);
 
   // element e of acc[i][j]: column m0 + mi + 8 (e / 4) + e % 4, row n0 + nj (nj per lane)
   const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
@@ -379,10 +397,11 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
     stat[(n0 + tid) * ntile + it.m] = make_float2((top - r) * c > kHeadRange ? top : r, sum);
   }
   if (!E) return;
+  // E lies in blocks of 32 columns, [column / 32][row][32]: 16 rows of a block are 1 KB
   for (int at = tid; at < C::BN * 32; at += C::NT) {
-    const int nj = at >> 5, chunk = at & 31;
+    const int nj = (at >> 2) % C::BN, chunk = at / (4 * C::BN) * 4 + (at & 3);
     if (n0 + nj >= n || m0 + chunk * 8 >= lde) continue;
-    *reinterpret_cast<u32x4_t *>(E + (n0 + nj) * lde + m0 + chunk * 8) =
+    *reinterpret_cast<u32x4_t *>(E + ((m0 / 32 + (chunk >> 2)) * te + n0 + nj) * 32 + (chunk & 3) * 8) =
         *reinterpret_cast<const u32x4_t *>(stage(nj >> 5) + (nj & 31) * BM + (((chunk ^ nj) & 31) << 3));
   }
 }
@@ -391,14 +410,14 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
 // m: columns of X, n: counted rows of the block; reduction over the vocabulary (lde of it: E is zero past V).
 template <class C>
 __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, int64_t tb,
-                                                   const bf16_t *__restrict__ E, int64_t lde,
+                                                   const bf16_t *__restrict__ E, int64_t lde, int64_t te,
                                                    const bf16_t *__restrict__ W, int64_t V, int64_t K,
                                                    const float *__restrict__ scale, float *__restrict__ part,
                                                    bf16_t *__restrict__ dX) {
   QLORA_RING(C, ring);
   const int64_t n = block_rows(rows, row0, tb);
   if (n <= 0) return;
-  const int ranges = head_dx_ranges(n, K, lde, C::BN);
+  const int ranges = *rows.ranges;
   Item it;
   if (!item_of((K + BM - 1) / BM, (n + C::BN - 1) / C::BN, ranges, &it)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -406,12 +425,12 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
   const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
   const int64_t steps = lde / BK, per = (steps + ranges - 1) / ranges;
   const int64_t s0 = it.range * per, s1 = s0 + per < steps ? s0 + per : steps;
-  Tile<BM, C::NT, true> ta;
-  Tile<C::BN, C::NT, false> tbl;
+  Tile<BM, C::NT, ACROSS> ta;
+  Tile<C::BN, C::NT, BLOCKS> tbl;
   ta.init(W, K, m0, K, nullptr, wave, lane);
-  tbl.init(E, lde, n0, n, nullptr, wave, lane);
+  tbl.init(E, te, n0, n, nullptr, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, true, false>(ta, tbl, V, s0, s1, ring, wm, wn, lane, acc);
+  reduce_steps<C, ACROSS, BLOCKS>(ta, tbl, V, s0, s1, ring, wm, wn, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::WN; ++j) {
     const int64_t i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
@@ -440,9 +459,9 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
 // blocks) the binary32 sums are carried in it from block to block and rounded to dW after the last.
 template <class C>
 __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, int64_t tb,
-                                                   const bf16_t *__restrict__ E, int64_t lde,
+                                                   const bf16_t *__restrict__ E, int64_t lde, int64_t te,
                                                    const bf16_t *__restrict__ Xs, int64_t V, int64_t K,
-                                                   const bf16_t *__restrict__ zero, float *__restrict__ sums,
+                                                   float *__restrict__ sums,
                                                    int first, int last, bf16_t *__restrict__ dW) {
   QLORA_RING(C, ring);
   const int64_t n = block_rows(rows, row0, tb) < 0 ? 0 : block_rows(rows, row0, tb);
@@ -451,12 +470,12 @@ __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
-  Tile<BM, C::NT, true> ta;
-  Tile<C::BN, C::NT, true> tbl;
+  Tile<BM, C::NT, ACROSS> ta;
+  Tile<C::BN, C::NT, BLOCKS_ACROSS> tbl;
   ta.init(Xs, K, m0, K, nullptr, wave, lane);
-  tbl.init(E, lde, n0, lde, nullptr, wave, lane);
+  tbl.init(E, te, n0, lde, nullptr, wave, lane);
   f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, true, true>(ta, tbl, n, 0, (n + BK - 1) / BK, ring, wm, wn, lane, acc);
+  reduce_steps<C, ACROSS, BLOCKS_ACROSS>(ta, tbl, n, 0, (n + BK - 1) / BK, ring, wm, wn, lane, acc);
 #pragma unroll
   for (int j = 0; j < C::WN; ++j) {
     const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 31);
@@ -488,9 +507,6 @@ int64_t items8(int64_t items) { return (items + 7) / 8 * 8; }  // every XCD's ru
 
 }  // namespace
 
-// Few rows take narrow tiles: the padding rows' MFMA work would cost more than the wider tile's operand reuse gains.
-int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
-
 size_t head_part_floats(int64_t tb, int64_t K, int64_t lde) {
   const int bn = head_tile_rows(tb);
   size_t most = 0;
@@ -504,23 +520,27 @@ size_t head_part_floats(int64_t tb, int64_t K, int64_t lde) {
 
 #define QLORA_HEAD_TILES(rows_, CALL)   \
   switch (head_tile_rows(rows_)) {      \
-    case 64: CALL(H64); break;          \
-    case 128: CALL(H128); break;        \
-    default: CALL(H256); break;         \
+    case 64: { CALL(H64); break; }      \
+    case 128: { CALL(H128); break; }    \
+    default: { CALL(H256); break; }     \
   }
 
-hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *X, const bf16_t *W,
-                              int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E, int64_t lde,
-                              const bf16_t *zero, hipStream_t s) {
-#define QLORA_CALL(CFG)                                                                                             \
-  launch(k_head_logits<CFG>, dim3((unsigned)items8(ntile * ((tb + CFG::BN - 1) / CFG::BN))), dim3(CFG::NT), 0, s, rows, row0, \
-         tb, X, W, V, K, c, stat, ntile, E, lde, zero)
+hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *X, const bf16_t *Xt,
+                              int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
+                              bf16_t *E, int64_t lde, int64_t te, hipStream_t s) {
+#define QLORA_CALL(CFG)                                                                                         \
+  const dim3 grid((unsigned)items8(ntile * ((tb + CFG::BN - 1) / CFG::BN)));                                    \
+  if (Xt)                                                                                                       \
+    launch(k_head_logits<CFG, BLOCKS>, grid, dim3(CFG::NT), 0, s, rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, \
+           te);                                                                                                 \
+  else                                                                                                          \
+    launch(k_head_logits<CFG, LINES>, grid, dim3(CFG::NT), 0, s, rows, row0, tb, X, K, W, V, K, c, stat, ntile, E, lde, te)
   QLORA_HEAD_TILES(tb, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();
 }
 
-hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde,
+hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
                           hipStream_t s) {
   const int bn = head_tile_rows(tb);
@@ -529,19 +549,19 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
     const int64_t items = t * ((K + BM - 1) / BM) * head_dx_ranges(t * bn, K, lde, bn);
     most = items > most ? items : most;
   }
-#define QLORA_CALL(CFG)                                                                                          \
-  launch(k_head_dx<CFG>, dim3((unsigned)items8(most)), dim3(CFG::NT), 0, s, rows, row0, tb, E, lde, W, V, K, scale, part, \
+#define QLORA_CALL(CFG)                                                                                              \
+  launch(k_head_dx<CFG>, dim3((unsigned)items8(most)), dim3(CFG::NT), 0, s, rows, row0, tb, E, lde, te, W, V, K, scale, part, \
          dX)
   QLORA_HEAD_TILES(tb, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();
 }
 
-hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde,
-                          const bf16_t *Xs, int64_t V, int64_t K, const bf16_t *zero, float *sums, bool first,
-                          bool last, bf16_t *dW, hipStream_t s) {
+hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
+                          const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,
+                          hipStream_t s) {
   launch(k_head_dw<H256>, dim3((unsigned)items8(((K + BM - 1) / BM) * ((V + 255) / 256))), dim3(H256::NT), 0, s, rows,
-         row0, tb, E, lde, Xs, V, K, zero, sums, first ? 1 : 0, last ? 1 : 0, dW);
+         row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, dW);
   return hipGetLastError();
 }
 

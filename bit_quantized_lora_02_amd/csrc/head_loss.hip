@@ -66,6 +66,15 @@ __device__ __forceinline__ void dots(const bf16_t *__restrict__ x, const bf16_t 
   for (int j = 0; j < N; ++j) out[j] = wave_sum(out[j]);
 }
 
+// One row x to the blocks of 32 columns that the logit product reads: piece r of it to xt[r][ldx][32], zeros past K.
+__device__ __forceinline__ void block_row(const bf16_t *__restrict__ x, int64_t K, int lane, bf16_t *__restrict__ xt,
+                                          int64_t ldx) {
+  for (int64_t at = 8 * lane; at < (K + 31) / 32 * 32; at += 512) {
+    const u32x4_t v = at < K ? *reinterpret_cast<const u32x4_t *>(x + at) : u32x4_t{0u, 0u, 0u, 0u};
+    *reinterpret_cast<u32x4_t *>(xt + at / 32 * ldx * 32 + at % 32) = v;
+  }
+}
+
 // Workgroup 0 numbers the rows that count, in order; the others take rows of X (cross entropy: one per wave,
 // distillation: one per workgroup): the targets' logits by dot products (binary32 FMA), the teacher's softmax, or,
 // for a row that does not count, its zeros.
@@ -75,12 +84,13 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
                                                             const int32_t *__restrict__ index,
                                                             const float *__restrict__ logit, int k, float tau,
                                                             int32_t *__restrict__ n, int32_t *__restrict__ list,
+                                                            int32_t *__restrict__ ranges, HeadBlocks blocks,
                                                             HeadRows rows, float *__restrict__ loss,
-                                                            bf16_t *__restrict__ dX, uint32_t *__restrict__ zero) {
+                                                            bf16_t *__restrict__ dX, bf16_t *__restrict__ Xt,
+                                                            int64_t ldx) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (blockIdx.x == 0) {
     __shared__ int s_wave[kPrepThreads / 64];
-    if (tid < 64) zero[tid] = 0u;
     int base = 0;
     for (int64_t t0 = 0; t0 < T; t0 += kPrepThreads * kScanRows) {
       const int64_t mine = t0 + (int64_t)tid * kScanRows;
@@ -110,6 +120,11 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
       __syncthreads();
     }
     if (tid == 0) *n = base;
+    for (int64_t b = tid; b < blocks.count; b += kPrepThreads) {
+      const int64_t row0 = b * blocks.tb, tb = T - row0 < blocks.tb ? T - row0 : blocks.tb;
+      const int64_t have = base - row0 < tb ? base - row0 : tb;
+      ranges[b] = have > 0 ? head_dx_ranges(have, K, blocks.lde, head_tile_rows(tb)) : 1;
+    }
     return;
   }
   if (labels) {
@@ -120,6 +135,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
       const bf16_t *const w[1] = {W + y * K};
       float z[1];
       dots<1>(X + t * K, w, K, lane, z);
+      if (Xt) block_row(X + t * K, K, lane, Xt + t * 32, ldx);
       if (lane == 0) {
         rows.ref[t] = z[0];
         rows.refcol[t] = (int32_t)y;
@@ -135,6 +151,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
   }
   __shared__ float s_z[256];
   const int64_t t = blockIdx.x - 1;
+  if (Xt && wave == 3) block_row(X + t * K, K, lane, Xt + t * 32, ldx);
   const int32_t *idx = index + t * k;
   for (int i0 = 4 * wave; i0 < k; i0 += 4 * (kPrepThreads / 64)) {
     const bf16_t *w[4];
@@ -204,7 +221,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
                                                       const int32_t *__restrict__ index, int k, float tau,
                                                       const float *__restrict__ weight, float *__restrict__ loss,
                                                       float *__restrict__ scale, bf16_t *__restrict__ E, int64_t lde,
-                                                      const bf16_t *__restrict__ X, int64_t K,
+                                                      int64_t te, const bf16_t *__restrict__ X, int64_t K,
                                                       bf16_t *__restrict__ Xs) {
   const int lane = threadIdx.x & 63;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // row of the block
@@ -234,14 +251,14 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   S = rest + eref;
   if (lane == 0) loss[t] = tau * tau * (rows.h[t] + nlogq);
   if (!E) return;
-  bf16_t *e = E + i * lde;
+  auto e = [&](int64_t v) { return E + (v / 32 * te + i) * 32 + v % 32; };
   if (wide) {  // bring the row's tiles to one unit (a factor below binary32's range is applied in two halves)
     for (int64_t at = 8 * lane; at < lde; at += 512) {
       const float d = exp2f(0.5f * (st[at / kHeadTile].x - u) * c);
-      u32x4_t v = *reinterpret_cast<u32x4_t *>(e + at);
+      u32x4_t v = *reinterpret_cast<u32x4_t *>(e(at));
 #pragma unroll
       for (int w = 0; w < 4; ++w) v[w] = pack_bf16x2(bf16_lo_to_f32(v[w]) * d * d, bf16_hi_to_f32(v[w]) * d * d);
-      *reinterpret_cast<u32x4_t *>(e + at) = v;
+      *reinterpret_cast<u32x4_t *>(e(at)) = v;
     }
     __threadfence_block();  // the targets' entries below follow these stores
   }
@@ -249,7 +266,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   if (lane == 0) scale[i] = f;
   const int32_t rc = rows.refcol[t];
   if (labels) {
-    if (lane == 0) e[rc] = f32_to_bf16(-rest);
+    if (lane == 0) *e(rc) = f32_to_bf16(-rest);
   } else {
     for (int i0 = 0; i0 < k; i0 += 64) {
       const int me = i0 + lane;
@@ -257,7 +274,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
       float P = 0.f;  // all of the row's probability at this column
       for (int j = 0; j < k; ++j) P += index[t * k + j] == v ? rows.pt[t * k + j] : 0.f;
       if (target_ok(v, V))
-        e[v] = f32_to_bf16(v == rc ? eref * (1.f - P) - P * rest : exp2f((rows.zt[t * k + me] - u) * c) - P * S);
+        *e(v) = f32_to_bf16(v == rc ? eref * (1.f - P) - P * rest : exp2f((rows.zt[t * k + me] - u) * c) - P * S);
     }
   }
   if (Xs)  // rows of X times the row factor: the dW product's second operand, rounded to bf16 for the matrix unit
@@ -270,13 +287,13 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
 }
 
 // dX rows of the block from the ranges' partial sums part[range][row of the block][K], added in range order.
-__global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0, int64_t tb, int tile_rows,
-                                                     const float *__restrict__ part, int64_t K, int64_t lde,
+__global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0, int64_t tb,
+                                                     const float *__restrict__ part, int64_t K,
                                                      const float *__restrict__ scale, bf16_t *__restrict__ dX) {
   int64_t n = *rows.n - row0;
   n = n < tb ? n : tb;
   if (n <= 0) return;
-  const int ranges = head_dx_ranges(n, K, lde, tile_rows);
+  const int ranges = *rows.ranges;
   if (ranges == 1) return;  // the product wrote dX itself
   const int64_t per = K / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= n * per) return;
@@ -301,26 +318,27 @@ __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0
 
 hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t V, int64_t K, const int64_t *labels,
                             const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
-                            const HeadRows &rows, float *loss, bf16_t *dX, uint32_t *zero, hipStream_t s) {
+                            int32_t *ranges, const HeadBlocks &blocks, const HeadRows &rows, float *loss, bf16_t *dX,
+                            bf16_t *Xt, int64_t ldx, hipStream_t s) {
   const int64_t wgs = labels ? (T + 3) / 4 : T;
   launch(k_head_prep, dim3((unsigned)(1 + wgs)), dim3(kPrepThreads), 0, s, X, T, W, V, K, labels, index, logit, k, tau,
-         n, list, rows, loss, dX, zero);
+         n, list, ranges, blocks, rows, loss, dX, Xt, ldx);
   return hipGetLastError();
 }
 
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
-                               const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde,
+                               const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde, int64_t te,
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s) {
   launch(k_head_combine, dim3((unsigned)((tb + 3) / 4)), dim3(256), 0, s, rows, row0, stat, ntile, V, labels, index, k,
-         tau, weight, loss, scale, E, lde, X, K, Xs);
+         tau, weight, loss, scale, E, lde, te, X, K, Xs);
   return hipGetLastError();
 }
 
-hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t V, int64_t K,
-                              int64_t lde, const float *scale, bf16_t *dX, hipStream_t s) {
-  launch(k_head_reduce, dim3((unsigned)((tb * (K / 8) + 255) / 256)), dim3(256), 0, s, rows, row0, tb,
-         head_tile_rows(tb), part, K, lde, scale, dX);
+hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t K,
+                              const float *scale, bf16_t *dX, hipStream_t s) {
+  launch(k_head_reduce, dim3((unsigned)((tb * (K / 8) + 255) / 256)), dim3(256), 0, s, rows, row0, tb, part, K, scale,
+         dX);
   return hipGetLastError();
 }
 

@@ -361,7 +361,7 @@ int qlora_adamw8_step(const qlora_adamw8_tensor *tensors, int32_t count, double 
  *
  * X, W, dX, dW 16-byte aligned, labels 8-byte, loss and weight 4-byte; none
  * may overlap an output.  n_in % 8 == 0, n_vocab >= 1, both at most 2^22,
- * n_vocab * n_in <= 2^34, T <= 2^22, T * n_in < 2^32.  ws: at least
+ * n_vocab * n_in <= 2^34, T <= 2^22, T * n_in < 2^31.  ws: at least
  * qlora_head_workspace_bytes(T, n_vocab, n_in, 0, dX != NULL, dW != NULL),
  * 256-byte aligned; nothing in it needs to start at zero, and calls that
  * overlap in time need workspaces of their own.  The call can be captured into

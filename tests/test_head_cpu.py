@@ -35,7 +35,7 @@ SHARED = [
     (dict(T=-1), "T must"), (dict(T=(1 << 22) + 1), "T must"),
     (dict(V=0), "n_vocab"), (dict(V=(1 << 22) + 1), "n_vocab"),
     (dict(K=0), "multiple of 8"), (dict(K=60), "multiple of 8"), (dict(K=(1 << 22) + 8), "2^22"),
-    (dict(V=1 << 21, K=1 << 14), "2^34"), (dict(T=1 << 20, K=1 << 12), "2^32"),
+    (dict(V=1 << 21, K=1 << 14), "2^34"), (dict(T=1 << 20, K=1 << 11), "2^31"),
     (dict(X=None), "X and loss"), (dict(loss=None), "X and loss"), (dict(W=None), "W must"),
     (dict(X=MIS), "16-byte"), (dict(W=MIS), "16-byte"), (dict(dX=MIS), "16-byte"), (dict(dW=MIS), "16-byte"),
     (dict(loss=ODD), "4-byte"), (dict(weight=ODD), "4-byte"),
