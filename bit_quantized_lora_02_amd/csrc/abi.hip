@@ -424,7 +424,7 @@ constexpr size_t kHeadBlockBytes = (size_t)1 << 30;
 struct HeadPlan {
   HeadBlocks b = {};
   int64_t ntile = 0;
-  int64_t ldx = 0;  // rows per block of the laid out X (0: it is read as it is)
+  int64_t ldx = 0;  // rows per block of the laid out X
   size_t off_n = 0, off_ranges = 0, off_xt = 0, off_list = 0, off_ref = 0, off_col = 0, off_h = 0, off_zt = 0, off_pt = 0,
          off_stat = 0, off_scale = 0, off_e = 0, off_part = 0, off_xs = 0, off_sums = 0, total = 0;
   bool split = false;  // dX may come as partial sums
@@ -442,8 +442,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   p.b.tb = p.b.count == 1 ? (T < 1 ? 1 : T) : (int64_t)up((size_t)ceil_div(T, p.b.count), 256);
   p.b.count = T < 1 ? 1 : ceil_div(T, p.b.tb);
   p.b.te = (int64_t)up((size_t)p.b.tb, 16);
-  // up to 64 rows the logits are bound by the stream of W and take X as it is
-  p.ldx = head_tile_rows(p.b.tb) > 64 ? (int64_t)up((size_t)T, 16) : 0;
+  p.ldx = (int64_t)up((size_t)T, 16);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -452,7 +451,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   };
   p.off_n = take(4);
   p.off_ranges = take((size_t)p.b.count * 4);
-  if (p.ldx) p.off_xt = take((size_t)ceil_div(K, 32) * p.ldx * 64);
+  p.off_xt = take((size_t)ceil_div(K, 128) * p.ldx * 256);
   p.off_list = take((size_t)T * 4);
   p.off_ref = take((size_t)T * 4);
   p.off_col = take((size_t)T * 4);
@@ -470,7 +469,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
     p.off_part = take(part);
   }
   if (dw) {
-    p.off_xs = take((size_t)p.b.tb * K * 2);
+    p.off_xs = take(up((size_t)p.b.tb, 128) * K * 2);
     if (p.b.count > 1) p.off_sums = take((size_t)V * K * 4);
   }
   p.total = off;
@@ -527,7 +526,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   float *part = p.split ? (float *)(w + p.off_part) : nullptr;
   bf16_t *Xs = dW ? (bf16_t *)(w + p.off_xs) : nullptr;
   float *sums = p.off_sums ? (float *)(w + p.off_sums) : nullptr;
-  bf16_t *Xt = p.ldx ? (bf16_t *)(w + p.off_xt) : nullptr;
+  bf16_t *Xt = (bf16_t *)(w + p.off_xt);
   int32_t *ranges = (int32_t *)(w + p.off_ranges);
   const float c = 1.44269504f / tau;
   const int64_t lde = p.b.lde, te = p.b.te;
@@ -536,14 +535,14 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   for (int64_t b = 0; b < p.b.count; ++b) {
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
     rows.ranges = ranges + b;
-    if (tb > 0) {
-      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, X, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, s));
+    if (tb > 0)
+      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, s));
+    if (tb > 0 || dW)
       LAUNCH("head_combine", launch_head_combine(rows, row0, tb, stat, p.ntile, V, labels, index, k, tau, weight, loss,
                                                  scale, E, lde, te, X, K, Xs, s));
-      if (dX) {
-        LAUNCH("head_dx", launch_head_dx(rows, row0, tb, E, lde, te, W, V, K, scale, part, dX, s));
-        if (part) LAUNCH("head_dx_reduce", launch_head_reduce(rows, row0, tb, part, K, scale, dX, s));
-      }
+    if (tb > 0 && dX) {
+      LAUNCH("head_dx", launch_head_dx(rows, row0, tb, E, lde, te, W, V, K, scale, part, dX, s));
+      if (part) LAUNCH("head_dx_reduce", launch_head_reduce(rows, row0, tb, part, K, scale, dX, s));
     }
     if (dW)
       LAUNCH("head_dw",

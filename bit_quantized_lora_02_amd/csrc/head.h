@@ -28,7 +28,7 @@ struct HeadRows {
 // Columns of W (rows of the output layer) per tile of the logit product, and the row statistics' unit.
 constexpr int kHeadTile = 256;
 // Rows of E are padded with zero columns to a multiple of this.
-constexpr int kHeadPad = 64;
+constexpr int kHeadPad = 128;
 // A logit may exceed the row's reference by 2^kHeadRange before the tile takes a unit of its own.
 constexpr float kHeadRange = 40.f;
 
@@ -73,15 +73,16 @@ hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, co
 __host__ __device__ inline int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
 // Largest size in floats of the dX product's partial sums over all row counts up to tb (0: never split).
 size_t head_part_floats(int64_t tb, int64_t K, int64_t lde);
-// Ranges of the dX product of n rows.
+// Ranges of the dX product of n rows: all of the same length but the last, none empty.
 __host__ __device__ inline int head_dx_ranges(int64_t n, int64_t K, int64_t lde, int tile_rows) {
   const int64_t tiles = ((n + tile_rows - 1) / tile_rows) * ((K + 255) / 256);
-  return head_split(tiles, lde / 64, tile_rows == 64 ? 512 : 256, 256 * tile_rows);
+  const int fours = (int)(lde / 128), s = head_split(tiles, lde / 64, tile_rows == 64 ? 512 : 256, 256 * tile_rows);
+  const int per = (fours + s - 1) / s;
+  return (fours + per - 1) / per;
 }
 
-// The logits take X as it is (Xt NULL) or as k_head_prep lays it out: Xt [K / 32 rounded up][ldx][32], zero past K.
-hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *X, const bf16_t *Xt,
-                              int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
+// The logits take X as k_head_prep lays it out: Xt [4 (K / 128 rounded up)][ldx][32], zero past K.
+hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
                               bf16_t *E, int64_t lde, int64_t te, hipStream_t s);
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,

@@ -43,6 +43,34 @@ using H64 = HeadCfg<4, 1, 2, 2>;   // 64 x 64 per wave, two workgroups per CU
 
 __device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0); }
 
+// The LDS tiles of one workgroup: slot i holds the m-side's tile and behind it the n-side's.  Each slot is an array
+// of its own, so that the compiler can tell reads of one from the direct copies into another and adds no waits.
+typedef __attribute__((address_space(3))) char lds_char;
+struct Ring {
+  lds_char *slot[STAGES];
+};
+#define QLORA_RING(C, ring)                                                                                     \
+  __shared__ __attribute__((aligned(1024))) char ring0[(BM + C::BN) * BK * 2], ring1[(BM + C::BN) * BK * 2],    \
+      ring2[(BM + C::BN) * BK * 2], ring3[(BM + C::BN) * BK * 2];                                               \
+  const Ring ring = {{(lds_char *)ring0, (lds_char *)ring1, (lds_char *)ring2, (lds_char *)ring3}}
+
+// Lane offsets into the slots.  An LDS instruction adds at most 65535 to its address register, so a lane keeps its
+// offset twice, plain for slots 0 and 1 and plus `kFar` for slots 2 and 3, whose constant then is slot - kFar: all the
+// reads of a tile share these registers.  The values are hidden from the compiler, which would otherwise keep a
+// register for every sum.
+constexpr int kFar = 65536;
+struct Lane {
+  int near, far;
+  __device__ __forceinline__ void set(int v) {
+    near = v, far = v + kFar;
+    asm("" : "+v"(near));
+    asm("" : "+v"(far));
+  }
+};
+__device__ __forceinline__ lds_char *in_slot(const Ring &ring, int slot, const Lane &l, int more) {
+  return slot < 2 ? ring.slot[slot] + l.near + more : ring.slot[slot] + l.far + (more - kFar);
+}
+
 // How an operand lies in memory (element (i, r): row or column i of the tile's side, reduction index r):
 //  LINES:   row-major [i][r].
 //  BLOCKS:  32 reduction indices at a time, [r / 32][i][32]: a step's tile is one contiguous piece, where LINES
@@ -52,9 +80,10 @@ __device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0
 enum { LINES, BLOCKS, ACROSS, BLOCKS_ACROSS };
 
 // One operand's tile of ROWS rows (columns for the ACROSS ones).  `ld` is the row length of a row-major matrix, the
-// number of rows in a block otherwise.  Rows may be gathered through `list`; those past the last one repeat it.
-// Reduction indices from the reduction's length on read as zero (BLOCKS are zero there in memory).  A step's
-// addresses are a wave-uniform base plus 32-bit lane offsets that do not change from step to step.
+// number of rows in a block otherwise.  BLOCKS rows are gathered through `list` if there is one; rows past the last
+// one repeat it.  Steps go to the next multiple of 128 reduction indices: indices past `red` repeat the last one (or
+// the last eight), and the other operand holds zeros there in memory.  A step's addresses are a wave-uniform base
+// plus 32-bit lane offsets.
 template <int ROWS, int NT, int KIND>
 struct Tile {
   static constexpr bool TR = KIND == ACROSS || KIND == BLOCKS_ACROSS;
@@ -64,84 +93,100 @@ struct Tile {
   static constexpr int RSTEP = NW * 64 / CH;
   static_assert(ROWS * BK / 8 % NT == 0 && LD >= 1, "unsupported tile");
   static_assert(!TR || (64 % CH == 0 && RSTEP % 4 == 0), "the copies of a thread share one swizzle");
-  const char *base;  // reduction index 0 of the tile
-  uint32_t off[TR ? 1 : LD];
-  int64_t ld;
-  int wave;
+  const char *base;
+  uint32_t off[TR ? 1 : LD];  // across: of the column
+  uint32_t k0;                // reduction index of the thread's first copy (rows: of all) within a step
+  uint32_t ld;
+  int red;
 
-  __device__ __forceinline__ void init(const bf16_t *src, int64_t ld_, int64_t first, int64_t count,
-                                       const int32_t *list, int w, int lane) {
-    ld = ld_, wave = w;
-    const int k0 = first_index(w, lane);
+  // XOR of the 64-byte group index of LDS row r: rows r .. r + 3 then start in different quarters of the 64 banks
+  static __device__ __forceinline__ int swz(int r) { return ROWS >= 128 ? (r & 3) : ((r >> 1) & 1); }
+
+  __device__ __forceinline__ void init(const bf16_t *src, int64_t ld_, int64_t first, int64_t count, int64_t red_,
+                                       const int32_t *list, int wave, int lane) {
+    ld = (uint32_t)ld_, red = (int)red_;
     if constexpr (!TR) {
+      k0 = 8 * ((lane & 3) ^ ((lane >> 4) & 3));  // the rows of a thread's copies are equal modulo 16
       const int64_t row = KIND == BLOCKS ? BK : ld;
       base = (const char *)(list ? src : src + first * row);
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int rr = 16 * (i * NW + w) + (lane >> 2);
+        const int rr = 16 * (i * NW + wave) + (lane >> 2);
         const int64_t at = first + rr < count ? rr : count - 1 - first;
-        off[i] = (uint32_t)(((list ? list[first + at] : at) * row + k0) * 2);
+        off[i] = (uint32_t)((list ? list[first + at] : at) * row * 2 + (KIND == BLOCKS ? k0 * 2 : 0));
       }
     } else {
+      k0 = wave * (64 / CH) + lane / CH;
       int64_t c = first + 8 * ((lane % CH) ^ (swz(k0) << 2));
       if (c > count - 8) c = count - 8;  // count % 8 == 0
       if constexpr (KIND == ACROSS) {
         base = (const char *)src;
-        off[0] = (uint32_t)((k0 * ld + c) * 2);
+        off[0] = (uint32_t)(c * 2);
       } else {
         base = (const char *)(src + first / 32 * ld * 32);
-        off[0] = (uint32_t)((((c - first) / 32 * ld + k0) * 32 + c % 32) * 2);
+        off[0] = (uint32_t)((c - first) / 32 * ld * 64 + c % 32 * 2);
       }
     }
   }
-  // XOR of the 64-byte group index of LDS row r: rows r .. r + 3 then start in different quarters of the 64 banks
-  static __device__ __forceinline__ int swz(int r) { return ROWS >= 128 ? (r & 3) : ((r >> 1) & 1); }
-  // Reduction index within a step of this thread's first copy (rows: of all, their rows / 4 are equal modulo 4).
-  static __device__ __forceinline__ int first_index(int w, int lane) {
-    return TR ? w * (64 / CH) + lane / CH : 8 * ((lane & 3) ^ ((lane >> 4) & 3));
-  }
-  __device__ __forceinline__ const char *at(int64_t step) const {
-    return base + step * (KIND == ACROSS || KIND == BLOCKS ? ld * (2 * BK) : KIND == LINES ? 2 * BK : 64 * BK);
-  }
-  __device__ __forceinline__ int64_t next(int i) const {  // bytes from an across operand's first copy to copy i
-    return KIND == ACROSS ? i * (ld * (2 * RSTEP)) : KIND == BLOCKS_ACROSS ? i * 64 * RSTEP : 0;
-  }
-  // Copy i of this thread.  (Buffer loads take the uniform part of the address in scalar registers; the descriptor
-  // spans all of memory behind the base, every address is inside the operand by construction.)
-  __device__ __forceinline__ void issue(int64_t step, int i, bf16_t *s) const {
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)at(step), 0, -1, 0x00020000);
+  // Copy i of this thread of the tile of step `s`.  (Buffer loads take the uniform part of the address in scalar
+  // registers; the descriptor spans all of memory behind the base, every address is inside the operand by
+  // construction.)
+  __device__ __forceinline__ void copy(int s, int i, lds_char *to, int wave) const {
+    const char *b = base;
+    uint32_t o;
+    if constexpr (KIND == LINES) {
+      o = off[i] + 2 * min(k0 + s * BK, (uint32_t)red - 8);
+    } else if constexpr (KIND == BLOCKS) {
+      b += (int64_t)s * ld * (2 * BK);
+      o = off[i];
+    } else if constexpr (KIND == ACROSS) {  // ld * 2 < 2^24
+      const int r0 = min(s * BK, max(red - BK, 0));
+      b += (int64_t)r0 * ld * 2;
+      o = off[0] + __umul24(min(k0 + (i * RSTEP + s * BK - r0), (uint32_t)(red - 1 - r0)), ld * 2);
+    } else {
+      o = off[0] + 64 * min(k0 + (i * RSTEP + s * BK), (uint32_t)red - 1);
+    }
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)b, 0, -1, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rsrc, (__attribute__((address_space(3))) void *)(s + (i * NW + wave) * 512), 16, off[TR ? 0 : i], (int)next(i),
-        0, 0);
+        rsrc, (__attribute__((address_space(3))) void *)(to + (i * NW + wave) * 1024), 16, o, 0, 0, 0);
   }
-  // The last step of a reduction that is no multiple of 32 deep: through registers, `left` < 32 indices remain.
-  __device__ __forceinline__ void issue_part(int64_t step, int left, bf16_t *s) const {
-    const int lane = threadIdx.x & 63, k0 = first_index(wave, lane);
+};
+
+// Reads of the MFMA operands of one side: N tiles of 32 rows (columns) from `first` of a ROWS-wide tile that starts
+// `base` bytes into its slot.
+template <int ROWS, int N, bool TR>
+struct Operand {
+  // rows: [row][32], the 16-byte chunk swizzled; the two halves of a step differ in one bit of the chunk.
+  // across: [32][ROWS]: in each 16-lane group, lane i of a transposing read gets element (i & 3) of the 8 bytes
+  // addressed by lane 4 m + (i >> 2), so lane a points at row base + (a >> 2), columns 4 (a & 3) .. + 3, and the reads
+  // of rows + 0..3 and + 4..7 give its 8 reduction values; the 64-byte group of tile i is swizzled, so each needs its
+  // own offset (i of the first two bits; first is a multiple of 32 N).
+  static constexpr int NO = TR ? N : 2;
+  Lane at[NO];
+  __device__ __forceinline__ void init(int base, int first, int lane) {
+    if constexpr (!TR) {
+      const int r = lane & 31, chunk = (lane >> 5) ^ ((r >> 2) & 3);
+      at[0].set(base + (first + r) * 64 + chunk * 16);
+      at[1].set(base + (first + r) * 64 + (chunk ^ 2) * 16);
+    } else {
+      const int grp = lane >> 4, ai = lane & 15;
+      const int r = 8 * (grp >> 1) + (ai >> 2);
+      const int swz = ROWS >= 128 ? (r & 3) : ((r >> 1) & 1);
 #pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      u32x4_t v = u32x4_t{0u, 0u, 0u, 0u};
-      if (KIND == BLOCKS || k0 + (TR ? i * RSTEP : 0) < left)
-        v = *reinterpret_cast<const u32x4_t *>(at(step) + off[TR ? 0 : i] + next(i));
-      *reinterpret_cast<u32x4_t *>(s + (i * NW + wave) * 512 + lane * 8) = v;
+      for (int i = 0; i < N; ++i)
+        at[i].set(base + (r * ROWS + ((first + 32 * i) ^ (swz << 5)) + 16 * (grp & 1) + 4 * (ai & 3)) * 2);
     }
   }
-  // MFMA operand of the 32 rows from `at`, reduction 16 kk .. 16 kk + 15 of the step
-  static __device__ __forceinline__ u32x4_t read(const bf16_t *s, int at, int kk, int lane) {
+  // tile i, reduction indices 16 kk .. 16 kk + 15 of the step
+  __device__ __forceinline__ u32x4_t read(const Ring &ring, int slot, int kk, int i) const {
     if constexpr (!TR) {
-      const int r = at + (lane & 31), chunk = kk * 2 + (lane >> 5);
-      return *reinterpret_cast<const u32x4_t *>(s + r * BK + ((chunk ^ ((r >> 2) & 3)) << 3));
+      return *(const __attribute__((address_space(3))) u32x4_t *)in_slot(ring, slot, at[kk], i * 32 * 64);
     } else {
-      // In each 16-lane group, lane i of a transposing read gets element (i & 3) of the 8 bytes addressed by lane
-      // 4 m + (i >> 2): lane a points at row base + (a >> 2), columns 4 (a & 3) .. + 3, and the reads of rows + 0..3
-      // and + 4..7 give its 8 reduction values.
       typedef short s4_t __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s4_t lds_s4;
-      const int grp = lane >> 4, ai = lane & 15;
-      const int r = kk * 16 + 8 * (grp >> 1) + (ai >> 2);
-      const int c = at + 16 * (grp & 1) + 4 * (ai & 3);
-      const int off = r * ROWS + (c ^ (swz(r) << 5));  // r and r + 4 have the same swizzle
-      const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(s + off));
-      const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(s + off + 4 * ROWS));
+      const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)in_slot(ring, slot, at[i], kk * 32 * ROWS));
+      const s4_t hi =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)in_slot(ring, slot, at[i], kk * 32 * ROWS + 8 * ROWS));
       const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
       return u32x4_t{l2.x, l2.y, h2.x, h2.y};
     }
@@ -151,162 +196,160 @@ struct Tile {
 template <class C>
 using Acc = f32x16_t[C::WM][C::WN];
 
-// The LDS tiles of one workgroup.  Each is an array of its own, so that the compiler can tell reads of one from the
-// direct copies into another and adds no waits.
-template <class C>
-struct Ring {
-  bf16_t *a[STAGES], *b[STAGES];
-};
-#define QLORA_RING(C, ring)                                                                            \
-  __shared__ __attribute__((aligned(16))) bf16_t ra0[BM * BK], ra1[BM * BK], ra2[BM * BK], ra3[BM * BK];   \
-  __shared__ __attribute__((aligned(16))) bf16_t rb0[C::BN * BK], rb1[C::BN * BK], rb2[C::BN * BK], rb3[C::BN * BK]; \
-  const Ring<C> ring = {{ra0, ra1, ra2, ra3}, {rb0, rb1, rb2, rb3}}
-
-// Wait until at most VM vector-memory operations are in flight and all LDS operations are done, then meet the
-// workgroup's other waves (without the full memory fence of __syncthreads, which would wait for every copy).
+// Meet the workgroup's other waves once this one's LDS operations are done, without the full memory fence of
+// __syncthreads, which would wait for every copy in flight.
 // s_waitcnt fields: vmcnt[3:0] and [15:14], expcnt[6:4] (7 = no wait), lgkmcnt[11:8].
-template <int VM>
 __device__ __forceinline__ void meet() {
-  __builtin_amdgcn_s_waitcnt((VM & 15) | (VM >> 4 << 14) | 0x0070);
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-// The reduction over steps [s0, s1) into acc; `red` is the reduction's length.
+// This wave's copies have landed (before the epilogue's stores are issued, so that only the copies are waited for).
+__device__ __forceinline__ void arrive() {
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0
+  asm volatile("" ::: "memory");
+}
+
+// Output tiles ("items") are numbered so that each XCD (workgroups go round the 8 XCDs) takes a run of consecutive
+// ones, and consecutive ones are blocks of 4 m-tiles x all n-tiles: the 32 workgroups of an XCD then share 4 + 8
+// operand tiles.  Workgroup w takes the items of lin = w, w + gridDim, ...
+struct Items {
+  int tiles_m, tiles_n, ranges;
+  int m, n, range;
+  __device__ __forceinline__ bool take(uint32_t lin) {
+    const uint32_t total = (uint32_t)tiles_m * tiles_n * ranges, per = (total + 7) / 8, id = (lin & 7) * per + (lin >> 3);
+    if ((lin >> 3) >= per || id >= total) return false;
+    const uint32_t plane = (uint32_t)tiles_m * tiles_n, in = id % plane;
+    const uint32_t band = in / (4u * tiles_n), left = in - band * 4u * tiles_n;
+    const uint32_t wide = min(tiles_m - band * 4, 4u);
+    range = id / plane;
+    m = band * 4 + left % wide;
+    n = left / wide;
+    return true;
+  }
+};
+
+// A workgroup's loop over its items, each a reduction over steps [s0, s1) of both operands' tiles, a multiple of four.
 //
 // Step s multiplies the tiles of slot s % 4 while the copies of steps s + 1 .. s + 3 are in flight.  Its first MFMAs'
 // operands are in registers; the second half's are read under them; then the waves meet (every wave holds the last
 // operands of slot s, and step s + 1 has landed), read the first operands of step s + 1 and run the second half's
 // MFMAs.  The copies of step s + 3 (into the slot of step s - 1, which all waves have left) are issued one at a time
 // between the MFMAs: issued together they would hold the waves up for as long as the load unit takes to accept them.
-template <class C, int KA, int KB>
-__device__ __forceinline__ void reduce_steps(const Tile<BM, C::NT, KA> &ta, const Tile<C::BN, C::NT, KB> &tb,
-                                             int64_t red, int64_t s0, int64_t s1, const Ring<C> &ring, int wm, int wn, int lane,
-                                             Acc<C> &acc) {
+// The last three steps of an item copy the first three of the next one, so the ring never drains and an item's
+// epilogue hides the first latency of the next.
+//
+//  setup(ta, tb, s0, s1): the tiles and steps of the item just taken     begin(): notes for its epilogue
+//  finish(acc): its epilogue; calls arrive() before its first store
+template <class C, int KA, int KB, class Setup, class Begin, class Finish>
+__device__ __forceinline__ void products(Items &items, const Ring &ring, int wave, int lane, Setup setup, Begin begin,
+                                         Finish finish) {
   typedef Tile<BM, C::NT, KA> TileA;
   typedef Tile<C::BN, C::NT, KB> TileB;
   constexpr int L = TileA::LD + TileB::LD, L1 = L / 2;  // copies per thread and step, those before the meeting
+  static_assert(2 * L < 64, "copies in flight are counted in six bits");
+  uint32_t lin = blockIdx.x;
+  if (!items.take(lin)) return;
+  TileA ta;
+  TileB tb;
+  int s0, s1;
+  setup(ta, tb, &s0, &s1);
+  Operand<BM, C::WM, TileA::TR> oa;
+  Operand<C::BN, C::WN, TileB::TR> ob;
+  oa.init(0, wave / C::WAVES_N * C::WM * 32, lane);
+  ob.init(BM * BK * 2, wave % C::WAVES_N * C::WN * 32, lane);
+  auto copies = [&](int s, int slot, int q0, int q1) {
 #pragma unroll
-  for (int i = 0; i < C::WM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::WN; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-  if (s0 >= s1) return;
-  u32x4_t a[2][C::WM], b[2][C::WN];
-  auto read = [&](int slot, int kk) {
-#pragma unroll
-    for (int i = 0; i < C::WM; ++i) a[kk][i] = TileA::read(ring.a[slot], (wm * C::WM + i) * 32, kk, lane);
-#pragma unroll
-    for (int j = 0; j < C::WN; ++j) b[kk][j] = TileB::read(ring.b[slot], (wn * C::WN + j) * 32, kk, lane);
-  };
-  auto copy = [&](int64_t s, int slot, int q) {
-    if (q < TileA::LD)
-      ta.issue(s, q, ring.a[slot]);
-    else
-      tb.issue(s, q - TileA::LD, ring.b[slot]);
-  };
-  auto copy_all = [&](int64_t s, int slot) {
-    if ((s + 1) * BK <= red) {
-#pragma unroll
-      for (int q = 0; q < L; ++q) copy(s, slot, q);
-    } else {
-      ta.issue_part(s, (int)(red - s * BK), ring.a[slot]);
-      tb.issue_part(s, (int)(red - s * BK), ring.b[slot]);
-    }
-  };
-  // the MFMAs of half kk with copies [q0, q1) of step s spread among them
-  auto mma = [&](int kk, int64_t s, int slot, int q0, int q1) {
-#pragma unroll
-    for (int i = 0; i < C::WM; ++i) {
-#pragma unroll
-      for (int j = 0; j < C::WN; ++j) acc[i][j] = mfma_32x32x16(a[kk][i], b[kk][j], acc[i][j]);
+    for (int q = q0; q < q1; ++q) {
+      if (q < TileA::LD)
+        ta.copy(s, q, ring.slot[slot], wave);
+      else
+        tb.copy(s, q - TileA::LD, ring.slot[slot] + BM * BK * 2, wave);
       fence_sched();
-#pragma unroll
-      for (int q = q0 + (q1 - q0) * i / C::WM; q < q0 + (q1 - q0) * (i + 1) / C::WM; ++q) {
-        copy(s, slot, q);
-        fence_sched();
-      }
     }
   };
-  const int64_t whole = red / BK < s1 ? red / BK : s1;  // steps before this one are full
 #pragma unroll
-  for (int q = 0; q < STAGES - 1; ++q)
-    if (s0 + q < s1) copy_all(s0 + q, q);
-  if (s0 + STAGES - 1 <= whole)
-    meet<2 * L>();
-  else
-    meet<0>();
-  read(0, 0);
-  // steady state: copies of step s + 3 are issued, those of s + 2 and the first ones of s + 3 stay in flight
-  auto step = [&](auto pc, int64_t s) {
-    constexpr int P = decltype(pc)::value;
-    read(P, 1);
-    fence_sched();
-    mma(0, s + 3, (P + 3) % STAGES, 0, L1);
-    meet<L + L1>();
-    read((P + 1) % STAGES, 0);
-    fence_sched();
-    mma(1, s + 3, (P + 3) % STAGES, L1, L);
-  };
-  // the last steps: at most a part step is still to be copied; everything is waited for
-  auto last = [&](auto pc, int64_t s) {
-    constexpr int P = decltype(pc)::value;
-    read(P, 1);
-    if (s + 3 < s1) copy_all(s + 3, (P + 3) % STAGES);
-    fence_sched();
-    mma(0, 0, 0, 0, 0);
-    meet<0>();
-    if (s + 1 < s1) read((P + 1) % STAGES, 0);
-    fence_sched();
-    mma(1, 0, 0, 0, 0);
-  };
-  int64_t s = s0;
-  for (; s + STAGES + 2 < whole; s += STAGES) {  // s + 3 + 3 < whole: four steady steps
-    step(std::integral_constant<int, 0>(), s);
-    step(std::integral_constant<int, 1>(), s + 1);
-    step(std::integral_constant<int, 2>(), s + 2);
-    step(std::integral_constant<int, 3>(), s + 3);
+  for (int q = 0; q < 3; ++q) copies(s0 + q, q, 0, L);
+  arrive();
+  for (;;) {
+    begin();
+    f32x16_t acc[C::WM][C::WN];
+#pragma unroll
+    for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::WN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    u32x4_t a[2][C::WM], b[2][C::WN];
+    auto read = [&](int slot, int kk) {
+#pragma unroll
+      for (int i = 0; i < C::WM; ++i) a[kk][i] = oa.read(ring, slot, kk, i);
+#pragma unroll
+      for (int j = 0; j < C::WN; ++j) b[kk][j] = ob.read(ring, slot, kk, j);
+      fence_sched();
+    };
+    // the MFMAs of half kk with copies [q0, q1) of step s spread among them
+    auto mma = [&](int kk, int s, int slot, int q0, int q1) {
+#pragma unroll
+      for (int i = 0; i < C::WM; ++i) {
+#pragma unroll
+        for (int j = 0; j < C::WN; ++j) acc[i][j] = mfma_32x32x16(a[kk][i], b[kk][j], acc[i][j]);
+        fence_sched();
+        copies(s, slot, q0 + (q1 - q0) * i / C::WM, q0 + (q1 - q0) * (i + 1) / C::WM);
+      }
+    };
+    // the step in slot P; `s` is the one to copy, `fresh`: the item's first two steps, whose successors are known to
+    // have landed (arrive()) while the last epilogue's stores may still be on their way
+    auto step = [&](auto pc, int s, bool fresh) {
+      constexpr int P = decltype(pc)::value, NEXT = (P + 1) % STAGES, TO = (P + 3) % STAGES;
+      read(P, 1);
+      mma(0, s, TO, 0, L1);
+      if (!(P < 2 && fresh)) __builtin_amdgcn_s_waitcnt(0x0f70 | (L + L1));  // step s + 2's and the first of s + 3's
+      meet();
+      read(NEXT, 0);
+      mma(1, s, TO, L1, L);
+    };
+    meet();
+    read(0, 0);
+    int s = s0;
+    for (; s + 4 < s1; s += 4) {
+      step(std::integral_constant<int, 0>(), s + 3, s == s0);
+      step(std::integral_constant<int, 1>(), s + 4, s == s0);
+      step(std::integral_constant<int, 2>(), s + 5, false);
+      step(std::integral_constant<int, 3>(), s + 6, false);
+    }
+    step(std::integral_constant<int, 0>(), s + 3, s == s0);
+    lin += gridDim.x;
+    const bool more = items.take(lin);
+    const bool fresh = s == s0;
+    if (more) setup(ta, tb, &s0, &s1);  // (else the first steps of this item are copied once more)
+    step(std::integral_constant<int, 1>(), s0, fresh);
+    step(std::integral_constant<int, 2>(), s0 + 1, false);
+    step(std::integral_constant<int, 3>(), s0 + 2, false);
+    finish(acc);
+    if (!more) return;
   }
-  for (; s < s1; s += STAGES) {
-    last(std::integral_constant<int, 0>(), s);
-    if (s + 1 < s1) last(std::integral_constant<int, 1>(), s + 1);
-    if (s + 2 < s1) last(std::integral_constant<int, 2>(), s + 2);
-    if (s + 3 < s1) last(std::integral_constant<int, 3>(), s + 3);
-  }
-  meet<0>();  // the tiles may be reused
 }
 
-// Work item of this workgroup: items are numbered so that each XCD (workgroups go round the 8 XCDs) takes a run of
-// consecutive ones, and consecutive ones are blocks of 4 m-tiles x all n-tiles: the 32 workgroups of an XCD then
-// share 4 + 8 operand tiles.
-struct Item {
-  int64_t m, n;
-  int range;
-};
-__device__ __forceinline__ bool item_of(int64_t tiles_m, int64_t tiles_n, int ranges, Item *it) {
-  const int64_t total = tiles_m * tiles_n * ranges, per = (total + 7) / 8;
-  const int64_t lin = blockIdx.x, id = (lin & 7) * per + (lin >> 3);
-  if ((lin >> 3) >= per || id >= total) return false;
-  const int64_t in = id % (tiles_m * tiles_n);
-  it->range = (int)(id / (tiles_m * tiles_n));
-  const int64_t band = in / (4 * tiles_n), left = in % (4 * tiles_n);
-  const int64_t wide = tiles_m - band * 4 < 4 ? tiles_m - band * 4 : 4;
-  it->m = band * 4 + left % wide;
-  it->n = left / wide;
-  return true;
+// Two lanes of a wave, l and l + 32, hold columns 0..3 and 4..7 of two groups of eight (lo and hi, packed bf16).
+// Afterwards l holds all eight of the first group, l + 32 of the second: 16 bytes to store each.
+__device__ __forceinline__ u32x4_t join_halves(const u32x2_t &lo, const u32x2_t &hi) {
+  const auto x = __builtin_amdgcn_permlane32_swap(lo.x, hi.x, false, false);
+  const auto y = __builtin_amdgcn_permlane32_swap(lo.y, hi.y, false, false);
+  return u32x4_t{x[0], y[0], x[1], y[1]};
 }
 
-__device__ __forceinline__ int64_t block_rows(const HeadRows &rows, int64_t row0, int64_t tb) {
+__device__ __forceinline__ int block_rows(const HeadRows &rows, int64_t row0, int64_t tb) {
   const int64_t n = *rows.n - row0;
-  return n < tb ? n : tb;
+  return n < 0 ? 0 : (int)(n < tb ? n : tb);
 }
 
 // ------------------------------------------------------------------ logits
 // m: columns of the vocabulary, n: counted rows of the block.
-// X row-major (LINES) or as k_head_prep lays it out (BLOCKS, ldx rows per block).
-template <class C, int KX>
+// X as k_head_prep lays it out (ldx rows per block).
+template <class C>
 __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t row0, int64_t tb,
                                                        const bf16_t *__restrict__ X, int64_t ldx,
                                                        const bf16_t *__restrict__ W, int64_t V, int64_t K, float c,
@@ -314,96 +357,98 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
                                                        bf16_t *__restrict__ E, int64_t lde, int64_t te) {
   QLORA_RING(C, ring);
   __shared__ float s_max[C::WAVES_M][C::BN], s_sum[C::WAVES_M][C::BN];
-  const int64_t n = block_rows(rows, row0, tb);
-  if (n <= 0) return;
-  Item it;
-  if (!item_of(ntile, (n + C::BN - 1) / C::BN, 1, &it)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = block_rows(rows, row0, tb);
+  if (n == 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
-  Tile<BM, C::NT, LINES> ta;
-  Tile<C::BN, C::NT, KX> tbl;
-  ta.init(W, K, m0, V, nullptr, wave, lane);
-  tbl.init(X, ldx, n0, n, rows.list + row0, wave, lane);
-  f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, LINES, KX>(ta, tbl, K, 0, (K + BK - 1) / BK, ring, wm, wn, lane, acc);
-
-  // element e of acc[i][j]: column m0 + mi + 8 (e / 4) + e % 4, row n0 + nj (nj per lane)
+  Items items = {(int)ntile, (n + C::BN - 1) / C::BN, 1};
+  int m0 = 0, n0 = 0;
+  auto setup = [&](Tile<BM, C::NT, LINES> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
+    ta.init(W, K, (int64_t)items.m * BM, V, K, nullptr, wave, lane);
+    tbl.init(X, ldx, (int64_t)items.n * C::BN, n, K, rows.list + row0, wave, lane);
+    *s0 = 0;
+    *s1 = (int)((K + 127) / 128 * 4);
+  };
+  auto begin = [&]() { m0 = items.m * BM, n0 = items.n * C::BN; };
+  // element e of acc[i][j]: column m0 + mlane + 32 i + 8 (e / 4) + e % 4 of the lane's row j
   const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
-  float ref[C::WN];
+  auto finish = [&](Acc<C> &acc) {
+    float ref[C::WN];
 #pragma unroll
-  for (int j = 0; j < C::WN; ++j) {
-    const int nj = (wn * C::WN + j) * 32 + (lane & 31);
-    const int64_t row = n0 + nj < n ? n0 + nj : n - 1;
-    const int64_t t = rows.list[row0 + row];
-    ref[j] = rows.ref[t];
-    const int64_t rc = rows.refcol[t] - m0;  // the reference's own column stays out of the sums
-    if (__any((rc >= 0 && rc < BM) || m0 + BM > V)) {
+    for (int j = 0; j < C::WN; ++j) {
+      const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
+      const int64_t t = rows.list[row0 + (row < n ? row : n - 1)];
+      ref[j] = rows.ref[t];
+      // the reference's own column and those past the vocabulary stay out of the sums
+      int rc = rows.refcol[t] - m0 - mlane, end = (int)(V - m0) - mlane;
+      if (__any((rc >= -4 && rc < BM) || m0 + BM > V)) {
+        asm("" : "+v"(rc), "+v"(end));
+#pragma unroll
+        for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int m = 32 * i + 8 * (e >> 2) + (e & 3);
+            acc[i][j][e] = (m == rc) | (m >= end) ? -INFINITY : acc[i][j][e];
+          }
+      }
+      float top = acc[0][j][0];
 #pragma unroll
       for (int i = 0; i < C::WM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int m = mlane + 32 * i + 8 * (e >> 2) + (e & 3);
-          if (m == rc || m0 + m >= V) acc[i][j][e] = -INFINITY;
-        }
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (lane < 32) s_max[wm][(wn * C::WN + j) * 32 + lane] = top;
     }
-    float top = acc[0][j][0];
+    arrive();
+    meet();
+    float u[C::WN];
 #pragma unroll
-    for (int i = 0; i < C::WM; ++i)
+    for (int j = 0; j < C::WN; ++j) {
+      const int nj = (wn * C::WN + j) * 32 + (lane & 31);
+      float top = s_max[0][nj];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
-    top = fmaxf(top, __shfl_xor(top, 32));
-    if (lane < 32) s_max[wm][nj] = top;
-  }
-  __syncthreads();
-  // E's tile is turned through the ring's arrays, 32 rows of 256 columns in each (the narrow tiles use the first ones)
-  auto stage = [&](int i) {
-    return i == 0 ? ra0 : i == 1 ? ra1 : i == 2 ? ra2 : i == 3 ? ra3 : i == 4 ? rb0 : i == 5 ? rb1 : i == 6 ? rb2 : rb3;
-  };
+      for (int w = 1; w < C::WAVES_M; ++w) top = fmaxf(top, s_max[w][nj]);
+      u[j] = (top - ref[j]) * c > kHeadRange ? top : ref[j];
+      float sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < C::WN; ++j) {
-    const int nj = (wn * C::WN + j) * 32 + (lane & 31);
-    float top = s_max[0][nj];
+      for (int i = 0; i < C::WM; ++i) {
 #pragma unroll
-    for (int w = 1; w < C::WAVES_M; ++w) top = fmaxf(top, s_max[w][nj]);
-    const float u = (top - ref[j]) * c > kHeadRange ? top : ref[j];
-    float sum = 0.f;
-    bf16_t *const srow = stage(nj >> 5) + (nj & 31) * BM;
-#pragma unroll
-    for (int i = 0; i < C::WM; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = __builtin_amdgcn_exp2f((acc[i][j][4 * q + e] - u) * c);
-          sum += p[e];
-        }
-        if (E) {  // 16-byte chunk index swizzled by the row: conflict-free here and in the row-wise reads below
-          const int m = mlane + 32 * i + 8 * q;
-          *reinterpret_cast<u32x2_t *>(srow + ((((m >> 3) ^ nj) & 31) << 3) + (m & 7)) =
-              u32x2_t{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
+        for (int e = 0; e < 16; ++e) {
+          acc[i][j][e] = __builtin_amdgcn_exp2f((acc[i][j][e] - u[j]) * c);
+          sum += acc[i][j][e];
         }
       }
-    sum += __shfl_xor(sum, 32);
-    if (lane < 32) s_sum[wm][nj] = sum;
-  }
-  __syncthreads();
-  if (tid < C::BN && n0 + tid < n) {
-    float top = s_max[0][tid], sum = s_sum[0][tid];
+      sum += __shfl_xor(sum, 32);
+      if (lane < 32) s_sum[wm][nj] = sum;
+      if (!E) continue;
+      // E lies in blocks of 32 columns, [column / 32][row][32]: a wave's store is 32 rows of 32 bytes
+      const int row = n0 + nj;
 #pragma unroll
-    for (int w = 1; w < C::WAVES_M; ++w) top = fmaxf(top, s_max[w][tid]), sum += s_sum[w][tid];
-    const float r = rows.ref[rows.list[row0 + n0 + tid]];
-    stat[(n0 + tid) * ntile + it.m] = make_float2((top - r) * c > kHeadRange ? top : r, sum);
-  }
-  if (!E) return;
-  // E lies in blocks of 32 columns, [column / 32][row][32]: 16 rows of a block are 1 KB
-  for (int at = tid; at < C::BN * 32; at += C::NT) {
-    const int nj = (at >> 2) % C::BN, chunk = at / (4 * C::BN) * 4 + (at & 3);
-    if (n0 + nj >= n || m0 + chunk * 8 >= lde) continue;
-    *reinterpret_cast<u32x4_t *>(E + ((m0 / 32 + (chunk >> 2)) * te + n0 + nj) * 32 + (chunk & 3) * 8) =
-        *reinterpret_cast<const u32x4_t *>(stage(nj >> 5) + (nj & 31) * BM + (((chunk ^ nj) & 31) << 3));
-  }
+      for (int i = 0; i < C::WM; ++i) {
+        bf16_t *const out = E + ((m0 / 32 + wm * C::WM + i) * te + row) * 32 + 8 * (lane >> 5);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const f32x16_t &v = acc[i][j];
+          const u32x4_t o = join_halves(
+              u32x2_t{pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3])},
+              u32x2_t{pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7])});
+          if (row < n && m0 + (wm * C::WM + i) * 32 < lde) *reinterpret_cast<u32x4_t *>(out + 16 * q) = o;
+        }
+      }
+    }
+    meet();
+    if (wm == 0 && lane < 32) {
+#pragma unroll
+      for (int j = 0; j < C::WN; ++j) {
+        const int nj = (wn * C::WN + j) * 32 + lane;
+        float sum = s_sum[0][nj];
+#pragma unroll
+        for (int w = 1; w < C::WAVES_M; ++w) sum += s_sum[w][nj];
+        if (n0 + nj < n) stat[(int64_t)(n0 + nj) * ntile + m0 / BM] = make_float2(u[j], sum);
+      }
+    }
+  };
+  products<C, LINES, BLOCKS>(items, ring, wave, lane, setup, begin, finish);
 }
 
 // ---------------------------------------------------------------------- dX
@@ -415,43 +460,56 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
                                                    const float *__restrict__ scale, float *__restrict__ part,
                                                    bf16_t *__restrict__ dX) {
   QLORA_RING(C, ring);
-  const int64_t n = block_rows(rows, row0, tb);
-  if (n <= 0) return;
+  const int n = block_rows(rows, row0, tb);
+  if (n == 0) return;
   const int ranges = *rows.ranges;
-  Item it;
-  if (!item_of((K + BM - 1) / BM, (n + C::BN - 1) / C::BN, ranges, &it)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
-  const int64_t steps = lde / BK, per = (steps + ranges - 1) / ranges;
-  const int64_t s0 = it.range * per, s1 = s0 + per < steps ? s0 + per : steps;
-  Tile<BM, C::NT, ACROSS> ta;
-  Tile<C::BN, C::NT, BLOCKS> tbl;
-  ta.init(W, K, m0, K, nullptr, wave, lane);
-  tbl.init(E, te, n0, n, nullptr, wave, lane);
-  f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, ACROSS, BLOCKS>(ta, tbl, V, s0, s1, ring, wm, wn, lane, acc);
+  Items items = {(int)((K + BM - 1) / BM), (n + C::BN - 1) / C::BN, ranges};
+  int m0 = 0, n0 = 0, range = 0;
+  auto setup = [&](Tile<BM, C::NT, ACROSS> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
+    ta.init(W, K, (int64_t)items.m * BM, K, V, nullptr, wave, lane);
+    tbl.init(E, te, (int64_t)items.n * C::BN, n, lde, nullptr, wave, lane);
+    const int fours = (int)(lde / 128), per = (fours + ranges - 1) / ranges;
+    *s0 = items.range * per * 4;
+    *s1 = min(*s0 + per * 4, fours * 4);
+  };
+  auto begin = [&]() { m0 = items.m * BM, n0 = items.n * C::BN, range = items.range; };
+  auto finish = [&](Acc<C> &acc) {
+    arrive();
 #pragma unroll
-  for (int j = 0; j < C::WN; ++j) {
-    const int64_t i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
-    if (i >= n) continue;
-    const float f = ranges > 1 ? 1.f : scale[i];
-    bf16_t *const out = dX + (int64_t)rows.list[row0 + i] * K;
-    float *const psum = part + (it.range * n + i) * K;
+    for (int j = 0; j < C::WN; ++j) {
+      const int i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
+      const bool in = i < n;
+      const float f = in && ranges == 1 ? scale[i] : 1.f;
+      const int64_t t = in ? rows.list[row0 + i] : 0;
 #pragma unroll
-    for (int mi = 0; mi < C::WM; ++mi)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t m = m0 + (wm * C::WM + mi) * 32 + 8 * q + 4 * (lane >> 5);
-        if (m >= K) continue;  // K % 8 == 0: four columns are all in or all out
+      for (int mi = 0; mi < C::WM; ++mi) {
+        const int64_t m = m0 + (wm * C::WM + mi) * 32;
         const f32x16_t &v = acc[mi][j];
-        if (ranges > 1)
-          *reinterpret_cast<float4 *>(psum + m) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        else
-          *reinterpret_cast<u32x2_t *>(out + m) =
-              u32x2_t{pack_bf16x2(v[4 * q] * f, v[4 * q + 1] * f), pack_bf16x2(v[4 * q + 2] * f, v[4 * q + 3] * f)};
+        if (ranges > 1) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int64_t mq = m + 8 * q + 4 * (lane >> 5);
+            if (in && mq < K)  // K % 8 == 0: eight columns are all in or all out
+              *reinterpret_cast<float4 *>(part + ((int64_t)range * n + i) * K + mq) =
+                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const u32x4_t o = join_halves(u32x2_t{pack_bf16x2(v[8 * q] * f, v[8 * q + 1] * f),
+                                                  pack_bf16x2(v[8 * q + 2] * f, v[8 * q + 3] * f)},
+                                          u32x2_t{pack_bf16x2(v[8 * q + 4] * f, v[8 * q + 5] * f),
+                                                  pack_bf16x2(v[8 * q + 6] * f, v[8 * q + 7] * f)});
+            const int64_t mq = m + 16 * q + 8 * (lane >> 5);
+            if (in && mq < K) *reinterpret_cast<u32x4_t *>(dX + t * K + mq) = o;
+          }
+        }
       }
-  }
+    }
+  };
+  products<C, ACROSS, BLOCKS>(items, ring, wave, lane, setup, begin, finish);
 }
 
 // ---------------------------------------------------------------------- dW
@@ -461,49 +519,66 @@ template <class C>
 __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, int64_t tb,
                                                    const bf16_t *__restrict__ E, int64_t lde, int64_t te,
                                                    const bf16_t *__restrict__ Xs, int64_t V, int64_t K,
-                                                   float *__restrict__ sums,
-                                                   int first, int last, bf16_t *__restrict__ dW) {
+                                                   float *__restrict__ sums, int first, int last,
+                                                   bf16_t *__restrict__ dW) {
   QLORA_RING(C, ring);
-  const int64_t n = block_rows(rows, row0, tb) < 0 ? 0 : block_rows(rows, row0, tb);
-  Item it;
-  if (!item_of((K + BM - 1) / BM, (V + C::BN - 1) / C::BN, 1, &it)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = block_rows(rows, row0, tb);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  const int64_t m0 = it.m * BM, n0 = it.n * C::BN;
-  Tile<BM, C::NT, ACROSS> ta;
-  Tile<C::BN, C::NT, BLOCKS_ACROSS> tbl;
-  ta.init(Xs, K, m0, K, nullptr, wave, lane);
-  tbl.init(E, te, n0, lde, nullptr, wave, lane);
-  f32x16_t acc[C::WM][C::WN];
-  reduce_steps<C, ACROSS, BLOCKS_ACROSS>(ta, tbl, n, 0, (n + BK - 1) / BK, ring, wm, wn, lane, acc);
+  Items items = {(int)((K + BM - 1) / BM), (int)((V + C::BN - 1) / C::BN), 1};
+  int m0 = 0, n0 = 0;
+  // (no rows: four steps over the zeros that k_head_combine leaves behind the block's last row)
+  auto setup = [&](Tile<BM, C::NT, ACROSS> &ta, Tile<C::BN, C::NT, BLOCKS_ACROSS> &tbl, int *s0, int *s1) {
+    const int deep = max((n + 127) / 128, 1);
+    ta.init(Xs, K, (int64_t)items.m * BM, K, deep * 128, nullptr, wave, lane);
+    tbl.init(E, te, (int64_t)items.n * C::BN, lde, max(n, 1), nullptr, wave, lane);
+    *s0 = 0;
+    *s1 = deep * 4;
+  };
+  auto begin = [&]() { m0 = items.m * BM, n0 = items.n * C::BN; };
+  auto finish = [&](Acc<C> &acc) {
+    arrive();
 #pragma unroll
-  for (int j = 0; j < C::WN; ++j) {
-    const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 31);
-    if (v >= V) continue;
+    for (int j = 0; j < C::WN; ++j) {
+      const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 31);
 #pragma unroll
-    for (int mi = 0; mi < C::WM; ++mi)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t m = m0 + (wm * C::WM + mi) * 32 + 8 * q + 4 * (lane >> 5);
-        if (m >= K) continue;
-        float4 o = make_float4(acc[mi][j][4 * q], acc[mi][j][4 * q + 1], acc[mi][j][4 * q + 2], acc[mi][j][4 * q + 3]);
+      for (int mi = 0; mi < C::WM; ++mi) {
+        const int64_t m = m0 + (wm * C::WM + mi) * 32;
+        f32x16_t &o = acc[mi][j];
         if (sums) {
-          float4 *const p = reinterpret_cast<float4 *>(sums + v * K + m);
-          if (!first) {
-            const float4 was = *p;
-            o = make_float4(o.x + was.x, o.y + was.y, o.z + was.z, o.w + was.w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int64_t mq = m + 8 * q + 4 * (lane >> 5);
+            if (v >= V || mq >= K) continue;
+            float4 *const p = reinterpret_cast<float4 *>(sums + v * K + mq);
+            if (!first) {
+              const float4 was = *p;
+              o[4 * q] += was.x, o[4 * q + 1] += was.y, o[4 * q + 2] += was.z, o[4 * q + 3] += was.w;
+            }
+            if (!last) *p = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
-          if (!last) {
-            *p = o;
-            continue;
-          }
+          if (!last) continue;
         }
-        *reinterpret_cast<u32x2_t *>(dW + v * K + m) = u32x2_t{pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w)};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const u32x4_t x =
+              join_halves(u32x2_t{pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3])},
+                          u32x2_t{pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7])});
+          const int64_t mq = m + 16 * q + 8 * (lane >> 5);
+          if (v < V && mq < K) *reinterpret_cast<u32x4_t *>(dW + v * K + mq) = x;
+        }
       }
-  }
+    }
+  };
+  products<C, ACROSS, BLOCKS_ACROSS>(items, ring, wave, lane, setup, begin, finish);
 }
 
-int64_t items8(int64_t items) { return (items + 7) / 8 * 8; }  // every XCD's run has the same length
+// Workgroups of a launch over `items` output tiles: as many as run at once (one per CU, two of the narrow tile), each
+// taking several; below that one each, in eights (every XCD's run of items has the same length).
+int64_t groups(int64_t items, int tile_rows) {
+  const int64_t most = tile_rows == 64 ? 512 : 256;
+  return items < most ? (items + 7) / 8 * 8 : most;
+}
 
 }  // namespace
 
@@ -525,16 +600,12 @@ size_t head_part_floats(int64_t tb, int64_t K, int64_t lde) {
     default: { CALL(H256); break; }     \
   }
 
-hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *X, const bf16_t *Xt,
-                              int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
-                              bf16_t *E, int64_t lde, int64_t te, hipStream_t s) {
-#define QLORA_CALL(CFG)                                                                                         \
-  const dim3 grid((unsigned)items8(ntile * ((tb + CFG::BN - 1) / CFG::BN)));                                    \
-  if (Xt)                                                                                                       \
-    launch(k_head_logits<CFG, BLOCKS>, grid, dim3(CFG::NT), 0, s, rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, \
-           te);                                                                                                 \
-  else                                                                                                          \
-    launch(k_head_logits<CFG, LINES>, grid, dim3(CFG::NT), 0, s, rows, row0, tb, X, K, W, V, K, c, stat, ntile, E, lde, te)
+hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx,
+                              const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E,
+                              int64_t lde, int64_t te, hipStream_t s) {
+#define QLORA_CALL(CFG)                                                                                               \
+  launch(k_head_logits<CFG>, dim3((unsigned)groups(ntile * ((tb + CFG::BN - 1) / CFG::BN), CFG::BN)), dim3(CFG::NT), 0, s, \
+         rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, te)
   QLORA_HEAD_TILES(tb, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();
@@ -550,7 +621,7 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
     most = items > most ? items : most;
   }
 #define QLORA_CALL(CFG)                                                                                              \
-  launch(k_head_dx<CFG>, dim3((unsigned)items8(most)), dim3(CFG::NT), 0, s, rows, row0, tb, E, lde, te, W, V, K, scale, part, \
+  launch(k_head_dx<CFG>, dim3((unsigned)groups(most, CFG::BN)), dim3(CFG::NT), 0, s, rows, row0, tb, E, lde, te, W, V, K, scale, part, \
          dX)
   QLORA_HEAD_TILES(tb, QLORA_CALL)
 #undef QLORA_CALL
@@ -560,7 +631,7 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,
                           hipStream_t s) {
-  launch(k_head_dw<H256>, dim3((unsigned)items8(((K + BM - 1) / BM) * ((V + 255) / 256))), dim3(H256::NT), 0, s, rows,
+  launch(k_head_dw<H256>, dim3((unsigned)groups(((K + BM - 1) / BM) * ((V + 255) / 256), 256)), dim3(H256::NT), 0, s, rows,
          row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, dW);
   return hipGetLastError();
 }

@@ -69,7 +69,7 @@ __device__ __forceinline__ void dots(const bf16_t *__restrict__ x, const bf16_t 
 // One row x to the blocks of 32 columns that the logit product reads: piece r of it to xt[r][ldx][32], zeros past K.
 __device__ __forceinline__ void block_row(const bf16_t *__restrict__ x, int64_t K, int lane, bf16_t *__restrict__ xt,
                                           int64_t ldx) {
-  for (int64_t at = 8 * lane; at < (K + 31) / 32 * 32; at += 512) {
+  for (int64_t at = 8 * lane; at < (K + 127) / 128 * 128; at += 512) {
     const u32x4_t v = at < K ? *reinterpret_cast<const u32x4_t *>(x + at) : u32x4_t{0u, 0u, 0u, 0u};
     *reinterpret_cast<u32x4_t *>(xt + at / 32 * ldx * 32 + at % 32) = v;
   }
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
       const bf16_t *const w[1] = {W + y * K};
       float z[1];
       dots<1>(X + t * K, w, K, lane, z);
-      if (Xt) block_row(X + t * K, K, lane, Xt + t * 32, ldx);
+      block_row(X + t * K, K, lane, Xt + t * 32, ldx);
       if (lane == 0) {
         rows.ref[t] = z[0];
         rows.refcol[t] = (int32_t)y;
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
   }
   __shared__ float s_z[256];
   const int64_t t = blockIdx.x - 1;
-  if (Xt && wave == 3) block_row(X + t * K, K, lane, Xt + t * 32, ldx);
+  if (wave == 3) block_row(X + t * K, K, lane, Xt + t * 32, ldx);
   const int32_t *idx = index + t * k;
   for (int i0 = 4 * wave; i0 < k; i0 += 4 * (kPrepThreads / 64)) {
     const bf16_t *w[4];
@@ -216,8 +216,8 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
 }
 
 // One wave per counted row of the block.
-__global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, const float2 *__restrict__ stat,
-                                                      int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
+__global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, int64_t tb,
+                                                      const float2 *__restrict__ stat, int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
                                                       const int32_t *__restrict__ index, int k, float tau,
                                                       const float *__restrict__ weight, float *__restrict__ loss,
                                                       float *__restrict__ scale, bf16_t *__restrict__ E, int64_t lde,
@@ -225,7 +225,17 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
                                                       bf16_t *__restrict__ Xs) {
   const int lane = threadIdx.x & 63;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // row of the block
-  if (row0 + i >= *rows.n) return;
+  int64_t n = *rows.n - row0;
+  n = n < 0 ? 0 : n < tb ? n : tb;
+  if (i >= n) {  // the dW product's steps go to the next 128 rows (at least one such group)
+    if (Xs && i < (n > 0 ? (n + 127) / 128 * 128 : 128)) {
+      for (int64_t at = 8 * lane; at < K; at += 512) *reinterpret_cast<u32x4_t *>(Xs + i * K + at) = u32x4_t{0u, 0u, 0u, 0u};
+      if (n == 0 && i == 0)
+        for (int64_t v = 8 * lane; v < lde; v += 512)
+          *reinterpret_cast<u32x4_t *>(E + (v / 32 * te) * 32 + v % 32) = u32x4_t{0u, 0u, 0u, 0u};
+    }
+    return;
+  }
   const int64_t t = rows.list[row0 + i];
   const float ref = rows.ref[t], c = 1.44269504f / tau;
   const float2 *st = stat + i * ntile;
@@ -330,7 +340,8 @@ hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, c
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
                                const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde, int64_t te,
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s) {
-  launch(k_head_combine, dim3((unsigned)((tb + 3) / 4)), dim3(256), 0, s, rows, row0, stat, ntile, V, labels, index, k,
+  const int64_t grid_rows = Xs ? (tb > 0 ? (tb + 127) / 128 * 128 : 128) : tb;
+  launch(k_head_combine, dim3((unsigned)((grid_rows + 3) / 4)), dim3(256), 0, s, rows, row0, tb, stat, ntile, V, labels, index, k,
          tau, weight, loss, scale, E, lde, te, X, K, Xs);
   return hipGetLastError();
 }
