@@ -425,7 +425,8 @@ struct HeadPlan {
   HeadBlocks b = {};
   int64_t ntile = 0;
   int64_t ldx = 0;  // rows per block of the laid out X
-  size_t off_n = 0, off_ranges = 0, off_xt = 0, off_list = 0, off_ref = 0, off_col = 0, off_h = 0, off_zt = 0, off_pt = 0,
+  size_t off_n = 0, off_ranges = 0, off_xt = 0, off_list = 0, off_ref = 0, off_col = 0, off_zt = 0, off_pt = 0, off_bucket = 0,
+         off_target = 0,
          off_stat = 0, off_scale = 0, off_e = 0, off_part = 0, off_xs = 0, off_sums = 0, total = 0;
   bool split = false;  // dX may come as partial sums
 };
@@ -455,16 +456,18 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   p.off_list = take((size_t)T * 4);
   p.off_ref = take((size_t)T * 4);
   p.off_col = take((size_t)T * 4);
-  p.off_h = take((size_t)T * 4);
   if (k > 0) {
     p.off_zt = take((size_t)T * k * 4);
     p.off_pt = take((size_t)T * k * 4);
+    const size_t tr = head_tile_rows(p.b.tb), row_tiles = ((size_t)p.b.tb + tr - 1) / tr;
+    p.off_bucket = take(row_tiles * (size_t)(p.ntile + 1) * 4);
+    p.off_target = take(row_tiles * tr * (size_t)k * 4);
   }
   p.off_stat = take((size_t)p.b.tb * p.ntile * sizeof(float2));
   p.off_scale = take((size_t)p.b.tb * 4);
   if (grad) p.off_e = take((size_t)p.b.te * p.b.lde * 2);
   if (dx) {
-    const size_t part = head_part_floats(p.b.tb, K, p.b.lde) * 4;
+    const size_t part = head_part_floats(p.b.tb, K) * 4;
     p.split = part > 0;
     p.off_part = take(part);
   }
@@ -516,9 +519,10 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   rows.list = list;
   rows.ref = (float *)(w + p.off_ref);
   rows.refcol = (int32_t *)(w + p.off_col);
-  rows.h = (float *)(w + p.off_h);
   rows.zt = k > 0 ? (float *)(w + p.off_zt) : nullptr;
   rows.pt = k > 0 ? (float *)(w + p.off_pt) : nullptr;
+  rows.bucket = k > 0 ? (int32_t *)(w + p.off_bucket) : nullptr;
+  rows.target = k > 0 ? (uint32_t *)(w + p.off_target) : nullptr;
   const bool grad = dX || dW;
   float2 *stat = (float2 *)(w + p.off_stat);
   float *scale = (float *)(w + p.off_scale);
@@ -530,13 +534,14 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   int32_t *ranges = (int32_t *)(w + p.off_ranges);
   const float c = 1.44269504f / tau;
   const int64_t lde = p.b.lde, te = p.b.te;
-  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, ranges, p.b, rows, loss, dX,
-                                       Xt, p.ldx, s));
+  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, dX ? ranges : nullptr, p.b, rows,
+                                       loss, dX, Xt, p.ldx, s));
   for (int64_t b = 0; b < p.b.count; ++b) {
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
     rows.ranges = ranges + b;
+    if (tb > 0 && k > 0) LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, p.ntile, s));
     if (tb > 0)
-      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, s));
+      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, k, s));
     if (tb > 0 || dW)
       LAUNCH("head_combine", launch_head_combine(rows, row0, tb, stat, p.ntile, V, labels, index, k, tau, weight, loss,
                                                  scale, E, lde, te, X, K, Xs, s));

@@ -20,9 +20,11 @@ struct HeadRows {
   const int32_t *list;  // [T] their rows in X
   float *ref;           // [T] by row of X: the logit of the row's first target
   int32_t *refcol;      // [T] by row of X: that target's column
-  float *h;             // [T] by row of X: sum_i p_i (log p_i - (z_i - ref) / tau); 0 for a one-hot target
-  float *zt;            // [T][k] logits of the k targets (NULL: one target)
-  float *pt;            // [T][k] their probabilities (NULL: one target)
+  // several targets (NULL for one):
+  float *zt;             // [T][k] their logits, from the product's tiles
+  float *pt;             // [T][k] their probabilities
+  int32_t *bucket;       // [row tiles][ntile + 1] where each output tile's targets start in `target`
+  uint32_t *target;      // [row tiles][rows of a tile * k]: target | column in the tile << 8 | row in the tile << 16
 };
 
 // Columns of W (rows of the output layer) per tile of the logit product, and the row statistics' unit.
@@ -35,10 +37,12 @@ constexpr float kHeadRange = 40.f;
 // Reduction ranges of the dX product: `tiles` output tiles of `steps` 64-deep steps on `slots` workgroups that run
 // at once.  A round of workgroups costs its steps plus about 10 (first loads, output); more than one range also
 // costs the binary32 partial sums, written and read once: about 33 steps' time for 256 tiles of 256 x 256.
-__host__ __device__ inline int head_split(int64_t tiles, int64_t steps, int slots, int tile_elems) {
+__host__ __device__ inline int head_split(int tiles, int steps, int slots, int tile_elems) {
   int best = 1;
   float best_cost = 3.4e38f;
-  for (int s = 1; s <= 16 && (s == 1 || steps / s >= 8); ++s) {
+#pragma unroll
+  for (int s = 1; s <= 16; ++s) {
+    if (s > 1 && (steps < 8 * s || tiles * s > 4 * slots)) break;
     const float rounds = (float)((tiles * s + slots - 1) / slots);
     const float cost = rounds * (float)((steps + s - 1) / s + 10) +
                        (s > 1 ? 33.f * (float)(tiles * s) * (float)tile_elems / (256.f * 65536.f) : 0.f);
@@ -57,10 +61,14 @@ struct HeadBlocks {
   int64_t te;         // rows of E's blocks of columns (E is [lde / 32][te][32])
 };
 
+// (ranges NULL: no dX)
 hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t V, int64_t K, const int64_t *labels,
                             const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
                             int32_t *ranges, const HeadBlocks &blocks, const HeadRows &rows, float *loss, bf16_t *dX,
                             bf16_t *Xt, int64_t ldx, hipStream_t s);
+// Sorts the targets of a block's counted rows by the output tile of the logit product they fall into.
+hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
+                              int64_t ntile, hipStream_t s);
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
                                const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde, int64_t te,
@@ -71,19 +79,23 @@ hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, co
 // Rows of X per tile of the three products for blocks of at most `tb` rows.
 // Few rows take narrow tiles: the padding rows' MFMA work would cost more than the wider tile's operand reuse gains.
 __host__ __device__ inline int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
-// Largest size in floats of the dX product's partial sums over all row counts up to tb (0: never split).
-size_t head_part_floats(int64_t tb, int64_t K, int64_t lde);
+// Room in floats for the dX product's partial sums: ranges * tiles is at most 4 times the slots, and 16 ranges.
+inline size_t head_part_floats(int64_t tb, int64_t K) {
+  const size_t bn = head_tile_rows(tb), slots = bn == 64 ? 512 : 256;
+  const size_t most = 4 * slots * bn * 256, all = 16 * (size_t)tb * K;
+  return all < most ? all : most;
+}
 // Ranges of the dX product of n rows: all of the same length but the last, none empty.
 __host__ __device__ inline int head_dx_ranges(int64_t n, int64_t K, int64_t lde, int tile_rows) {
-  const int64_t tiles = ((n + tile_rows - 1) / tile_rows) * ((K + 255) / 256);
-  const int fours = (int)(lde / 128), s = head_split(tiles, lde / 64, tile_rows == 64 ? 512 : 256, 256 * tile_rows);
+  const int tiles = (int)(((uint32_t)n + tile_rows - 1) / tile_rows * (uint32_t)((K + 255) / 256));
+  const int fours = (int)(lde / 128), s = head_split(tiles, fours * 2, tile_rows == 64 ? 512 : 256, 256 * tile_rows);
   const int per = (fours + s - 1) / s;
   return (fours + per - 1) / per;
 }
 
 // The logits take X as k_head_prep lays it out: Xt [4 (K / 128 rounded up)][ldx][32], zero past K.
 hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
-                              bf16_t *E, int64_t lde, int64_t te, hipStream_t s);
+                              bf16_t *E, int64_t lde, int64_t te, int k, hipStream_t s);
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
                           hipStream_t s);

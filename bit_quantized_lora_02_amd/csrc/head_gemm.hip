@@ -354,7 +354,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
                                                        const bf16_t *__restrict__ X, int64_t ldx,
                                                        const bf16_t *__restrict__ W, int64_t V, int64_t K, float c,
                                                        float2 *__restrict__ stat, int64_t ntile,
-                                                       bf16_t *__restrict__ E, int64_t lde, int64_t te) {
+                                                       bf16_t *__restrict__ E, int64_t lde, int64_t te, int k) {
   QLORA_RING(C, ring);
   __shared__ float s_max[C::WAVES_M][C::BN], s_sum[C::WAVES_M][C::BN];
   const int n = block_rows(rows, row0, tb);
@@ -369,18 +369,58 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
     *s0 = 0;
     *s1 = (int)((K + 127) / 128 * 4);
   };
-  auto begin = [&]() { m0 = items.m * BM, n0 = items.n * C::BN; };
-  // element e of acc[i][j]: column m0 + mlane + 32 i + 8 (e / 4) + e % 4 of the lane's row j
-  const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
-  auto finish = [&](Acc<C> &acc) {
-    float ref[C::WN];
+  // The epilogue's first loads are issued before the reduction: the lane's rows in X, and the item's targets (one per
+  // lane, the first 64 of them).
+  int32_t t[C::WN];
+  int t0 = 0, t1 = 0;
+  uint32_t target = 0;
+  const uint32_t *targets = nullptr;
+  auto begin = [&]() {
+    m0 = items.m * BM, n0 = items.n * C::BN;
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
       const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
-      const int64_t t = rows.list[row0 + (row < n ? row : n - 1)];
-      ref[j] = rows.ref[t];
+      t[j] = rows.list[row0 + (row < n ? row : n - 1)];
+    }
+    if (rows.target) {
+      const int32_t *const b = rows.bucket + (int64_t)items.n * (ntile + 1) + items.m;
+      t0 = b[0], t1 = b[1];
+      targets = rows.target + (int64_t)items.n * C::BN * k;
+      if (t0 + lane < t1) target = targets[t0 + lane];
+    }
+  };
+  // Logits of the tile's targets, for the loss and the targets' gradient: each wave picks its own out of acc.
+  auto pick = [&](Acc<C> &acc) {
+    for (int at = t0; at < t1; at += 64) {
+      const bool in = at + lane < t1;
+      if (at != t0 && in) target = targets[at + lane];
+      const int nj = target >> 16, m = target >> 8 & 255;
+      uint64_t mine = __ballot(in && nj / (C::WN * 32) == wn && m / (C::WM * 32) == wm);
+      while (mine) {
+        const uint32_t one = __builtin_amdgcn_readlane(target, __builtin_ctzll(mine));
+        mine &= mine - 1;
+        const int un = one >> 16, um = one >> 8 & 255;
+        const int i1 = um / 32 % C::WM, j1 = un / 32 % C::WN, e1 = (um >> 3 & 3) * 4 + (um & 3);
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::WN; ++j)
+            if (i == i1 && j == j1) z = acc[i][j][e1];
+        if (lane == (un & 31) + 32 * (um >> 2 & 1)) rows.zt[(int64_t)rows.list[row0 + n0 + un] * k + (one & 255)] = z;
+      }
+    }
+  };
+  // element e of acc[i][j]: column m0 + mlane + 32 i + 8 (e / 4) + e % 4 of the lane's row j
+  const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
+  auto finish = [&](Acc<C> &acc) {
+    if (rows.target) pick(acc);
+    float ref[C::WN];
+#pragma unroll
+    for (int j = 0; j < C::WN; ++j) {
+      ref[j] = rows.ref[t[j]];
       // the reference's own column and those past the vocabulary stay out of the sums
-      int rc = rows.refcol[t] - m0 - mlane, end = (int)(V - m0) - mlane;
+      int rc = rows.refcol[t[j]] - m0 - mlane, end = (int)(V - m0) - mlane;
       if (__any((rc >= -4 && rc < BM) || m0 + BM > V)) {
         asm("" : "+v"(rc), "+v"(end));
 #pragma unroll
@@ -582,17 +622,6 @@ int64_t groups(int64_t items, int tile_rows) {
 
 }  // namespace
 
-size_t head_part_floats(int64_t tb, int64_t K, int64_t lde) {
-  const int bn = head_tile_rows(tb);
-  size_t most = 0;
-  for (int64_t n = tb;; n = (n - 1) / bn * bn) {  // the largest row count of each number of tiles
-    const int s = head_dx_ranges(n, K, lde, bn);
-    const size_t need = s > 1 ? (size_t)s * n * K : 0;
-    most = need > most ? need : most;
-    if (n <= bn) return most;
-  }
-}
-
 #define QLORA_HEAD_TILES(rows_, CALL)   \
   switch (head_tile_rows(rows_)) {      \
     case 64: { CALL(H64); break; }      \
@@ -602,10 +631,10 @@ size_t head_part_floats(int64_t tb, int64_t K, int64_t lde) {
 
 hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx,
                               const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E,
-                              int64_t lde, int64_t te, hipStream_t s) {
+                              int64_t lde, int64_t te, int k, hipStream_t s) {
 #define QLORA_CALL(CFG)                                                                                               \
   launch(k_head_logits<CFG>, dim3((unsigned)groups(ntile * ((tb + CFG::BN - 1) / CFG::BN), CFG::BN)), dim3(CFG::NT), 0, s, \
-         rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, te)
+         rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, te, k)
   QLORA_HEAD_TILES(tb, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();
@@ -614,12 +643,7 @@ hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, co
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
                           hipStream_t s) {
-  const int bn = head_tile_rows(tb);
-  int64_t most = 0;  // workgroups over all row counts of the block (the kernel takes as many as the count needs)
-  for (int64_t t = 1; t <= (tb + bn - 1) / bn; ++t) {
-    const int64_t items = t * ((K + BM - 1) / BM) * head_dx_ranges(t * bn, K, lde, bn);
-    most = items > most ? items : most;
-  }
+  const int64_t most = (tb + head_tile_rows(tb) - 1) / head_tile_rows(tb) * ((K + BM - 1) / BM) * 16;  // 16 ranges
 #define QLORA_CALL(CFG)                                                                                              \
   launch(k_head_dx<CFG>, dim3((unsigned)groups(most, CFG::BN)), dim3(CFG::NT), 0, s, rows, row0, tb, E, lde, te, W, V, K, scale, part, \
          dX)

@@ -44,40 +44,10 @@ __device__ __forceinline__ bool row_counts(const int64_t *__restrict__ labels, c
   return false;
 }
 
-// Sum over this lane's share of x . w (16-byte pieces lane, lane + 64, ...) for N rows w at once.
-template <int N>
-__device__ __forceinline__ void dots(const bf16_t *__restrict__ x, const bf16_t *const (&w)[N], int64_t K, int lane,
-                                     float (&out)[N]) {
-#pragma unroll
-  for (int j = 0; j < N; ++j) out[j] = 0.f;
-  for (int64_t at = 8 * lane; at < K; at += 512) {
-    const u32x4_t xv = *reinterpret_cast<const u32x4_t *>(x + at);
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const u32x4_t wv = *reinterpret_cast<const u32x4_t *>(w[j] + at);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        out[j] = fmaf(bf16_lo_to_f32(xv[e]), bf16_lo_to_f32(wv[e]), out[j]);
-        out[j] = fmaf(bf16_hi_to_f32(xv[e]), bf16_hi_to_f32(wv[e]), out[j]);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < N; ++j) out[j] = wave_sum(out[j]);
-}
-
-// One row x to the blocks of 32 columns that the logit product reads: piece r of it to xt[r][ldx][32], zeros past K.
-__device__ __forceinline__ void block_row(const bf16_t *__restrict__ x, int64_t K, int lane, bf16_t *__restrict__ xt,
-                                          int64_t ldx) {
-  for (int64_t at = 8 * lane; at < (K + 127) / 128 * 128; at += 512) {
-    const u32x4_t v = at < K ? *reinterpret_cast<const u32x4_t *>(x + at) : u32x4_t{0u, 0u, 0u, 0u};
-    *reinterpret_cast<u32x4_t *>(xt + at / 32 * ldx * 32 + at % 32) = v;
-  }
-}
-
-// Workgroup 0 numbers the rows that count, in order; the others take rows of X (cross entropy: one per wave,
-// distillation: one per workgroup): the targets' logits by dot products (binary32 FMA), the teacher's softmax, or,
-// for a row that does not count, its zeros.
+// Workgroup 0 numbers the rows that count, in order; the other workgroups' waves take a row of X each: its first
+// target (the label, or the teacher's most probable one; the first of equals) and that target's logit by a dot
+// product (binary32 FMA), the teacher's softmax, and the row in the blocks of 32 columns that the logit product reads
+// (zeros past K); or, for a row that does not count, its zero loss and gradient.
 __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__restrict__ X, int64_t T,
                                                             const bf16_t *__restrict__ W, int64_t V, int64_t K,
                                                             const int64_t *__restrict__ labels,
@@ -120,99 +90,130 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
       __syncthreads();
     }
     if (tid == 0) *n = base;
-    for (int64_t b = tid; b < blocks.count; b += kPrepThreads) {
+    for (int64_t b = tid; ranges && b < blocks.count; b += kPrepThreads) {
       const int64_t row0 = b * blocks.tb, tb = T - row0 < blocks.tb ? T - row0 : blocks.tb;
       const int64_t have = base - row0 < tb ? base - row0 : tb;
       ranges[b] = have > 0 ? head_dx_ranges(have, K, blocks.lde, head_tile_rows(tb)) : 1;
     }
     return;
   }
+  const int64_t t = (int64_t)(blockIdx.x - 1) * (kPrepThreads / 64) + wave;
+  if (t >= T) return;
+  int64_t y;
   if (labels) {
-    const int64_t t = (int64_t)(blockIdx.x - 1) * (kPrepThreads / 64) + wave;
-    if (t >= T) return;
-    const int64_t y = labels[t];
-    if (target_ok(y, V)) {
-      const bf16_t *const w[1] = {W + y * K};
-      float z[1];
-      dots<1>(X + t * K, w, K, lane, z);
-      block_row(X + t * K, K, lane, Xt + t * 32, ldx);
-      if (lane == 0) {
-        rows.ref[t] = z[0];
-        rows.refcol[t] = (int32_t)y;
-        rows.h[t] = 0.f;
-      }
-    } else {
-      if (lane == 0) loss[t] = 0.f;
-      if (dX)
-        for (int64_t at = 8 * lane; at < K; at += 512)
-          *reinterpret_cast<u32x4_t *>(dX + t * K + at) = u32x4_t{0u, 0u, 0u, 0u};
-    }
-    return;
-  }
-  __shared__ float s_z[256];
-  const int64_t t = blockIdx.x - 1;
-  if (wave == 3) block_row(X + t * K, K, lane, Xt + t * 32, ldx);
-  const int32_t *idx = index + t * k;
-  for (int i0 = 4 * wave; i0 < k; i0 += 4 * (kPrepThreads / 64)) {
-    const bf16_t *w[4];
+    y = labels[t];
+    if (!target_ok(y, V)) y = -1;
+  } else {  // the teacher's softmax over the row's targets, up to four per lane
+    float tl[4], top = -INFINITY;
+    int id[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t v = i0 + j < k ? idx[i0 + j] : 0;
-      w[j] = W + (target_ok(v, V) ? v : 0) * K;
+      const int i = lane + 64 * j;
+      id[j] = i < k ? index[t * k + i] : -1;
+      tl[j] = target_ok(id[j], V) ? logit[t * k + i] : -INFINITY;
+      top = fmaxf(top, tl[j]);
     }
-    const bf16_t *const wc[4] = {w[0], w[1], w[2], w[3]};
-    float z[4];
-    dots<4>(X + t * K, wc, K, lane, z);
-    if (lane == 0)
-      for (int j = 0; j < 4 && i0 + j < k; ++j) s_z[i0 + j] = z[j];
-  }
-  __syncthreads();
-  if (wave != 0) return;
-  // the teacher's softmax over the row's targets, up to four per lane
-  float tl[4], top = -INFINITY;
+    top = wave_max(top);
+    int first = 256;
+    float e[4], sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int i = lane + 64 * j;
-    tl[j] = i < k && target_ok(idx[i], V) ? logit[t * k + i] : -INFINITY;
-    top = fmaxf(top, tl[j]);
+    for (int j = 0; j < 4; ++j) {
+      e[j] = tl[j] == -INFINITY ? 0.f : expf((tl[j] - top) / tau);
+      sum += e[j];
+      if (tl[j] == top) first = min(first, lane + 64 * j);
+    }
+    sum = wave_sum(sum);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) first = min(first, __shfl_xor(first, o));
+    y = -1;
+    if (top > -INFINITY) {
+      y = index[t * k + first];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (lane + 64 * j < k) rows.pt[t * k + lane + 64 * j] = e[j] / sum;
+    }
   }
-  top = wave_max(top);
-  if (top == -INFINITY) {  // nothing to learn from in this row
+  if (y < 0) {
     if (lane == 0) loss[t] = 0.f;
     if (dX)
       for (int64_t at = 8 * lane; at < K; at += 512)
         *reinterpret_cast<u32x4_t *>(dX + t * K + at) = u32x4_t{0u, 0u, 0u, 0u};
     return;
   }
-  int first = 1 << 20;
-  float e[4], sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    e[j] = expf((tl[j] - top) / tau);
-    sum += e[j];
-    if (tl[j] == top) first = min(first, lane + 64 * j);
-  }
-  sum = wave_sum(sum);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) first = min(first, __shfl_xor(first, o));
-  const float ref = s_z[first], lsum = logf(sum);
-  float h = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int i = lane + 64 * j;
-    const float p = e[j] / sum;
-    if (i < k) {
-      rows.pt[t * k + i] = p;
-      rows.zt[t * k + i] = s_z[i];
-      if (p > 0.f) h += p * ((tl[j] - top) / tau - lsum - (s_z[i] - ref) / tau);
+  const bf16_t *x = X + t * K, *w = W + y * K;
+  float z = 0.f;
+#pragma unroll 4
+  for (int64_t at = 8 * lane; at < (K + 127) / 128 * 128; at += 512) {
+    u32x4_t xv = u32x4_t{0u, 0u, 0u, 0u}, wv = xv;
+    if (at < K) {
+      xv = *reinterpret_cast<const u32x4_t *>(x + at);
+      wv = *reinterpret_cast<const u32x4_t *>(w + at);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      z = fmaf(bf16_lo_to_f32(xv[e]), bf16_lo_to_f32(wv[e]), z);
+      z = fmaf(bf16_hi_to_f32(xv[e]), bf16_hi_to_f32(wv[e]), z);
+    }
+    *reinterpret_cast<u32x4_t *>(Xt + (at / 32 * ldx + t) * 32 + at % 32) = xv;
   }
-  h = wave_sum(h);
+  z = wave_sum(z);
   if (lane == 0) {
-    rows.ref[t] = ref;
-    rows.refcol[t] = idx[first];
-    rows.h[t] = h;
+    rows.ref[t] = z;
+    rows.refcol[t] = (int32_t)y;
   }
+}
+
+// One workgroup per tile of rows: a counting sort of its targets by output tile.  (The order within an output tile is
+// that of the LDS counters; every target's logit goes to a place of its own, so no result depends on it.)
+constexpr int kBucketThreads = 1024;
+__global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, int64_t row0, int64_t tb, int tile_rows,
+                                                                const int32_t *__restrict__ index, int k, int64_t V,
+                                                                int ntile) {
+  extern __shared__ int s_count[];  // [ntile]
+  __shared__ int s_wave[kBucketThreads / 64];
+  int64_t n = *rows.n - row0;
+  n = n < tb ? n : tb;
+  const int64_t n0 = (int64_t)blockIdx.x * tile_rows;
+  if (n0 >= n) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int have = (int)(n - n0 < tile_rows ? n - n0 : tile_rows) * k;
+  for (int i = tid; i < ntile; i += kBucketThreads) s_count[i] = 0;
+  __syncthreads();
+  auto each = [&](auto use) {
+    for (int e = tid; e < have; e += kBucketThreads) {
+      const int nj = e / k, j = e - nj * k;
+      const int64_t v = index[(int64_t)rows.list[row0 + n0 + nj] * k + j];
+      if (target_ok(v, V)) use((int)v, nj, j);
+    }
+  };
+  each([&](int v, int, int) { atomicAdd(&s_count[v / kHeadTile], 1); });
+  __syncthreads();
+  // exclusive sums over the tiles, a run of `per` of them per thread
+  const int per = (ntile + kBucketThreads - 1) / kBucketThreads, i0 = tid * per;
+  int mine = 0;
+  for (int i = i0; i < i0 + per && i < ntile; ++i) mine += s_count[i];
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(before, o);
+    if (lane >= o) before += up;
+  }
+  if (lane == 63) s_wave[wave] = before;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) before += s_wave[w];
+  int at = before - mine;
+  int32_t *bucket = rows.bucket + (int64_t)blockIdx.x * (ntile + 1);
+  for (int i = i0; i < i0 + per && i < ntile; ++i) {
+    const int c = s_count[i];
+    bucket[i] = s_count[i] = at;
+    at += c;
+  }
+  if (i0 < ntile && i0 + per >= ntile) bucket[ntile] = at;
+  __syncthreads();
+  uint32_t *target = rows.target + (int64_t)blockIdx.x * tile_rows * k;
+  each([&](int v, int nj, int j) {
+    target[atomicAdd(&s_count[v / kHeadTile], 1)] = (uint32_t)j | (uint32_t)(v % kHeadTile) << 8 | (uint32_t)nj << 16;
+  });
 }
 
 // One wave per counted row of the block.
@@ -259,7 +260,14 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
     nlogq = logf(rest + eref) + (u - ref) / tau;
   }
   S = rest + eref;
-  if (lane == 0) loss[t] = tau * tau * (rows.h[t] + nlogq);
+  float h = 0.f;  // sum_i p_i (log p_i - (z_i - z_r) / tau)
+  if (!labels)
+    for (int j = lane; j < k; j += 64) {
+      const float p = rows.pt[t * k + j];
+      if (p > 0.f) h += p * (logf(p) - (rows.zt[t * k + j] - ref) / tau);
+    }
+  h = wave_sum(h);
+  if (lane == 0) loss[t] = tau * tau * (h + nlogq);
   if (!E) return;
   auto e = [&](int64_t v) { return E + (v / 32 * te + i) * 32 + v % 32; };
   if (wide) {  // bring the row's tiles to one unit (a factor below binary32's range is applied in two halves)
@@ -330,9 +338,17 @@ hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t
                             const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
                             int32_t *ranges, const HeadBlocks &blocks, const HeadRows &rows, float *loss, bf16_t *dX,
                             bf16_t *Xt, int64_t ldx, hipStream_t s) {
-  const int64_t wgs = labels ? (T + 3) / 4 : T;
+  const int64_t wgs = (T + kPrepThreads / 64 - 1) / (kPrepThreads / 64);
   launch(k_head_prep, dim3((unsigned)(1 + wgs)), dim3(kPrepThreads), 0, s, X, T, W, V, K, labels, index, logit, k, tau,
          n, list, ranges, blocks, rows, loss, dX, Xt, ldx);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
+                              int64_t ntile, hipStream_t s) {
+  const int tr = head_tile_rows(tb);
+  launch(k_head_bucket, dim3((unsigned)((tb + tr - 1) / tr)), dim3(kBucketThreads), (uint32_t)ntile * 4, s, rows, row0,
+         tb, tr, index, k, V, (int)ntile);
   return hipGetLastError();
 }
 

@@ -71,7 +71,7 @@ def test_workspace_is_checked_and_bounded(lib):
     T, V = 8192, 131072
     assert B.head_workspace_bytes(T, V, 4096, 0, False, False) < T * V / 32 + 2 * T * 4096 + (1 << 20)
     # gradients hold a block of at most 1 GiB and the dX product's partial sums, however many rows there are
-    for T in (4096, 65536, 1 << 19):
+    for T in (4096, 65536, 1 << 18):
         assert B.head_workspace_bytes(T, V, 4096, 0, True, False) < (3 << 29) + (2 * 4096 + 32) * T
 
 
