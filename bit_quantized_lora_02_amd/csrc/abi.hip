@@ -434,7 +434,9 @@ struct HeadPlan {
 HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw) {
   HeadPlan p;
   const bool grad = dx || dw;
-  p.ntile = ceil_div(V, kHeadTile);
+  // (a block holds at least 256 rows where there are several, so the tile follows from T)
+  p.b.tile_rows = head_tile_rows(T);
+  p.ntile = ceil_div(V, head_tile_cols(p.b.tile_rows));
   p.b.lde = ceil_div(V, kHeadPad) * kHeadPad;
   const size_t row = (size_t)p.ntile * sizeof(float2) + (grad ? (size_t)p.b.lde * 2 : 0);
   int64_t most = (int64_t)(kHeadBlockBytes / row) / 256 * 256;
@@ -459,7 +461,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   if (k > 0) {
     p.off_zt = take((size_t)T * k * 4);
     p.off_pt = take((size_t)T * k * 4);
-    const size_t tr = head_tile_rows(p.b.tb), row_tiles = ((size_t)p.b.tb + tr - 1) / tr;
+    const size_t tr = p.b.tile_rows, row_tiles = ((size_t)p.b.tb + tr - 1) / tr;
     p.off_bucket = take(row_tiles * (size_t)(p.ntile + 1) * 4);
     p.off_target = take(row_tiles * tr * (size_t)k * 4);
   }
@@ -467,7 +469,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   p.off_scale = take((size_t)p.b.tb * 4);
   if (grad) p.off_e = take((size_t)p.b.te * p.b.lde * 2);
   if (dx) {
-    const size_t part = head_part_floats(p.b.tb, K) * 4;
+    const size_t part = head_part_floats(p.b.tb, K, p.b.tile_rows) * 4;
     p.split = part > 0;
     p.off_part = take(part);
   }
@@ -516,6 +518,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   HeadRows rows;
   rows.n = n;
   rows.ranges = nullptr;
+  rows.tile_rows = p.b.tile_rows;
   rows.list = list;
   rows.ref = (float *)(w + p.off_ref);
   rows.refcol = (int32_t *)(w + p.off_col);
@@ -532,14 +535,17 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   float *sums = p.off_sums ? (float *)(w + p.off_sums) : nullptr;
   bf16_t *Xt = (bf16_t *)(w + p.off_xt);
   int32_t *ranges = (int32_t *)(w + p.off_ranges);
+  int32_t *const rg = dX ? ranges : nullptr;
   const float c = 1.44269504f / tau;
   const int64_t lde = p.b.lde, te = p.b.te;
-  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, dX ? ranges : nullptr, p.b, rows,
-                                       loss, dX, Xt, p.ldx, s));
+  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, rg, p.b, rows, loss, dX, Xt, p.ldx,
+                                       s));
+  if (k > 0 && !(T > 0 && head_one_tile(T, rows))) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, rg, p.b, s));
   for (int64_t b = 0; b < p.b.count; ++b) {
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
     rows.ranges = ranges + b;
-    if (tb > 0 && k > 0) LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, p.ntile, s));
+    if (tb > 0 && k > 0)
+      LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, p.ntile, T, K, n, list, rg, p.b, s));
     if (tb > 0)
       LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, k, s));
     if (tb > 0 || dW)

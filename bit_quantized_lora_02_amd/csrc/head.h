@@ -17,6 +17,7 @@ typedef uint16_t bf16_t;
 struct HeadRows {
   const int32_t *n;       // rows that count
   const int32_t *ranges;  // the dX product's ranges for the block at hand
+  int tile_rows;          // rows of the products' tiles
   const int32_t *list;  // [T] their rows in X
   float *ref;           // [T] by row of X: the logit of the row's first target
   int32_t *refcol;      // [T] by row of X: that target's column
@@ -27,12 +28,20 @@ struct HeadRows {
   uint32_t *target;      // [row tiles][rows of a tile * k]: target | column in the tile << 8 | row in the tile << 16
 };
 
-// Columns of W (rows of the output layer) per tile of the logit product, and the row statistics' unit.
-constexpr int kHeadTile = 256;
 // Rows of E are padded with zero columns to a multiple of this.
 constexpr int kHeadPad = 128;
 // A logit may exceed the row's reference by 2^kHeadRange before the tile takes a unit of its own.
 constexpr float kHeadRange = 40.f;
+
+// Rows of X per tile of the three products, by the rows of a block (one choice for all blocks of a call).
+// Few rows take narrow tiles: the padding rows' MFMA work would cost more than the wider tile's operand reuse gains.
+inline int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
+// Columns of a tile (of the vocabulary in the logit product, of X in the dX product); the row statistics are per tile.
+// Up to 64 rows the products are bound by the stream of W, and the smaller tile gives every CU some of it.
+__host__ __device__ inline int head_tile_cols(int tile_rows) { return tile_rows == 64 ? 128 : 256; }
+
+// Most ranges of the dX product's reduction, and workgroups of the narrow tile that run at once (three per CU).
+constexpr int kHeadRanges = 32, kHeadSlots64 = 768;
 
 // Reduction ranges of the dX product: `tiles` output tiles of `steps` 64-deep steps on `slots` workgroups that run
 // at once.  A round of workgroups costs its steps plus about 10 (first loads, output); more than one range also
@@ -41,7 +50,7 @@ __host__ __device__ inline int head_split(int tiles, int steps, int slots, int t
   int best = 1;
   float best_cost = 3.4e38f;
 #pragma unroll
-  for (int s = 1; s <= 16; ++s) {
+  for (int s = 1; s <= kHeadRanges; ++s) {
     if (s > 1 && (steps < 8 * s || tiles * s > 4 * slots)) break;
     const float rounds = (float)((tiles * s + slots - 1) / slots);
     const float cost = rounds * (float)((steps + s - 1) / s + 10) +
@@ -58,6 +67,7 @@ __host__ __device__ inline int head_split(int tiles, int steps, int slots, int t
 struct HeadBlocks {
   int64_t tb, count;  // rows per block (the last: what is left of T), blocks
   int64_t lde;        // columns of E: V rounded up to kHeadPad
+  int tile_rows;
   int64_t te;         // rows of E's blocks of columns (E is [lde / 32][te][32])
 };
 
@@ -66,9 +76,14 @@ hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t
                             const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
                             int32_t *ranges, const HeadBlocks &blocks, const HeadRows &rows, float *loss, bf16_t *dX,
                             bf16_t *Xt, int64_t ldx, hipStream_t s);
+// Without labels: numbers the rows after launch_head_prep (where one row tile holds them all, launch_head_bucket does).
+hipError_t launch_head_list(const HeadRows &rows, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
+                            const HeadBlocks &blocks, hipStream_t s);
+inline bool head_one_tile(int64_t T, const HeadRows &rows) { return T <= rows.tile_rows; }
 // Sorts the targets of a block's counted rows by the output tile of the logit product they fall into.
 hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
-                              int64_t ntile, hipStream_t s);
+                              int64_t ntile, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
+                              const HeadBlocks &blocks, hipStream_t s);
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
                                const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde, int64_t te,
@@ -76,19 +91,18 @@ hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, c
 hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t K,
                               const float *scale, bf16_t *dX, hipStream_t s);
 
-// Rows of X per tile of the three products for blocks of at most `tb` rows.
-// Few rows take narrow tiles: the padding rows' MFMA work would cost more than the wider tile's operand reuse gains.
-__host__ __device__ inline int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
-// Room in floats for the dX product's partial sums: ranges * tiles is at most 4 times the slots, and 16 ranges.
-inline size_t head_part_floats(int64_t tb, int64_t K) {
-  const size_t bn = head_tile_rows(tb), slots = bn == 64 ? 512 : 256;
-  const size_t most = 4 * slots * bn * 256, all = 16 * (size_t)tb * K;
+// Room in floats for the dX product's partial sums: ranges * tiles is at most 4 times the slots.
+inline size_t head_part_floats(int64_t tb, int64_t K, int tile_rows) {
+  const size_t bn = tile_rows, slots = bn == 64 ? kHeadSlots64 : 256;
+  const size_t most = 4 * slots * bn * head_tile_cols(tile_rows), all = kHeadRanges * (size_t)tb * K;
   return all < most ? all : most;
 }
 // Ranges of the dX product of n rows: all of the same length but the last, none empty.
 __host__ __device__ inline int head_dx_ranges(int64_t n, int64_t K, int64_t lde, int tile_rows) {
-  const int tiles = (int)(((uint32_t)n + tile_rows - 1) / tile_rows * (uint32_t)((K + 255) / 256));
-  const int fours = (int)(lde / 128), s = head_split(tiles, fours * 2, tile_rows == 64 ? 512 : 256, 256 * tile_rows);
+  const int cols = head_tile_cols(tile_rows);
+  const int tiles = (int)(((uint32_t)n + tile_rows - 1) / tile_rows * (uint32_t)((K + cols - 1) / cols));
+  const int fours = (int)(lde / 128);
+  const int s = head_split(tiles, fours * 2, tile_rows == 64 ? kHeadSlots64 : 256, cols * tile_rows);
   const int per = (fours + s - 1) / s;
   return (fours + per - 1) / per;
 }

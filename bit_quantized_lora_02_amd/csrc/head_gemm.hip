@@ -28,18 +28,16 @@ namespace {
 
 constexpr int BK = 32;      // reduction depth of a step
 constexpr int STAGES = 4;   // tiles in LDS: one being multiplied, three on their way
-constexpr int BM = kHeadTile;
 
 template <int WAVES_M_, int WAVES_N_, int WM_, int WN_>
 struct HeadCfg {
   static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WM = WM_, WN = WN_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
-  static constexpr int BN = WAVES_N * WN * 32;
-  static_assert(WAVES_M * WM * 32 == BM, "tiles are 256 wide");
+  static constexpr int BM = WAVES_M * WM * 32, BN = WAVES_N * WN * 32;
 };
 using H256 = HeadCfg<2, 4, 4, 2>;  // 128 x 64 per wave
 using H128 = HeadCfg<4, 2, 2, 2>;  // 64 x 64 per wave
-using H64 = HeadCfg<4, 1, 2, 2>;   // 64 x 64 per wave, two workgroups per CU
+using H64 = HeadCfg<4, 1, 1, 2>;   // 128 x 64, 32 x 64 per wave, three workgroups per CU
 
 __device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0); }
 
@@ -50,8 +48,8 @@ struct Ring {
   lds_char *slot[STAGES];
 };
 #define QLORA_RING(C, ring)                                                                                     \
-  __shared__ __attribute__((aligned(1024))) char ring0[(BM + C::BN) * BK * 2], ring1[(BM + C::BN) * BK * 2],    \
-      ring2[(BM + C::BN) * BK * 2], ring3[(BM + C::BN) * BK * 2];                                               \
+  __shared__ __attribute__((aligned(1024))) char ring0[(C::BM + C::BN) * BK * 2], ring1[(C::BM + C::BN) * BK * 2],    \
+      ring2[(C::BM + C::BN) * BK * 2], ring3[(C::BM + C::BN) * BK * 2];                                               \
   const Ring ring = {{(lds_char *)ring0, (lds_char *)ring1, (lds_char *)ring2, (lds_char *)ring3}}
 
 // Lane offsets into the slots.  An LDS instruction adds at most 65535 to its address register, so a lane keeps its
@@ -246,7 +244,7 @@ struct Items {
 template <class C, int KA, int KB, class Setup, class Begin, class Finish>
 __device__ __forceinline__ void products(Items &items, const Ring &ring, int wave, int lane, Setup setup, Begin begin,
                                          Finish finish) {
-  typedef Tile<BM, C::NT, KA> TileA;
+  typedef Tile<C::BM, C::NT, KA> TileA;
   typedef Tile<C::BN, C::NT, KB> TileB;
   constexpr int L = TileA::LD + TileB::LD, L1 = L / 2;  // copies per thread and step, those before the meeting
   static_assert(2 * L < 64, "copies in flight are counted in six bits");
@@ -256,17 +254,17 @@ __device__ __forceinline__ void products(Items &items, const Ring &ring, int wav
   TileB tb;
   int s0, s1;
   setup(ta, tb, &s0, &s1);
-  Operand<BM, C::WM, TileA::TR> oa;
+  Operand<C::BM, C::WM, TileA::TR> oa;
   Operand<C::BN, C::WN, TileB::TR> ob;
   oa.init(0, wave / C::WAVES_N * C::WM * 32, lane);
-  ob.init(BM * BK * 2, wave % C::WAVES_N * C::WN * 32, lane);
+  ob.init(C::BM * BK * 2, wave % C::WAVES_N * C::WN * 32, lane);
   auto copies = [&](int s, int slot, int q0, int q1) {
 #pragma unroll
     for (int q = q0; q < q1; ++q) {
       if (q < TileA::LD)
         ta.copy(s, q, ring.slot[slot], wave);
       else
-        tb.copy(s, q - TileA::LD, ring.slot[slot] + BM * BK * 2, wave);
+        tb.copy(s, q - TileA::LD, ring.slot[slot] + C::BM * BK * 2, wave);
       fence_sched();
     }
   };
@@ -363,8 +361,8 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   Items items = {(int)ntile, (n + C::BN - 1) / C::BN, 1};
   int m0 = 0, n0 = 0;
-  auto setup = [&](Tile<BM, C::NT, LINES> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
-    ta.init(W, K, (int64_t)items.m * BM, V, K, nullptr, wave, lane);
+  auto setup = [&](Tile<C::BM, C::NT, LINES> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
+    ta.init(W, K, (int64_t)items.m * C::BM, V, K, nullptr, wave, lane);
     tbl.init(X, ldx, (int64_t)items.n * C::BN, n, K, rows.list + row0, wave, lane);
     *s0 = 0;
     *s1 = (int)((K + 127) / 128 * 4);
@@ -376,7 +374,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
   uint32_t target = 0;
   const uint32_t *targets = nullptr;
   auto begin = [&]() {
-    m0 = items.m * BM, n0 = items.n * C::BN;
+    m0 = items.m * C::BM, n0 = items.n * C::BN;
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
       const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
@@ -402,12 +400,15 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
         const int un = one >> 16, um = one >> 8 & 255;
         const int i1 = um / 32 % C::WM, j1 = un / 32 % C::WN, e1 = (um >> 3 & 3) * 4 + (um & 3);
         float z = 0.f;
+        int32_t row = 0;
 #pragma unroll
-        for (int i = 0; i < C::WM; ++i)
+        for (int j = 0; j < C::WN; ++j) {
+          row = j == j1 ? t[j] : row;
 #pragma unroll
-          for (int j = 0; j < C::WN; ++j)
+          for (int i = 0; i < C::WM; ++i)
             if (i == i1 && j == j1) z = acc[i][j][e1];
-        if (lane == (un & 31) + 32 * (um >> 2 & 1)) rows.zt[(int64_t)rows.list[row0 + n0 + un] * k + (one & 255)] = z;
+        }
+        if (lane == (un & 31) + 32 * (um >> 2 & 1)) rows.zt[(int64_t)row * k + (one & 255)] = z;
       }
     }
   };
@@ -421,7 +422,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
       ref[j] = rows.ref[t[j]];
       // the reference's own column and those past the vocabulary stay out of the sums
       int rc = rows.refcol[t[j]] - m0 - mlane, end = (int)(V - m0) - mlane;
-      if (__any((rc >= -4 && rc < BM) || m0 + BM > V)) {
+      if (__any((rc >= -4 && rc < C::BM) || m0 + C::BM > V)) {
         asm("" : "+v"(rc), "+v"(end));
 #pragma unroll
         for (int i = 0; i < C::WM; ++i)
@@ -484,7 +485,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
         float sum = s_sum[0][nj];
 #pragma unroll
         for (int w = 1; w < C::WAVES_M; ++w) sum += s_sum[w][nj];
-        if (n0 + nj < n) stat[(int64_t)(n0 + nj) * ntile + m0 / BM] = make_float2(u[j], sum);
+        if (n0 + nj < n) stat[(int64_t)(n0 + nj) * ntile + m0 / C::BM] = make_float2(u[j], sum);
       }
     }
   };
@@ -505,16 +506,16 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
   const int ranges = *rows.ranges;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  Items items = {(int)((K + BM - 1) / BM), (n + C::BN - 1) / C::BN, ranges};
+  Items items = {(int)((K + C::BM - 1) / C::BM), (n + C::BN - 1) / C::BN, ranges};
   int m0 = 0, n0 = 0, range = 0;
-  auto setup = [&](Tile<BM, C::NT, ACROSS> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
-    ta.init(W, K, (int64_t)items.m * BM, K, V, nullptr, wave, lane);
+  auto setup = [&](Tile<C::BM, C::NT, ACROSS> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
+    ta.init(W, K, (int64_t)items.m * C::BM, K, V, nullptr, wave, lane);
     tbl.init(E, te, (int64_t)items.n * C::BN, n, lde, nullptr, wave, lane);
     const int fours = (int)(lde / 128), per = (fours + ranges - 1) / ranges;
     *s0 = items.range * per * 4;
     *s1 = min(*s0 + per * 4, fours * 4);
   };
-  auto begin = [&]() { m0 = items.m * BM, n0 = items.n * C::BN, range = items.range; };
+  auto begin = [&]() { m0 = items.m * C::BM, n0 = items.n * C::BN, range = items.range; };
   auto finish = [&](Acc<C> &acc) {
     arrive();
 #pragma unroll
@@ -565,17 +566,17 @@ __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, 
   const int n = block_rows(rows, row0, tb);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  Items items = {(int)((K + BM - 1) / BM), (int)((V + C::BN - 1) / C::BN), 1};
+  Items items = {(int)((K + C::BM - 1) / C::BM), (int)((V + C::BN - 1) / C::BN), 1};
   int m0 = 0, n0 = 0;
   // (no rows: four steps over the zeros that k_head_combine leaves behind the block's last row)
-  auto setup = [&](Tile<BM, C::NT, ACROSS> &ta, Tile<C::BN, C::NT, BLOCKS_ACROSS> &tbl, int *s0, int *s1) {
+  auto setup = [&](Tile<C::BM, C::NT, ACROSS> &ta, Tile<C::BN, C::NT, BLOCKS_ACROSS> &tbl, int *s0, int *s1) {
     const int deep = max((n + 127) / 128, 1);
-    ta.init(Xs, K, (int64_t)items.m * BM, K, deep * 128, nullptr, wave, lane);
+    ta.init(Xs, K, (int64_t)items.m * C::BM, K, deep * 128, nullptr, wave, lane);
     tbl.init(E, te, (int64_t)items.n * C::BN, lde, max(n, 1), nullptr, wave, lane);
     *s0 = 0;
     *s1 = deep * 4;
   };
-  auto begin = [&]() { m0 = items.m * BM, n0 = items.n * C::BN; };
+  auto begin = [&]() { m0 = items.m * C::BM, n0 = items.n * C::BN; };
   auto finish = [&](Acc<C> &acc) {
     arrive();
 #pragma unroll
@@ -613,17 +614,17 @@ __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, 
   products<C, ACROSS, BLOCKS_ACROSS>(items, ring, wave, lane, setup, begin, finish);
 }
 
-// Workgroups of a launch over `items` output tiles: as many as run at once (one per CU, two of the narrow tile), each
+// Workgroups of a launch over `items` output tiles: as many as run at once (one per CU, three of the narrow tile), each
 // taking several; below that one each, in eights (every XCD's run of items has the same length).
 int64_t groups(int64_t items, int tile_rows) {
-  const int64_t most = tile_rows == 64 ? 512 : 256;
+  const int64_t most = tile_rows == 64 ? kHeadSlots64 : 256;
   return items < most ? (items + 7) / 8 * 8 : most;
 }
 
 }  // namespace
 
 #define QLORA_HEAD_TILES(rows_, CALL)   \
-  switch (head_tile_rows(rows_)) {      \
+  switch ((rows_).tile_rows) {          \
     case 64: { CALL(H64); break; }      \
     case 128: { CALL(H128); break; }    \
     default: { CALL(H256); break; }     \
@@ -635,7 +636,7 @@ hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, co
 #define QLORA_CALL(CFG)                                                                                               \
   launch(k_head_logits<CFG>, dim3((unsigned)groups(ntile * ((tb + CFG::BN - 1) / CFG::BN), CFG::BN)), dim3(CFG::NT), 0, s, \
          rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, te, k)
-  QLORA_HEAD_TILES(tb, QLORA_CALL)
+  QLORA_HEAD_TILES(rows, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();
 }
@@ -643,11 +644,12 @@ hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, co
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
                           hipStream_t s) {
-  const int64_t most = (tb + head_tile_rows(tb) - 1) / head_tile_rows(tb) * ((K + BM - 1) / BM) * 16;  // 16 ranges
+  const int tr = rows.tile_rows, tc = head_tile_cols(tr);
+  const int64_t most = (tb + tr - 1) / tr * ((K + tc - 1) / tc) * kHeadRanges;
 #define QLORA_CALL(CFG)                                                                                              \
   launch(k_head_dx<CFG>, dim3((unsigned)groups(most, CFG::BN)), dim3(CFG::NT), 0, s, rows, row0, tb, E, lde, te, W, V, K, scale, part, \
          dX)
-  QLORA_HEAD_TILES(tb, QLORA_CALL)
+  QLORA_HEAD_TILES(rows, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();
 }
@@ -655,7 +657,7 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,
                           hipStream_t s) {
-  launch(k_head_dw<H256>, dim3((unsigned)groups(((K + BM - 1) / BM) * ((V + 255) / 256), 256)), dim3(H256::NT), 0, s, rows,
+  launch(k_head_dw<H256>, dim3((unsigned)groups(((K + 255) / 256) * ((V + 255) / 256), 256)), dim3(H256::NT), 0, s, rows,
          row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, dW);
   return hipGetLastError();
 }

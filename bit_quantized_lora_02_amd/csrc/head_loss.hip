@@ -20,7 +20,7 @@ namespace qlora {
 namespace {
 
 constexpr int kPrepThreads = 256;
-constexpr int kScanRows = 16;  // consecutive rows per thread and pass of the numbering
+constexpr int kScanRows = 8;  // consecutive rows per thread and pass of the numbering
 
 __device__ __forceinline__ float wave_sum(float x) {
 #pragma unroll
@@ -35,16 +35,51 @@ __device__ __forceinline__ float wave_max(float x) {
 
 __device__ __forceinline__ bool target_ok(int64_t v, int64_t V) { return v >= 0 && v < V; }
 
-// A row of a distillation batch counts if one of its targets is inside the vocabulary with a logit above -inf.
-__device__ __forceinline__ bool row_counts(const int64_t *__restrict__ labels, const int32_t *__restrict__ index,
-                                           const float *__restrict__ logit, int k, int64_t V, int64_t t) {
-  if (labels) return target_ok(labels[t], V);
-  for (int i = 0; i < k; ++i)
-    if (target_ok(index[t * k + i], V) && logit[t * k + i] > -INFINITY) return true;
-  return false;
+// Numbers the rows with counts(t), in order, by one workgroup of `threads`; then the blocks' dX ranges.
+template <int threads, class Counts>
+__device__ __forceinline__ void number_rows(int64_t T, int64_t K, Counts counts, int32_t *__restrict__ n,
+                                            int32_t *__restrict__ list, int32_t *__restrict__ ranges,
+                                            const HeadBlocks &blocks) {
+  __shared__ int s_wave[threads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  for (int64_t t0 = 0; t0 < T; t0 += threads * kScanRows) {
+    const int64_t mine = t0 + (int64_t)tid * kScanRows;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < kScanRows; ++j)
+      if (mine + j < T && counts(mine + j)) bits |= 1u << j;
+    int before = __popc(bits);  // inclusive sum over the wave, then over the waves
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(before, o);
+      if (lane >= o) before += up;
+    }
+    if (lane == 63) s_wave[wave] = before;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < threads / 64; ++w) {
+      if (w < wave) before += s_wave[w];
+      total += s_wave[w];
+    }
+    int at = base + before - __popc(bits);
+#pragma unroll
+    for (int j = 0; j < kScanRows; ++j)
+      if (bits >> j & 1) list[at++] = (int32_t)(mine + j);
+    base += total;
+    __syncthreads();
+  }
+  if (tid == 0) *n = base;
+  for (int64_t b = tid; ranges && b < blocks.count; b += threads) {
+    const int64_t row0 = b * blocks.tb, tb = T - row0 < blocks.tb ? T - row0 : blocks.tb;
+    const int64_t have = base - row0 < tb ? base - row0 : tb;
+    ranges[b] = have > 0 ? head_dx_ranges(have, K, blocks.lde, blocks.tile_rows) : 1;
+  }
 }
 
-// Workgroup 0 numbers the rows that count, in order; the other workgroups' waves take a row of X each: its first
+// With labels, workgroup 0 numbers the rows that count (their teachers' rows are looked at first: k_head_list); the
+// other workgroups' waves take a row of X each: its first
 // target (the label, or the teacher's most probable one; the first of equals) and that target's logit by a dot
 // product (binary32 FMA), the teacher's softmax, and the row in the blocks of 32 columns that the logit product reads
 // (zeros past K); or, for a row that does not count, its zero loss and gradient.
@@ -60,41 +95,8 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
                                                             int64_t ldx) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (blockIdx.x == 0) {
-    __shared__ int s_wave[kPrepThreads / 64];
-    int base = 0;
-    for (int64_t t0 = 0; t0 < T; t0 += kPrepThreads * kScanRows) {
-      const int64_t mine = t0 + (int64_t)tid * kScanRows;
-      uint32_t bits = 0;
-#pragma unroll
-      for (int j = 0; j < kScanRows; ++j)
-        if (mine + j < T && row_counts(labels, index, logit, k, V, mine + j)) bits |= 1u << j;
-      int before = __popc(bits);  // inclusive sum over the wave, then over the waves
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int up = __shfl_up(before, o);
-        if (lane >= o) before += up;
-      }
-      if (lane == 63) s_wave[wave] = before;
-      __syncthreads();
-      int total = 0;
-#pragma unroll
-      for (int w = 0; w < kPrepThreads / 64; ++w) {
-        if (w < wave) before += s_wave[w];
-        total += s_wave[w];
-      }
-      int at = base + before - __popc(bits);
-#pragma unroll
-      for (int j = 0; j < kScanRows; ++j)
-        if (bits >> j & 1) list[at++] = (int32_t)(mine + j);
-      base += total;
-      __syncthreads();
-    }
-    if (tid == 0) *n = base;
-    for (int64_t b = tid; ranges && b < blocks.count; b += kPrepThreads) {
-      const int64_t row0 = b * blocks.tb, tb = T - row0 < blocks.tb ? T - row0 : blocks.tb;
-      const int64_t have = base - row0 < tb ? base - row0 : tb;
-      ranges[b] = have > 0 ? head_dx_ranges(have, K, blocks.lde, head_tile_rows(tb)) : 1;
-    }
+    if (labels)
+      number_rows<kPrepThreads>(T, K, [&](int64_t t) { return target_ok(labels[t], V); }, n, list, ranges, blocks);
     return;
   }
   const int64_t t = (int64_t)(blockIdx.x - 1) * (kPrepThreads / 64) + wave;
@@ -134,7 +136,10 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
     }
   }
   if (y < 0) {
-    if (lane == 0) loss[t] = 0.f;
+    if (lane == 0) {
+      loss[t] = 0.f;
+      rows.refcol[t] = -1;
+    }
     if (dX)
       for (int64_t at = 8 * lane; at < K; at += 512)
         *reinterpret_cast<u32x4_t *>(dX + t * K + at) = u32x4_t{0u, 0u, 0u, 0u};
@@ -163,15 +168,29 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
   }
 }
 
+// Numbers the rows whose first target k_head_prep found.
+constexpr int kListThreads = 1024;
+__global__ __launch_bounds__(kListThreads) void k_head_list(int64_t T, int64_t K, const int32_t *__restrict__ refcol,
+                                                            int32_t *__restrict__ n, int32_t *__restrict__ list,
+                                                            int32_t *__restrict__ ranges, HeadBlocks blocks) {
+  number_rows<kListThreads>(T, K, [&](int64_t t) { return refcol[t] >= 0; }, n, list, ranges, blocks);
+}
+
 // One workgroup per tile of rows: a counting sort of its targets by output tile.  (The order within an output tile is
 // that of the LDS counters; every target's logit goes to a place of its own, so no result depends on it.)
 constexpr int kBucketThreads = 1024;
 __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, int64_t row0, int64_t tb, int tile_rows,
                                                                 const int32_t *__restrict__ index, int k, int64_t V,
-                                                                int ntile) {
+                                                                int ntile, int tile_cols, int64_t T, int64_t K,
+                                                                int32_t *n_out, int32_t *list, int32_t *ranges,
+                                                                HeadBlocks blocks) {
   extern __shared__ int s_count[];  // [ntile]
   __shared__ int s_wave[kBucketThreads / 64];
-  int64_t n = *rows.n - row0;
+  if (n_out) {  // one tile of rows: this workgroup numbers them
+    number_rows<kBucketThreads>(T, K, [&](int64_t t) { return rows.refcol[t] >= 0; }, n_out, list, ranges, blocks);
+    __syncthreads();
+  }
+  int64_t n = *(volatile const int32_t *)rows.n - row0;
   n = n < tb ? n : tb;
   const int64_t n0 = (int64_t)blockIdx.x * tile_rows;
   if (n0 >= n) return;
@@ -180,13 +199,14 @@ __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, i
   for (int i = tid; i < ntile; i += kBucketThreads) s_count[i] = 0;
   __syncthreads();
   auto each = [&](auto use) {
+#pragma unroll 4
     for (int e = tid; e < have; e += kBucketThreads) {
       const int nj = e / k, j = e - nj * k;
-      const int64_t v = index[(int64_t)rows.list[row0 + n0 + nj] * k + j];
+      const int64_t v = index[(int64_t)((volatile const int32_t *)rows.list)[row0 + n0 + nj] * k + j];
       if (target_ok(v, V)) use((int)v, nj, j);
     }
   };
-  each([&](int v, int, int) { atomicAdd(&s_count[v / kHeadTile], 1); });
+  each([&](int v, int, int) { atomicAdd(&s_count[v / tile_cols], 1); });
   __syncthreads();
   // exclusive sums over the tiles, a run of `per` of them per thread
   const int per = (ntile + kBucketThreads - 1) / kBucketThreads, i0 = tid * per;
@@ -212,12 +232,12 @@ __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, i
   __syncthreads();
   uint32_t *target = rows.target + (int64_t)blockIdx.x * tile_rows * k;
   each([&](int v, int nj, int j) {
-    target[atomicAdd(&s_count[v / kHeadTile], 1)] = (uint32_t)j | (uint32_t)(v % kHeadTile) << 8 | (uint32_t)nj << 16;
+    target[atomicAdd(&s_count[v / tile_cols], 1)] = (uint32_t)j | (uint32_t)(v % tile_cols) << 8 | (uint32_t)nj << 16;
   });
 }
 
 // One wave per counted row of the block.
-__global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, int64_t tb,
+__global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, int64_t tb, int tile_cols,
                                                       const float2 *__restrict__ stat, int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
                                                       const int32_t *__restrict__ index, int k, float tau,
                                                       const float *__restrict__ weight, float *__restrict__ loss,
@@ -272,7 +292,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   auto e = [&](int64_t v) { return E + (v / 32 * te + i) * 32 + v % 32; };
   if (wide) {  // bring the row's tiles to one unit (a factor below binary32's range is applied in two halves)
     for (int64_t at = 8 * lane; at < lde; at += 512) {
-      const float d = exp2f(0.5f * (st[at / kHeadTile].x - u) * c);
+      const float d = exp2f(0.5f * (st[at / tile_cols].x - u) * c);
       u32x4_t v = *reinterpret_cast<u32x4_t *>(e(at));
 #pragma unroll
       for (int w = 0; w < 4; ++w) v[w] = pack_bf16x2(bf16_lo_to_f32(v[w]) * d * d, bf16_hi_to_f32(v[w]) * d * d);
@@ -344,11 +364,19 @@ hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t
   return hipGetLastError();
 }
 
+hipError_t launch_head_list(const HeadRows &rows, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
+                            const HeadBlocks &blocks, hipStream_t s) {
+  launch(k_head_list, dim3(1), dim3(kListThreads), 0, s, T, K, (const int32_t *)rows.refcol, n, list, ranges, blocks);
+  return hipGetLastError();
+}
+
 hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
-                              int64_t ntile, hipStream_t s) {
-  const int tr = head_tile_rows(tb);
+                              int64_t ntile, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
+                              const HeadBlocks &blocks, hipStream_t s) {
+  const int tr = rows.tile_rows;
   launch(k_head_bucket, dim3((unsigned)((tb + tr - 1) / tr)), dim3(kBucketThreads), (uint32_t)ntile * 4, s, rows, row0,
-         tb, tr, index, k, V, (int)ntile);
+         tb, tr, index, k, V, (int)ntile, head_tile_cols(tr), T, K, head_one_tile(T, rows) ? n : (int32_t *)nullptr, list,
+         ranges, blocks);
   return hipGetLastError();
 }
 
@@ -357,8 +385,8 @@ hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, c
                                const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde, int64_t te,
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s) {
   const int64_t grid_rows = Xs ? (tb > 0 ? (tb + 127) / 128 * 128 : 128) : tb;
-  launch(k_head_combine, dim3((unsigned)((grid_rows + 3) / 4)), dim3(256), 0, s, rows, row0, tb, stat, ntile, V, labels, index, k,
-         tau, weight, loss, scale, E, lde, te, X, K, Xs);
+  launch(k_head_combine, dim3((unsigned)((grid_rows + 3) / 4)), dim3(256), 0, s, rows, row0, tb,
+         head_tile_cols(rows.tile_rows), stat, ntile, V, labels, index, k, tau, weight, loss, scale, E, lde, te, X, K, Xs);
   return hipGetLastError();
 }
 
