@@ -453,7 +453,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
     return at;
   };
   p.off_n = take(4);
-  p.off_ranges = take((size_t)p.b.count * 4);
+  p.off_ranges = take((size_t)p.b.count * 8);
   p.off_xt = take((size_t)ceil_div(K, 128) * p.ldx * 256);
   p.off_list = take((size_t)T * 4);
   p.off_ref = take((size_t)T * 4);
@@ -543,7 +543,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   if (k > 0 && !(T > 0 && head_one_tile(T, rows))) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, rg, p.b, s));
   for (int64_t b = 0; b < p.b.count; ++b) {
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
-    rows.ranges = ranges + b;
+    rows.ranges = ranges + 2 * b;
     if (tb > 0 && k > 0)
       LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, p.ntile, T, K, n, list, rg, p.b, s));
     if (tb > 0)

@@ -16,7 +16,7 @@ typedef uint16_t bf16_t;
 // and E[v] = exp2((z[v] - u) c) is what is kept of logit v.
 struct HeadRows {
   const int32_t *n;       // rows that count
-  const int32_t *ranges;  // the dX product's ranges for the block at hand
+  const int32_t *ranges;  // the dX product's ranges for the block at hand: of its whole tiles, of the rows behind them
   int tile_rows;          // rows of the products' tiles
   const int32_t *list;  // [T] their rows in X
   float *ref;           // [T] by row of X: the logit of the row's first target
@@ -40,28 +40,9 @@ inline int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 :
 // Up to 64 rows the products are bound by the stream of W, and the smaller tile gives every CU some of it.
 __host__ __device__ inline int head_tile_cols(int tile_rows) { return tile_rows == 64 ? 128 : 256; }
 
-// Most ranges of the dX product's reduction, and workgroups of the narrow tile that run at once (three per CU).
+// Most ranges of the dX product's reduction (one per lane of half a wave when they are chosen), and workgroups of the
+// narrow tile that run at once (three per CU).
 constexpr int kHeadRanges = 32, kHeadSlots64 = 768;
-
-// Reduction ranges of the dX product: `tiles` output tiles of `steps` 64-deep steps on `slots` workgroups that run
-// at once.  A round of workgroups costs its steps plus about 10 (first loads, output); more than one range also
-// costs the binary32 partial sums, written and read once: about 33 steps' time for 256 tiles of 256 x 256.
-__host__ __device__ inline int head_split(int tiles, int steps, int slots, int tile_elems) {
-  int best = 1;
-  float best_cost = 3.4e38f;
-#pragma unroll
-  for (int s = 1; s <= kHeadRanges; ++s) {
-    if (s > 1 && (steps < 8 * s || tiles * s > 4 * slots)) break;
-    const float rounds = (float)((tiles * s + slots - 1) / slots);
-    const float cost = rounds * (float)((steps + s - 1) / s + 10) +
-                       (s > 1 ? 33.f * (float)(tiles * s) * (float)tile_elems / (256.f * 65536.f) : 0.f);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  return best;
-}
 
 // How the counted rows are taken in blocks.
 struct HeadBlocks {
@@ -91,23 +72,33 @@ hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, c
 hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t K,
                               const float *scale, bf16_t *dX, hipStream_t s);
 
-// Room in floats for the dX product's partial sums: ranges * tiles is at most 4 times the slots.
-inline size_t head_part_floats(int64_t tb, int64_t K, int tile_rows) {
-  const size_t bn = tile_rows, slots = bn == 64 ? kHeadSlots64 : 256;
-  const size_t most = 4 * slots * bn * head_tile_cols(tile_rows), all = kHeadRanges * (size_t)tb * K;
-  return all < most ? all : most;
+// Rows that go to tiles of `tile_rows`: all, but for 128 or fewer behind the last whole 256-row tile, which take
+// 128-row tiles (measured: a 256 x 128 tile costs 0.6 of a 256 x 256 one).
+__host__ __device__ inline int head_whole_rows(int n, int tile_rows) {
+  const int rest = n % 256;
+  return tile_rows == 256 && rest >= 1 && rest <= 128 ? n - rest : n;
 }
-// Ranges of the dX product of n rows: all of the same length but the last, none empty.
-__host__ __device__ inline int head_dx_ranges(int64_t n, int64_t K, int64_t lde, int tile_rows) {
-  const int cols = head_tile_cols(tile_rows);
-  const int tiles = (int)(((uint32_t)n + tile_rows - 1) / tile_rows * (uint32_t)((K + cols - 1) / cols));
-  const int fours = (int)(lde / 128);
-  const int s = head_split(tiles, fours * 2, tile_rows == 64 ? kHeadSlots64 : 256, cols * tile_rows);
-  const int per = (fours + s - 1) / s;
-  return (fours + per - 1) / per;
+// Columns of the vocabulary (of V) that the dW product takes in 256-wide tiles, `tiles_m` tiles of X's columns each:
+// all, but where the last round of 256 workgroups would be half empty its tiles are cut in two.
+__host__ __device__ inline int head_whole_columns(int64_t V, int tiles_m) {
+  const int tiles = (int)((V + 255) / 256), rounds = (int)((int64_t)tiles * tiles_m / 256);
+  const int64_t rest = (int64_t)tiles * tiles_m - (int64_t)rounds * 256;
+  const int keep = (int)((int64_t)rounds * 256 / tiles_m);
+  return rounds > 0 && keep > 0 && rest >= 1 && rest <= 128 && keep * 256 < V ? keep * 256 : (int)V;
 }
 
-// The logits take X as k_head_prep lays it out: Xt [4 (K / 128 rounded up)][ldx][32], zero past K.
+// The dX product's partial sums: of the whole tiles' rows first, where they have any.
+__host__ __device__ inline int64_t head_first_sums(int64_t whole, int ranges, int64_t K) {
+  return ranges > 1 ? ranges * whole * K : 0;
+}
+// Room in floats for them: ranges * tiles is at most 4 times the slots, in either pass.
+inline size_t head_part_floats(int64_t tb, int64_t K, int tile_rows) {
+  const size_t bn = tile_rows, slots = bn == 64 ? kHeadSlots64 : 256;
+  const size_t most = 4 * slots * (bn + (bn == 256 ? 128 : 0)) * head_tile_cols(tile_rows);
+  const size_t all = kHeadRanges * (size_t)tb * K;
+  return all < most ? all : most;
+}
+
 hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
                               bf16_t *E, int64_t lde, int64_t te, int k, hipStream_t s);
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,

@@ -212,7 +212,7 @@ __device__ __forceinline__ void arrive() {
 
 // Output tiles ("items") are numbered so that each XCD (workgroups go round the 8 XCDs) takes a run of consecutive
 // ones, and consecutive ones are blocks of 4 m-tiles x all n-tiles: the 32 workgroups of an XCD then share 4 + 8
-// operand tiles.  Workgroup w takes the items of lin = w, w + gridDim, ...
+// operand tiles.  A workgroup takes the items lin, lin + stride, ...
 struct Items {
   int tiles_m, tiles_n, ranges;
   int m, n, range;
@@ -229,6 +229,23 @@ struct Items {
   }
 };
 
+// A kernel whose rows do not fill whole 256-row tiles gives the last 128 or fewer to narrower tiles, in a second pass
+// over items.  The workgroups that had one item less in the first pass take them, where that is at most two each
+// (a narrow item takes 0.6 of the time of a wide one), else all of them.
+struct Turn {
+  uint32_t lin, stride;
+};
+__device__ __forceinline__ Turn second_pass(const Items &first, uint32_t more) {
+  const uint32_t total = (uint32_t)first.tiles_m * first.tiles_n * first.ranges, per = (total + 7) / 8;
+  const uint32_t groups = gridDim.x / 8, at = blockIdx.x >> 3, busy = per % groups, free = groups - busy;
+  if ((more + 7) / 8 > 2 * free) return Turn{(at + free) % groups * 8 + (blockIdx.x & 7), gridDim.x};
+  return Turn{at < busy ? 0x7ffffff8u : (at - busy) * 8 + (blockIdx.x & 7), free * 8};  // (out of range: none)
+}
+__device__ __forceinline__ void between_passes() {
+  arrive();
+  meet();
+}
+
 // A workgroup's loop over its items, each a reduction over steps [s0, s1) of both operands' tiles, a multiple of four.
 //
 // Step s multiplies the tiles of slot s % 4 while the copies of steps s + 1 .. s + 3 are in flight.  Its first MFMAs'
@@ -242,13 +259,13 @@ struct Items {
 //  setup(ta, tb, s0, s1): the tiles and steps of the item just taken     begin(): notes for its epilogue
 //  finish(acc): its epilogue; calls arrive() before its first store
 template <class C, int KA, int KB, class Setup, class Begin, class Finish>
-__device__ __forceinline__ void products(Items &items, const Ring &ring, int wave, int lane, Setup setup, Begin begin,
-                                         Finish finish) {
+__device__ __forceinline__ void products(Items &items, Turn turn, const Ring &ring, int wave, int lane, Setup setup,
+                                         Begin begin, Finish finish) {
   typedef Tile<C::BM, C::NT, KA> TileA;
   typedef Tile<C::BN, C::NT, KB> TileB;
   constexpr int L = TileA::LD + TileB::LD, L1 = L / 2;  // copies per thread and step, those before the meeting
   static_assert(2 * L < 64, "copies in flight are counted in six bits");
-  uint32_t lin = blockIdx.x;
+  uint32_t lin = turn.lin;
   if (!items.take(lin)) return;
   TileA ta;
   TileB tb;
@@ -319,7 +336,7 @@ __device__ __forceinline__ void products(Items &items, const Ring &ring, int wav
       step(std::integral_constant<int, 3>(), s + 6, false);
     }
     step(std::integral_constant<int, 0>(), s + 3, s == s0);
-    lin += gridDim.x;
+    lin += turn.stride;
     const bool more = items.take(lin);
     const bool fresh = s == s0;
     if (more) setup(ta, tb, &s0, &s1);  // (else the first steps of this item are copied once more)
@@ -347,23 +364,37 @@ __device__ __forceinline__ int block_rows(const HeadRows &rows, int64_t row0, in
 // ------------------------------------------------------------------ logits
 // m: columns of the vocabulary, n: counted rows of the block.
 // X as k_head_prep lays it out (ldx rows per block).
+struct LogitArgs {
+  HeadRows rows;
+  int64_t row0, tb;
+  const bf16_t *X;
+  int64_t ldx;
+  const bf16_t *W;
+  int64_t V, K;
+  float c;
+  float2 *stat;
+  int64_t ntile;
+  bf16_t *E;
+  int64_t lde, te;
+  int k;
+};
+
+// Rows [first, n) of the block; `s_max` and `s_sum` hold WAVES_M x BN each.
 template <class C>
-__global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t row0, int64_t tb,
-                                                       const bf16_t *__restrict__ X, int64_t ldx,
-                                                       const bf16_t *__restrict__ W, int64_t V, int64_t K, float c,
-                                                       float2 *__restrict__ stat, int64_t ntile,
-                                                       bf16_t *__restrict__ E, int64_t lde, int64_t te, int k) {
-  QLORA_RING(C, ring);
-  __shared__ float s_max[C::WAVES_M][C::BN], s_sum[C::WAVES_M][C::BN];
-  const int n = block_rows(rows, row0, tb);
-  if (n == 0) return;
+__device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n, Items &items, Turn turn,
+                                            const Ring &ring, float *s_max_, float *s_sum_) {
+  const HeadRows &rows = g.rows;
+  const int64_t row0 = g.row0, V = g.V, K = g.K, ntile = g.ntile, te = g.te;
+  const float c = g.c;
+  const int k = g.k;
+  bf16_t *const E = g.E;
+  float(*const s_max)[C::BN] = (float(*)[C::BN])s_max_, (*const s_sum)[C::BN] = (float(*)[C::BN])s_sum_;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  Items items = {(int)ntile, (n + C::BN - 1) / C::BN, 1};
   int m0 = 0, n0 = 0;
   auto setup = [&](Tile<C::BM, C::NT, LINES> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
-    ta.init(W, K, (int64_t)items.m * C::BM, V, K, nullptr, wave, lane);
-    tbl.init(X, ldx, (int64_t)items.n * C::BN, n, K, rows.list + row0, wave, lane);
+    ta.init(g.W, K, (int64_t)items.m * C::BM, V, K, nullptr, wave, lane);
+    tbl.init(g.X, g.ldx, first + (int64_t)items.n * C::BN, n, K, rows.list + row0, wave, lane);
     *s0 = 0;
     *s1 = (int)((K + 127) / 128 * 4);
   };
@@ -374,16 +405,17 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
   uint32_t target = 0;
   const uint32_t *targets = nullptr;
   auto begin = [&]() {
-    m0 = items.m * C::BM, n0 = items.n * C::BN;
+    m0 = items.m * C::BM, n0 = first + items.n * C::BN;
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
       const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
       t[j] = rows.list[row0 + (row < n ? row : n - 1)];
     }
     if (rows.target) {
-      const int32_t *const b = rows.bucket + (int64_t)items.n * (ntile + 1) + items.m;
+      const int row_tile = n0 / rows.tile_rows;
+      const int32_t *const b = rows.bucket + (int64_t)row_tile * (ntile + 1) + items.m;
       t0 = b[0], t1 = b[1];
-      targets = rows.target + (int64_t)items.n * C::BN * k;
+      targets = rows.target + (int64_t)row_tile * rows.tile_rows * k;
       if (t0 + lane < t1) target = targets[t0 + lane];
     }
   };
@@ -473,7 +505,7 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
           const u32x4_t o = join_halves(
               u32x2_t{pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3])},
               u32x2_t{pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7])});
-          if (row < n && m0 + (wm * C::WM + i) * 32 < lde) *reinterpret_cast<u32x4_t *>(out + 16 * q) = o;
+          if (row < n && m0 + (wm * C::WM + i) * 32 < g.lde) *reinterpret_cast<u32x4_t *>(out + 16 * q) = o;
         }
       }
     }
@@ -485,37 +517,64 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(HeadRows rows, int64_t ro
         float sum = s_sum[0][nj];
 #pragma unroll
         for (int w = 1; w < C::WAVES_M; ++w) sum += s_sum[w][nj];
-        if (n0 + nj < n) stat[(int64_t)(n0 + nj) * ntile + m0 / C::BM] = make_float2(u[j], sum);
+        if (n0 + nj < n) g.stat[(int64_t)(n0 + nj) * ntile + m0 / C::BM] = make_float2(u[j], sum);
       }
     }
   };
-  products<C, LINES, BLOCKS>(items, ring, wave, lane, setup, begin, finish);
+  products<C, LINES, BLOCKS>(items, turn, ring, wave, lane, setup, begin, finish);
+}
+
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_head_logits(LogitArgs g) {
+  QLORA_RING(C, ring);
+  __shared__ float s_max[C::WAVES_M * C::BN], s_sum[C::WAVES_M * C::BN];
+  const int n = block_rows(g.rows, g.row0, g.tb);
+  if (n == 0) return;
+  const int whole = head_whole_rows(n, C::BN);
+  Items items = {(int)g.ntile, (whole + C::BN - 1) / C::BN, 1};
+  if (whole > 0) logit_items<C>(g, 0, whole, items, Turn{blockIdx.x, gridDim.x}, ring, s_max, s_sum);
+  if constexpr (C::BN == 256) {
+    if (whole == n) return;
+    const Turn turn = second_pass(items, (uint32_t)g.ntile);
+    between_passes();
+    items = {(int)g.ntile, 1, 1};
+    logit_items<H128>(g, whole, n, items, turn, ring, s_max, s_sum);
+  }
 }
 
 // ---------------------------------------------------------------------- dX
 // m: columns of X, n: counted rows of the block; reduction over the vocabulary (lde of it: E is zero past V).
+struct DxArgs {
+  HeadRows rows;
+  int64_t row0, tb;
+  const bf16_t *E;
+  int64_t lde, te;
+  const bf16_t *W;
+  int64_t V, K;
+  const float *scale;
+  float *part;
+  bf16_t *dX;
+};
+
+// Rows [first, n) of the block in `ranges` ranges; with more than one their sums go to part[range][row - first][K].
 template <class C>
-__global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, int64_t tb,
-                                                   const bf16_t *__restrict__ E, int64_t lde, int64_t te,
-                                                   const bf16_t *__restrict__ W, int64_t V, int64_t K,
-                                                   const float *__restrict__ scale, float *__restrict__ part,
-                                                   bf16_t *__restrict__ dX) {
-  QLORA_RING(C, ring);
-  const int n = block_rows(rows, row0, tb);
-  if (n == 0) return;
-  const int ranges = *rows.ranges;
+__device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int ranges, float *part, Items &items,
+                                         Turn turn, const Ring &ring) {
+  const HeadRows &rows = g.rows;
+  const int64_t row0 = g.row0, K = g.K;
+  const float *const scale = g.scale;
+  bf16_t *const dX = g.dX;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  Items items = {(int)((K + C::BM - 1) / C::BM), (n + C::BN - 1) / C::BN, ranges};
   int m0 = 0, n0 = 0, range = 0;
   auto setup = [&](Tile<C::BM, C::NT, ACROSS> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
-    ta.init(W, K, (int64_t)items.m * C::BM, K, V, nullptr, wave, lane);
-    tbl.init(E, te, (int64_t)items.n * C::BN, n, lde, nullptr, wave, lane);
-    const int fours = (int)(lde / 128), per = (fours + ranges - 1) / ranges;
+    ta.init(g.W, K, (int64_t)items.m * C::BM, K, g.V, nullptr, wave, lane);
+    tbl.init(g.E, g.te, first + (int64_t)items.n * C::BN, n, g.lde, nullptr, wave, lane);
+    const int fours = (int)(g.lde / 128), per = (fours + ranges - 1) / ranges;
     *s0 = items.range * per * 4;
     *s1 = min(*s0 + per * 4, fours * 4);
   };
-  auto begin = [&]() { m0 = items.m * C::BM, n0 = items.n * C::BN, range = items.range; };
+  auto begin = [&]() { m0 = items.m * C::BM, n0 = first + items.n * C::BN, range = items.range; };
   auto finish = [&](Acc<C> &acc) {
     arrive();
 #pragma unroll
@@ -533,7 +592,7 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
           for (int q = 0; q < 4; ++q) {
             const int64_t mq = m + 8 * q + 4 * (lane >> 5);
             if (in && mq < K)  // K % 8 == 0: eight columns are all in or all out
-              *reinterpret_cast<float4 *>(part + ((int64_t)range * n + i) * K + mq) =
+              *reinterpret_cast<float4 *>(part + ((int64_t)range * (n - first) + (i - first)) * K + mq) =
                   make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
         } else {
@@ -550,33 +609,62 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(HeadRows rows, int64_t row0, 
       }
     }
   };
-  products<C, ACROSS, BLOCKS>(items, ring, wave, lane, setup, begin, finish);
+  products<C, ACROSS, BLOCKS>(items, turn, ring, wave, lane, setup, begin, finish);
+}
+
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_head_dx(DxArgs g) {
+  QLORA_RING(C, ring);
+  const int n = block_rows(g.rows, g.row0, g.tb);
+  if (n == 0) return;
+  const int tiles_m = (int)((g.K + C::BM - 1) / C::BM), ranges = g.rows.ranges[0], more = g.rows.ranges[1];
+  const int whole = more > 0 ? head_whole_rows(n, C::BN) : n;
+  Items items = {tiles_m, (whole + C::BN - 1) / C::BN, ranges};
+  if (whole > 0) dx_items<C>(g, 0, whole, ranges, g.part, items, Turn{blockIdx.x, gridDim.x}, ring);
+  if constexpr (C::BN == 256) {
+    if (whole == n) return;
+    const Turn turn = second_pass(items, (uint32_t)(tiles_m * more));
+    between_passes();
+    items = {tiles_m, 1, more};
+    dx_items<H128>(g, whole, n, more, g.part + head_first_sums(whole, ranges, g.K), items, turn, ring);
+  }
 }
 
 // ---------------------------------------------------------------------- dW
 // m: columns of X, n: columns of the vocabulary; reduction over the block's counted rows.  With `sums` (several
 // blocks) the binary32 sums are carried in it from block to block and rounded to dW after the last.
+struct DwArgs {
+  HeadRows rows;
+  int64_t row0, tb;
+  const bf16_t *E;
+  int64_t lde, te;
+  const bf16_t *Xs;
+  int64_t V, K;
+  float *sums;
+  int first, last;
+  bf16_t *dW;
+};
+
+// Columns [begin_v, end_v) of the vocabulary.
 template <class C>
-__global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, int64_t tb,
-                                                   const bf16_t *__restrict__ E, int64_t lde, int64_t te,
-                                                   const bf16_t *__restrict__ Xs, int64_t V, int64_t K,
-                                                   float *__restrict__ sums, int first, int last,
-                                                   bf16_t *__restrict__ dW) {
-  QLORA_RING(C, ring);
-  const int n = block_rows(rows, row0, tb);
+__device__ __forceinline__ void dw_items(const DwArgs &g, int begin_v, int end_v, Items &items, Turn turn,
+                                         const Ring &ring) {
+  const int64_t K = g.K;
+  float *const sums = g.sums;
+  bf16_t *const dW = g.dW;
+  const int n = block_rows(g.rows, g.row0, g.tb);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  Items items = {(int)((K + C::BM - 1) / C::BM), (int)((V + C::BN - 1) / C::BN), 1};
   int m0 = 0, n0 = 0;
   // (no rows: four steps over the zeros that k_head_combine leaves behind the block's last row)
   auto setup = [&](Tile<C::BM, C::NT, ACROSS> &ta, Tile<C::BN, C::NT, BLOCKS_ACROSS> &tbl, int *s0, int *s1) {
     const int deep = max((n + 127) / 128, 1);
-    ta.init(Xs, K, (int64_t)items.m * C::BM, K, deep * 128, nullptr, wave, lane);
-    tbl.init(E, te, (int64_t)items.n * C::BN, lde, max(n, 1), nullptr, wave, lane);
+    ta.init(g.Xs, K, (int64_t)items.m * C::BM, K, deep * 128, nullptr, wave, lane);
+    tbl.init(g.E, g.te, begin_v + (int64_t)items.n * C::BN, g.lde, max(n, 1), nullptr, wave, lane);
     *s0 = 0;
     *s1 = deep * 4;
   };
-  auto begin = [&]() { m0 = items.m * C::BM, n0 = items.n * C::BN; };
+  auto begin = [&]() { m0 = items.m * C::BM, n0 = begin_v + items.n * C::BN; };
   auto finish = [&](Acc<C> &acc) {
     arrive();
 #pragma unroll
@@ -590,15 +678,15 @@ __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, 
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int64_t mq = m + 8 * q + 4 * (lane >> 5);
-            if (v >= V || mq >= K) continue;
+            if (v >= end_v || mq >= K) continue;
             float4 *const p = reinterpret_cast<float4 *>(sums + v * K + mq);
-            if (!first) {
+            if (!g.first) {
               const float4 was = *p;
               o[4 * q] += was.x, o[4 * q + 1] += was.y, o[4 * q + 2] += was.z, o[4 * q + 3] += was.w;
             }
-            if (!last) *p = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            if (!g.last) *p = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
-          if (!last) continue;
+          if (!g.last) continue;
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -606,12 +694,25 @@ __global__ __launch_bounds__(C::NT) void k_head_dw(HeadRows rows, int64_t row0, 
               join_halves(u32x2_t{pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3])},
                           u32x2_t{pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7])});
           const int64_t mq = m + 16 * q + 8 * (lane >> 5);
-          if (v < V && mq < K) *reinterpret_cast<u32x4_t *>(dW + v * K + mq) = x;
+          if (v < end_v && mq < K) *reinterpret_cast<u32x4_t *>(dW + v * K + mq) = x;
         }
       }
     }
   };
-  products<C, ACROSS, BLOCKS_ACROSS>(items, ring, wave, lane, setup, begin, finish);
+  products<C, ACROSS, BLOCKS_ACROSS>(items, turn, ring, wave, lane, setup, begin, finish);
+}
+
+__global__ __launch_bounds__(H256::NT) void k_head_dw(DwArgs g) {
+  QLORA_RING(H256, ring);
+  const int tiles_m = (int)((g.K + 255) / 256), whole = head_whole_columns(g.V, tiles_m);
+  Items items = {tiles_m, (whole + 255) / 256, 1};
+  dw_items<H256>(g, 0, whole, items, Turn{blockIdx.x, gridDim.x}, ring);
+  if (whole == g.V) return;
+  const int narrow = ((int)g.V - whole + H128::BN - 1) / H128::BN;
+  const Turn turn = second_pass(items, (uint32_t)(tiles_m * narrow));
+  between_passes();
+  items = {tiles_m, narrow, 1};
+  dw_items<H128>(g, whole, (int)g.V, items, turn, ring);
 }
 
 // Workgroups of a launch over `items` output tiles: as many as run at once (one per CU, three of the narrow tile), each
@@ -635,7 +736,7 @@ hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, co
                               int64_t lde, int64_t te, int k, hipStream_t s) {
 #define QLORA_CALL(CFG)                                                                                               \
   launch(k_head_logits<CFG>, dim3((unsigned)groups(ntile * ((tb + CFG::BN - 1) / CFG::BN), CFG::BN)), dim3(CFG::NT), 0, s, \
-         rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, te, k)
+         LogitArgs{rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, te, k})
   QLORA_HEAD_TILES(rows, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();
@@ -647,8 +748,8 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
   const int tr = rows.tile_rows, tc = head_tile_cols(tr);
   const int64_t most = (tb + tr - 1) / tr * ((K + tc - 1) / tc) * kHeadRanges;
 #define QLORA_CALL(CFG)                                                                                              \
-  launch(k_head_dx<CFG>, dim3((unsigned)groups(most, CFG::BN)), dim3(CFG::NT), 0, s, rows, row0, tb, E, lde, te, W, V, K, scale, part, \
-         dX)
+  launch(k_head_dx<CFG>, dim3((unsigned)groups(most, CFG::BN)), dim3(CFG::NT), 0, s, \
+         DxArgs{rows, row0, tb, E, lde, te, W, V, K, scale, part, dX})
   QLORA_HEAD_TILES(rows, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();
@@ -657,8 +758,8 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,
                           hipStream_t s) {
-  launch(k_head_dw<H256>, dim3((unsigned)groups(((K + 255) / 256) * ((V + 255) / 256), 256)), dim3(H256::NT), 0, s, rows,
-         row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, dW);
+  launch(k_head_dw, dim3((unsigned)groups(((K + 255) / 256) * ((V + 255) / 256), 256)), dim3(H256::NT), 0, s,
+         DwArgs{rows, row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, dW});
   return hipGetLastError();
 }
 

@@ -35,6 +35,53 @@ __device__ __forceinline__ float wave_max(float x) {
 
 __device__ __forceinline__ bool target_ok(int64_t v, int64_t V) { return v >= 0 && v < V; }
 
+// Reduction ranges of the dX product, by one wave: `tiles` output tiles of `steps` 64-deep steps on `slots` workgroups
+// that run at once, lane s - 1 looking at s ranges.  A round of workgroups costs its steps plus about 10 (first
+// loads, output); more than one range also costs the binary32 partial sums, written and read once: about 33 steps'
+// time for 256 tiles of 256 x 256.
+struct Split {
+  int ranges;
+  float cost;  // in steps
+};
+__device__ __forceinline__ Split wave_split(int tiles, int steps, int slots, int tile_elems, int lane) {
+  const int s = (lane & (kHeadRanges - 1)) + 1;
+  const int rounds = (tiles * s + slots - 1) / slots;
+  float cost = (float)rounds * ((float)steps / (float)s + 10.f) +
+               (s > 1 ? 33.f * (float)tile_elems / (256.f * 65536.f) * (float)(tiles * s) : 0.f);
+  if (s > 1 && (steps < 8 * s || tiles * s > 4 * slots)) cost = INFINITY;
+  Split best = {s, cost};
+#pragma unroll
+  for (int o = kHeadRanges / 2; o > 0; o >>= 1) {
+    const Split other = {__shfl_xor(best.ranges, o), __shfl_xor(best.cost, o)};
+    if (other.cost < best.cost || (other.cost == best.cost && other.ranges < best.ranges)) best = other;
+  }
+  return best;
+}
+
+// Ranges for n rows: of their tiles, and of the rows behind the last whole tile where those take narrower ones (0:
+// they do not).  All of the same length but the last, none empty.
+__device__ __forceinline__ void dx_ranges(int n, int64_t K, int64_t lde, int tile_rows, int lane, int32_t *out) {
+  const int cols = head_tile_cols(tile_rows), tiles_m = (int)((K + cols - 1) / cols), fours = (int)(lde / 128);
+  const int slots = tile_rows == 64 ? kHeadSlots64 : 256, whole = head_whole_rows(n, tile_rows);
+  Split one = wave_split((n + tile_rows - 1) / tile_rows * tiles_m, fours * 2, slots, cols * tile_rows, lane);
+  int second = 0;
+  if (whole < n) {
+    const Split two = wave_split(tiles_m, fours * 2, slots, cols * 128, lane);
+    Split rest = {1, 0.f};
+    if (whole > 0) rest = wave_split(whole / tile_rows * tiles_m, fours * 2, slots, cols * tile_rows, lane);
+    if (rest.cost + 0.6f * two.cost < one.cost) {
+      one = rest;
+      const int per = (fours + two.ranges - 1) / two.ranges;
+      second = (fours + per - 1) / per;
+    }
+  }
+  const int per = (fours + one.ranges - 1) / one.ranges;
+  if (lane == 0) {
+    out[0] = (fours + per - 1) / per;
+    out[1] = second;
+  }
+}
+
 // Numbers the rows with counts(t), in order, by one workgroup of `threads`; then the blocks' dX ranges.
 template <int threads, class Counts>
 __device__ __forceinline__ void number_rows(int64_t T, int64_t K, Counts counts, int32_t *__restrict__ n,
@@ -71,10 +118,10 @@ __device__ __forceinline__ void number_rows(int64_t T, int64_t K, Counts counts,
     __syncthreads();
   }
   if (tid == 0) *n = base;
-  for (int64_t b = tid; ranges && b < blocks.count; b += threads) {
+  for (int64_t b = wave; ranges && b < blocks.count; b += threads / 64) {
     const int64_t row0 = b * blocks.tb, tb = T - row0 < blocks.tb ? T - row0 : blocks.tb;
     const int64_t have = base - row0 < tb ? base - row0 : tb;
-    ranges[b] = have > 0 ? head_dx_ranges(have, K, blocks.lde, blocks.tile_rows) : 1;
+    if (have > 0) dx_ranges((int)have, K, blocks.lde, blocks.tile_rows, lane, ranges + 2 * b);
   }
 }
 
@@ -331,17 +378,23 @@ __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0
   int64_t n = *rows.n - row0;
   n = n < tb ? n : tb;
   if (n <= 0) return;
-  const int ranges = *rows.ranges;
-  if (ranges == 1) return;  // the product wrote dX itself
   const int64_t per = K / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= n * per) return;
   const int64_t i = at / per, col = (at % per) * 8;
+  const int whole = rows.ranges[1] > 0 ? head_whole_rows((int)n, rows.tile_rows) : (int)n;
+  const bool second = i >= whole;
+  const int ranges = rows.ranges[second];
+  if (ranges == 1) return;  // the product wrote dX itself
+  const float *p = part + (second ? head_first_sums(whole, rows.ranges[0], K) : 0);
+  const int64_t count = second ? n - whole : whole;
+  p += (second ? i - whole : i) * K + col;
   float s[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) s[j] = 0.f;
-  for (int r = 0; r < ranges; ++r) {
-    const float4 a = *reinterpret_cast<const float4 *>(part + (r * n + i) * K + col);
-    const float4 b = *reinterpret_cast<const float4 *>(part + (r * n + i) * K + col + 4);
+#pragma unroll 4
+  for (int r = 0; r < ranges; ++r, p += count * K) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
     s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
     s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
   }

@@ -98,7 +98,8 @@ def verify(X, W, targets, weight, tau, call, dev="cuda"):
 
 
 SIZES = [(1, 1, 8), (1, 1000, 264), (2, 64, 2056), (3, 257, 64), (64, 256, 72), (65, 300, 128), (129, 1030, 200),
-         (300, 999, 520), (513, 2055, 256), (1100, 700, 1040)]
+         (300, 999, 520), (385, 300, 136), (513, 2055, 256), (1100, 700, 1040),
+         (300, 65536 + 7, 264), (40, 1 << 22, 8)]
 
 
 @pytest.mark.parametrize("T,V,K", SIZES)
