@@ -65,12 +65,14 @@ inline bool head_one_tile(int64_t T, const HeadRows &rows) { return T <= rows.ti
 hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
                               int64_t ntile, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
                               const HeadBlocks &blocks, hipStream_t s);
+// Losses, the targets' entries of E, and per row of the block the factor of dX and the remainder of the first target's
+// entry (scale), rows of X times the factor (Xs, for dW).
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
-                               const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde, int64_t te,
+                               const float *weight, float *loss, float2 *scale, bf16_t *E, int64_t lde, int64_t te,
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s);
-hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t K,
-                              const float *scale, bf16_t *dX, hipStream_t s);
+hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, const bf16_t *W,
+                              int64_t K, const float2 *scale, bf16_t *dX, hipStream_t s);
 
 // Rows that go to tiles of `tile_rows`: all, but for 128 or fewer behind the last whole 256-row tile, which take
 // 128-row tiles (measured: a 256 x 128 tile costs 0.6 of a 256 x 256 one).
@@ -102,7 +104,7 @@ inline size_t head_part_floats(int64_t tb, int64_t K, int tile_rows) {
 hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
                               bf16_t *E, int64_t lde, int64_t te, int k, hipStream_t s);
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
-                          const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
+                          const bf16_t *W, int64_t V, int64_t K, const float2 *scale, float *part, bf16_t *dX,
                           hipStream_t s);
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,

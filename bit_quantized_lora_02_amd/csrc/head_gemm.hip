@@ -551,7 +551,7 @@ struct DxArgs {
   int64_t lde, te;
   const bf16_t *W;
   int64_t V, K;
-  const float *scale;
+  const float2 *scale;
   float *part;
   bf16_t *dX;
 };
@@ -562,7 +562,7 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
                                          Turn turn, const Ring &ring) {
   const HeadRows &rows = g.rows;
   const int64_t row0 = g.row0, K = g.K;
-  const float *const scale = g.scale;
+  const float2 *const scale = g.scale;
   bf16_t *const dX = g.dX;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
@@ -581,8 +581,9 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
     for (int j = 0; j < C::WN; ++j) {
       const int i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
       const bool in = i < n;
-      const float f = in && ranges == 1 ? scale[i] : 1.f;
-      const int64_t t = in ? rows.list[row0 + i] : 0;
+      const float2 f = scale[in ? i : n - 1];
+      const int64_t t = rows.list[row0 + (in ? i : n - 1)];
+      const bf16_t *const w = g.W + rows.refcol[t] * K + 4 * (lane >> 5);
 #pragma unroll
       for (int mi = 0; mi < C::WM; ++mi) {
         const int64_t m = m0 + (wm * C::WM + mi) * 32;
@@ -596,12 +597,18 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
                   make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
         } else {
+          u32x2_t x[4];  // with the first target's remainder times its row of W
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const u32x2_t wv = m + 8 * q < K ? *reinterpret_cast<const u32x2_t *>(w + m + 8 * q) : u32x2_t{0u, 0u};
+            x[q] = u32x2_t{pack_bf16x2(fmaf(f.y, bf16_lo_to_f32(wv.x), v[4 * q]) * f.x,
+                                       fmaf(f.y, bf16_hi_to_f32(wv.x), v[4 * q + 1]) * f.x),
+                           pack_bf16x2(fmaf(f.y, bf16_lo_to_f32(wv.y), v[4 * q + 2]) * f.x,
+                                       fmaf(f.y, bf16_hi_to_f32(wv.y), v[4 * q + 3]) * f.x)};
+          }
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const u32x4_t o = join_halves(u32x2_t{pack_bf16x2(v[8 * q] * f, v[8 * q + 1] * f),
-                                                  pack_bf16x2(v[8 * q + 2] * f, v[8 * q + 3] * f)},
-                                          u32x2_t{pack_bf16x2(v[8 * q + 4] * f, v[8 * q + 5] * f),
-                                                  pack_bf16x2(v[8 * q + 6] * f, v[8 * q + 7] * f)});
+            const u32x4_t o = join_halves(x[2 * q], x[2 * q + 1]);
             const int64_t mq = m + 16 * q + 8 * (lane >> 5);
             if (in && mq < K) *reinterpret_cast<u32x4_t *>(dX + t * K + mq) = o;
           }
@@ -743,7 +750,7 @@ hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, co
 }
 
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
-                          const bf16_t *W, int64_t V, int64_t K, const float *scale, float *part, bf16_t *dX,
+                          const bf16_t *W, int64_t V, int64_t K, const float2 *scale, float *part, bf16_t *dX,
                           hipStream_t s) {
   const int tr = rows.tile_rows, tc = head_tile_cols(tr);
   const int64_t most = (tb + tr - 1) / tr * ((K + tc - 1) / tc) * kHeadRanges;

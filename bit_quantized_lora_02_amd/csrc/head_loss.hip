@@ -10,7 +10,8 @@
 // E_v = exp2((z_v - u) c) and S = 1 + rest, the gradient by the logits is
 //   G_v = w tau (q_v - P_v) = (w tau / S) (E_v - S P_v),   P_v = sum of the p_i whose target is v,
 // so the product kernels take E with only the targets' entries replaced by E_v - S P_v (at r: (1 - P_r) - P_r rest,
-// again without cancellation), and the row factor w tau / S is applied in binary32 afterwards.
+// again without cancellation), and the row factor w tau / S is applied in binary32 afterwards.  Entries are rounded to
+// bf16 for the matrix unit; at r, whose entry outweighs the others, dX also gets the remainder.
 #include "device.h"
 #include "head.h"
 #include "launch.h"
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
                                                       const float2 *__restrict__ stat, int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
                                                       const int32_t *__restrict__ index, int k, float tau,
                                                       const float *__restrict__ weight, float *__restrict__ loss,
-                                                      float *__restrict__ scale, bf16_t *__restrict__ E, int64_t lde,
+                                                      float2 *__restrict__ scale, bf16_t *__restrict__ E, int64_t lde,
                                                       int64_t te, const bf16_t *__restrict__ X, int64_t K,
                                                       bf16_t *__restrict__ Xs) {
   const int lane = threadIdx.x & 63;
@@ -348,18 +349,25 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
     __threadfence_block();  // the targets' entries below follow these stores
   }
   const float f = (weight ? weight[t] : 1.f) * tau / S;
-  if (lane == 0) scale[i] = f;
+  // The first target's entry is the row's largest as a rule; what its rounding to bf16 leaves goes to dX in binary32.
   const int32_t rc = rows.refcol[t];
+  auto first_target = [&](float g) {
+    const bf16_t r = f32_to_bf16(g);
+    *e(rc) = r;
+    scale[i] = make_float2(f, g - bf16_lo_to_f32(r));
+  };
   if (labels) {
-    if (lane == 0) *e(rc) = f32_to_bf16(-rest);
+    if (lane == 0) first_target(-rest);
   } else {
     for (int i0 = 0; i0 < k; i0 += 64) {
       const int me = i0 + lane;
       const int32_t v = me < k ? index[t * k + me] : -1;
       float P = 0.f;  // all of the row's probability at this column
       for (int j = 0; j < k; ++j) P += index[t * k + j] == v ? rows.pt[t * k + j] : 0.f;
-      if (target_ok(v, V))
-        *e(v) = f32_to_bf16(v == rc ? eref * (1.f - P) - P * rest : exp2f((rows.zt[t * k + me] - u) * c) - P * S);
+      if (v == rc)
+        first_target(eref * (1.f - P) - P * rest);
+      else if (target_ok(v, V))
+        *e(v) = f32_to_bf16(exp2f((rows.zt[t * k + me] - u) * c) - P * S);
     }
   }
   if (Xs)  // rows of X times the row factor: the dW product's second operand, rounded to bf16 for the matrix unit
@@ -371,10 +379,12 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
     }
 }
 
-// dX rows of the block from the ranges' partial sums part[range][row of the block][K], added in range order.
+// dX rows of the block from the ranges' partial sums part[range][row][K], added in range order, and the first target's
+// remainder.
 __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0, int64_t tb,
-                                                     const float *__restrict__ part, int64_t K,
-                                                     const float *__restrict__ scale, bf16_t *__restrict__ dX) {
+                                                     const float *__restrict__ part, const bf16_t *__restrict__ W,
+                                                     int64_t K, const float2 *__restrict__ scale,
+                                                     bf16_t *__restrict__ dX) {
   int64_t n = *rows.n - row0;
   n = n < tb ? n : tb;
   if (n <= 0) return;
@@ -398,11 +408,14 @@ __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0
     s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
     s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
   }
-  const float f = scale[i];
+  const float2 f = scale[i];
+  const int64_t t = rows.list[row0 + i];
+  const u32x4_t wv = *reinterpret_cast<const u32x4_t *>(W + rows.refcol[t] * K + col);
   u32x4_t o;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) o[w] = pack_bf16x2(s[2 * w] * f, s[2 * w + 1] * f);
-  *reinterpret_cast<u32x4_t *>(dX + (int64_t)rows.list[row0 + i] * K + col) = o;
+  for (int w = 0; w < 4; ++w)
+    o[w] = pack_bf16x2(fmaf(f.y, bf16_lo_to_f32(wv[w]), s[2 * w]) * f.x, fmaf(f.y, bf16_hi_to_f32(wv[w]), s[2 * w + 1]) * f.x);
+  *reinterpret_cast<u32x4_t *>(dX + t * K + col) = o;
 }
 
 }  // namespace
@@ -435,7 +448,7 @@ hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, co
 
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
-                               const float *weight, float *loss, float *scale, bf16_t *E, int64_t lde, int64_t te,
+                               const float *weight, float *loss, float2 *scale, bf16_t *E, int64_t lde, int64_t te,
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s) {
   const int64_t grid_rows = Xs ? (tb > 0 ? (tb + 127) / 128 * 128 : 128) : tb;
   launch(k_head_combine, dim3((unsigned)((grid_rows + 3) / 4)), dim3(256), 0, s, rows, row0, tb,
@@ -443,10 +456,10 @@ hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, c
   return hipGetLastError();
 }
 
-hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int64_t K,
-                              const float *scale, bf16_t *dX, hipStream_t s) {
-  launch(k_head_reduce, dim3((unsigned)((tb * (K / 8) + 255) / 256)), dim3(256), 0, s, rows, row0, tb, part, K, scale,
-         dX);
+hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, const bf16_t *W,
+                              int64_t K, const float2 *scale, bf16_t *dX, hipStream_t s) {
+  launch(k_head_reduce, dim3((unsigned)((tb * (K / 8) + 255) / 256)), dim3(256), 0, s, rows, row0, tb, part, W, K,
+         scale, dX);
   return hipGetLastError();
 }
 
