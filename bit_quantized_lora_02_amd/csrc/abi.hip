@@ -466,7 +466,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
     p.off_target = take(row_tiles * tr * (size_t)k * 4);
   }
   p.off_stat = take((size_t)p.b.tb * p.ntile * sizeof(float2));
-  p.off_scale = take((size_t)p.b.tb * sizeof(float2));
+  p.off_scale = take((size_t)p.b.tb * sizeof(float4));
   if (grad) p.off_e = take((size_t)p.b.te * p.b.lde * 2);
   if (dx) {
     const size_t part = head_part_floats(p.b.tb, K, p.b.tile_rows) * 4;
@@ -528,7 +528,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   rows.target = k > 0 ? (uint32_t *)(w + p.off_target) : nullptr;
   const bool grad = dX || dW;
   float2 *stat = (float2 *)(w + p.off_stat);
-  float2 *scale = (float2 *)(w + p.off_scale);
+  float4 *scale = (float4 *)(w + p.off_scale);
   bf16_t *E = grad ? (bf16_t *)(w + p.off_e) : nullptr;
   float *part = p.split ? (float *)(w + p.off_part) : nullptr;
   bf16_t *Xs = dW ? (bf16_t *)(w + p.off_xs) : nullptr;
@@ -554,6 +554,10 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
     if (tb > 0 && dX) {
       LAUNCH("head_dx", launch_head_dx(rows, row0, tb, E, lde, te, W, V, K, scale, part, dX, s));
       if (part) LAUNCH("head_dx_reduce", launch_head_reduce(rows, row0, tb, part, W, K, scale, dX, s));
+    }
+    if (dW && tb > 0) {
+      LAUNCH("head_scale", launch_head_scale(rows, row0, tb, scale, E, lde, te, s));
+      if (k > 0) LAUNCH("head_put", launch_head_put(rows, row0, tb, V, index, k, scale, E, te, s));
     }
     if (dW)
       LAUNCH("head_dw",

@@ -22,7 +22,7 @@ struct HeadRows {
   float *ref;           // [T] by row of X: the logit of the row's first target
   int32_t *refcol;      // [T] by row of X: that target's column
   // several targets (NULL for one):
-  float *zt;             // [T][k] their logits, from the product's tiles
+  float *zt;             // [T][k] their logits, from the product's tiles; then their entries of E before rounding
   float *pt;             // [T][k] their probabilities
   int32_t *bucket;       // [row tiles][ntile + 1] where each output tile's targets start in `target`
   uint32_t *target;      // [row tiles][rows of a tile * k]: target | column in the tile << 8 | row in the tile << 16
@@ -65,14 +65,18 @@ inline bool head_one_tile(int64_t T, const HeadRows &rows) { return T <= rows.ti
 hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
                               int64_t ntile, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
                               const HeadBlocks &blocks, hipStream_t s);
-// Losses, the targets' entries of E, and per row of the block the factor of dX and the remainder of the first target's
-// entry (scale), rows of X times the factor (Xs, for dW).
+// Losses, the targets' entries of E, and per row of the block (scale) the factor, what the first target's entry lost in
+// rounding, the factor's fraction and that target's column; rows of X times the factor's power of two (Xs, for dW).
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
-                               const float *weight, float *loss, float2 *scale, bf16_t *E, int64_t lde, int64_t te,
+                               const float *weight, float *loss, float4 *scale, bf16_t *E, int64_t lde, int64_t te,
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s);
+hipError_t launch_head_scale(const HeadRows &rows, int64_t row0, int64_t tb, const float4 *scale, bf16_t *E, int64_t lde,
+                             int64_t te, hipStream_t s);
+hipError_t launch_head_put(const HeadRows &rows, int64_t row0, int64_t tb, int64_t V, const int32_t *index, int k,
+                           const float4 *scale, bf16_t *E, int64_t te, hipStream_t s);
 hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, const bf16_t *W,
-                              int64_t K, const float2 *scale, bf16_t *dX, hipStream_t s);
+                              int64_t K, const float4 *scale, bf16_t *dX, hipStream_t s);
 
 // Rows that go to tiles of `tile_rows`: all, but for 128 or fewer behind the last whole 256-row tile, which take
 // 128-row tiles (measured: a 256 x 128 tile costs 0.6 of a 256 x 256 one).
@@ -104,7 +108,7 @@ inline size_t head_part_floats(int64_t tb, int64_t K, int tile_rows) {
 hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
                               bf16_t *E, int64_t lde, int64_t te, int k, hipStream_t s);
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
-                          const bf16_t *W, int64_t V, int64_t K, const float2 *scale, float *part, bf16_t *dX,
+                          const bf16_t *W, int64_t V, int64_t K, const float4 *scale, float *part, bf16_t *dX,
                           hipStream_t s);
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,

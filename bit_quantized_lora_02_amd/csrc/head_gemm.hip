@@ -2,7 +2,7 @@
 //
 //   logits   z = X W^T       per tile: softmax statistics, and E = exp2((z - u) c) in bf16 (never z itself)
 //   dX       dX = f o (E W)  reduction over the vocabulary, f the rows' factors
-//   dW       dW = E^T (f o X)  reduction over the rows
+//   dW       dW = (f o E)^T X  reduction over the rows, f split between E and X
 //
 // (E with its targets' entries put in by k_head_combine; see head_loss.hip for the mathematics.)
 //
@@ -551,7 +551,7 @@ struct DxArgs {
   int64_t lde, te;
   const bf16_t *W;
   int64_t V, K;
-  const float2 *scale;
+  const float4 *scale;
   float *part;
   bf16_t *dX;
 };
@@ -562,7 +562,7 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
                                          Turn turn, const Ring &ring) {
   const HeadRows &rows = g.rows;
   const int64_t row0 = g.row0, K = g.K;
-  const float2 *const scale = g.scale;
+  const float4 *const scale = g.scale;
   bf16_t *const dX = g.dX;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
@@ -581,7 +581,7 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
     for (int j = 0; j < C::WN; ++j) {
       const int i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
       const bool in = i < n;
-      const float2 f = scale[in ? i : n - 1];
+      const float4 f = scale[in ? i : n - 1];
       const int64_t t = rows.list[row0 + (in ? i : n - 1)];
       const bf16_t *const w = g.W + rows.refcol[t] * K + 4 * (lane >> 5);
 #pragma unroll
@@ -750,7 +750,7 @@ hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, co
 }
 
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
-                          const bf16_t *W, int64_t V, int64_t K, const float2 *scale, float *part, bf16_t *dX,
+                          const bf16_t *W, int64_t V, int64_t K, const float4 *scale, float *part, bf16_t *dX,
                           hipStream_t s) {
   const int tr = rows.tile_rows, tc = head_tile_cols(tr);
   const int64_t most = (tb + tr - 1) / tr * ((K + tc - 1) / tc) * kHeadRanges;

@@ -289,7 +289,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
                                                       const float2 *__restrict__ stat, int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
                                                       const int32_t *__restrict__ index, int k, float tau,
                                                       const float *__restrict__ weight, float *__restrict__ loss,
-                                                      float2 *__restrict__ scale, bf16_t *__restrict__ E, int64_t lde,
+                                                      float4 *__restrict__ scale, bf16_t *__restrict__ E, int64_t lde,
                                                       int64_t te, const bf16_t *__restrict__ X, int64_t K,
                                                       bf16_t *__restrict__ Xs) {
   const int lane = threadIdx.x & 63;
@@ -351,10 +351,12 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   const float f = (weight ? weight[t] : 1.f) * tau / S;
   // The first target's entry is the row's largest as a rule; what its rounding to bf16 leaves goes to dX in binary32.
   const int32_t rc = rows.refcol[t];
+  int ex;
+  const float fm = frexpf(f, &ex);
   auto first_target = [&](float g) {
     const bf16_t r = f32_to_bf16(g);
     *e(rc) = r;
-    scale[i] = make_float2(f, g - bf16_lo_to_f32(r));
+    scale[i] = make_float4(f, g - bf16_lo_to_f32(r), fm, __int_as_float(rc));
   };
   if (labels) {
     if (lane == 0) first_target(-rest);
@@ -364,26 +366,72 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
       const int32_t v = me < k ? index[t * k + me] : -1;
       float P = 0.f;  // all of the row's probability at this column
       for (int j = 0; j < k; ++j) P += index[t * k + j] == v ? rows.pt[t * k + j] : 0.f;
+      if (!target_ok(v, V)) continue;
+      const float g = v == rc ? eref * (1.f - P) - P * rest : exp2f((rows.zt[t * k + me] - u) * c) - P * S;
       if (v == rc)
-        first_target(eref * (1.f - P) - P * rest);
-      else if (target_ok(v, V))
-        *e(v) = f32_to_bf16(exp2f((rows.zt[t * k + me] - u) * c) - P * S);
+        first_target(g);
+      else
+        *e(v) = f32_to_bf16(g);
+      rows.zt[t * k + me] = g;  // for k_head_put
     }
   }
-  if (Xs)  // rows of X times the row factor: the dW product's second operand, rounded to bf16 for the matrix unit
+  if (Xs)  // rows of X times the row factor's power of two, exactly (k_head_scale gives E the rest of the factor)
     for (int64_t at = 8 * lane; at < K; at += 512) {
       u32x4_t v = *reinterpret_cast<const u32x4_t *>(X + t * K + at);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) v[w] = pack_bf16x2(bf16_lo_to_f32(v[w]) * f, bf16_hi_to_f32(v[w]) * f);
+      for (int w = 0; w < 4; ++w) v[w] = pack_bf16x2(ldexpf(bf16_lo_to_f32(v[w]), ex), ldexpf(bf16_hi_to_f32(v[w]), ex));
       *reinterpret_cast<u32x4_t *>(Xs + i * K + at) = v;
     }
+}
+
+// E's rows times the fraction (in [1/2, 1)) of their factors, for dW, whose reduction runs over the rows, so that no
+// factor can wait for the product's epilogue.  (Rounding X times the factor instead would round every term of a row of
+// dW twice; here the first target's entry, which outweighs the others, is rounded once, from its value with the
+// remainder, and k_head_put does the same for a teacher's other targets.)  Bound by E's read and write.  A thread takes eight columns of a row in each of kScaleBlocks blocks.
+constexpr int kScaleBlocks = 8;
+__global__ __launch_bounds__(256) void k_head_scale(HeadRows rows, int64_t row0, int64_t tb,
+                                                    const float4 *__restrict__ scale, bf16_t *__restrict__ E,
+                                                    int64_t lde, int64_t te) {
+  int64_t n = *rows.n - row0;
+  n = n < tb ? n : tb;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, i = at >> 2;
+  if (i >= n) return;
+  const float4 f = scale[i];
+  const int rc = __float_as_int(f.w), col = (int)(at & 3) * 8;
+  const int64_t b0 = (int64_t)blockIdx.y * kScaleBlocks, blocks = lde / 32;
+#pragma unroll
+  for (int b = 0; b < kScaleBlocks; ++b) {
+    if (b0 + b >= blocks) break;
+    u32x4_t *const p = reinterpret_cast<u32x4_t *>(E + ((b0 + b) * te + i) * 32 + col);
+    const u32x4_t v = *p;
+    float x[8];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) x[2 * w] = bf16_lo_to_f32(v[w]), x[2 * w + 1] = bf16_hi_to_f32(v[w]);
+    const int mine = rc - (int)(b0 + b) * 32 - col;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) x[w] = (mine == w ? x[w] + f.y : x[w]) * f.z;
+    *p = u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+  }
+}
+
+// The targets' entries once more after k_head_scale, rounded once from what k_head_combine kept of them.
+__global__ __launch_bounds__(256) void k_head_put(HeadRows rows, int64_t row0, int64_t tb, int64_t V,
+                                                  const int32_t *__restrict__ index, int k,
+                                                  const float4 *__restrict__ scale, bf16_t *__restrict__ E, int64_t te) {
+  int64_t n = *rows.n - row0;
+  n = n < tb ? n : tb;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, i = at / k;
+  if (i >= n) return;
+  const int64_t e = (int64_t)rows.list[row0 + i] * k + (at - i * k);
+  const int64_t v = index[e];
+  if (target_ok(v, V)) E[(v / 32 * te + i) * 32 + v % 32] = f32_to_bf16(rows.zt[e] * scale[i].z);
 }
 
 // dX rows of the block from the ranges' partial sums part[range][row][K], added in range order, and the first target's
 // remainder.
 __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0, int64_t tb,
                                                      const float *__restrict__ part, const bf16_t *__restrict__ W,
-                                                     int64_t K, const float2 *__restrict__ scale,
+                                                     int64_t K, const float4 *__restrict__ scale,
                                                      bf16_t *__restrict__ dX) {
   int64_t n = *rows.n - row0;
   n = n < tb ? n : tb;
@@ -408,7 +456,7 @@ __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0
     s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
     s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
   }
-  const float2 f = scale[i];
+  const float4 f = scale[i];
   const int64_t t = rows.list[row0 + i];
   const u32x4_t wv = *reinterpret_cast<const u32x4_t *>(W + rows.refcol[t] * K + col);
   u32x4_t o;
@@ -448,7 +496,7 @@ hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, co
 
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,
                                int64_t V, const int64_t *labels, const int32_t *index, int k, float tau,
-                               const float *weight, float *loss, float2 *scale, bf16_t *E, int64_t lde, int64_t te,
+                               const float *weight, float *loss, float4 *scale, bf16_t *E, int64_t lde, int64_t te,
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s) {
   const int64_t grid_rows = Xs ? (tb > 0 ? (tb + 127) / 128 * 128 : 128) : tb;
   launch(k_head_combine, dim3((unsigned)((grid_rows + 3) / 4)), dim3(256), 0, s, rows, row0, tb,
@@ -457,9 +505,23 @@ hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, c
 }
 
 hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, const bf16_t *W,
-                              int64_t K, const float2 *scale, bf16_t *dX, hipStream_t s) {
+                              int64_t K, const float4 *scale, bf16_t *dX, hipStream_t s) {
   launch(k_head_reduce, dim3((unsigned)((tb * (K / 8) + 255) / 256)), dim3(256), 0, s, rows, row0, tb, part, W, K,
          scale, dX);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_put(const HeadRows &rows, int64_t row0, int64_t tb, int64_t V, const int32_t *index, int k,
+                           const float4 *scale, bf16_t *E, int64_t te, hipStream_t s) {
+  launch(k_head_put, dim3((unsigned)((tb * k + 255) / 256)), dim3(256), 0, s, rows, row0, tb, V, index, k, scale, E, te);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_scale(const HeadRows &rows, int64_t row0, int64_t tb, const float4 *scale, bf16_t *E, int64_t lde,
+                             int64_t te, hipStream_t s) {
+  const int64_t blocks = (lde / 32 + kScaleBlocks - 1) / kScaleBlocks;
+  launch(k_head_scale, dim3((unsigned)((tb * 4 + 255) / 256), (unsigned)blocks), dim3(256), 0, s, rows, row0, tb, scale, E,
+         lde, te);
   return hipGetLastError();
 }
 
