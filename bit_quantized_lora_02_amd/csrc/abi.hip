@@ -436,9 +436,10 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   const bool grad = dx || dw;
   // (a block holds at least 256 rows where there are several, so the tile follows from T)
   p.b.tile_rows = head_tile_rows(T);
-  p.ntile = ceil_div(V, head_tile_cols(p.b.tile_rows));
+  p.ntile = ceil_div(V, kHeadStat);
+  const int64_t tiles = ceil_div(V, head_tile_cols(p.b.tile_rows));
   p.b.lde = ceil_div(V, kHeadPad) * kHeadPad;
-  const size_t row = (size_t)p.ntile * sizeof(float2) + (grad ? (size_t)p.b.lde * 2 : 0);
+  const size_t row = grad ? (size_t)p.b.lde * 2 : (size_t)p.ntile * sizeof(float2);
   int64_t most = (int64_t)(kHeadBlockBytes / row) / 256 * 256;
   most = most < 256 ? 256 : most;
   p.b.count = T <= most ? 1 : ceil_div(T, most);
@@ -462,7 +463,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
     p.off_zt = take((size_t)T * k * 4);
     p.off_pt = take((size_t)T * k * 4);
     const size_t tr = p.b.tile_rows, row_tiles = ((size_t)p.b.tb + tr - 1) / tr;
-    p.off_bucket = take(row_tiles * (size_t)(p.ntile + 1) * 4);
+    p.off_bucket = take(row_tiles * (size_t)(tiles + 1) * 4);
     p.off_target = take(row_tiles * tr * (size_t)k * 4);
   }
   p.off_stat = take((size_t)p.b.tb * p.ntile * sizeof(float2));
@@ -545,7 +546,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
     rows.ranges = ranges + 2 * b;
     if (tb > 0 && k > 0)
-      LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, p.ntile, T, K, n, list, rg, p.b, s));
+      LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, T, K, n, list, rg, p.b, s));
     if (tb > 0)
       LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, k, s));
     if (tb > 0 || dW)

@@ -30,13 +30,16 @@ struct HeadRows {
 
 // Rows of E are padded with zero columns to a multiple of this.
 constexpr int kHeadPad = 128;
-// A logit may exceed the row's reference by 2^kHeadRange before the tile takes a unit of its own.
-constexpr float kHeadRange = 40.f;
+// Where a wave's columns of E sum to this or more, they take a unit of their own instead of the row's reference.
+constexpr float kHeadRange = 1.0995116e12f;  // 2^40
+// Columns per entry of the softmax statistics: a wave's share of a tile, 64, or 128 in the 256 x 256 tile.
+constexpr int kHeadStat = 64;
+__host__ __device__ inline int head_stat_cols(bool wide_tile) { return wide_tile ? 128 : kHeadStat; }
 
 // Rows of X per tile of the three products, by the rows of a block (one choice for all blocks of a call).
 // Few rows take narrow tiles: the padding rows' MFMA work would cost more than the wider tile's operand reuse gains.
 inline int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
-// Columns of a tile (of the vocabulary in the logit product, of X in the dX product); the row statistics are per tile.
+// Columns of a tile (of the vocabulary in the logit product, of X in the dX product).
 // Up to 64 rows the products are bound by the stream of W, and the smaller tile gives every CU some of it.
 __host__ __device__ inline int head_tile_cols(int tile_rows) { return tile_rows == 64 ? 128 : 256; }
 
@@ -63,7 +66,7 @@ hipError_t launch_head_list(const HeadRows &rows, int64_t T, int64_t K, int32_t 
 inline bool head_one_tile(int64_t T, const HeadRows &rows) { return T <= rows.tile_rows; }
 // Sorts the targets of a block's counted rows by the output tile of the logit product they fall into.
 hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
-                              int64_t ntile, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
+                              int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
                               const HeadBlocks &blocks, hipStream_t s);
 // Losses, the targets' entries of E, and per row of the block (scale) the factor, what the first target's entry lost in
 // rounding, the factor's fraction and that target's column; rows of X times the factor's power of two (Xs, for dW).

@@ -34,29 +34,43 @@ struct HeadCfg {
   static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WM = WM_, WN = WN_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
   static constexpr int BM = WAVES_M * WM * 32, BN = WAVES_N * WN * 32;
+  // 16-byte copies per thread of a step's tile of the n-side: the last ones of an item's last four steps, which its
+  // epilogue need not wait for (the next item asks for them in its third step)
+  static constexpr int LB = BN * BK / 8 / NT;
 };
 using H256 = HeadCfg<2, 4, 4, 2>;  // 128 x 64 per wave
 using H128 = HeadCfg<4, 2, 2, 2>;  // 64 x 64 per wave
-using H64 = HeadCfg<4, 1, 1, 2>;   // 128 x 64, 32 x 64 per wave, three workgroups per CU
+using H64 = HeadCfg<2, 2, 2, 1>;   // 128 x 64, 64 x 32 per wave, three workgroups per CU
 
 __device__ __forceinline__ void fence_sched() { __builtin_amdgcn_sched_barrier(0); }
 
-// The LDS tiles of one workgroup: slot i holds the m-side's tile and behind it the n-side's.  Each slot is an array
-// of its own, so that the compiler can tell reads of one from the direct copies into another and adds no waits.
+// The LDS tiles of one workgroup, by slot.  Each slot is an array of its own, so that the compiler can tell reads of
+// one from the direct copies into another and adds no waits.  `a` and `b` are the m-side's and the n-side's tiles: the
+// two halves of a slot's array (QLORA_RING), or, where the m-side's tiles are copied two steps at a time, arrays of
+// their own of which slots 0 and 1, and 2 and 3, share one (QLORA_RING_PAIRS).
 typedef __attribute__((address_space(3))) char lds_char;
 struct Ring {
-  lds_char *slot[STAGES];
+  lds_char *a[STAGES], *b[STAGES];
 };
 #define QLORA_RING(C, ring)                                                                                     \
   __shared__ __attribute__((aligned(1024))) char ring0[(C::BM + C::BN) * BK * 2], ring1[(C::BM + C::BN) * BK * 2],    \
       ring2[(C::BM + C::BN) * BK * 2], ring3[(C::BM + C::BN) * BK * 2];                                               \
-  const Ring ring = {{(lds_char *)ring0, (lds_char *)ring1, (lds_char *)ring2, (lds_char *)ring3}}
+  const Ring ring = {{(lds_char *)ring0, (lds_char *)ring1, (lds_char *)ring2, (lds_char *)ring3},              \
+                     {(lds_char *)ring0 + C::BM * BK * 2, (lds_char *)ring1 + C::BM * BK * 2,                   \
+                      (lds_char *)ring2 + C::BM * BK * 2, (lds_char *)ring3 + C::BM * BK * 2}}
+#define QLORA_RING_PAIRS(C, ring)                                                                               \
+  __shared__ __attribute__((aligned(1024))) char pair0[C::BM * BK * 4], pair1[C::BM * BK * 4], ring0[C::BN * BK * 2],  \
+      ring1[C::BN * BK * 2], ring2[C::BN * BK * 2], ring3[C::BN * BK * 2];                                      \
+  const Ring ring = {{(lds_char *)pair0, (lds_char *)pair0, (lds_char *)pair1, (lds_char *)pair1},              \
+                     {(lds_char *)ring0, (lds_char *)ring1, (lds_char *)ring2, (lds_char *)ring3}}
 
-// Lane offsets into the slots.  An LDS instruction adds at most 65535 to its address register, so a lane keeps its
-// offset twice, plain for slots 0 and 1 and plus `kFar` for slots 2 and 3, whose constant then is slot - kFar: all the
+// Lane offsets into the slots.  An LDS instruction adds at most 65535 to its address register, so where the arrays
+// reach further a lane keeps its offset twice, plain and plus `kFar`, the constant then being array - kFar: all the
 // reads of a tile share these registers.  The values are hidden from the compiler, which would otherwise keep a
-// register for every sum.
+// register for every sum.  (Which of the two is taken follows where the arrays come to lie: slots 0 and 1 of QLORA_RING
+// and the pairs below 64 KB, the rest above.  A wrong guess would cost an addition, nothing else.)
 constexpr int kFar = 65536;
+enum { BY_SLOT, NEAR, FAR };
 struct Lane {
   int near, far;
   __device__ __forceinline__ void set(int v) {
@@ -65,17 +79,20 @@ struct Lane {
     asm("" : "+v"(far));
   }
 };
-__device__ __forceinline__ lds_char *in_slot(const Ring &ring, int slot, const Lane &l, int more) {
-  return slot < 2 ? ring.slot[slot] + l.near + more : ring.slot[slot] + l.far + (more - kFar);
+template <int REACH>
+__device__ __forceinline__ lds_char *in_slot(lds_char *base, int slot, const Lane &l, int more) {
+  return REACH == NEAR || (REACH == BY_SLOT && slot < 2) ? base + l.near + more : base + l.far + (more - kFar);
 }
 
 // How an operand lies in memory (element (i, r): row or column i of the tile's side, reduction index r):
-//  LINES:   row-major [i][r].
-//  BLOCKS:  32 reduction indices at a time, [r / 32][i][32]: a step's tile is one contiguous piece, where LINES
-//           would fetch half of every 128-byte line it touches in one step and the other half in the next.
+//  LINES:   row-major [i][r]; copied 64 reduction indices (whole 128-byte lines) and two steps at a time: in halves
+//           every line is fetched twice, which costs the 256 x 256 tile 4% (1355 against 1308 TFLOP/s).
+//  HALF_LINES: the same, a step at a time: more of W's stream in flight, which is what few rows need (17 rows x 32000
+//           x 2048: 24.6 us against 29.1).
+//  BLOCKS:  32 reduction indices at a time, [r / 32][i][32]: a step's tile is one contiguous piece.
 //  ACROSS:  row-major [r][i].
 //  BLOCKS_ACROSS: [i / 32][r][32], what BLOCKS is seen from its other side.
-enum { LINES, BLOCKS, ACROSS, BLOCKS_ACROSS };
+enum { LINES, HALF_LINES, BLOCKS, ACROSS, BLOCKS_ACROSS };
 
 // One operand's tile of ROWS rows (columns for the ACROSS ones).  `ld` is the row length of a row-major matrix, the
 // number of rows in a block otherwise.  BLOCKS rows are gathered through `list` if there is one; rows past the last
@@ -85,11 +102,12 @@ enum { LINES, BLOCKS, ACROSS, BLOCKS_ACROSS };
 template <int ROWS, int NT, int KIND>
 struct Tile {
   static constexpr bool TR = KIND == ACROSS || KIND == BLOCKS_ACROSS;
-  static constexpr int LD = ROWS * BK / 8 / NT;  // 16-byte copies per thread and step
+  static constexpr bool PAIR = KIND == LINES;
+  static constexpr int LD = ROWS * (PAIR ? 2 : 1) * BK / 8 / NT;  // 16-byte copies per thread and step (pair of steps)
   static constexpr int NW = NT / 64;
   static constexpr int CH = ROWS / 8;  // across: 16-byte chunks per LDS row, and LDS rows from copy to copy
   static constexpr int RSTEP = NW * 64 / CH;
-  static_assert(ROWS * BK / 8 % NT == 0 && LD >= 1, "unsupported tile");
+  static_assert(ROWS * (PAIR ? 2 : 1) * BK / 8 % NT == 0 && LD >= 1, "unsupported tile");
   static_assert(!TR || (64 % CH == 0 && RSTEP % 4 == 0), "the copies of a thread share one swizzle");
   const char *base;
   uint32_t off[TR ? 1 : LD];  // across: of the column
@@ -104,12 +122,13 @@ struct Tile {
                                        const int32_t *list, int wave, int lane) {
     ld = (uint32_t)ld_, red = (int)red_;
     if constexpr (!TR) {
-      k0 = 8 * ((lane & 3) ^ ((lane >> 4) & 3));  // the rows of a thread's copies are equal modulo 16
+      // the rows of a thread's copies are equal modulo 16
+      k0 = PAIR ? 8 * ((lane & 7) ^ (((8 * wave + (lane >> 3)) >> 1) & 7)) : 8 * ((lane & 3) ^ ((lane >> 4) & 3));
       const int64_t row = KIND == BLOCKS ? BK : ld;
       base = (const char *)(list ? src : src + first * row);
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int rr = 16 * (i * NW + wave) + (lane >> 2);
+        const int rr = PAIR ? 8 * (i * NW + wave) + (lane >> 3) : 16 * (i * NW + wave) + (lane >> 2);
         const int64_t at = first + rr < count ? rr : count - 1 - first;
         off[i] = (uint32_t)((list ? list[first + at] : at) * row * 2 + (KIND == BLOCKS ? k0 * 2 : 0));
       }
@@ -126,14 +145,14 @@ struct Tile {
       }
     }
   }
-  // Copy i of this thread of the tile of step `s`.  (Buffer loads take the uniform part of the address in scalar
+  // Copy i of this thread of the tile of step (or pair of steps) `s`.  (Buffer loads take the uniform part of the address in scalar
   // registers; the descriptor spans all of memory behind the base, every address is inside the operand by
   // construction.)
   __device__ __forceinline__ void copy(int s, int i, lds_char *to, int wave) const {
     const char *b = base;
     uint32_t o;
-    if constexpr (KIND == LINES) {
-      o = off[i] + 2 * min(k0 + s * BK, (uint32_t)red - 8);
+    if constexpr (KIND == LINES || KIND == HALF_LINES) {
+      o = off[i] + 2 * min(k0 + s * (PAIR ? 2 * BK : BK), (uint32_t)red - 8);
     } else if constexpr (KIND == BLOCKS) {
       b += (int64_t)s * ld * (2 * BK);
       o = off[i];
@@ -150,22 +169,23 @@ struct Tile {
   }
 };
 
-// Reads of the MFMA operands of one side: N tiles of 32 rows (columns) from `first` of a ROWS-wide tile that starts
-// `base` bytes into its slot.
-template <int ROWS, int N, bool TR>
+// Reads of the MFMA operands of one side: N tiles of 32 rows (columns) from `first` of a ROWS-wide tile.
+template <int ROWS, int N, int KIND, int REACH>
 struct Operand {
-  // rows: [row][32], the 16-byte chunk swizzled; the two halves of a step differ in one bit of the chunk.
+  // rows: [row][32] or, in pairs of steps, [row][64], the 16-byte chunk swizzled (by row / 4 % 4, row / 2 % 8); the
+  // quarters differ in a bit or two of the chunk.
   // across: [32][ROWS]: in each 16-lane group, lane i of a transposing read gets element (i & 3) of the 8 bytes
   // addressed by lane 4 m + (i >> 2), so lane a points at row base + (a >> 2), columns 4 (a & 3) .. + 3, and the reads
   // of rows + 0..3 and + 4..7 give its 8 reduction values; the 64-byte group of tile i is swizzled, so each needs its
-  // own offset (i of the first two bits; first is a multiple of 32 N).
-  static constexpr int NO = TR ? N : 2;
+  // own offset.
+  static constexpr bool TR = KIND == ACROSS || KIND == BLOCKS_ACROSS, PAIR = KIND == LINES;
+  static constexpr int NO = TR ? N : PAIR ? 4 : 2;
   Lane at[NO];
   __device__ __forceinline__ void init(int base, int first, int lane) {
     if constexpr (!TR) {
-      const int r = lane & 31, chunk = (lane >> 5) ^ ((r >> 2) & 3);
-      at[0].set(base + (first + r) * 64 + chunk * 16);
-      at[1].set(base + (first + r) * 64 + (chunk ^ 2) * 16);
+      const int r = lane & 31, chunk = (lane >> 5) ^ (PAIR ? (r >> 1) & 7 : (r >> 2) & 3);
+#pragma unroll
+      for (int q = 0; q < NO; ++q) at[q].set(base + (first + r) * (PAIR ? 128 : 64) + (chunk ^ (2 * q)) * 16);
     } else {
       const int grp = lane >> 4, ai = lane & 15;
       const int r = 8 * (grp >> 1) + (ai >> 2);
@@ -175,16 +195,19 @@ struct Operand {
         at[i].set(base + (r * ROWS + ((first + 32 * i) ^ (swz << 5)) + 16 * (grp & 1) + 4 * (ai & 3)) * 2);
     }
   }
-  // tile i, reduction indices 16 kk .. 16 kk + 15 of the step
-  __device__ __forceinline__ u32x4_t read(const Ring &ring, int slot, int kk, int i) const {
+  // tile i, reduction indices 16 kk .. 16 kk + 15 of the step in `slot`
+  __device__ __forceinline__ u32x4_t read(lds_char *const (&side)[STAGES], int slot, int kk, int i) const {
     if constexpr (!TR) {
-      return *(const __attribute__((address_space(3))) u32x4_t *)in_slot(ring, slot, at[kk], i * 32 * 64);
+      const int q = PAIR ? 2 * (slot & 1) + kk : kk;
+      return *(const __attribute__((address_space(3))) u32x4_t *)in_slot<REACH>(side[slot], slot, at[q],
+                                                                               i * 32 * (PAIR ? 128 : 64));
     } else {
       typedef short s4_t __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s4_t lds_s4;
-      const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)in_slot(ring, slot, at[i], kk * 32 * ROWS));
-      const s4_t hi =
-          __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)in_slot(ring, slot, at[i], kk * 32 * ROWS + 8 * ROWS));
+      const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s4 *)in_slot<REACH>(side[slot], slot, at[i], kk * 32 * ROWS));
+      const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s4 *)in_slot<REACH>(side[slot], slot, at[i], kk * 32 * ROWS + 8 * ROWS));
       const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
       return u32x4_t{l2.x, l2.y, h2.x, h2.y};
     }
@@ -204,9 +227,12 @@ __device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
 }
 
-// This wave's copies have landed (before the epilogue's stores are issued, so that only the copies are waited for).
+// All but this wave's last VM copies have landed (called before an epilogue's stores are issued, so that only copies
+// are waited for).
+template <int VM = 0>
 __device__ __forceinline__ void arrive() {
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0
+  static_assert(VM < 16, "the low four bits");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | VM);
   asm volatile("" ::: "memory");
 }
 
@@ -251,42 +277,53 @@ __device__ __forceinline__ void between_passes() {
 // Step s multiplies the tiles of slot s % 4 while the copies of steps s + 1 .. s + 3 are in flight.  Its first MFMAs'
 // operands are in registers; the second half's are read under them; then the waves meet (every wave holds the last
 // operands of slot s, and step s + 1 has landed), read the first operands of step s + 1 and run the second half's
-// MFMAs.  The copies of step s + 3 (into the slot of step s - 1, which all waves have left) are issued one at a time
-// between the MFMAs: issued together they would hold the waves up for as long as the load unit takes to accept them.
-// The last three steps of an item copy the first three of the next one, so the ring never drains and an item's
-// epilogue hides the first latency of the next.
+// MFMAs.  The copies of step s + 4 into the slot just left are issued one at a time between those: issued together they
+// would hold the waves up for as long as the load unit takes to accept them.  (Timed without them, without the LDS reads
+// and without the MFMAs, the copies alone take 0.7 of the whole time and the MFMAs 0.6, so each copy gets as much time
+// as the ring allows: more than two steps.)  The last four steps of an item copy the first four of the next one, so the
+// ring never drains and an item's epilogue hides the first latency of the next.
 //
-//  setup(ta, tb, s0, s1): the tiles and steps of the item just taken     begin(): notes for its epilogue
-//  finish(acc): its epilogue; calls arrive() before its first store
-template <class C, int KA, int KB, class Setup, class Begin, class Finish>
+//  setup(ta, tb, s0, s1): the tiles and steps of the item just taken
+//  begin(): notes for its epilogue    late(): before its last four steps (loads that the epilogue needs at once)
+//  finish(acc): its epilogue; calls arrive<LB>() before its first store
+template <class C, int KA, int KB, class Setup, class Begin, class Late, class Finish>
 __device__ __forceinline__ void products(Items &items, Turn turn, const Ring &ring, int wave, int lane, Setup setup,
-                                         Begin begin, Finish finish) {
+                                         Begin begin, Late late, Finish finish) {
   typedef Tile<C::BM, C::NT, KA> TileA;
   typedef Tile<C::BN, C::NT, KB> TileB;
-  constexpr int L = TileA::LD + TileB::LD, L1 = L / 2;  // copies per thread and step, those before the meeting
-  static_assert(2 * L < 64, "copies in flight are counted in six bits");
+  constexpr bool PAIR = TileA::PAIR;
+  constexpr int LA = TileA::LD, LB = TileB::LD;
+  // copies that may be in flight when the waves meet in an even and in an odd step: those of the steps after the next
+  // (in pairs: of the n-side, and, in an even step, the m-side's next pair)
+  constexpr int EVEN = PAIR ? 2 * LB + LA : 2 * (LA + LB), ODD = PAIR ? 2 * LB : EVEN;
+  static_assert(EVEN < 16, "counted in four bits");
   uint32_t lin = turn.lin;
   if (!items.take(lin)) return;
   TileA ta;
   TileB tb;
   int s0, s1;
   setup(ta, tb, &s0, &s1);
-  Operand<C::BM, C::WM, TileA::TR> oa;
-  Operand<C::BN, C::WN, TileB::TR> ob;
+  Operand<C::BM, C::WM, KA, PAIR ? NEAR : BY_SLOT> oa;
+  Operand<C::BN, C::WN, KB, PAIR ? FAR : BY_SLOT> ob;
   oa.init(0, wave / C::WAVES_N * C::WM * 32, lane);
-  ob.init(C::BM * BK * 2, wave % C::WAVES_N * C::WN * 32, lane);
+  ob.init(0, wave % C::WAVES_N * C::WN * 32, lane);
+  // copies [q0, q1) of those that go with step s into `slot`: of both sides; in pairs, of the m-side with odd steps
+  // only, both steps' together and first
+  auto count = [](int slot) { return PAIR && !(slot & 1) ? LB : LA + LB; };
   auto copies = [&](int s, int slot, int q0, int q1) {
 #pragma unroll
     for (int q = q0; q < q1; ++q) {
-      if (q < TileA::LD)
-        ta.copy(s, q, ring.slot[slot], wave);
+      if (PAIR && !(slot & 1))
+        tb.copy(s, q, ring.b[slot], wave);
+      else if (q < LA)
+        ta.copy(PAIR ? s >> 1 : s, q, ring.a[slot], wave);
       else
-        tb.copy(s, q - TileA::LD, ring.slot[slot] + C::BM * BK * 2, wave);
+        tb.copy(s, q - LA, ring.b[slot], wave);
       fence_sched();
     }
   };
 #pragma unroll
-  for (int q = 0; q < 3; ++q) copies(s0 + q, q, 0, L);
+  for (int q = 0; q < STAGES; ++q) copies(s0 + q, q, 0, count(q));
   arrive();
   for (;;) {
     begin();
@@ -300,51 +337,54 @@ __device__ __forceinline__ void products(Items &items, Turn turn, const Ring &ri
     u32x4_t a[2][C::WM], b[2][C::WN];
     auto read = [&](int slot, int kk) {
 #pragma unroll
-      for (int i = 0; i < C::WM; ++i) a[kk][i] = oa.read(ring, slot, kk, i);
+      for (int i = 0; i < C::WM; ++i) a[kk][i] = oa.read(ring.a, slot, kk, i);
 #pragma unroll
-      for (int j = 0; j < C::WN; ++j) b[kk][j] = ob.read(ring, slot, kk, j);
+      for (int j = 0; j < C::WN; ++j) b[kk][j] = ob.read(ring.b, slot, kk, j);
       fence_sched();
     };
-    // the MFMAs of half kk with copies [q0, q1) of step s spread among them
-    auto mma = [&](int kk, int s, int slot, int q0, int q1) {
+    // the MFMAs of half kk, the copies of step s into `slot` (none: -1) spread among them
+    auto mma = [&](int kk, int s, int slot) {
 #pragma unroll
       for (int i = 0; i < C::WM; ++i) {
 #pragma unroll
         for (int j = 0; j < C::WN; ++j) acc[i][j] = mfma_32x32x16(a[kk][i], b[kk][j], acc[i][j]);
         fence_sched();
-        copies(s, slot, q0 + (q1 - q0) * i / C::WM, q0 + (q1 - q0) * (i + 1) / C::WM);
+        if (slot >= 0) copies(s, slot, count(slot) * i / C::WM, count(slot) * (i + 1) / C::WM);
       }
     };
     // the step in slot P; `s` is the one to copy, `fresh`: the item's first two steps, whose successors are known to
     // have landed (arrive()) while the last epilogue's stores may still be on their way
     auto step = [&](auto pc, int s, bool fresh) {
-      constexpr int P = decltype(pc)::value, NEXT = (P + 1) % STAGES, TO = (P + 3) % STAGES;
+      constexpr int P = decltype(pc)::value, NEXT = (P + 1) % STAGES;
       read(P, 1);
-      mma(0, s, TO, 0, L1);
-      if (!(P < 2 && fresh)) __builtin_amdgcn_s_waitcnt(0x0f70 | (L + L1));  // step s + 2's and the first of s + 3's
+      mma(0, 0, -1);
+      if (!(P < 2 && fresh)) __builtin_amdgcn_s_waitcnt(0x0f70 | (P & 1 ? ODD : EVEN));
       meet();
       read(NEXT, 0);
-      mma(1, s, TO, L1, L);
+      mma(1, s, P);
     };
     meet();
     read(0, 0);
     int s = s0;
     for (; s + 4 < s1; s += 4) {
-      step(std::integral_constant<int, 0>(), s + 3, s == s0);
-      step(std::integral_constant<int, 1>(), s + 4, s == s0);
-      step(std::integral_constant<int, 2>(), s + 5, false);
-      step(std::integral_constant<int, 3>(), s + 6, false);
+      step(std::integral_constant<int, 0>(), s + 4, s == s0);
+      step(std::integral_constant<int, 1>(), s + 5, s == s0);
+      step(std::integral_constant<int, 2>(), s + 6, false);
+      step(std::integral_constant<int, 3>(), s + 7, false);
     }
-    step(std::integral_constant<int, 0>(), s + 3, s == s0);
+    late();
     lin += turn.stride;
-    const bool more = items.take(lin);
-    const bool fresh = s == s0;
+    const bool more = items.take(lin), fresh = s == s0;
     if (more) setup(ta, tb, &s0, &s1);  // (else the first steps of this item are copied once more)
-    step(std::integral_constant<int, 1>(), s0, fresh);
-    step(std::integral_constant<int, 2>(), s0 + 1, false);
-    step(std::integral_constant<int, 3>(), s0 + 2, false);
+    step(std::integral_constant<int, 0>(), s0, fresh);
+    step(std::integral_constant<int, 1>(), s0 + 1, fresh);
+    step(std::integral_constant<int, 2>(), s0 + 2, false);
+    step(std::integral_constant<int, 3>(), s0 + 3, false);
     finish(acc);
-    if (!more) return;
+    if (!more) {
+      arrive();  // nothing is left on its way into LDS
+      return;
+    }
   }
 }
 
@@ -373,26 +413,27 @@ struct LogitArgs {
   int64_t V, K;
   float c;
   float2 *stat;
-  int64_t ntile;
+  int64_t ntile;  // entries per row
+  int tiles;      // of the vocabulary
   bf16_t *E;
   int64_t lde, te;
   int k;
 };
 
-// Rows [first, n) of the block; `s_max` and `s_sum` hold WAVES_M x BN each.
+// Rows [first, n) of the block.
 template <class C>
 __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n, Items &items, Turn turn,
-                                            const Ring &ring, float *s_max_, float *s_sum_) {
+                                            const Ring &ring) {
   const HeadRows &rows = g.rows;
   const int64_t row0 = g.row0, V = g.V, K = g.K, ntile = g.ntile, te = g.te;
   const float c = g.c;
   const int k = g.k;
   bf16_t *const E = g.E;
-  float(*const s_max)[C::BN] = (float(*)[C::BN])s_max_, (*const s_sum)[C::BN] = (float(*)[C::BN])s_sum_;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   int m0 = 0, n0 = 0;
-  auto setup = [&](Tile<C::BM, C::NT, LINES> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
+  constexpr int KW = C::BN == 64 ? HALF_LINES : LINES;
+  auto setup = [&](Tile<C::BM, C::NT, KW> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
     ta.init(g.W, K, (int64_t)items.m * C::BM, V, K, nullptr, wave, lane);
     tbl.init(g.X, g.ldx, first + (int64_t)items.n * C::BN, n, K, rows.list + row0, wave, lane);
     *s0 = 0;
@@ -413,7 +454,7 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
     }
     if (rows.target) {
       const int row_tile = n0 / rows.tile_rows;
-      const int32_t *const b = rows.bucket + (int64_t)row_tile * (ntile + 1) + items.m;
+      const int32_t *const b = rows.bucket + (int64_t)row_tile * (g.tiles + 1) + items.m;
       t0 = b[0], t1 = b[1];
       targets = rows.target + (int64_t)row_tile * rows.tile_rows * k;
       if (t0 + lane < t1) target = targets[t0 + lane];
@@ -444,16 +485,23 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
       }
     }
   };
+  float ref[C::WN];
+  int rcol[C::WN];
+  auto late = [&]() {
+#pragma unroll
+    for (int j = 0; j < C::WN; ++j) {
+      ref[j] = rows.ref[t[j]];
+      rcol[j] = rows.refcol[t[j]];
+    }
+  };
   // element e of acc[i][j]: column m0 + mlane + 32 i + 8 (e / 4) + e % 4 of the lane's row j
   const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
   auto finish = [&](Acc<C> &acc) {
     if (rows.target) pick(acc);
-    float ref[C::WN];
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
-      ref[j] = rows.ref[t[j]];
       // the reference's own column and those past the vocabulary stay out of the sums
-      int rc = rows.refcol[t[j]] - m0 - mlane, end = (int)(V - m0) - mlane;
+      int rc = rcol[j] - m0 - mlane, end = (int)(V - m0) - mlane;
       if (__any((rc >= -4 && rc < C::BM) || m0 + C::BM > V)) {
         asm("" : "+v"(rc), "+v"(end));
 #pragma unroll
@@ -464,81 +512,90 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
             acc[i][j][e] = (m == rc) | (m >= end) ? -INFINITY : acc[i][j][e];
           }
       }
-      float top = acc[0][j][0];
+    }
+#pragma unroll
+    for (int j = 0; j < C::WN; ++j) {
+      // Against the reference (one FMA and one exp2 per logit); where that is out of range, against the largest logit
+      // of the wave's columns.  The statistics are per wave: nothing is exchanged.
+      float u = ref[j], sum = 0.f;
+      const float uc = u * c;
+      u32x2_t x[C::WM][4];
 #pragma unroll
       for (int i = 0; i < C::WM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (lane < 32) s_max[wm][(wn * C::WN + j) * 32 + lane] = top;
-    }
-    arrive();
-    meet();
-    float u[C::WN];
+        for (int q = 0; q < 4; ++q) {
+          float p[4];
 #pragma unroll
-    for (int j = 0; j < C::WN; ++j) {
-      const int nj = (wn * C::WN + j) * 32 + (lane & 31);
-      float top = s_max[0][nj];
-#pragma unroll
-      for (int w = 1; w < C::WAVES_M; ++w) top = fmaxf(top, s_max[w][nj]);
-      u[j] = (top - ref[j]) * c > kHeadRange ? top : ref[j];
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < C::WM; ++i) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          acc[i][j][e] = __builtin_amdgcn_exp2f((acc[i][j][e] - u[j]) * c);
-          sum += acc[i][j][e];
+          for (int e = 0; e < 4; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][4 * q + e], c, -uc));
+            sum += p[e];
+          }
+          x[i][q] = u32x2_t{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
         }
-      }
       sum += __shfl_xor(sum, 32);
-      if (lane < 32) s_sum[wm][nj] = sum;
+      const bool over = !(sum < kHeadRange);
+      if (__any(over)) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        u = over ? top : u;
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              p[e] = __builtin_amdgcn_exp2f((acc[i][j][4 * q + e] - u) * c);
+              sum += p[e];
+            }
+            x[i][q] = u32x2_t{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
+          }
+        sum += __shfl_xor(sum, 32);
+      }
+      if (j == 0) arrive<C::LB>();
+      const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
+      if (row < n && lane < 32 && m0 + wm * C::WM * 32 < V) g.stat[(int64_t)row * ntile + m0 / (C::WM * 32) + wm] = make_float2(u, sum);
       if (!E) continue;
       // E lies in blocks of 32 columns, [column / 32][row][32]: a wave's store is 32 rows of 32 bytes
-      const int row = n0 + nj;
 #pragma unroll
       for (int i = 0; i < C::WM; ++i) {
         bf16_t *const out = E + ((m0 / 32 + wm * C::WM + i) * te + row) * 32 + 8 * (lane >> 5);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const f32x16_t &v = acc[i][j];
-          const u32x4_t o = join_halves(
-              u32x2_t{pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3])},
-              u32x2_t{pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7])});
+          const u32x4_t o = join_halves(x[i][2 * q], x[i][2 * q + 1]);
           if (row < n && m0 + (wm * C::WM + i) * 32 < g.lde) *reinterpret_cast<u32x4_t *>(out + 16 * q) = o;
         }
       }
     }
-    meet();
-    if (wm == 0 && lane < 32) {
-#pragma unroll
-      for (int j = 0; j < C::WN; ++j) {
-        const int nj = (wn * C::WN + j) * 32 + lane;
-        float sum = s_sum[0][nj];
-#pragma unroll
-        for (int w = 1; w < C::WAVES_M; ++w) sum += s_sum[w][nj];
-        if (n0 + nj < n) g.stat[(int64_t)(n0 + nj) * ntile + m0 / C::BM] = make_float2(u[j], sum);
-      }
-    }
   };
-  products<C, LINES, BLOCKS>(items, turn, ring, wave, lane, setup, begin, finish);
+  products<C, KW, BLOCKS>(items, turn, ring, wave, lane, setup, begin, late, finish);
 }
 
 template <class C>
 __global__ __launch_bounds__(C::NT) void k_head_logits(LogitArgs g) {
-  QLORA_RING(C, ring);
-  __shared__ float s_max[C::WAVES_M * C::BN], s_sum[C::WAVES_M * C::BN];
   const int n = block_rows(g.rows, g.row0, g.tb);
   if (n == 0) return;
   const int whole = head_whole_rows(n, C::BN);
-  Items items = {(int)g.ntile, (whole + C::BN - 1) / C::BN, 1};
-  if (whole > 0) logit_items<C>(g, 0, whole, items, Turn{blockIdx.x, gridDim.x}, ring, s_max, s_sum);
-  if constexpr (C::BN == 256) {
-    if (whole == n) return;
-    const Turn turn = second_pass(items, (uint32_t)g.ntile);
-    between_passes();
-    items = {(int)g.ntile, 1, 1};
-    logit_items<H128>(g, whole, n, items, turn, ring, s_max, s_sum);
+  Items items = {g.tiles, (whole + C::BN - 1) / C::BN, 1};
+  const Turn all = {blockIdx.x, gridDim.x};
+  if constexpr (C::BN == 64) {
+    QLORA_RING(C, ring);
+    logit_items<C>(g, 0, n, items, all, ring);
+  } else {
+    QLORA_RING_PAIRS(C, ring);
+    if (whole > 0) logit_items<C>(g, 0, whole, items, all, ring);
+    if constexpr (C::BN == 256) {
+      if (whole == n) return;
+      const Turn turn = second_pass(items, (uint32_t)g.tiles);
+      between_passes();
+      items = {g.tiles, 1, 1};
+      logit_items<H128>(g, whole, n, items, turn, ring);
+    }
   }
 }
 
@@ -575,8 +632,9 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
     *s1 = min(*s0 + per * 4, fours * 4);
   };
   auto begin = [&]() { m0 = items.m * C::BM, n0 = first + items.n * C::BN, range = items.range; };
+  auto late = []() {};
   auto finish = [&](Acc<C> &acc) {
-    arrive();
+    arrive<C::LB>();
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
       const int i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
@@ -616,7 +674,7 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
       }
     }
   };
-  products<C, ACROSS, BLOCKS>(items, turn, ring, wave, lane, setup, begin, finish);
+  products<C, ACROSS, BLOCKS>(items, turn, ring, wave, lane, setup, begin, late, finish);
 }
 
 template <class C>
@@ -672,8 +730,9 @@ __device__ __forceinline__ void dw_items(const DwArgs &g, int begin_v, int end_v
     *s1 = deep * 4;
   };
   auto begin = [&]() { m0 = items.m * C::BM, n0 = begin_v + items.n * C::BN; };
+  auto late = []() {};
   auto finish = [&](Acc<C> &acc) {
-    arrive();
+    arrive<C::LB>();
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
       const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 31);
@@ -706,7 +765,7 @@ __device__ __forceinline__ void dw_items(const DwArgs &g, int begin_v, int end_v
       }
     }
   };
-  products<C, ACROSS, BLOCKS_ACROSS>(items, turn, ring, wave, lane, setup, begin, finish);
+  products<C, ACROSS, BLOCKS_ACROSS>(items, turn, ring, wave, lane, setup, begin, late, finish);
 }
 
 __global__ __launch_bounds__(H256::NT) void k_head_dw(DwArgs g) {
@@ -741,9 +800,10 @@ int64_t groups(int64_t items, int tile_rows) {
 hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx,
                               const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E,
                               int64_t lde, int64_t te, int k, hipStream_t s) {
+  const int64_t cols = head_tile_cols(rows.tile_rows), tiles = (V + cols - 1) / cols;
 #define QLORA_CALL(CFG)                                                                                               \
-  launch(k_head_logits<CFG>, dim3((unsigned)groups(ntile * ((tb + CFG::BN - 1) / CFG::BN), CFG::BN)), dim3(CFG::NT), 0, s, \
-         LogitArgs{rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, E, lde, te, k})
+  launch(k_head_logits<CFG>, dim3((unsigned)groups(tiles * ((tb + CFG::BN - 1) / CFG::BN), CFG::BN)), dim3(CFG::NT), 0, s, \
+         LogitArgs{rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, (int)tiles, E, lde, te, k})
   QLORA_HEAD_TILES(rows, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();

@@ -285,7 +285,7 @@ __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, i
 }
 
 // One wave per counted row of the block.
-__global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, int64_t tb, int tile_cols,
+__global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, int64_t tb,
                                                       const float2 *__restrict__ stat, int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
                                                       const int32_t *__restrict__ index, int k, float tau,
                                                       const float *__restrict__ weight, float *__restrict__ loss,
@@ -308,8 +308,11 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   const int64_t t = rows.list[row0 + i];
   const float ref = rows.ref[t], c = 1.44269504f / tau;
   const float2 *st = stat + i * ntile;
+  const int stat_cols = head_stat_cols(rows.tile_rows == 256 && i < head_whole_rows((int)n, 256));
+  const int entries = (int)((V + stat_cols - 1) / stat_cols);
   float u = ref, sum = 0.f;
-  for (int64_t j = lane; j < ntile; j += 64) {
+#pragma unroll 4
+  for (int j = lane; j < entries; j += 64) {
     const float2 v = st[j];
     u = fmaxf(u, v.x);
     sum += v.x == ref ? v.y : 0.f;
@@ -322,7 +325,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
     nlogq = log1pf(rest);
   } else {
     sum = 0.f;
-    for (int64_t j = lane; j < ntile; j += 64) sum += st[j].y * exp2f((st[j].x - u) * c);
+    for (int j = lane; j < entries; j += 64) sum += st[j].y * exp2f((st[j].x - u) * c);
     rest = wave_sum(sum);
     eref = exp2f((ref - u) * c);
     nlogq = logf(rest + eref) + (u - ref) / tau;
@@ -340,7 +343,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   auto e = [&](int64_t v) { return E + (v / 32 * te + i) * 32 + v % 32; };
   if (wide) {  // bring the row's tiles to one unit (a factor below binary32's range is applied in two halves)
     for (int64_t at = 8 * lane; at < lde; at += 512) {
-      const float d = exp2f(0.5f * (st[at / tile_cols].x - u) * c);
+      const float d = exp2f(0.5f * (st[min(at / stat_cols, (int64_t)entries - 1)].x - u) * c);
       u32x4_t v = *reinterpret_cast<u32x4_t *>(e(at));
 #pragma unroll
       for (int w = 0; w < 4; ++w) v[w] = pack_bf16x2(bf16_lo_to_f32(v[w]) * d * d, bf16_hi_to_f32(v[w]) * d * d);
@@ -485,11 +488,12 @@ hipError_t launch_head_list(const HeadRows &rows, int64_t T, int64_t K, int32_t 
 }
 
 hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
-                              int64_t ntile, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
+                              int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
                               const HeadBlocks &blocks, hipStream_t s) {
-  const int tr = rows.tile_rows;
+  const int tr = rows.tile_rows, tc = head_tile_cols(tr);
+  const int64_t ntile = (V + tc - 1) / tc;
   launch(k_head_bucket, dim3((unsigned)((tb + tr - 1) / tr)), dim3(kBucketThreads), (uint32_t)ntile * 4, s, rows, row0,
-         tb, tr, index, k, V, (int)ntile, head_tile_cols(tr), T, K, head_one_tile(T, rows) ? n : (int32_t *)nullptr, list,
+         tb, tr, index, k, V, (int)ntile, tc, T, K, head_one_tile(T, rows) ? n : (int32_t *)nullptr, list,
          ranges, blocks);
   return hipGetLastError();
 }
@@ -500,7 +504,7 @@ hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, c
                                const bf16_t *X, int64_t K, bf16_t *Xs, hipStream_t s) {
   const int64_t grid_rows = Xs ? (tb > 0 ? (tb + 127) / 128 * 128 : 128) : tb;
   launch(k_head_combine, dim3((unsigned)((grid_rows + 3) / 4)), dim3(256), 0, s, rows, row0, tb,
-         head_tile_cols(rows.tile_rows), stat, ntile, V, labels, index, k, tau, weight, loss, scale, E, lde, te, X, K, Xs);
+         stat, ntile, V, labels, index, k, tau, weight, loss, scale, E, lde, te, X, K, Xs);
   return hipGetLastError();
 }
 

@@ -67,9 +67,9 @@ def test_workspace_is_checked_and_bounded(lib):
     assert lib.qlora_head_workspace_bytes(8, 100, 64, 257, 1, 0, ctypes.byref(c)) == B.QLORA_EINVAL
     assert lib.qlora_head_workspace_bytes(8, 100, 60, 0, 1, 0, ctypes.byref(c)) == B.QLORA_EINVAL
     assert lib.qlora_head_workspace_bytes(8, 100, 64, 0, 1, 0, None) == B.QLORA_EINVAL
-    # scoring keeps only statistics, 8 bytes per row and 256 columns, and a copy of X
+    # scoring keeps only statistics, 8 bytes per row and 64 columns, and a copy of X
     T, V = 8192, 131072
-    assert B.head_workspace_bytes(T, V, 4096, 0, False, False) < T * V / 32 + 2 * T * 4096 + (1 << 20)
+    assert B.head_workspace_bytes(T, V, 4096, 0, False, False) < T * V / 8 + 2 * T * 4096 + (1 << 20)
     # gradients hold a block of at most 1 GiB and the dX product's partial sums, however many rows there are
     for T in (4096, 65536, 1 << 18):
         assert B.head_workspace_bytes(T, V, 4096, 0, True, False) < (3 << 29) + (2 * 4096 + 32) * T
