@@ -427,8 +427,9 @@ struct HeadPlan {
   int64_t ldx = 0;  // rows per block of the laid out X
   size_t off_n = 0, off_ranges = 0, off_xt = 0, off_list = 0, off_ref = 0, off_col = 0, off_zt = 0, off_pt = 0, off_bucket = 0,
          off_target = 0,
-         off_stat = 0, off_scale = 0, off_e = 0, off_part = 0, off_xs = 0, off_sums = 0, total = 0;
+         off_stat = 0, off_scale = 0, off_z = 0, off_e = 0, off_part = 0, off_xs = 0, off_sums = 0, total = 0;
   bool split = false;  // dX may come as partial sums
+  int ranges = 1;      // of the logit product's reduction
 };
 
 HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw) {
@@ -468,6 +469,8 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   }
   p.off_stat = take((size_t)p.b.tb * p.ntile * sizeof(float2));
   p.off_scale = take((size_t)p.b.tb * sizeof(float4));
+  p.ranges = p.b.count == 1 && T > 0 ? head_logit_ranges(T, V, K, p.b.tile_rows) : 1;
+  if (p.ranges > 1) p.off_z = take((size_t)p.ranges * T * p.b.lde * 4);
   if (grad) p.off_e = take((size_t)p.b.te * p.b.lde * 2);
   if (dx) {
     const size_t part = head_part_floats(p.b.tb, K, p.b.tile_rows) * 4;
@@ -526,7 +529,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   rows.zt = k > 0 ? (float *)(w + p.off_zt) : nullptr;
   rows.pt = k > 0 ? (float *)(w + p.off_pt) : nullptr;
   rows.bucket = k > 0 ? (int32_t *)(w + p.off_bucket) : nullptr;
-  rows.target = k > 0 ? (uint32_t *)(w + p.off_target) : nullptr;
+  rows.target = k > 0 && p.ranges == 1 ? (uint32_t *)(w + p.off_target) : nullptr;
   const bool grad = dX || dW;
   float2 *stat = (float2 *)(w + p.off_stat);
   float4 *scale = (float4 *)(w + p.off_scale);
@@ -541,14 +544,19 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   const int64_t lde = p.b.lde, te = p.b.te;
   LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, rg, p.b, rows, loss, dX, Xt, p.ldx,
                                        s));
-  if (k > 0 && !(T > 0 && head_one_tile(T, rows))) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, rg, p.b, s));
+  const bool sorted = k > 0 && p.ranges == 1;  // the targets go by the product's tiles
+  float *zpart = p.ranges > 1 ? (float *)(w + p.off_z) : nullptr;
+  if (k > 0 && !(T > 0 && sorted && head_one_tile(T, rows))) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, rg, p.b, s));
   for (int64_t b = 0; b < p.b.count; ++b) {
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
     rows.ranges = ranges + 2 * b;
-    if (tb > 0 && k > 0)
+    if (tb > 0 && sorted)
       LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, T, K, n, list, rg, p.b, s));
     if (tb > 0)
-      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, k, s));
+      LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, k,
+                                               p.ranges, zpart, s));
+    if (tb > 0 && zpart)
+      LAUNCH("head_soft", launch_head_soft(rows, row0, tb, zpart, p.ranges, V, c, stat, p.ntile, index, k, E, lde, te, s));
     if (tb > 0 || dW)
       LAUNCH("head_combine", launch_head_combine(rows, row0, tb, stat, p.ntile, V, labels, index, k, tau, weight, loss,
                                                  scale, E, lde, te, X, K, Xs, s));

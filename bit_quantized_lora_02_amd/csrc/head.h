@@ -47,6 +47,25 @@ __host__ __device__ inline int head_tile_cols(int tile_rows) { return tile_rows 
 // narrow tile that run at once (three per CU).
 constexpr int kHeadRanges = 32, kHeadSlots64 = 768;
 
+// Ranges of the logit product's reduction over K for T rows: more than one where the output has too few tiles to
+// occupy the chip (a small vocabulary, few rows).  In microseconds: a 32-deep step takes 0.8 in a 256-wide tile and 0.25
+// in a 128-wide one however few there are; splitting costs a launch, about 5, and the binary32 sums, written and read
+// once at about 4.5 TB/s.
+inline int head_logit_ranges(int64_t T, int64_t V, int64_t K, int tile_rows) {
+  const int64_t cols = head_tile_cols(tile_rows), tiles = (V + cols - 1) / cols * ((T + tile_rows - 1) / tile_rows);
+  const int64_t slots = tile_rows == 64 ? kHeadSlots64 : 256, fours = (K + 127) / 128;
+  if (tiles * 2 > slots) return 1;
+  const float step = tile_rows == 64 ? 0.25f : 0.8f, sums = (float)(T * V) * 8.f / 4.5e6f;
+  int best = 1;
+  float least = 4.f * (float)fours * step;
+  for (int s = 2; s <= 16 && s <= fours && tiles * s <= slots; ++s) {
+    const float cost = 4.f * (float)((fours + s - 1) / s) * step + 5.f + sums * (float)s;
+    if (cost < least) least = cost, best = s;
+  }
+  const int64_t per = (fours + best - 1) / best;
+  return (int)((fours + per - 1) / per);
+}
+
 // How the counted rows are taken in blocks.
 struct HeadBlocks {
   int64_t tb, count;  // rows per block (the last: what is left of T), blocks
@@ -109,7 +128,11 @@ inline size_t head_part_floats(int64_t tb, int64_t K, int tile_rows) {
 }
 
 hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
-                              bf16_t *E, int64_t lde, int64_t te, int k, hipStream_t s);
+                              bf16_t *E, int64_t lde, int64_t te, int k, int ranges, float *part, hipStream_t s);
+// Where the logits came as the partial sums of several ranges: their statistics, E, and the targets' logits.
+hipError_t launch_head_soft(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int ranges, int64_t V,
+                            float c, float2 *stat, int64_t ntile, const int32_t *index, int k, bf16_t *E, int64_t lde,
+                            int64_t te, hipStream_t s);
 hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *W, int64_t V, int64_t K, const float4 *scale, float *part, bf16_t *dX,
                           hipStream_t s);

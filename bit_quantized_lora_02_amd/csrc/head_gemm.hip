@@ -415,13 +415,15 @@ struct LogitArgs {
   float2 *stat;
   int64_t ntile;  // entries per row
   int tiles;      // of the vocabulary
+  int ranges;     // of the reduction; with more than one its binary32 sums go to part[range][row][lde]
+  float *part;
   bf16_t *E;
   int64_t lde, te;
   int k;
 };
 
 // Rows [first, n) of the block.
-template <class C>
+template <class C, bool SPLIT>
 __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n, Items &items, Turn turn,
                                             const Ring &ring) {
   const HeadRows &rows = g.rows;
@@ -436,17 +438,18 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
   auto setup = [&](Tile<C::BM, C::NT, KW> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
     ta.init(g.W, K, (int64_t)items.m * C::BM, V, K, nullptr, wave, lane);
     tbl.init(g.X, g.ldx, first + (int64_t)items.n * C::BN, n, K, rows.list + row0, wave, lane);
-    *s0 = 0;
-    *s1 = (int)((K + 127) / 128 * 4);
+    const int fours = (int)((K + 127) / 128), per = SPLIT ? (fours + g.ranges - 1) / g.ranges : fours;
+    *s0 = SPLIT ? items.range * per * 4 : 0;
+    *s1 = SPLIT ? min(*s0 + per * 4, fours * 4) : fours * 4;
   };
   // The epilogue's first loads are issued before the reduction: the lane's rows in X, and the item's targets (one per
   // lane, the first 64 of them).
   int32_t t[C::WN];
-  int t0 = 0, t1 = 0;
+  int t0 = 0, t1 = 0, range = 0;
   uint32_t target = 0;
   const uint32_t *targets = nullptr;
   auto begin = [&]() {
-    m0 = items.m * C::BM, n0 = first + items.n * C::BN;
+    m0 = items.m * C::BM, n0 = first + items.n * C::BN, range = items.range;
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
       const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
@@ -497,6 +500,24 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
   // element e of acc[i][j]: column m0 + mlane + 32 i + 8 (e / 4) + e % 4 of the lane's row j
   const int mlane = wm * C::WM * 32 + 4 * (lane >> 5);
   auto finish = [&](Acc<C> &acc) {
+    if constexpr (SPLIT) {  // k_head_soft does the rest
+      arrive<C::LB>();
+#pragma unroll
+      for (int j = 0; j < C::WN; ++j) {
+        const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
+        float *const out = g.part + ((int64_t)range * n + row) * g.lde + m0 + mlane;
+#pragma unroll
+        for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16_t &v = acc[i][j];
+            if (row < n && m0 + mlane + 32 * i + 8 * q < g.lde)
+              *reinterpret_cast<float4 *>(out + 32 * i + 8 * q) =
+                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
+      }
+      return;
+    }
     if (rows.target) pick(acc);
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
@@ -576,25 +597,25 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
   products<C, KW, BLOCKS>(items, turn, ring, wave, lane, setup, begin, late, finish);
 }
 
-template <class C>
+template <class C, bool SPLIT>
 __global__ __launch_bounds__(C::NT) void k_head_logits(LogitArgs g) {
   const int n = block_rows(g.rows, g.row0, g.tb);
   if (n == 0) return;
-  const int whole = head_whole_rows(n, C::BN);
-  Items items = {g.tiles, (whole + C::BN - 1) / C::BN, 1};
+  const int whole = SPLIT ? n : head_whole_rows(n, C::BN);
+  Items items = {g.tiles, (whole + C::BN - 1) / C::BN, SPLIT ? g.ranges : 1};
   const Turn all = {blockIdx.x, gridDim.x};
   if constexpr (C::BN == 64) {
     QLORA_RING(C, ring);
-    logit_items<C>(g, 0, n, items, all, ring);
+    logit_items<C, SPLIT>(g, 0, n, items, all, ring);
   } else {
     QLORA_RING_PAIRS(C, ring);
-    if (whole > 0) logit_items<C>(g, 0, whole, items, all, ring);
-    if constexpr (C::BN == 256) {
+    if (whole > 0) logit_items<C, SPLIT>(g, 0, whole, items, all, ring);
+    if constexpr (C::BN == 256 && !SPLIT) {
       if (whole == n) return;
       const Turn turn = second_pass(items, (uint32_t)g.tiles);
       between_passes();
       items = {g.tiles, 1, 1};
-      logit_items<H128>(g, whole, n, items, turn, ring);
+      logit_items<H128, false>(g, whole, n, items, turn, ring);
     }
   }
 }
@@ -799,11 +820,12 @@ int64_t groups(int64_t items, int tile_rows) {
 
 hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx,
                               const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E,
-                              int64_t lde, int64_t te, int k, hipStream_t s) {
+                              int64_t lde, int64_t te, int k, int ranges, float *part, hipStream_t s) {
   const int64_t cols = head_tile_cols(rows.tile_rows), tiles = (V + cols - 1) / cols;
 #define QLORA_CALL(CFG)                                                                                               \
-  launch(k_head_logits<CFG>, dim3((unsigned)groups(tiles * ((tb + CFG::BN - 1) / CFG::BN), CFG::BN)), dim3(CFG::NT), 0, s, \
-         LogitArgs{rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, (int)tiles, E, lde, te, k})
+  launch(ranges > 1 ? k_head_logits<CFG, true> : k_head_logits<CFG, false>,                                           \
+         dim3((unsigned)groups(tiles * ((tb + CFG::BN - 1) / CFG::BN) * ranges, CFG::BN)), dim3(CFG::NT), 0, s,       \
+         LogitArgs{rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, (int)tiles, ranges, part, E, lde, te, k})
   QLORA_HEAD_TILES(rows, QLORA_CALL)
 #undef QLORA_CALL
   return hipGetLastError();

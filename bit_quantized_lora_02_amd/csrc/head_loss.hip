@@ -284,6 +284,73 @@ __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, i
   });
 }
 
+// A workgroup per counted row and 2048 columns: z from the ranges' sums, in order, then what the product's epilogue does with it (see
+// logit_items), a lane taking eight columns.
+__global__ __launch_bounds__(256) void k_head_soft(HeadRows rows, int64_t row0, int64_t tb,
+                                                   const float *__restrict__ part, int ranges, int64_t V, float c,
+                                                   float2 *__restrict__ stat, int64_t ntile,
+                                                   const int32_t *__restrict__ index, int k, bf16_t *__restrict__ E,
+                                                   int64_t lde, int64_t te) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t i = blockIdx.x;
+  int64_t n = *rows.n - row0;
+  n = n < tb ? n : tb;
+  if (i >= n) return;
+  const int64_t t = rows.list[row0 + i];
+  const float ref = rows.ref[t], uc = ref * c;
+  const int rc = rows.refcol[t];
+  const float *const p = part + i * lde;
+  for (int j = tid; blockIdx.y == 0 && j < k; j += 256) {
+    const int64_t v = index[t * k + j];
+    float z = 0.f;
+    if (target_ok(v, V))
+#pragma unroll 4
+      for (int r = 0; r < ranges; ++r) z += p[(int64_t)r * n * lde + v];
+    rows.zt[t * k + j] = z;
+  }
+  const int cols = head_stat_cols(rows.tile_rows == 256 && i < head_whole_rows((int)n, 256)), group = cols / 8;
+  const int64_t v = ((int64_t)blockIdx.y * 256 + tid) * 8;
+  const bool in = v < lde;  // lde % 128 == 0: a group's lanes are all in or all out
+  float z[8], e[8], sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) z[q] = 0.f;
+  if (in)
+#pragma unroll 4
+    for (int r = 0; r < ranges; ++r) {
+      const float4 a = *reinterpret_cast<const float4 *>(p + (int64_t)r * n * lde + v);
+      const float4 b = *reinterpret_cast<const float4 *>(p + (int64_t)r * n * lde + v + 4);
+      z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
+      z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+    }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    if (!in || v + q >= V || v + q == rc) z[q] = -INFINITY;
+    e[q] = __builtin_amdgcn_exp2f(fmaf(z[q], c, -uc));
+    sum += e[q];
+  }
+  for (int o = 1; o < group; o <<= 1) sum += __shfl_xor(sum, o);
+  float u = ref;
+  const bool over = !(sum < kHeadRange);
+  if (__any(over)) {
+    float top = z[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) top = fmaxf(top, z[q]);
+    for (int o = 1; o < group; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    u = over ? top : ref;
+    sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      e[q] = __builtin_amdgcn_exp2f((z[q] - u) * c);
+      sum += e[q];
+    }
+    for (int o = 1; o < group; o <<= 1) sum += __shfl_xor(sum, o);
+  }
+  if (v < V && lane % group == 0) stat[i * ntile + v / cols] = make_float2(u, sum);
+  if (E && in)
+    *reinterpret_cast<u32x4_t *>(E + (v / 32 * te + i) * 32 + v % 32) =
+        u32x4_t{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])};
+}
+
 // One wave per counted row of the block.
 __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, int64_t tb,
                                                       const float2 *__restrict__ stat, int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
@@ -495,6 +562,14 @@ hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, co
   launch(k_head_bucket, dim3((unsigned)((tb + tr - 1) / tr)), dim3(kBucketThreads), (uint32_t)ntile * 4, s, rows, row0,
          tb, tr, index, k, V, (int)ntile, tc, T, K, head_one_tile(T, rows) ? n : (int32_t *)nullptr, list,
          ranges, blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_soft(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int ranges, int64_t V,
+                            float c, float2 *stat, int64_t ntile, const int32_t *index, int k, bf16_t *E, int64_t lde,
+                            int64_t te, hipStream_t s) {
+  launch(k_head_soft, dim3((unsigned)tb, (unsigned)((lde + 2047) / 2048)), dim3(256), 0, s, rows, row0, tb, part, ranges, V, c, stat, ntile, index, k, E,
+         lde, te);
   return hipGetLastError();
 }
 

@@ -99,7 +99,8 @@ def verify(X, W, targets, weight, tau, call, dev="cuda"):
 
 SIZES = [(1, 1, 8), (1, 1000, 264), (2, 64, 2056), (3, 257, 64), (64, 256, 72), (65, 300, 128), (129, 1030, 200),
          (300, 999, 520), (385, 300, 136), (513, 2055, 256), (1100, 700, 1040),
-         (300, 65536 + 7, 264), (40, 1 << 22, 8)]
+         (300, 65536 + 7, 264), (40, 1 << 22, 8), (33, 640, 4104), (200, 1500, 2056),
+         (600, 800, 2048)]
 
 
 @pytest.mark.parametrize("T,V,K", SIZES)
@@ -118,7 +119,8 @@ def test_cross_entropy(T, V, K):
 
 
 @pytest.mark.parametrize("T,V,K,k,tau", [(1, 1, 8, 1, 1.0), (1, 300, 64, 3, 2.0), (5, 1000, 264, 256, 1.0),
-                                         (66, 257, 128, 65, 0.5), (300, 999, 520, 17, 4.0), (513, 2055, 256, 64, 1.5)])
+                                         (66, 257, 128, 65, 0.5), (300, 999, 520, 17, 4.0), (513, 2055, 256, 64, 1.5),
+                                         (33, 640, 4104, 7, 1.0), (300, 700, 2056, 20, 2.0)])
 def test_distillation(T, V, K, k, tau):
     print(f"head_distill T={T} V={V} K={K} k={k} tau={tau}", flush=True)
     X, W, y, weight = inputs(T, V, K, seed=T + V + k)
@@ -143,10 +145,11 @@ def test_distillation(T, V, K, k, tau):
            lambda dx, dw: B.head_distill(Xg, Wg, ig, lg, tau, wg, need_dx=dx, need_dw=dw), dev="cpu")
 
 
-@pytest.mark.parametrize("T", [7, 70, 300])
-def test_logits_far_above_the_target(T):
-    """Rows whose largest logit exceeds the target's by hundreds: beyond what bf16 holds relative to the target."""
-    X, W, y, weight = inputs(T, 1300, 128, seed=T, spread=60.0, lift=0.0)
+@pytest.mark.parametrize("T,K", [(7, 128), (70, 128), (300, 128), (7, 2048), (200, 2048)])
+def test_logits_far_above_the_target(T, K):
+    """Rows whose largest logit exceeds the target's by hundreds: beyond what bf16 holds relative to the target (with the
+    deep reductions, whose few tiles are split, in the kernel that adds the ranges)."""
+    X, W, y, weight = inputs(T, 1300, K, seed=T, spread=60.0, lift=0.0)
     X[::3] *= 0.01  # a third of the rows are ordinary
     Xg, Wg, yg, wg = (t.cuda() for t in (X, W, y, weight))
     verify(X, W, ce_targets(y, 1300), weight, 1.0,
@@ -217,7 +220,7 @@ def test_no_rows():
     assert (loss == 0).all() and (dX == 0).all() and (dW == 0).all()
 
 
-@pytest.mark.parametrize("T,V,K", [(40, 1000, 256), (700, 2055, 520)])
+@pytest.mark.parametrize("T,V,K", [(40, 1000, 256), (700, 2055, 520), (90, 500, 2048)])
 def test_repeatable_and_independent_of_the_workspace(T, V, K):
     X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=1))
     first = B.head_ce(X, W, y, weight, need_dw=True)
@@ -279,7 +282,8 @@ class Guarded:
         return bool((self.raw[:4096] == 0xA5).all()) and bool((self.raw[4096 + self.n:] == 0xA5).all())
 
 
-@pytest.mark.parametrize("T,V,K,k", [(1, 1000, 264, 0), (65, 300, 128, 3), (129, 1030, 200, 0), (513, 2055, 256, 9)])
+@pytest.mark.parametrize("T,V,K,k", [(1, 1000, 264, 0), (65, 300, 128, 3), (129, 1030, 200, 0), (513, 2055, 256, 9),
+                                     (35, 640, 4104, 3)])
 def test_writes_only_its_buffers(T, V, K, k):
     print(f"guard bands T={T} V={V} K={K} k={k}", flush=True)
     X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=2))
