@@ -86,13 +86,12 @@ __device__ __forceinline__ lds_char *in_slot(lds_char *base, int slot, const Lan
 
 // How an operand lies in memory (element (i, r): row or column i of the tile's side, reduction index r):
 //  LINES:   row-major [i][r]; copied 64 reduction indices (whole 128-byte lines) and two steps at a time: in halves
-//           every line is fetched twice, which costs the 256 x 256 tile 4% (1355 against 1308 TFLOP/s).
-//  HALF_LINES: the same, a step at a time: more of W's stream in flight, which is what few rows need (17 rows x 32000
-//           x 2048: 24.6 us against 29.1).
+//           every line is fetched twice (logits of 8192 rows 1308 against 1355 TFLOP/s, of 64 rows x 50257 x 1024 28
+//           against 24 us).
 //  BLOCKS:  32 reduction indices at a time, [r / 32][i][32]: a step's tile is one contiguous piece.
 //  ACROSS:  row-major [r][i].
 //  BLOCKS_ACROSS: [i / 32][r][32], what BLOCKS is seen from its other side.
-enum { LINES, HALF_LINES, BLOCKS, ACROSS, BLOCKS_ACROSS };
+enum { LINES, BLOCKS, ACROSS, BLOCKS_ACROSS };
 
 // One operand's tile of ROWS rows (columns for the ACROSS ones).  `ld` is the row length of a row-major matrix, the
 // number of rows in a block otherwise.  BLOCKS rows are gathered through `list` if there is one; rows past the last
@@ -151,8 +150,8 @@ struct Tile {
   __device__ __forceinline__ void copy(int s, int i, lds_char *to, int wave) const {
     const char *b = base;
     uint32_t o;
-    if constexpr (KIND == LINES || KIND == HALF_LINES) {
-      o = off[i] + 2 * min(k0 + s * (PAIR ? 2 * BK : BK), (uint32_t)red - 8);
+    if constexpr (KIND == LINES) {
+      o = off[i] + 2 * min(k0 + s * (2 * BK), (uint32_t)red - 8);
     } else if constexpr (KIND == BLOCKS) {
       b += (int64_t)s * ld * (2 * BK);
       o = off[i];
@@ -434,8 +433,7 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   int m0 = 0, n0 = 0;
-  constexpr int KW = C::BN == 64 ? HALF_LINES : LINES;
-  auto setup = [&](Tile<C::BM, C::NT, KW> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
+  auto setup = [&](Tile<C::BM, C::NT, LINES> &ta, Tile<C::BN, C::NT, BLOCKS> &tbl, int *s0, int *s1) {
     ta.init(g.W, K, (int64_t)items.m * C::BM, V, K, nullptr, wave, lane);
     tbl.init(g.X, g.ldx, first + (int64_t)items.n * C::BN, n, K, rows.list + row0, wave, lane);
     const int fours = (int)((K + 127) / 128), per = SPLIT ? (fours + g.ranges - 1) / g.ranges : fours;
@@ -594,7 +592,7 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
       }
     }
   };
-  products<C, KW, BLOCKS>(items, turn, ring, wave, lane, setup, begin, late, finish);
+  products<C, LINES, BLOCKS>(items, turn, ring, wave, lane, setup, begin, late, finish);
 }
 
 template <class C, bool SPLIT>
@@ -604,19 +602,14 @@ __global__ __launch_bounds__(C::NT) void k_head_logits(LogitArgs g) {
   const int whole = SPLIT ? n : head_whole_rows(n, C::BN);
   Items items = {g.tiles, (whole + C::BN - 1) / C::BN, SPLIT ? g.ranges : 1};
   const Turn all = {blockIdx.x, gridDim.x};
-  if constexpr (C::BN == 64) {
-    QLORA_RING(C, ring);
-    logit_items<C, SPLIT>(g, 0, n, items, all, ring);
-  } else {
-    QLORA_RING_PAIRS(C, ring);
-    if (whole > 0) logit_items<C, SPLIT>(g, 0, whole, items, all, ring);
-    if constexpr (C::BN == 256 && !SPLIT) {
-      if (whole == n) return;
-      const Turn turn = second_pass(items, (uint32_t)g.tiles);
-      between_passes();
-      items = {g.tiles, 1, 1};
-      logit_items<H128, false>(g, whole, n, items, turn, ring);
-    }
+  QLORA_RING_PAIRS(C, ring);
+  if (whole > 0) logit_items<C, SPLIT>(g, 0, whole, items, all, ring);
+  if constexpr (C::BN == 256 && !SPLIT) {
+    if (whole == n) return;
+    const Turn turn = second_pass(items, (uint32_t)g.tiles);
+    between_passes();
+    items = {g.tiles, 1, 1};
+    logit_items<H128, false>(g, whole, n, items, turn, ring);
   }
 }
 
