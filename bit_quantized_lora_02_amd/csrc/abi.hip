@@ -1071,7 +1071,7 @@ int qlora_head_distill(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int6
                        const int32_t *index, const float *logit, int32_t k, float tau, const float *weight,
                        float *loss, qlora_bf16 *dX, qlora_bf16 *dW, void *ws, size_t ws_bytes, void *stream) {
   if (k < 1 || k > QLORA_MAX_TARGETS) return fail(QLORA_EINVAL, "k must be in [1, %d] (got %d)", QLORA_MAX_TARGETS, (int)k);
-  if (!(tau > 0.f) || !isfinite(tau)) return fail(QLORA_EINVAL, "tau must be positive and finite (got %g)", (double)tau);
+  if (!(tau >= 1e-4f && tau <= 1e4f)) return fail(QLORA_EINVAL, "tau must be in [1e-4, 1e4] (got %g)", (double)tau);
   if (T > 0 && (!index || !logit)) return fail(QLORA_EINVAL, "index and logit must not be NULL");
   if (!aligned_to(index, 4) || !aligned_to(logit, 4)) return fail(QLORA_EINVAL, "index and logit must be 4-byte aligned");
   return head_loss(X, T, W, n_vocab, n_in, nullptr, index, logit, k, tau, weight, loss, dX, dW, ws, ws_bytes, stream);

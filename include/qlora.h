@@ -383,7 +383,8 @@ int qlora_head_ce(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t n
  * [0, n_vocab) or whose logit is -inf has no part (fill short lists with -1); a
  * row without any other entry is ignored as in qlora_head_ce.  The same index
  * twice in a row adds its probabilities.  Logits are otherwise finite.
- * 1 <= k <= QLORA_MAX_TARGETS, tau > 0.  index and logit are 4-byte aligned.
+ * 1 <= k <= QLORA_MAX_TARGETS, 1e-4 <= tau <= 1e4.  index and logit are 4-byte
+ * aligned.
  * ws: qlora_head_workspace_bytes(T, n_vocab, n_in, k, dX != NULL, dW != NULL).
  */
 int qlora_head_distill(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t n_vocab, int64_t n_in,

@@ -51,7 +51,7 @@ def test_cross_entropy_refuses(lib, kw, text):
 
 @pytest.mark.parametrize("kw,text", SHARED + [
     (dict(index=None), "index"), (dict(logit=None), "logit"), (dict(index=ODD), "4-byte"), (dict(logit=ODD), "4-byte"),
-    (dict(k=0), "k must"), (dict(k=257), "k must"), (dict(tau=0.0), "tau"), (dict(tau=-1.0), "tau"),
+    (dict(k=0), "k must"), (dict(k=257), "k must"), (dict(tau=0.0), "tau"), (dict(tau=-1.0), "tau"), (dict(tau=9e-5), "tau"), (dict(tau=1.1e4), "tau"),
     (dict(tau=float("nan")), "tau"), (dict(tau=float("inf")), "tau")])
 def test_distillation_refuses(lib, kw, text):
     assert kd(lib, **kw) == B.QLORA_EINVAL

@@ -120,7 +120,9 @@ def test_cross_entropy(T, V, K):
 
 @pytest.mark.parametrize("T,V,K,k,tau", [(1, 1, 8, 1, 1.0), (1, 300, 64, 3, 2.0), (5, 1000, 264, 256, 1.0),
                                          (66, 257, 128, 65, 0.5), (300, 999, 520, 17, 4.0), (513, 2055, 256, 64, 1.5),
-                                         (33, 640, 4104, 7, 1.0), (300, 700, 2056, 20, 2.0)])
+                                         (33, 640, 4104, 7, 1.0), (300, 700, 2056, 20, 2.0),
+                                         (1, 5000, 520, 9, 1.0), (40, 1 << 22, 8, 5, 1.0), (300, 1 << 20, 16, 5, 1.0),
+                                         (70, 1000, 128, 4, 1e-2), (70, 1000, 128, 4, 1e4)])
 def test_distillation(T, V, K, k, tau):
     print(f"head_distill T={T} V={V} K={K} k={k} tau={tau}", flush=True)
     X, W, y, weight = inputs(T, V, K, seed=T + V + k)
@@ -202,6 +204,40 @@ def test_several_blocks_of_rows():
             wdw += gw
             bdw += bw
         check("dW", dW, wdw, bdw + (T / 8 + 16) * U * bdw / BF)
+
+
+def test_output_layer_beyond_4_gib():
+    """Offsets into W, and into dW, pass 32 bits; the rows of dW are checked at both ends and in the middle."""
+    T, V, K = 70, 524800, 4104
+    assert V * K * 2 > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    W = torch.empty(V, K, dtype=torch.bfloat16, device="cuda").normal_(0.0, 0.03, generator=g)
+    X = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    y = torch.randint(V - 1000, V, (T,), generator=g, device="cuda")
+    y[::7] = torch.arange(0, T, 7, device="cuda")
+    weight = torch.randn(T, generator=g, device="cuda")
+    loss, dX, dW = B.head_ce(X, W, y, weight, need_dw=True)
+    # the definition a part of the vocabulary at a time
+    Xd, parts = X.double(), [slice(a, min(a + 65536, V)) for a in range(0, V, 65536)]
+    z = torch.cat([Xd @ W[p].double().t() for p in parts], 1)
+    dz = (K / 8 + 16) * U * torch.cat([(Xd.abs() @ W[p].double().abs().t()).amax(1, keepdim=True) for p in parts], 1).amax(1)
+    logq = torch.log_softmax(z, 1)
+    nll, zmax = -logq.gather(1, y[:, None])[:, 0], z.abs().amax(1)
+    check("loss", loss, nll, (2 * dz + 8 * U * (zmax + nll.abs() + 4)) * (1 + 2.0 ** -6))
+    P = torch.zeros_like(logq).scatter_(1, y[:, None], 1.0)
+    f = weight.double()[:, None]
+    G = f * (logq.exp() - P)
+    dG = BF * G.abs() + f.abs() * (logq.exp() + P) * (4 * dz + 16 * U * (zmax + 8))[:, None]
+    want, bound = torch.zeros(T, K, dtype=torch.float64, device="cuda"), torch.zeros(T, K, dtype=torch.float64, device="cuda")
+    for p in parts:
+        Wp = W[p].double()
+        want += G[:, p] @ Wp
+        bound += (dG[:, p] + (V / 8 + 16) * U * G[:, p].abs()) @ Wp.abs()
+    check("dX", dX, want, (bound + BF * want.abs()) * (1 + 2.0 ** -6))
+    for p in (slice(0, 500), slice(V // 2, V // 2 + 500), slice(V - 1000, V)):
+        want = G[:, p].t() @ Xd
+        bound = (dG[:, p] + (BF + (T / 8 + 16) * U) * G[:, p].abs()).t() @ Xd.abs() + BF * want.abs()
+        check("dW", dW[p], want, bound * (1 + 2.0 ** -6))
 
 
 def test_no_rows():
@@ -370,8 +406,11 @@ def test_autograd_functions():
                 (total * 2.0).backward()
             assert (x.grad is None) if not gx else torch.equal(x.grad, dX * 2.0)
             assert (w.grad is None) if not gw else torch.equal(w.grad, dW * 2.0)
-    total, _ = B.HeadCEFn.apply(X.clone().requires_grad_(True), W, y)
-    assert torch.allclose(total, B.head_ce(X, W, y, need_dx=False)[0].sum())
+    x = X.clone().requires_grad_(True)
+    total, _ = B.HeadCEFn.apply(x, W, y)
+    total.backward()
+    loss, dX, _ = B.head_ce(X, W, y)
+    assert torch.equal(total, loss.sum()) and torch.equal(x.grad, dX)
 
 
 def test_a_training_step():
