@@ -663,48 +663,70 @@ class QLoRALinearFn(torch.autograd.Function):
         return dX, None, dA, dB, None
 
 
-def _head_total(ctx, loss, weight, dX, dW):
-    ctx.save_for_backward(*(t for t in (dX, dW) if t is not None))
+def _sum(x):
+    # In pieces that one workgroup adds each: torch's sum over several workgroups clears its counters with a memset, which
+    # does not replay reliably from a captured graph.
+    while x.numel() > 4096:
+        x = torch.nn.functional.pad(x, (0, -x.numel() % 1024)).view(-1, 1024).sum(1)
+    return x.sum()
+
+
+def _head_total(ctx, loss, weight, dX, dW, weight_at):
     ctx.have = (dX is not None, dW is not None)
+    ctx.weight_at = weight_at if weight is not None and ctx.needs_input_grad[weight_at] else None
+    ctx.save_for_backward(*(t for t in (dX, dW, loss if ctx.weight_at else None) if t is not None))
     ctx.mark_non_differentiable(loss)
-    return (loss if weight is None else loss * weight).sum(), loss
+    # (an ignored row's weight may be anything)
+    return _sum(loss if weight is None else torch.where(loss == 0, loss, loss * weight)), loss
 
 
 def _head_grads(ctx, g):
     saved = list(ctx.saved_tensors)
-    return tuple(saved.pop(0) * g if have else None for have in ctx.have)
+    grads = [None] * len(ctx.needs_input_grad)
+    for at in (0, 1):
+        if ctx.have[at]:
+            grads[at] = saved.pop(0) * g
+    if ctx.weight_at:
+        grads[ctx.weight_at] = saved.pop(0) * g
+    return tuple(grads)
 
 
 class HeadCEFn(torch.autograd.Function):
     """Autograd wrapper of ``head_ce``: forward(X, W, labels, weight) -> (sum(weight * loss), loss [T]).
 
     The gradients are formed with the losses, in one call, for those of X and W that need them; the backward
-    multiplies them by the incoming scalar. The per-token losses carry no gradient."""
+    multiplies them by the incoming scalar (and the losses, for a weight that needs a gradient). The per-token losses
+    carry no gradient. Forward and backward can be captured into a HIP graph, as any autograd function, where no eager
+    graph of the same leaves is alive."""
 
     @staticmethod
     def forward(ctx, X, W, labels, weight=None):
         loss, dX, dW = head_ce(X, W, labels, weight, need_dx=ctx.needs_input_grad[0], need_dw=ctx.needs_input_grad[1])
-        return _head_total(ctx, loss, weight, dX, dW)
+        return _head_total(ctx, loss, weight, dX, dW, 3)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g, _):
-        return *_head_grads(ctx, g), None, None
+        return _head_grads(ctx, g)
 
 
 class HeadDistillFn(torch.autograd.Function):
-    """Autograd wrapper of ``head_distill``: forward(X, W, index, logit, tau, weight) -> (sum(weight * loss), loss)."""
+    """Autograd wrapper of ``head_distill``: forward(X, W, index, logit, tau, weight) -> (sum(weight * loss), loss [T]).
+
+    As ``HeadCEFn``; the teacher's logits get no gradient, so ones that ask for it are refused."""
 
     @staticmethod
     def forward(ctx, X, W, index, logit, tau=1.0, weight=None):
+        if ctx.needs_input_grad[3]:
+            raise ValueError("the teacher's logits get no gradient: detach them")
         loss, dX, dW = head_distill(X, W, index, logit, tau, weight, need_dx=ctx.needs_input_grad[0],
                                     need_dw=ctx.needs_input_grad[1])
-        return _head_total(ctx, loss, weight, dX, dW)
+        return _head_total(ctx, loss, weight, dX, dW, 5)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g, _):
-        return *_head_grads(ctx, g), None, None, None, None
+        return _head_grads(ctx, g)
 
 
 def timing_enable(kernel: str, enable: bool = True):

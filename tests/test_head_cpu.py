@@ -124,3 +124,10 @@ def test_distill_binding_refuses(lib, change, exc):
     kw = dict(X=X, W=W, index=torch.zeros(8, 4, dtype=torch.int32), logit=torch.zeros(8, 4)) | change
     with pytest.raises(exc):
         B.head_distill(**kw)
+
+
+def test_distill_function_refuses_teacher_gradients():
+    X, W = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(5, 64, dtype=torch.bfloat16)
+    index, logit = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1, requires_grad=True)
+    with pytest.raises(ValueError, match="teacher's logits get no gradient"):
+        B.HeadDistillFn.apply(X, W, index, logit)

@@ -443,3 +443,80 @@ def test_a_training_step():
     state = [B.AdamState.zeros_like(p.detach()) for p in (A, Bm)]
     B.adamw_step([A.detach(), Bm.detach()], [A.grad, Bm.grad], state, lr=1e-2, step=1)
     assert not torch.equal(was, A.detach()) and torch.isfinite(A.detach()).all()
+
+
+def test_distillation_in_several_blocks():
+    """Teacher's targets of rows in two blocks of the workspace, whose gradient of W is carried from one to the next."""
+    T, V, K, k, tau = 2300, 262145, 64, 7, 2.0
+    assert B.head_workspace_bytes(T, V, K, k, True, False) < 1.4 * 2 ** 30 and T * V * 2 > 2 ** 30
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=10))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    index = torch.randint(0, V, (T, k), generator=g, device="cuda")
+    index[:, 0] = y
+    index[torch.rand(T, generator=g, device="cuda") < 0.2] = -1
+    index[::3, k // 2:] = -1
+    index = index.to(torch.int32)
+    logit = 3.0 * torch.randn(T, k, generator=g, device="cuda")
+    loss, dX, dW = B.head_distill(X, W, index, logit, tau, weight, need_dw=True)
+    wdw, bdw = torch.zeros(V, K, dtype=torch.float64, device="cuda"), torch.zeros(V, K, dtype=torch.float64, device="cuda")
+    for part in torch.arange(T, device="cuda").split(460):
+        l, gx, gw, bl, bx, bw = reference(X[part], W, *kd_targets(index[part], logit[part], V, tau), weight[part], tau)
+        check("loss", loss[part], l, bl)
+        check("dX", dX[part], gx, bx)
+        wdw += gw
+        bdw += bw
+    check("dW", dW, wdw, bdw + (T / 8 + 16) * U * bdw / BF)
+
+
+def test_autograd_gradient_of_the_weights():
+    """total = sum(weight * loss): the weights' gradient is the losses; an ignored row may have any weight."""
+    T, V, K = 80, 500, 64
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=11))
+    y[3], weight[3] = -100, float("inf")
+    index, logit = y[:, None].to(torch.int32), torch.randn(T, 1, device="cuda")
+    for fn in (lambda x, w: B.HeadCEFn.apply(x, W, y, w), lambda x, w: B.HeadDistillFn.apply(x, W, index, logit, 1.0, w)):
+        for gx in (True, False):
+            x, w = X.clone().requires_grad_(gx), weight.clone().requires_grad_(True)
+            total, loss = fn(x, w)
+            keep = torch.arange(T, device="cuda") != 3
+            assert torch.isfinite(total) and loss[3] == 0
+            # two orders of the same T binary32 terms
+            terms = (loss * weight)[keep].double()
+            assert (total.double() - terms.sum()).abs() <= T * U * terms.abs().sum()
+            (total * 0.5).backward()
+            assert torch.equal(w.grad, loss * 0.5)
+            assert (x.grad is not None) == gx
+
+
+def test_autograd_captured():
+    """Forward and backward of the wrapper in one graph, with so many rows that a plain sum of their losses would take
+    several workgroups; replayed on new inputs with eager work between."""
+    T, V, K = 20000, 100, 64
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=12))
+    x = X.clone().requires_grad_(True)
+
+    def step(x):
+        total, loss = B.HeadCEFn.apply(x, W, y, weight)
+        return total.detach(), loss, torch.autograd.grad(total, x)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(x)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for rep in range(4):
+        with torch.no_grad():
+            x.copy_(torch.randn(T, K, generator=g, device="cuda"))
+        want = step(x.detach().clone().requires_grad_(True))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, a, b in zip(("total", "loss", "dX"), outs, want):
+            assert torch.equal(a, b), f"{name} of replay {rep}"
+        terms = (want[1] * weight).double()
+        assert (want[0].double() - terms.sum()).abs() <= T * U * terms.abs().sum()
