@@ -546,12 +546,12 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
                                        s));
   const bool sorted = k > 0 && p.ranges == 1;  // the targets go by the product's tiles
   float *zpart = p.ranges > 1 ? (float *)(w + p.off_z) : nullptr;
-  if (k > 0 && !(T > 0 && sorted && head_one_tile(T, rows))) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, rg, p.b, s));
+  const bool few = k > 0 && head_few_targets(T, k, p.b.tile_rows);
+  if (k > 0 && !few) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, rg, p.b, s));
   for (int64_t b = 0; b < p.b.count; ++b) {
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
     rows.ranges = ranges + 2 * b;
-    if (tb > 0 && sorted)
-      LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, T, K, n, list, rg, p.b, s));
+    if (tb > 0 && sorted && !few) LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, s));
     if (tb > 0)
       LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, k,
                                                p.ranges, zpart, s));

@@ -48,22 +48,35 @@ __host__ __device__ inline int head_tile_cols(int tile_rows) { return tile_rows 
 constexpr int kHeadRanges = 32, kHeadSlots64 = 768;
 
 // Ranges of the logit product's reduction over K for T rows: more than one where the output has too few tiles to
-// occupy the chip (a small vocabulary, few rows).  In microseconds: a 32-deep step takes 0.8 in a 256-wide tile and 0.25
-// in a 128-wide one however few there are; splitting costs a launch, about 5, and the binary32 sums, written and read
-// once at about 4.5 TB/s.
+// occupy the chip (a small vocabulary, few rows).  In microseconds: a 32-deep step takes 0.8 in a 256-wide tile however
+// few there are; in a 128-wide one 0.25 and 0.001 for each workgroup that shares the memory, from about 450 of them on
+// their 8 KB of W at 5.3 TB/s (250 workgroups 0.51, 375 0.71, 750 1.16).  Splitting costs a launch, about 5, and the
+// binary32 sums, written and read once at about 4.5 TB/s.  (16 x 32000 x 4096: 55 us in three ranges, 66 in one;
+// 60 x 48000 x 4096: 107 in two, 91 in one.)
 inline int head_logit_ranges(int64_t T, int64_t V, int64_t K, int tile_rows) {
   const int64_t cols = head_tile_cols(tile_rows), tiles = (V + cols - 1) / cols * ((T + tile_rows - 1) / tile_rows);
   const int64_t slots = tile_rows == 64 ? kHeadSlots64 : 256, fours = (K + 127) / 128;
   if (tiles * 2 > slots) return 1;
-  const float step = tile_rows == 64 ? 0.25f : 0.8f, sums = (float)(T * V) * 8.f / 4.5e6f;
+  auto step = [&](int64_t wgs) {
+    const float some = 0.25f + 0.001f * (float)wgs, many = 0.00155f * (float)wgs;
+    return tile_rows == 64 ? (some > many ? some : many) : 0.8f;
+  };
+  const float sums = (float)(T * V) * 8.f / 4.5e6f;
   int best = 1;
-  float least = 4.f * (float)fours * step;
+  float least = 4.f * (float)fours * step(tiles);
   for (int s = 2; s <= 16 && s <= fours && tiles * s <= slots; ++s) {
-    const float cost = 4.f * (float)((fours + s - 1) / s) * step + 5.f + sums * (float)s;
+    const float cost = 4.f * (float)((fours + s - 1) / s) * step(tiles * s) + 5.f + sums * (float)s;
     if (cost < least) least = cost, best = s;
   }
   const int64_t per = (fours + best - 1) / best;
   return (int)((fours + per - 1) / per);
+}
+
+// A teacher's targets of one row tile and at most this many: one of k_head_prep's workgroups numbers the rows and sorts
+// the targets while the others take the rows, which saves one launch or two.
+constexpr int kHeadFewTargets = 4096;
+__host__ __device__ inline bool head_few_targets(int64_t T, int k, int tile_rows) {
+  return T <= tile_rows && T * k <= kHeadFewTargets;
 }
 
 // How the counted rows are taken in blocks.
@@ -79,14 +92,12 @@ hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t
                             const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
                             int32_t *ranges, const HeadBlocks &blocks, const HeadRows &rows, float *loss, bf16_t *dX,
                             bf16_t *Xt, int64_t ldx, hipStream_t s);
-// Without labels: numbers the rows after launch_head_prep (where one row tile holds them all, launch_head_bucket does).
+// Without labels and unless head_few_targets: numbers the rows after launch_head_prep.
 hipError_t launch_head_list(const HeadRows &rows, int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
                             const HeadBlocks &blocks, hipStream_t s);
-inline bool head_one_tile(int64_t T, const HeadRows &rows) { return T <= rows.tile_rows; }
 // Sorts the targets of a block's counted rows by the output tile of the logit product they fall into.
 hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
-                              int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
-                              const HeadBlocks &blocks, hipStream_t s);
+                              hipStream_t s);
 // Losses, the targets' entries of E, and per row of the block (scale) the factor, what the first target's entry lost in
 // rounding, the factor's fraction and that target's column; rows of X times the factor's power of two (Xs, for dW).
 hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, const float2 *stat, int64_t ntile,

@@ -37,6 +37,11 @@ struct HeadCfg {
   // 16-byte copies per thread of a step's tile of the n-side: the last ones of an item's last four steps, which its
   // epilogue need not wait for (the next item asks for them in its third step)
   static constexpr int LB = BN * BK / 8 / NT;
+  // Few rows: the logit product is bound by the stream of W's rows, and workgroups that all begin at column 0 of theirs ask
+  // for addresses a row's length apart, which for powers of two lie in few memory channels.  Each output tile begins
+  // 128 columns after the one before it instead (16 x 32000 x 8192 in two ranges 124 -> 94 us; 128 x 128256 x 4096 221 ->
+  // 211; a length that is no power of two: no change).  Wide tiles are bound by the MFMAs and share X's tiles in L2.
+  static constexpr bool TURNS = BN < 256;
 };
 using H256 = HeadCfg<2, 4, 4, 2>;  // 128 x 64 per wave
 using H128 = HeadCfg<4, 2, 2, 2>;  // 64 x 64 per wave
@@ -282,7 +287,8 @@ __device__ __forceinline__ void between_passes() {
 // as the ring allows: more than two steps.)  The last four steps of an item copy the first four of the next one, so the
 // ring never drains and an item's epilogue hides the first latency of the next.
 //
-//  setup(ta, tb, s0, s1): the tiles and steps of the item just taken
+//  setup(ta, tb, s0, s1): the tiles and steps of the item just taken; returns the step to begin with (TURNS: s0 + 4 i,
+//  after the last step come those before it; else s0)
 //  begin(): notes for its epilogue    late(): before its last four steps (loads that the epilogue needs at once)
 //  finish(acc): its epilogue; calls arrive<LB>() before its first store
 template <class C, int KA, int KB, class Setup, class Begin, class Late, class Finish>
@@ -300,8 +306,7 @@ __device__ __forceinline__ void products(Items &items, Turn turn, const Ring &ri
   if (!items.take(lin)) return;
   TileA ta;
   TileB tb;
-  int s0, s1;
-  setup(ta, tb, &s0, &s1);
+  int s0, s1, begin_at = setup(ta, tb, &s0, &s1);
   Operand<C::BM, C::WM, KA, PAIR ? NEAR : BY_SLOT> oa;
   Operand<C::BN, C::WN, KB, PAIR ? FAR : BY_SLOT> ob;
   oa.init(0, wave / C::WAVES_N * C::WM * 32, lane);
@@ -322,7 +327,7 @@ __device__ __forceinline__ void products(Items &items, Turn turn, const Ring &ri
     }
   };
 #pragma unroll
-  for (int q = 0; q < STAGES; ++q) copies(s0 + q, q, 0, count(q));
+  for (int q = 0; q < STAGES; ++q) copies((C::TURNS ? begin_at : s0) + q, q, 0, count(q));
   arrive();
   for (;;) {
     begin();
@@ -366,19 +371,22 @@ __device__ __forceinline__ void products(Items &items, Turn turn, const Ring &ri
     read(0, 0);
     int s = s0;
     for (; s + 4 < s1; s += 4) {
-      step(std::integral_constant<int, 0>(), s + 4, s == s0);
-      step(std::integral_constant<int, 1>(), s + 5, s == s0);
-      step(std::integral_constant<int, 2>(), s + 6, false);
-      step(std::integral_constant<int, 3>(), s + 7, false);
+      if constexpr (C::TURNS) begin_at = begin_at + 4 == s1 ? s0 : begin_at + 4;
+      const int next = C::TURNS ? begin_at : s + 4;
+      step(std::integral_constant<int, 0>(), next, s == s0);
+      step(std::integral_constant<int, 1>(), next + 1, s == s0);
+      step(std::integral_constant<int, 2>(), next + 2, false);
+      step(std::integral_constant<int, 3>(), next + 3, false);
     }
     late();
     lin += turn.stride;
     const bool more = items.take(lin), fresh = s == s0;
-    if (more) setup(ta, tb, &s0, &s1);  // (else the first steps of this item are copied once more)
-    step(std::integral_constant<int, 0>(), s0, fresh);
-    step(std::integral_constant<int, 1>(), s0 + 1, fresh);
-    step(std::integral_constant<int, 2>(), s0 + 2, false);
-    step(std::integral_constant<int, 3>(), s0 + 3, false);
+    if (more) begin_at = setup(ta, tb, &s0, &s1);  // (else four steps of this item are copied once more)
+    const int next = C::TURNS ? begin_at : s0;
+    step(std::integral_constant<int, 0>(), next, fresh);
+    step(std::integral_constant<int, 1>(), next + 1, fresh);
+    step(std::integral_constant<int, 2>(), next + 2, false);
+    step(std::integral_constant<int, 3>(), next + 3, false);
     finish(acc);
     if (!more) {
       arrive();  // nothing is left on its way into LDS
@@ -439,6 +447,7 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
     const int fours = (int)((K + 127) / 128), per = SPLIT ? (fours + g.ranges - 1) / g.ranges : fours;
     *s0 = SPLIT ? items.range * per * 4 : 0;
     *s1 = SPLIT ? min(*s0 + per * 4, fours * 4) : fours * 4;
+    return C::TURNS ? *s0 + items.m * 4 % (*s1 - *s0) : *s0;
   };
   // The epilogue's first loads are issued before the reduction: the lane's rows in X, and the item's targets (one per
   // lane, the first 64 of them).
@@ -528,7 +537,7 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int m = 32 * i + 8 * (e >> 2) + (e & 3);
-            acc[i][j][e] = (m == rc) | (m >= end) ? -INFINITY : acc[i][j][e];
+            acc[i][j][e] = ((m == rc) | (m >= end)) ? -INFINITY : acc[i][j][e];
           }
       }
     }
@@ -644,6 +653,7 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
     const int fours = (int)(g.lde / 128), per = (fours + ranges - 1) / ranges;
     *s0 = items.range * per * 4;
     *s1 = min(*s0 + per * 4, fours * 4);
+    return *s0;
   };
   auto begin = [&]() { m0 = items.m * C::BM, n0 = first + items.n * C::BN, range = items.range; };
   auto late = []() {};
@@ -742,6 +752,7 @@ __device__ __forceinline__ void dw_items(const DwArgs &g, int begin_v, int end_v
     tbl.init(g.E, g.te, begin_v + (int64_t)items.n * C::BN, g.lde, max(n, 1), nullptr, wave, lane);
     *s0 = 0;
     *s1 = deep * 4;
+    return 0;
   };
   auto begin = [&]() { m0 = items.m * C::BM, n0 = begin_v + items.n * C::BN; };
   auto late = []() {};

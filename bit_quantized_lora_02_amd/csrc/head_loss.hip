@@ -12,6 +12,8 @@
 // so the product kernels take E with only the targets' entries replaced by E_v - S P_v (at r: (1 - P_r) - P_r rest,
 // again without cancellation), and the row factor w tau / S is applied in binary32 afterwards.  Entries are rounded to
 // bf16 for the matrix unit; at r, whose entry outweighs the others, dX also gets the remainder.
+#include <type_traits>
+
 #include "device.h"
 #include "head.h"
 #include "launch.h"
@@ -126,25 +128,89 @@ __device__ __forceinline__ void number_rows(int64_t T, int64_t K, Counts counts,
   }
 }
 
-// With labels, workgroup 0 numbers the rows that count (their teachers' rows are looked at first: k_head_list); the
-// other workgroups' waves take a row of X each: its first
-// target (the label, or the teacher's most probable one; the first of equals) and that target's logit by a dot
-// product (binary32 FMA), the teacher's softmax, and the row in the blocks of 32 columns that the logit product reads
-// (zeros past K); or, for a row that does not count, its zero loss and gradient.
+// One workgroup's counting sort of a row tile's targets by output tile of the logit product: `have` rows of the block's
+// list from `first`, into rows.bucket and rows.target at row tile `tile`.  (The order within an output tile is that of
+// the LDS counters; every target's logit goes to a place of its own, so no result depends on it.)
+template <int threads>
+__device__ __forceinline__ void sort_targets(const HeadRows &rows, int64_t tile, int64_t first, int have, int tile_rows,
+                                             int tile_cols, int ntile, const int32_t *__restrict__ index, int k,
+                                             int64_t V, int *s_count /* [ntile] */) {
+  __shared__ int s_sum[threads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  have *= k;
+  for (int i = tid; i < ntile; i += threads) s_count[i] = 0;
+  __syncthreads();
+  auto each = [&](auto use) {
+#pragma unroll 4
+    for (int e = tid; e < have; e += threads) {
+      const int nj = e / k, j = e - nj * k;
+      const int64_t v = index[(int64_t)((volatile const int32_t *)rows.list)[first + nj] * k + j];
+      if (target_ok(v, V)) use((int)v, nj, j);
+    }
+  };
+  each([&](int v, int, int) { atomicAdd(&s_count[v / tile_cols], 1); });
+  __syncthreads();
+  // exclusive sums over the tiles, a run of `per` of them per thread
+  const int per = (ntile + threads - 1) / threads, i0 = tid * per;
+  int mine = 0;
+  for (int i = i0; i < i0 + per && i < ntile; ++i) mine += s_count[i];
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(before, o);
+    if (lane >= o) before += up;
+  }
+  if (lane == 63) s_sum[wave] = before;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) before += s_sum[w];
+  int at = before - mine;
+  int32_t *bucket = rows.bucket + tile * (ntile + 1);
+  for (int i = i0; i < i0 + per && i < ntile; ++i) {
+    const int c = s_count[i];
+    bucket[i] = s_count[i] = at;
+    at += c;
+  }
+  if (i0 < ntile && i0 + per >= ntile) bucket[ntile] = at;
+  __syncthreads();
+  uint32_t *target = rows.target + tile * tile_rows * k;
+  each([&](int v, int nj, int j) {
+    target[atomicAdd(&s_count[v / tile_cols], 1)] = (uint32_t)j | (uint32_t)(v % tile_cols) << 8 | (uint32_t)nj << 16;
+  });
+}
+
+// Workgroup 0 numbers the rows that count: with labels, or where the teacher's targets are few (head_few_targets), which
+// it then also sorts; k_head_list and k_head_bucket do it otherwise.  The other workgroups' waves take a row of X each:
+// its first target (the label, or the teacher's most probable one; the first of equals) and that target's logit by a
+// dot product (binary32 FMA), the teacher's softmax, and the row in the blocks of 32 columns that the logit product
+// reads (zeros past K); or, for a row that does not count, its zero loss and gradient.
 __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__restrict__ X, int64_t T,
                                                             const bf16_t *__restrict__ W, int64_t V, int64_t K,
                                                             const int64_t *__restrict__ labels,
                                                             const int32_t *__restrict__ index,
                                                             const float *__restrict__ logit, int k, float tau,
-                                                            int32_t *__restrict__ n, int32_t *__restrict__ list,
-                                                            int32_t *__restrict__ ranges, HeadBlocks blocks,
-                                                            HeadRows rows, float *__restrict__ loss,
-                                                            bf16_t *__restrict__ dX, bf16_t *__restrict__ Xt,
-                                                            int64_t ldx) {
+                                                            int32_t *n, int32_t *list, int32_t *__restrict__ ranges,
+                                                            HeadBlocks blocks, HeadRows rows, int tile_cols, int ntile,
+                                                            float *__restrict__ loss, bf16_t *__restrict__ dX,
+                                                            bf16_t *__restrict__ Xt, int64_t ldx) {
+  extern __shared__ int s_count[];  // [ntile] where workgroup 0 sorts the targets
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (blockIdx.x == 0) {
-    if (labels)
+    if (labels) {
       number_rows<kPrepThreads>(T, K, [&](int64_t t) { return target_ok(labels[t], V); }, n, list, ranges, blocks);
+    } else if (head_few_targets(T, k, blocks.tile_rows)) {
+      __shared__ int s_counts[256];  // (the most rows of a tile)
+      for (int t = tid; t < T; t += kPrepThreads) s_counts[t] = 0;
+      __syncthreads();
+#pragma unroll 4
+      for (int e = tid; e < (int)T * k; e += kPrepThreads)
+        if (target_ok(index[e], V) && logit[e] > -INFINITY) s_counts[e / k] = 1;
+      __syncthreads();
+      number_rows<kPrepThreads>(T, K, [&](int64_t t) { return s_counts[t] != 0; }, n, list, ranges, blocks);
+      __syncthreads();
+      if (rows.target)
+        sort_targets<kPrepThreads>(rows, 0, 0, *(volatile const int32_t *)n, blocks.tile_rows, tile_cols, ntile, index, k,
+                                   V, s_count);
+    }
     return;
   }
   const int64_t t = (int64_t)(blockIdx.x - 1) * (kPrepThreads / 64) + wave;
@@ -195,20 +261,36 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
   }
   const bf16_t *x = X + t * K, *w = W + y * K;
   float z = 0.f;
-#pragma unroll 4
-  for (int64_t at = 8 * lane; at < (K + 127) / 128 * 128; at += 512) {
-    u32x4_t xv = u32x4_t{0u, 0u, 0u, 0u}, wv = xv;
-    if (at < K) {
-      xv = *reinterpret_cast<const u32x4_t *>(x + at);
-      wv = *reinterpret_cast<const u32x4_t *>(w + at);
-    }
+  const int64_t end = (K + 127) / 128 * 128;
+  auto dot = [&](auto deep) {  // `deep` pieces of 512 columns asked for before the first is used
+    constexpr int D = decltype(deep)::value;
+    for (int64_t at0 = 8 * lane; at0 < end; at0 += 512 * D) {
+      u32x4_t xv[D], wv[D];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      z = fmaf(bf16_lo_to_f32(xv[e]), bf16_lo_to_f32(wv[e]), z);
-      z = fmaf(bf16_hi_to_f32(xv[e]), bf16_hi_to_f32(wv[e]), z);
+      for (int q = 0; q < D; ++q) {
+        const int64_t at = at0 + 512 * q, from = at < K ? at : 0;
+        xv[q] = *reinterpret_cast<const u32x4_t *>(x + from);
+        wv[q] = *reinterpret_cast<const u32x4_t *>(w + from);
+      }
+#pragma unroll
+      for (int q = 0; q < D; ++q) {
+        const int64_t at = at0 + 512 * q;
+        if (at >= K) xv[q] = wv[q] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z = fmaf(bf16_lo_to_f32(xv[q][e]), bf16_lo_to_f32(wv[q][e]), z);
+          z = fmaf(bf16_hi_to_f32(xv[q][e]), bf16_hi_to_f32(wv[q][e]), z);
+        }
+        if (at < end) *reinterpret_cast<u32x4_t *>(Xt + (at / 32 * ldx + t) * 32 + at % 32) = xv[q];
+      }
     }
-    *reinterpret_cast<u32x4_t *>(Xt + (at / 32 * ldx + t) * 32 + at % 32) = xv;
-  }
+  };
+  // (short rows ask for no more than they have: 5719 x 456 took 12.7 us with eight pieces, 8.9 with two; a single row of
+  // 4096 5.7 us with four, 4.1 with eight)
+  if (end <= 1024)
+    dot(std::integral_constant<int, 2>());
+  else
+    dot(std::integral_constant<int, 8>());
   z = wave_sum(z);
   if (lane == 0) {
     rows.ref[t] = z;
@@ -224,64 +306,18 @@ __global__ __launch_bounds__(kListThreads) void k_head_list(int64_t T, int64_t K
   number_rows<kListThreads>(T, K, [&](int64_t t) { return refcol[t] >= 0; }, n, list, ranges, blocks);
 }
 
-// One workgroup per tile of rows: a counting sort of its targets by output tile.  (The order within an output tile is
-// that of the LDS counters; every target's logit goes to a place of its own, so no result depends on it.)
+// One workgroup per tile of rows of the block.
 constexpr int kBucketThreads = 1024;
-__global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, int64_t row0, int64_t tb, int tile_rows,
-                                                                const int32_t *__restrict__ index, int k, int64_t V,
-                                                                int ntile, int tile_cols, int64_t T, int64_t K,
-                                                                int32_t *n_out, int32_t *list, int32_t *ranges,
-                                                                HeadBlocks blocks) {
+__global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, int64_t row0, int64_t tb, int tile_cols,
+                                                                int ntile, const int32_t *__restrict__ index, int k,
+                                                                int64_t V) {
   extern __shared__ int s_count[];  // [ntile]
-  __shared__ int s_wave[kBucketThreads / 64];
-  if (n_out) {  // one tile of rows: this workgroup numbers them
-    number_rows<kBucketThreads>(T, K, [&](int64_t t) { return rows.refcol[t] >= 0; }, n_out, list, ranges, blocks);
-    __syncthreads();
-  }
-  int64_t n = *(volatile const int32_t *)rows.n - row0;
+  int64_t n = *rows.n - row0;
   n = n < tb ? n : tb;
-  const int64_t n0 = (int64_t)blockIdx.x * tile_rows;
+  const int64_t n0 = (int64_t)blockIdx.x * rows.tile_rows;
   if (n0 >= n) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int have = (int)(n - n0 < tile_rows ? n - n0 : tile_rows) * k;
-  for (int i = tid; i < ntile; i += kBucketThreads) s_count[i] = 0;
-  __syncthreads();
-  auto each = [&](auto use) {
-#pragma unroll 4
-    for (int e = tid; e < have; e += kBucketThreads) {
-      const int nj = e / k, j = e - nj * k;
-      const int64_t v = index[(int64_t)((volatile const int32_t *)rows.list)[row0 + n0 + nj] * k + j];
-      if (target_ok(v, V)) use((int)v, nj, j);
-    }
-  };
-  each([&](int v, int, int) { atomicAdd(&s_count[v / tile_cols], 1); });
-  __syncthreads();
-  // exclusive sums over the tiles, a run of `per` of them per thread
-  const int per = (ntile + kBucketThreads - 1) / kBucketThreads, i0 = tid * per;
-  int mine = 0;
-  for (int i = i0; i < i0 + per && i < ntile; ++i) mine += s_count[i];
-  int before = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int up = __shfl_up(before, o);
-    if (lane >= o) before += up;
-  }
-  if (lane == 63) s_wave[wave] = before;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) before += s_wave[w];
-  int at = before - mine;
-  int32_t *bucket = rows.bucket + (int64_t)blockIdx.x * (ntile + 1);
-  for (int i = i0; i < i0 + per && i < ntile; ++i) {
-    const int c = s_count[i];
-    bucket[i] = s_count[i] = at;
-    at += c;
-  }
-  if (i0 < ntile && i0 + per >= ntile) bucket[ntile] = at;
-  __syncthreads();
-  uint32_t *target = rows.target + (int64_t)blockIdx.x * tile_rows * k;
-  each([&](int v, int nj, int j) {
-    target[atomicAdd(&s_count[v / tile_cols], 1)] = (uint32_t)j | (uint32_t)(v % tile_cols) << 8 | (uint32_t)nj << 16;
-  });
+  sort_targets<kBucketThreads>(rows, blockIdx.x, row0 + n0, (int)(n - n0 < rows.tile_rows ? n - n0 : rows.tile_rows),
+                               rows.tile_rows, tile_cols, ntile, index, k, V, s_count);
 }
 
 // A workgroup per counted row and 2048 columns: z from the ranges' sums, in order, then what the product's epilogue does with it (see
@@ -435,7 +471,12 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
       const int me = i0 + lane;
       const int32_t v = me < k ? index[t * k + me] : -1;
       float P = 0.f;  // all of the row's probability at this column
-      for (int j = 0; j < k; ++j) P += index[t * k + j] == v ? rows.pt[t * k + j] : 0.f;
+      for (int j0 = 0; j0 < k; j0 += 64) {
+        const int32_t vj = j0 + lane < k ? index[t * k + j0 + lane] : -1;
+        const float pj = j0 + lane < k ? rows.pt[t * k + j0 + lane] : 0.f;
+        for (int j = 0; j < min(64, k - j0); ++j)
+          P += __builtin_amdgcn_readlane(vj, j) == v ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pj), j)) : 0.f;
+      }
       if (!target_ok(v, V)) continue;
       const float g = v == rc ? eref * (1.f - P) - P * rest : exp2f((rows.zt[t * k + me] - u) * c) - P * S;
       if (v == rc)
@@ -543,8 +584,10 @@ hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t
                             int32_t *ranges, const HeadBlocks &blocks, const HeadRows &rows, float *loss, bf16_t *dX,
                             bf16_t *Xt, int64_t ldx, hipStream_t s) {
   const int64_t wgs = (T + kPrepThreads / 64 - 1) / (kPrepThreads / 64);
-  launch(k_head_prep, dim3((unsigned)(1 + wgs)), dim3(kPrepThreads), 0, s, X, T, W, V, K, labels, index, logit, k, tau,
-         n, list, ranges, blocks, rows, loss, dX, Xt, ldx);
+  const int tc = head_tile_cols(blocks.tile_rows), ntile = (int)((V + tc - 1) / tc);
+  const bool sorts = rows.target && head_few_targets(T, k, blocks.tile_rows);
+  launch(k_head_prep, dim3((unsigned)(1 + wgs)), dim3(kPrepThreads), sorts ? (uint32_t)ntile * 4 : 0u, s, X, T, W, V, K,
+         labels, index, logit, k, tau, n, list, ranges, blocks, rows, tc, ntile, loss, dX, Xt, ldx);
   return hipGetLastError();
 }
 
@@ -555,13 +598,11 @@ hipError_t launch_head_list(const HeadRows &rows, int64_t T, int64_t K, int32_t 
 }
 
 hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, const int32_t *index, int k, int64_t V,
-                              int64_t T, int64_t K, int32_t *n, int32_t *list, int32_t *ranges,
-                              const HeadBlocks &blocks, hipStream_t s) {
+                              hipStream_t s) {
   const int tr = rows.tile_rows, tc = head_tile_cols(tr);
   const int64_t ntile = (V + tc - 1) / tc;
   launch(k_head_bucket, dim3((unsigned)((tb + tr - 1) / tr)), dim3(kBucketThreads), (uint32_t)ntile * 4, s, rows, row0,
-         tb, tr, index, k, V, (int)ntile, tc, T, K, head_one_tile(T, rows) ? n : (int32_t *)nullptr, list,
-         ranges, blocks);
+         tb, tc, (int)ntile, index, k, V);
   return hipGetLastError();
 }
 
