@@ -435,8 +435,8 @@ struct HeadPlan {
 HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw) {
   HeadPlan p;
   const bool grad = dx || dw;
-  // (a block holds at least 256 rows where there are several, so the tile follows from T)
-  p.b.tile_rows = head_tile_rows(T);
+  // (a block holds at least 256 rows where there are several, and then the vocabulary is wide: the tile follows from T, V)
+  p.b.tile_rows = head_tile_rows(T, V);
   p.ntile = ceil_div(V, kHeadStat);
   const int64_t tiles = ceil_div(V, head_tile_cols(p.b.tile_rows));
   p.b.lde = ceil_div(V, kHeadPad) * kHeadPad;
@@ -455,7 +455,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
     return at;
   };
   p.off_n = take(4);
-  p.off_ranges = take((size_t)p.b.count * 8);
+  p.off_ranges = take((size_t)p.b.count * 16);
   p.off_xt = take((size_t)ceil_div(K, 128) * p.ldx * 256);
   p.off_list = take((size_t)T * 4);
   p.off_ref = take((size_t)T * 4);
@@ -550,7 +550,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   if (k > 0 && !few) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, rg, p.b, s));
   for (int64_t b = 0; b < p.b.count; ++b) {
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
-    rows.ranges = ranges + 2 * b;
+    rows.ranges = ranges + 4 * b;
     if (tb > 0 && sorted && !few) LAUNCH("head_bucket", launch_head_bucket(rows, row0, tb, index, k, V, s));
     if (tb > 0)
       LAUNCH("head_logits", launch_head_logits(rows, row0, tb, Xt, p.ldx, W, V, K, c, stat, p.ntile, E, lde, te, k,

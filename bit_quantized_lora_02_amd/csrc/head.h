@@ -16,7 +16,8 @@ typedef uint16_t bf16_t;
 // and E[v] = exp2((z[v] - u) c) is what is kept of logit v.
 struct HeadRows {
   const int32_t *n;       // rows that count
-  const int32_t *ranges;  // the dX product's ranges for the block at hand: of its whole tiles, of the rows behind them
+  const int32_t *ranges;  // the dX product's for the block at hand: ranges of its first rows, of the others (which take
+                          // 128-row tiles), number of first rows
   int tile_rows;          // rows of the products' tiles
   const int32_t *list;  // [T] their rows in X
   float *ref;           // [T] by row of X: the logit of the row's first target
@@ -36,9 +37,14 @@ constexpr float kHeadRange = 1.0995116e12f;  // 2^40
 constexpr int kHeadStat = 64;
 __host__ __device__ inline int head_stat_cols(bool wide_tile) { return wide_tile ? 128 : kHeadStat; }
 
-// Rows of X per tile of the three products, by the rows of a block (one choice for all blocks of a call).
-// Few rows take narrow tiles: the padding rows' MFMA work would cost more than the wider tile's operand reuse gains.
-inline int head_tile_rows(int64_t tb) { return tb <= 64 ? 64 : tb <= 128 ? 128 : 256; }
+// Rows of X per tile of the logit and dX products.  Few rows take narrow tiles: the padding rows' MFMA work would cost
+// more than the wider tile's operand reuse gains.  So do small outputs, whose 256-wide tiles would not occupy half of the
+// chip: a 128-row tile takes 0.6 of the time of a 256-row one (1910 x 1890 x 3232: logits with their sums 50 us in
+// 256-row tiles, 44 in 128-row ones; 600 x 8000 x 2048: 46 and 32; but 512 x 32000 x 4096, 250 tiles: 115 and 159).
+inline int head_tile_rows(int64_t T, int64_t V) {
+  if (T <= 64) return 64;
+  return T <= 128 || (V + 255) / 256 * ((T + 255) / 256) <= 128 ? 128 : 256;
+}
 // Columns of a tile (of the vocabulary in the logit product, of X in the dX product).
 // Up to 64 rows the products are bound by the stream of W, and the smaller tile gives every CU some of it.
 __host__ __device__ inline int head_tile_cols(int tile_rows) { return tile_rows == 64 ? 128 : 256; }
@@ -48,24 +54,25 @@ __host__ __device__ inline int head_tile_cols(int tile_rows) { return tile_rows 
 constexpr int kHeadRanges = 32, kHeadSlots64 = 768;
 
 // Ranges of the logit product's reduction over K for T rows: more than one where the output has too few tiles to
-// occupy the chip (a small vocabulary, few rows).  In microseconds: a 32-deep step takes 0.8 in a 256-wide tile however
-// few there are; in a 128-wide one 0.25 and 0.001 for each workgroup that shares the memory, from about 450 of them on
-// their 8 KB of W at 5.3 TB/s (250 workgroups 0.51, 375 0.71, 750 1.16).  Splitting costs a launch, about 5, and the
-// binary32 sums, written and read once at about 4.5 TB/s.  (16 x 32000 x 4096: 55 us in three ranges, 66 in one;
-// 60 x 48000 x 4096: 107 in two, 91 in one.)
+// occupy the chip (a small vocabulary, few rows).  In microseconds: a 32-deep step of a 64-row tile takes 0.25 and 0.001
+// for each workgroup that shares the memory, from about 450 of them on their 8 KB of W at 5.3 TB/s (250 workgroups 0.51,
+// 375 0.71, 750 1.16); one of a 128-row tile 0.5 and 0.002 for each that streams other rows of W (T = 100: 125 workgroups
+// 0.7, 250 1.0; T = 1910: 240 0.6).  Splitting costs a launch, about 5, and the binary32 sums, written and read once
+// at about 4.5 TB/s.  (16 x 32000 x 4096: 57 us in two ranges, 60 in one; 64 x 64000 x 4096: 111 in two, 96 in one.)
 inline int head_logit_ranges(int64_t T, int64_t V, int64_t K, int tile_rows) {
-  const int64_t cols = head_tile_cols(tile_rows), tiles = (V + cols - 1) / cols * ((T + tile_rows - 1) / tile_rows);
+  const int64_t cols = head_tile_cols(tile_rows), tiles_m = (V + cols - 1) / cols;
+  const int64_t tiles = tiles_m * ((T + tile_rows - 1) / tile_rows);
   const int64_t slots = tile_rows == 64 ? kHeadSlots64 : 256, fours = (K + 127) / 128;
-  if (tiles * 2 > slots) return 1;
-  auto step = [&](int64_t wgs) {
-    const float some = 0.25f + 0.001f * (float)wgs, many = 0.00155f * (float)wgs;
-    return tile_rows == 64 ? (some > many ? some : many) : 0.8f;
+  if (tile_rows == 256 || tiles * 2 > slots) return 1;
+  auto step = [&](int s) {
+    const float streams = (float)(tiles_m * s), some = 0.25f + 0.001f * streams, many = 0.00155f * streams;
+    return tile_rows == 128 ? 0.5f + 0.002f * streams : some > many ? some : many;
   };
   const float sums = (float)(T * V) * 8.f / 4.5e6f;
   int best = 1;
-  float least = 4.f * (float)fours * step(tiles);
+  float least = 4.f * (float)fours * step(1);
   for (int s = 2; s <= 16 && s <= fours && tiles * s <= slots; ++s) {
-    const float cost = 4.f * (float)((fours + s - 1) / s) * step(tiles * s) + 5.f + sums * (float)s;
+    const float cost = 4.f * (float)((fours + s - 1) / s) * step(s) + 5.f + sums * (float)s;
     if (cost < least) least = cost, best = s;
   }
   const int64_t per = (fours + best - 1) / best;
@@ -123,7 +130,7 @@ __host__ __device__ inline int head_whole_columns(int64_t V, int tiles_m) {
   const int tiles = (int)((V + 255) / 256), rounds = (int)((int64_t)tiles * tiles_m / 256);
   const int64_t rest = (int64_t)tiles * tiles_m - (int64_t)rounds * 256;
   const int keep = (int)((int64_t)rounds * 256 / tiles_m);
-  return rounds > 0 && keep > 0 && rest >= 1 && rest <= 128 && keep * 256 < V ? keep * 256 : (int)V;
+  return rest >= 1 && rest <= 128 && keep * 256 < V ? keep * 256 : (int)V;
 }
 
 // The dX product's partial sums: of the whole tiles' rows first, where they have any.

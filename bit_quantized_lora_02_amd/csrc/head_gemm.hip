@@ -259,8 +259,7 @@ struct Items {
   }
 };
 
-// A kernel whose rows do not fill whole 256-row tiles gives the last 128 or fewer to narrower tiles, in a second pass
-// over items.  The workgroups that had one item less in the first pass take them, where that is at most two each
+// A kernel whose rows do not fill whole 256-row tiles gives the last of them to narrower tiles, in a second pass over items.  The workgroups that had one item less in the first pass take them, where that is at most two each
 // (a narrow item takes 0.6 of the time of a wide one), else all of them.
 struct Turn {
   uint32_t lin, stride;
@@ -706,15 +705,15 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(DxArgs g) {
   QLORA_RING(C, ring);
   const int n = block_rows(g.rows, g.row0, g.tb);
   if (n == 0) return;
-  const int tiles_m = (int)((g.K + C::BM - 1) / C::BM), ranges = g.rows.ranges[0], more = g.rows.ranges[1];
-  const int whole = more > 0 ? head_whole_rows(n, C::BN) : n;
+  const int tiles_m = (int)((g.K + C::BM - 1) / C::BM), ranges = g.rows.ranges[0], whole = g.rows.ranges[2];
   Items items = {tiles_m, (whole + C::BN - 1) / C::BN, ranges};
   if (whole > 0) dx_items<C>(g, 0, whole, ranges, g.part, items, Turn{blockIdx.x, gridDim.x}, ring);
   if constexpr (C::BN == 256) {
     if (whole == n) return;
-    const Turn turn = second_pass(items, (uint32_t)(tiles_m * more));
+    const int narrow = (n - whole + H128::BN - 1) / H128::BN, more = g.rows.ranges[1];
+    const Turn turn = second_pass(items, (uint32_t)(tiles_m * narrow * more));
     between_passes();
-    items = {tiles_m, 1, more};
+    items = {tiles_m, narrow, more};
     dx_items<H128>(g, whole, n, more, g.part + head_first_sums(whole, ranges, g.K), items, turn, ring);
   }
 }
@@ -797,7 +796,7 @@ __global__ __launch_bounds__(H256::NT) void k_head_dw(DwArgs g) {
   QLORA_RING(H256, ring);
   const int tiles_m = (int)((g.K + 255) / 256), whole = head_whole_columns(g.V, tiles_m);
   Items items = {tiles_m, (whole + 255) / 256, 1};
-  dw_items<H256>(g, 0, whole, items, Turn{blockIdx.x, gridDim.x}, ring);
+  if (whole > 0) dw_items<H256>(g, 0, whole, items, Turn{blockIdx.x, gridDim.x}, ring);
   if (whole == g.V) return;
   const int narrow = ((int)g.V - whole + H128::BN - 1) / H128::BN;
   const Turn turn = second_pass(items, (uint32_t)(tiles_m * narrow));
@@ -826,9 +825,9 @@ hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, co
                               const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E,
                               int64_t lde, int64_t te, int k, int ranges, float *part, hipStream_t s) {
   const int64_t cols = head_tile_cols(rows.tile_rows), tiles = (V + cols - 1) / cols;
-#define QLORA_CALL(CFG)                                                                                               \
-  launch(ranges > 1 ? k_head_logits<CFG, true> : k_head_logits<CFG, false>,                                           \
-         dim3((unsigned)groups(tiles * ((tb + CFG::BN - 1) / CFG::BN) * ranges, CFG::BN)), dim3(CFG::NT), 0, s,       \
+#define QLORA_CALL(CFG)                                                                                            \
+  launch(CFG::BN < 256 && ranges > 1 ? k_head_logits<CFG, CFG::BN < 256> : k_head_logits<CFG, false>,              \
+         dim3((unsigned)groups(tiles * ((tb + CFG::BN - 1) / CFG::BN) * ranges, CFG::BN)), dim3(CFG::NT), 0, s,    \
          LogitArgs{rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, (int)tiles, ranges, part, E, lde, te, k})
   QLORA_HEAD_TILES(rows, QLORA_CALL)
 #undef QLORA_CALL
@@ -839,7 +838,7 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
                           const bf16_t *W, int64_t V, int64_t K, const float4 *scale, float *part, bf16_t *dX,
                           hipStream_t s) {
   const int tr = rows.tile_rows, tc = head_tile_cols(tr);
-  const int64_t most = (tb + tr - 1) / tr * ((K + tc - 1) / tc) * kHeadRanges;
+  const int64_t most = (tb + 127) / 128 * ((K + tc - 1) / tc) * kHeadRanges;  // (all rows may take 128-row tiles)
 #define QLORA_CALL(CFG)                                                                                              \
   launch(k_head_dx<CFG>, dim3((unsigned)groups(most, CFG::BN)), dim3(CFG::NT), 0, s, \
          DxArgs{rows, row0, tb, E, lde, te, W, V, K, scale, part, dX})
@@ -851,7 +850,9 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,
                           hipStream_t s) {
-  launch(k_head_dw, dim3((unsigned)groups(((K + 255) / 256) * ((V + 255) / 256), 256)), dim3(H256::NT), 0, s,
+  const int64_t tiles_m = (K + 255) / 256, whole = head_whole_columns(V, (int)tiles_m);
+  const int64_t items = tiles_m * (whole > 0 ? (whole + 255) / 256 : (V + H128::BN - 1) / H128::BN);
+  launch(k_head_dw, dim3((unsigned)groups(items, 256)), dim3(H256::NT), 0, s,
          DwArgs{rows, row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, dW});
   return hipGetLastError();
 }

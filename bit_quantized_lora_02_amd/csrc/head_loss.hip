@@ -40,17 +40,18 @@ __device__ __forceinline__ bool target_ok(int64_t v, int64_t V) { return v >= 0 
 
 // Reduction ranges of the dX product, by one wave: `tiles` output tiles of `steps` 64-deep steps on `slots` workgroups
 // that run at once, lane s - 1 looking at s ranges.  A round of workgroups costs its steps plus about 10 (first
-// loads, output); more than one range also costs the binary32 partial sums, written and read once: about 33 steps'
-// time for 256 tiles of 256 x 256.
+// loads, output), a 128-row tile's 0.6 of a 256-row one's; more than one range also costs the binary32 partial sums,
+// written and read once: about 33 steps' time for 256 tiles of 256 x 256.
 struct Split {
   int ranges;
   float cost;  // in steps
 };
-__device__ __forceinline__ Split wave_split(int tiles, int steps, int slots, int tile_elems, int lane) {
-  const int s = (lane & (kHeadRanges - 1)) + 1;
+__device__ __forceinline__ Split wave_split(int tiles, int steps, int tile_rows, int lane) {
+  const int s = (lane & (kHeadRanges - 1)) + 1, slots = tile_rows == 64 ? kHeadSlots64 : 256;
   const int rounds = (tiles * s + slots - 1) / slots;
-  float cost = (float)rounds * ((float)steps / (float)s + 10.f) +
-               (s > 1 ? 33.f * (float)tile_elems / (256.f * 65536.f) * (float)(tiles * s) : 0.f);
+  const float elems = (float)(tile_rows * head_tile_cols(tile_rows));
+  float cost = (float)rounds * ((float)steps / (float)s + 10.f) * (tile_rows == 128 ? 0.6f : 1.f) +
+               (s > 1 ? 33.f * elems / (256.f * 65536.f) * (float)(tiles * s) : 0.f);
   if (s > 1 && (steps < 8 * s || tiles * s > 4 * slots)) cost = INFINITY;
   Split best = {s, cost};
 #pragma unroll
@@ -61,28 +62,28 @@ __device__ __forceinline__ Split wave_split(int tiles, int steps, int slots, int
   return best;
 }
 
-// Ranges for n rows: of their tiles, and of the rows behind the last whole tile where those take narrower ones (0:
-// they do not).  All of the same length but the last, none empty.
+// For n rows: the first of them in tiles of tile_rows, the others in tiles of 128 rows where tile_rows is 256 (the rows
+// behind the last whole tile, or, of few tiles, all: 300 x 32000 x 4096 with the sums 120 us in 256-row tiles, 101 in
+// 128-row ones), and the ranges of both, all of the same length but the last, none empty (0: no such rows).
 __device__ __forceinline__ void dx_ranges(int n, int64_t K, int64_t lde, int tile_rows, int lane, int32_t *out) {
   const int cols = head_tile_cols(tile_rows), tiles_m = (int)((K + cols - 1) / cols), fours = (int)(lde / 128);
-  const int slots = tile_rows == 64 ? kHeadSlots64 : 256, whole = head_whole_rows(n, tile_rows);
-  Split one = wave_split((n + tile_rows - 1) / tile_rows * tiles_m, fours * 2, slots, cols * tile_rows, lane);
-  int second = 0;
-  if (whole < n) {
-    const Split two = wave_split(tiles_m, fours * 2, slots, cols * 128, lane);
-    Split rest = {1, 0.f};
-    if (whole > 0) rest = wave_split(whole / tile_rows * tiles_m, fours * 2, slots, cols * tile_rows, lane);
-    if (rest.cost + 0.6f * two.cost < one.cost) {
-      one = rest;
-      const int per = (fours + two.ranges - 1) / two.ranges;
-      second = (fours + per - 1) / per;
+  auto split = [&](int rows, int tr) { return wave_split((rows + tr - 1) / tr * tiles_m, fours * 2, tr, lane); };
+  Split first = split(n, tile_rows), second = {0, 0.f};
+  int whole = n;
+  if (tile_rows == 256) {
+    const int some = head_whole_rows(n, 256);
+    if (some < n && some > 0) {
+      const Split a = split(some, 256), b = split(n - some, 128);
+      if (a.cost + b.cost < first.cost) first = a, first.cost += b.cost, second = b, whole = some;
     }
+    const Split all = split(n, 128);
+    if (all.cost < first.cost) first = {0, 0.f}, second = all, whole = 0;
   }
-  const int per = (fours + one.ranges - 1) / one.ranges;
-  if (lane == 0) {
-    out[0] = (fours + per - 1) / per;
-    out[1] = second;
-  }
+  auto even = [&](int r) {
+    const int per = r > 0 ? (fours + r - 1) / r : 1;
+    return r > 0 ? (fours + per - 1) / per : 0;
+  };
+  if (lane == 0) out[0] = even(first.ranges), out[1] = even(second.ranges), out[2] = whole;
 }
 
 // Numbers the rows with counts(t), in order, by one workgroup of `threads`; then the blocks' dX ranges.
@@ -124,7 +125,7 @@ __device__ __forceinline__ void number_rows(int64_t T, int64_t K, Counts counts,
   for (int64_t b = wave; ranges && b < blocks.count; b += threads / 64) {
     const int64_t row0 = b * blocks.tb, tb = T - row0 < blocks.tb ? T - row0 : blocks.tb;
     const int64_t have = base - row0 < tb ? base - row0 : tb;
-    if (have > 0) dx_ranges((int)have, K, blocks.lde, blocks.tile_rows, lane, ranges + 2 * b);
+    if (have > 0) dx_ranges((int)have, K, blocks.lde, blocks.tile_rows, lane, ranges + 4 * b);
   }
 }
 
@@ -320,8 +321,9 @@ __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, i
                                rows.tile_rows, tile_cols, ntile, index, k, V, s_count);
 }
 
-// A workgroup per counted row and 2048 columns: z from the ranges' sums, in order, then what the product's epilogue does with it (see
-// logit_items), a lane taking eight columns.
+// A workgroup per counted row and 2048 columns: z from the ranges' sums, in order, then what the product's epilogue does
+// with it (see logit_items), a lane taking eight columns.
+// (Only narrow tiles' reductions are split: every entry of the statistics is of kHeadStat columns.)
 __global__ __launch_bounds__(256) void k_head_soft(HeadRows rows, int64_t row0, int64_t tb,
                                                    const float *__restrict__ part, int ranges, int64_t V, float c,
                                                    float2 *__restrict__ stat, int64_t ntile,
@@ -344,7 +346,6 @@ __global__ __launch_bounds__(256) void k_head_soft(HeadRows rows, int64_t row0, 
       for (int r = 0; r < ranges; ++r) z += p[(int64_t)r * n * lde + v];
     rows.zt[t * k + j] = z;
   }
-  const int cols = head_stat_cols(rows.tile_rows == 256 && i < head_whole_rows((int)n, 256)), group = cols / 8;
   const int64_t v = ((int64_t)blockIdx.y * 256 + tid) * 8;
   const bool in = v < lde;  // lde % 128 == 0: a group's lanes are all in or all out
   float z[8], e[8], sum = 0.f;
@@ -364,14 +365,14 @@ __global__ __launch_bounds__(256) void k_head_soft(HeadRows rows, int64_t row0, 
     e[q] = __builtin_amdgcn_exp2f(fmaf(z[q], c, -uc));
     sum += e[q];
   }
-  for (int o = 1; o < group; o <<= 1) sum += __shfl_xor(sum, o);
+  for (int o = 1; o < kHeadStat / 8; o <<= 1) sum += __shfl_xor(sum, o);
   float u = ref;
   const bool over = !(sum < kHeadRange);
   if (__any(over)) {
     float top = z[0];
 #pragma unroll
     for (int q = 1; q < 8; ++q) top = fmaxf(top, z[q]);
-    for (int o = 1; o < group; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    for (int o = 1; o < kHeadStat / 8; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
     u = over ? top : ref;
     sum = 0.f;
 #pragma unroll
@@ -379,9 +380,9 @@ __global__ __launch_bounds__(256) void k_head_soft(HeadRows rows, int64_t row0, 
       e[q] = __builtin_amdgcn_exp2f((z[q] - u) * c);
       sum += e[q];
     }
-    for (int o = 1; o < group; o <<= 1) sum += __shfl_xor(sum, o);
+    for (int o = 1; o < kHeadStat / 8; o <<= 1) sum += __shfl_xor(sum, o);
   }
-  if (v < V && lane % group == 0) stat[i * ntile + v / cols] = make_float2(u, sum);
+  if (v < V && lane % (kHeadStat / 8) == 0) stat[i * ntile + v / kHeadStat] = make_float2(u, sum);
   if (E && in)
     *reinterpret_cast<u32x4_t *>(E + (v / 32 * te + i) * 32 + v % 32) =
         u32x4_t{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])};
@@ -550,7 +551,7 @@ __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0
   const int64_t per = K / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= n * per) return;
   const int64_t i = at / per, col = (at % per) * 8;
-  const int whole = rows.ranges[1] > 0 ? head_whole_rows((int)n, rows.tile_rows) : (int)n;
+  const int whole = rows.ranges[2];
   const bool second = i >= whole;
   const int ranges = rows.ranges[second];
   if (ranges == 1) return;  // the product wrote dX itself
