@@ -430,6 +430,7 @@ struct HeadPlan {
          off_stat = 0, off_scale = 0, off_z = 0, off_e = 0, off_part = 0, off_xs = 0, off_sums = 0, total = 0;
   bool split = false;  // dX may come as partial sums
   int ranges = 1;      // of the logit product's reduction
+  int dw_ranges = 1;   // of the dW product's
 };
 
 HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw) {
@@ -479,7 +480,8 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   }
   if (dw) {
     p.off_xs = take(up((size_t)p.b.tb, 128) * K * 2);
-    if (p.b.count > 1) p.off_sums = take((size_t)V * K * 4);
+    p.dw_ranges = head_dw_ranges(T, V, K, p.b.count);
+    if (p.b.count > 1 || p.dw_ranges > 1) p.off_sums = take((size_t)V * K * p.dw_ranges * 4);
   }
   p.total = off;
   return p;
@@ -570,7 +572,10 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
     }
     if (dW)
       LAUNCH("head_dw",
-             launch_head_dw(rows, row0, tb, E, lde, te, Xs, V, K, sums, b == 0, b + 1 == p.b.count, dW, s));
+             launch_head_dw(rows, row0, tb, E, lde, te, Xs, V, K, sums, b == 0, b + 1 == p.b.count && p.dw_ranges == 1,
+                            p.dw_ranges, dW, s));
+    if (dW && p.dw_ranges > 1)
+      LAUNCH("head_dw_reduce", launch_head_dw_reduce(rows, tb, sums, p.dw_ranges, V, K, dW, s));
   }
   return QLORA_OK;
 }

@@ -133,6 +133,26 @@ __host__ __device__ inline int head_whole_columns(int64_t V, int tiles_m) {
   return rest >= 1 && rest <= 128 && keep * 256 < V ? keep * 256 : (int)V;
 }
 
+// Ranges of the dW product's reduction over T rows (one block of them): more than one where even the narrow tiles leave
+// half of the chip idle (a small W).  In microseconds, as for the logits: 0.5 a step, a launch, the binary32 sums.
+inline int head_dw_ranges(int64_t T, int64_t V, int64_t K, int64_t blocks) {
+  const int64_t tiles_m = (K + 255) / 256, tiles = tiles_m * ((V + 127) / 128), fours = (T + 127) / 128;
+  if (blocks > 1 || tiles * 2 > 256) return 1;
+  const float sums = (float)(V * K) * 8.f / 4.5e6f;
+  int best = 1;
+  float least = 2.f * (float)fours;
+  for (int s = 2; s <= fours && tiles * s <= 256; ++s) {
+    const float cost = 2.f * (float)((fours + s - 1) / s) + 5.f + sums * (float)s;
+    if (cost < least) least = cost, best = s;
+  }
+  return best;
+}
+// Those of n counted rows: all of the same length but the last, none empty.
+__host__ __device__ inline int head_dw_steps(int n, int ranges) {  // 128-row steps of one
+  const int deep = n > 128 ? (n + 127) / 128 : 1;
+  return (deep + ranges - 1) / ranges;
+}
+
 // The dX product's partial sums: of the whole tiles' rows first, where they have any.
 __host__ __device__ inline int64_t head_first_sums(int64_t whole, int ranges, int64_t K) {
   return ranges > 1 ? ranges * whole * K : 0;
@@ -155,7 +175,10 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
                           const bf16_t *W, int64_t V, int64_t K, const float4 *scale, float *part, bf16_t *dX,
                           hipStream_t s);
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
-                          const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,
-                          hipStream_t s);
+                          const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, int ranges,
+                          bf16_t *dW, hipStream_t s);
+// dW from the sums of several ranges.
+hipError_t launch_head_dw_reduce(const HeadRows &rows, int64_t tb, const float *sums, int ranges, int64_t V, int64_t K,
+                                 bf16_t *dW, hipStream_t s);
 
 }  // namespace qlora

@@ -720,7 +720,8 @@ __global__ __launch_bounds__(C::NT) void k_head_dx(DxArgs g) {
 
 // ---------------------------------------------------------------------- dW
 // m: columns of X, n: columns of the vocabulary; reduction over the block's counted rows.  With `sums` (several
-// blocks) the binary32 sums are carried in it from block to block and rounded to dW after the last.
+// blocks) the binary32 sums are carried in it from block to block and rounded to dW after the last; or, with several
+// `ranges` of one block's rows, each range's are left in it ([range][V][K], neither the last) for k_head_dw_reduce.
 struct DwArgs {
   HeadRows rows;
   int64_t row0, tb;
@@ -729,7 +730,7 @@ struct DwArgs {
   const bf16_t *Xs;
   int64_t V, K;
   float *sums;
-  int first, last;
+  int first, last, ranges;
   bf16_t *dW;
 };
 
@@ -738,7 +739,7 @@ template <class C>
 __device__ __forceinline__ void dw_items(const DwArgs &g, int begin_v, int end_v, Items &items, Turn turn,
                                          const Ring &ring) {
   const int64_t K = g.K;
-  float *const sums = g.sums;
+  float *sums = g.sums;
   bf16_t *const dW = g.dW;
   const int n = block_rows(g.rows, g.row0, g.tb);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -749,11 +750,15 @@ __device__ __forceinline__ void dw_items(const DwArgs &g, int begin_v, int end_v
     const int deep = max((n + 127) / 128, 1);
     ta.init(g.Xs, K, (int64_t)items.m * C::BM, K, deep * 128, nullptr, wave, lane);
     tbl.init(g.E, g.te, begin_v + (int64_t)items.n * C::BN, g.lde, max(n, 1), nullptr, wave, lane);
-    *s0 = 0;
-    *s1 = deep * 4;
-    return 0;
+    const int per = head_dw_steps(n, items.ranges);
+    *s0 = items.range * per * 4;
+    *s1 = min(*s0 + per * 4, deep * 4);
+    return *s0;
   };
-  auto begin = [&]() { m0 = items.m * C::BM, n0 = begin_v + items.n * C::BN; };
+  auto begin = [&]() {
+    m0 = items.m * C::BM, n0 = begin_v + items.n * C::BN;
+    if (sums) sums = g.sums + items.range * g.V * K;
+  };
   auto late = []() {};
   auto finish = [&](Acc<C> &acc) {
     arrive<C::LB>();
@@ -799,9 +804,12 @@ __global__ __launch_bounds__(H256::NT) void k_head_dw(DwArgs g) {
   if (whole > 0) dw_items<H256>(g, 0, whole, items, Turn{blockIdx.x, gridDim.x}, ring);
   if (whole == g.V) return;
   const int narrow = ((int)g.V - whole + H128::BN - 1) / H128::BN;
-  const Turn turn = second_pass(items, (uint32_t)(tiles_m * narrow));
+  // (several ranges: the columns all go to narrow tiles)
+  const int n = block_rows(g.rows, g.row0, g.tb), per = head_dw_steps(n, g.ranges);
+  const Items second = {tiles_m, narrow, (max((n + 127) / 128, 1) + per - 1) / per};
+  const Turn turn = second_pass(items, (uint32_t)(tiles_m * narrow * second.ranges));
   between_passes();
-  items = {tiles_m, narrow, 1};
+  items = second;
   dw_items<H128>(g, whole, (int)g.V, items, turn, ring);
 }
 
@@ -848,12 +856,12 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
 }
 
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
-                          const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, bf16_t *dW,
-                          hipStream_t s) {
+                          const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, int ranges,
+                          bf16_t *dW, hipStream_t s) {
   const int64_t tiles_m = (K + 255) / 256, whole = head_whole_columns(V, (int)tiles_m);
-  const int64_t items = tiles_m * (whole > 0 ? (whole + 255) / 256 : (V + H128::BN - 1) / H128::BN);
+  const int64_t items = tiles_m * (whole > 0 ? (whole + 255) / 256 : (V + H128::BN - 1) / H128::BN * ranges);
   launch(k_head_dw, dim3((unsigned)groups(items, 256)), dim3(H256::NT), 0, s,
-         DwArgs{rows, row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, dW});
+         DwArgs{rows, row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, ranges, dW});
   return hipGetLastError();
 }
 

@@ -40,8 +40,8 @@ __device__ __forceinline__ bool target_ok(int64_t v, int64_t V) { return v >= 0 
 
 // Reduction ranges of the dX product, by one wave: `tiles` output tiles of `steps` 64-deep steps on `slots` workgroups
 // that run at once, lane s - 1 looking at s ranges.  A round of workgroups costs its steps plus about 10 (first
-// loads, output), a 128-row tile's 0.6 of a 256-row one's; more than one range also costs the binary32 partial sums,
-// written and read once: about 33 steps' time for 256 tiles of 256 x 256.
+// loads, output), a 128-row tile's 0.57 of a 256-row one's; more than one range also costs the binary32 partial sums,
+// written and read once: about 20 steps' time for 256 tiles of 256 x 256.
 struct Split {
   int ranges;
   float cost;  // in steps
@@ -50,8 +50,8 @@ __device__ __forceinline__ Split wave_split(int tiles, int steps, int tile_rows,
   const int s = (lane & (kHeadRanges - 1)) + 1, slots = tile_rows == 64 ? kHeadSlots64 : 256;
   const int rounds = (tiles * s + slots - 1) / slots;
   const float elems = (float)(tile_rows * head_tile_cols(tile_rows));
-  float cost = (float)rounds * ((float)steps / (float)s + 10.f) * (tile_rows == 128 ? 0.6f : 1.f) +
-               (s > 1 ? 33.f * elems / (256.f * 65536.f) * (float)(tiles * s) : 0.f);
+  float cost = (float)rounds * ((float)steps / (float)s + 10.f) * (tile_rows == 128 ? 0.57f : 1.f) +
+               (s > 1 ? 20.f * elems / (256.f * 65536.f) * (float)(tiles * s) : 0.f);
   if (s > 1 && (steps < 8 * s || tiles * s > 4 * slots)) cost = INFINITY;
   Split best = {s, cost};
 #pragma unroll
@@ -578,6 +578,28 @@ __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0
   *reinterpret_cast<u32x4_t *>(dX + t * K + col) = o;
 }
 
+// dW from the ranges' partial sums [range][V][K], in range order.
+__global__ __launch_bounds__(256) void k_head_dw_reduce(HeadRows rows, int64_t tb, const float *__restrict__ part,
+                                                        int ranges, int64_t count, bf16_t *__restrict__ dW) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (at >= count) return;
+  const int n = min(*rows.n, (int)tb), per = head_dw_steps(n, ranges);
+  ranges = (max((n + 127) / 128, 1) + per - 1) / per;
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = 0.f;
+  const float *p = part + at;
+#pragma unroll 4
+  for (int r = 0; r < ranges; ++r, p += count) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+    s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
+    s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+  }
+  *reinterpret_cast<u32x4_t *>(dW + at) = u32x4_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
+                                                  pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])};
+}
+
 }  // namespace
 
 hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t V, int64_t K, const int64_t *labels,
@@ -629,6 +651,12 @@ hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, co
                               int64_t K, const float4 *scale, bf16_t *dX, hipStream_t s) {
   launch(k_head_reduce, dim3((unsigned)((tb * (K / 8) + 255) / 256)), dim3(256), 0, s, rows, row0, tb, part, W, K,
          scale, dX);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_dw_reduce(const HeadRows &rows, int64_t tb, const float *sums, int ranges, int64_t V, int64_t K,
+                                 bf16_t *dW, hipStream_t s) {
+  launch(k_head_dw_reduce, dim3((unsigned)((V * K / 8 + 255) / 256)), dim3(256), 0, s, rows, tb, sums, ranges, V * K, dW);
   return hipGetLastError();
 }
 

@@ -520,3 +520,27 @@ def test_autograd_captured():
             assert torch.equal(a, b), f"{name} of replay {rep}"
         terms = (want[1] * weight).double()
         assert (want[0].double() - terms.sum()).abs() <= T * U * terms.abs().sum()
+
+
+@pytest.mark.parametrize("T,V,K,ignored", [(1100, 9000, 4104, 0.0), (1024, 9000, 4104, 0.0), (1500, 17000, 4104, 0.1),
+                                           (700, 33000, 520, 0.1), (3000, 1000, 264, 0.3), (5000, 300, 520, 0.0),
+                                           (2000, 130, 1032, 0.95)])
+def test_ways_through_the_products(T, V, K, ignored):
+    """Wide tiles with and without partial sums and with narrow ones behind them, narrow tiles alone, and the sums of dW of
+    a long batch over a small output layer (once with few rows left of it)."""
+    print(f"head_ce and head_distill T={T} V={V} K={K}", flush=True)
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=T + K))
+    drop = torch.rand(T, generator=torch.Generator().manual_seed(T)).cuda() < ignored
+    y = torch.where(drop, -100, y)
+    loss, dX, dW = B.head_ce(X, W, y, weight, need_dw=True)
+    wl, wx, ww, bl, bx, bw = reference(X, W, *ce_targets(y, V), weight, 1.0)
+    check("loss", loss, wl, bl)
+    check("dX", dX, wx, bx)
+    check("dW", dW, ww, bw)
+    index = torch.stack([y, torch.where(drop, -1, (y + 7) % V)], 1).to(torch.int32)
+    logit = torch.randn(T, 2, device="cuda")
+    loss, dX, dW = B.head_distill(X, W, index, logit, 2.0, weight, need_dw=True)
+    wl, wx, ww, bl, bx, bw = reference(X, W, *kd_targets(index, logit, V, 2.0), weight, 2.0)
+    check("loss", loss, wl, bl)
+    check("dX", dX, wx, bx)
+    check("dW", dW, ww, bw)
