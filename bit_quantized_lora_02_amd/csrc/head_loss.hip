@@ -488,11 +488,17 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
     }
   }
   if (Xs)  // rows of X times the row factor's power of two, exactly (k_head_scale gives E the rest of the factor)
-    for (int64_t at = 8 * lane; at < K; at += 512) {
-      u32x4_t v = *reinterpret_cast<const u32x4_t *>(X + t * K + at);
+    for (int64_t at0 = 8 * lane; at0 < K; at0 += 512 * 4) {
+      u32x4_t v[4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) v[w] = pack_bf16x2(ldexpf(bf16_lo_to_f32(v[w]), ex), ldexpf(bf16_hi_to_f32(v[w]), ex));
-      *reinterpret_cast<u32x4_t *>(Xs + i * K + at) = v;
+      for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const u32x4_t *>(X + t * K + (at0 + 512 * q < K ? at0 + 512 * q : 0));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          v[q][w] = pack_bf16x2(ldexpf(bf16_lo_to_f32(v[q][w]), ex), ldexpf(bf16_hi_to_f32(v[q][w]), ex));
+        if (at0 + 512 * q < K) *reinterpret_cast<u32x4_t *>(Xs + i * K + at0 + 512 * q) = v[q];
+      }
     }
 }
 
