@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["abi.hip", "quant.hip", "nf4_gemm.hip", "nf4_gemv.hip", "lora_gemm.hip", "adamw.hip", "merge.hip",
-           "head_gemm.hip", "head_loss.hip"]
+           "head_abi.hip", "head_gemm.hip", "head_loss.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
