@@ -165,8 +165,9 @@ inline size_t head_part_floats(int64_t tb, int64_t K, int tile_rows) {
   return all < most ? all : most;
 }
 
-hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx, const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile,
-                              bf16_t *E, int64_t lde, int64_t te, int k, int ranges, float *part, hipStream_t s);
+hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *Xt, int64_t ldx,
+                              const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E,
+                              int64_t lde, int64_t te, int k, int ranges, float *part, hipStream_t s);
 // Where the logits came as the partial sums of several ranges: their statistics, E, and the targets' logits.
 hipError_t launch_head_soft(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int ranges, int64_t V,
                             float c, float2 *stat, int64_t ntile, const int32_t *index, int k, bf16_t *E, int64_t lde,

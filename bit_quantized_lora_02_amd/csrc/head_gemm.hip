@@ -8,14 +8,21 @@
 //
 // One kernel body serves all three: C[n][m] = sum_r A(m, r) B(n, r), the operands read from global memory either
 // along the reduction ("rows": [m][r]) or across it ("transposed": [r][m]).  A workgroup of 4 or 8 waves computes a
-// 256 x BN tile with v_mfma_f32_32x32x16_bf16; m is the MFMA's row index, so a lane holds four consecutive m of
-// one n, which makes the softmax statistics of a row of X (n) a reduction inside the lane.  The reduction runs in
-// 32-deep steps over a ring of four LDS tiles that the load unit fills directly (16 bytes per lane, see
-// reduce_steps).
+// 256 x 256, 256 x 128 or 128 x 64 tile (m x n) with v_mfma_f32_32x32x16_bf16; m is the MFMA's row index, so a lane holds
+// four consecutive m of one n, which makes the softmax statistics of a row of X (n) a reduction inside the lane.  The
+// reduction runs in 32-deep steps over a ring of four LDS tiles that the load unit fills directly (16 bytes per lane, see
+// products).
 //
-// LDS tiles: "rows" [row][32] with the 16-byte chunk index XOR-swizzled by (row / 4) % 4; "transposed" [32][cols]
-// with the 64-byte groups of a row XOR-swizzled by row % 4 (a transposing read takes four rows at once), both
-// conflict-free; the direct copies write lane-consecutive LDS, so the swizzle is applied to the source address.
+// LDS tiles: "rows" [row][32] with the 16-byte chunk index XOR-swizzled by (row / 4) % 4, or in pairs of steps [row][64]
+// by (row / 2) % 8; "transposed" [32][cols] with the 64-byte groups of a row XOR-swizzled by row % 4 (a transposing read
+// takes four rows at once), all without bank conflicts; the direct copies write lane-consecutive LDS, so the swizzle is
+// applied to the source address.
+//
+// Measured at 3686 counted rows x 128256 x 4096: logits 3051 us (1270 TFLOP/s with the softmax; a plain library product
+// of the same data 1310), dX 3135 us (1235; 880); at 1843 x 32000 x 4096 dW 423 us (1141; 820).  Bound by the power that
+// the MFMAs draw: under them the clock falls from 2.4 to about 1.6 GHz, of whose cycles the matrix units are busy in 0.73,
+// and without its copies dX still takes 0.84 of its time.  Few rows are bound by the stream of W: 48 x 128256 x 4096 188
+// us, 5.6 TB/s.
 #include <type_traits>
 
 #include "device.h"
@@ -37,8 +44,8 @@ struct HeadCfg {
   // 16-byte copies per thread of a step's tile of the n-side: the last ones of an item's last four steps, which its
   // epilogue need not wait for (the next item asks for them in its third step)
   static constexpr int LB = BN * BK / 8 / NT;
-  // Few rows: the logit product is bound by the stream of W's rows, and workgroups that all begin at column 0 of theirs ask
-  // for addresses a row's length apart, which for powers of two lie in few memory channels.  Each output tile begins
+  // Few rows: the logit product is bound by the stream of W's rows, and workgroups that all begin at column 0 of theirs
+  // ask for addresses a row's length apart, which for powers of two lie in few memory channels.  Each output tile begins
   // 128 columns after the one before it instead (16 x 32000 x 8192 in two ranges 124 -> 94 us; 128 x 128256 x 4096 221 ->
   // 211; a length that is no power of two: no change).  Wide tiles are bound by the MFMAs and share X's tiles in L2.
   static constexpr bool TURNS = BN < 256;
@@ -149,8 +156,8 @@ struct Tile {
       }
     }
   }
-  // Copy i of this thread of the tile of step (or pair of steps) `s`.  (Buffer loads take the uniform part of the address in scalar
-  // registers; the descriptor spans all of memory behind the base, every address is inside the operand by
+  // Copy i of this thread of the tile of step (or pair of steps) `s`.  (Buffer loads take the uniform part of the address
+  // in scalar registers; the descriptor spans all of memory behind the base, every address is inside the operand by
   // construction.)
   __device__ __forceinline__ void copy(int s, int i, lds_char *to, int wave) const {
     const char *b = base;
@@ -259,8 +266,9 @@ struct Items {
   }
 };
 
-// A kernel whose rows do not fill whole 256-row tiles gives the last of them to narrower tiles, in a second pass over items.  The workgroups that had one item less in the first pass take them, where that is at most two each
-// (a narrow item takes 0.6 of the time of a wide one), else all of them.
+// A kernel whose rows do not fill whole 256-row tiles gives the last of them to narrower tiles, in a second pass over
+// items.  The workgroups that had one item less in the first pass take them, where that is at most two each (a narrow item
+// takes 0.6 of the time of a wide one), else all of them.
 struct Turn {
   uint32_t lin, stride;
 };
@@ -586,7 +594,8 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
       }
       if (j == 0) arrive<C::LB>();
       const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
-      if (row < n && lane < 32 && m0 + wm * C::WM * 32 < V) g.stat[(int64_t)row * ntile + m0 / (C::WM * 32) + wm] = make_float2(u, sum);
+      if (row < n && lane < 32 && m0 + wm * C::WM * 32 < V)
+        g.stat[(int64_t)row * ntile + m0 / (C::WM * 32) + wm] = make_float2(u, sum);
       if (!E) continue;
       // E lies in blocks of 32 columns, [column / 32][row][32]: a wave's store is 32 rows of 32 bytes
 #pragma unroll

@@ -1,6 +1,7 @@
 // head_loss.hip -- the row-wise kernels of the output layer's losses: which rows count and their targets' logits
-// (k_head_prep), the loss, the row's factor and the targets' gradient (k_head_combine), and the sum of the dX
-// product's partial sums (k_head_reduce).
+// (k_head_prep, k_head_list), the targets by output tile (k_head_bucket), the statistics of logits that came in ranges
+// (k_head_soft), the loss, the row's factor and the targets' gradient (k_head_combine), the factor for dW (k_head_scale,
+// k_head_put), and the sums of the dX and dW products' ranges (k_head_reduce, k_head_dw_reduce).
 //
 // For a row with logits z, targets v_i with probabilities p_i (one target with p = 1: cross entropy), temperature
 // tau and c = log2(e) / tau, everything is taken against the first target r (the most probable one):
@@ -10,8 +11,9 @@
 // E_v = exp2((z_v - u) c) and S = 1 + rest, the gradient by the logits is
 //   G_v = w tau (q_v - P_v) = (w tau / S) (E_v - S P_v),   P_v = sum of the p_i whose target is v,
 // so the product kernels take E with only the targets' entries replaced by E_v - S P_v (at r: (1 - P_r) - P_r rest,
-// again without cancellation), and the row factor w tau / S is applied in binary32 afterwards.  Entries are rounded to
-// bf16 for the matrix unit; at r, whose entry outweighs the others, dX also gets the remainder.
+// again without cancellation), and the row factor w tau / S is applied to dX in binary32 afterwards (dW: see
+// k_head_scale).  Entries are rounded to bf16 for the matrix unit; at r, whose entry outweighs the others, dX also gets the
+// remainder.
 #include <type_traits>
 
 #include "device.h"
@@ -183,7 +185,8 @@ __device__ __forceinline__ void sort_targets(const HeadRows &rows, int64_t tile,
 // it then also sorts; k_head_list and k_head_bucket do it otherwise.  The other workgroups' waves take a row of X each:
 // its first target (the label, or the teacher's most probable one; the first of equals) and that target's logit by a
 // dot product (binary32 FMA), the teacher's softmax, and the row in the blocks of 32 columns that the logit product
-// reads (zeros past K); or, for a row that does not count, its zero loss and gradient.
+// reads (zeros past K); or, for a row that does not count, its zero loss and gradient.  Bound by its loads: 4096 x 4096
+// 24 us (X, the targets' rows of W and the copy, 4.2 TB/s), a single row 4.
 __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__restrict__ X, int64_t T,
                                                             const bf16_t *__restrict__ W, int64_t V, int64_t K,
                                                             const int64_t *__restrict__ labels,
@@ -299,7 +302,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
   }
 }
 
-// Numbers the rows whose first target k_head_prep found.
+// Numbers the rows whose first target k_head_prep found, by one workgroup: 4096 rows 8 us.
 constexpr int kListThreads = 1024;
 __global__ __launch_bounds__(kListThreads) void k_head_list(int64_t T, int64_t K, const int32_t *__restrict__ refcol,
                                                             int32_t *__restrict__ n, int32_t *__restrict__ list,
@@ -307,7 +310,7 @@ __global__ __launch_bounds__(kListThreads) void k_head_list(int64_t T, int64_t K
   number_rows<kListThreads>(T, K, [&](int64_t t) { return refcol[t] >= 0; }, n, list, ranges, blocks);
 }
 
-// One workgroup per tile of rows of the block.
+// One workgroup per tile of rows of the block: 4096 rows of 64 targets 36 us, of latency, beside products of 6200.
 constexpr int kBucketThreads = 1024;
 __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, int64_t row0, int64_t tb, int tile_cols,
                                                                 int ntile, const int32_t *__restrict__ index, int k,
@@ -323,7 +326,8 @@ __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, i
 
 // A workgroup per counted row and 2048 columns: z from the ranges' sums, in order, then what the product's epilogue does
 // with it (see logit_items), a lane taking eight columns.
-// (Only narrow tiles' reductions are split: every entry of the statistics is of kHeadStat columns.)
+// (Only narrow tiles' reductions are split: every entry of the statistics is of kHeadStat columns.)  Bound by the sums'
+// read: 1910 x 1890 in two ranges 8.5 us, launch included.
 __global__ __launch_bounds__(256) void k_head_soft(HeadRows rows, int64_t row0, int64_t tb,
                                                    const float *__restrict__ part, int ranges, int64_t V, float c,
                                                    float2 *__restrict__ stat, int64_t ntile,
@@ -388,9 +392,11 @@ __global__ __launch_bounds__(256) void k_head_soft(HeadRows rows, int64_t row0, 
         u32x4_t{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])};
 }
 
-// One wave per counted row of the block.
+// One wave per counted row of the block.  Bound by latency: 3686 rows of a 128256-wide vocabulary 14 us, with 64 targets
+// each 27.
 __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row0, int64_t tb,
-                                                      const float2 *__restrict__ stat, int64_t ntile, int64_t V, const int64_t *__restrict__ labels,
+                                                      const float2 *__restrict__ stat, int64_t ntile, int64_t V,
+                                                      const int64_t *__restrict__ labels,
                                                       const int32_t *__restrict__ index, int k, float tau,
                                                       const float *__restrict__ weight, float *__restrict__ loss,
                                                       float4 *__restrict__ scale, bf16_t *__restrict__ E, int64_t lde,
@@ -402,7 +408,8 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   n = n < 0 ? 0 : n < tb ? n : tb;
   if (i >= n) {  // the dW product's steps go to the next 128 rows (at least one such group)
     if (Xs && i < (n > 0 ? (n + 127) / 128 * 128 : 128)) {
-      for (int64_t at = 8 * lane; at < K; at += 512) *reinterpret_cast<u32x4_t *>(Xs + i * K + at) = u32x4_t{0u, 0u, 0u, 0u};
+      for (int64_t at = 8 * lane; at < K; at += 512)
+        *reinterpret_cast<u32x4_t *>(Xs + i * K + at) = u32x4_t{0u, 0u, 0u, 0u};
       if (n == 0 && i == 0)
         for (int64_t v = 8 * lane; v < lde; v += 512)
           *reinterpret_cast<u32x4_t *>(E + (v / 32 * te) * 32 + v % 32) = u32x4_t{0u, 0u, 0u, 0u};
@@ -476,7 +483,8 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
         const int32_t vj = j0 + lane < k ? index[t * k + j0 + lane] : -1;
         const float pj = j0 + lane < k ? rows.pt[t * k + j0 + lane] : 0.f;
         for (int j = 0; j < min(64, k - j0); ++j)
-          P += __builtin_amdgcn_readlane(vj, j) == v ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pj), j)) : 0.f;
+          if (__builtin_amdgcn_readlane(vj, j) == v)
+            P += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pj), j));
       }
       if (!target_ok(v, V)) continue;
       const float g = v == rc ? eref * (1.f - P) - P * rest : exp2f((rows.zt[t * k + me] - u) * c) - P * S;
@@ -491,7 +499,8 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
     for (int64_t at0 = 8 * lane; at0 < K; at0 += 512 * 4) {
       u32x4_t v[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const u32x4_t *>(X + t * K + (at0 + 512 * q < K ? at0 + 512 * q : 0));
+      for (int q = 0; q < 4; ++q)
+        v[q] = *reinterpret_cast<const u32x4_t *>(X + t * K + (at0 + 512 * q < K ? at0 + 512 * q : 0));
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
 #pragma unroll
@@ -505,7 +514,9 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
 // E's rows times the fraction (in [1/2, 1)) of their factors, for dW, whose reduction runs over the rows, so that no
 // factor can wait for the product's epilogue.  (Rounding X times the factor instead would round every term of a row of
 // dW twice; here the first target's entry, which outweighs the others, is rounded once, from its value with the
-// remainder, and k_head_put does the same for a teacher's other targets.)  Bound by E's read and write.  A thread takes eight columns of a row in each of kScaleBlocks blocks.
+// remainder, and k_head_put does the same for a teacher's other targets.  dW's error against 64 bits falls from 2.9e-3 to
+// 2.3e-3 of its norm.)  Bound by E's read and write: 1843 x 32000 40 us, 5.9 TB/s.  A thread takes eight columns of a row
+// in each of kScaleBlocks blocks.
 constexpr int kScaleBlocks = 8;
 __global__ __launch_bounds__(256) void k_head_scale(HeadRows rows, int64_t row0, int64_t tb,
                                                     const float4 *__restrict__ scale, bf16_t *__restrict__ E,
@@ -546,7 +557,7 @@ __global__ __launch_bounds__(256) void k_head_put(HeadRows rows, int64_t row0, i
 }
 
 // dX rows of the block from the ranges' partial sums part[range][row][K], added in range order, and the first target's
-// remainder.
+// remainder.  Bound by the sums' read: 1838 x 4096 in two ranges 19 us.
 __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0, int64_t tb,
                                                      const float *__restrict__ part, const bf16_t *__restrict__ W,
                                                      int64_t K, const float4 *__restrict__ scale,
@@ -580,11 +591,12 @@ __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0
   u32x4_t o;
 #pragma unroll
   for (int w = 0; w < 4; ++w)
-    o[w] = pack_bf16x2(fmaf(f.y, bf16_lo_to_f32(wv[w]), s[2 * w]) * f.x, fmaf(f.y, bf16_hi_to_f32(wv[w]), s[2 * w + 1]) * f.x);
+    o[w] = pack_bf16x2(fmaf(f.y, bf16_lo_to_f32(wv[w]), s[2 * w]) * f.x,
+                       fmaf(f.y, bf16_hi_to_f32(wv[w]), s[2 * w + 1]) * f.x);
   *reinterpret_cast<u32x4_t *>(dX + t * K + col) = o;
 }
 
-// dW from the ranges' partial sums [range][V][K], in range order.
+// dW from the ranges' partial sums [range][V][K], in range order.  Bound by their read: 2000 x 504 in eight ranges 6 us.
 __global__ __launch_bounds__(256) void k_head_dw_reduce(HeadRows rows, int64_t tb, const float *__restrict__ part,
                                                         int ranges, int64_t count, bf16_t *__restrict__ dW) {
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
@@ -638,8 +650,8 @@ hipError_t launch_head_bucket(const HeadRows &rows, int64_t row0, int64_t tb, co
 hipError_t launch_head_soft(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, int ranges, int64_t V,
                             float c, float2 *stat, int64_t ntile, const int32_t *index, int k, bf16_t *E, int64_t lde,
                             int64_t te, hipStream_t s) {
-  launch(k_head_soft, dim3((unsigned)tb, (unsigned)((lde + 2047) / 2048)), dim3(256), 0, s, rows, row0, tb, part, ranges, V, c, stat, ntile, index, k, E,
-         lde, te);
+  launch(k_head_soft, dim3((unsigned)tb, (unsigned)((lde + 2047) / 2048)), dim3(256), 0, s, rows, row0, tb, part, ranges,
+         V, c, stat, ntile, index, k, E, lde, te);
   return hipGetLastError();
 }
 

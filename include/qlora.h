@@ -333,11 +333,14 @@ int qlora_adamw8_step(const qlora_adamw8_tensor *tensors, int32_t count, double 
  * beside the quantized linears ("What stays in full precision", katajob); the
  * step is forward -> loss -> backward into the adapters (glossary, steps 3 and
  * 4).  With X [T, n_in] the last hidden states and W [n_vocab, n_in] the output
- * layer (bf16, device), z = X . W^T.  The logits are never stored: the losses
- * come from softmax statistics of pieces of the vocabulary, and the gradients
- * from bf16 values exp(z - reference) of a bounded block of rows in the
- * workspace (at most about 1 GiB however many tokens there are; 256 rows at
- * least).
+ * layer (bf16, device), z = X . W^T.  The [T, n_vocab] logits are not kept:
+ * the losses come from softmax statistics of pieces of the vocabulary, and the
+ * gradients from bf16 values exp(z - reference) of a bounded block of rows in
+ * the workspace (at most 1 GiB of them however many tokens there are; 256 rows
+ * at least).  Besides them the workspace holds a copy of X, 8 bytes of
+ * statistics per 64 columns and row of a block, and binary32 partial sums where
+ * a product has few output tiles (few rows or a small vocabulary: of the
+ * logits too).
  *
  * Cross entropy, y_t = labels[t] (device int64):
  *   loss[t] = log(sum_v exp(z_tv)) - z_t,y        [T] binary32
@@ -355,9 +358,11 @@ int qlora_adamw8_step(const qlora_adamw8_tensor *tensors, int32_t count, double 
  * bits; the sums of the softmax, the losses and the rows' factors are
  * binary32.  The loss is formed against the target's logit, log1p of the other
  * terms, so a loss near 0 keeps its digits.  The gradient's entries are rounded
- * to bf16 once for the matrix unit (for dW, X times the row factor once more);
- * the products accumulate in binary32 and are rounded to bf16 once.  Reductions
- * run in a fixed order: results are bitwise repeatable.
+ * to bf16 once for the matrix unit, before the row's factor weight / sum, which
+ * multiplies dX in binary32 (for dW its fraction multiplies the rounded entries,
+ * which are rounded once more, the targets' excepted; its power of two multiplies
+ * X exactly); the products accumulate in binary32 and are rounded to bf16 once.
+ * Reductions run in a fixed order: results are bitwise repeatable.
  *
  * X, W, dX, dW 16-byte aligned, labels 8-byte, loss and weight 4-byte; none
  * may overlap an output.  n_in % 8 == 0, n_vocab >= 1, both at most 2^22,
