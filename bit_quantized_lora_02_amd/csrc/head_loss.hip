@@ -88,6 +88,33 @@ __device__ __forceinline__ void dx_ranges(int n, int64_t K, int64_t lde, int til
   if (lane == 0) out[0] = even(first.ranges), out[1] = even(second.ranges), out[2] = whole;
 }
 
+// s[j] = the sum over r = 0 .. ranges - 1, in order, of p[r * step + j], D of the ranges asked for at a time (FULL: also of
+// the last ones, some of them twice).
+template <int D, bool FULL, int N>
+__device__ __forceinline__ void add_ranges(const float *p, int64_t step, int ranges, float (&s)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = 0.f;
+  int r = 0;
+  auto add = [&](auto count) {
+    constexpr int C = decltype(count)::value;
+    float4 a[C][N / 4];
+#pragma unroll
+    for (int q = 0; q < C; ++q)
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j)
+        a[q][j] = *reinterpret_cast<const float4 *>(p + (FULL ? min(r + q, ranges - 1) : r + q) * step + 4 * j);
+#pragma unroll
+    for (int q = 0; q < C; ++q)
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j)
+        if (!FULL || r + q < ranges)
+          s[4 * j] += a[q][j].x, s[4 * j + 1] += a[q][j].y, s[4 * j + 2] += a[q][j].z, s[4 * j + 3] += a[q][j].w;
+    r += C;
+  };
+  while (r + (FULL ? 1 : D) <= ranges) add(std::integral_constant<int, D>());
+  while (r < ranges) add(std::integral_constant<int, 1>());
+}
+
 // Numbers the rows with counts(t), in order, by one workgroup of `threads`; then the blocks' dX ranges.
 template <int threads, class Counts>
 __device__ __forceinline__ void number_rows(int64_t T, int64_t K, Counts counts, int32_t *__restrict__ n,
@@ -138,16 +165,18 @@ template <int threads>
 __device__ __forceinline__ void sort_targets(const HeadRows &rows, int64_t tile, int64_t first, int have, int tile_rows,
                                              int tile_cols, int ntile, const int32_t *__restrict__ index, int k,
                                              int64_t V, int *s_count /* [ntile] */) {
-  __shared__ int s_sum[threads / 64];
+  __shared__ int s_sum[threads / 64], s_row[256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < have; i += threads) s_row[i] = ((volatile const int32_t *)rows.list)[first + i];
   have *= k;
   for (int i = tid; i < ntile; i += threads) s_count[i] = 0;
   __syncthreads();
+  const uint32_t per_k = 0xffffffffu / (uint32_t)k + 1;  // e / k = e per_k / 2^32 for e < 2^16 (k = 1: per_k = 0)
   auto each = [&](auto use) {
-#pragma unroll 4
+#pragma unroll 8
     for (int e = tid; e < have; e += threads) {
-      const int nj = e / k, j = e - nj * k;
-      const int64_t v = index[(int64_t)((volatile const int32_t *)rows.list)[first + nj] * k + j];
+      const int nj = k == 1 ? e : (int)__umulhi((uint32_t)e, per_k), j = e - nj * k;
+      const int64_t v = index[(int64_t)s_row[nj] * k + j];
       if (target_ok(v, V)) use((int)v, nj, j);
     }
   };
@@ -310,7 +339,7 @@ __global__ __launch_bounds__(kListThreads) void k_head_list(int64_t T, int64_t K
   number_rows<kListThreads>(T, K, [&](int64_t t) { return refcol[t] >= 0; }, n, list, ranges, blocks);
 }
 
-// One workgroup per tile of rows of the block: 4096 rows of 64 targets 36 us, of latency, beside products of 6200.
+// One workgroup per tile of rows of the block: 4096 rows of 64 targets 27 us, of latency, beside products of 6200.
 constexpr int kBucketThreads = 1024;
 __global__ __launch_bounds__(kBucketThreads) void k_head_bucket(HeadRows rows, int64_t row0, int64_t tb, int tile_cols,
                                                                 int ntile, const int32_t *__restrict__ index, int k,
@@ -355,14 +384,7 @@ __global__ __launch_bounds__(256) void k_head_soft(HeadRows rows, int64_t row0, 
   float z[8], e[8], sum = 0.f;
 #pragma unroll
   for (int q = 0; q < 8; ++q) z[q] = 0.f;
-  if (in)
-#pragma unroll 4
-    for (int r = 0; r < ranges; ++r) {
-      const float4 a = *reinterpret_cast<const float4 *>(p + (int64_t)r * n * lde + v);
-      const float4 b = *reinterpret_cast<const float4 *>(p + (int64_t)r * n * lde + v + 4);
-      z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
-      z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
-    }
+  if (in) add_ranges<4, false>(p + v, n * lde, ranges, z);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     if (!in || v + q >= V || v + q == rc) z[q] = -INFINITY;
@@ -557,7 +579,10 @@ __global__ __launch_bounds__(256) void k_head_put(HeadRows rows, int64_t row0, i
 }
 
 // dX rows of the block from the ranges' partial sums part[range][row][K], added in range order, and the first target's
-// remainder.  Bound by the sums' read: 1838 x 4096 in two ranges 19 us.
+// remainder, N columns a thread, D ranges in flight.  Bound by the sums' read: 1838 x 4096 in two ranges 19 us (with four
+// columns a thread 24).  Few rows come in many ranges and have few threads: 17 x 2048 in 32 ranges 5.1 us with four
+// columns and 16 ranges in flight, 6.7 with eight and four.
+template <int N, int D>
 __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0, int64_t tb,
                                                      const float *__restrict__ part, const bf16_t *__restrict__ W,
                                                      int64_t K, const float4 *__restrict__ scale,
@@ -565,35 +590,27 @@ __global__ __launch_bounds__(256) void k_head_reduce(HeadRows rows, int64_t row0
   int64_t n = *rows.n - row0;
   n = n < tb ? n : tb;
   if (n <= 0) return;
-  const int64_t per = K / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t per = K / N, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= n * per) return;
-  const int64_t i = at / per, col = (at % per) * 8;
+  const int64_t i = at / per, col = (at % per) * N;
   const int whole = rows.ranges[2];
   const bool second = i >= whole;
   const int ranges = rows.ranges[second];
   if (ranges == 1) return;  // the product wrote dX itself
   const float *p = part + (second ? head_first_sums(whole, rows.ranges[0], K) : 0);
   const int64_t count = second ? n - whole : whole;
-  p += (second ? i - whole : i) * K + col;
-  float s[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = 0.f;
-#pragma unroll 4
-  for (int r = 0; r < ranges; ++r, p += count * K) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
-    s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
-  }
+  float v[N];
+  add_ranges<D, D == 16>(p + (second ? i - whole : i) * K + col, count * K, ranges, v);
   const float4 f = scale[i];
   const int64_t t = rows.list[row0 + i];
-  const u32x4_t wv = *reinterpret_cast<const u32x4_t *>(W + rows.refcol[t] * K + col);
-  u32x4_t o;
+  typedef uint32_t word_t __attribute__((ext_vector_type(N / 2)));
+  const word_t wv = *reinterpret_cast<const word_t *>(W + rows.refcol[t] * K + col);
+  word_t o;
 #pragma unroll
-  for (int w = 0; w < 4; ++w)
-    o[w] = pack_bf16x2(fmaf(f.y, bf16_lo_to_f32(wv[w]), s[2 * w]) * f.x,
-                       fmaf(f.y, bf16_hi_to_f32(wv[w]), s[2 * w + 1]) * f.x);
-  *reinterpret_cast<u32x4_t *>(dX + t * K + col) = o;
+  for (int w = 0; w < N / 2; ++w)
+    o[w] = pack_bf16x2(fmaf(f.y, bf16_lo_to_f32(wv[w]), v[2 * w]) * f.x,
+                       fmaf(f.y, bf16_hi_to_f32(wv[w]), v[2 * w + 1]) * f.x);
+  *reinterpret_cast<word_t *>(dX + t * K + col) = o;
 }
 
 // dW from the ranges' partial sums [range][V][K], in range order.  Bound by their read: 2000 x 504 in eight ranges 6 us.
@@ -602,20 +619,10 @@ __global__ __launch_bounds__(256) void k_head_dw_reduce(HeadRows rows, int64_t t
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (at >= count) return;
   const int n = min(*rows.n, (int)tb), per = head_dw_steps(n, ranges);
-  ranges = (max((n + 127) / 128, 1) + per - 1) / per;
-  float s[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = 0.f;
-  const float *p = part + at;
-#pragma unroll 4
-  for (int r = 0; r < ranges; ++r, p += count) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
-    s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
-  }
-  *reinterpret_cast<u32x4_t *>(dW + at) = u32x4_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
-                                                  pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])};
+  float v[8];
+  add_ranges<4, false>(part + at, count, (max((n + 127) / 128, 1) + per - 1) / per, v);
+  *reinterpret_cast<u32x4_t *>(dW + at) = u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
 }  // namespace
@@ -667,8 +674,10 @@ hipError_t launch_head_combine(const HeadRows &rows, int64_t row0, int64_t tb, c
 
 hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, const float *part, const bf16_t *W,
                               int64_t K, const float4 *scale, bf16_t *dX, hipStream_t s) {
-  launch(k_head_reduce, dim3((unsigned)((tb * (K / 8) + 255) / 256)), dim3(256), 0, s, rows, row0, tb, part, W, K,
-         scale, dX);
+  const bool few = rows.tile_rows == 64;
+  const int64_t threads = tb * (K / (few ? 4 : 8));
+  launch(few ? k_head_reduce<4, 16> : k_head_reduce<8, 4>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, rows,
+         row0, tb, part, W, K, scale, dX);
   return hipGetLastError();
 }
 
