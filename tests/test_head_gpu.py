@@ -544,3 +544,75 @@ def test_ways_through_the_products(T, V, K, ignored):
     check("loss", loss, wl, bl)
     check("dX", dX, wx, bx)
     check("dW", dW, ww, bw)
+
+
+@pytest.mark.parametrize("T,V,K,k", [(700, 33000, 520, 3), (5000, 300, 520, 0), (2000, 130, 1032, 2), (1500, 17000, 264, 0),
+                                     (256, 9000, 264, 16), (64, 40000, 1032, 64), (1, 8, 8, 1)])
+def test_writes_only_its_buffers_in_every_way(T, V, K, k):
+    test_writes_only_its_buffers(T, V, K, k)
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("T,V,K", [(3000, 1000, 264), (700, 33000, 136), (100, 700, 2056), (60, 5000, 1032)])
+def test_captured_with_any_number_of_rows(op, T, V, K):
+    """One captured call, replayed with no row that counts, with one, with a few and with all of them."""
+    print(f"captured {op} T={T} V={V} K={K}", flush=True)
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=T))
+    all_y = y.clone()
+    index = torch.stack([y, (y + 11) % V], 1).to(torch.int32)
+    logit = torch.randn(T, 2, device="cuda")
+    ws = torch.empty(B.head_workspace_bytes(T, V, K, 0 if op == "ce" else 2, True, True), dtype=torch.uint8,
+                     device="cuda")
+    outs = (torch.empty(T, device="cuda"), torch.empty_like(X), torch.empty_like(W))
+    call = (lambda **n: B.head_ce(X, W, y, weight, **n)) if op == "ce" else \
+        (lambda **n: B.head_distill(X, W, index, logit, 2.0, weight, **n))
+    call(ws=ws, outs=outs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(ws=ws, outs=outs)
+    for keep in (0, 1, T // 10, T, 0):
+        mask = torch.zeros(T, dtype=torch.bool, device="cuda")
+        mask[torch.randperm(T, generator=torch.Generator().manual_seed(keep))[:keep].cuda()] = True
+        y.copy_(torch.where(mask, all_y, -100))
+        index.copy_(torch.stack([y, torch.where(mask, (all_y + 11) % V, -1)], 1))
+        want = [t.clone() for t in call(need_dw=True)]
+        for t in outs:
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, a, b in zip(("loss", "dX", "dW"), outs, want):
+            assert torch.equal(a, b), f"{name} with {keep} rows"
+            assert torch.isfinite(a).all()
+            if keep == 0:
+                assert (a == 0).all(), f"{name} of no rows"
+
+
+@pytest.mark.parametrize("T,V,K", [(3000, 1000, 264), (700, 33000, 520), (256, 9000, 4104), (60, 5000, 1032), (1500, 17000, 4104)])
+def test_independent_of_the_workspace_in_every_way(T, V, K):
+    test_repeatable_and_independent_of_the_workspace(T, V, K)
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+def test_the_largest_batch(op):
+    """2^22 rows, the most that the call takes, of the smallest width."""
+    T, V, K = 1 << 22, 16, 8
+    print(f"{op} T={T}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    X = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    W = torch.randn(V, K, generator=g, device="cuda").to(torch.bfloat16)
+    y = torch.randint(-1, V, (T,), generator=g, device="cuda")
+    weight = torch.randn(T, generator=g, device="cuda")
+    if op == "ce":
+        targets, tau = ce_targets(y, V), 1.0
+        loss, dX, dW = B.head_ce(X, W, y, weight, need_dw=True)
+    else:
+        index = torch.stack([y, torch.where(y < 0, -1, (y + 3) % V)], 1).to(torch.int32)
+        logit, tau = torch.randn(T, 2, generator=g, device="cuda"), 2.0
+        targets = kd_targets(index, logit, V, tau)
+        loss, dX, dW = B.head_distill(X, W, index, logit, tau, weight, need_dw=True)
+    wl, wx, ww, bl, bx, bw = reference(X, W, *targets, weight, tau)
+    check("loss", loss, wl, bl)
+    check("dX", dX, wx, bx)
+    check("dW", dW, ww, bw)
