@@ -16,8 +16,8 @@ typedef uint16_t bf16_t;
 // and E[v] = exp2((z[v] - u) c) is what is kept of logit v.
 struct HeadRows {
   const int32_t *n;       // rows that count
-  const int32_t *ranges;  // the dX product's for the block at hand: ranges of its first rows, of the others (which take
-                          // 128-row tiles), number of first rows
+  const int32_t *ranges;  // for the block at hand: the dX product's ranges of its first rows, of the others (which take
+                          // 128-row tiles), number of first rows; that number in the logit product
   int tile_rows;          // rows of the products' tiles
   const int32_t *list;  // [T] their rows in X
   float *ref;           // [T] by row of X: the logit of the row's first target
@@ -94,7 +94,6 @@ struct HeadBlocks {
   int64_t te;         // rows of E's blocks of columns (E is [lde / 32][te][32])
 };
 
-// (ranges NULL: no dX)
 hipError_t launch_head_prep(const bf16_t *X, int64_t T, const bf16_t *W, int64_t V, int64_t K, const int64_t *labels,
                             const int32_t *index, const float *logit, int k, float tau, int32_t *n, int32_t *list,
                             int32_t *ranges, const HeadBlocks &blocks, const HeadRows &rows, float *loss, bf16_t *dX,
@@ -120,7 +119,7 @@ hipError_t launch_head_reduce(const HeadRows &rows, int64_t row0, int64_t tb, co
 
 // Rows that go to tiles of `tile_rows`: all, but for 128 or fewer behind the last whole 256-row tile, which take
 // 128-row tiles (measured: a 256 x 128 tile costs 0.6 of a 256 x 256 one).
-__host__ __device__ inline int head_whole_rows(int n, int tile_rows) {
+__device__ inline int head_whole_rows(int n, int tile_rows) {
   const int rest = n % 256;
   return tile_rows == 256 && rest >= 1 && rest <= 128 ? n - rest : n;
 }

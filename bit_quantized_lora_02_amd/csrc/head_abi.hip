@@ -133,15 +133,14 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   float *sums = p.off_sums ? (float *)(w + p.off_sums) : nullptr;
   bf16_t *Xt = (bf16_t *)(w + p.off_xt);
   int32_t *ranges = (int32_t *)(w + p.off_ranges);
-  int32_t *const rg = dX ? ranges : nullptr;
   const float c = 1.44269504f / tau;
   const int64_t lde = p.b.lde, te = p.b.te;
-  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, rg, p.b, rows, loss, dX, Xt,
+  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, ranges, p.b, rows, loss, dX, Xt,
                                        p.ldx, s));
   const bool sorted = k > 0 && p.ranges == 1;  // the targets go by the product's tiles
   float *zpart = p.ranges > 1 ? (float *)(w + p.off_z) : nullptr;
   const bool few = k > 0 && head_few_targets(T, k, p.b.tile_rows);
-  if (k > 0 && !few) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, rg, p.b, s));
+  if (k > 0 && !few) LAUNCH("head_list", launch_head_list(rows, T, K, n, list, ranges, p.b, s));
   for (int64_t b = 0; b < p.b.count; ++b) {
     const int64_t row0 = b * p.b.tb, tb = T - row0 < p.b.tb ? T - row0 : p.b.tb;
     rows.ranges = ranges + 4 * b;

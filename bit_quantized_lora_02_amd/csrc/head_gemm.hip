@@ -459,7 +459,7 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
   // The epilogue's first loads are issued before the reduction: the lane's rows in X, and the item's targets (one per
   // lane, the first 64 of them).
   int32_t t[C::WN];
-  int t0 = 0, t1 = 0, range = 0;
+  int t0 = 0, t1 = 0, range = 0, row_of = 0;  // row_of: the item's first row in the row tile of its targets
   uint32_t target = 0;
   const uint32_t *targets = nullptr;
   auto begin = [&]() {
@@ -471,6 +471,7 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
     }
     if (rows.target) {
       const int row_tile = n0 / rows.tile_rows;
+      row_of = n0 - row_tile * rows.tile_rows;
       const int32_t *const b = rows.bucket + (int64_t)row_tile * (g.tiles + 1) + items.m;
       t0 = b[0], t1 = b[1];
       targets = rows.target + (int64_t)row_tile * rows.tile_rows * k;
@@ -482,12 +483,12 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
     for (int at = t0; at < t1; at += 64) {
       const bool in = at + lane < t1;
       if (at != t0 && in) target = targets[at + lane];
-      const int nj = target >> 16, m = target >> 8 & 255;
-      uint64_t mine = __ballot(in && nj / (C::WN * 32) == wn && m / (C::WM * 32) == wm);
+      const int nj = (int)(target >> 16) - row_of, m = target >> 8 & 255;
+      uint64_t mine = __ballot(in && nj >= 0 && nj / (C::WN * 32) == wn && m / (C::WM * 32) == wm);
       while (mine) {
         const uint32_t one = __builtin_amdgcn_readlane(target, __builtin_ctzll(mine));
         mine &= mine - 1;
-        const int un = one >> 16, um = one >> 8 & 255;
+        const int un = (int)(one >> 16) - row_of, um = one >> 8 & 255;
         const int i1 = um / 32 % C::WM, j1 = un / 32 % C::WN, e1 = (um >> 3 & 3) * 4 + (um & 3);
         float z = 0.f;
         int32_t row = 0;
@@ -616,16 +617,17 @@ template <class C, bool SPLIT>
 __global__ __launch_bounds__(C::NT) void k_head_logits(LogitArgs g) {
   const int n = block_rows(g.rows, g.row0, g.tb);
   if (n == 0) return;
-  const int whole = SPLIT ? n : head_whole_rows(n, C::BN);
+  const int whole = C::BN == 256 ? g.rows.ranges[3] : n;
   Items items = {g.tiles, (whole + C::BN - 1) / C::BN, SPLIT ? g.ranges : 1};
   const Turn all = {blockIdx.x, gridDim.x};
   QLORA_RING_PAIRS(C, ring);
   if (whole > 0) logit_items<C, SPLIT>(g, 0, whole, items, all, ring);
-  if constexpr (C::BN == 256 && !SPLIT) {
+  if constexpr (C::BN == 256) {
     if (whole == n) return;
-    const Turn turn = second_pass(items, (uint32_t)g.tiles);
+    const int narrow = (n - whole + H128::BN - 1) / H128::BN;
+    const Turn turn = second_pass(items, (uint32_t)(g.tiles * narrow));
     between_passes();
-    items = {g.tiles, 1, 1};
+    items = {g.tiles, narrow, 1};
     logit_items<H128, false>(g, whole, n, items, turn, ring);
   }
 }
@@ -842,9 +844,10 @@ hipError_t launch_head_logits(const HeadRows &rows, int64_t row0, int64_t tb, co
                               const bf16_t *W, int64_t V, int64_t K, float c, float2 *stat, int64_t ntile, bf16_t *E,
                               int64_t lde, int64_t te, int k, int ranges, float *part, hipStream_t s) {
   const int64_t cols = head_tile_cols(rows.tile_rows), tiles = (V + cols - 1) / cols;
+  const int64_t most = rows.tile_rows < 128 ? rows.tile_rows : 128;  // (all rows may take 128-row tiles)
 #define QLORA_CALL(CFG)                                                                                            \
   launch(CFG::BN < 256 && ranges > 1 ? k_head_logits<CFG, CFG::BN < 256> : k_head_logits<CFG, false>,              \
-         dim3((unsigned)groups(tiles * ((tb + CFG::BN - 1) / CFG::BN) * ranges, CFG::BN)), dim3(CFG::NT), 0, s,    \
+         dim3((unsigned)groups(tiles * ((tb + most - 1) / most) * ranges, CFG::BN)), dim3(CFG::NT), 0, s,          \
          LogitArgs{rows, row0, tb, Xt, ldx, W, V, K, c, stat, ntile, (int)tiles, ranges, part, E, lde, te, k})
   QLORA_HEAD_TILES(rows, QLORA_CALL)
 #undef QLORA_CALL

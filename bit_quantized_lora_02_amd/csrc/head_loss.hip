@@ -115,7 +115,25 @@ __device__ __forceinline__ void add_ranges(const float *p, int64_t step, int ran
   while (r < ranges) add(std::integral_constant<int, 1>());
 }
 
-// Numbers the rows with counts(t), in order, by one workgroup of `threads`; then the blocks' dX ranges.
+// Of n rows, those that the logit product takes in 256-row tiles, `tiles_m` of the vocabulary; the others go to tiles of
+// 128 rows: those behind the last whole tile (see second_pass), or all, where fewer rounds of workgroups at 0.62 of the time
+// make up for them (rows that do not count are known only here: 256 of 512 rows x 32000 x 4096 in 125 wide tiles 119 us, in
+// 250 narrow ones 104; 240 of 600 x 30000 x 1024 30 and 23).
+__device__ __forceinline__ int logit_whole(int n, int tiles_m) {
+  const int whole = head_whole_rows(n, 256);
+  auto rounds = [](int items, int slots) { return (float)((items + slots - 1) / slots); };
+  const int wide = tiles_m * ((whole + 255) / 256), busy = wide % 256;
+  float cost = (float)(wide / 256);
+  if (whole == n)
+    cost += busy > 0 ? 1.f : 0.f;
+  else if (busy > 0 && tiles_m <= 2 * (256 - busy))
+    cost += fmaxf(1.f, 0.6f * rounds(tiles_m, 256 - busy));
+  else
+    cost += (busy > 0 ? 1.f : 0.f) + 0.6f * rounds(tiles_m, 256);
+  return 0.62f * rounds(tiles_m * ((n + 127) / 128), 256) < cost ? 0 : whole;
+}
+
+// Numbers the rows with counts(t), in order, by one workgroup of `threads`; then the blocks' ways through the products.
 template <int threads, class Counts>
 __device__ __forceinline__ void number_rows(int64_t T, int64_t K, Counts counts, int32_t *__restrict__ n,
                                             int32_t *__restrict__ list, int32_t *__restrict__ ranges,
@@ -151,10 +169,12 @@ __device__ __forceinline__ void number_rows(int64_t T, int64_t K, Counts counts,
     __syncthreads();
   }
   if (tid == 0) *n = base;
-  for (int64_t b = wave; ranges && b < blocks.count; b += threads / 64) {
+  for (int64_t b = wave; b < blocks.count; b += threads / 64) {
     const int64_t row0 = b * blocks.tb, tb = T - row0 < blocks.tb ? T - row0 : blocks.tb;
     const int64_t have = base - row0 < tb ? base - row0 : tb;
-    if (have > 0) dx_ranges((int)have, K, blocks.lde, blocks.tile_rows, lane, ranges + 4 * b);
+    if (have <= 0) continue;
+    dx_ranges((int)have, K, blocks.lde, blocks.tile_rows, lane, ranges + 4 * b);
+    if (lane == 0) ranges[4 * b + 3] = logit_whole((int)have, (int)((blocks.lde + 255) / 256));
   }
 }
 
@@ -441,7 +461,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   const int64_t t = rows.list[row0 + i];
   const float ref = rows.ref[t], c = 1.44269504f / tau;
   const float2 *st = stat + i * ntile;
-  const int stat_cols = head_stat_cols(rows.tile_rows == 256 && i < head_whole_rows((int)n, 256));
+  const int stat_cols = head_stat_cols(rows.tile_rows == 256 && i < rows.ranges[3]);
   const int entries = (int)((V + stat_cols - 1) / stat_cols);
   float u = ref, sum = 0.f;
 #pragma unroll 4

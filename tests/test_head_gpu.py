@@ -616,3 +616,21 @@ def test_the_largest_batch(op):
     check("loss", loss, wl, bl)
     check("dX", dX, wx, bx)
     check("dW", dW, ww, bw)
+
+
+@pytest.mark.parametrize("T,V,K,k,ignored", [(512, 33000, 136, 1, 0.55), (900, 33000, 136, 3, 0.72), (900, 33000, 264, 3, 0.0),
+                                             (300, 33000, 136, 256, 0.0)])
+def test_targets_in_narrow_tiles_of_a_wide_call(T, V, K, k, ignored):
+    """The rows that count decide how many go to narrow tiles, which find their targets in the lists of the wide ones."""
+    print(f"head_distill T={T} V={V} K={K} k={k} ignored={ignored}", flush=True)
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=T + k))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    index = torch.randint(0, V, (T, k), generator=g, device="cuda")
+    index[:, 0] = y
+    index[torch.rand(T, generator=g, device="cuda") < ignored] = -1
+    index, logit = index.to(torch.int32), 2.0 * torch.randn(T, k, generator=g, device="cuda")
+    loss, dX, dW = B.head_distill(X, W, index, logit, 1.5, weight, need_dw=True)
+    wl, wx, ww, bl, bx, bw = reference(X, W, *kd_targets(index, logit, V, 1.5), weight, 1.5)
+    check("loss", loss, wl, bl)
+    check("dX", dX, wx, bx)
+    check("dW", dW, ww, bw)
