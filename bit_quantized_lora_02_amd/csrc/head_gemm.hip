@@ -410,6 +410,28 @@ __device__ __forceinline__ u32x4_t join_halves(const u32x2_t &lo, const u32x2_t 
   return u32x4_t{x[0], y[0], x[1], y[1]};
 }
 
+// Pieces a and b (16 bytes a lane, rows lane % 32, halves lane / 32) of adjacent columns.  Afterwards a holds rows 0..15
+// of both and b rows 16..31: lanes 0..15 and 32..47 the halves of what was a's columns, the others of b's, so a store
+// covers 64 contiguous bytes of a row, not 32 (dW of 622 x 50257 x 1024 81 -> 78 us, of 7 x 6463 x 5992 28 -> 25; no
+// change where stores are few).
+__device__ __forceinline__ void join_rows(u32x4_t &a, u32x4_t &b) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t aw = a[w], bw = b[w];
+    const auto x = __builtin_amdgcn_permlane16_swap(aw, bw, false, false);
+    a[w] = x[0], b[w] = x[1];
+  }
+}
+// Column of a lane's piece afterwards: halves are `half` columns long, b's columns `next` after a's.
+__device__ __forceinline__ int store_column(int lane, int half, int next) {
+  return (lane >> 5) * half + (lane >> 4 & 1) * next;
+}
+// Four binary32 values of an MFMA result as 16 bytes.
+__device__ __forceinline__ u32x4_t four(const f32x16_t &v, int q) {
+  return u32x4_t{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                 __float_as_uint(v[4 * q + 3])};
+}
+
 __device__ __forceinline__ int block_rows(const HeadRows &rows, int64_t row0, int64_t tb) {
   const int64_t n = *rows.n - row0;
   return n < 0 ? 0 : (int)(n < tb ? n : tb);
@@ -519,16 +541,17 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
       arrive<C::LB>();
 #pragma unroll
       for (int j = 0; j < C::WN; ++j) {
-        const int row = n0 + (wn * C::WN + j) * 32 + (lane & 31);
-        float *const out = g.part + ((int64_t)range * n + row) * g.lde + m0 + mlane;
+        const int row = n0 + (wn * C::WN + j) * 32 + (lane & 15), m = m0 + wm * C::WM * 32 + store_column(lane, 4, 8);
+        float *const out = g.part + ((int64_t)range * n + row) * g.lde + m;
 #pragma unroll
         for (int i = 0; i < C::WM; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x16_t &v = acc[i][j];
-            if (row < n && m0 + mlane + 32 * i + 8 * q < g.lde)
-              *reinterpret_cast<float4 *>(out + 32 * i + 8 * q) =
-                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          for (int q = 0; q < 4; q += 2) {
+            u32x4_t lo = four(acc[i][j], q), hi = four(acc[i][j], q + 1);
+            join_rows(lo, hi);
+            const int at = 32 * i + 8 * q;
+            if (m + at < g.lde && row < n) *reinterpret_cast<u32x4_t *>(out + at) = lo;
+            if (m + at < g.lde && row + 16 < n) *reinterpret_cast<u32x4_t *>(out + 16 * g.lde + at) = hi;
           }
       }
       return;
@@ -598,15 +621,16 @@ __device__ __forceinline__ void logit_items(const LogitArgs &g, int first, int n
       if (row < n && lane < 32 && m0 + wm * C::WM * 32 < V)
         g.stat[(int64_t)row * ntile + m0 / (C::WM * 32) + wm] = make_float2(u, sum);
       if (!E) continue;
-      // E lies in blocks of 32 columns, [column / 32][row][32]: a wave's store is 32 rows of 32 bytes
+      // E lies in blocks of 32 columns, [column / 32][row][32]: a wave's store is 16 whole rows of a block, 1 KB
+      const int first_row = n0 + (wn * C::WN + j) * 32 + (lane & 15);
 #pragma unroll
       for (int i = 0; i < C::WM; ++i) {
-        bf16_t *const out = E + ((m0 / 32 + wm * C::WM + i) * te + row) * 32 + 8 * (lane >> 5);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const u32x4_t o = join_halves(x[i][2 * q], x[i][2 * q + 1]);
-          if (row < n && m0 + (wm * C::WM + i) * 32 < g.lde) *reinterpret_cast<u32x4_t *>(out + 16 * q) = o;
-        }
+        bf16_t *const out = E + ((m0 / 32 + wm * C::WM + i) * te + first_row) * 32 + store_column(lane, 8, 16);
+        u32x4_t lo = join_halves(x[i][0], x[i][1]), hi = join_halves(x[i][2], x[i][3]);
+        join_rows(lo, hi);
+        const bool in = m0 + (wm * C::WM + i) * 32 < g.lde;
+        if (in && first_row < n) *reinterpret_cast<u32x4_t *>(out) = lo;
+        if (in && first_row + 16 < n) *reinterpret_cast<u32x4_t *>(out + 16 * 32) = hi;
       }
     }
   };
@@ -671,22 +695,26 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
     arrive<C::LB>();
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
-      const int i = n0 + (wn * C::WN + j) * 32 + (lane & 31);
-      const bool in = i < n;
-      const float4 f = scale[in ? i : n - 1];
-      const int64_t t = rows.list[row0 + (in ? i : n - 1)];
-      const bf16_t *const w = g.W + rows.refcol[t] * K + 4 * (lane >> 5);
+      const int base = n0 + (wn * C::WN + j) * 32;
+      const int i = min(base + (lane & 31), n - 1);     // the lane's row of the sums
+      const int lo_row = base + (lane & 15), hi_row = lo_row + 16;  // and those that it stores
+      const float4 f = scale[i];
+      const bf16_t *const w = g.W + rows.refcol[rows.list[row0 + i]] * K + 4 * (lane >> 5);
+      const int64_t lo_t = rows.list[row0 + min(lo_row, n - 1)], hi_t = rows.list[row0 + min(hi_row, n - 1)];
 #pragma unroll
       for (int mi = 0; mi < C::WM; ++mi) {
         const int64_t m = m0 + (wm * C::WM + mi) * 32;
         const f32x16_t &v = acc[mi][j];
         if (ranges > 1) {
+          const int64_t row = (int64_t)range * (n - first) + (lo_row - first);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int64_t mq = m + 8 * q + 4 * (lane >> 5);
-            if (in && mq < K)  // K % 8 == 0: eight columns are all in or all out
-              *reinterpret_cast<float4 *>(part + ((int64_t)range * (n - first) + (i - first)) * K + mq) =
-                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          for (int q = 0; q < 4; q += 2) {
+            u32x4_t lo = four(v, q), hi = four(v, q + 1);
+            join_rows(lo, hi);
+            const int64_t mq = m + 8 * q + store_column(lane, 4, 8);
+            // K % 8 == 0: eight columns are all in or all out
+            if (mq < K && lo_row < n) *reinterpret_cast<u32x4_t *>(part + row * K + mq) = lo;
+            if (mq < K && hi_row < n) *reinterpret_cast<u32x4_t *>(part + (row + 16) * K + mq) = hi;
           }
         } else {
           u32x2_t x[4];  // with the first target's remainder times its row of W
@@ -698,12 +726,11 @@ __device__ __forceinline__ void dx_items(const DxArgs &g, int first, int n, int 
                            pack_bf16x2(fmaf(f.y, bf16_lo_to_f32(wv.y), v[4 * q + 2]) * f.x,
                                        fmaf(f.y, bf16_hi_to_f32(wv.y), v[4 * q + 3]) * f.x)};
           }
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const u32x4_t o = join_halves(x[2 * q], x[2 * q + 1]);
-            const int64_t mq = m + 16 * q + 8 * (lane >> 5);
-            if (in && mq < K) *reinterpret_cast<u32x4_t *>(dX + t * K + mq) = o;
-          }
+          u32x4_t lo = join_halves(x[0], x[1]), hi = join_halves(x[2], x[3]);
+          join_rows(lo, hi);
+          const int64_t mq = m + store_column(lane, 8, 16);
+          if (mq < K && lo_row < n) *reinterpret_cast<u32x4_t *>(dX + lo_t * K + mq) = lo;
+          if (mq < K && hi_row < n) *reinterpret_cast<u32x4_t *>(dX + hi_t * K + mq) = hi;
         }
       }
     }
@@ -775,33 +802,41 @@ __device__ __forceinline__ void dw_items(const DwArgs &g, int begin_v, int end_v
     arrive<C::LB>();
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) {
-      const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 31);
+      const int64_t v = n0 + (wn * C::WN + j) * 32 + (lane & 15);
 #pragma unroll
       for (int mi = 0; mi < C::WM; ++mi) {
         const int64_t m = m0 + (wm * C::WM + mi) * 32;
         f32x16_t &o = acc[mi][j];
         if (sums) {
+          const int64_t at = n0 + (wn * C::WN + j) * 32 + (lane & 31);  // the lane's row of the sums
+          if (!g.first)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int64_t mq = m + 8 * q + 4 * (lane >> 5);
-            if (v >= end_v || mq >= K) continue;
-            float4 *const p = reinterpret_cast<float4 *>(sums + v * K + mq);
-            if (!g.first) {
-              const float4 was = *p;
+            for (int q = 0; q < 4; ++q) {
+              const int64_t mq = m + 8 * q + 4 * (lane >> 5);
+              if (at >= end_v || mq >= K) continue;
+              const float4 was = *reinterpret_cast<const float4 *>(sums + at * K + mq);
               o[4 * q] += was.x, o[4 * q + 1] += was.y, o[4 * q + 2] += was.z, o[4 * q + 3] += was.w;
             }
-            if (!g.last) *p = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-          }
-          if (!g.last) continue;
-        }
+          if (!g.last) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const u32x4_t x =
-              join_halves(u32x2_t{pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3])},
-                          u32x2_t{pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7])});
-          const int64_t mq = m + 16 * q + 8 * (lane >> 5);
-          if (v < end_v && mq < K) *reinterpret_cast<u32x4_t *>(dW + v * K + mq) = x;
+            for (int q = 0; q < 4; q += 2) {
+              u32x4_t lo = four(o, q), hi = four(o, q + 1);
+              join_rows(lo, hi);
+              const int64_t mq = m + 8 * q + store_column(lane, 4, 8);
+              if (mq < K && v < end_v) *reinterpret_cast<u32x4_t *>(sums + v * K + mq) = lo;
+              if (mq < K && v + 16 < end_v) *reinterpret_cast<u32x4_t *>(sums + (v + 16) * K + mq) = hi;
+            }
+            continue;
+          }
         }
+        u32x4_t lo = join_halves(u32x2_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])},
+                                 u32x2_t{pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])});
+        u32x4_t hi = join_halves(u32x2_t{pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11])},
+                                 u32x2_t{pack_bf16x2(o[12], o[13]), pack_bf16x2(o[14], o[15])});
+        join_rows(lo, hi);
+        const int64_t mq = m + store_column(lane, 8, 16);
+        if (mq < K && v < end_v) *reinterpret_cast<u32x4_t *>(dW + v * K + mq) = lo;
+        if (mq < K && v + 16 < end_v) *reinterpret_cast<u32x4_t *>(dW + (v + 16) * K + mq) = hi;
       }
     }
   };
@@ -822,6 +857,14 @@ __global__ __launch_bounds__(H256::NT) void k_head_dw(DwArgs g) {
   between_passes();
   items = second;
   dw_items<H128>(g, whole, (int)g.V, items, turn, ring);
+}
+
+// Few rows (T <= 64): bound by dW's stores, which three workgroups a CU overlap with each other's steps (7 x 6463 x 5992
+// 25 us, 3.1 TB/s, 28 in wide tiles; 1 x 1000 x 256 4.4, 7.4).
+__global__ __launch_bounds__(H64::NT) void k_head_dw_few(DwArgs g) {
+  QLORA_RING(H64, ring);
+  Items items = {(int)((g.K + H64::BM - 1) / H64::BM), (int)((g.V + H64::BN - 1) / H64::BN), 1};
+  dw_items<H64>(g, 0, (int)g.V, items, Turn{blockIdx.x, gridDim.x}, ring);
 }
 
 // Workgroups of a launch over `items` output tiles: as many as run at once (one per CU, three of the narrow tile), each
@@ -870,10 +913,15 @@ hipError_t launch_head_dx(const HeadRows &rows, int64_t row0, int64_t tb, const 
 hipError_t launch_head_dw(const HeadRows &rows, int64_t row0, int64_t tb, const bf16_t *E, int64_t lde, int64_t te,
                           const bf16_t *Xs, int64_t V, int64_t K, float *sums, bool first, bool last, int ranges,
                           bf16_t *dW, hipStream_t s) {
+  const DwArgs args = {rows, row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, ranges, dW};
+  if (rows.tile_rows == 64) {
+    const int64_t items = (K + H64::BM - 1) / H64::BM * ((V + H64::BN - 1) / H64::BN);
+    launch(k_head_dw_few, dim3((unsigned)groups(items, 64)), dim3(H64::NT), 0, s, args);
+    return hipGetLastError();
+  }
   const int64_t tiles_m = (K + 255) / 256, whole = head_whole_columns(V, (int)tiles_m);
   const int64_t items = tiles_m * (whole > 0 ? (whole + 255) / 256 : (V + H128::BN - 1) / H128::BN * ranges);
-  launch(k_head_dw, dim3((unsigned)groups(items, 256)), dim3(H256::NT), 0, s,
-         DwArgs{rows, row0, tb, E, lde, te, Xs, V, K, sums, first ? 1 : 0, last ? 1 : 0, ranges, dW});
+  launch(k_head_dw, dim3((unsigned)groups(items, 256)), dim3(H256::NT), 0, s, args);
   return hipGetLastError();
 }
 
