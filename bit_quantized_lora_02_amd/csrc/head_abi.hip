@@ -8,8 +8,8 @@ using namespace qlora;
 
 namespace {
 
-// E (2 bytes per row and column of the vocabulary), or without gradients the tile statistics, is held for a block of rows
-// at a time, of at most this many bytes: at 4096 rows of a 128256-wide vocabulary the products run at full size (256
+// E (2 bytes per row and column of the vocabulary), or without gradients the tile statistics, is held for a block of
+// rows at a time, of at most this many bytes: at 4096 rows of a 128256-wide vocabulary the products run at full size (256
 // tiles of dX), so larger blocks gain nothing and smaller ones would leave compute units idle.
 constexpr size_t kHeadBlockBytes = (size_t)1 << 30;
 
@@ -20,7 +20,6 @@ struct HeadPlan {
   size_t off_n = 0, off_ranges = 0, off_xt = 0, off_list = 0, off_ref = 0, off_col = 0, off_zt = 0, off_pt = 0,
          off_bucket = 0, off_target = 0, off_stat = 0, off_scale = 0, off_z = 0, off_e = 0, off_part = 0, off_xs = 0,
          off_sums = 0, total = 0;
-  bool split = false;  // dX may come as partial sums
   int ranges = 1;      // of the logit product's reduction
   int dw_ranges = 1;   // of the dW product's
 };
@@ -65,11 +64,7 @@ HeadPlan head_plan(int64_t T, int64_t V, int64_t K, int32_t k, bool dx, bool dw)
   p.ranges = p.b.count == 1 && T > 0 ? head_logit_ranges(T, V, K, p.b.tile_rows) : 1;
   if (p.ranges > 1) p.off_z = take((size_t)p.ranges * T * p.b.lde * 4);
   if (grad) p.off_e = take((size_t)p.b.te * p.b.lde * 2);
-  if (dx) {
-    const size_t part = head_part_floats(p.b.tb, K, p.b.tile_rows) * 4;
-    p.split = part > 0;
-    p.off_part = take(part);
-  }
+  if (dx) p.off_part = take(head_part_floats(p.b.tb, K, p.b.tile_rows) * 4);
   if (dw) {
     p.off_xs = take(up((size_t)p.b.tb, 128) * K * 2);
     p.dw_ranges = head_dw_ranges(T, V, K, p.b.count);
@@ -128,15 +123,15 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
   float2 *stat = (float2 *)(w + p.off_stat);
   float4 *scale = (float4 *)(w + p.off_scale);
   bf16_t *E = grad ? (bf16_t *)(w + p.off_e) : nullptr;
-  float *part = p.split ? (float *)(w + p.off_part) : nullptr;
+  float *part = dX ? (float *)(w + p.off_part) : nullptr;
   bf16_t *Xs = dW ? (bf16_t *)(w + p.off_xs) : nullptr;
   float *sums = p.off_sums ? (float *)(w + p.off_sums) : nullptr;
   bf16_t *Xt = (bf16_t *)(w + p.off_xt);
   int32_t *ranges = (int32_t *)(w + p.off_ranges);
   const float c = 1.44269504f / tau;
   const int64_t lde = p.b.lde, te = p.b.te;
-  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, ranges, p.b, rows, loss, dX, Xt,
-                                       p.ldx, s));
+  LAUNCH("head_prep", launch_head_prep(X, T, W, V, K, labels, index, logit, k, tau, n, list, ranges, p.b, rows, loss, dX,
+                                       Xt, p.ldx, s));
   const bool sorted = k > 0 && p.ranges == 1;  // the targets go by the product's tiles
   float *zpart = p.ranges > 1 ? (float *)(w + p.off_z) : nullptr;
   const bool few = k > 0 && head_few_targets(T, k, p.b.tile_rows);
@@ -155,7 +150,7 @@ int head_loss(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t V, in
                                                  scale, E, lde, te, X, K, Xs, s));
     if (tb > 0 && dX) {
       LAUNCH("head_dx", launch_head_dx(rows, row0, tb, E, lde, te, W, V, K, scale, part, dX, s));
-      if (part) LAUNCH("head_dx_reduce", launch_head_reduce(rows, row0, tb, part, W, K, scale, dX, s));
+      LAUNCH("head_dx_reduce", launch_head_reduce(rows, row0, tb, part, W, K, scale, dX, s));
     }
     if (dW && tb > 0) {
       LAUNCH("head_scale", launch_head_scale(rows, row0, tb, scale, E, lde, te, s));

@@ -634,3 +634,36 @@ def test_targets_in_narrow_tiles_of_a_wide_call(T, V, K, k, ignored):
     check("loss", loss, wl, bl)
     check("dX", dX, wx, bx)
     check("dW", dW, ww, bw)
+
+
+@pytest.mark.parametrize("T,V,K", [(5, 7, 1 << 22), (300, 33, 1 << 22), (70, 600, 1 << 20)])
+def test_the_longest_rows(T, V, K):
+    """n_in up to 2^22. X holds 0 and +-1, W 0 and +-1/4, at places shared by all rows, so every logit is a sum of
+    quarters that binary32 holds exactly in any order: it has no error, and the bounds are those above with dz = 0."""
+    print(f"T={T} V={V} K={K}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    at = torch.randperm(K, generator=g, device="cuda")[:300]
+    at[:4] = torch.tensor([0, K - 1, K - 8, K // 2], device="cuda")
+    at = at.unique()
+    sign = lambda *s: 2.0 * torch.randint(0, 2, s, generator=g, device="cuda") - 1.0  # noqa: E731
+    X, W = (torch.zeros(n, K, dtype=torch.bfloat16, device="cuda") for n in (T, V))
+    x, w = sign(T, len(at)), 0.25 * sign(V, len(at)) * (torch.rand(V, len(at), generator=g, device="cuda") < 0.2)
+    X[:, at], W[:, at] = x.to(torch.bfloat16), w.to(torch.bfloat16)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    y[1] = -100
+    loss, dX, dW = B.head_ce(X, W, y, need_dw=True)
+    x, w, keep = x.double(), w.double(), (y >= 0).double()[:, None]
+    logq = torch.log_softmax(x @ w.t(), 1)
+    nll = -logq.gather(1, y.clamp_min(0)[:, None])[:, 0] * keep[:, 0]
+    zmax = (x @ w.t()).abs().amax(1)
+    check("loss", loss, nll, 8 * U * (zmax + nll.abs() + 4))
+    P = torch.zeros_like(logq).scatter_(1, y.clamp_min(0)[:, None], 1.0)
+    G = (logq.exp() - P) * keep
+    dG = BF * G.abs() + (logq.exp() + P) * (16 * U * (zmax + 8))[:, None] * keep
+    for name, got, a, da, b, depth in (("dX", dX, G, dG, w, V), ("dW", dW, G.t(), dG.t() + BF * G.t().abs(), x, T)):
+        want = a @ b
+        bound = da @ b.abs() + (depth / 8 + 16) * U * (a.abs() @ b.abs()) + BF * want.abs() + 1e-30
+        check(name, got[:, at], want, bound * (1 + 2.0 ** -6))
+        rest = got.clone()
+        rest[:, at] = 0
+        assert (rest == 0).all(), f"{name} is not zero where its factor is"
