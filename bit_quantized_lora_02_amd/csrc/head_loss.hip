@@ -468,7 +468,9 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   for (int j = lane; j < entries; j += 64) {
     const float2 v = st[j];
     u = fmaxf(u, v.x);
-    sum += v.x == ref ? v.y : 0.f;
+    // (units are the reference or above it, but where the columns hold a NaN: theirs is the largest of the others, their sum
+    // NaN, and the row's loss and gradients are to be)
+    sum += v.x > ref ? 0.f : v.y;
   }
   u = wave_max(u);
   float S, eref = 1.f, rest, nlogq;

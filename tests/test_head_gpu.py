@@ -667,3 +667,38 @@ def test_the_longest_rows(T, V, K):
         rest = got.clone()
         rest[:, at] = 0
         assert (rest == 0).all(), f"{name} is not zero where its factor is"
+
+
+# (64-row tiles, the same in ranges, 128-row tiles in ranges, 128- and 256-row tiles)
+EVERY_TILE = [(3, 300, 264), (7, 1300, 2048), (100, 700, 2056), (90, 40000, 128), (300, 33000, 136)]
+
+
+def same_kind(name, got, want):
+    """NaN where the definition gives NaN, an infinity where it gives that one, finite otherwise."""
+    got, want = got.double().cpu(), want.double().cpu()
+    for kind, of in (("NaN", torch.isnan), ("+inf", torch.isposinf), ("-inf", torch.isneginf)):
+        wrong = of(got) != of(want)
+        assert not wrong.any(), f"{name}: {int(wrong.sum())} of {wrong.numel()} entries are {kind} where the definition " \
+                                f"is not, or the reverse"
+
+
+@pytest.mark.parametrize("T,V,K", EVERY_TILE)
+def test_nan_in_the_output_layer(T, V, K):
+    """A NaN in one row of W, no row's target and far below most targets' logits: every row's softmax is NaN, so each
+    counted row's loss and dX and all of dW are."""
+    print(f"NaN in W T={T} V={V} K={K}", flush=True)
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=T + 1, lift=30.0))
+    at = V // 2
+    y[y == at] = at + 1
+    y[1] = -100
+    W[at, K // 2] = float("nan")
+    keep = (y >= 0)[:, None]
+    index = torch.stack([y, torch.where(y < 0, -1, (y + V // 3) % at)], 1).to(torch.int32)
+    logit = torch.tensor([3.0, 1.0], device="cuda").repeat(T, 1)
+    for name, got in (("ce", B.head_ce(X, W, y, weight, need_dw=True)), ("ce, loss alone", B.head_ce(X, W, y, need_dx=False)),
+                      ("kd", B.head_distill(X, W, index, logit, 2.0, weight, need_dw=True))):
+        nan = lambda *s: torch.full(s, float("nan"), device="cuda")  # noqa: E731
+        same_kind(f"{name} loss", got[0], torch.where(keep[:, 0], nan(T), 0.0))
+        if got[1] is not None:
+            same_kind(f"{name} dX", got[1], torch.where(keep, nan(T, K), 0.0))
+            same_kind(f"{name} dW", got[2], nan(V, K))
