@@ -486,11 +486,15 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
     nlogq = logf(rest + eref) + (u - ref) / tau;
   }
   S = rest + eref;
-  float h = 0.f;  // sum_i p_i (log p_i - (z_i - z_r) / tau)
+  const int32_t rc = rows.refcol[t];
+  // sum_i p_i (log p_i - (z_i - z_r) / tau).  At the first target's column z_i is z_r, though the product's and the dot's
+  // sums of it differ in their last places, which would outweigh the loss of a sure row.
+  float h = 0.f;
   if (!labels)
     for (int j = lane; j < k; j += 64) {
       const float p = rows.pt[t * k + j];
-      if (p > 0.f) h += p * (logf(p) - (rows.zt[t * k + j] - ref) / tau);
+      const float z = index[t * k + j] == rc ? 0.f : (rows.zt[t * k + j] - ref) / tau;
+      if (p > 0.f) h += p * (logf(p) - z);
     }
   h = wave_sum(h);
   if (lane == 0) loss[t] = tau * tau * (h + nlogq);
@@ -508,7 +512,6 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   }
   const float f = (weight ? weight[t] : 1.f) * tau / S;
   // The first target's entry is the row's largest as a rule; what its rounding to bf16 leaves goes to dX in binary32.
-  const int32_t rc = rows.refcol[t];
   int ex;
   const float fm = frexpf(f, &ex);
   auto first_target = [&](float g) {

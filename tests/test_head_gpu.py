@@ -702,3 +702,28 @@ def test_nan_in_the_output_layer(T, V, K):
         if got[1] is not None:
             same_kind(f"{name} dX", got[1], torch.where(keep, nan(T, K), 0.0))
             same_kind(f"{name} dW", got[2], nan(V, K))
+
+
+@pytest.mark.parametrize("T,V,K", EVERY_TILE)
+@pytest.mark.parametrize("k,tau", [(1, 1.0), (4, 2.0)])
+def test_distillation_losses_near_zero_keep_their_digits(T, V, K, k, tau):
+    """A one-hot teacher whose target stands 20 to 60 (of tau) above the rest: p log p is 0, so the loss is tau^2 log1p of
+    the others, and is held to the relative bound of the logits' own error as the cross entropy's is."""
+    print(f"near zero T={T} V={V} K={K} k={k} tau={tau}", flush=True)
+    X, W, y, _ = (t.cuda() for t in inputs(T, V, K, seed=T + 3, spread=0.5, lift=0.0))
+    up = 4 * tau * torch.linspace(20, 60, T, dtype=torch.float64, device="cuda")[:, None]
+    X = (X.double() + W[y].double() * up).to(torch.bfloat16)
+    z = X.double() @ W.double().t()
+    dz = (K / 8 + 16) * U * (X.double().abs() @ W.double().abs().t()).amax(1)
+    rest = ((z - z.gather(1, y[:, None])) / tau).scatter(1, y[:, None], -float("inf")).exp().sum(1)
+    want = tau * tau * torch.log1p(rest)
+    index = torch.stack([(y + 5 * i) % V for i in range(k)], 1).to(torch.int32)
+    logit = torch.full((T, k), -float("inf"), device="cuda")
+    logit[:, 0] = 7.0
+    loss, dX, _ = B.head_distill(X, W, index, logit, tau)
+    rel = 2 * dz / tau + 16 * U * (z.abs().amax(1) / tau + 4)
+    assert (want > 0).all()
+    over = (loss.double() - want).abs() - (rel * want * (1 + 2.0 ** -6) + 1e-44)
+    assert over.max() <= 0, f"{int((over > 0).sum())} of {T} losses beyond the bound, worst {loss[over.argmax()]:.3e} for " \
+                            f"{want[over.argmax()]:.3e}"
+    assert torch.isfinite(dX).all()
