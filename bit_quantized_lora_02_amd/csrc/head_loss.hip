@@ -476,7 +476,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
   float S, eref = 1.f, rest, nlogq;
   const bool wide = u != ref;  // some tile's logits are far above the reference: the row takes the largest unit
   if (!wide) {
-    rest = wave_sum(sum);
+    rest = ref == INFINITY ? NAN : wave_sum(sum);  // (against +inf every finite logit's term is 0)
     nlogq = log1pf(rest);
   } else {
     sum = 0.f;

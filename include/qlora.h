@@ -362,7 +362,9 @@ int qlora_adamw8_step(const qlora_adamw8_tensor *tensors, int32_t count, double 
  * multiplies dX in binary32 (for dW its fraction multiplies the rounded entries,
  * which are rounded once more, the targets' excepted; its power of two multiplies
  * X exactly); the products accumulate in binary32 and are rounded to bf16 once.
- * Reductions run in a fixed order: results are bitwise repeatable.
+ * Reductions run in a fixed order: results are bitwise repeatable.  A logit of
+ * NaN or +inf makes its row's loss and dX, and dW, NaN; a target's logit of -inf
+ * makes the loss +inf.
  *
  * X, W, dX, dW 16-byte aligned, labels 8-byte, loss and weight 4-byte; none
  * may overlap an output.  n_in % 8 == 0, n_vocab >= 1, both at most 2^22,

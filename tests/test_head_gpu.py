@@ -727,3 +727,30 @@ def test_distillation_losses_near_zero_keep_their_digits(T, V, K, k, tau):
     assert over.max() <= 0, f"{int((over > 0).sum())} of {T} losses beyond the bound, worst {loss[over.argmax()]:.3e} for " \
                             f"{want[over.argmax()]:.3e}"
     assert torch.isfinite(dX).all()
+
+
+@pytest.mark.parametrize("T,V,K", EVERY_TILE)
+def test_infinite_logits(T, V, K):
+    """An infinity in one row of W makes logits of +inf and -inf, the target's among them: the loss is what the definition
+    gives, NaN beside a +inf, +inf for a target at -inf, and the finite value where another column is at -inf."""
+    print(f"infinity in W T={T} V={V} K={K}", flush=True)
+    X, W, y, _ = (t.cuda() for t in inputs(T, V, K, seed=T + 2))
+    X[:, 0] = X[:, 0].abs() + 0.5
+    X[::2, 0] *= -1.0
+    at = V // 2
+    y[:T // 2 + 1] = at
+    W[at, 0] = float("inf")
+    z = X.double() @ torch.where(torch.isinf(W), torch.zeros_like(W), W).double().t()
+    dz = (K / 8 + 16) * U * (X.double().abs() @ torch.where(torch.isinf(W), torch.zeros_like(W), W).double().abs().t()).amax(1)
+    zmax = z.abs().amax(1)
+    z[:, at] = X[:, 0].double() * float("inf")
+    want = -torch.log_softmax(z, 1).gather(1, y[:, None])[:, 0]
+    assert {float("inf")} < {float(v) for v in want} and torch.isnan(want).any() and torch.isfinite(want).any()
+    index = y[:, None].to(torch.int32)
+    for name, loss in (("ce", B.head_ce(X, W, y, need_dx=False)[0]), ("ce with dX", B.head_ce(X, W, y)[0]),
+                       ("kd", B.head_distill(X, W, index, torch.ones(T, 1, device="cuda"), need_dx=False)[0])):
+        same_kind(name, loss, want)
+        ok = torch.isfinite(want)
+        check(name, loss[ok], want[ok], ((2 * dz + 8 * U * (zmax + want.abs() + 4)) * (1 + 2.0 ** -6))[ok])
+    _, dX, dW = B.head_ce(X, W, y, need_dw=True)
+    assert torch.isnan(dX[torch.isnan(want)]).all() and torch.isnan(dW).all()
