@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
       __syncthreads();
 #pragma unroll 4
       for (int e = tid; e < (int)T * k; e += kPrepThreads)
-        if (target_ok(index[e], V) && logit[e] > -INFINITY) s_counts[e / k] = 1;
+        if (target_ok(index[e], V) && logit[e] != -INFINITY) s_counts[e / k] = 1;
       __syncthreads();
       number_rows<kPrepThreads>(T, K, [&](int64_t t) { return s_counts[t] != 0; }, n, list, ranges, blocks);
       __syncthreads();
@@ -272,7 +272,8 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
   if (labels) {
     y = labels[t];
     if (!target_ok(y, V)) y = -1;
-  } else {  // the teacher's softmax over the row's targets, up to four per lane
+  } else {  // the teacher's softmax over the row's targets, up to four per lane (NaN is taken for +inf: either counts and
+            // leaves the row's probabilities NaN)
     float tl[4], top = -INFINITY;
     int id[4];
 #pragma unroll
@@ -280,6 +281,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_head_prep(const bf16_t *__rest
       const int i = lane + 64 * j;
       id[j] = i < k ? index[t * k + i] : -1;
       tl[j] = target_ok(id[j], V) ? logit[t * k + i] : -INFINITY;
+      if (tl[j] != tl[j]) tl[j] = INFINITY;
       top = fmaxf(top, tl[j]);
     }
     top = wave_max(top);
@@ -494,7 +496,7 @@ __global__ __launch_bounds__(256) void k_head_combine(HeadRows rows, int64_t row
     for (int j = lane; j < k; j += 64) {
       const float p = rows.pt[t * k + j];
       const float z = index[t * k + j] == rc ? 0.f : (rows.zt[t * k + j] - ref) / tau;
-      if (p > 0.f) h += p * (logf(p) - z);
+      if (p != 0.f) h += p * (logf(p) - z);
     }
   h = wave_sum(h);
   if (lane == 0) loss[t] = tau * tau * (h + nlogq);

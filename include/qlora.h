@@ -389,10 +389,11 @@ int qlora_head_ce(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int64_t n
  * (the gradient of weight[t] loss[t] by z).  An entry whose index is outside
  * [0, n_vocab) or whose logit is -inf has no part (fill short lists with -1); a
  * row without any other entry is ignored as in qlora_head_ce.  The same index
- * twice in a row adds its probabilities.  Logits are otherwise finite.  The loss
- * of a one-hot teacher keeps its digits near 0 as the cross entropy's does; where
- * several entries share the probability their terms cancel, and a loss near 0 is
- * held to the binary32 error of the logits' differences.
+ * twice in a row adds its probabilities.  Logits are otherwise finite: one of
+ * NaN or +inf makes its row's loss and dX NaN.  The loss of a one-hot teacher
+ * keeps its digits near 0 as the cross entropy's does; where several entries
+ * share the probability their terms cancel, and a loss near 0 is held to the
+ * binary32 error of the logits' differences.
  * 1 <= k <= QLORA_MAX_TARGETS, 1e-4 <= tau <= 1e4.  index and logit are 4-byte
  * aligned.
  * ws: qlora_head_workspace_bytes(T, n_vocab, n_in, k, dX != NULL, dW != NULL).

@@ -754,3 +754,24 @@ def test_infinite_logits(T, V, K):
         check(name, loss[ok], want[ok], ((2 * dz + 8 * U * (zmax + want.abs() + 4)) * (1 + 2.0 ** -6))[ok])
     _, dX, dW = B.head_ce(X, W, y, need_dw=True)
     assert torch.isnan(dX[torch.isnan(want)]).all() and torch.isnan(dW).all()
+
+
+@pytest.mark.parametrize("T,V,K", EVERY_TILE)
+@pytest.mark.parametrize("k", [1, 5, 100])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_teacher_logits_that_are_not_finite(T, V, K, k, bad):
+    """A NaN or +inf among a row's teacher logits leaves it without probabilities: its loss and dX are NaN, not those of an
+    ignored row; the other rows are as without it."""
+    print(f"teacher's {bad} T={T} V={V} K={K} k={k}", flush=True)
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=T + 4))
+    index = torch.stack([(y + 2 * i) % V for i in range(k)], 1).to(torch.int32)
+    logit = torch.randn(T, k, generator=torch.Generator(device="cuda").manual_seed(k), device="cuda")
+    index[2] = -1
+    want = B.head_distill(X, W, index, logit, 1.5, weight)[:2]
+    logit[0, k - 1] = bad  # one of the row's
+    logit[1] = bad  # all of them
+    logit[2, 0] = bad  # of an entry that has no part
+    loss, dX, _ = B.head_distill(X, W, index, logit, 1.5, weight)
+    assert torch.isnan(loss[:2]).all(), loss[:2]
+    assert torch.isnan(dX[:2]).all()
+    assert torch.equal(loss[2:], want[0][2:]) and torch.equal(dX[2:], want[1][2:])
