@@ -671,9 +671,9 @@ def _sum(x):
     return x.sum()
 
 
-def _head_total(ctx, loss, weight, dX, dW, weight_at):
+def _head_total(ctx, loss, weight, dX, dW, weight_at, recorded):
     ctx.have = (dX is not None, dW is not None)
-    ctx.weight_at = weight_at if weight is not None and ctx.needs_input_grad[weight_at] else None
+    ctx.weight_at = weight_at if recorded and weight is not None and ctx.needs_input_grad[weight_at] else None
     ctx.save_for_backward(*(t for t in (dX, dW, loss if ctx.weight_at else None) if t is not None))
     ctx.mark_non_differentiable(loss)
     # (an ignored row's weight may be anything)
@@ -694,15 +694,21 @@ def _head_grads(ctx, g):
 class HeadCEFn(torch.autograd.Function):
     """Autograd wrapper of ``head_ce``: forward(X, W, labels, weight) -> (sum(weight * loss), loss [T]).
 
-    The gradients are formed with the losses, in one call, for those of X and W that need them; the backward
-    multiplies them by the incoming scalar (and the losses, for a weight that needs a gradient). The per-token losses
-    carry no gradient. Forward and backward can be captured into a HIP graph, as any autograd function, where no eager
-    graph of the same leaves is alive."""
+    The gradients are formed with the losses, in one call, for those of X and W that need them (for neither where
+    gradients are off, as under ``torch.no_grad``); the backward multiplies them by the incoming scalar (and the losses,
+    for a weight that needs a gradient). The per-token losses carry no gradient. Forward and backward can be captured
+    into a HIP graph, as any autograd function, where no eager graph of the same leaves is alive."""
+
+    @classmethod
+    def apply(cls, X, W, labels, weight=None):
+        # (inside forward gradients are always off, and needs_input_grad does not know whether they were before)
+        return super().apply(X, W, labels, weight, torch.is_grad_enabled())
 
     @staticmethod
-    def forward(ctx, X, W, labels, weight=None):
-        loss, dX, dW = head_ce(X, W, labels, weight, need_dx=ctx.needs_input_grad[0], need_dw=ctx.needs_input_grad[1])
-        return _head_total(ctx, loss, weight, dX, dW, 3)
+    def forward(ctx, X, W, labels, weight, recorded):
+        loss, dX, dW = head_ce(X, W, labels, weight, need_dx=recorded and ctx.needs_input_grad[0],
+                               need_dw=recorded and ctx.needs_input_grad[1])
+        return _head_total(ctx, loss, weight, dX, dW, 3, recorded)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -715,13 +721,17 @@ class HeadDistillFn(torch.autograd.Function):
 
     As ``HeadCEFn``; the teacher's logits get no gradient, so ones that ask for it are refused."""
 
+    @classmethod
+    def apply(cls, X, W, index, logit, tau=1.0, weight=None):
+        return super().apply(X, W, index, logit, tau, weight, torch.is_grad_enabled())
+
     @staticmethod
-    def forward(ctx, X, W, index, logit, tau=1.0, weight=None):
-        if ctx.needs_input_grad[3]:
+    def forward(ctx, X, W, index, logit, tau, weight, recorded):
+        if recorded and ctx.needs_input_grad[3]:
             raise ValueError("the teacher's logits get no gradient: detach them")
-        loss, dX, dW = head_distill(X, W, index, logit, tau, weight, need_dx=ctx.needs_input_grad[0],
-                                    need_dw=ctx.needs_input_grad[1])
-        return _head_total(ctx, loss, weight, dX, dW, 5)
+        loss, dX, dW = head_distill(X, W, index, logit, tau, weight, need_dx=recorded and ctx.needs_input_grad[0],
+                                    need_dw=recorded and ctx.needs_input_grad[1])
+        return _head_total(ctx, loss, weight, dX, dW, 5, recorded)
 
     @staticmethod
     @torch.autograd.function.once_differentiable

@@ -131,3 +131,46 @@ def test_distill_function_refuses_teacher_gradients():
     index, logit = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1, requires_grad=True)
     with pytest.raises(ValueError, match="teacher's logits get no gradient"):
         B.HeadDistillFn.apply(X, W, index, logit)
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_functions_form_no_gradient_where_none_is_recorded(monkeypatch, op, mode):
+    """Scoring with trained operands: neither dX nor dW is asked for with gradients off, both are with them on (head_ce and
+    head_distill stand-ins on the CPU record what they are asked for)."""
+    T, V, K = 3, 5, 8
+    asked = []
+
+    def call(X, W, *targets, need_dx=True, need_dw=False):
+        asked.append((need_dx, need_dw))
+        return torch.ones(T), torch.full((T, K), 2.0, dtype=bf) if need_dx else None, \
+            torch.full((V, K), 3.0, dtype=bf) if need_dw else None
+
+    monkeypatch.setattr(B, "head_ce", call)
+    monkeypatch.setattr(B, "head_distill", call)
+    X, W, weight = torch.zeros(T, K, dtype=bf), torch.zeros(V, K, dtype=bf), torch.full((T,), 0.5)
+    for t in (X, W, weight):
+        t.requires_grad_(True)
+    index, logit = torch.zeros(T, 1, dtype=torch.int32), torch.zeros(T, 1)
+    if op == "ce":
+        calls = [lambda: B.HeadCEFn.apply(X, W, torch.zeros(T, dtype=torch.int64)),
+                 lambda: B.HeadCEFn.apply(X, W, torch.zeros(T, dtype=torch.int64), weight)]
+    else:
+        calls = [lambda: B.HeadDistillFn.apply(X, W, index, logit),
+                 lambda: B.HeadDistillFn.apply(X, W, index, logit, 2.0, weight)]
+    for fn, total in zip(calls, (3.0, 1.5)):
+        with mode():
+            got, loss = fn()
+        assert asked.pop() == (False, False) and not got.requires_grad and got == total and loss.shape == (T,)
+        got, loss = fn()
+        assert asked.pop() == (True, True) and got.requires_grad and not loss.requires_grad and got == total
+        got.backward()
+        assert (X.grad == 2.0).all() and (W.grad == 3.0).all()
+        assert weight.grad is None if total == 3.0 else (weight.grad == 1.0).all()
+        X.grad = W.grad = None
+    if op == "kd":  # a teacher's logits that ask for a gradient are refused only where one would be recorded
+        logit.requires_grad_(True)
+        with mode():
+            calls[0]()
+        with pytest.raises(ValueError, match="teacher's logits get no gradient"):
+            calls[0]()
