@@ -775,3 +775,22 @@ def test_teacher_logits_that_are_not_finite(T, V, K, k, bad):
     assert torch.isnan(loss[:2]).all(), loss[:2]
     assert torch.isnan(dX[:2]).all()
     assert torch.equal(loss[2:], want[0][2:]) and torch.equal(dX[2:], want[1][2:])
+
+
+@pytest.mark.parametrize("T,V,K,k", [(1, 1000, 264, 0), (65, 300, 128, 3), (129, 1030, 200, 0), (513, 2055, 256, 9),
+                                     (35, 640, 4104, 3), (700, 33000, 520, 3), (5000, 300, 520, 0), (2000, 130, 1032, 2),
+                                     (64, 40000, 1032, 64), (1, 8, 8, 1)])
+def test_fills_the_buffers_it_is_given(T, V, K, k):
+    """The caller's loss, dX and dW, whatever they held, hold bit for bit what a call that makes its own returns."""
+    print(f"given buffers T={T} V={V} K={K} k={k}", flush=True)
+    X, W, y, weight = (t.cuda() for t in inputs(T, V, K, seed=2))
+    index = torch.stack([(y + 3 * i) % V for i in range(max(k, 1))], 1).to(torch.int32)
+    logit = torch.randn(T, max(k, 1), device="cuda")
+    call = (lambda **n: B.head_distill(X, W, index, logit, 1.5, weight, **n)) if k else \
+        (lambda **n: B.head_ce(X, W, y, weight, **n))
+    for dx, dw in ((True, True), (False, True)):
+        want = call(need_dx=dx, need_dw=dw)
+        nan = lambda t: None if t is None else torch.full_like(t, float("nan"))  # noqa: E731
+        outs = tuple(nan(t) for t in want)
+        call(outs=outs)
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[2], want[2]) and (not dx or torch.equal(outs[1], want[1]))
