@@ -10,7 +10,8 @@ namespace {
 
 // E (2 bytes per row and column of the vocabulary), or without gradients the tile statistics, is held for a block of
 // rows at a time, of at most this many bytes: at 4096 rows of a 128256-wide vocabulary the products run at full size (256
-// tiles of dX), so larger blocks gain nothing and smaller ones would leave compute units idle.
+// tiles of dX), so larger blocks would gain logits and dX nothing and smaller ones would leave compute units idle.  dW
+// reads and writes its carried sums once per block, which larger ones would save some of.
 constexpr size_t kHeadBlockBytes = (size_t)1 << 30;
 
 struct HeadPlan {
@@ -79,7 +80,8 @@ int check_head_sizes(int64_t T, int64_t V, int64_t K) {
   if (V < 1 || V > kMaxDim || K < 8 || K > kMaxDim || K % 8 != 0)
     return fail(QLORA_EINVAL, "need n_vocab >= 1 and n_in a positive multiple of 8, each at most 2^22 (got %lld x %lld)",
                 (long long)V, (long long)K);
-  // (rows of X are addressed by 32-bit byte offsets)
+  // (T n_in: no kernel needs this limit, offsets into X, its copies and dX are 64 bits wide or within a block of 32 columns;
+  // larger batches have not been run)
   if (V * K > kMaxWeights || T * K >= (int64_t)1 << 31)
     return fail(QLORA_EINVAL, "n_vocab x n_in must be at most 2^34 and T x n_in below 2^31 (got T=%lld, %lld x %lld)",
                 (long long)T, (long long)V, (long long)K);

@@ -336,19 +336,32 @@ int qlora_adamw8_step(const qlora_adamw8_tensor *tensors, int32_t count, double 
  * layer (bf16, device), z = X . W^T.  The [T, n_vocab] logits are not kept:
  * the losses come from softmax statistics of pieces of the vocabulary, and the
  * gradients from bf16 values exp(z - reference) of a bounded block of rows in
- * the workspace (at most 1 GiB of them however many tokens there are; 256 rows
- * at least).  Besides them the workspace holds a copy of X, 8 bytes of
- * statistics per 64 columns and row of a block, and binary32 partial sums where
- * a product has few output tiles (few rows or a small vocabulary: of the
- * logits too).
+ * the workspace.  The workspace holds
+ *   - a copy of X, n_in rounded up to 128;
+ *   - 8 bytes of statistics per 64 columns and row of a block (without gradients
+ *     a block is what fits 1 GiB of them, 256 rows at least);
+ *   - with dX or dW the block's values, 2 bytes per row and column (at most 1 GiB
+ *     however many tokens there are; 256 rows at least);
+ *   - with dX binary32 partial sums of up to 32 ranges of the vocabulary, 4 n_in
+ *     bytes per row of a block and range, at most 384 MiB, kept whether or not
+ *     the rows that count make the call use them;
+ *   - with dW a scaled copy of a block's rows of X, and where there are several
+ *     blocks the binary32 sums that are carried from one to the next, 4 n_vocab
+ *     n_in bytes (8192 x 128256 x 4096: 2.0 of 3.5 GiB);
+ *   - binary32 sums of a product with few output tiles whose reduction is split
+ *     (the logits of few rows or a small vocabulary, dW of a small one), at most
+ *     32 MiB each;
+ *   - the rows' list and factors, and a teacher's targets (12 bytes each and a
+ *     table of 4 bytes per column tile and tile of rows).
  *
  * Cross entropy, y_t = labels[t] (device int64):
  *   loss[t] = log(sum_v exp(z_tv)) - z_t,y        [T] binary32
  *   G_tv    = weight[t] (softmax(z_t)_v - [v = y_t])
  *   dX = G . W   [T, n_in] bf16,   dW = G^T . X   [n_vocab, n_in] bf16
  * A row whose label is outside [0, n_vocab) (-100, say) is ignored: its loss
- * is 0, its dX row 0, its X row is not read (it may hold anything), and no
- * work is spent on it.
+ * is 0, its dX row 0, its X row is not read (it may hold anything), and the
+ * products do not contain it (where dW takes several blocks, one without counted
+ * rows still passes the carried sums on).
  * weight: [T] binary32, finite, the rows' factors in the gradients (1 / number
  * of counted tokens for a mean), or NULL for 1; the losses are not multiplied.
  * dX and dW are overwritten; either may be NULL (a frozen output layer needs
@@ -361,7 +374,9 @@ int qlora_adamw8_step(const qlora_adamw8_tensor *tensors, int32_t count, double 
  * to bf16 once for the matrix unit, before the row's factor weight / sum, which
  * multiplies dX in binary32 (for dW its fraction multiplies the rounded entries,
  * which are rounded once more, the targets' excepted; its power of two multiplies
- * X exactly); the products accumulate in binary32 and are rounded to bf16 once.
+ * X exactly).  Where the other logits' terms of 64 or 128 columns reach 2^40 times
+ * the target's, the row's entries are brought to a common unit and rounded once more
+ * for that, the targets' excepted.  The products accumulate in binary32 and are rounded to bf16 once.
  * Reductions run in a fixed order: results are bitwise repeatable.  A logit of
  * NaN or +inf makes its row's loss and dX, and dW, NaN; a target's logit of -inf
  * makes the loss +inf.

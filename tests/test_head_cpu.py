@@ -174,3 +174,27 @@ def test_functions_form_no_gradient_where_none_is_recorded(monkeypatch, op, mode
             calls[0]()
         with pytest.raises(ValueError, match="teacher's logits get no gradient"):
             calls[0]()
+
+
+@pytest.mark.parametrize("T", [1, 300, 4096, 8192, 65536, 1 << 18])
+@pytest.mark.parametrize("V,K", [(1000, 256), (32000, 4096), (128256, 4096), (1 << 20, 1024)])
+def test_workspace_holds_what_the_header_names(T, V, K):
+    """Every part of the workspace, as the header lists it, with and without dX and dW."""
+    lde, rows = -(-V // 128) * 128, T + 15
+    most = min(T + 15, max(256, (1 << 30) // (2 * lde)) + 15)  # rows of a block of E
+    x = -(-K // 128) * 256 * rows
+    few = 40 << 20  # binary32 sums of a product with at most half as many output tiles as workgroups
+    lists = 32 * T + 4096
+    for dx in (False, True):
+        for dw in (False, True):
+            grad = dx or dw
+            e = 2 * lde * most * grad
+            stat = 8 * (V // 64 + 1) * most if grad else max(1 << 30, 256 * 8 * (V // 64 + 1))
+            parts = 4 * min(32 * most * K, 4 * 256 * 384 * 256) * dx
+            copy = 2 * (most + 128) * K * dw
+            carried = 4 * V * K * (dw and T > most)
+            bound = x + e + stat + lists + parts + copy + carried + few * (1 + dw)
+            got = B.head_workspace_bytes(T, V, K, 0, dx, dw)
+            assert got <= bound, (dx, dw, got, bound)
+            if carried:
+                assert got > carried
