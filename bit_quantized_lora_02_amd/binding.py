@@ -696,8 +696,9 @@ class HeadCEFn(torch.autograd.Function):
 
     The gradients are formed with the losses, in one call, for those of X and W that need them (for neither where
     gradients are off, as under ``torch.no_grad``); the backward multiplies them by the incoming scalar (and the losses,
-    for a weight that needs a gradient). The per-token losses carry no gradient. Forward and backward can be captured
-    into a HIP graph, as any autograd function, where no eager graph of the same leaves is alive."""
+    for a weight that needs a gradient). They are bf16, so a scalar that is no power of two rounds them once more: a mean's
+    1 / n belongs into ``weight``. The per-token losses carry no gradient. Forward and backward can be captured into a HIP
+    graph, as any autograd function, where no eager graph of the same leaves is alive."""
 
     @classmethod
     def apply(cls, X, W, labels, weight=None):
