@@ -7,9 +7,9 @@ library is missing or the device is not gfx950, calls raise.
 
 Names follow the C ABI: ``quantize_nf4``, ``dequant``, ``linear_fwd``,
 ``linear_bwd``, ``linear_fwd_dropout``, ``linear_bwd_dropout``, ``linear_fwd_multi``, ``adamw_step``,
-``adamw8_step``, ``merge``, ``head_ce``, ``head_distill``, plus ``QLoRALinearFn`` (a torch.autograd.Function whose backward
+``adamw8_step``, ``merge``, ``head_ce``, ``head_distill``, ``embed``, ``embed_bwd``, ``layer_norm``, ``layer_norm_bwd``, plus ``QLoRALinearFn`` (a torch.autograd.Function whose backward
 returns gradients for X, A and B and none for the frozen NF4 weight), ``HeadCEFn`` and ``HeadDistillFn``
-(the output layer's losses with their gradients).
+(the output layer's losses with their gradients), ``EmbedFn`` and ``LayerNormFn``.
 """
 from __future__ import annotations
 
@@ -34,6 +34,9 @@ OP_FWD_DROPOUT = 2
 OP_FWD_MULTI = 3
 MAX_RANK = 128
 MAX_TARGETS = 256
+MAX_NORM = 32768
+WEIGHT_BF16 = 0
+WEIGHT_F32 = 1
 
 EXPORTED = (
     "qlora_nf4_storage",
@@ -53,6 +56,12 @@ EXPORTED = (
     "qlora_head_ce",
     "qlora_head_distill",
     "qlora_head_workspace_bytes",
+    "qlora_embed",
+    "qlora_embed_bwd",
+    "qlora_embed_workspace_bytes",
+    "qlora_layer_norm",
+    "qlora_layer_norm_bwd",
+    "qlora_layer_norm_workspace_bytes",
     "qlora_strerror",
     "qlora_last_error",
     "qlora_timing_enable",
@@ -138,6 +147,12 @@ def load_library() -> ctypes.CDLL:
         "qlora_head_distill": ([P, i64, P, i64, i64, P, P, i32, ctypes.c_float, P, P, P, P, P, sz, P], ctypes.c_int),
         "qlora_head_workspace_bytes": ([i64, i64, i64, i32, ctypes.c_int, ctypes.c_int, ctypes.POINTER(sz)],
                                        ctypes.c_int),
+        "qlora_embed": ([P, i64, P, i64, i64, ctypes.c_float, P, P], ctypes.c_int),
+        "qlora_embed_bwd": ([P, P, i64, i64, i64, ctypes.c_float, ctypes.c_int, P, P, sz, P], ctypes.c_int),
+        "qlora_embed_workspace_bytes": ([i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
+        "qlora_layer_norm": ([P, i64, i64, P, P, ctypes.c_int, ctypes.c_float, P, P, P, P], ctypes.c_int),
+        "qlora_layer_norm_bwd": ([P, P, i64, i64, P, ctypes.c_int, P, P, P, P, P, P, sz, P], ctypes.c_int),
+        "qlora_layer_norm_workspace_bytes": ([i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
         "qlora_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "qlora_last_error": ([], ctypes.c_char_p),
         "qlora_timing_enable": ([ctypes.c_char_p, ctypes.c_int], ctypes.c_int),
@@ -646,6 +661,160 @@ def head_distill(X: torch.Tensor, W: torch.Tensor, index: torch.Tensor, logit: t
     return loss, dX, dW
 
 
+def _run(name: str, device: torch.device, *args):
+    """Calls an entry point with the current stream of the operands' device, and that device current."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(device))
+    if rc != QLORA_OK:
+        _check(rc, name)
+
+
+def _at(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _shaped(out, shape: tuple, dtype: torch.dtype, device: torch.device, name: str) -> torch.Tensor:
+    """The caller's buffer, checked, or a new one."""
+    return torch.empty(shape, dtype=dtype, device=device) if out is None else _want(out, shape, dtype, device, name)
+
+
+def _scratch(ws, nb: int, device: torch.device):
+    """(workspace, its bytes): the caller's, or a new one of nb bytes."""
+    if ws is not None:
+        return ws, _ws_bytes(ws, device)
+    return torch.empty(nb, dtype=torch.uint8, device=device), nb
+
+
+@functools.lru_cache(maxsize=256)
+def embed_workspace_bytes(T: int, n_in: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load_library().qlora_embed_workspace_bytes(T, n_in, ctypes.byref(b)), "qlora_embed_workspace_bytes")
+    return b.value
+
+
+@functools.lru_cache(maxsize=256)
+def layer_norm_workspace_bytes(T: int, n_in: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load_library().qlora_layer_norm_workspace_bytes(T, n_in, ctypes.byref(b)), "qlora_layer_norm_workspace_bytes")
+    return b.value
+
+
+def _tokens(tokens) -> None:
+    if not isinstance(tokens, torch.Tensor) or tokens.dtype != torch.int64 or tokens.dim() != 1:
+        raise TypeError("tokens must be a 1-D int64 tensor")
+
+
+def embed(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """scale * W[tokens] (bf16 [n_vocab, n_in] -> [T, n_in], rounded once); tokens int64 [T], one outside the vocabulary
+    gives a row of zeros."""
+    _tokens(tokens)
+    W = _bits(W)
+    if W.dim() != 2:
+        raise ValueError(f"W must be [n_vocab, n_in], got {tuple(W.shape)}")
+    T, dev = tokens.shape[0], W.device
+    n_vocab, n_in = W.shape
+    tokens = _want(tokens.contiguous(), (T,), torch.int64, dev, "tokens")
+    Y = _shaped(out, (T, n_in), torch.bfloat16, dev, "out")
+    _on_gpu(W)
+    _run("qlora_embed", dev, tokens.data_ptr(), T, W.data_ptr(), n_vocab, n_in, float(scale), Y.data_ptr())
+    return Y
+
+
+def embed_bwd(tokens: torch.Tensor, dY: torch.Tensor, n_vocab: int, scale: float = 1.0, dW: torch.Tensor | None = None,
+              accumulate: bool = False, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of ``embed`` by W: bf16 [n_vocab, n_in], each row scale times the sum of its tokens' rows of dY.
+
+    ``dW`` is an optional preallocated result; with ``accumulate`` the sums are added to what it holds (a tied output
+    layer's gradient) and the rows that no token names stay as they are."""
+    _tokens(tokens)
+    dY = _bits(dY)
+    if dY.dim() != 2:
+        raise ValueError(f"dY must be [T, n_in], got {tuple(dY.shape)}")
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs dW")
+    (T, n_in), dev = dY.shape, dY.device
+    tokens = _want(tokens.contiguous(), (T,), torch.int64, dev, "tokens")
+    dW = _shaped(dW, (n_vocab, n_in), torch.bfloat16, dev, "dW")
+    ws, nb = _scratch(ws, embed_workspace_bytes(T, n_in), dev)
+    _on_gpu(dY)
+    _run("qlora_embed_bwd", dev, tokens.data_ptr(), dY.data_ptr(), T, n_vocab, n_in, float(scale), int(accumulate),
+         dW.data_ptr(), ws.data_ptr(), nb)
+    return dW
+
+
+def _norm_weight(weight, n_in: int, device, name: str = "weight", dtype=None) -> int:
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+    _want(weight, (n_in,), dtype or weight.dtype, device, name)
+    return WEIGHT_F32 if weight.dtype == torch.float32 else WEIGHT_BF16
+
+
+def layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
+               outs: tuple | None = None):
+    """Layer norm of the rows of X (bf16 [T, n_in]); weight and bias bf16 or float32, of one type.
+
+    Returns (Y bf16, mean float32 [T], rstd float32 [T]), the statistics for ``layer_norm_bwd``. ``outs`` are optional
+    preallocated (Y, mean or None, rstd or None); Y may be X."""
+    X = _bits(X)
+    if X.dim() != 2:
+        raise ValueError(f"X must be 2-D [T, n_in], got {tuple(X.shape)}")
+    (T, n_in), dev = X.shape, X.device
+    kind = _norm_weight(weight, n_in, dev)
+    if bias is not None:
+        _norm_weight(bias, n_in, dev, "bias", weight.dtype)
+    if outs is None:
+        Y = torch.empty_like(X)
+        mean, rstd = torch.empty((2, T), dtype=torch.float32, device=dev).unbind(0)
+    else:
+        Y, mean, rstd = outs
+        _want(Y, (T, n_in), torch.bfloat16, dev, "Y")
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            if t is not None:
+                _want(t, (T,), torch.float32, dev, name)
+    _on_gpu(X)
+    _run("qlora_layer_norm", dev, X.data_ptr(), T, n_in, weight.data_ptr(), _at(bias), kind, float(eps), Y.data_ptr(),
+         _at(mean), _at(rstd))
+    return Y, mean, rstd
+
+
+def layer_norm_bwd(X: torch.Tensor, dY: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   need_dx: bool = True, need_dweight: bool = True, need_dbias: bool = True,
+                   ws: torch.Tensor | None = None, outs: tuple | None = None):
+    """Gradients (dX, dweight, dbias) of ``layer_norm``, None where not needed; the last two of the weight's type.
+
+    ``outs`` are optional preallocated (dX or None, dweight or None, dbias or None), which then say which gradients are
+    formed."""
+    X, dY = _bits(X), _bits(dY)
+    _inputs(X, dY)
+    if dY.shape != X.shape:
+        raise ValueError(f"dY must be {tuple(X.shape)}, got {tuple(dY.shape)}")
+    (T, n_in), dev = X.shape, X.device
+    kind = _norm_weight(weight, n_in, dev)
+    _want(mean, (T,), torch.float32, dev, "mean")
+    _want(rstd, (T,), torch.float32, dev, "rstd")
+    if outs is None:
+        dX = torch.empty_like(X) if need_dx else None
+        dw = torch.empty_like(weight) if need_dweight else None
+        db = torch.empty_like(weight) if need_dbias else None
+    else:
+        dX, dw, db = outs
+        for t, shape, dtype, name in ((dX, (T, n_in), torch.bfloat16, "dX"), (dw, (n_in,), weight.dtype, "dweight"),
+                                      (db, (n_in,), weight.dtype, "dbias")):
+            if t is not None:
+                _want(t, shape, dtype, dev, name)
+    nb = 0
+    if dw is not None or db is not None:
+        ws, nb = _scratch(ws, layer_norm_workspace_bytes(T, n_in), dev)
+    _on_gpu(X)
+    _run("qlora_layer_norm_bwd", dev, X.data_ptr(), dY.data_ptr(), T, n_in, weight.data_ptr(), kind, mean.data_ptr(),
+         rstd.data_ptr(), _at(dX), _at(dw), _at(db), _at(ws), nb)
+    return dX, dw, db
+
+
 class QLoRALinearFn(torch.autograd.Function):
     """Autograd wrapper: forward(X, w, A, B, alpha) -> Y; gradients for X, A, B only."""
 
@@ -738,6 +907,47 @@ class HeadDistillFn(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, g, _):
         return _head_grads(ctx, g)
+
+
+class EmbedFn(torch.autograd.Function):
+    """Autograd wrapper of ``embed``: forward(tokens, W, scale) -> Y; the gradient of W is dense."""
+
+    @classmethod
+    def apply(cls, tokens, W, scale=1.0):
+        return super().apply(tokens, W, scale)
+
+    @staticmethod
+    def forward(ctx, tokens, W, scale):
+        Y = embed(tokens, W, scale)
+        ctx.save_for_backward(tokens)
+        ctx.n_vocab, ctx.scale = W.shape[0], scale
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        (tokens,) = ctx.saved_tensors
+        return None, embed_bwd(tokens, dY, ctx.n_vocab, ctx.scale) if ctx.needs_input_grad[1] else None, None
+
+
+class LayerNormFn(torch.autograd.Function):
+    """Autograd wrapper of ``layer_norm``: forward(X, weight, bias, eps) -> Y; gradients for X, weight and bias."""
+
+    @classmethod
+    def apply(cls, X, weight, bias=None, eps=1e-5):
+        return super().apply(X, weight, bias, eps)
+
+    @staticmethod
+    def forward(ctx, X, weight, bias, eps):
+        Y, mean, rstd = layer_norm(X, weight, bias, eps)
+        ctx.save_for_backward(X, weight, mean, rstd)
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        X, weight, mean, rstd = ctx.saved_tensors
+        return (*layer_norm_bwd(X, dY, weight, mean, rstd, *ctx.needs_input_grad[:3]), None)
 
 
 def timing_enable(kernel: str, enable: bool = True):

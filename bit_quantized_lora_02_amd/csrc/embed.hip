@@ -1,0 +1,303 @@
+// embed.hip -- the embedding beside the 4-bit linears: lookup with scaling, and its gradient by sorted tokens.
+//
+//   Y[t]  = bf16(scale W[token_t]),  0 where token_t lies outside the vocabulary
+//   dW[v] = bf16((dW[v] +) scale sum_{t: token_t = v} dY[t])
+//
+// The lookup moves 4 bytes per value and computes next to nothing: it is bound by HBM.  The gradient reads dY once and
+// writes the whole of dW, nearly all of it zeros (a vocabulary of 128256 x 4096: 1.05 GB against 0.13 GB of 16384 rows of
+// dY).  Nothing is added atomically: the positions are sorted by token, stably, and each row of dW is the sum of its
+// rows of dY in the order of their positions, cut into pieces at fixed places, so results repeat bit by bit.
+//   1. k_embed_order  ranks the positions against each other; the workgroups that have no positions to rank fill dW with
+//                     zeros, which takes longer, so the sort costs no time of its own where dW is large.
+//   2. k_embed_merge  (more than kOrderChunk positions) merges the sorted chunks.
+//   3. k_embed_sum    a wave adds a piece of the sorted list over 512 columns; a row that lies in one piece is written at once.
+//   4. k_embed_join   rows that were cut at the pieces' borders.
+#include "step.h"
+#include "step_device.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kWaveCols = 512;  // columns of a row that one wave takes: 16 bytes per lane
+
+__global__ __launch_bounds__(256) void k_embed(const int64_t *__restrict__ tokens, int64_t T, const bf16_t *__restrict__ W,
+                                               int64_t V, int64_t D, float scale, bf16_t *__restrict__ Y, int64_t chunks) {
+  const int64_t per = D / 8;  // 16-byte chunks of a row
+  for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < chunks; c += (int64_t)gridDim.x * 256) {
+    const int64_t t = c / per, d = (c - t * per) * 8;
+    const int64_t v = tokens[t];
+    u32x4_t o = {0u, 0u, 0u, 0u};
+    if ((uint64_t)v < (uint64_t)V) {
+      float x[8];
+      unpack8(load16(W + v * D + d), x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= scale;
+      o = pack8(x);
+    }
+    store16(Y + t * D + d, o);
+  }
+}
+
+// Ranks 64 positions of a chunk against the whole chunk: the rank of position i is the number of keys below its own plus
+// the number of equal ones before it.  16 waves count a sixteenth of the chunk each, the keys broadcast from LDS, two
+// instructions per pair (8192 positions: 67 million pairs over the whole GPU).
+constexpr int kRankWaves = 16;
+__device__ __forceinline__ void rank_chunk(const int64_t *__restrict__ tokens, int64_t T, int64_t V, int64_t block,
+                                           int32_t *__restrict__ order, int32_t *__restrict__ key) {
+  __shared__ __attribute__((aligned(16))) uint32_t s_key[kOrderChunk];
+  __shared__ uint32_t s_rank[kRankWaves][64];
+  constexpr int64_t kBlocks = kOrderChunk / 64;
+  const int64_t base = block / kBlocks * kOrderChunk;
+  const int n = (int)(T - base < kOrderChunk ? T - base : kOrderChunk);
+  const int padded = (n + 63) & ~63;
+  for (int i = threadIdx.x; i < padded; i += 1024) {
+    uint32_t k = 0xffffffffu;  // behind the end: above every key
+    if (i < n) {
+      const int64_t v = tokens[base + i];
+      k = (uint64_t)v < (uint64_t)V ? (uint32_t)v : (uint32_t)V;
+    }
+    s_key[i] = k;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i0 = (int)(block % kBlocks) * 64, i = i0 + lane;
+  const uint32_t mine = s_key[i];
+  uint32_t rank = 0;
+  for (int j0 = wave * 64; j0 < padded; j0 += kRankWaves * 64) {
+    if (j0 == i0) {
+#pragma unroll 8
+      for (int j = 0; j < 64; ++j) {
+        const uint32_t k = s_key[j0 + j];
+        rank += (k < mine || (k == mine && j < lane)) ? 1u : 0u;
+      }
+    } else {
+      const uint32_t below = mine + (j0 < i0 ? 1u : 0u);  // (of lanes behind the end it may wrap: their rank is not used)
+#pragma unroll
+      for (int j = 0; j < 64; j += 4) {
+        const u32x4_t k = *reinterpret_cast<const u32x4_t *>(&s_key[j0 + j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rank += k[e] < below ? 1u : 0u;
+      }
+    }
+  }
+  s_rank[wave][lane] = rank;
+  __syncthreads();
+  if (wave == 0 && i < n) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int w = 0; w < kRankWaves; ++w) r += s_rank[w][lane];
+    order[base + r] = (int32_t)(base + i);
+    key[base + r] = (int32_t)mine;
+  }
+}
+
+__global__ __launch_bounds__(1024) void k_embed_order(const int64_t *__restrict__ tokens, int64_t T, int64_t V,
+                                                      int32_t *__restrict__ order, int32_t *__restrict__ key, int64_t blocks,
+                                                      bf16_t *__restrict__ fill, int64_t fill_n) {
+  if (blockIdx.x < blocks) {
+    rank_chunk(tokens, T, V, blockIdx.x, order, key);
+    return;
+  }
+  const int64_t step = ((int64_t)gridDim.x - blocks) * 1024 * 8;
+  for (int64_t e = ((int64_t)(blockIdx.x - blocks) * 1024 + threadIdx.x) * 8; e < fill_n; e += step)
+    store16(fill + e, u32x4_t{0u, 0u, 0u, 0u});
+}
+
+// First place in [0, n) whose key is not below k (UPPER: above k).
+template <bool UPPER>
+__device__ __forceinline__ int bound(const int32_t *__restrict__ key, int n, int k) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (UPPER ? key[mid] <= k : key[mid] < k) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A place of a sorted chunk among all chunks: its place there plus, in each earlier chunk, the keys not above its own
+// and, in each later one, those below.
+__global__ __launch_bounds__(256) void k_embed_merge(int64_t T, const int32_t *__restrict__ order,
+                                                     const int32_t *__restrict__ key, int32_t *__restrict__ order_out,
+                                                     int32_t *__restrict__ key_out) {
+  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (p >= T) return;
+  const int64_t own = p / kOrderChunk;
+  const int k = key[p];
+  int64_t at = p - own * kOrderChunk;
+  for (int64_t c = 0; c * kOrderChunk < T; ++c) {
+    const int64_t base = c * kOrderChunk;
+    const int n = (int)(T - base < kOrderChunk ? T - base : kOrderChunk);
+    if (c < own) at += bound<true>(key + base, n, k);
+    else if (c > own) at += bound<false>(key + base, n, k);
+  }
+  order_out[at] = order[p];
+  key_out[at] = k;
+}
+
+__device__ __forceinline__ void write_row(bf16_t *__restrict__ at, const float sum[8], float scale, bool add) {
+  float o[8];
+  if (add) {
+    unpack8(load16(at), o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = fmaf(sum[i], scale, o[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = sum[i] * scale;
+  }
+  store16(at, pack8(o));
+}
+
+// One piece of the sorted list, 512 columns.  A row whose positions all lie in the piece is written; the binary32 sum of
+// one that began in an earlier piece goes to part[piece][0], of one that begins here and goes on to part[piece][1].
+__global__ __launch_bounds__(256) void k_embed_sum(const int32_t *__restrict__ order, const int32_t *__restrict__ key,
+                                                   int64_t T, int piece, const bf16_t *__restrict__ dY, int64_t V, int64_t D,
+                                                   int64_t slices, int64_t jobs, float scale, bool add,
+                                                   bf16_t *__restrict__ dW, float *__restrict__ part) {
+  constexpr int N = 8;  // rows in flight
+  const int64_t job = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (job >= jobs) return;
+  const int64_t c = job / slices, d = (job - c * slices) * kWaveCols + (threadIdx.x & 63) * 8;
+  const int64_t p0 = c * piece, p1 = p0 + piece < T ? p0 + piece : T;
+  int cur = key[p0];
+  if (cur >= V) return;  // what names no row comes last
+  const bool in = d < D;
+  bool head = p0 > 0 && key[p0 - 1] == cur;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  auto flush = [&](bool goes_on) {
+    if (!in) return;
+    if (!head && !goes_on) {
+      write_row(dW + (int64_t)cur * D + d, sum, scale, add);
+    } else {
+      float *at = part + ((c * 2 + (head ? 0 : 1)) * D + d);
+      *reinterpret_cast<float4 *>(at) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      *reinterpret_cast<float4 *>(at + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+    }
+  };
+  for (int64_t p = p0; p < p1; p += N) {
+    u32x4_t row[N];
+    int k[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      k[e] = p + e < p1 ? key[p + e] : (int)V;
+      row[e] = u32x4_t{0u, 0u, 0u, 0u};
+      if (k[e] < V && in) row[e] = load16(dY + (int64_t)order[p + e] * D + d);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (p + e >= p1) break;
+      if (k[e] != cur) {
+        flush(false);
+        if (k[e] >= V) return;
+        cur = k[e];
+        head = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+      }
+      float x[8];
+      unpack8(row[e], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += x[i];
+    }
+  }
+  flush(p1 < T && key[p1] == cur);
+}
+
+// The row that begins in a piece and goes on: its sums of the pieces, added in order (four waves a quarter of them each,
+// then the quarters).
+__global__ __launch_bounds__(256) void k_embed_join(const int32_t *__restrict__ key, int64_t T, int piece, int64_t V,
+                                                    int64_t D, int64_t slices, float scale, bool add,
+                                                    bf16_t *__restrict__ dW, const float *__restrict__ part) {
+  __shared__ float s_sum[3][64][9];
+  const int64_t c = blockIdx.x / slices;
+  const int64_t p0 = c * piece, p1 = p0 + piece;
+  if (p1 >= T) return;
+  const int cur = key[p1 - 1];
+  if (cur >= V || key[p1] != cur) return;              // its last row ends in it
+  if (p0 > 0 && key[p0] == cur && key[p0 - 1] == cur) return;  // begins in an earlier piece
+  int64_t lo = p1, hi = T;                             // the first place behind the row
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (key[mid] <= cur) lo = mid + 1;
+    else hi = mid;
+  }
+  const int64_t last = (lo - 1) / piece, n = last - c;  // pieces that continue it
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t d = (blockIdx.x - c * slices) * kWaveCols + lane * 8;
+  const bool in = d < D;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int64_t per = (n + 3) / 4, a = c + 1 + wave * per, b = a + per < last + 1 ? a + per : last + 1;
+  if (in) {
+    if (wave == 0) {
+      const float4 *at = reinterpret_cast<const float4 *>(part + (c * 2 + 1) * D + d);
+      const float4 x = at[0], y = at[1];
+      sum[0] = x.x, sum[1] = x.y, sum[2] = x.z, sum[3] = x.w, sum[4] = y.x, sum[5] = y.y, sum[6] = y.z, sum[7] = y.w;
+    }
+#pragma unroll 8
+    for (int64_t q = a; q < b; ++q) {
+      const float4 *at = reinterpret_cast<const float4 *>(part + q * 2 * D + d);
+      const float4 x = at[0], y = at[1];
+      sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+      sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
+    }
+  }
+  if (wave > 0)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_sum[wave - 1][lane][i] = sum[i];
+  __syncthreads();
+  if (wave == 0 && in) {
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += s_sum[w][lane][i];
+    write_row(dW + (int64_t)cur * D + d, sum, scale, add);
+  }
+}
+
+int64_t slices_of(int64_t D) { return (D + kWaveCols - 1) / kWaveCols; }
+
+}  // namespace
+
+hipError_t launch_embed(const int64_t *tokens, int64_t T, const bf16_t *W, int64_t V, int64_t D, float scale, bf16_t *Y,
+                        hipStream_t s) {
+  const int64_t chunks = T * (D / 8), blocks = (chunks + 255) / 256;
+  launch(k_embed, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, tokens, T, W, V, D, scale, Y, chunks);
+  return hipGetLastError();
+}
+
+int embed_piece(int64_t T) { return T <= 2048 ? 8 : T <= 8192 ? 16 : 32; }
+
+hipError_t launch_embed_order(const int64_t *tokens, int64_t T, int64_t V, const Order &o, bf16_t *fill, int64_t fill_n,
+                              hipStream_t s) {
+  const int64_t blocks = (T + 63) / 64, fills = (fill_n + 8191) / 8192;
+  const bool merged = T > kOrderChunk;
+  launch(k_embed_order, dim3((uint32_t)(blocks + (fills < 2048 ? fills : 2048))), dim3(1024), 0, s, tokens, T, V,
+         merged ? o.order2 : o.order, merged ? o.key2 : o.key, blocks, fill, fill_n);
+  return hipGetLastError();
+}
+
+hipError_t launch_embed_merge(int64_t T, const Order &o, hipStream_t s) {
+  launch(k_embed_merge, dim3((uint32_t)((T + 255) / 256)), dim3(256), 0, s, T, (const int32_t *)o.order2,
+         (const int32_t *)o.key2, o.order, o.key);
+  return hipGetLastError();
+}
+
+hipError_t launch_embed_sum(const Order &o, int64_t T, const bf16_t *dY, int64_t V, int64_t D, float scale, bool add,
+                            bf16_t *dW, float *part, hipStream_t s) {
+  const int piece = embed_piece(T);
+  const int64_t slices = slices_of(D), jobs = (T + piece - 1) / piece * slices;
+  launch(k_embed_sum, dim3((uint32_t)((jobs + 3) / 4)), dim3(256), 0, s, (const int32_t *)o.order, (const int32_t *)o.key, T,
+         piece, dY, V, D, slices, jobs, scale, add, dW, part);
+  return hipGetLastError();
+}
+
+hipError_t launch_embed_join(const Order &o, int64_t T, int64_t V, int64_t D, float scale, bool add, bf16_t *dW,
+                             const float *part, hipStream_t s) {
+  const int piece = embed_piece(T);
+  const int64_t slices = slices_of(D), pieces = (T + piece - 1) / piece;
+  launch(k_embed_join, dim3((uint32_t)(pieces * slices)), dim3(256), 0, s, (const int32_t *)o.key, T, piece, V, D, slices,
+         scale, add, dW, part);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

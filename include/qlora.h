@@ -59,6 +59,10 @@ typedef uint16_t qlora_bf16; /* bf16 bit pattern */
 
 #define QLORA_MAX_RANK 128
 #define QLORA_MAX_TARGETS 256 /* teacher logits per row of qlora_head_distill */
+#define QLORA_MAX_NORM 32768  /* columns of qlora_layer_norm */
+
+#define QLORA_WEIGHT_BF16 0 /* type of a layer norm's weight and bias and of their gradients */
+#define QLORA_WEIGHT_F32 1
 
 /*
  * An NF4 weight of logical shape [n_out, n_in] (katajob, "NF4" and "Double
@@ -420,6 +424,59 @@ int qlora_head_distill(const qlora_bf16 *X, int64_t T, const qlora_bf16 *W, int6
 /* Workspace bytes of qlora_head_ce (k = 0) and qlora_head_distill (its k) into host *bytes (no HIP call). */
 int qlora_head_workspace_bytes(int64_t T, int64_t n_vocab, int64_t n_in, int32_t k, int need_dx, int need_dw,
                                size_t *bytes);
+
+/*
+ * What else a step holds beside the quantized linears and stays in 16 bits or more ("What stays in full precision",
+ * katajob; the preparation for k-bit training casts the norms to binary32, "4. QLoRA in code", ainiketan.in, Module 08).
+ * Sums are binary32 in a fixed order: results are bitwise repeatable.  The calls can be captured into a HIP graph.
+ *
+ * Embedding lookup:  Y[t] = bf16_rne(scale . W[tokens[t]])   [T, n_in],  W [n_vocab, n_in] bf16 (device).
+ * tokens: [T] int64, device.  A token outside [0, n_vocab) gives a row of zeros.  n_in % 8 == 0, T <= 2^22,
+ * n_vocab, n_in <= 2^22, n_vocab * n_in <= 2^34, T * n_in < 2^32.  W and Y 16-byte aligned, tokens 8-byte; Y overlaps
+ * neither.
+ */
+int qlora_embed(const int64_t *tokens, int64_t T, const qlora_bf16 *W, int64_t n_vocab, int64_t n_in, float scale,
+                qlora_bf16 *Y, void *stream);
+
+/*
+ * Its gradient by W, for an embedding that is trained (tokens were added to the vocabulary):
+ *   dW[v] = bf16_rne(scale . sum of dY[t] over the t with tokens[t] = v)     [n_vocab, n_in]
+ * dW is written completely, rows that no token names with zeros.  With accumulate != 0 the sum is added to what dW
+ * holds, dW[v] = bf16_rne(dW[v] + scale . sum), and rows that no token names are neither read nor written (an embedding
+ * tied to the output layer: after qlora_head_ce has written its dW).  dY [T, n_in] bf16; the rows of tokens outside the
+ * vocabulary are not read.  A token's rows are added in pieces of the sorted positions, then the pieces, all in the
+ * order of the positions.  With T = 0 dW is set to zero (accumulate: left as it is).
+ * ws: qlora_embed_workspace_bytes(T, n_in), 256-byte aligned; nothing in it needs to start at zero, and calls that
+ * overlap in time need workspaces of their own.  It holds the sorted positions and tokens (8 bytes per token, 16 past
+ * 8192 tokens) and two binary32 rows per piece of 8 to 32 tokens.
+ */
+int qlora_embed_bwd(const int64_t *tokens, const qlora_bf16 *dY, int64_t T, int64_t n_vocab, int64_t n_in, float scale,
+                    int accumulate, qlora_bf16 *dW, void *ws, size_t ws_bytes, void *stream);
+int qlora_embed_workspace_bytes(int64_t T, int64_t n_in, size_t *bytes);
+
+/*
+ * Layer norm of the rows of X [T, n_in] bf16:
+ *   mean = sum_i x_i / n_in,  rstd = 1 / sqrt(sum_i (x_i - mean)^2 / n_in + eps)
+ *   Y[t, i] = bf16_rne((x_i - mean) rstd weight_i + bias_i)
+ * weight, bias: [n_in] of weight_type (QLORA_WEIGHT_*), 16-byte aligned; bias may be NULL (none).  mean, rstd: [T]
+ * binary32, the backward's input; either may be NULL.  Y may be X itself.  n_in % 8 == 0, n_in <= QLORA_MAX_NORM,
+ * T <= 2^22, T * n_in < 2^32, eps >= 0 and finite (with eps = 0 a row of equal values divides by zero).
+ */
+int qlora_layer_norm(const qlora_bf16 *X, int64_t T, int64_t n_in, const void *weight, const void *bias, int weight_type,
+                     float eps, qlora_bf16 *Y, float *mean, float *rstd, void *stream);
+
+/*
+ * Its gradients, from X and the statistics that the forward wrote; xh = (x - mean) rstd, g = dY weight:
+ *   dX      = bf16_rne(rstd (g - mean_i(g) - xh mean_i(g xh)))     [T, n_in]
+ *   dweight = sum_t dY xh,   dbias = sum_t dY                      [n_in], of weight_type, rounded once
+ * Each of dX, dweight and dbias may be NULL (not formed); with T = 0 dweight and dbias are set to zero.  dX may be dY
+ * itself.  ws: qlora_layer_norm_workspace_bytes(T, n_in), binary32 sums of at most 256 groups of rows, 256-byte aligned;
+ * not read where dweight and dbias are NULL.
+ */
+int qlora_layer_norm_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, int64_t n_in, const void *weight,
+                         int weight_type, const float *mean, const float *rstd, qlora_bf16 *dX, void *dweight, void *dbias,
+                         void *ws, size_t ws_bytes, void *stream);
+int qlora_layer_norm_workspace_bytes(int64_t T, int64_t n_in, size_t *bytes);
 
 /* Static text for a QLORA_E* code. */
 const char *qlora_strerror(int code);
