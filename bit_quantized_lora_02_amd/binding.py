@@ -7,9 +7,10 @@ library is missing or the device is not gfx950, calls raise.
 
 Names follow the C ABI: ``quantize_nf4``, ``dequant``, ``linear_fwd``,
 ``linear_bwd``, ``linear_fwd_dropout``, ``linear_bwd_dropout``, ``linear_fwd_multi``, ``adamw_step``,
-``adamw8_step``, ``merge``, ``head_ce``, ``head_distill``, ``embed``, ``embed_bwd``, ``layer_norm``, ``layer_norm_bwd``, plus ``QLoRALinearFn`` (a torch.autograd.Function whose backward
+``adamw8_step``, ``merge``, ``head_ce``, ``head_distill``, ``embed``, ``embed_bwd``, ``layer_norm``, ``layer_norm_bwd``,
+``adapters_fwd``, ``adapters_bwd``, plus ``QLoRALinearFn`` (a torch.autograd.Function whose backward
 returns gradients for X, A and B and none for the frozen NF4 weight), ``HeadCEFn`` and ``HeadDistillFn``
-(the output layer's losses with their gradients), ``EmbedFn`` and ``LayerNormFn``.
+(the output layer's losses with their gradients), ``EmbedFn``, ``LayerNormFn`` and ``AdaptersFn``.
 """
 from __future__ import annotations
 
@@ -35,6 +36,7 @@ OP_FWD_MULTI = 3
 MAX_RANK = 128
 MAX_TARGETS = 256
 MAX_NORM = 32768
+MAX_POOL = 1000
 WEIGHT_BF16 = 0
 WEIGHT_F32 = 1
 
@@ -62,6 +64,9 @@ EXPORTED = (
     "qlora_layer_norm",
     "qlora_layer_norm_bwd",
     "qlora_layer_norm_workspace_bytes",
+    "qlora_adapters_fwd",
+    "qlora_adapters_bwd",
+    "qlora_adapters_workspace_bytes",
     "qlora_strerror",
     "qlora_last_error",
     "qlora_timing_enable",
@@ -153,6 +158,9 @@ def load_library() -> ctypes.CDLL:
         "qlora_layer_norm": ([P, i64, i64, P, P, ctypes.c_int, ctypes.c_float, P, P, P, P], ctypes.c_int),
         "qlora_layer_norm_bwd": ([P, P, i64, i64, P, ctypes.c_int, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "qlora_layer_norm_workspace_bytes": ([i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
+        "qlora_adapters_fwd": ([P, i64, i64, P, P, i64, i32, i32, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
+        "qlora_adapters_bwd": ([P, P, i64, i64, P, P, i64, i32, i32, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
+        "qlora_adapters_workspace_bytes": ([i64, i64, i64, i32, i32, ctypes.c_int, ctypes.POINTER(sz)], ctypes.c_int),
         "qlora_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "qlora_last_error": ([], ctypes.c_char_p),
         "qlora_timing_enable": ([ctypes.c_char_p, ctypes.c_int], ctypes.c_int),
@@ -815,6 +823,85 @@ def layer_norm_bwd(X: torch.Tensor, dY: torch.Tensor, weight: torch.Tensor, mean
     return dX, dw, db
 
 
+@functools.lru_cache(maxsize=256)
+def adapters_workspace_bytes(T: int, n_in: int, n_out: int, n_pool: int, r: int, backward: bool = False) -> int:
+    b = ctypes.c_size_t()
+    _check(load_library().qlora_adapters_workspace_bytes(T, n_in, n_out, n_pool, r, int(backward), ctypes.byref(b)),
+           "qlora_adapters_workspace_bytes")
+    return b.value
+
+
+def _adapters(X, A_pool, B_pool, scale, index, rank):
+    """Checked operands of the adapters by token: (X, A_pool, B_pool, T, n_in, n_out, n_pool, r)."""
+    X, A_pool, B_pool = _bits(X), _bits(A_pool), _bits(B_pool)
+    _inputs(X, A_pool, B_pool)
+    T, n_in = X.shape
+    if A_pool.dim() != 3 or B_pool.dim() != 3:
+        raise ValueError(f"A_pool must be [n_pool, r, n_in] and B_pool [n_pool, n_out, r], got {tuple(A_pool.shape)}, "
+                         f"{tuple(B_pool.shape)}")
+    n_pool, n_out, r = B_pool.shape
+    if A_pool.shape != (n_pool, r, n_in):
+        raise ValueError(f"A_pool must be {(n_pool, r, n_in)}, got {tuple(A_pool.shape)}")
+    _want(scale, (n_pool,), torch.float32, X.device, "scale")
+    _want(index, (T,), torch.int32, X.device, "index")
+    if rank is not None:
+        _want(rank, (n_pool,), torch.int32, X.device, "rank")
+    return X, A_pool, B_pool, T, n_in, n_out, n_pool, r
+
+
+def adapters_fwd(X: torch.Tensor, A_pool: torch.Tensor, B_pool: torch.Tensor, scale: torch.Tensor, index: torch.Tensor,
+                 rank: torch.Tensor | None = None, base: torch.Tensor | None = None, save_u: bool = True,
+                 ws: torch.Tensor | None = None, out: torch.Tensor | None = None, u_out: torch.Tensor | None = None):
+    """base + scale[a] (X A_a^T) B_a^T with the adapter a = index[t] of each token; returns (Y, U float32 [T, r] or None).
+
+    A_pool [n_pool, r, n_in], B_pool [n_pool, n_out, r] bf16; scale float32 [n_pool]; index int32 [T], outside of
+    [0, n_pool) for no adapter; rank int32 [n_pool], the ranks in use (default r). base [T, n_out] is the shared
+    projection's output (default zeros) and may also be ``out``. ``linear_fwd_multi`` is the form for tokens in
+    segments, adapters of one rank and alpha, and the NF4 projection in the same call."""
+    X, A_pool, B_pool, T, n_in, n_out, n_pool, r = _adapters(X, A_pool, B_pool, scale, index, rank)
+    dev, bf = X.device, torch.bfloat16
+    if base is not None:
+        base = _want(_bits(base), (T, n_out), bf, dev, "base")
+    Y = _shaped(out, (T, n_out), bf, dev, "out")
+    U = _shaped(u_out, (T, r), torch.float32, dev, "u_out") if save_u or u_out is not None else None
+    ws, nb = _scratch(ws, adapters_workspace_bytes(T, n_in, n_out, n_pool, r), dev)
+    _on_gpu(X)
+    _run("qlora_adapters_fwd", dev, X.data_ptr(), T, n_in, A_pool.data_ptr(), B_pool.data_ptr(), n_out, n_pool, r, _at(rank),
+         scale.data_ptr(), index.data_ptr(), _at(base), Y.data_ptr(), _at(U), ws.data_ptr(), nb)
+    return Y, U
+
+
+def adapters_bwd(X: torch.Tensor, dY: torch.Tensor, A_pool: torch.Tensor, B_pool: torch.Tensor, scale: torch.Tensor,
+                 index: torch.Tensor, rank: torch.Tensor | None = None, U: torch.Tensor | None = None,
+                 base: torch.Tensor | None = None, need_dx: bool = True, need_dw: bool = True,
+                 ws: torch.Tensor | None = None, outs: tuple | None = None):
+    """Gradients (dX, dA_pool, dB_pool) of ``adapters_fwd``, None where not needed.
+
+    U is what the forward returned (None: recomputed); base [T, n_in] is the shared projection's part of dX, which the
+    adapters' is added to (default zeros). ``outs`` are optional preallocated (dX or None, dA or None, dB or None), which
+    then say which gradients are formed; dX may be base."""
+    X, A_pool, B_pool, T, n_in, n_out, n_pool, r = _adapters(X, A_pool, B_pool, scale, index, rank)
+    dev, bf = X.device, torch.bfloat16
+    dY = _want(_bits(dY), (T, n_out), bf, dev, "dY")
+    if U is not None:
+        _want(U, (T, r), torch.float32, dev, "U")
+    if base is not None:
+        base = _want(_bits(base), (T, n_in), bf, dev, "base")
+    if outs is None:
+        dX = torch.empty_like(X) if need_dx else None  # (X and the pools are contiguous here)
+        dA, dB = (torch.empty_like(A_pool), torch.empty_like(B_pool)) if need_dw else (None, None)
+    else:
+        dX, dA, dB = outs
+        for t, like, name in ((dX, X, "dX"), (dA, A_pool, "dA"), (dB, B_pool, "dB")):
+            if t is not None:
+                _want(t, tuple(like.shape), bf, dev, name)
+    ws, nb = _scratch(ws, adapters_workspace_bytes(T, n_in, n_out, n_pool, r, True), dev)
+    _on_gpu(X)
+    _run("qlora_adapters_bwd", dev, X.data_ptr(), dY.data_ptr(), T, n_in, A_pool.data_ptr(), B_pool.data_ptr(), n_out, n_pool,
+         r, _at(rank), scale.data_ptr(), index.data_ptr(), _at(U), _at(base), _at(dX), _at(dA), _at(dB), ws.data_ptr(), nb)
+    return dX, dA, dB
+
+
 class QLoRALinearFn(torch.autograd.Function):
     """Autograd wrapper: forward(X, w, A, B, alpha) -> Y; gradients for X, A, B only."""
 
@@ -948,6 +1035,38 @@ class LayerNormFn(torch.autograd.Function):
     def backward(ctx, dY):
         X, weight, mean, rstd = ctx.saved_tensors
         return (*layer_norm_bwd(X, dY, weight, mean, rstd, *ctx.needs_input_grad[:3]), None)
+
+
+class AdaptersFn(torch.autograd.Function):
+    """Autograd wrapper of ``adapters_fwd``: forward(X, A_pool, B_pool, scale, index, rank, base) -> Y; gradients for X,
+    A_pool, B_pool and base (whose gradient is Y's)."""
+
+    @classmethod
+    def apply(cls, X, A_pool, B_pool, scale, index, rank=None, base=None):
+        return super().apply(X, A_pool, B_pool, scale, index, rank, base, torch.is_grad_enabled())
+
+    @staticmethod
+    def forward(ctx, X, A_pool, B_pool, scale, index, rank, base, recorded):
+        if recorded and ctx.needs_input_grad[3]:
+            raise ValueError("the scales get no gradient: detach them")
+        Y, U = adapters_fwd(X, A_pool, B_pool, scale, index, rank, base,
+                            save_u=recorded and ctx.needs_input_grad[2])
+        ctx.save_for_backward(X, A_pool, B_pool, scale, index, *(t for t in (rank, U) if t is not None))
+        ctx.has_rank = rank is not None
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        X, A_pool, B_pool, scale, index, *rest = ctx.saved_tensors
+        rank = rest.pop(0) if ctx.has_rank else None
+        need = ctx.needs_input_grad
+        dX = dA = dB = None
+        if any(need[:3]):
+            dX, dA, dB = adapters_bwd(X, dY, A_pool, B_pool, scale, index, rank, rest[0] if rest else None, None,
+                                      outs=tuple(torch.empty_like(t, memory_format=torch.contiguous_format) if n else None
+                                                 for n, t in zip(need, (X, A_pool, B_pool))))
+        return dX, dA, dB, None, None, None, dY if need[6] else None, None
 
 
 def timing_enable(kernel: str, enable: bool = True):

@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["abi.hip", "quant.hip", "nf4_gemm.hip", "nf4_gemv.hip", "lora_gemm.hip", "adamw.hip", "merge.hip",
            "head_abi.hip", "head_gemm.hip", "head_loss.hip",
-           "step_abi.hip", "embed.hip", "norm.hip"]
+           "step_abi.hip", "embed.hip", "norm.hip", "adapters.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

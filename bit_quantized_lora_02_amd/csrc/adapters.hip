@@ -1,0 +1,674 @@
+// adapters.hip -- low-rank adapters of many requests beside a shared projection, each token with an adapter of its own.
+//
+//   u_t  = X_t A_a^T,              Y_t  = bf16(base_t + s_a u_t B_a^T)        a = index[t]
+//   du_t = s_a dY_t B_a,           dX_t = bf16(base_t + du_t A_a)
+//   dA_a = sum_t du_t^T X_t,       dB_a = s_a sum_t dY_t^T u_t               over the tokens of adapter a
+//
+// ("QLoRA: fine-tuning a large model on one GPU" (learn.pranaymahendrakar.com), Researcher level, "LoRA, stated once" and
+// "The variants worth knowing": one base model in memory, requests for different adapters batched together.)
+// At ranks up to 128 every product has far fewer operations per byte than the matrix units need to be the bound: the
+// floor is the traffic of X, Y and the adapters in use.  So each product streams its long operand once, straight from
+// HBM into MFMA operands, and the rank-wide results u and du stay in binary32: where one of them is an operand it enters
+// as two bf16 parts (16 bits of it), which costs a second MFMA on idle units and leaves the outputs with the one rounding
+// of their type.
+//   1. k_adapt_plan    one workgroup groups the tokens by adapter (stably); the others transpose the pools for the backward.
+//                      Up to kAdaptSmall tokens in the forward, the next kernels find their tokens themselves.
+//   2. k_adapt_shrink  u or du: 16 tokens of one adapter against its r rows, the long axis over 8 waves (and ranges of it
+//                      over workgroups where there are few tokens).
+//   3. k_adapt_expand  base + u B^T (or du A): 16 or 32 tokens of one adapter, 64 columns per wave.
+//   4. k_adapt_grads   dA and dB: a piece of an adapter's tokens, 256 columns; transposed operands through LDS.
+//   5. k_adapt_reduce  sums of the pieces, in order; zeros for adapters without tokens.
+// No kernel writes a value in more than one place or adds atomically: results repeat bit by bit.
+#include "step.h"
+#include "step_device.h"
+
+namespace qlora {
+namespace {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+// 16x16x32: lane l holds A[m = l%16][k = 8(l/16)..+7], B[k = 8(l/16)..+7][n = l%16], C[m = 4(l/16)+i][n = l%16].
+__device__ __forceinline__ f32x4_t mfma16(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0,
+                                                 0);
+}
+
+__device__ __forceinline__ int scan_dpp(int x) {  // inclusive sums over the wave's lanes
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, true);
+  return x;
+}
+
+// Group of a token (n_pool: none).
+__device__ __forceinline__ int group_of(const AdaptRows &a, int64_t t) {
+  const int k = a.index[t];
+  return (uint32_t)k < (uint32_t)a.n_pool ? k : a.n_pool;
+}
+__device__ __forceinline__ int rank_of(const AdaptRows &a, int group) {
+  if (group >= a.n_pool) return 0;
+  if (!a.rank) return a.r;
+  const int k = a.rank[group];
+  return k < 0 ? 0 : k > a.r ? a.r : k;
+}
+
+// At most M tokens of one group: places p0 .. p0 + n - 1 of the order.  Of a group that is cut into several tiles, `slot`
+// numbers them over all such groups (-1: the group's only tile).
+struct Tile {
+  int group, p0, n, slot;
+};
+// The id-th tile of the groups in order (wave-wide, the same in every lane); false: there are fewer.
+__device__ __forceinline__ bool find_tile(const AdaptRows &a, int M, int id, Tile *out) {
+  const int lane = threadIdx.x & 63;
+  int before = 0, slots = 0;
+  for (int k0 = 0; k0 <= a.n_pool; k0 += 64) {
+    const int k = k0 + lane;
+    int lo = 0, hi = 0;
+    if (k <= a.n_pool) lo = a.start[k], hi = a.start[k + 1];
+    const int tiles = (hi - lo + M - 1) / M, several = tiles > 1 ? tiles : 0;
+    const int sum = scan_dpp(tiles), sum2 = scan_dpp(several);
+    const int all = __builtin_amdgcn_readlane(sum, 63);
+    if (id < before + all) {
+      const int l = __builtin_ctzll(__ballot(before + sum > id));
+      const int j = id - (before + __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(tiles, l));
+      const int end = __builtin_amdgcn_readlane(hi, l), n_tiles = __builtin_amdgcn_readlane(tiles, l);
+      out->group = k0 + l;
+      out->p0 = __builtin_amdgcn_readlane(lo, l) + j * M;
+      out->n = end - out->p0 < M ? end - out->p0 : M;
+      out->slot = n_tiles > 1 ? slots + __builtin_amdgcn_readlane(sum2, l) - n_tiles + j : -1;
+      return true;
+    }
+    before += all;
+    slots += __builtin_amdgcn_readlane(sum2, 63);
+  }
+  return false;
+}
+
+// The id-th tile of M tokens and this lane's token in it, place lane % M (behind the tile's end: its first token).
+// Without a plan (T <= 64) the groups come in the order of their first tokens.
+template <int M>
+__device__ __forceinline__ bool find_tokens(const AdaptRows &a, int id, Tile *tile, int tokens[(M + 15) / 16]) {
+  const int lane = threadIdx.x & 63;
+  if (a.start) {
+    if (!find_tile(a, M, id, tile)) return false;
+#pragma unroll
+    for (int m = 0; m < (M + 15) / 16; ++m) {
+      const int p = m * 16 + (lane & 15);
+      tokens[m] = a.order[tile->p0 + (p < tile->n ? p : 0)];
+    }
+    return true;
+  }
+  const int group = lane < a.T ? group_of(a, lane) : -1;
+  uint64_t rest = __ballot(lane < a.T);
+  while (rest) {
+    const int g = __builtin_amdgcn_readlane(group, __builtin_ctzll(rest));
+    const uint64_t mine = __ballot(group == g);
+    const int n = __popcll(mine), tiles = (n + M - 1) / M;
+    if (id < tiles) {
+      tile->group = g;
+      tile->p0 = id * M;
+      tile->n = n - id * M < M ? n - id * M : M;
+      tile->slot = -1;
+#pragma unroll
+      for (int m = 0; m < (M + 15) / 16; ++m) {
+        const int p = m * 16 + (lane & 15), place = tile->p0 + (p < tile->n ? p : 0);
+        uint64_t left = mine;  // its place-th bit
+        for (int i = 0; i < place; ++i) left &= left - 1;
+        tokens[m] = __builtin_ctzll(left);
+      }
+      return true;
+    }
+    id -= tiles;
+    rest &= ~mine;
+  }
+  return false;
+}
+
+// u as two bf16 parts, hi + lo (16 bits of it).
+__device__ __forceinline__ void split8(const float u[8], u32x4_t *hi, u32x4_t *lo) {
+  float rest[8];
+  u32x4_t h = pack8(u);
+  unpack8(h, rest);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rest[i] = u[i] - rest[i];
+  *hi = h;
+  *lo = pack8(rest);
+}
+
+// Zero for the columns j0 .. j0 + 7 of an adapter at and past its rank (they may hold anything).
+__device__ __forceinline__ u32x4_t below_rank(u32x4_t v, int left) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t keep = (left > 2 * w ? 0xffffu : 0u) | (left > 2 * w + 1 ? 0xffff0000u : 0u);
+    v[w] &= keep;
+  }
+  return v;
+}
+
+// ----------------------------------------------------------------------- plan
+constexpr int kPlanWaves = 16;
+struct PlanShared {
+  int at[kPlanWaves][1024];  // tokens of a wave's share in each group, then where the next of them goes
+  int wave[kPlanWaves];
+};
+__device__ __forceinline__ void plan_tokens(const AdaptRows &a, PlanShared &sh) {
+  auto &s_at = sh.at;
+  auto &s_wave = sh.wave;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, groups = a.n_pool + 1;
+  for (int k = tid; k < kPlanWaves * 1024; k += 1024) (&s_at[0][0])[k] = 0;
+  __syncthreads();
+  const int64_t per = ((a.T + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64, t0 = wave * per;
+  const int64_t t1 = t0 + per < a.T ? t0 + per : a.T;
+  for (int64_t t = t0 + lane; t < t1; t += 64) atomicAdd(&s_at[wave][group_of(a, t)], 1);
+  __syncthreads();
+  int n = 0;  // thread k: tokens of group k
+  if (tid < groups)
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) n += s_at[w][tid];
+  const int sum = scan_dpp(n);
+  if (lane == 63) s_wave[wave] = sum;
+  __syncthreads();
+  int at = sum - n;
+  for (int w = 0; w < wave; ++w) at += s_wave[w];
+  if (tid < groups) {
+    a.start[tid] = at;
+    if (tid == a.n_pool) a.start[groups] = at + n;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int c = s_at[w][tid];
+      s_at[w][tid] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  for (int64_t t = t0 + lane; t - lane < t1; t += 64) {
+    const bool in = t < t1;
+    const int group = in ? group_of(a, t) : -1;
+    const uint64_t same = __ballot(group == __builtin_amdgcn_readfirstlane(group));
+    int rank, count;
+    if (same == __ballot(true)) {  // one group's tokens (a wave's lanes behind t1 are none: then not all are the same)
+      rank = lane;
+      count = 64;
+    } else {
+      rank = count = 0;
+#pragma unroll 8
+      for (int j = 0; j < 64; ++j) {
+        const bool eq = __builtin_amdgcn_readlane(group, j) == group;
+        rank += eq && j < lane ? 1 : 0;
+        count += eq ? 1 : 0;
+      }
+    }
+    int base = 0;
+    if (in) base = s_at[wave][group];
+    __builtin_amdgcn_wave_barrier();
+    if (in) {
+      a.order[base + rank] = (int32_t)t;
+      if (rank + 1 == count) s_at[wave][group] = base + count;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+constexpr int kTurn = 64;  // a workgroup turns 64 rows x 128 columns
+struct TurnShared {
+  bf16_t tile[kTurn][136];
+};
+__device__ __forceinline__ void turn_pool(const AdaptTurn &t, int64_t id, TurnShared &sh) {
+  auto &s_tile = sh.tile;
+  const int64_t rb = (t.rows + kTurn - 1) / kTurn, cb = (t.cols + 127) / 128;
+  const int64_t pool = id / (rb * cb), rest = id - pool * rb * cb;
+  const int64_t r0 = rest % rb * kTurn, c0 = rest / rb * 128;
+  const bf16_t *from = t.from + pool * t.rows * t.cols;
+  bf16_t *to = t.to + pool * t.rows * t.cols;
+  const int tid = threadIdx.x;
+  {
+    const int row = tid >> 4, col = (tid & 15) * 8;
+    if (r0 + row < t.rows && c0 + col < t.cols)
+      *reinterpret_cast<u32x4_t *>(&s_tile[row][col]) = load16(from + (r0 + row) * t.cols + c0 + col);
+  }
+  __syncthreads();
+  const int col = tid >> 3, row = (tid & 7) * 8;  // (both sizes are multiples of 8)
+  if (c0 + col < t.cols && r0 + row < t.rows) {
+    u32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = s_tile[row + 2 * i][col] | (uint32_t)s_tile[row + 2 * i + 1][col] << 16;
+    store16(to + (c0 + col) * t.rows + r0 + row, v);
+  }
+}
+int64_t turn_blocks(const AdaptTurn &t, int n_pool) {
+  return t.to ? n_pool * ((t.rows + kTurn - 1) / kTurn) * ((t.cols + 127) / 128) : 0;
+}
+
+__global__ __launch_bounds__(1024) void k_adapt_plan(AdaptRows a, AdaptTurn t0, AdaptTurn t1, int64_t blocks0) {
+  __shared__ __attribute__((aligned(16))) char shared[sizeof(PlanShared)];
+  static_assert(sizeof(TurnShared) <= sizeof(PlanShared), "one piece of LDS for both");
+  if (blockIdx.x == 0) plan_tokens(a, *reinterpret_cast<PlanShared *>(shared));
+  else if (blockIdx.x - 1 < blocks0) turn_pool(t0, blockIdx.x - 1, *reinterpret_cast<TurnShared *>(shared));
+  else turn_pool(t1, blockIdx.x - 1 - blocks0, *reinterpret_cast<TurnShared *>(shared));
+}
+
+// --------------------------------------------------------------------- shrink
+// RT: rank tiles of 16.  Operands come straight from HBM: a lane reads 16 bytes of its row, four lanes 64 adjacent ones,
+// and two steps of the reduction a line.  What stands in a row that is none (behind the tile's tokens, past the rank)
+// stays in the sums of that row, which are not stored: such rows read a valid one's address.
+constexpr int kShrinkWaves = 8;
+template <int RT>
+__global__ __launch_bounds__(64 * kShrinkWaves) void k_adapt_shrink(AdaptRows a, const bf16_t *__restrict__ P, int64_t K,
+                                                                    const bf16_t *__restrict__ Q, bool scaled, int ranges,
+                                                                    float *__restrict__ U) {
+  constexpr int LD = RT * 16 + 4;
+  __shared__ __attribute__((aligned(16))) float s_sum[kShrinkWaves][16][LD];
+  __shared__ int s_token[16];
+  const int id = blockIdx.x / ranges, range = blockIdx.x - id * ranges;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+  Tile tile;
+  int token[1];
+  if (!find_tokens<16>(a, id, &tile, token)) return;
+  const int rank = rank_of(a, tile.group);
+  if (wave == 0 && lane < 16) s_token[lane] = token[0];
+  f32x4_t acc[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (rank > 0) {
+    const bf16_t *p = P + (int64_t)token[0] * K + 8 * g;
+    const bf16_t *q[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      const int row = j * 16 + l;
+      q[j] = Q + ((int64_t)tile.group * a.r + (row < rank ? row : 0)) * K + 8 * g;
+    }
+    const int64_t steps = (K + 63) / 64, per = (steps + ranges - 1) / ranges;
+    const int64_t first = range * per, end = first + per < steps ? first + per : steps;
+    u32x4_t pv[2][2], qv[2][RT][2];
+    auto load = [&](int64_t step, u32x4_t(&pv_)[2], u32x4_t(&qv_)[RT][2]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t k = step * 64 + h * 32;
+        const bool in = k + 8 * g < K;
+        pv_[h] = in ? load16(p + k) : u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < RT; ++j) qv_[j][h] = in ? load16(q[j] + k) : u32x4_t{0u, 0u, 0u, 0u};
+      }
+    };
+    auto mma = [&](const u32x4_t(&pv_)[2], const u32x4_t(&qv_)[RT][2]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[j] = mfma16(qv_[j][h], pv_[h], acc[j]);
+    };
+    int64_t step = first + wave;
+    if (step < end) load(step, pv[0], qv[0]);
+    while (step < end) {
+      if (step + kShrinkWaves < end) load(step + kShrinkWaves, pv[1], qv[1]);
+      mma(pv[0], qv[0]);
+      step += kShrinkWaves;
+      if (step >= end) break;
+      if (step + kShrinkWaves < end) load(step + kShrinkWaves, pv[0], qv[0]);
+      mma(pv[1], qv[1]);
+      step += kShrinkWaves;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < RT; ++j) *reinterpret_cast<f32x4_t *>(&s_sum[wave][l][j * 16 + 4 * g]) = acc[j];
+  __syncthreads();
+  const float scale = scaled && tile.group < a.n_pool ? a.scale[tile.group] : 1.f;
+  for (int e = threadIdx.x; e < 16 * RT * 16; e += 64 * kShrinkWaves) {
+    const int n = e / (RT * 16), j = e % (RT * 16);
+    if (n >= tile.n || j >= a.r) continue;
+    float sum = 0.f;
+    if (j < rank) {
+#pragma unroll
+      for (int w = 0; w < kShrinkWaves; ++w) sum += s_sum[w][n][j];
+      sum *= scale;
+    }
+    U[((int64_t)range * a.T + s_token[n]) * a.r + j] = sum;
+  }
+}
+
+// Columns j0 .. j0 + 7 of a token's u: the ranges' sums, times the scale, zero at and past the rank.
+__device__ __forceinline__ void load_u(const AdaptRows &a, const float *__restrict__ U, int ranges, int64_t token, int j0,
+                                       int rank, float u[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = 0.f;
+  if (j0 >= rank) return;
+  const float *p = U + token * a.r + j0;
+  for (int q = 0; q < ranges; ++q, p += a.T * a.r) {
+    const float4 x = reinterpret_cast<const float4 *>(p)[0], y = reinterpret_cast<const float4 *>(p)[1];
+    u[0] += x.x, u[1] += x.y, u[2] += x.z, u[3] += x.w, u[4] += y.x, u[5] += y.y, u[6] += y.z, u[7] += y.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = j0 + i < rank ? u[i] : 0.f;
+}
+
+// --------------------------------------------------------------------- expand
+// KS: 32-wide steps over the rank, each an MFMA with u's high part and one with its low part; KS = 0 (rank up to 16): both
+// parts side by side in one.  The rows of Q that an MFMA takes are chosen so that a lane ends up with 16 adjacent columns
+// of its token: tile p of the four takes rows 16 (m / 4) + 4 p + m % 4.
+template <int KS, int MT>
+__global__ __launch_bounds__(256) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
+                                                      const bf16_t *__restrict__ Q, int64_t N, bool scaled, int64_t per,
+                                                      int blocks, const bf16_t *base, bf16_t *out,
+                                                      float *__restrict__ U_out) {
+  constexpr int KQ = KS ? KS : 1;
+  const int id = blockIdx.x / blocks, block = blockIdx.x - id * blocks;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+  Tile tile;
+  int token[MT];
+  if (!find_tokens<16 * MT>(a, id, &tile, token)) return;
+  const int rank = rank_of(a, tile.group);
+  const float scale = scaled && tile.group < a.n_pool ? a.scale[tile.group] : 1.f;
+  if (U_out && block == 0 && wave == 0) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      if (m * 16 + l < tile.n)
+        for (int j = 8 * g; j < a.r; j += 32) {
+          float u[8];
+          load_u(a, U, ranges, token[m], j, rank, u);
+          float4 *to = reinterpret_cast<float4 *>(U_out + (int64_t)token[m] * a.r + j);
+          to[0] = make_float4(u[0], u[1], u[2], u[3]);
+          to[1] = make_float4(u[4], u[5], u[6], u[7]);
+        }
+  }
+  if (rank == 0 && base == out) return;
+  u32x4_t hi[MT][KQ], lo[MT][KQ];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int k = 0; k < KQ; ++k) {
+      float u[8];
+      load_u(a, U, ranges, token[m], KS ? k * 32 + 8 * g : 8 * (g & 1), rank, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] *= scale;
+      split8(u, &hi[m][k], &lo[m][k]);
+      if (!KS && g >= 2) hi[m][k] = lo[m][k];
+    }
+  const bf16_t *q = Q + (int64_t)(tile.group < a.n_pool ? tile.group : 0) * N * a.r;
+  const int64_t first = block * per, end = first + per < N ? first + per : N;
+  for (int64_t n0 = first + wave * 64; n0 < end; n0 += 256) {
+    u32x4_t qv[4][KQ], bv[MT][2];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int64_t row = n0 + 16 * (l >> 2) + 4 * p + (l & 3);
+#pragma unroll
+      for (int k = 0; k < KQ; ++k) {
+        const int j0 = KS ? k * 32 + 8 * g : 8 * (g & 1);
+        qv[p][k] = u32x4_t{0u, 0u, 0u, 0u};
+        if (j0 < rank && row < N) qv[p][k] = load16(q + row * a.r + j0);
+        if (rank & 7) qv[p][k] = below_rank(qv[p][k], rank - j0);
+      }
+    }
+    const int64_t col = n0 + 16 * g;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bv[m][h] = u32x4_t{0u, 0u, 0u, 0u};
+        if (base && m * 16 + l < tile.n && col + 8 * h < N) bv[m][h] = load16(base + (int64_t)token[m] * N + col + 8 * h);
+      }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      f32x4_t acc[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        acc[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KQ; ++k) {
+          acc[p] = mfma16(qv[p][k], hi[m][k], acc[p]);
+          if (KS) acc[p] = mfma16(qv[p][k], lo[m][k], acc[p]);
+        }
+      }
+      if (m * 16 + l < tile.n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (col + 8 * h < N) {
+            float y[8];
+            unpack8(bv[m][h], y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += acc[2 * h + (i >> 2)][i & 3];
+            store16(out + (int64_t)token[m] * N + col + 8 * h, pack8(y));
+          }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- grads
+// One piece of an adapter's tokens, 256 columns of the long operand (64 per wave).  Steps of 64 tokens: their rows go to
+// LDS as they are and are read back transposed (ds_read_b64_tr_b16: lane i of 16 gets element i % 4 of the 8 bytes that
+// lanes 4 m + i / 4 address, m = 0 .. 3), the rank-wide operand likewise in two bf16 parts.
+__device__ __forceinline__ u32x4_t turned(const bf16_t *base, int ld, int row, int col) {
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(base + row * ld + col));
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(base + (row + 4) * ld + col));
+  const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+  return u32x4_t{l2.x, l2.y, h2.x, h2.y};
+}
+
+constexpr int kGradCols = 256, kGradLd = kGradCols + 16;
+// BY_J: the output is [n][r] (dB), else [r][n] (dA).
+template <int RT, bool BY_J>
+__device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile, int rank, const float *__restrict__ V,
+                                           int ranges, float scale, const bf16_t *__restrict__ X, int64_t N, int64_t c0,
+                                           float *__restrict__ part, bf16_t *__restrict__ grad, bf16_t *s_x, bf16_t *s_hi,
+                                           bf16_t *s_lo) {
+  constexpr int LV = RT * 16 + (RT > 1 ? 16 : 0);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l = lane & 15;
+  f32x4_t acc[4][RT];
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int j = 0; j < RT; ++j) acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int t0 = 0; t0 < tile.n; t0 += 64) {
+    u32x4_t x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = (tid >> 5) + 8 * i, col = (tid & 31) * 8;
+      x[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (t0 + row < tile.n && c0 + col < N) x[i] = load16(X + (int64_t)a.order[tile.p0 + t0 + row] * N + c0 + col);
+    }
+    if (t0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<u32x4_t *>(s_x + ((tid >> 5) + 8 * i) * kGradLd + (tid & 31) * 8) = x[i];
+    for (int e = tid; e < 64 * RT * 2; e += 256) {
+      const int row = e / (RT * 2), j0 = e % (RT * 2) * 8;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (t0 + row < tile.n) load_u(a, V, ranges, a.order[tile.p0 + t0 + row], j0, rank, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= scale;
+      u32x4_t hi, lo;
+      split8(v, &hi, &lo);
+      *reinterpret_cast<u32x4_t *>(s_hi + row * LV + j0) = hi;
+      *reinterpret_cast<u32x4_t *>(s_lo + row * LV + j0) = lo;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = k * 32 + 8 * g + (l >> 2);
+      u32x4_t xv[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        xv[p] = turned(s_x, kGradLd, row, wave * 64 + (BY_J ? 16 * p + 4 * (l & 3) : 16 * (l & 3) + 4 * p));
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const u32x4_t hi = turned(s_hi, LV, row, j * 16 + 4 * (l & 3)), lo = turned(s_lo, LV, row, j * 16 + 4 * (l & 3));
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          if (BY_J) {
+            acc[p][j] = mfma16(hi, xv[p], acc[p][j]);
+            acc[p][j] = mfma16(lo, xv[p], acc[p][j]);
+          } else {
+            acc[p][j] = mfma16(xv[p], hi, acc[p][j]);
+            acc[p][j] = mfma16(xv[p], lo, acc[p][j]);
+          }
+        }
+      }
+    }
+  }
+  const int64_t n0 = c0 + wave * 64, size = (int64_t)a.r * N;
+  if (BY_J) {  // lane: column 16 p + l, ranks 16 j + 4 g .. + 3
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const int64_t n = n0 + 16 * p + l;
+        const int j0 = j * 16 + 4 * g;
+        if (n >= N || j0 >= a.r) continue;
+        const f32x4_t v = acc[p][j];
+        if (tile.slot >= 0)
+          *reinterpret_cast<f32x4_t *>(part + tile.slot * size + n * a.r + j0) = v;
+        else
+          *reinterpret_cast<u32x2_t *>(grad + tile.group * size + n * a.r + j0) =
+              u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
+  } else {  // lane: rank 16 j + l, columns 16 g + 4 p .. + 3
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      const int j0 = j * 16 + l;
+      if (j0 >= a.r) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t n = n0 + 16 * g + 8 * h;
+        if (n >= N) continue;
+        const f32x4_t v = acc[2 * h][j], w = acc[2 * h + 1][j];
+        if (tile.slot >= 0) {
+          f32x4_t *to = reinterpret_cast<f32x4_t *>(part + tile.slot * size + j0 * N + n);
+          to[0] = v;
+          to[1] = w;
+        } else {
+          store16(grad + tile.group * size + j0 * N + n, u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                 pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3])});
+        }
+      }
+    }
+  }
+}
+
+template <int RT>
+__global__ __launch_bounds__(256) void k_adapt_grads(AdaptRows a, AdaptGrads g, int piece, int blocks_a, int blocks) {
+  constexpr int LV = RT * 16 + (RT > 1 ? 16 : 0);
+  __shared__ __attribute__((aligned(16))) bf16_t s_x[64 * kGradLd], s_hi[64 * LV], s_lo[64 * LV];
+  const int id = blockIdx.x / blocks, block = blockIdx.x - id * blocks;
+  Tile tile;
+  if (!find_tile(a, piece, id, &tile) || tile.group >= a.n_pool) return;
+  const int rank = rank_of(a, tile.group);
+  if (block < blocks_a)
+    grad_piece<RT, false>(a, tile, rank, g.dU, g.dU_ranges, 1.f, g.X, g.n_in, (int64_t)block * kGradCols, g.part_a, g.dA,
+                          s_x, s_hi, s_lo);
+  else
+    grad_piece<RT, true>(a, tile, rank, g.U, g.U_ranges, a.scale[tile.group], g.dY, g.n_out,
+                         (int64_t)(block - blocks_a) * kGradCols, g.part_b, g.dB, s_x, s_hi, s_lo);
+}
+
+// A group's gradient from the sums of its pieces, in order, 8 values per thread; zeros for a group without tokens.  What
+// has one piece is written already.
+__global__ __launch_bounds__(256) void k_adapt_reduce(AdaptRows a, AdaptGrads g, int piece, int64_t blocks_a) {
+  const int group = blockIdx.y, lane = threadIdx.x & 63;
+  const int n = a.start[group + 1] - a.start[group], pieces = (n + piece - 1) / piece;
+  if (pieces == 1) return;
+  int slot = 0;  // pieces of earlier groups of several
+  for (int k0 = 0; k0 < group && pieces; k0 += 64) {
+    int c = 0;
+    if (k0 + lane < group) c = (a.start[k0 + lane + 1] - a.start[k0 + lane] + piece - 1) / piece;
+    slot += __builtin_amdgcn_readlane(scan_dpp(c > 1 ? c : 0), 63);
+  }
+  const bool of_a = blockIdx.x < blocks_a;
+  const int64_t size = (int64_t)a.r * (of_a ? g.n_in : g.n_out);
+  const int64_t e = ((blockIdx.x - (of_a ? 0 : blocks_a)) * 256 + threadIdx.x) * 8;
+  if (e >= size) return;
+  const float *p = (of_a ? g.part_a : g.part_b) + slot * size + e;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int q = 0; q < pieces; ++q) {
+    const float4 x = reinterpret_cast<const float4 *>(p + q * size)[0], y = reinterpret_cast<const float4 *>(p + q * size)[1];
+    sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w, sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
+  }
+  store16((of_a ? g.dA : g.dB) + group * size + e, pack8(sum));
+}
+
+// Tiles of M tokens, at most: groups do not share one.
+int64_t most_tiles(const AdaptRows &a, int M) {
+  const int64_t groups = a.n_pool + 1 < a.T ? a.n_pool + 1 : a.T;
+  return a.T / M + groups;
+}
+
+}  // namespace
+
+hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const AdaptTurn &t1, hipStream_t s) {
+  const int64_t b0 = turn_blocks(t0, a.n_pool), b1 = turn_blocks(t1, a.n_pool);
+  launch(k_adapt_plan, dim3((uint32_t)(1 + b0 + b1)), dim3(1024), 0, s, a, t0, t1, b0);
+  return hipGetLastError();
+}
+
+int adapt_ranges(int64_t T, int n_pool, int64_t K) {
+  const int64_t tiles = (T + 15) / 16 + (n_pool < T ? n_pool : T) / 2, most = (K + 511) / 512;
+  int64_t n = tiles < 1 ? 1 : 512 / tiles;
+  n = n < 1 ? 1 : n > 16 ? 16 : n;
+  return (int)(n < most ? n : most);
+}
+
+hipError_t launch_adapt_shrink(const AdaptRows &a, const bf16_t *P, int64_t K, const bf16_t *Q, bool scaled, int ranges,
+                               float *U, hipStream_t s) {
+  const dim3 grid((uint32_t)(most_tiles(a, 16) * ranges)), block(64 * kShrinkWaves);
+#define SHRINK(RT_) launch(k_adapt_shrink<RT_>, grid, block, 0, s, a, P, K, Q, scaled, ranges, U)
+  if (a.r <= 16) SHRINK(1);
+  else if (a.r <= 32) SHRINK(2);
+  else if (a.r <= 64) SHRINK(4);
+  else SHRINK(8);
+#undef SHRINK
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, const bf16_t *Q, int64_t N, bool scaled,
+                               const bf16_t *base, bf16_t *out, float *U_out, hipStream_t s) {
+  const bool wide = a.T >= 2048;
+  const int64_t tiles = most_tiles(a, wide ? 32 : 16), cols = (N + 255) / 256;
+  int64_t per = 1;  // steps of 256 columns per workgroup
+  while (per < 4 && tiles * ((cols + 2 * per - 1) / (2 * per)) >= 2048) per *= 2;
+  const int blocks = (int)((cols + per - 1) / per);
+  const dim3 grid((uint32_t)(blocks * tiles)), block(256);
+#define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * 256, blocks, base, out, U_out
+#define EXPAND(KS_)                                               \
+  do {                                                            \
+    if (wide) launch(k_adapt_expand<KS_, 2>, EXPAND_ARGS);        \
+    else launch(k_adapt_expand<KS_, 1>, EXPAND_ARGS);             \
+  } while (0)
+  if (a.r <= 16) EXPAND(0);
+  else if (a.r <= 32) EXPAND(1);
+  else if (a.r <= 64) EXPAND(2);
+  else EXPAND(4);
+#undef EXPAND
+#undef EXPAND_ARGS
+  return hipGetLastError();
+}
+
+int adapt_piece(int64_t T, int64_t n_in, int64_t n_out) {
+  const int64_t blocks = (n_in + kGradCols - 1) / kGradCols + (n_out + kGradCols - 1) / kGradCols;
+  int piece = 1024;
+  while (piece > 64 && T / piece * blocks < 512) piece /= 2;
+  return piece;
+}
+
+hipError_t launch_adapt_grads(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s) {
+  const int ba = g.dA ? (int)((g.n_in + kGradCols - 1) / kGradCols) : 0;
+  const int bb = g.dB ? (int)((g.n_out + kGradCols - 1) / kGradCols) : 0;
+  const dim3 grid((uint32_t)((ba + bb) * most_tiles(a, piece))), block(256);
+#define GRADS(RT_) launch(k_adapt_grads<RT_>, grid, block, 0, s, a, g, piece, ba, ba + bb)
+  if (a.r <= 16) GRADS(1);
+  else if (a.r <= 32) GRADS(2);
+  else if (a.r <= 64) GRADS(4);
+  else GRADS(8);
+#undef GRADS
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_reduce(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s) {
+  const int64_t ba = g.dA ? (a.r * g.n_in + 2047) / 2048 : 0, bb = g.dB ? (a.r * g.n_out + 2047) / 2048 : 0;
+  launch(k_adapt_reduce, dim3((uint32_t)(ba + bb), (uint32_t)a.n_pool), dim3(256), 0, s, a, g, piece, ba);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

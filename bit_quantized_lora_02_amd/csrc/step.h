@@ -38,4 +38,45 @@ hipError_t launch_norm_bwd(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t
                            const float *mean, const float *rstd, bf16_t *dX, float *part, hipStream_t s);
 hipError_t launch_norm_reduce(const float *part, int groups, int64_t D, bool f32, void *dw, void *db, hipStream_t s);
 
+// Adapters by token.  The tokens' rows, grouped by adapter: order holds the tokens in groups, group a at start[a] ..
+// start[a + 1] - 1 (group n_pool: those without an adapter), each in the order of the batch.
+constexpr int kPoolMax = 1000;
+constexpr int64_t kAdaptSmall = 64;  // up to so many tokens the forward's workgroups group them by themselves
+struct AdaptRows {
+  const int32_t *index = nullptr;  // [T] adapter of each token
+  int64_t T = 0;
+  int n_pool = 0, r = 0;
+  const int32_t *rank = nullptr;   // [n_pool] or null (r)
+  const float *scale = nullptr;    // [n_pool]
+  int32_t *order = nullptr, *start = nullptr;  // [T], [n_pool + 2]; null: at most kAdaptSmall tokens
+};
+// Groups the tokens and, for each non-null `to`, transposes a pool: from [n_pool][rows][cols] to [n_pool][cols][rows].
+struct AdaptTurn {
+  const bf16_t *from = nullptr;
+  bf16_t *to = nullptr;
+  int64_t rows = 0, cols = 0;
+};
+hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const AdaptTurn &t1, hipStream_t s);
+// U[split][t][j] = (scale) P[t] . Q_a[j] over a range of K, Q [n_pool][r][K]: ranges of K (their sums come apart).
+int adapt_ranges(int64_t T, int n_pool, int64_t K);
+hipError_t launch_adapt_shrink(const AdaptRows &a, const bf16_t *P, int64_t K, const bf16_t *Q, bool scaled, int ranges,
+                               float *U, hipStream_t s);
+// out[t] = bf16(base[t] + (scale) U[t] . Q_a^T), Q [n_pool][N][r], U the sum of its ranges (also to U_out unless null).
+hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, const bf16_t *Q, int64_t N, bool scaled,
+                               const bf16_t *base, bf16_t *out, float *U_out, hipStream_t s);
+// Gradients of the pools: dA[a][j][k] = sum over the group's tokens of dU[t][j] X[t][k], dB[a][n][j] = scale times that of
+// U[t][j] dY[t][n].  Groups are cut into pieces of `piece` tokens; those of a group of several go to part.
+int adapt_piece(int64_t T, int64_t n_in, int64_t n_out);
+inline int64_t adapt_slots(int64_t T, int piece) { return 2 * (T / piece); }  // pieces of groups of several, at most
+struct AdaptGrads {
+  const float *dU = nullptr, *U = nullptr;
+  int dU_ranges = 1, U_ranges = 1;
+  const bf16_t *X = nullptr, *dY = nullptr;
+  int64_t n_in = 0, n_out = 0;
+  float *part_a = nullptr, *part_b = nullptr;  // [slots][r][n_in], [slots][n_out][r]
+  bf16_t *dA = nullptr, *dB = nullptr;
+};
+hipError_t launch_adapt_grads(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s);
+hipError_t launch_adapt_reduce(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s);
+
 }  // namespace qlora

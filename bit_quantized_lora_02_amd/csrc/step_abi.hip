@@ -74,9 +74,175 @@ int check_norm(int64_t T, int64_t D, int weights) {
   return QLORA_OK;
 }
 
+// ------------------------------------------------------------------- adapters
+int check_adapters(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32_t r) {
+  if (int rc = check_tokens(T)) return rc;
+  if (n_in < 8 || n_in > kMaxDim || n_in % 8 || n_out < 8 || n_out > kMaxDim || n_out % 8)
+    return fail(QLORA_EINVAL, "n_in and n_out must be positive multiples of 8, at most 2^22 (got %lld, %lld)", (long long)n_in,
+                (long long)n_out);
+  if (n_pool < 1 || n_pool > kPoolMax) return fail(QLORA_EINVAL, "n_pool must be in [1, %d] (got %d)", kPoolMax, (int)n_pool);
+  if (r < 8 || r > QLORA_MAX_RANK || r % 8)
+    return fail(QLORA_EINVAL, "r must be a multiple of 8 in [8, %d] (got %d)", QLORA_MAX_RANK, (int)r);
+  if (n_pool * n_in > (int64_t)1 << 28 || n_pool * n_out > (int64_t)1 << 28)
+    return fail(QLORA_EINVAL, "n_pool x n_in and n_pool x n_out must be at most 2^28");
+  if (T * n_in >= (int64_t)1 << 32 || T * n_out >= (int64_t)1 << 32)
+    return fail(QLORA_EINVAL, "T x n_in and T x n_out must be below 2^32");
+  return QLORA_OK;
+}
+
+struct AdaptPlan {
+  int ranges_u = 1, ranges_du = 1, piece = 0;
+  size_t order = 0, start = 0, u = 0, du = 0, at = 0, bt = 0, part_a = 0, part_b = 0, total = 0;
+};
+
+AdaptPlan adapt_plan(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32_t r, bool backward) {
+  AdaptPlan p;
+  Parts w;
+  p.order = w.take((size_t)T * 4);
+  p.start = w.take((size_t)(n_pool + 2) * 4);
+  p.ranges_u = adapt_ranges(T, n_pool, n_in);
+  p.u = w.take((size_t)p.ranges_u * T * r * 4);
+  if (backward) {
+    p.ranges_du = adapt_ranges(T, n_pool, n_out);
+    p.du = w.take((size_t)p.ranges_du * T * r * 4);
+    p.at = w.take((size_t)n_pool * r * n_in * 2);
+    p.bt = w.take((size_t)n_pool * r * n_out * 2);
+    p.piece = adapt_piece(T, n_in, n_out);
+    const size_t slots = (size_t)adapt_slots(T, p.piece);
+    p.part_a = w.take(slots * r * n_in * 4);
+    p.part_b = w.take(slots * r * n_out * 4);
+  }
+  p.total = w.total;
+  return p;
+}
+
+int check_pool(const void *X, const void *A, const void *B, const int32_t *rank, const float *scale, const int32_t *index,
+               int64_t T) {
+  if (!A || !B || !scale) return fail(QLORA_EINVAL, "A_pool, B_pool and scale must not be NULL");
+  if (T > 0 && (!X || !index)) return fail(QLORA_EINVAL, "X and index must not be NULL");
+  if (!aligned16(X) || !aligned16(A) || !aligned16(B)) return fail(QLORA_EINVAL, "X, A_pool and B_pool must be 16-byte aligned");
+  if (!aligned_to(rank, 4) || !aligned_to(scale, 4) || !aligned_to(index, 4))
+    return fail(QLORA_EINVAL, "rank, scale and index must be 4-byte aligned");
+  return QLORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int qlora_adapters_workspace_bytes(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32_t r, int backward,
+                                   size_t *bytes) {
+  if (!bytes) return fail(QLORA_EINVAL, "bytes is NULL");
+  if (int rc = check_adapters(T, n_in, n_out, n_pool, r)) return rc;
+  *bytes = adapt_plan(T, n_in, n_out, n_pool, r, backward != 0).total;
+  return QLORA_OK;
+}
+
+int qlora_adapters_fwd(const qlora_bf16 *X, int64_t T, int64_t n_in, const qlora_bf16 *A_pool, const qlora_bf16 *B_pool,
+                       int64_t n_out, int32_t n_pool, int32_t r, const int32_t *rank, const float *scale,
+                       const int32_t *index, const qlora_bf16 *base, qlora_bf16 *Y, float *U_out, void *ws, size_t ws_bytes,
+                       void *stream) {
+  int rc = check_adapters(T, n_in, n_out, n_pool, r);
+  if (rc) return rc;
+  if ((rc = check_pool(X, A_pool, B_pool, rank, scale, index, T))) return rc;
+  if (T > 0 && !Y) return fail(QLORA_EINVAL, "Y must not be NULL");
+  if (!aligned16(base) || !aligned16(Y) || !aligned16(U_out))
+    return fail(QLORA_EINVAL, "base, Y and U_out must be 16-byte aligned");
+  const AdaptPlan p = adapt_plan(T, n_in, n_out, n_pool, r, false);
+  if ((rc = check_workspace(ws, ws_bytes, p.total))) return rc;
+  if ((rc = check_device(nullptr))) return rc;
+  if (T == 0) return QLORA_OK;
+  hipStream_t s = (hipStream_t)stream;
+  char *w = (char *)ws;
+  AdaptRows a;
+  a.index = index;
+  a.T = T;
+  a.n_pool = n_pool;
+  a.r = r;
+  a.rank = rank;
+  a.scale = scale;
+  if (T > kAdaptSmall) {
+    a.order = (int32_t *)(w + p.order);
+    a.start = (int32_t *)(w + p.start);
+    LAUNCH("adapters_plan", launch_adapt_plan(a, AdaptTurn(), AdaptTurn(), s));
+  }
+  const bool direct = U_out && p.ranges_u == 1;
+  float *U = direct ? U_out : (float *)(w + p.u);
+  LAUNCH("adapters_shrink", launch_adapt_shrink(a, X, n_in, A_pool, false, p.ranges_u, U, s));
+  LAUNCH("adapters_expand",
+         launch_adapt_expand(a, U, p.ranges_u, B_pool, n_out, true, base, Y, direct ? nullptr : U_out, s));
+  return QLORA_OK;
+}
+
+int qlora_adapters_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, int64_t n_in, const qlora_bf16 *A_pool,
+                       const qlora_bf16 *B_pool, int64_t n_out, int32_t n_pool, int32_t r, const int32_t *rank,
+                       const float *scale, const int32_t *index, const float *U, const qlora_bf16 *base, qlora_bf16 *dX,
+                       qlora_bf16 *dA, qlora_bf16 *dB, void *ws, size_t ws_bytes, void *stream) {
+  int rc = check_adapters(T, n_in, n_out, n_pool, r);
+  if (rc) return rc;
+  if ((rc = check_pool(X, A_pool, B_pool, rank, scale, index, T))) return rc;
+  if (T > 0 && !dY) return fail(QLORA_EINVAL, "dY must not be NULL");
+  if (!aligned16(dY) || !aligned16(U) || !aligned16(base) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB))
+    return fail(QLORA_EINVAL, "dY, U, base, dX, dA and dB must be 16-byte aligned");
+  const AdaptPlan p = adapt_plan(T, n_in, n_out, n_pool, r, true);
+  if ((rc = check_workspace(ws, ws_bytes, p.total))) return rc;
+  if ((rc = check_device(nullptr))) return rc;
+  const bool dx = dX && T > 0;
+  if (!dx && !dA && !dB) return QLORA_OK;
+  hipStream_t s = (hipStream_t)stream;
+  char *w = (char *)ws;
+  AdaptRows a;
+  a.index = index;
+  a.T = T;
+  a.n_pool = n_pool;
+  a.r = r;
+  a.rank = rank;
+  a.scale = scale;
+  a.order = (int32_t *)(w + p.order);
+  a.start = (int32_t *)(w + p.start);
+  AdaptTurn ta, tb;  // A [r][n_in] to [n_in][r] for dX, B [n_out][r] to [r][n_out] for dU
+  if (dx) {
+    ta.from = A_pool;
+    ta.to = (bf16_t *)(w + p.at);
+    ta.rows = r;
+    ta.cols = n_in;
+  }
+  if (T > 0 && (dx || dA)) {
+    tb.from = B_pool;
+    tb.to = (bf16_t *)(w + p.bt);
+    tb.rows = n_out;
+    tb.cols = r;
+  }
+  LAUNCH("adapters_plan", launch_adapt_plan(a, ta, tb, s));
+  AdaptGrads g;
+  g.X = X;
+  g.dY = dY;
+  g.n_in = n_in;
+  g.n_out = n_out;
+  g.part_a = (float *)(w + p.part_a);
+  g.part_b = (float *)(w + p.part_b);
+  g.dA = dA;
+  g.dB = dB;
+  g.U = U;
+  if (T > 0) {
+    if (dB && !U) {
+      float *u = (float *)(w + p.u);
+      LAUNCH("adapters_shrink", launch_adapt_shrink(a, X, n_in, A_pool, false, p.ranges_u, u, s));
+      g.U = u;
+      g.U_ranges = p.ranges_u;
+    }
+    if (dx || dA) {
+      float *du = (float *)(w + p.du);
+      LAUNCH("adapters_shrink", launch_adapt_shrink(a, dY, n_out, tb.to, true, p.ranges_du, du, s));
+      g.dU = du;
+      g.dU_ranges = p.ranges_du;
+    }
+    if (dx) LAUNCH("adapters_expand", launch_adapt_expand(a, g.dU, p.ranges_du, ta.to, n_in, false, base, dX, nullptr, s));
+    if (dA || dB) LAUNCH("adapters_grads", launch_adapt_grads(a, g, p.piece, s));
+  }
+  if (dA || dB) LAUNCH("adapters_reduce", launch_adapt_reduce(a, g, p.piece, s));
+  return QLORA_OK;
+}
 
 int qlora_embed(const int64_t *tokens, int64_t T, const qlora_bf16 *W, int64_t n_vocab, int64_t n_in, float scale,
                 qlora_bf16 *Y, void *stream) {

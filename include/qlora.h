@@ -60,6 +60,7 @@ typedef uint16_t qlora_bf16; /* bf16 bit pattern */
 #define QLORA_MAX_RANK 128
 #define QLORA_MAX_TARGETS 256 /* teacher logits per row of qlora_head_distill */
 #define QLORA_MAX_NORM 32768  /* columns of qlora_layer_norm */
+#define QLORA_MAX_POOL 1000   /* adapters of qlora_adapters_fwd */
 
 #define QLORA_WEIGHT_BF16 0 /* type of a layer norm's weight and bias and of their gradients */
 #define QLORA_WEIGHT_F32 1
@@ -477,6 +478,47 @@ int qlora_layer_norm_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, i
                          int weight_type, const float *mean, const float *rstd, qlora_bf16 *dX, void *dweight, void *dbias,
                          void *ws, size_t ws_bytes, void *stream);
 int qlora_layer_norm_workspace_bytes(int64_t T, int64_t n_in, size_t *bytes);
+
+/*
+ * Adapters of many requests beside a shared projection (pranaymahendrakar, Researcher level, "The variants worth
+ * knowing": one base model in memory, many adapters, requests for different adapters batched together), each token with
+ * an adapter of its own, in any order, added to what any projection gave:
+ *   u_t = X[t] . A_a^T,   Y[t] = bf16_rne(base[t] + scale[a] . u_t . B_a^T),   a = index[t]
+ * A_pool [n_pool, r, n_in], B_pool [n_pool, n_out, r] bf16; index [T] int32: one outside [0, n_pool) means no adapter
+ * (Y[t] = base[t], its row of X is not read).  rank [n_pool] int32, or NULL for r: adapter a has the first rank[a] rows of
+ * its A and columns of its B (cut to [0, r]); the others are not part of it and may hold anything.  scale [n_pool]
+ * binary32 (alpha_a / rank_a, say).  base [T, n_out] bf16, or NULL for zeros; Y may be base itself.  U_out [T, r]
+ * binary32 receives u (zeros past the rank and where there is no adapter) for the backward, or NULL.  All device memory;
+ * rank, scale and index are read by the kernels.  u is binary32 and enters its second product as two bf16 parts (off by
+ * at most 2^-16 of it); the products accumulate in binary32 in a fixed order and Y is rounded once.
+ * n_in, n_out % 8 == 0, 8 <= r <= QLORA_MAX_RANK with r % 8 == 0, 1 <= n_pool <= QLORA_MAX_POOL, n_pool * n_in and
+ * n_pool * n_out <= 2^28, T <= 2^22, T * n_in and T * n_out < 2^32.  X, A_pool, B_pool, base, Y, U_out 16-byte aligned,
+ * rank, scale, index 4-byte; outputs overlap no input except Y base.
+ * ws: qlora_adapters_workspace_bytes(T, n_in, n_out, n_pool, r, 0), 256-byte aligned; nothing in it needs to start at
+ * zero, and calls that overlap in time need workspaces of their own.
+ */
+int qlora_adapters_fwd(const qlora_bf16 *X, int64_t T, int64_t n_in, const qlora_bf16 *A_pool, const qlora_bf16 *B_pool,
+                       int64_t n_out, int32_t n_pool, int32_t r, const int32_t *rank, const float *scale,
+                       const int32_t *index, const qlora_bf16 *base, qlora_bf16 *Y, float *U_out, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/*
+ * Its backward, for adapters that are trained together (each on its own tokens):
+ *   du_t = scale[a] . dY[t] . B_a                       dX[t] = bf16_rne(base[t] + du_t . A_a)
+ *   dA_a = sum over a's tokens of du_t^T . X[t]         dB_a  = scale[a] . sum of dY[t]^T . u_t
+ * U [T, r] binary32 as written by the forward, or NULL to recompute it.  base [T, n_in] bf16: the shared projection's
+ * part of dX, or NULL for zeros; dX may be base itself.  dA [n_pool, r, n_in], dB [n_pool, n_out, r] bf16 are written
+ * completely, with zeros past the ranks and for adapters without tokens (T = 0: everywhere).  Each of dX, dA and dB may be
+ * NULL (not formed).  u and du stay binary32 and enter the products as two bf16 parts; sums run in a fixed order.
+ * ws: qlora_adapters_workspace_bytes(..., 1): the tokens in groups, u and du, both pools transposed, and binary32 sums of
+ * pieces of 64 to 1024 tokens.
+ */
+int qlora_adapters_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, int64_t n_in, const qlora_bf16 *A_pool,
+                       const qlora_bf16 *B_pool, int64_t n_out, int32_t n_pool, int32_t r, const int32_t *rank,
+                       const float *scale, const int32_t *index, const float *U, const qlora_bf16 *base, qlora_bf16 *dX,
+                       qlora_bf16 *dA, qlora_bf16 *dB, void *ws, size_t ws_bytes, void *stream);
+int qlora_adapters_workspace_bytes(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32_t r, int backward,
+                                   size_t *bytes);
 
 /* Static text for a QLORA_E* code. */
 const char *qlora_strerror(int code);
