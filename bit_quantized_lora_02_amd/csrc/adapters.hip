@@ -57,6 +57,17 @@ __device__ __forceinline__ int rank_of(const AdaptRows &a, int group) {
   return k < 0 ? 0 : k > a.r ? a.r : k;
 }
 
+// Lanes whose number is this lane's, by a vote on each of its bits.
+__device__ __forceinline__ uint64_t same_lanes(int number, int bits) {
+  uint64_t m = ~(uint64_t)0;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (number >> b) & 1;
+    const uint64_t vote = __ballot(one);
+    m &= one ? vote : ~vote;
+  }
+  return m;
+}
+
 // At most M tokens of one group: places p0 .. p0 + n - 1 of the order.  Of a group that is cut into several tiles, `slot`
 // numbers them over all such groups (-1: the group's only tile).
 struct Tile {
@@ -103,30 +114,30 @@ __device__ __forceinline__ bool find_tokens(const AdaptRows &a, int id, Tile *ti
     }
     return true;
   }
-  const int group = lane < a.T ? group_of(a, lane) : -1;
-  uint64_t rest = __ballot(lane < a.T);
-  while (rest) {
-    const int g = __builtin_amdgcn_readlane(group, __builtin_ctzll(rest));
-    const uint64_t mine = __ballot(group == g);
-    const int n = __popcll(mine), tiles = (n + M - 1) / M;
-    if (id < tiles) {
-      tile->group = g;
-      tile->p0 = id * M;
-      tile->n = n - id * M < M ? n - id * M : M;
-      tile->slot = -1;
+  // (the lanes of a group by a vote per bit of its number; its first lane counts its tiles)
+  const int groups = a.n_pool + 1, group = lane < a.T ? group_of(a, lane) : groups;
+  const uint64_t same = same_lanes(group, 32 - __builtin_clz(groups)), before = ((uint64_t)1 << lane) - 1;
+  const int count = __popcll(same);
+  const int tiles = lane < a.T && (same & before) == 0 ? (count + M - 1) / M : 0, sum = scan_dpp(tiles);
+  const uint64_t at = __ballot(sum > id);
+  if (at == 0) return false;
+  const int lead = __builtin_ctzll(at), n = __builtin_amdgcn_readlane(count, lead);
+  const int j = id - (__builtin_amdgcn_readlane(sum, lead) - __builtin_amdgcn_readlane(tiles, lead));
+  tile->group = __builtin_amdgcn_readlane(group, lead);
+  tile->p0 = j * M;
+  tile->n = n - j * M < M ? n - j * M : M;
+  tile->slot = -1;
+  // the group's lanes go to the front, in order, and each lane takes its token from there
+  const bool mine = group == tile->group;
+  const uint64_t all = __ballot(mine);
+  const int to = mine ? __popcll(all & before) : n + __popcll(~all & before);
+  const int sorted = __builtin_amdgcn_ds_permute(to * 4, lane);
 #pragma unroll
-      for (int m = 0; m < (M + 15) / 16; ++m) {
-        const int p = m * 16 + (lane & 15), place = tile->p0 + (p < tile->n ? p : 0);
-        uint64_t left = mine;  // its place-th bit
-        for (int i = 0; i < place; ++i) left &= left - 1;
-        tokens[m] = __builtin_ctzll(left);
-      }
-      return true;
-    }
-    id -= tiles;
-    rest &= ~mine;
+  for (int m = 0; m < (M + 15) / 16; ++m) {
+    const int p = m * 16 + (lane & 15);
+    tokens[m] = __builtin_amdgcn_ds_bpermute((tile->p0 + (p < tile->n ? p : 0)) * 4, sorted);
   }
-  return false;
+  return true;
 }
 
 // u as two bf16 parts, hi + lo (16 bits of it).
@@ -150,67 +161,89 @@ __device__ __forceinline__ u32x4_t below_rank(u32x4_t v, int left) {
   return v;
 }
 
+// Values that are used once (long ones): past the caches, which the adapters' rows need.
+template <bool ONCE>
+__device__ __forceinline__ u32x4_t load_once(const bf16_t *p) {
+  return ONCE ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(p)) : load16(p);
+}
+template <bool ONCE>
+__device__ __forceinline__ void store_once(bf16_t *p, const u32x4_t &v) {
+  if (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(p));
+  else store16(p, v);
+}
+
 // ----------------------------------------------------------------------- plan
 constexpr int kPlanWaves = 16;
 struct PlanShared {
   int at[kPlanWaves][1024];  // tokens of a wave's share in each group, then where the next of them goes
   int wave[kPlanWaves];
 };
+// The tokens are shared out to 16 waves in order.  A lane finds the lanes with its own group by a vote per bit of the
+// group's number; the first of them adds their count to the wave's, and a lane's place is the group's start, plus the
+// counts of earlier waves and steps, plus the equal lanes before it: the order of the batch is kept.
+constexpr int kPlanSteps = 8;  // of 64 tokens, whose groups a wave holds at once (all of its share up to 8192 tokens)
 __device__ __forceinline__ void plan_tokens(const AdaptRows &a, PlanShared &sh) {
-  auto &s_at = sh.at;
-  auto &s_wave = sh.wave;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, groups = a.n_pool + 1;
-  for (int k = tid; k < kPlanWaves * 1024; k += 1024) (&s_at[0][0])[k] = 0;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), groups = a.n_pool + 1;
+  const int bits = 32 - __builtin_clz(groups);
+  const int64_t per = ((a.T + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64, first = wave * per;
+  const int64_t end = first + per < a.T ? first + per : a.T;
+  int group[kPlanSteps];
+  uint64_t same[kPlanSteps];
+  auto load = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      const int64_t t = t0 + i * 64 + lane;
+      group[i] = t < end ? group_of(a, t) : groups;  // (no token: a group of its own)
+    }
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) same[i] = same_lanes(group[i], bits);
+  };
+  const uint64_t before = ((uint64_t)1 << lane) - 1;
+  load(first);
+  if (tid < groups)
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) sh.at[w][tid] = 0;
   __syncthreads();
-  const int64_t per = ((a.T + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64, t0 = wave * per;
-  const int64_t t1 = t0 + per < a.T ? t0 + per : a.T;
-  for (int64_t t = t0 + lane; t < t1; t += 64) atomicAdd(&s_at[wave][group_of(a, t)], 1);
+  for (int64_t t0 = first; t0 < end; t0 += 64 * kPlanSteps) {
+    if (t0 > first) load(t0);
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i)
+      if (group[i] < groups && (same[i] & before) == 0) atomicAdd(&sh.at[wave][group[i]], __popcll(same[i]));
+  }
   __syncthreads();
   int n = 0;  // thread k: tokens of group k
   if (tid < groups)
 #pragma unroll
-    for (int w = 0; w < kPlanWaves; ++w) n += s_at[w][tid];
+    for (int w = 0; w < kPlanWaves; ++w) n += sh.at[w][tid];
   const int sum = scan_dpp(n);
-  if (lane == 63) s_wave[wave] = sum;
+  if (lane == 63) sh.wave[wave] = sum;
   __syncthreads();
   int at = sum - n;
-  for (int w = 0; w < wave; ++w) at += s_wave[w];
+  for (int w = 0; w < wave; ++w) at += sh.wave[w];
   if (tid < groups) {
     a.start[tid] = at;
     if (tid == a.n_pool) a.start[groups] = at + n;
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) {
-      const int c = s_at[w][tid];
-      s_at[w][tid] = at;
+      const int c = sh.at[w][tid];
+      sh.at[w][tid] = at;
       at += c;
     }
   }
   __syncthreads();
-  for (int64_t t = t0 + lane; t - lane < t1; t += 64) {
-    const bool in = t < t1;
-    const int group = in ? group_of(a, t) : -1;
-    const uint64_t same = __ballot(group == __builtin_amdgcn_readfirstlane(group));
-    int rank, count;
-    if (same == __ballot(true)) {  // one group's tokens (a wave's lanes behind t1 are none: then not all are the same)
-      rank = lane;
-      count = 64;
-    } else {
-      rank = count = 0;
-#pragma unroll 8
-      for (int j = 0; j < 64; ++j) {
-        const bool eq = __builtin_amdgcn_readlane(group, j) == group;
-        rank += eq && j < lane ? 1 : 0;
-        count += eq ? 1 : 0;
+  const bool whole = per <= 64 * kPlanSteps;
+  if (!whole) load(first);
+  for (int64_t t0 = first; t0 < end; t0 += 64 * kPlanSteps) {
+    if (t0 > first) load(t0);
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      if (group[i] < groups) {
+        int *const at_ = &sh.at[wave][group[i]];
+        const int base = *at_;
+        a.order[base + __popcll(same[i] & before)] = (int32_t)(t0 + i * 64 + lane);
+        if ((same[i] & before) == 0) *at_ = base + __popcll(same[i]);  // (after all lanes have read it: one wave, in order)
       }
     }
-    int base = 0;
-    if (in) base = s_at[wave][group];
-    __builtin_amdgcn_wave_barrier();
-    if (in) {
-      a.order[base + rank] = (int32_t)t;
-      if (rank + 1 == count) s_at[wave][group] = base + count;
-    }
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -252,18 +285,26 @@ __global__ __launch_bounds__(1024) void k_adapt_plan(AdaptRows a, AdaptTurn t0, 
   else turn_pool(t1, blockIdx.x - 1 - blocks0, *reinterpret_cast<TurnShared *>(shared));
 }
 
+// A 16-byte chunk of a row of 64 values in LDS: the eight chunks of rows in turn, so that the 16 rows that an MFMA operand
+// reads at one place begin in different banks.
+__device__ __forceinline__ int chunk_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
 // --------------------------------------------------------------------- shrink
-// RT: rank tiles of 16.  Operands come straight from HBM: a lane reads 16 bytes of its row, four lanes 64 adjacent ones,
-// and two steps of the reduction a line.  What stands in a row that is none (behind the tile's tokens, past the rank)
-// stays in the sums of that row, which are not stored: such rows read a valid one's address.
+// RT: rank tiles of 16.  Eight waves take 64-value steps of the long axis in turn.  A step's rows come in whole lines
+// (eight lanes each) and go through a part of LDS that is the wave's own: no barriers.  Straight into the MFMA's layout,
+// where neighbouring lanes are neighbouring rows, each lane is a cache access of its own, which alone took 15 of 20 us
+// (4096 x 4096, rank up to 64; now 9).  What stands in a row that is none (past the rank) stays in that row's sums,
+// which are not stored.
 constexpr int kShrinkWaves = 8;
 template <int RT>
-__global__ __launch_bounds__(64 * kShrinkWaves) void k_adapt_shrink(AdaptRows a, const bf16_t *__restrict__ P, int64_t K,
+__global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_shrink(AdaptRows a, const bf16_t *__restrict__ P, int64_t K,
                                                                     const bf16_t *__restrict__ Q, bool scaled, int ranges,
                                                                     float *__restrict__ U) {
-  constexpr int LD = RT * 16 + 4;
-  __shared__ __attribute__((aligned(16))) float s_sum[kShrinkWaves][16][LD];
+  constexpr int LD = RT * 16 + 4, PART = RT < 2 ? RT : 2;  // rank tiles that are in LDS at once
+  constexpr int kOwn = 2048 * (1 + PART), kAll = kShrinkWaves * kOwn, kSums = kShrinkWaves * 16 * LD * 4;
+  __shared__ __attribute__((aligned(128))) char shared[kAll > kSums ? kAll : kSums];
   __shared__ int s_token[16];
+  float(*const s_sum)[16][LD] = reinterpret_cast<float(*)[16][LD]>(shared);
   const int id = blockIdx.x / ranges, range = blockIdx.x - id * ranges;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
   Tile tile;
@@ -275,44 +316,83 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapt_shrink(AdaptRows a,
 #pragma unroll
   for (int j = 0; j < RT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (rank > 0) {
-    const bf16_t *p = P + (int64_t)token[0] * K + 8 * g;
-    const bf16_t *q[RT];
+    char *const own = shared + wave * kOwn;
+    const int row0 = lane >> 3, chunk = lane & 7;  // of this lane's loads: rows row0 and row0 + 8 of 16
+    const bf16_t *p[2];
+    bool there[2];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      const int row = j * 16 + l;
-      q[j] = Q + ((int64_t)tile.group * a.r + (row < rank ? row : 0)) * K + 8 * g;
+    for (int h = 0; h < 2; ++h) {
+      there[h] = row0 + 8 * h < tile.n;
+      p[h] = P + (int64_t)__builtin_amdgcn_ds_bpermute((row0 + 8 * h) * 4, token[0]) * K + chunk * 8;
     }
-    const int64_t steps = (K + 63) / 64, per = (steps + ranges - 1) / ranges;
-    const int64_t first = range * per, end = first + per < steps ? first + per : steps;
-    u32x4_t pv[2][2], qv[2][RT][2];
-    auto load = [&](int64_t step, u32x4_t(&pv_)[2], u32x4_t(&qv_)[RT][2]) {
+    const char *q = (const char *)(Q + (int64_t)tile.group * a.r * K);
+    uint32_t row[RT][2];  // bytes from the adapter's first (r K <= 2^29)
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t k = step * 64 + h * 32;
-        const bool in = k + 8 * g < K;
-        pv_[h] = in ? load16(p + k) : u32x4_t{0u, 0u, 0u, 0u};
+        const int at = j * 16 + row0 + 8 * h;
+        row[j][h] = (uint32_t)(((at < rank ? at : 0) * K + chunk * 8) * 2);
+      }
+    const int64_t steps = (K + 63) / 64, per = (steps + ranges - 1) / ranges;
+    const int64_t first = range * per, end = first + per < steps ? first + per : steps;
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+    u32x4_t pv[2], qv[RT][2];
+    auto load = [&](int64_t k) {
+      const bool in = k + chunk * 8 < K;
 #pragma unroll
-        for (int j = 0; j < RT; ++j) qv_[j][h] = in ? load16(q[j] + k) : u32x4_t{0u, 0u, 0u, 0u};
+      for (int h = 0; h < 2; ++h) pv[h] = in && there[h] ? load16(p[h] + k) : zero;
+      if (k + 64 <= K) {
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) qv[j][h] = *reinterpret_cast<const u32x4_t *>(q + (row[j][h] + (uint32_t)k * 2));
+      } else {  // the rows' end
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            qv[j][h] = in ? *reinterpret_cast<const u32x4_t *>(q + (row[j][h] + (uint32_t)k * 2)) : zero;
       }
     };
-    auto mma = [&](const u32x4_t(&pv_)[2], const u32x4_t(&qv_)[RT][2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < RT; ++j) acc[j] = mfma16(qv_[j][h], pv_[h], acc[j]);
+    // Each tile begins at a step of its own: rows a power of two apart would otherwise meet in few memory channels.
+    const int n = (int)(end - first);
+    int at = n > 0 ? (int)((uint32_t)(id * 8 + wave) % (uint32_t)n) : 0;
+    auto next = [&] {
+      at += kShrinkWaves;
+      if (at >= n) at = at - n < n ? at - n : (int)((uint32_t)at % (uint32_t)n);
     };
-    int64_t step = first + wave;
-    if (step < end) load(step, pv[0], qv[0]);
-    while (step < end) {
-      if (step + kShrinkWaves < end) load(step + kShrinkWaves, pv[1], qv[1]);
-      mma(pv[0], qv[0]);
-      step += kShrinkWaves;
-      if (step >= end) break;
-      if (step + kShrinkWaves < end) load(step + kShrinkWaves, pv[0], qv[0]);
-      mma(pv[1], qv[1]);
-      step += kShrinkWaves;
+    if (wave < n) load((first + at) * 64);
+    for (int i = wave; i < n; i += kShrinkWaves) {
+      u32x4_t pf[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4_t *>(own + chunk_at(row0 + 8 * h, chunk)) = pv[h];
+#pragma unroll
+      for (int j0 = 0; j0 < RT; j0 += PART) {
+#pragma unroll
+        for (int j = 0; j < PART; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<u32x4_t *>(own + 2048 * (1 + j) + chunk_at(row0 + 8 * h, chunk)) = qv[j0 + j][h];
+        if (j0 + PART == RT) {  // (all of this step is on its way)
+          next();
+          if (i + kShrinkWaves < n) load((first + at) * 64);
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (j0 == 0)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) pf[h] = *reinterpret_cast<const u32x4_t *>(own + chunk_at(l, 4 * h + g));
+#pragma unroll
+        for (int j = 0; j < PART; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[j0 + j] = mfma16(*reinterpret_cast<const u32x4_t *>(own + 2048 * (1 + j) + chunk_at(l, 4 * h + g)), pf[h],
+                                 acc[j0 + j]);
+        __builtin_amdgcn_wave_barrier();
+      }
     }
   }
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < RT; ++j) *reinterpret_cast<f32x4_t *>(&s_sum[wave][l][j * 16 + 4 * g]) = acc[j];
   __syncthreads();
@@ -337,102 +417,154 @@ __device__ __forceinline__ void load_u(const AdaptRows &a, const float *__restri
   for (int i = 0; i < 8; ++i) u[i] = 0.f;
   if (j0 >= rank) return;
   const float *p = U + token * a.r + j0;
-  for (int q = 0; q < ranges; ++q, p += a.T * a.r) {
-    const float4 x = reinterpret_cast<const float4 *>(p)[0], y = reinterpret_cast<const float4 *>(p)[1];
-    u[0] += x.x, u[1] += x.y, u[2] += x.z, u[3] += x.w, u[4] += y.x, u[5] += y.y, u[6] += y.z, u[7] += y.w;
+  const int64_t step = a.T * a.r;
+  for (int q = 0; q < ranges; q += 4) {  // four ranges in flight; what is behind the last adds nothing
+    float4 x[4], y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (q + e < ranges) {
+        x[e] = reinterpret_cast<const float4 *>(p + (q + e) * step)[0];
+        y[e] = reinterpret_cast<const float4 *>(p + (q + e) * step)[1];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u[0] += x[e].x, u[1] += x[e].y, u[2] += x[e].z, u[3] += x[e].w;
+      u[4] += y[e].x, u[5] += y[e].y, u[6] += y[e].z, u[7] += y[e].w;
+    }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) u[i] = j0 + i < rank ? u[i] : 0.f;
 }
 
 // --------------------------------------------------------------------- expand
-// KS: 32-wide steps over the rank, each an MFMA with u's high part and one with its low part; KS = 0 (rank up to 16): both
-// parts side by side in one.  The rows of Q that an MFMA takes are chosen so that a lane ends up with 16 adjacent columns
-// of its token: tile p of the four takes rows 16 (m / 4) + 4 p + m % 4.
+// MT: tiles of 16 tokens.  KS: 32-wide steps over the rank, each an MFMA with u's high part and one with its low part;
+// KS = 0 (rank up to 16): both parts side by side in one.  A wave takes 32 rows of Q at a time, which lie together in
+// memory, through its own part of LDS (see k_adapt_shrink), and the products of the four waves go through LDS, so that base
+// and output are read and written 256 bytes of a row at a time: from the MFMA's layout (64 bytes of 16 tokens each)
+// a copy alone reached 3.9 to 4.9 TB/s, in such pieces 5.8.
+constexpr int kExpandCols = 128;
 template <int KS, int MT>
-__global__ __launch_bounds__(256) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
-                                                      const bf16_t *__restrict__ Q, int64_t N, bool scaled, int64_t per,
-                                                      int blocks, const bf16_t *base, bf16_t *out,
-                                                      float *__restrict__ U_out) {
-  constexpr int KQ = KS ? KS : 1;
+__global__ __launch_bounds__(256, 4) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
+                                                         const bf16_t *__restrict__ Q, int64_t N, bool scaled, int64_t per,
+                                                         int blocks, const bf16_t *base, bf16_t *out,
+                                                         float *__restrict__ U_out) {
+  constexpr int CP = KS ? KS * 4 : 2, KQ = KS ? KS : 1, TOKENS = 16 * MT;  // CP: 16-byte chunks of a row of the adapter
+  constexpr int kRowsQ = 32 * CP * 16, kOut = TOKENS * (kExpandCols + 4) * 4, kParts = TOKENS * CP * 32;
+  __shared__ __attribute__((aligned(128))) char s_q[4][kRowsQ];
+  __shared__ __attribute__((aligned(128))) char s_mem[kOut > kParts ? kOut : kParts];
+  __shared__ int s_token[TOKENS];
+  float(*const s_out)[kExpandCols + 4] = reinterpret_cast<float(*)[kExpandCols + 4]>(s_mem);
   const int id = blockIdx.x / blocks, block = blockIdx.x - id * blocks;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l = lane & 15;
+  // chunk of a row of CP chunks: rows in turn, as chunk_at
+  auto swizzled = [](int row, int chunk) {
+    return (row * CP + (CP == 2 ? chunk : chunk ^ (CP == 4 ? (row >> 2) & 3 : row & 7))) * 16;
+  };
   Tile tile;
   int token[MT];
-  if (!find_tokens<16 * MT>(a, id, &tile, token)) return;
+  if (!find_tokens<TOKENS>(a, id, &tile, token)) return;
   const int rank = rank_of(a, tile.group);
-  const float scale = scaled && tile.group < a.n_pool ? a.scale[tile.group] : 1.f;
-  if (U_out && block == 0 && wave == 0) {
+  if (rank == 0 && base == out && !U_out) return;
+  if (wave == 0 && g == 0)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      if (m * 16 + l < tile.n)
-        for (int j = 8 * g; j < a.r; j += 32) {
-          float u[8];
-          load_u(a, U, ranges, token[m], j, rank, u);
-          float4 *to = reinterpret_cast<float4 *>(U_out + (int64_t)token[m] * a.r + j);
-          to[0] = make_float4(u[0], u[1], u[2], u[3]);
-          to[1] = make_float4(u[4], u[5], u[6], u[7]);
-        }
+    for (int m = 0; m < MT; ++m) s_token[m * 16 + l] = token[m];
+  __syncthreads();
+  const float scale = scaled && tile.group < a.n_pool ? a.scale[tile.group] : 1.f;
+  // u of the tile's tokens: the ranges' sums, to U_out, and times the scale in two parts to LDS
+  for (int e = tid; e < TOKENS * CP; e += 256) {
+    const int n = e / CP, c = e % CP;
+    float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (n < tile.n) load_u(a, U, ranges, s_token[n], c * 8, rank, u);
+    if (U_out && block == 0 && n < tile.n && c * 8 < a.r) {
+      float4 *to = reinterpret_cast<float4 *>(U_out + (int64_t)s_token[n] * a.r + c * 8);
+      to[0] = make_float4(u[0], u[1], u[2], u[3]);
+      to[1] = make_float4(u[4], u[5], u[6], u[7]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] *= scale;
+    u32x4_t h, o;
+    split8(u, &h, &o);
+    *reinterpret_cast<u32x4_t *>(s_mem + swizzled(n, c)) = h;
+    *reinterpret_cast<u32x4_t *>(s_mem + TOKENS * CP * 16 + swizzled(n, c)) = o;
   }
-  if (rank == 0 && base == out) return;
+  __syncthreads();
   u32x4_t hi[MT][KQ], lo[MT][KQ];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int k = 0; k < KQ; ++k) {
-      float u[8];
-      load_u(a, U, ranges, token[m], KS ? k * 32 + 8 * g : 8 * (g & 1), rank, u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] *= scale;
-      split8(u, &hi[m][k], &lo[m][k]);
-      if (!KS && g >= 2) hi[m][k] = lo[m][k];
+      const char *from = s_mem + swizzled(m * 16 + l, KS ? k * 4 + g : g & 1);
+      if (KS) {
+        hi[m][k] = *reinterpret_cast<const u32x4_t *>(from);
+        lo[m][k] = *reinterpret_cast<const u32x4_t *>(from + TOKENS * CP * 16);
+      } else {
+        hi[m][k] = *reinterpret_cast<const u32x4_t *>(from + (g < 2 ? 0 : TOKENS * CP * 16));
+      }
     }
-  const bf16_t *q = Q + (int64_t)(tile.group < a.n_pool ? tile.group : 0) * N * a.r;
+  __syncthreads();
   const int64_t first = block * per, end = first + per < N ? first + per : N;
-  for (int64_t n0 = first + wave * 64; n0 < end; n0 += 256) {
-    u32x4_t qv[4][KQ], bv[MT][2];
+  // rows as they lie in memory: a thread's 8 columns of every 16th token; its chunks of the wave's 32 rows of Q
+  const int row0 = tid >> 4, col0 = (tid & 15) * 8;
+  int64_t at[MT];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int64_t row = n0 + 16 * (l >> 2) + 4 * p + (l & 3);
+  for (int i = 0; i < MT; ++i) at[i] = (int64_t)s_token[row0 + 16 * i] * N + col0;
+  const char *const q = (const char *)(Q + (int64_t)(rank ? tile.group : 0) * N * a.r);
+  char *const own = s_q[wave];
+  const bool full = rank == CP * 8;
+  for (int64_t n0 = first; n0 < end; n0 += kExpandCols) {
+    u32x4_t bv[MT];
 #pragma unroll
-      for (int k = 0; k < KQ; ++k) {
-        const int j0 = KS ? k * 32 + 8 * g : 8 * (g & 1);
-        qv[p][k] = u32x4_t{0u, 0u, 0u, 0u};
-        if (j0 < rank && row < N) qv[p][k] = load16(q + row * a.r + j0);
-        if (rank & 7) qv[p][k] = below_rank(qv[p][k], rank - j0);
-      }
+    for (int i = 0; i < MT; ++i) {
+      bv[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (base && row0 + 16 * i < tile.n && n0 + col0 < end) bv[i] = load_once<MT == 2>(base + at[i] + n0);
     }
-    const int64_t col = n0 + 16 * g;
+    if (rank) {
+      u32x4_t qv[CP / 2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        bv[m][h] = u32x4_t{0u, 0u, 0u, 0u};
-        if (base && m * 16 + l < tile.n && col + 8 * h < N) bv[m][h] = load16(base + (int64_t)token[m] * N + col + 8 * h);
+      for (int i = 0; i < CP / 2; ++i) {  // (behind the last row: any row, whose products are not stored)
+        const int r = i * (64 / CP) + lane / CP, c = lane % CP;
+        const int64_t n = n0 + wave * 32 + r, row = n < N ? n : N - 1;
+        qv[i] = *reinterpret_cast<const u32x4_t *>(q + ((uint32_t)row * (uint32_t)a.r + (c * 8 < a.r ? c * 8 : 0)) * 2u);
+        if (!full) qv[i] = below_rank(qv[i], rank - c * 8);
+        *reinterpret_cast<u32x4_t *>(own + swizzled(r, c)) = qv[i];
       }
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      f32x4_t acc[4];
+      for (int p = 0; p < 2; ++p) {
+        u32x4_t qf[KQ];
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        acc[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < KQ; ++k)
+          qf[k] = *reinterpret_cast<const u32x4_t *>(own + swizzled(p * 16 + l, KS ? k * 4 + g : g & 1));
 #pragma unroll
-        for (int k = 0; k < KQ; ++k) {
-          acc[p] = mfma16(qv[p][k], hi[m][k], acc[p]);
-          if (KS) acc[p] = mfma16(qv[p][k], lo[m][k], acc[p]);
+        for (int m = 0; m < MT; ++m) {
+          f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < KQ; ++k) {
+            acc = mfma16(qf[k], hi[m][k], acc);
+            if (KS) acc = mfma16(qf[k], lo[m][k], acc);
+          }
+          *reinterpret_cast<f32x4_t *>(&s_out[m * 16 + l][wave * 32 + 16 * p + 4 * g]) = acc;
         }
       }
-      if (m * 16 + l < tile.n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (col + 8 * h < N) {
-            float y[8];
-            unpack8(bv[m][h], y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] += acc[2 * h + (i >> 2)][i & 3];
-            store16(out + (int64_t)token[m] * N + col + 8 * h, pack8(y));
-          }
+      __syncthreads();
     }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      if (row0 + 16 * i < tile.n && n0 + col0 < end) {
+        if (rank) {
+          float y[8];
+          unpack8(bv[i], y);
+          const f32x4_t *d = reinterpret_cast<const f32x4_t *>(&s_out[row0 + 16 * i][col0]);
+          const f32x4_t d0 = d[0], d1 = d[1];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] += d0[e], y[4 + e] += d1[e];
+          bv[i] = pack8(y);
+        }
+        store_once<MT == 2>(out + at[i] + n0, bv[i]);
+      }
+    if (rank) __syncthreads();
   }
 }
 
@@ -605,8 +737,8 @@ hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const Adap
 
 int adapt_ranges(int64_t T, int n_pool, int64_t K) {
   const int64_t tiles = (T + 15) / 16 + (n_pool < T ? n_pool : T) / 2, most = (K + 511) / 512;
-  int64_t n = tiles < 1 ? 1 : 512 / tiles;
-  n = n < 1 ? 1 : n > 16 ? 16 : n;
+  int64_t n = tiles < 1 ? 1 : 768 / tiles;
+  n = n < 1 ? 1 : n > 8 ? 8 : n;
   return (int)(n < most ? n : most);
 }
 
@@ -625,12 +757,14 @@ hipError_t launch_adapt_shrink(const AdaptRows &a, const bf16_t *P, int64_t K, c
 hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, const bf16_t *Q, int64_t N, bool scaled,
                                const bf16_t *base, bf16_t *out, float *U_out, hipStream_t s) {
   const bool wide = a.T >= 2048;
-  const int64_t tiles = most_tiles(a, wide ? 32 : 16), cols = (N + 255) / 256;
-  int64_t per = 1;  // steps of 256 columns per workgroup
-  while (per < 4 && tiles * ((cols + 2 * per - 1) / (2 * per)) >= 2048) per *= 2;
-  const int blocks = (int)((cols + per - 1) / per);
+  const int64_t tiles = most_tiles(a, wide ? 32 : 16), cols = (N + kExpandCols - 1) / kExpandCols;
+  // Column blocks: enough workgroups for the GPU, few enough that their lookups and u are shared by several steps; a
+  // multiple of 8, so that a block's rows of Q stay in the L2 of one XCD (workgroups go round the eight).
+  int64_t blocks = (2048 + tiles - 1) / tiles;
+  blocks = cols <= 8 ? cols : blocks >= cols ? (cols + 7) / 8 * 8 : (blocks + 7) / 8 * 8;
+  const int64_t per = (cols + blocks - 1) / blocks;
   const dim3 grid((uint32_t)(blocks * tiles)), block(256);
-#define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * 256, blocks, base, out, U_out
+#define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, base, out, U_out
 #define EXPAND(KS_)                                               \
   do {                                                            \
     if (wide) launch(k_adapt_expand<KS_, 2>, EXPAND_ARGS);        \
