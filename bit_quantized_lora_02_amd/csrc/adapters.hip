@@ -569,9 +569,11 @@ __global__ __launch_bounds__(256, 4) void k_adapt_expand(AdaptRows a, const floa
 }
 
 // ---------------------------------------------------------------------- grads
-// One piece of an adapter's tokens, 256 columns of the long operand (64 per wave).  Steps of 64 tokens: their rows go to
-// LDS as they are and are read back transposed (ds_read_b64_tr_b16: lane i of 16 gets element i % 4 of the 8 bytes that
-// lanes 4 m + i / 4 address, m = 0 .. 3), the rank-wide operand likewise in two bf16 parts.
+// One piece of an adapter's tokens, CW columns of the long operand.  Each of four waves takes 32 tokens in turn: their
+// rows go to its own part of LDS as they are and are read back transposed (ds_read_b64_tr_b16: lane i of 16 gets element
+// i % 4 of the 8 bytes that lanes 4 m + i / 4 address, m = 0 .. 3), the rank-wide operand likewise in two bf16 parts; the
+// next 32 tokens' rows are on their way meanwhile, and there are no barriers.  At the end the waves' sums are added in LDS
+// ((0 + 2) + (1 + 3)).
 __device__ __forceinline__ u32x4_t turned(const bf16_t *base, int ld, int row, int col) {
   const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(base + row * ld + col));
   const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(base + (row + 4) * ld + col));
@@ -579,120 +581,156 @@ __device__ __forceinline__ u32x4_t turned(const bf16_t *base, int ld, int row, i
   return u32x4_t{l2.x, l2.y, h2.x, h2.y};
 }
 
-constexpr int kGradCols = 256, kGradLd = kGradCols + 16;
+// Columns per workgroup: the sums, CW x rank, are the larger part of the registers.
+constexpr int grad_cols(int rt) { return rt <= 2 ? 128 : 64; }
+template <int RT>
+struct GradShape {
+  static constexpr int CW = grad_cols(RT), LX = CW + 16, LV = RT * 16 + (RT > 1 ? 16 : 0);
+  static constexpr int kOwn = 32 * (LX + 2 * LV) * 2;                                // bytes of a wave
+  static constexpr int LD_A = CW + 4, LD_B = RT * 16 + 4;                            // rows of the sums of dA, dB
+  static constexpr int kSums = (RT * 16 * LD_A > CW * LD_B ? RT * 16 * LD_A : CW * LD_B) * 4;  // bytes, of one wave
+  static constexpr int kAll = 4 * kOwn > 2 * kSums ? 4 * kOwn : 2 * kSums;
+};
+
 // BY_J: the output is [n][r] (dB), else [r][n] (dA).
 template <int RT, bool BY_J>
 __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile, int rank, const float *__restrict__ V,
-                                           int ranges, float scale, const bf16_t *__restrict__ X, int64_t N, int64_t c0,
-                                           float *__restrict__ part, bf16_t *__restrict__ grad, bf16_t *s_x, bf16_t *s_hi,
-                                           bf16_t *s_lo) {
-  constexpr int LV = RT * 16 + (RT > 1 ? 16 : 0);
+                                           float scale, const bf16_t *__restrict__ X, int64_t N, int64_t c0,
+                                           float *__restrict__ part, bf16_t *__restrict__ grad, char *shared) {
+  using S = GradShape<RT>;
+  constexpr int CW = S::CW, LX = S::LX, LV = S::LV, XL = CW / 16, PT = CW / 16;  // XL: 16-byte loads of X per lane
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l = lane & 15;
-  f32x4_t acc[4][RT];
+  bf16_t *const s_x = reinterpret_cast<bf16_t *>(shared + wave * S::kOwn), *const s_hi = s_x + 32 * LX,
+                *const s_lo = s_hi + 32 * LV;
+  f32x4_t acc[PT][RT];
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
+  for (int p = 0; p < PT; ++p)
 #pragma unroll
     for (int j = 0; j < RT; ++j) acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int t0 = 0; t0 < tile.n; t0 += 64) {
-    u32x4_t x[8];
+  constexpr int XC = CW / 8;  // 16-byte chunks of a row of X
+  const int xrow = lane / XC, xcol = lane % XC * 8;
+  const int64_t col = c0 + xcol < N ? c0 + xcol : N - 8;  // (behind the row's end: any, whose products are not stored)
+  auto tokens_of = [&](int t) {  // lane i: the token at place t + i % 32, the last one behind the end
+    const int p = t + (lane & 31);
+    return a.order[tile.p0 + (p < tile.n ? p : tile.n - 1)];
+  };
+  u32x4_t x[XL];
+  float4 v[RT][2];
+  auto load = [&](int tokens) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = (tid >> 5) + 8 * i, col = (tid & 31) * 8;
-      x[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (t0 + row < tile.n && c0 + col < N) x[i] = load16(X + (int64_t)a.order[tile.p0 + t0 + row] * N + c0 + col);
+    for (int i = 0; i < XL; ++i) {
+      const int64_t t = __builtin_amdgcn_ds_bpermute((xrow + i * (64 / XC)) * 4, tokens);
+      x[i] = load16(X + t * N + col);
     }
-    if (t0) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<u32x4_t *>(s_x + ((tid >> 5) + 8 * i) * kGradLd + (tid & 31) * 8) = x[i];
-    for (int e = tid; e < 64 * RT * 2; e += 256) {
-      const int row = e / (RT * 2), j0 = e % (RT * 2) * 8;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (t0 + row < tile.n) load_u(a, V, ranges, a.order[tile.p0 + t0 + row], j0, rank, v);
+    for (int i = 0; i < RT; ++i) {
+      const int e = lane + 64 * i, row = e / (RT * 2), j0 = e % (RT * 2) * 8;
+      const int64_t t = __builtin_amdgcn_ds_bpermute(row * 4, tokens);
+      const float4 *from = reinterpret_cast<const float4 *>(V + t * a.r + (j0 < a.r ? j0 : 0));
+      v[i][0] = from[0];
+      v[i][1] = from[1];
+    }
+  };
+  int tokens = 0;
+  if (wave * 32 < tile.n) {
+    load(tokens_of(wave * 32));
+    tokens = tokens_of(wave * 32 + 128);
+  }
+  for (int t0 = wave * 32; t0 < tile.n; t0 += 128) {
+    const int left = tile.n - t0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= scale;
+    for (int i = 0; i < XL; ++i) {
+      const int row = xrow + i * (64 / XC);
+      *reinterpret_cast<u32x4_t *>(s_x + row * LX + xcol) = row < left ? x[i] : u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int e = lane + 64 * i, row = e / (RT * 2), j0 = e % (RT * 2) * 8;
+      const float4 p = v[i][0], q = v[i][1];
+      float u[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = row < left && j0 + k < rank ? u[k] * scale : 0.f;
       u32x4_t hi, lo;
-      split8(v, &hi, &lo);
+      split8(u, &hi, &lo);
       *reinterpret_cast<u32x4_t *>(s_hi + row * LV + j0) = hi;
       *reinterpret_cast<u32x4_t *>(s_lo + row * LV + j0) = lo;
     }
-    __syncthreads();
+    if (left > 128) {
+      load(tokens);
+      tokens = tokens_of(t0 + 256);
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int row = 8 * g + (l >> 2), at = 4 * (l & 3);
+    u32x4_t xv[PT];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int row = k * 32 + 8 * g + (l >> 2);
-      u32x4_t xv[4];
+    for (int p = 0; p < PT; ++p) xv[p] = turned(s_x, LX, row, 16 * p + at);
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        xv[p] = turned(s_x, kGradLd, row, wave * 64 + (BY_J ? 16 * p + 4 * (l & 3) : 16 * (l & 3) + 4 * p));
+    for (int j = 0; j < RT; ++j) {
+      const u32x4_t hi = turned(s_hi, LV, row, 16 * j + at), lo = turned(s_lo, LV, row, 16 * j + at);
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const u32x4_t hi = turned(s_hi, LV, row, j * 16 + 4 * (l & 3)), lo = turned(s_lo, LV, row, j * 16 + 4 * (l & 3));
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          if (BY_J) {
-            acc[p][j] = mfma16(hi, xv[p], acc[p][j]);
-            acc[p][j] = mfma16(lo, xv[p], acc[p][j]);
-          } else {
-            acc[p][j] = mfma16(xv[p], hi, acc[p][j]);
-            acc[p][j] = mfma16(xv[p], lo, acc[p][j]);
-          }
+      for (int p = 0; p < PT; ++p) {
+        if (BY_J) {
+          acc[p][j] = mfma16(hi, xv[p], acc[p][j]);
+          acc[p][j] = mfma16(lo, xv[p], acc[p][j]);
+        } else {
+          acc[p][j] = mfma16(xv[p], hi, acc[p][j]);
+          acc[p][j] = mfma16(xv[p], lo, acc[p][j]);
         }
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
-  const int64_t n0 = c0 + wave * 64, size = (int64_t)a.r * N;
-  if (BY_J) {  // lane: column 16 p + l, ranks 16 j + 4 g .. + 3
+  // the sums of two waves at a time, in the output's layout: [rank][column] or [column][rank]
+  constexpr int LD = BY_J ? S::LD_B : S::LD_A;
+  float *const s_sum = reinterpret_cast<float *>(shared + (wave & 1) * S::kSums);
+  auto each = [&](auto &&f) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
+    for (int p = 0; p < PT; ++p)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int64_t n = n0 + 16 * p + l;
-        const int j0 = j * 16 + 4 * g;
-        if (n >= N || j0 >= a.r) continue;
-        const f32x4_t v = acc[p][j];
-        if (tile.slot >= 0)
-          *reinterpret_cast<f32x4_t *>(part + tile.slot * size + n * a.r + j0) = v;
-        else
-          *reinterpret_cast<u32x2_t *>(grad + tile.group * size + n * a.r + j0) =
-              u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-      }
-  } else {  // lane: rank 16 j + l, columns 16 g + 4 p .. + 3
-#pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      const int j0 = j * 16 + l;
-      if (j0 >= a.r) continue;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t n = n0 + 16 * g + 8 * h;
-        if (n >= N) continue;
-        const f32x4_t v = acc[2 * h][j], w = acc[2 * h + 1][j];
-        if (tile.slot >= 0) {
-          f32x4_t *to = reinterpret_cast<f32x4_t *>(part + tile.slot * size + j0 * N + n);
-          to[0] = v;
-          to[1] = w;
-        } else {
-          store16(grad + tile.group * size + j0 * N + n, u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                                 pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3])});
-        }
-      }
+      for (int j = 0; j < RT; ++j)
+        f(acc[p][j], reinterpret_cast<f32x4_t *>(BY_J ? s_sum + (16 * p + l) * LD + 16 * j + 4 * g
+                                                      : s_sum + (16 * j + l) * LD + 16 * p + 4 * g));
+  };
+  __syncthreads();
+  if (wave >= 2) each([](f32x4_t &v_, f32x4_t *at) { *at = v_; });
+  __syncthreads();
+  if (wave < 2) each([](f32x4_t &v_, f32x4_t *at) { *at = v_ + *at; });
+  __syncthreads();
+  const int64_t size = (int64_t)a.r * N;
+  constexpr int ROW = BY_J ? RT * 16 : CW, ROWS = BY_J ? CW : RT * 16;
+  for (int e = tid; e < ROWS * (ROW / 8); e += 256) {
+    const int row = e / (ROW / 8), c = e % (ROW / 8) * 8;
+    const int64_t n = c0 + (BY_J ? row : c);
+    const int j = BY_J ? c : row;
+    if (n >= N || j >= a.r) continue;
+    const f32x4_t *p = reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(shared) + row * LD + c);
+    const f32x4_t *q = reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(shared + S::kSums) + row * LD + c);
+    const f32x4_t v0 = p[0] + q[0], v1 = p[1] + q[1];
+    const int64_t to = BY_J ? n * a.r + j : j * N + n;
+    if (tile.slot >= 0) {
+      f32x4_t *out = reinterpret_cast<f32x4_t *>(part + tile.slot * size + to);
+      out[0] = v0;
+      out[1] = v1;
+    } else {
+      store16(grad + tile.group * size + to, u32x4_t{pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v0[2], v0[3]),
+                                                     pack_bf16x2(v1[0], v1[1]), pack_bf16x2(v1[2], v1[3])});
     }
   }
 }
 
 template <int RT>
 __global__ __launch_bounds__(256) void k_adapt_grads(AdaptRows a, AdaptGrads g, int piece, int blocks_a, int blocks) {
-  constexpr int LV = RT * 16 + (RT > 1 ? 16 : 0);
-  __shared__ __attribute__((aligned(16))) bf16_t s_x[64 * kGradLd], s_hi[64 * LV], s_lo[64 * LV];
+  constexpr int CW = GradShape<RT>::CW;
+  __shared__ __attribute__((aligned(128))) char shared[GradShape<RT>::kAll];
   const int id = blockIdx.x / blocks, block = blockIdx.x - id * blocks;
   Tile tile;
   if (!find_tile(a, piece, id, &tile) || tile.group >= a.n_pool) return;
   const int rank = rank_of(a, tile.group);
   if (block < blocks_a)
-    grad_piece<RT, false>(a, tile, rank, g.dU, g.dU_ranges, 1.f, g.X, g.n_in, (int64_t)block * kGradCols, g.part_a, g.dA,
-                          s_x, s_hi, s_lo);
+    grad_piece<RT, false>(a, tile, rank, g.dU, 1.f, g.X, g.n_in, (int64_t)block * CW, g.part_a, g.dA, shared);
   else
-    grad_piece<RT, true>(a, tile, rank, g.U, g.U_ranges, a.scale[tile.group], g.dY, g.n_out,
-                         (int64_t)(block - blocks_a) * kGradCols, g.part_b, g.dB, s_x, s_hi, s_lo);
+    grad_piece<RT, true>(a, tile, rank, g.U, a.scale[tile.group], g.dY, g.n_out, (int64_t)(block - blocks_a) * CW, g.part_b,
+                         g.dB, shared);
 }
 
 // A group's gradient from the sums of its pieces, in order, 8 values per thread; zeros for a group without tokens.  What
@@ -779,21 +817,26 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
   return hipGetLastError();
 }
 
-int adapt_piece(int64_t T, int64_t n_in, int64_t n_out) {
-  const int64_t blocks = (n_in + kGradCols - 1) / kGradCols + (n_out + kGradCols - 1) / kGradCols;
+namespace {
+int rank_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
+}  // namespace
+
+int adapt_piece(int64_t T, int64_t n_in, int64_t n_out, int r) {
+  const int cols = grad_cols(rank_tiles(r));
+  const int64_t blocks = (n_in + cols - 1) / cols + (n_out + cols - 1) / cols;
   int piece = 1024;
-  while (piece > 64 && T / piece * blocks < 512) piece /= 2;
+  while (piece > 128 && T / piece * blocks < 512) piece /= 2;
   return piece;
 }
 
 hipError_t launch_adapt_grads(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s) {
-  const int ba = g.dA ? (int)((g.n_in + kGradCols - 1) / kGradCols) : 0;
-  const int bb = g.dB ? (int)((g.n_out + kGradCols - 1) / kGradCols) : 0;
+  const int rt = rank_tiles(a.r), cols = grad_cols(rt);
+  const int64_t ba = g.dA ? (g.n_in + cols - 1) / cols : 0, bb = g.dB ? (g.n_out + cols - 1) / cols : 0;
   const dim3 grid((uint32_t)((ba + bb) * most_tiles(a, piece))), block(256);
-#define GRADS(RT_) launch(k_adapt_grads<RT_>, grid, block, 0, s, a, g, piece, ba, ba + bb)
-  if (a.r <= 16) GRADS(1);
-  else if (a.r <= 32) GRADS(2);
-  else if (a.r <= 64) GRADS(4);
+#define GRADS(RT_) launch(k_adapt_grads<RT_>, grid, block, 0, s, a, g, piece, (int)ba, (int)(ba + bb))
+  if (rt == 1) GRADS(1);
+  else if (rt == 2) GRADS(2);
+  else if (rt == 4) GRADS(4);
   else GRADS(8);
 #undef GRADS
   return hipGetLastError();

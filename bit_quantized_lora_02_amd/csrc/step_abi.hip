@@ -92,7 +92,7 @@ int check_adapters(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32
 
 struct AdaptPlan {
   int ranges_u = 1, ranges_du = 1, piece = 0;
-  size_t order = 0, start = 0, u = 0, du = 0, at = 0, bt = 0, part_a = 0, part_b = 0, total = 0;
+  size_t order = 0, start = 0, u = 0, du = 0, du_sum = 0, at = 0, bt = 0, part_a = 0, part_b = 0, total = 0;
 };
 
 AdaptPlan adapt_plan(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32_t r, bool backward) {
@@ -105,9 +105,10 @@ AdaptPlan adapt_plan(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int
   if (backward) {
     p.ranges_du = adapt_ranges(T, n_pool, n_out);
     p.du = w.take((size_t)p.ranges_du * T * r * 4);
+    p.du_sum = p.ranges_du > 1 ? w.take((size_t)T * r * 4) : p.du;
     p.at = w.take((size_t)n_pool * r * n_in * 2);
     p.bt = w.take((size_t)n_pool * r * n_out * 2);
-    p.piece = adapt_piece(T, n_in, n_out);
+    p.piece = adapt_piece(T, n_in, n_out, r);
     const size_t slots = (size_t)adapt_slots(T, p.piece);
     p.part_a = w.take(slots * r * n_in * 4);
     p.part_b = w.take(slots * r * n_out * 4);
@@ -225,19 +226,21 @@ int qlora_adapters_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, int
   g.dB = dB;
   g.U = U;
   if (T > 0) {
+    // (the gradients of the pools take u and du whole: ranges of du are added where dX is formed)
     if (dB && !U) {
       float *u = (float *)(w + p.u);
-      LAUNCH("adapters_shrink", launch_adapt_shrink(a, X, n_in, A_pool, false, p.ranges_u, u, s));
+      LAUNCH("adapters_shrink", launch_adapt_shrink(a, X, n_in, A_pool, false, 1, u, s));
       g.U = u;
-      g.U_ranges = p.ranges_u;
     }
     if (dx || dA) {
-      float *du = (float *)(w + p.du);
-      LAUNCH("adapters_shrink", launch_adapt_shrink(a, dY, n_out, tb.to, true, p.ranges_du, du, s));
-      g.dU = du;
-      g.dU_ranges = p.ranges_du;
+      float *du = (float *)(w + p.du), *sum = (float *)(w + p.du_sum);
+      const int ranges = dx ? p.ranges_du : 1;
+      LAUNCH("adapters_shrink", launch_adapt_shrink(a, dY, n_out, tb.to, true, ranges, du, s));
+      if (dx)
+        LAUNCH("adapters_expand", launch_adapt_expand(a, du, ranges, ta.to, n_in, false, base, dX,
+                                                      dA && ranges > 1 ? sum : nullptr, s));
+      g.dU = ranges > 1 ? sum : du;
     }
-    if (dx) LAUNCH("adapters_expand", launch_adapt_expand(a, g.dU, p.ranges_du, ta.to, n_in, false, base, dX, nullptr, s));
     if (dA || dB) LAUNCH("adapters_grads", launch_adapt_grads(a, g, p.piece, s));
   }
   if (dA || dB) LAUNCH("adapters_reduce", launch_adapt_reduce(a, g, p.piece, s));
