@@ -446,7 +446,7 @@ __device__ __forceinline__ void load_u(const AdaptRows &a, const float *__restri
 // a copy alone reached 3.9 to 4.9 TB/s, in such pieces 5.8.
 constexpr int kExpandCols = 128;
 template <int KS, int MT>
-__global__ __launch_bounds__(256, 4) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
+__global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 3) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
                                                          const bf16_t *__restrict__ Q, int64_t N, bool scaled, int64_t per,
                                                          int blocks, const bf16_t *base, bf16_t *out,
                                                          float *__restrict__ U_out) {
@@ -471,6 +471,31 @@ __global__ __launch_bounds__(256, 4) void k_adapt_expand(AdaptRows a, const floa
 #pragma unroll
     for (int m = 0; m < MT; ++m) s_token[m * 16 + l] = token[m];
   __syncthreads();
+  const int64_t first = block * per, end = first + per < N ? first + per : N;
+  // rows as they lie in memory: a thread's 8 columns of every 16th token; its chunks of the wave's 32 rows of Q.  The first
+  // step's are on their way before u is, and each next step's before the present one is stored.
+  const int row0 = tid >> 4, col0 = (tid & 15) * 8;
+  int64_t at[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) at[i] = (int64_t)s_token[row0 + 16 * i] * N + col0;
+  const char *const q = (const char *)(Q + (int64_t)(rank ? tile.group : 0) * N * a.r);
+  char *const own = s_q[wave];
+  u32x4_t bv[MT], qv[CP / 2];
+  auto load = [&](int64_t n0) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      bv[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (base && row0 + 16 * i < tile.n && n0 + col0 < end) bv[i] = load_once<MT == 2>(base + at[i] + n0);
+    }
+    if (rank)
+#pragma unroll
+      for (int i = 0; i < CP / 2; ++i) {  // (behind the last row: any row, whose products are not stored)
+        const int r = i * (64 / CP) + lane / CP, c = lane % CP;
+        const int64_t n = n0 + wave * 32 + r, row = n < N ? n : N - 1;
+        qv[i] = *reinterpret_cast<const u32x4_t *>(q + ((uint32_t)row * (uint32_t)a.r + (c * 8 < a.r ? c * 8 : 0)) * 2u);
+      }
+  };
+  load(first);
   const float scale = scaled && tile.group < a.n_pool ? a.scale[tile.group] : 1.f;
   // u of the tile's tokens: the ranges' sums, to U_out, and times the scale in two parts to LDS
   for (int e = tid; e < TOKENS * CP; e += 256) {
@@ -504,32 +529,19 @@ __global__ __launch_bounds__(256, 4) void k_adapt_expand(AdaptRows a, const floa
       }
     }
   __syncthreads();
-  const int64_t first = block * per, end = first + per < N ? first + per : N;
-  // rows as they lie in memory: a thread's 8 columns of every 16th token; its chunks of the wave's 32 rows of Q
-  const int row0 = tid >> 4, col0 = (tid & 15) * 8;
-  int64_t at[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) at[i] = (int64_t)s_token[row0 + 16 * i] * N + col0;
-  const char *const q = (const char *)(Q + (int64_t)(rank ? tile.group : 0) * N * a.r);
-  char *const own = s_q[wave];
   const bool full = rank == CP * 8;
   for (int64_t n0 = first; n0 < end; n0 += kExpandCols) {
-    u32x4_t bv[MT];
+    u32x4_t now[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      bv[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (base && row0 + 16 * i < tile.n && n0 + col0 < end) bv[i] = load_once<MT == 2>(base + at[i] + n0);
-    }
-    if (rank) {
-      u32x4_t qv[CP / 2];
+    for (int i = 0; i < MT; ++i) now[i] = bv[i];
+    if (rank)
 #pragma unroll
-      for (int i = 0; i < CP / 2; ++i) {  // (behind the last row: any row, whose products are not stored)
+      for (int i = 0; i < CP / 2; ++i) {
         const int r = i * (64 / CP) + lane / CP, c = lane % CP;
-        const int64_t n = n0 + wave * 32 + r, row = n < N ? n : N - 1;
-        qv[i] = *reinterpret_cast<const u32x4_t *>(q + ((uint32_t)row * (uint32_t)a.r + (c * 8 < a.r ? c * 8 : 0)) * 2u);
-        if (!full) qv[i] = below_rank(qv[i], rank - c * 8);
-        *reinterpret_cast<u32x4_t *>(own + swizzled(r, c)) = qv[i];
+        *reinterpret_cast<u32x4_t *>(own + swizzled(r, c)) = full ? qv[i] : below_rank(qv[i], rank - c * 8);
       }
+    if (n0 + kExpandCols < end) load(n0 + kExpandCols);
+    if (rank) {
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -555,14 +567,14 @@ __global__ __launch_bounds__(256, 4) void k_adapt_expand(AdaptRows a, const floa
       if (row0 + 16 * i < tile.n && n0 + col0 < end) {
         if (rank) {
           float y[8];
-          unpack8(bv[i], y);
+          unpack8(now[i], y);
           const f32x4_t *d = reinterpret_cast<const f32x4_t *>(&s_out[row0 + 16 * i][col0]);
           const f32x4_t d0 = d[0], d1 = d[1];
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] += d0[e], y[4 + e] += d1[e];
-          bv[i] = pack8(y);
+          now[i] = pack8(y);
         }
-        store_once<MT == 2>(out + at[i] + n0, bv[i]);
+        store_once<MT == 2>(out + at[i] + n0, now[i]);
       }
     if (rank) __syncthreads();
   }
@@ -798,9 +810,9 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
   const int64_t tiles = most_tiles(a, wide ? 32 : 16), cols = (N + kExpandCols - 1) / kExpandCols;
   // Column blocks: enough workgroups for the GPU, few enough that their lookups and u are shared by several steps; a
   // multiple of 8, so that a block's rows of Q stay in the L2 of one XCD (workgroups go round the eight).
-  int64_t blocks = (2048 + tiles - 1) / tiles;
-  blocks = cols <= 8 ? cols : blocks >= cols ? (cols + 7) / 8 * 8 : (blocks + 7) / 8 * 8;
-  const int64_t per = (cols + blocks - 1) / blocks;
+  const int64_t want = (2048 / tiles + 8) / 8 * 8, per = cols <= want ? 1 : (cols + want - 1) / want;
+  int64_t blocks = (cols + per - 1) / per;
+  if (blocks > 8) blocks = (blocks + 7) / 8 * 8;
   const dim3 grid((uint32_t)(blocks * tiles)), block(256);
 #define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, base, out, U_out
 #define EXPAND(KS_)                                               \
