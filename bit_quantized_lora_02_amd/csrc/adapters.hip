@@ -161,17 +161,6 @@ __device__ __forceinline__ u32x4_t below_rank(u32x4_t v, int left) {
   return v;
 }
 
-// Values that are used once (long ones): past the caches, which the adapters' rows need.
-template <bool ONCE>
-__device__ __forceinline__ u32x4_t load_once(const bf16_t *p) {
-  return ONCE ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(p)) : load16(p);
-}
-template <bool ONCE>
-__device__ __forceinline__ void store_once(bf16_t *p, const u32x4_t &v) {
-  if (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(p));
-  else store16(p, v);
-}
-
 // ----------------------------------------------------------------------- plan
 constexpr int kPlanWaves = 16;
 struct PlanShared {
@@ -448,7 +437,7 @@ constexpr int kExpandCols = 128;
 template <int KS, int MT>
 __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 3) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
                                                          const bf16_t *__restrict__ Q, int64_t N, bool scaled, int64_t per,
-                                                         int blocks, const bf16_t *base, bf16_t *out,
+                                                         int blocks, bool once, const bf16_t *base, bf16_t *out,
                                                          float *__restrict__ U_out) {
   constexpr int CP = KS ? KS * 4 : 2, KQ = KS ? KS : 1, TOKENS = 16 * MT;  // CP: 16-byte chunks of a row of the adapter
   constexpr int kRowsQ = 32 * CP * 16, kOut = TOKENS * (kExpandCols + 4) * 4, kParts = TOKENS * CP * 32;
@@ -485,7 +474,7 @@ __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 3) void k_adapt_expand(Adap
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       bv[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (base && row0 + 16 * i < tile.n && n0 + col0 < end) bv[i] = load_once<MT == 2>(base + at[i] + n0);
+      if (base && row0 + 16 * i < tile.n && n0 + col0 < end) bv[i] = once ? load16_once(base + at[i] + n0) : load16(base + at[i] + n0);
     }
     if (rank)
 #pragma unroll
@@ -574,7 +563,7 @@ __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 3) void k_adapt_expand(Adap
           for (int e = 0; e < 4; ++e) y[e] += d0[e], y[4 + e] += d1[e];
           now[i] = pack8(y);
         }
-        store_once<MT == 2>(out + at[i] + n0, now[i]);
+        store16_once(out + at[i] + n0, now[i]);
       }
     if (rank) __syncthreads();
   }
@@ -813,8 +802,11 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
   const int64_t want = (2048 / tiles + 8) / 8 * 8, per = cols <= want ? 1 : (cols + want - 1) / want;
   int64_t blocks = (cols + per - 1) / per;
   if (blocks > 8) blocks = (blocks + 7) / 8 * 8;
+  // A base that the caches cannot hold beside the rest goes past them (4096 x 14336, 117 MB: the call 79 us, else 84; of
+  // 25 MB, just written, 19 us of the kernel, else 14).
+  const bool once = a.T * N * 2 > (int64_t)64 << 20;
   const dim3 grid((uint32_t)(blocks * tiles)), block(256);
-#define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, base, out, U_out
+#define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, once, base, out, U_out
 #define EXPAND(KS_)                                               \
   do {                                                            \
     if (wide) launch(k_adapt_expand<KS_, 2>, EXPAND_ARGS);        \

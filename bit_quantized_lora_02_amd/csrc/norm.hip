@@ -105,70 +105,81 @@ __global__ __launch_bounds__(NT) void k_norm(const bf16_t *__restrict__ X, int64
   }
 }
 
+// Eight columns' sums of dw and db, rows 0 and 1 of `out`.
+__device__ __forceinline__ void store_sums(float *__restrict__ out, int64_t D, int64_t d, const float dw[8],
+                                           const float db[8]) {
+  float4 *pw = reinterpret_cast<float4 *>(out + d), *pb = reinterpret_cast<float4 *>(out + D + d);
+  pw[0] = make_float4(dw[0], dw[1], dw[2], dw[3]);
+  pw[1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
+  pb[0] = make_float4(db[0], db[1], db[2], db[3]);
+  pb[1] = make_float4(db[4], db[5], db[6], db[7]);
+}
+
 // A workgroup of 1024 threads in groups of NT, each with a row at a time.  The sums of dw and db stay in registers over
 // the workgroup's rows; then the groups add theirs in LDS, one after the other, and the workgroup's go to part[block].
+// (C = 4, the longest rows: the sums do not fit the registers beside a row and come from k_norm_columns; 1024 x 32768 so
+// 86 us in all, with spilled registers 191.)
 template <int NT, int C, bool F32>
-__global__ __launch_bounds__(1024) void k_norm_bwd(const bf16_t *__restrict__ X, const bf16_t *__restrict__ dY, int64_t T,
-                                                   int64_t D, const void *__restrict__ w, const float *__restrict__ mean,
-                                                   const float *__restrict__ rstd, bf16_t *__restrict__ dX,
-                                                   float *__restrict__ part) {
+__global__ __launch_bounds__(1024) void k_norm_bwd(const bf16_t *__restrict__ X, const bf16_t *dY, int64_t T, int64_t D,
+                                                   const void *__restrict__ w, const float *__restrict__ mean,
+                                                   const float *__restrict__ rstd, bf16_t *dX, float *__restrict__ part) {
   constexpr int G = 1024 / NT, WAVES = NT / 64;
+  constexpr bool SUMS = C <= 2;
   __shared__ float s_sum[2][G][2][WAVES];
   __shared__ __attribute__((aligned(16))) float s_part[G > 1 ? NT * C * 16 : 1];
-  const int g = threadIdx.x / NT, tid = threadIdx.x % NT, wave = tid >> 6;
+  const int g = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   bool in[C];
-  int64_t d[C];
-  float wv[C][8], dw[C][8], db[C][8];
+  uint32_t d[C];
+  float wv[C][8], dw[SUMS ? C : 1][8], db[SUMS ? C : 1][8];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    d[c] = ((int64_t)c * NT + tid) * 8;
+    d[c] = (c * NT + tid) * 8;
     in[c] = d[c] < D;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wv[c][i] = dw[c][i] = db[c][i] = 0.f;
+    for (int i = 0; i < 8; ++i) wv[c][i] = dw[SUMS ? c : 0][i] = db[SUMS ? c : 0][i] = 0.f;
     if (in[c]) load_w<F32>(w, d[c], wv[c]);
   }
   const float n = (float)D;
-  u32x4_t nx[C], ng[C];
-  float nm, nr;
-  auto load = [&](int64_t t) {
+  struct Row {
+    u32x4_t x[C], g[C];
+    float m, r;
+  };
+  auto load = [&](Row &to, int64_t t) {
     const bool ok = t < T;
-    nm = ok ? mean[t] : 0.f;
-    nr = ok ? rstd[t] : 0.f;
+    to.m = ok ? mean[t] : 0.f;
+    to.r = ok ? rstd[t] : 0.f;
+    const bf16_t *const x = X + t * D, *const y = dY + t * D;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      nx[c] = ng[c] = u32x4_t{0u, 0u, 0u, 0u};
+      to.x[c] = to.g[c] = u32x4_t{0u, 0u, 0u, 0u};
       if (ok && in[c]) {
-        nx[c] = load16(X + t * D + d[c]);
-        ng[c] = load16(dY + t * D + d[c]);
+        to.x[c] = load16(x + d[c]);
+        to.g[c] = load16(y + d[c]);
       }
     }
   };
   const int64_t first = (int64_t)blockIdx.x * G, step = (int64_t)gridDim.x * G;
-  load(first + g);
-  int turn = 0;
-  for (int64_t t0 = first; t0 < T; t0 += step, turn ^= 1) {
-    const int64_t t = t0 + g;  // (a group behind the last row works on zeros: every thread meets the barriers)
-    const float m = nm, r = nr;
-    u32x4_t rx[C], rg[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) rx[c] = nx[c], rg[c] = ng[c];
-    load(t + step);
+  // row t of this group (behind the last one a row of zeros: every thread meets the barriers)
+  auto work = [&](const Row &row, int64_t t, int turn) {
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float x[8], y[8];
-      unpack8(rx[c], x);
-      unpack8(rg[c], y);
+      unpack8(row.x[c], x);
+      unpack8(row.g[c], y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float xh = (x[i] - m) * r, gd = y[i] * wv[c][i];
-        dw[c][i] = fmaf(y[i], xh, dw[c][i]);
-        db[c][i] += y[i];
+        const float xh = (x[i] - row.m) * row.r, gd = y[i] * wv[c][i];
+        if (SUMS) {
+          dw[c][i] = fmaf(y[i], xh, dw[c][i]);
+          db[c][i] += y[i];
+        }
         a += gd;
         b = fmaf(gd, xh, b);
       }
     }
-    if (!dX) continue;
+    if (!dX) return;
     a = wave_sum(a);
     b = wave_sum(b);
     if (NT > 64) {
@@ -178,21 +189,42 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const bf16_t *__restrict__ X,
 #pragma unroll
       for (int i = 0; i < WAVES; ++i) a += s_sum[turn][g][0][i], b += s_sum[turn][g][1][i];
     }
+    if (t >= T) return;
     a /= n;
     b /= n;
+    bf16_t *const out = dX + t * D;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (t < T && in[c]) {
+      if (in[c]) {
         float x[8], y[8];
-        unpack8(rx[c], x);
-        unpack8(rg[c], y);
+        unpack8(row.x[c], x);
+        unpack8(row.g[c], y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float xh = (x[i] - m) * r;
-          y[i] = (fmaf(y[i], wv[c][i], -a) - xh * b) * r;
+          const float xh = (x[i] - row.m) * row.r;
+          y[i] = (fmaf(y[i], wv[c][i], -a) - xh * b) * row.r;
         }
-        store16(dX + t * D + d[c], pack8(y));
+        store16(out + d[c], pack8(y));
       }
+  };
+  Row even;
+  if constexpr (SUMS) {
+    Row odd;
+    load(even, first + g);
+    for (int64_t t0 = first; t0 < T; t0 += 2 * step) {
+      load(odd, t0 + step + g);
+      work(even, t0 + g, 0);
+      if (t0 + step >= T) break;
+      load(even, t0 + 2 * step + g);
+      work(odd, t0 + step + g, 1);
+    }
+  } else {  // (one row in the registers)
+    int turn = 0;
+    for (int64_t t0 = first; t0 < T; t0 += step, turn ^= 1) {
+      load(even, t0 + g);
+      work(even, t0 + g, turn);
+    }
+    return;
   }
   if (!part) return;
   if (G > 1) {
@@ -214,14 +246,32 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const bf16_t *__restrict__ X,
   }
   float *out = part + (int64_t)blockIdx.x * 2 * D;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    if (in[c]) {
-      float4 *pw = reinterpret_cast<float4 *>(out + d[c]), *pb = reinterpret_cast<float4 *>(out + D + d[c]);
-      pw[0] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
-      pw[1] = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
-      pb[0] = make_float4(db[c][0], db[c][1], db[c][2], db[c][3]);
-      pb[1] = make_float4(db[c][4], db[c][5], db[c][6], db[c][7]);
+  for (int c = 0; c < (SUMS ? C : 0); ++c)
+    if (in[c]) store_sums(out, D, d[c], dw[c], db[c]);
+}
+
+// The sums alone: 2048 columns, every gridDim.y-th row.
+__global__ __launch_bounds__(256) void k_norm_columns(const bf16_t *__restrict__ X, const bf16_t *__restrict__ dY, int64_t T,
+                                                      int64_t D, const float *__restrict__ mean,
+                                                      const float *__restrict__ rstd, float *__restrict__ part) {
+  const int64_t d = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (d >= D) return;
+  float dw[8], db[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.f;
+#pragma unroll 4
+  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+    const float m = mean[t], r = rstd[t];
+    float x[8], y[8];
+    unpack8(load16(X + t * D + d), x);
+    unpack8(load16(dY + t * D + d), y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dw[i] = fmaf(y[i], (x[i] - m) * r, dw[i]);
+      db[i] += y[i];
     }
+  }
+  store_sums(part + (int64_t)blockIdx.y * 2 * D, D, d, dw, db);
 }
 
 // dw and db from the workgroups' sums: 64 columns per workgroup, each of 16 waves adds a sixteenth of the sums, then
@@ -301,9 +351,20 @@ hipError_t launch_norm_bwd(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t
   if (nt == 64) NORM_NT(64);
   else if (nt == 256) NORM_NT(256);
   else if (c <= 2) NORM_NT(1024);
-  else NORM_CASE(1024, 4, k_norm_bwd, NORM_ARGS);
+  else {
+    NORM_CASE(1024, 4, k_norm_bwd, NORM_ARGS);
+  }
 #undef NORM_NT
 #undef NORM_ARGS
+  return hipGetLastError();
+}
+
+bool norm_bwd_columns(int64_t D) { return D > 16384; }
+
+hipError_t launch_norm_columns(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t D, const float *mean, const float *rstd,
+                               float *part, hipStream_t s) {
+  launch(k_norm_columns, dim3((uint32_t)((D + 2047) / 2048), (uint32_t)norm_bwd_groups(T, D)), dim3(256), 0, s, X, dY, T, D,
+         mean, rstd, part);
   return hipGetLastError();
 }
 

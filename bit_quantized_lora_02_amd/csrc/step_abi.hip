@@ -341,7 +341,9 @@ int qlora_layer_norm_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, i
   const bool f32 = weight_type == QLORA_WEIGHT_F32;
   float *part = sums ? (float *)ws : nullptr;
   // (without rows: the sums are zero)
-  LAUNCH("layer_norm_bwd", launch_norm_bwd(X, dY, T, n_in, weight, f32, mean, rstd, dX, part, s));
+  const bool columns = norm_bwd_columns(n_in);
+  if (sums && columns) LAUNCH("layer_norm_columns", launch_norm_columns(X, dY, T, n_in, mean, rstd, part, s));
+  if (dX || !columns) LAUNCH("layer_norm_bwd", launch_norm_bwd(X, dY, T, n_in, weight, f32, mean, rstd, dX, part, s));
   if (sums) LAUNCH("layer_norm_reduce", launch_norm_reduce(part, groups, n_in, f32, dweight, dbias, s));
   return QLORA_OK;
 }

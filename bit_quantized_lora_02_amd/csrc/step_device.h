@@ -34,5 +34,12 @@ __device__ __forceinline__ u32x4_t pack8(const float v[8]) {
 }
 __device__ __forceinline__ u32x4_t load16(const bf16_t *p) { return *reinterpret_cast<const u32x4_t *>(p); }
 __device__ __forceinline__ void store16(bf16_t *p, const u32x4_t &v) { *reinterpret_cast<u32x4_t *>(p) = v; }
+// The same past the caches, where a long operand or output is used once.
+__device__ __forceinline__ u32x4_t load16_once(const bf16_t *p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(p));
+}
+__device__ __forceinline__ void store16_once(bf16_t *p, const u32x4_t &v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(p));
+}
 
 }  // namespace qlora
