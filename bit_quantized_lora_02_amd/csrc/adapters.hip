@@ -434,10 +434,11 @@ __device__ __forceinline__ void load_u(const AdaptRows &a, const float *__restri
 // and output are read and written 256 bytes of a row at a time: from the MFMA's layout (64 bytes of 16 tokens each)
 // a copy alone reached 3.9 to 4.9 TB/s, in such pieces 5.8.
 constexpr int kExpandCols = 128;
-template <int KS, int MT>
+// ONCE: the base goes past the caches.
+template <int KS, int MT, bool ONCE>
 __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 3) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
                                                          const bf16_t *__restrict__ Q, int64_t N, bool scaled, int64_t per,
-                                                         int blocks, bool once, const bf16_t *base, bf16_t *out,
+                                                         int blocks, const bf16_t *base, bf16_t *out,
                                                          float *__restrict__ U_out) {
   constexpr int CP = KS ? KS * 4 : 2, KQ = KS ? KS : 1, TOKENS = 16 * MT;  // CP: 16-byte chunks of a row of the adapter
   constexpr int kRowsQ = 32 * CP * 16, kOut = TOKENS * (kExpandCols + 4) * 4, kParts = TOKENS * CP * 32;
@@ -474,7 +475,7 @@ __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 3) void k_adapt_expand(Adap
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       bv[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (base && row0 + 16 * i < tile.n && n0 + col0 < end) bv[i] = once ? load16_once(base + at[i] + n0) : load16(base + at[i] + n0);
+      if (base && row0 + 16 * i < tile.n && n0 + col0 < end) bv[i] = ONCE ? load16_once(base + at[i] + n0) : load16(base + at[i] + n0);
     }
     if (rank)
 #pragma unroll
@@ -806,11 +807,12 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
   // 25 MB, just written, 19 us of the kernel, else 14).
   const bool once = a.T * N * 2 > (int64_t)64 << 20;
   const dim3 grid((uint32_t)(blocks * tiles)), block(256);
-#define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, once, base, out, U_out
-#define EXPAND(KS_)                                               \
-  do {                                                            \
-    if (wide) launch(k_adapt_expand<KS_, 2>, EXPAND_ARGS);        \
-    else launch(k_adapt_expand<KS_, 1>, EXPAND_ARGS);             \
+#define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, base, out, U_out
+#define EXPAND(KS_)                                                     \
+  do {                                                                  \
+    if (wide && once) launch(k_adapt_expand<KS_, 2, true>, EXPAND_ARGS);  \
+    else if (wide) launch(k_adapt_expand<KS_, 2, false>, EXPAND_ARGS);  \
+    else launch(k_adapt_expand<KS_, 1, false>, EXPAND_ARGS);            \
   } while (0)
   if (a.r <= 16) EXPAND(0);
   else if (a.r <= 32) EXPAND(1);
