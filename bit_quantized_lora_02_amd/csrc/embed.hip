@@ -38,69 +38,81 @@ __global__ __launch_bounds__(256) void k_embed(const int64_t *__restrict__ token
   }
 }
 
-// Ranks 64 positions of a chunk against the whole chunk: the rank of position i is the number of keys below its own plus
-// the number of equal ones before it.  16 waves count a sixteenth of the chunk each, the keys broadcast from LDS, two
-// instructions per pair (8192 positions: 67 million pairs over the whole GPU).
-constexpr int kRankWaves = 16;
+// Ranks 16 positions of a chunk against the whole chunk: the rank of position i is the number of keys below its own plus
+// the number of equal ones before it.  16 threads count for each position, a sixteenth of 2048 keys at a time, which all
+// read from LDS, two vector instructions per pair (8192 positions: 67 million pairs over the whole GPU, 6 us).
+constexpr int kRankItems = 16, kRankParts = 16, kRankKeys = 2048, kRankPart = kRankKeys / kRankParts;
 __device__ __forceinline__ void rank_chunk(const int64_t *__restrict__ tokens, int64_t T, int64_t V, int64_t block,
                                            int32_t *__restrict__ order, int32_t *__restrict__ key) {
-  __shared__ __attribute__((aligned(16))) uint32_t s_key[kOrderChunk];
-  __shared__ uint32_t s_rank[kRankWaves][64];
-  constexpr int64_t kBlocks = kOrderChunk / 64;
+  __shared__ __attribute__((aligned(16))) uint32_t s_key[kRankParts][kRankPart + 4];
+  __shared__ uint32_t s_rank[kRankParts][kRankItems];
+  constexpr int64_t kBlocks = kOrderChunk / kRankItems;
   const int64_t base = block / kBlocks * kOrderChunk;
   const int n = (int)(T - base < kOrderChunk ? T - base : kOrderChunk);
-  const int padded = (n + 63) & ~63;
-  for (int i = threadIdx.x; i < padded; i += 1024) {
-    uint32_t k = 0xffffffffu;  // behind the end: above every key
-    if (i < n) {
-      const int64_t v = tokens[base + i];
-      k = (uint64_t)v < (uint64_t)V ? (uint32_t)v : (uint32_t)V;
+  const int tid = threadIdx.x, item = tid % kRankItems, part = tid / kRankItems;
+  const int i0 = (int)(block % kBlocks) * kRankItems, i = i0 + item;
+  auto key_of = [&](int at, int64_t v) {  // (behind the end: above every key)
+    return at >= n ? 0xffffffffu : (uint64_t)v < (uint64_t)V ? (uint32_t)v : (uint32_t)V;
+  };
+  int64_t next[kRankKeys / 256];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int p = 0; p < kRankKeys / 256; ++p) {
+      const int at = j0 + p * 256 + tid;
+      next[p] = tokens[base + (at < n ? at : n - 1)];
     }
-    s_key[i] = k;
-  }
-  __syncthreads();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i0 = (int)(block % kBlocks) * 64, i = i0 + lane;
-  const uint32_t mine = s_key[i];
+  };
+  const int64_t token = tokens[base + (i < n ? i : n - 1)];
+  load(0);
+  const uint32_t mine = key_of(i, token);
   uint32_t rank = 0;
-  for (int j0 = wave * 64; j0 < padded; j0 += kRankWaves * 64) {
-    if (j0 == i0) {
-#pragma unroll 8
-      for (int j = 0; j < 64; ++j) {
-        const uint32_t k = s_key[j0 + j];
-        rank += (k < mine || (k == mine && j < lane)) ? 1u : 0u;
-      }
-    } else {
-      const uint32_t below = mine + (j0 < i0 ? 1u : 0u);  // (of lanes behind the end it may wrap: their rank is not used)
+  for (int j0 = 0; j0 < n; j0 += kRankKeys) {
+    if (j0) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 64; j += 4) {
-        const u32x4_t k = *reinterpret_cast<const u32x4_t *>(&s_key[j0 + j]);
+    for (int p = 0; p < kRankKeys / 256; ++p) 
+      s_key[(p * 256 + tid) / kRankPart][tid % kRankPart] = key_of(j0 + p * 256 + tid, next[p]);
+    if (j0 + kRankKeys < n) load(j0 + kRankKeys);
+    __syncthreads();
+    const int lo = j0 + part * kRankPart;
+#pragma unroll 1
+    for (int j = 0; j < kRankPart; j += kRankItems) {
+      const uint32_t *const at = &s_key[part][j];
+      if (lo + j == i0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rank += k[e] < below ? 1u : 0u;
+        for (int e = 0; e < kRankItems; ++e) rank += at[e] < mine + (e < item ? 1u : 0u) ? 1u : 0u;
+      } else {
+        const uint32_t below = mine + (lo + j < i0 ? 1u : 0u);
+#pragma unroll
+        for (int e = 0; e < kRankItems; e += 4) {
+          const u32x4_t k = *reinterpret_cast<const u32x4_t *>(at + e);
+          rank += (k[0] < below ? 1u : 0u) + (k[1] < below ? 1u : 0u) + (k[2] < below ? 1u : 0u) + (k[3] < below ? 1u : 0u);
+        }
       }
     }
   }
-  s_rank[wave][lane] = rank;
+  s_rank[part][item] = rank;
   __syncthreads();
-  if (wave == 0 && i < n) {
+  if (part == 0 && i < n) {
     uint32_t r = 0;
 #pragma unroll
-    for (int w = 0; w < kRankWaves; ++w) r += s_rank[w][lane];
+    for (int p = 0; p < kRankParts; ++p) r += s_rank[p][item];
     order[base + r] = (int32_t)(base + i);
     key[base + r] = (int32_t)mine;
   }
 }
+static_assert(kRankItems * kRankParts == 256 && 256 % kRankPart == 0 && kRankPart % kRankItems == 0, "layout of the keys");
 
-__global__ __launch_bounds__(1024) void k_embed_order(const int64_t *__restrict__ tokens, int64_t T, int64_t V,
-                                                      int32_t *__restrict__ order, int32_t *__restrict__ key, int64_t blocks,
-                                                      bf16_t *__restrict__ fill, int64_t fill_n) {
+// The rest of the workgroups fill: one store per thread, which reaches 6.8 TB/s (1.05 GB in 154 us; workgroups that stay
+// for several stores 4.4 to 6.2, nontemporal stores 4.4).
+__global__ __launch_bounds__(256) void k_embed_order(const int64_t *__restrict__ tokens, int64_t T, int64_t V,
+                                                     int32_t *__restrict__ order, int32_t *__restrict__ key, int64_t blocks,
+                                                     bf16_t *__restrict__ fill, int64_t fill_n) {
   if (blockIdx.x < blocks) {
     rank_chunk(tokens, T, V, blockIdx.x, order, key);
     return;
   }
-  const int64_t step = ((int64_t)gridDim.x - blocks) * 1024 * 8;
-  for (int64_t e = ((int64_t)(blockIdx.x - blocks) * 1024 + threadIdx.x) * 8; e < fill_n; e += step)
-    store16(fill + e, u32x4_t{0u, 0u, 0u, 0u});
+  const int64_t e = ((int64_t)(blockIdx.x - blocks) * 256 + threadIdx.x) * 8;
+  if (e < fill_n) store16(fill + e, u32x4_t{0u, 0u, 0u, 0u});
 }
 
 // First place in [0, n) whose key is not below k (UPPER: above k).
@@ -149,7 +161,9 @@ __device__ __forceinline__ void write_row(bf16_t *__restrict__ at, const float s
 }
 
 // One piece of the sorted list, 512 columns.  A row whose positions all lie in the piece is written; the binary32 sum of
-// one that began in an earlier piece goes to part[piece][0], of one that begins here and goes on to part[piece][1].
+// one that began in an earlier piece goes to part[piece][0], of one that begins here and goes on to part[piece][1].  Each
+// lane holds an entry of the list, so that the rows' loads wait for nothing else.
+constexpr int kPieceMost = 32;
 __global__ __launch_bounds__(256) void k_embed_sum(const int32_t *__restrict__ order, const int32_t *__restrict__ key,
                                                    int64_t T, int piece, const bf16_t *__restrict__ dY, int64_t V, int64_t D,
                                                    int64_t slices, int64_t jobs, float scale, bool add,
@@ -157,12 +171,21 @@ __global__ __launch_bounds__(256) void k_embed_sum(const int32_t *__restrict__ o
   constexpr int N = 8;  // rows in flight
   const int64_t job = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (job >= jobs) return;
-  const int64_t c = job / slices, d = (job - c * slices) * kWaveCols + (threadIdx.x & 63) * 8;
-  const int64_t p0 = c * piece, p1 = p0 + piece < T ? p0 + piece : T;
-  int cur = key[p0];
-  if (cur >= V) return;  // what names no row comes last
+  const int lane = threadIdx.x & 63;
+  const int64_t c = job / slices, d = (job - c * slices) * kWaveCols + lane * 8;
+  const int64_t p0 = c * piece;
+  const int n = (int)(T - p0 < piece ? T - p0 : piece);
+  // lane i: the key at place p0 - 1 + i, up to the one behind the piece (none: -1), and the position at p0 + i
+  const int64_t p = p0 - 1 + lane;
+  const int k = lane <= n + 1 && p >= 0 && p < T ? key[p] : -1;
+  const int row = lane < n ? order[p0 + lane] : 0;
+  const int first = __builtin_amdgcn_readlane(k, 1);
+  if (first >= V) return;  // what names no row comes last
+  const int count = __popcll(__ballot(lane >= 1 && lane <= n && k < V));
   const bool in = d < D;
-  bool head = p0 > 0 && key[p0 - 1] == cur;
+  const bf16_t *const from = dY + (in ? d : 0);
+  bool head = __builtin_amdgcn_readlane(k, 0) == first;
+  int cur = first;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   auto flush = [&](bool goes_on) {
     if (!in) return;
@@ -174,33 +197,39 @@ __global__ __launch_bounds__(256) void k_embed_sum(const int32_t *__restrict__ o
       *reinterpret_cast<float4 *>(at + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
     }
   };
-  for (int64_t p = p0; p < p1; p += N) {
-    u32x4_t row[N];
-    int k[N];
+  u32x4_t now[N], next[N];
+  auto load = [&](u32x4_t(&to)[N], int e0) {  // (behind the last entry: its row again, not added)
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      to[e] = load16(from + (int64_t)__builtin_amdgcn_readlane(row, e0 + e < count ? e0 + e : count - 1) * D);
+  };
+  auto take = [&](const u32x4_t(&rows)[N], int e0) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      k[e] = p + e < p1 ? key[p + e] : (int)V;
-      row[e] = u32x4_t{0u, 0u, 0u, 0u};
-      if (k[e] < V && in) row[e] = load16(dY + (int64_t)order[p + e] * D + d);
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if (p + e >= p1) break;
-      if (k[e] != cur) {
+      if (e0 + e >= count) break;
+      const int at = __builtin_amdgcn_readlane(k, e0 + e + 1);
+      if (at != cur) {
         flush(false);
-        if (k[e] >= V) return;
-        cur = k[e];
+        cur = at;
         head = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = 0.f;
       }
       float x[8];
-      unpack8(row[e], x);
+      unpack8(rows[e], x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += x[i];
     }
+  };
+  load(now, 0);
+  for (int e0 = 0; e0 < count; e0 += 2 * N) {
+    if (e0 + N < count) load(next, e0 + N);
+    take(now, e0);
+    if (e0 + N >= count) break;
+    if (e0 + 2 * N < count) load(now, e0 + 2 * N);
+    take(next, e0 + N);
   }
-  flush(p1 < T && key[p1] == cur);
+  flush(count == n && __builtin_amdgcn_readlane(k, n + 1) == cur);
 }
 
 // The row that begins in a piece and goes on: its sums of the pieces, added in order (four waves a quarter of them each,
@@ -265,13 +294,13 @@ hipError_t launch_embed(const int64_t *tokens, int64_t T, const bf16_t *W, int64
   return hipGetLastError();
 }
 
-int embed_piece(int64_t T) { return T <= 2048 ? 8 : T <= 8192 ? 16 : 32; }
+int embed_piece(int64_t T) { return T <= 2048 ? 8 : T <= 8192 ? 16 : kPieceMost; }
 
 hipError_t launch_embed_order(const int64_t *tokens, int64_t T, int64_t V, const Order &o, bf16_t *fill, int64_t fill_n,
                               hipStream_t s) {
-  const int64_t blocks = (T + 63) / 64, fills = (fill_n + 8191) / 8192;
+  const int64_t blocks = (T + kRankItems - 1) / kRankItems, fills = (fill_n + 2047) / 2048;
   const bool merged = T > kOrderChunk;
-  launch(k_embed_order, dim3((uint32_t)(blocks + (fills < 2048 ? fills : 2048))), dim3(1024), 0, s, tokens, T, V,
+  launch(k_embed_order, dim3((uint32_t)(blocks + fills)), dim3(256), 0, s, tokens, T, V,
          merged ? o.order2 : o.order, merged ? o.key2 : o.key, blocks, fill, fill_n);
   return hipGetLastError();
 }
