@@ -212,6 +212,8 @@ def _on_gpu(t: torch.Tensor) -> None:
 def _want(t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, name: str) -> torch.Tensor:
     """A caller-supplied buffer the library writes (or reads) by address: it must have exactly this shape
     and dtype, be contiguous and sit on `device` (the C ABI sees only the pointer)."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -669,10 +671,15 @@ def head_distill(X: torch.Tensor, W: torch.Tensor, index: torch.Tensor, logit: t
     return loss, dX, dW
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _run(name: str, device: torch.device, *args):
-    """Calls an entry point with the current stream of the operands' device, and that device current."""
-    fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
+    """Calls an entry point with the current stream of the operands' device (a GPU), and that device current."""
+    if device.type != "cuda":
+        raise TypeError("expected GPU tensors")
+    fn = getattr(_lib or load_library(), name)
+    if device.index == _get_device():
         rc = fn(*args, _stream(device))
     else:
         with torch.cuda.device(device):
@@ -727,7 +734,6 @@ def embed(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: torch.
     n_vocab, n_in = W.shape
     tokens = _want(tokens.contiguous(), (T,), torch.int64, dev, "tokens")
     Y = _shaped(out, (T, n_in), torch.bfloat16, dev, "out")
-    _on_gpu(W)
     _run("qlora_embed", dev, tokens.data_ptr(), T, W.data_ptr(), n_vocab, n_in, float(scale), Y.data_ptr())
     return Y
 
@@ -748,17 +754,17 @@ def embed_bwd(tokens: torch.Tensor, dY: torch.Tensor, n_vocab: int, scale: float
     tokens = _want(tokens.contiguous(), (T,), torch.int64, dev, "tokens")
     dW = _shaped(dW, (n_vocab, n_in), torch.bfloat16, dev, "dW")
     ws, nb = _scratch(ws, embed_workspace_bytes(T, n_in), dev)
-    _on_gpu(dY)
     _run("qlora_embed_bwd", dev, tokens.data_ptr(), dY.data_ptr(), T, n_vocab, n_in, float(scale), int(accumulate),
          dW.data_ptr(), ws.data_ptr(), nb)
     return dW
 
 
 def _norm_weight(weight, n_in: int, device, name: str = "weight", dtype=None) -> int:
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
+    kind = getattr(weight, "dtype", None)
+    if kind != torch.float32 and kind != torch.bfloat16:
         raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
-    _want(weight, (n_in,), dtype or weight.dtype, device, name)
-    return WEIGHT_F32 if weight.dtype == torch.float32 else WEIGHT_BF16
+    _want(weight, (n_in,), dtype or kind, device, name)
+    return WEIGHT_F32 if kind == torch.float32 else WEIGHT_BF16
 
 
 def layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
@@ -783,7 +789,6 @@ def layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
         for t, name in ((mean, "mean"), (rstd, "rstd")):
             if t is not None:
                 _want(t, (T,), torch.float32, dev, name)
-    _on_gpu(X)
     _run("qlora_layer_norm", dev, X.data_ptr(), T, n_in, weight.data_ptr(), _at(bias), kind, float(eps), Y.data_ptr(),
          _at(mean), _at(rstd))
     return Y, mean, rstd
@@ -817,7 +822,6 @@ def layer_norm_bwd(X: torch.Tensor, dY: torch.Tensor, weight: torch.Tensor, mean
     nb = 0
     if dw is not None or db is not None:
         ws, nb = _scratch(ws, layer_norm_workspace_bytes(T, n_in), dev)
-    _on_gpu(X)
     _run("qlora_layer_norm_bwd", dev, X.data_ptr(), dY.data_ptr(), T, n_in, weight.data_ptr(), kind, mean.data_ptr(),
          rstd.data_ptr(), _at(dX), _at(dw), _at(db), _at(ws), nb)
     return dX, dw, db
@@ -834,18 +838,18 @@ def adapters_workspace_bytes(T: int, n_in: int, n_out: int, n_pool: int, r: int,
 def _adapters(X, A_pool, B_pool, scale, index, rank):
     """Checked operands of the adapters by token: (X, A_pool, B_pool, T, n_in, n_out, n_pool, r)."""
     X, A_pool, B_pool = _bits(X), _bits(A_pool), _bits(B_pool)
-    _inputs(X, A_pool, B_pool)
+    _inputs(X)
     T, n_in = X.shape
-    if A_pool.dim() != 3 or B_pool.dim() != 3:
-        raise ValueError(f"A_pool must be [n_pool, r, n_in] and B_pool [n_pool, n_out, r], got {tuple(A_pool.shape)}, "
-                         f"{tuple(B_pool.shape)}")
+    dev = X.device
+    if B_pool.dim() != 3:
+        raise ValueError(f"B_pool must be [n_pool, n_out, r], got {tuple(B_pool.shape)}")
     n_pool, n_out, r = B_pool.shape
-    if A_pool.shape != (n_pool, r, n_in):
-        raise ValueError(f"A_pool must be {(n_pool, r, n_in)}, got {tuple(A_pool.shape)}")
-    _want(scale, (n_pool,), torch.float32, X.device, "scale")
-    _want(index, (T,), torch.int32, X.device, "index")
+    _want(A_pool, (n_pool, r, n_in), torch.bfloat16, dev, "A_pool")
+    _want(B_pool, (n_pool, n_out, r), torch.bfloat16, dev, "B_pool")
+    _want(scale, (n_pool,), torch.float32, dev, "scale")
+    _want(index, (T,), torch.int32, dev, "index")
     if rank is not None:
-        _want(rank, (n_pool,), torch.int32, X.device, "rank")
+        _want(rank, (n_pool,), torch.int32, dev, "rank")
     return X, A_pool, B_pool, T, n_in, n_out, n_pool, r
 
 
@@ -865,7 +869,6 @@ def adapters_fwd(X: torch.Tensor, A_pool: torch.Tensor, B_pool: torch.Tensor, sc
     Y = _shaped(out, (T, n_out), bf, dev, "out")
     U = _shaped(u_out, (T, r), torch.float32, dev, "u_out") if save_u or u_out is not None else None
     ws, nb = _scratch(ws, adapters_workspace_bytes(T, n_in, n_out, n_pool, r), dev)
-    _on_gpu(X)
     _run("qlora_adapters_fwd", dev, X.data_ptr(), T, n_in, A_pool.data_ptr(), B_pool.data_ptr(), n_out, n_pool, r, _at(rank),
          scale.data_ptr(), index.data_ptr(), _at(base), Y.data_ptr(), _at(U), ws.data_ptr(), nb)
     return Y, U
@@ -896,7 +899,6 @@ def adapters_bwd(X: torch.Tensor, dY: torch.Tensor, A_pool: torch.Tensor, B_pool
             if t is not None:
                 _want(t, tuple(like.shape), bf, dev, name)
     ws, nb = _scratch(ws, adapters_workspace_bytes(T, n_in, n_out, n_pool, r, True), dev)
-    _on_gpu(X)
     _run("qlora_adapters_bwd", dev, X.data_ptr(), dY.data_ptr(), T, n_in, A_pool.data_ptr(), B_pool.data_ptr(), n_out, n_pool,
          r, _at(rank), scale.data_ptr(), index.data_ptr(), _at(U), _at(base), _at(dX), _at(dA), _at(dB), ws.data_ptr(), nb)
     return dX, dA, dB
