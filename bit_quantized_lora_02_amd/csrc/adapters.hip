@@ -283,7 +283,7 @@ __device__ __forceinline__ int chunk_at(int row, int chunk) { return row * 128 +
 // (eight lanes each) and go through a part of LDS that is the wave's own: no barriers.  Straight into the MFMA's layout,
 // where neighbouring lanes are neighbouring rows, each lane is a cache access of its own, which alone took 15 of 20 us
 // (4096 x 4096, rank up to 64; now 9).  What stands in a row that is none (past the rank) stays in that row's sums,
-// which are not stored.
+// which are not stored.  (Tiles of 32 tokens, which read the adapter half as often: 12.4 -> 16.4 us.)
 constexpr int kShrinkWaves = 8;
 template <int RT>
 __global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_shrink(AdaptRows a, const bf16_t *__restrict__ P, int64_t K,
@@ -583,21 +583,20 @@ __device__ __forceinline__ u32x4_t turned(const bf16_t *base, int ld, int row, i
   return u32x4_t{l2.x, l2.y, h2.x, h2.y};
 }
 
-// Columns per workgroup: the sums, CW x rank, are the larger part of the registers.
-constexpr int grad_cols(int rt) { return rt <= 2 ? 128 : 64; }
+constexpr int kGradCols = 64;  // per workgroup (128 take more registers for the sums: rank 64 23 us, else 17; rank 16 9.4, 8.8)
 template <int RT>
 struct GradShape {
-  static constexpr int CW = grad_cols(RT), LX = CW + 16, LV = RT * 16 + (RT > 1 ? 16 : 0);
+  static constexpr int CW = kGradCols, LX = CW + 16, LV = RT * 16 + (RT > 1 ? 16 : 0);
   static constexpr int kOwn = 32 * (LX + 2 * LV) * 2;                                // bytes of a wave
   static constexpr int LD_A = CW + 4, LD_B = RT * 16 + 4;                            // rows of the sums of dA, dB
   static constexpr int kSums = (RT * 16 * LD_A > CW * LD_B ? RT * 16 * LD_A : CW * LD_B) * 4;  // bytes, of one wave
   static constexpr int kAll = 4 * kOwn > 2 * kSums ? 4 * kOwn : 2 * kSums;
 };
 
-// BY_J: the output is [n][r] (dB), else [r][n] (dA).
+// BY_J: the output is [n][r] (dB), else [r][n] (dA).  The ranks from jb on, 16 RT of them.
 template <int RT, bool BY_J>
-__device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile, int rank, const float *__restrict__ V,
-                                           float scale, const bf16_t *__restrict__ X, int64_t N, int64_t c0,
+__device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile, int rank, int jb,
+                                           const float *__restrict__ V, float scale, const bf16_t *__restrict__ X, int64_t N, int64_t c0,
                                            float *__restrict__ part, bf16_t *__restrict__ grad, char *shared) {
   using S = GradShape<RT>;
   constexpr int CW = S::CW, LX = S::LX, LV = S::LV, XL = CW / 16, PT = CW / 16;  // XL: 16-byte loads of X per lane
@@ -612,7 +611,8 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
   constexpr int XC = CW / 8;  // 16-byte chunks of a row of X
   const int xrow = lane / XC, xcol = lane % XC * 8;
   const int64_t col = c0 + xcol < N ? c0 + xcol : N - 8;  // (behind the row's end: any, whose products are not stored)
-  auto tokens_of = [&](int t) {  // lane i: the token at place t + i % 32, the last one behind the end
+  // lane i: the token at place t + i % 32; behind the end the last one again, whose row of X then counts as zero
+  auto tokens_of = [&](int t) {
     const int p = t + (lane & 31);
     return a.order[tile.p0 + (p < tile.n ? p : tile.n - 1)];
   };
@@ -628,7 +628,7 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
     for (int i = 0; i < RT; ++i) {
       const int e = lane + 64 * i, row = e / (RT * 2), j0 = e % (RT * 2) * 8;
       const int64_t t = __builtin_amdgcn_ds_bpermute(row * 4, tokens);
-      const float4 *from = reinterpret_cast<const float4 *>(V + t * a.r + (j0 < a.r ? j0 : 0));
+      const float4 *from = reinterpret_cast<const float4 *>(V + t * a.r + (jb + j0 < a.r ? jb + j0 : 0));
       v[i][0] = from[0];
       v[i][1] = from[1];
     }
@@ -649,9 +649,7 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
     for (int i = 0; i < RT; ++i) {
       const int e = lane + 64 * i, row = e / (RT * 2), j0 = e % (RT * 2) * 8;
       const float4 p = v[i][0], q = v[i][1];
-      float u[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = row < left && j0 + k < rank ? u[k] * scale : 0.f;
+      const float u[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
       u32x4_t hi, lo;
       split8(u, &hi, &lo);
       *reinterpret_cast<u32x4_t *>(s_hi + row * LV + j0) = hi;
@@ -703,11 +701,16 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
   for (int e = tid; e < ROWS * (ROW / 8); e += 256) {
     const int row = e / (ROW / 8), c = e % (ROW / 8) * 8;
     const int64_t n = c0 + (BY_J ? row : c);
-    const int j = BY_J ? c : row;
+    const int j = jb + (BY_J ? c : row);
     if (n >= N || j >= a.r) continue;
     const f32x4_t *p = reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(shared) + row * LD + c);
     const f32x4_t *q = reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(shared + S::kSums) + row * LD + c);
-    const f32x4_t v0 = p[0] + q[0], v1 = p[1] + q[1];
+    f32x4_t v0 = p[0] + q[0], v1 = p[1] + q[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // (past the rank: zero, whatever u holds there)
+      v0[i] = j + (BY_J ? i : 0) < rank ? v0[i] * scale : 0.f;
+      v1[i] = j + (BY_J ? 4 + i : 0) < rank ? v1[i] * scale : 0.f;
+    }
     const int64_t to = BY_J ? n * a.r + j : j * N + n;
     if (tile.slot >= 0) {
       f32x4_t *out = reinterpret_cast<f32x4_t *>(part + tile.slot * size + to);
@@ -720,19 +723,22 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
   }
 }
 
+// A workgroup takes at most 64 ranks, as their sums then leave room for others (8000 tokens, 4096 x 4096, rank 128: with
+// all of them in one, and one workgroup per CU, 95 us; so 80).
 template <int RT>
-__global__ __launch_bounds__(256) void k_adapt_grads(AdaptRows a, AdaptGrads g, int piece, int blocks_a, int blocks) {
-  constexpr int CW = GradShape<RT>::CW;
+__global__ __launch_bounds__(256) void k_adapt_grads(AdaptRows a, AdaptGrads g, int piece, int parts, int blocks_a,
+                                                     int blocks) {
+  constexpr int CW = kGradCols;
   __shared__ __attribute__((aligned(128))) char shared[GradShape<RT>::kAll];
-  const int id = blockIdx.x / blocks, block = blockIdx.x - id * blocks;
+  const int id = blockIdx.x / blocks, rest = blockIdx.x - id * blocks, block = rest / parts, jb = (rest - block * parts) * 64;
   Tile tile;
   if (!find_tile(a, piece, id, &tile) || tile.group >= a.n_pool) return;
   const int rank = rank_of(a, tile.group);
   if (block < blocks_a)
-    grad_piece<RT, false>(a, tile, rank, g.dU, 1.f, g.X, g.n_in, (int64_t)block * CW, g.part_a, g.dA, shared);
+    grad_piece<RT, false>(a, tile, rank, jb, g.dU, 1.f, g.X, g.n_in, (int64_t)block * CW, g.part_a, g.dA, shared);
   else
-    grad_piece<RT, true>(a, tile, rank, g.U, a.scale[tile.group], g.dY, g.n_out, (int64_t)(block - blocks_a) * CW, g.part_b,
-                         g.dB, shared);
+    grad_piece<RT, true>(a, tile, rank, jb, g.U, a.scale[tile.group], g.dY, g.n_out, (int64_t)(block - blocks_a) * CW,
+                         g.part_b, g.dB, shared);
 }
 
 // A group's gradient from the sums of its pieces, in order, 8 values per thread; zeros for a group without tokens.  What
@@ -823,27 +829,21 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
   return hipGetLastError();
 }
 
-namespace {
-int rank_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
-}  // namespace
-
-int adapt_piece(int64_t T, int64_t n_in, int64_t n_out, int r) {
-  const int cols = grad_cols(rank_tiles(r));
-  const int64_t blocks = (n_in + cols - 1) / cols + (n_out + cols - 1) / cols;
+int adapt_piece(int64_t T, int64_t n_in, int64_t n_out) {
+  const int64_t blocks = (n_in + kGradCols - 1) / kGradCols + (n_out + kGradCols - 1) / kGradCols;
   int piece = 1024;
-  while (piece > 128 && T / piece * blocks < 512) piece /= 2;
+  while (piece > 128 && T / piece * blocks < 256) piece /= 2;
   return piece;
 }
 
 hipError_t launch_adapt_grads(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s) {
-  const int rt = rank_tiles(a.r), cols = grad_cols(rt);
-  const int64_t ba = g.dA ? (g.n_in + cols - 1) / cols : 0, bb = g.dB ? (g.n_out + cols - 1) / cols : 0;
-  const dim3 grid((uint32_t)((ba + bb) * most_tiles(a, piece))), block(256);
-#define GRADS(RT_) launch(k_adapt_grads<RT_>, grid, block, 0, s, a, g, piece, (int)ba, (int)(ba + bb))
-  if (rt == 1) GRADS(1);
-  else if (rt == 2) GRADS(2);
-  else if (rt == 4) GRADS(4);
-  else GRADS(8);
+  const int64_t ba = g.dA ? (g.n_in + kGradCols - 1) / kGradCols : 0, bb = g.dB ? (g.n_out + kGradCols - 1) / kGradCols : 0;
+  const int parts = (a.r + 63) / 64;
+  const dim3 grid((uint32_t)((ba + bb) * parts * most_tiles(a, piece))), block(256);
+#define GRADS(RT_) launch(k_adapt_grads<RT_>, grid, block, 0, s, a, g, piece, parts, (int)ba, (int)(ba + bb) * parts)
+  if (a.r <= 16) GRADS(1);
+  else if (a.r <= 32) GRADS(2);
+  else GRADS(4);
 #undef GRADS
   return hipGetLastError();
 }

@@ -69,7 +69,7 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
                                const bf16_t *base, bf16_t *out, float *U_out, hipStream_t s);
 // Gradients of the pools: dA[a][j][k] = sum over the group's tokens of dU[t][j] X[t][k], dB[a][n][j] = scale times that of
 // U[t][j] dY[t][n].  Groups are cut into pieces of `piece` tokens; those of a group of several go to part.
-int adapt_piece(int64_t T, int64_t n_in, int64_t n_out, int r);
+int adapt_piece(int64_t T, int64_t n_in, int64_t n_out);
 inline int64_t adapt_slots(int64_t T, int piece) { return 2 * (T / piece); }  // pieces of groups of several, at most
 struct AdaptGrads {
   const float *dU = nullptr, *U = nullptr;

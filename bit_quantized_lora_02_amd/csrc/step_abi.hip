@@ -108,7 +108,7 @@ AdaptPlan adapt_plan(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int
     p.du_sum = p.ranges_du > 1 ? w.take((size_t)T * r * 4) : p.du;
     p.at = w.take((size_t)n_pool * r * n_in * 2);
     p.bt = w.take((size_t)n_pool * r * n_out * 2);
-    p.piece = adapt_piece(T, n_in, n_out, r);
+    p.piece = adapt_piece(T, n_in, n_out);
     const size_t slots = (size_t)adapt_slots(T, p.piece);
     p.part_a = w.take(slots * r * n_in * 4);
     p.part_b = w.take(slots * r * n_out * 4);
