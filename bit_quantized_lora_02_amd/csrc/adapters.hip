@@ -436,7 +436,7 @@ __device__ __forceinline__ void load_u(const AdaptRows &a, const float *__restri
 constexpr int kExpandCols = 128;
 // ONCE: the base goes past the caches.
 template <int KS, int MT, bool ONCE>
-__global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 3) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
+__global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 2) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
                                                          const bf16_t *__restrict__ Q, int64_t N, bool scaled, int64_t per,
                                                          int blocks, const bf16_t *base, bf16_t *out,
                                                          float *__restrict__ U_out) {
@@ -804,9 +804,12 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
                                const bf16_t *base, bf16_t *out, float *U_out, hipStream_t s) {
   const bool wide = a.T >= 2048;
   const int64_t tiles = most_tiles(a, wide ? 32 : 16), cols = (N + kExpandCols - 1) / kExpandCols;
-  // Column blocks: enough workgroups for the GPU, few enough that their lookups and u are shared by several steps; a
-  // multiple of 8, so that a block's rows of Q stay in the L2 of one XCD (workgroups go round the eight).
-  const int64_t want = (2048 / tiles + 8) / 8 * 8, per = cols <= want ? 1 : (cols + want - 1) / want;
+  // Column blocks: enough workgroups for the GPU, few enough that their lookups and u are shared by several steps (up to
+  // 8, which suffice: 1000 tokens, 4096 x 4096 8.4 us with one step each, 6.3 with two; 4096 x 14336 56 us with 7, 60 with
+  // 14).  A multiple of 8, so that a block's rows of Q stay in the L2 of one XCD (workgroups go round the eight).
+  int64_t want = (1024 / tiles + 8) / 8 * 8;
+  if (want * 8 < cols) want = (cols + 63) / 64 * 8;
+  const int64_t per = cols <= want ? 1 : (cols + want - 1) / want;
   int64_t blocks = (cols + per - 1) / per;
   if (blocks > 8) blocks = (blocks + 7) / 8 * 8;
   // A base that the caches cannot hold beside the rest goes past them (4096 x 14336, 117 MB: the call 79 us, else 84; of
