@@ -17,7 +17,7 @@
 //                      over workgroups where there are few tokens).
 //   3. k_adapt_expand  base + u B^T (or du A): 16 or 32 tokens of one adapter, 64 columns per wave.
 //   4. k_adapt_grads   dA and dB: a piece of an adapter's tokens, 256 columns; transposed operands through LDS.
-//   5. k_adapt_reduce  sums of the pieces, in order; zeros for adapters without tokens.
+//   5. k_adapt_reduce  sums of the pieces, in order.
 // No kernel writes a value in more than one place or adds atomically: results repeat bit by bit.
 #include "step.h"
 #include "step_device.h"
@@ -73,15 +73,18 @@ __device__ __forceinline__ uint64_t same_lanes(int number, int bits) {
 struct Tile {
   int group, p0, n, slot;
 };
-// The id-th tile of the groups in order (wave-wide, the same in every lane); false: there are fewer.
+// The id-th tile of the groups in order (wave-wide, the same in every lane); false: there are fewer.  POOL: of the
+// adapters' groups alone, and one without tokens has a tile too.
+template <bool POOL>
 __device__ __forceinline__ bool find_tile(const AdaptRows &a, int M, int id, Tile *out) {
   const int lane = threadIdx.x & 63;
   int before = 0, slots = 0;
   for (int k0 = 0; k0 <= a.n_pool; k0 += 64) {
     const int k = k0 + lane;
     int lo = 0, hi = 0;
-    if (k <= a.n_pool) lo = a.start[k], hi = a.start[k + 1];
-    const int tiles = (hi - lo + M - 1) / M, several = tiles > 1 ? tiles : 0;
+    const bool there = POOL ? k < a.n_pool : k <= a.n_pool;
+    if (there) lo = a.start[k], hi = a.start[k + 1];
+    const int tiles = POOL && there && hi == lo ? 1 : (hi - lo + M - 1) / M, several = tiles > 1 ? tiles : 0;
     const int sum = scan_dpp(tiles), sum2 = scan_dpp(several);
     const int all = __builtin_amdgcn_readlane(sum, 63);
     if (id < before + all) {
@@ -106,7 +109,7 @@ template <int M>
 __device__ __forceinline__ bool find_tokens(const AdaptRows &a, int id, Tile *tile, int tokens[(M + 15) / 16]) {
   const int lane = threadIdx.x & 63;
   if (a.start) {
-    if (!find_tile(a, M, id, tile)) return false;
+    if (!find_tile<false>(a, M, id, tile)) return false;
 #pragma unroll
     for (int m = 0; m < (M + 15) / 16; ++m) {
       const int p = m * 16 + (lane & 15);
@@ -435,18 +438,39 @@ __device__ __forceinline__ void load_u(const AdaptRows &a, const float *__restri
 // a copy alone reached 3.9 to 4.9 TB/s, in such pieces 5.8.
 constexpr int kExpandCols = 128;
 // ONCE: the base goes past the caches.
+struct ExpandArgs {
+  const float *U;
+  int ranges;
+  const bf16_t *Q;
+  int64_t N;
+  bool scaled;
+  int64_t per;  // columns of a block
+  int blocks;
+  const bf16_t *base;
+  bf16_t *out;
+  float *U_out;
+};
+template <int KS, int MT>
+struct ExpandShared {
+  static constexpr int CP = KS ? KS * 4 : 2, TOKENS = 16 * MT;  // CP: 16-byte chunks of a row of the adapter
+  static constexpr int kOut = TOKENS * (kExpandCols + 4) * 4, kParts = TOKENS * CP * 32;
+  char q[4][32 * CP * 16];
+  char mem[kOut > kParts ? kOut : kParts];
+  int token[TOKENS];
+};
 template <int KS, int MT, bool ONCE>
-__global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 2) void k_adapt_expand(AdaptRows a, const float *__restrict__ U, int ranges,
-                                                         const bf16_t *__restrict__ Q, int64_t N, bool scaled, int64_t per,
-                                                         int blocks, const bf16_t *base, bf16_t *out,
-                                                         float *__restrict__ U_out) {
-  constexpr int CP = KS ? KS * 4 : 2, KQ = KS ? KS : 1, TOKENS = 16 * MT;  // CP: 16-byte chunks of a row of the adapter
-  constexpr int kRowsQ = 32 * CP * 16, kOut = TOKENS * (kExpandCols + 4) * 4, kParts = TOKENS * CP * 32;
-  __shared__ __attribute__((aligned(128))) char s_q[4][kRowsQ];
-  __shared__ __attribute__((aligned(128))) char s_mem[kOut > kParts ? kOut : kParts];
-  __shared__ int s_token[TOKENS];
+__device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs &x, int at_block, char *shared) {
+  using S = ExpandShared<KS, MT>;
+  constexpr int CP = S::CP, KQ = KS ? KS : 1, TOKENS = S::TOKENS;
+  const float *const U = x.U;
+  const int64_t N = x.N;
+  const bf16_t *const base = x.base;
+  bf16_t *const out = x.out;
+  S &sh = *reinterpret_cast<S *>(shared);
+  char *const s_mem = sh.mem;
+  int *const s_token = sh.token;
   float(*const s_out)[kExpandCols + 4] = reinterpret_cast<float(*)[kExpandCols + 4]>(s_mem);
-  const int id = blockIdx.x / blocks, block = blockIdx.x - id * blocks;
+  const int id = at_block / x.blocks, block = at_block - id * x.blocks;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l = lane & 15;
   // chunk of a row of CP chunks: rows in turn, as chunk_at
   auto swizzled = [](int row, int chunk) {
@@ -456,20 +480,20 @@ __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 2) void k_adapt_expand(Adap
   int token[MT];
   if (!find_tokens<TOKENS>(a, id, &tile, token)) return;
   const int rank = rank_of(a, tile.group);
-  if (rank == 0 && base == out && !U_out) return;
+  if (rank == 0 && base == out && !x.U_out) return;
   if (wave == 0 && g == 0)
 #pragma unroll
     for (int m = 0; m < MT; ++m) s_token[m * 16 + l] = token[m];
   __syncthreads();
-  const int64_t first = block * per, end = first + per < N ? first + per : N;
+  const int64_t first = block * x.per, end = first + x.per < N ? first + x.per : N;
   // rows as they lie in memory: a thread's 8 columns of every 16th token; its chunks of the wave's 32 rows of Q.  The first
   // step's are on their way before u is, and each next step's before the present one is stored.
   const int row0 = tid >> 4, col0 = (tid & 15) * 8;
   int64_t at[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) at[i] = (int64_t)s_token[row0 + 16 * i] * N + col0;
-  const char *const q = (const char *)(Q + (int64_t)(rank ? tile.group : 0) * N * a.r);
-  char *const own = s_q[wave];
+  const char *const q = (const char *)(x.Q + (int64_t)(rank ? tile.group : 0) * N * a.r);
+  char *const own = sh.q[wave];
   u32x4_t bv[MT], qv[CP / 2];
   auto load = [&](int64_t n0) {
 #pragma unroll
@@ -486,14 +510,14 @@ __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 2) void k_adapt_expand(Adap
       }
   };
   load(first);
-  const float scale = scaled && tile.group < a.n_pool ? a.scale[tile.group] : 1.f;
-  // u of the tile's tokens: the ranges' sums, to U_out, and times the scale in two parts to LDS
+  const float scale = x.scaled && tile.group < a.n_pool ? a.scale[tile.group] : 1.f;
+  // u of the tile's tokens: the ranges' sums, to x.U_out, and times the scale in two parts to LDS
   for (int e = tid; e < TOKENS * CP; e += 256) {
     const int n = e / CP, c = e % CP;
     float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (n < tile.n) load_u(a, U, ranges, s_token[n], c * 8, rank, u);
-    if (U_out && block == 0 && n < tile.n && c * 8 < a.r) {
-      float4 *to = reinterpret_cast<float4 *>(U_out + (int64_t)s_token[n] * a.r + c * 8);
+    if (n < tile.n) load_u(a, U, x.ranges, s_token[n], c * 8, rank, u);
+    if (x.U_out && block == 0 && n < tile.n && c * 8 < a.r) {
+      float4 *to = reinterpret_cast<float4 *>(x.U_out + (int64_t)s_token[n] * a.r + c * 8);
       to[0] = make_float4(u[0], u[1], u[2], u[3]);
       to[1] = make_float4(u[4], u[5], u[6], u[7]);
     }
@@ -570,6 +594,12 @@ __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 2) void k_adapt_expand(Adap
   }
 }
 
+template <int KS, int MT, bool ONCE>
+__global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 2) void k_adapt_expand(AdaptRows a, ExpandArgs x) {
+  __shared__ __attribute__((aligned(128))) char shared[sizeof(ExpandShared<KS, MT>)];
+  expand_tile<KS, MT, ONCE>(a, x, blockIdx.x, shared);
+}
+
 // ---------------------------------------------------------------------- grads
 // One piece of an adapter's tokens, CW columns of the long operand.  Each of four waves takes 32 tokens in turn: their
 // rows go to its own part of LDS as they are and are read back transposed (ds_read_b64_tr_b16: lane i of 16 gets element
@@ -596,7 +626,7 @@ struct GradShape {
 // BY_J: the output is [n][r] (dB), else [r][n] (dA).  The ranks from jb on, 16 RT of them.
 template <int RT, bool BY_J>
 __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile, int rank, int jb,
-                                           const float *__restrict__ V, float scale, const bf16_t *__restrict__ X, int64_t N, int64_t c0,
+                                           const float *__restrict__ V, int ranges, float scale, const bf16_t *__restrict__ X, int64_t N, int64_t c0,
                                            float *__restrict__ part, bf16_t *__restrict__ grad, char *shared) {
   using S = GradShape<RT>;
   constexpr int CW = S::CW, LX = S::LX, LV = S::LV, XL = CW / 16, PT = CW / 16;  // XL: 16-byte loads of X per lane
@@ -618,6 +648,7 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
   };
   u32x4_t x[XL];
   float4 v[RT][2];
+  const int64_t step = a.T * a.r / 4;  // from range to range
   auto load = [&](int tokens) {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
@@ -631,6 +662,11 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
       const float4 *from = reinterpret_cast<const float4 *>(V + t * a.r + (jb + j0 < a.r ? jb + j0 : 0));
       v[i][0] = from[0];
       v[i][1] = from[1];
+      for (int q = 1; q < ranges; ++q) {  // (few tokens only: otherwise the ranges have been added)
+        const float4 y = from[q * step], z = from[q * step + 1];
+        v[i][0].x += y.x, v[i][0].y += y.y, v[i][0].z += y.z, v[i][0].w += y.w;
+        v[i][1].x += z.x, v[i][1].y += z.y, v[i][1].z += z.z, v[i][1].w += z.w;
+      }
     }
   };
   int tokens = 0;
@@ -725,30 +761,47 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
 
 // A workgroup takes at most 64 ranks, as their sums then leave room for others (8000 tokens, 4096 x 4096, rank 128: with
 // all of them in one, and one workgroup per CU, 95 us; so 80).
+struct GradArgs {
+  AdaptGrads g;
+  int piece, parts, blocks_a, blocks;  // blocks: of a piece, parts for each 64 columns, of X first
+};
 template <int RT>
-__global__ __launch_bounds__(256) void k_adapt_grads(AdaptRows a, AdaptGrads g, int piece, int parts, int blocks_a,
-                                                     int blocks) {
-  constexpr int CW = kGradCols;
-  __shared__ __attribute__((aligned(128))) char shared[GradShape<RT>::kAll];
-  const int id = blockIdx.x / blocks, rest = blockIdx.x - id * blocks, block = rest / parts, jb = (rest - block * parts) * 64;
+__device__ __forceinline__ void grads_tile(const AdaptRows &a, const GradArgs &q, int at_block, char *shared) {
+  const int id = at_block / q.blocks, rest = at_block - id * q.blocks;
+  const int block = rest / q.parts, jb = (rest - block * q.parts) * 64;
   Tile tile;
-  if (!find_tile(a, piece, id, &tile) || tile.group >= a.n_pool) return;
+  if (!find_tile<true>(a, q.piece, id, &tile)) return;
   const int rank = rank_of(a, tile.group);
-  if (block < blocks_a)
-    grad_piece<RT, false>(a, tile, rank, jb, g.dU, 1.f, g.X, g.n_in, (int64_t)block * CW, g.part_a, g.dA, shared);
+  const AdaptGrads &g = q.g;
+  if (block < q.blocks_a)
+    grad_piece<RT, false>(a, tile, rank, jb, g.dU, g.dU_ranges, 1.f, g.X, g.n_in, (int64_t)block * kGradCols, g.part_a, g.dA,
+                          shared);
   else
-    grad_piece<RT, true>(a, tile, rank, jb, g.U, a.scale[tile.group], g.dY, g.n_out, (int64_t)(block - blocks_a) * CW,
-                         g.part_b, g.dB, shared);
+    grad_piece<RT, true>(a, tile, rank, jb, g.U, 1, a.scale[tile.group], g.dY, g.n_out,
+                         (int64_t)(block - q.blocks_a) * kGradCols, g.part_b, g.dB, shared);
+}
+template <int RT>
+__global__ __launch_bounds__(256) void k_adapt_grads(AdaptRows a, GradArgs q) {
+  __shared__ __attribute__((aligned(128))) char shared[GradShape<RT>::kAll];
+  grads_tile<RT>(a, q, blockIdx.x, shared);
 }
 
-// A group's gradient from the sums of its pieces, in order, 8 values per thread; zeros for a group without tokens.  What
-// has one piece is written already.
+// Few tokens, whose kernels' time is mostly their start: dX and the gradients of the pools in one.
+template <int KS, int RT>
+__global__ __launch_bounds__(256) void k_adapt_back(AdaptRows a, ExpandArgs x, GradArgs q, int expand_blocks) {
+  constexpr int kExpand = sizeof(ExpandShared<KS, 1>), kGrads = GradShape<RT>::kAll;
+  __shared__ __attribute__((aligned(128))) char shared[kExpand > kGrads ? kExpand : kGrads];
+  if ((int)blockIdx.x < expand_blocks) expand_tile<KS, 1, false>(a, x, blockIdx.x, shared);
+  else grads_tile<RT>(a, q, blockIdx.x - expand_blocks, shared);
+}
+
+// A group's gradient from the sums of its pieces, in order, 8 values per thread.  What has one piece is written already.
 __global__ __launch_bounds__(256) void k_adapt_reduce(AdaptRows a, AdaptGrads g, int piece, int64_t blocks_a) {
   const int group = blockIdx.y, lane = threadIdx.x & 63;
   const int n = a.start[group + 1] - a.start[group], pieces = (n + piece - 1) / piece;
-  if (pieces == 1) return;
+  if (pieces <= 1) return;
   int slot = 0;  // pieces of earlier groups of several
-  for (int k0 = 0; k0 < group && pieces; k0 += 64) {
+  for (int k0 = 0; k0 < group; k0 += 64) {
     int c = 0;
     if (k0 + lane < group) c = (a.start[k0 + lane + 1] - a.start[k0 + lane] + piece - 1) / piece;
     slot += __builtin_amdgcn_readlane(scan_dpp(c > 1 ? c : 0), 63);
@@ -800,9 +853,10 @@ hipError_t launch_adapt_shrink(const AdaptRows &a, const bf16_t *P, int64_t K, c
   return hipGetLastError();
 }
 
-hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, const bf16_t *Q, int64_t N, bool scaled,
-                               const bf16_t *base, bf16_t *out, float *U_out, hipStream_t s) {
-  const bool wide = a.T >= 2048;
+namespace {
+// The expanding product's arguments and workgroups.
+ExpandArgs expand_args(const AdaptRows &a, bool wide, const float *U, int ranges, const bf16_t *Q, int64_t N, bool scaled,
+                       const bf16_t *base, bf16_t *out, float *U_out, int64_t *grid) {
   const int64_t tiles = most_tiles(a, wide ? 32 : 16), cols = (N + kExpandCols - 1) / kExpandCols;
   // Column blocks: enough workgroups for the GPU, few enough that their lookups and u are shared by several steps (up to
   // 8, which suffice: 1000 tokens, 4096 x 4096 8.4 us with one step each, 6.3 with two; 4096 x 14336 56 us with 7, 60 with
@@ -812,27 +866,43 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
   const int64_t per = cols <= want ? 1 : (cols + want - 1) / want;
   int64_t blocks = (cols + per - 1) / per;
   if (blocks > 8) blocks = (blocks + 7) / 8 * 8;
+  *grid = blocks * tiles;
+  return ExpandArgs{U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, base, out, U_out};
+}
+
+GradArgs grad_args(const AdaptRows &a, const AdaptGrads &g, int piece, int64_t *grid) {
+  const int64_t ba = g.dA ? (g.n_in + kGradCols - 1) / kGradCols : 0, bb = g.dB ? (g.n_out + kGradCols - 1) / kGradCols : 0;
+  const int parts = (a.r + 63) / 64;
+  *grid = (ba + bb) * parts * (a.T / piece + a.n_pool);
+  return GradArgs{g, piece, parts, (int)ba, (int)(ba + bb) * parts};
+}
+}  // namespace
+
+hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, const bf16_t *Q, int64_t N, bool scaled,
+                               const bf16_t *base, bf16_t *out, float *U_out, hipStream_t s) {
+  const bool wide = a.T >= 2048;
+  int64_t blocks;
+  const ExpandArgs x = expand_args(a, wide, U, ranges, Q, N, scaled, base, out, U_out, &blocks);
   // A base that the caches cannot hold beside the rest goes past them (4096 x 14336, 117 MB: the call 79 us, else 84; of
   // 25 MB, just written, 19 us of the kernel, else 14).
   const bool once = a.T * N * 2 > (int64_t)64 << 20;
-  const dim3 grid((uint32_t)(blocks * tiles)), block(256);
-#define EXPAND_ARGS grid, block, 0, s, a, U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, base, out, U_out
-#define EXPAND(KS_)                                                     \
-  do {                                                                  \
-    if (wide && once) launch(k_adapt_expand<KS_, 2, true>, EXPAND_ARGS);  \
-    else if (wide) launch(k_adapt_expand<KS_, 2, false>, EXPAND_ARGS);  \
-    else launch(k_adapt_expand<KS_, 1, false>, EXPAND_ARGS);            \
+  const dim3 grid((uint32_t)blocks), block(256);
+#define EXPAND(KS_)                                                                   \
+  do {                                                                                \
+    if (wide && once) launch(k_adapt_expand<KS_, 2, true>, grid, block, 0, s, a, x);  \
+    else if (wide) launch(k_adapt_expand<KS_, 2, false>, grid, block, 0, s, a, x);    \
+    else launch(k_adapt_expand<KS_, 1, false>, grid, block, 0, s, a, x);              \
   } while (0)
   if (a.r <= 16) EXPAND(0);
   else if (a.r <= 32) EXPAND(1);
   else if (a.r <= 64) EXPAND(2);
   else EXPAND(4);
 #undef EXPAND
-#undef EXPAND_ARGS
   return hipGetLastError();
 }
 
 int adapt_piece(int64_t T, int64_t n_in, int64_t n_out) {
+  if (T <= 512) return 512;  // (one piece: no sums to add)
   const int64_t blocks = (n_in + kGradCols - 1) / kGradCols + (n_out + kGradCols - 1) / kGradCols;
   int piece = 1024;
   while (piece > 128 && T / piece * blocks < 256) piece /= 2;
@@ -840,14 +910,26 @@ int adapt_piece(int64_t T, int64_t n_in, int64_t n_out) {
 }
 
 hipError_t launch_adapt_grads(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s) {
-  const int64_t ba = g.dA ? (g.n_in + kGradCols - 1) / kGradCols : 0, bb = g.dB ? (g.n_out + kGradCols - 1) / kGradCols : 0;
-  const int parts = (a.r + 63) / 64;
-  const dim3 grid((uint32_t)((ba + bb) * parts * most_tiles(a, piece))), block(256);
-#define GRADS(RT_) launch(k_adapt_grads<RT_>, grid, block, 0, s, a, g, piece, parts, (int)ba, (int)(ba + bb) * parts)
-  if (a.r <= 16) GRADS(1);
-  else if (a.r <= 32) GRADS(2);
-  else GRADS(4);
-#undef GRADS
+  int64_t blocks;
+  const GradArgs q = grad_args(a, g, piece, &blocks);
+  const dim3 grid((uint32_t)blocks), block(256);
+  if (a.r <= 16) launch(k_adapt_grads<1>, grid, block, 0, s, a, q);
+  else if (a.r <= 32) launch(k_adapt_grads<2>, grid, block, 0, s, a, q);
+  else launch(k_adapt_grads<4>, grid, block, 0, s, a, q);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_back(const AdaptRows &a, const AdaptGrads &g, int piece, const bf16_t *Q, const bf16_t *base,
+                             bf16_t *dX, hipStream_t s) {
+  int64_t eb, gb;
+  const ExpandArgs x = expand_args(a, false, g.dU, g.dU_ranges, Q, g.n_in, false, base, dX, nullptr, &eb);
+  const GradArgs q = grad_args(a, g, piece, &gb);
+  const dim3 grid((uint32_t)(eb + gb)), block(256);
+  const int e = (int)eb;
+  if (a.r <= 16) launch(k_adapt_back<0, 1>, grid, block, 0, s, a, x, q, e);
+  else if (a.r <= 32) launch(k_adapt_back<1, 2>, grid, block, 0, s, a, x, q, e);
+  else if (a.r <= 64) launch(k_adapt_back<2, 4>, grid, block, 0, s, a, x, q, e);
+  else launch(k_adapt_back<4, 4>, grid, block, 0, s, a, x, q, e);
   return hipGetLastError();
 }
 

@@ -45,6 +45,7 @@ hipError_t launch_norm_reduce(const float *part, int groups, int64_t D, bool f32
 // start[a + 1] - 1 (group n_pool: those without an adapter), each in the order of the batch.
 constexpr int kPoolMax = 1000;
 constexpr int64_t kAdaptSmall = 64;  // up to so many tokens the forward's workgroups group them by themselves
+constexpr int64_t kAdaptFew = 128;   // tokens of a backward whose last two products are one launch
 struct AdaptRows {
   const int32_t *index = nullptr;  // [T] adapter of each token
   int64_t T = 0;
@@ -73,12 +74,16 @@ int adapt_piece(int64_t T, int64_t n_in, int64_t n_out);
 inline int64_t adapt_slots(int64_t T, int piece) { return 2 * (T / piece); }  // pieces of groups of several, at most
 struct AdaptGrads {
   const float *dU = nullptr, *U = nullptr;
+  int dU_ranges = 1;  // that are not added yet (kAdaptFew tokens at most)
   const bf16_t *X = nullptr, *dY = nullptr;
   int64_t n_in = 0, n_out = 0;
   float *part_a = nullptr, *part_b = nullptr;  // [slots][r][n_in], [slots][n_out][r]
   bf16_t *dA = nullptr, *dB = nullptr;
 };
 hipError_t launch_adapt_grads(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s);
+// Up to kAdaptFew tokens: dX, as launch_adapt_expand forms it from dU and Q, and the gradients, which are one piece.
+hipError_t launch_adapt_back(const AdaptRows &a, const AdaptGrads &g, int piece, const bf16_t *Q, const bf16_t *base,
+                             bf16_t *dX, hipStream_t s);
 hipError_t launch_adapt_reduce(const AdaptRows &a, const AdaptGrads &g, int piece, hipStream_t s);
 
 }  // namespace qlora

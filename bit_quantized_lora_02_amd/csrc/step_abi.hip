@@ -232,18 +232,25 @@ int qlora_adapters_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, int
       LAUNCH("adapters_shrink", launch_adapt_shrink(a, X, n_in, A_pool, false, 1, u, s));
       g.U = u;
     }
+    const bool few = T <= kAdaptFew && dx && (dA || dB);
     if (dx || dA) {
       float *du = (float *)(w + p.du), *sum = (float *)(w + p.du_sum);
       const int ranges = dx ? p.ranges_du : 1;
       LAUNCH("adapters_shrink", launch_adapt_shrink(a, dY, n_out, tb.to, true, ranges, du, s));
+      g.dU = du;
+      if (few) {
+        g.dU_ranges = ranges;
+        LAUNCH("adapters_back", launch_adapt_back(a, g, p.piece, ta.to, base, dX, s));
+        return QLORA_OK;
+      }
       if (dx)
         LAUNCH("adapters_expand", launch_adapt_expand(a, du, ranges, ta.to, n_in, false, base, dX,
                                                       dA && ranges > 1 ? sum : nullptr, s));
-      g.dU = ranges > 1 ? sum : du;
+      if (ranges > 1) g.dU = sum;
     }
-    if (dA || dB) LAUNCH("adapters_grads", launch_adapt_grads(a, g, p.piece, s));
   }
-  if (dA || dB) LAUNCH("adapters_reduce", launch_adapt_reduce(a, g, p.piece, s));
+  if (dA || dB) LAUNCH("adapters_grads", launch_adapt_grads(a, g, p.piece, s));
+  if ((dA || dB) && T > p.piece) LAUNCH("adapters_reduce", launch_adapt_reduce(a, g, p.piece, s));
   return QLORA_OK;
 }
 
