@@ -83,8 +83,8 @@ int check_adapters(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32
   if (n_pool < 1 || n_pool > kPoolMax) return fail(QLORA_EINVAL, "n_pool must be in [1, %d] (got %d)", kPoolMax, (int)n_pool);
   if (r < 8 || r > QLORA_MAX_RANK || r % 8)
     return fail(QLORA_EINVAL, "r must be a multiple of 8 in [8, %d] (got %d)", QLORA_MAX_RANK, (int)r);
-  if (n_pool * n_in > (int64_t)1 << 28 || n_pool * n_out > (int64_t)1 << 28)
-    return fail(QLORA_EINVAL, "n_pool x n_in and n_pool x n_out must be at most 2^28");
+  if (n_pool * n_in > (int64_t)1 << 27 || n_pool * n_out > (int64_t)1 << 27)
+    return fail(QLORA_EINVAL, "n_pool x n_in and n_pool x n_out must be at most 2^27");
   if (T * n_in >= (int64_t)1 << 32 || T * n_out >= (int64_t)1 << 32)
     return fail(QLORA_EINVAL, "T x n_in and T x n_out must be below 2^32");
   return QLORA_OK;

@@ -492,7 +492,7 @@ int qlora_layer_norm_workspace_bytes(int64_t T, int64_t n_in, size_t *bytes);
  * rank, scale and index are read by the kernels.  u is binary32 and enters its second product as two bf16 parts (off by
  * at most 2^-16 of it); the products accumulate in binary32 in a fixed order and Y is rounded once.
  * n_in, n_out % 8 == 0, 8 <= r <= QLORA_MAX_RANK with r % 8 == 0, 1 <= n_pool <= QLORA_MAX_POOL, n_pool * n_in and
- * n_pool * n_out <= 2^28, T <= 2^22, T * n_in and T * n_out < 2^32.  X, A_pool, B_pool, base, Y, U_out 16-byte aligned,
+ * n_pool * n_out <= 2^27, T <= 2^22, T * n_in and T * n_out < 2^32.  X, A_pool, B_pool, base, Y, U_out 16-byte aligned,
  * rank, scale, index 4-byte; outputs overlap no input except Y base.
  * ws: qlora_adapters_workspace_bytes(T, n_in, n_out, n_pool, r, 0), 256-byte aligned; nothing in it needs to start at
  * zero, and calls that overlap in time need workspaces of their own.

@@ -36,7 +36,7 @@ SHARED = [(dict(T=-1), "T must"), (dict(T=(1 << 22) + 1), "T must"), (dict(K=0),
           (dict(K=60), "multiples of 8"), (dict(N=0), "multiples of 8"), (dict(N=71), "multiples of 8"),
           (dict(K=(1 << 22) + 8), "2^22"), (dict(N=(1 << 22) + 8), "2^22"), (dict(pool=0), "n_pool"),
           (dict(pool=1001), "n_pool"), (dict(r=0), "r must"), (dict(r=12), "r must"), (dict(r=136), "r must"),
-          (dict(pool=1000, K=1 << 20), "2^28"), (dict(pool=1000, N=1 << 20), "2^28"), (dict(T=1 << 20, K=1 << 12), "2^32"),
+          (dict(pool=1000, K=1 << 20), "2^27"), (dict(pool=1000, N=1 << 20), "2^27"), (dict(T=1 << 20, K=1 << 12), "2^32"),
           (dict(T=1 << 20, N=1 << 12), "2^32"), (dict(X=None), "X and index"), (dict(index=None), "X and index"),
           (dict(A=None), "A_pool"), (dict(Bp=None), "B_pool"), (dict(scale=None), "scale"), (dict(X=MIS), "16-byte"),
           (dict(A=MIS), "16-byte"), (dict(Bp=MIS), "16-byte"), (dict(rank=ODD), "4-byte"), (dict(scale=ODD), "4-byte"),
