@@ -718,22 +718,24 @@ def layer_norm_workspace_bytes(T: int, n_in: int) -> int:
     return b.value
 
 
-def _tokens(tokens) -> None:
+def _tokens(tokens, device) -> torch.Tensor:
     if not isinstance(tokens, torch.Tensor) or tokens.dtype != torch.int64 or tokens.dim() != 1:
         raise TypeError("tokens must be a 1-D int64 tensor")
+    if tokens.device != device:
+        raise ValueError(f"tokens are on {tokens.device}, expected {device}")
+    return tokens.contiguous()
 
 
 def embed(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
     """scale * W[tokens] (bf16 [n_vocab, n_in] -> [T, n_in], rounded once); tokens int64 [T], one outside the vocabulary
     gives a row of zeros."""
-    _tokens(tokens)
     W = _bits(W)
     if W.dim() != 2:
         raise ValueError(f"W must be [n_vocab, n_in], got {tuple(W.shape)}")
-    T, dev = tokens.shape[0], W.device
-    n_vocab, n_in = W.shape
-    tokens = _want(tokens.contiguous(), (T,), torch.int64, dev, "tokens")
-    Y = _shaped(out, (T, n_in), torch.bfloat16, dev, "out")
+    dev = W.device
+    tokens = _tokens(tokens, dev)
+    T, (n_vocab, n_in) = tokens.shape[0], W.shape
+    Y = W.new_empty((T, n_in)) if out is None else _want(out, (T, n_in), torch.bfloat16, dev, "out")
     _run("qlora_embed", dev, tokens.data_ptr(), T, W.data_ptr(), n_vocab, n_in, float(scale), Y.data_ptr())
     return Y
 
@@ -744,15 +746,16 @@ def embed_bwd(tokens: torch.Tensor, dY: torch.Tensor, n_vocab: int, scale: float
 
     ``dW`` is an optional preallocated result; with ``accumulate`` the sums are added to what it holds (a tied output
     layer's gradient) and the rows that no token names stay as they are."""
-    _tokens(tokens)
     dY = _bits(dY)
     if dY.dim() != 2:
         raise ValueError(f"dY must be [T, n_in], got {tuple(dY.shape)}")
     if accumulate and dW is None:
         raise ValueError("accumulate needs dW")
     (T, n_in), dev = dY.shape, dY.device
-    tokens = _want(tokens.contiguous(), (T,), torch.int64, dev, "tokens")
-    dW = _shaped(dW, (n_vocab, n_in), torch.bfloat16, dev, "dW")
+    tokens = _tokens(tokens, dev)
+    if tokens.shape[0] != T:
+        raise ValueError(f"{T} rows of dY, but {tokens.shape[0]} tokens")
+    dW = dY.new_empty((n_vocab, n_in)) if dW is None else _want(dW, (n_vocab, n_in), torch.bfloat16, dev, "dW")
     ws, nb = _scratch(ws, embed_workspace_bytes(T, n_in), dev)
     _run("qlora_embed_bwd", dev, tokens.data_ptr(), dY.data_ptr(), T, n_vocab, n_in, float(scale), int(accumulate),
          dW.data_ptr(), ws.data_ptr(), nb)

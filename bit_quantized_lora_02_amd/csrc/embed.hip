@@ -294,7 +294,8 @@ hipError_t launch_embed(const int64_t *tokens, int64_t T, const bf16_t *W, int64
   return hipGetLastError();
 }
 
-int embed_piece(int64_t T) { return T <= 2048 ? 8 : T <= 8192 ? 16 : kPieceMost; }
+// (Up to 32 tokens one piece, without a join; then enough pieces to fill the GPU.)
+int embed_piece(int64_t T) { return T <= kPieceMost ? kPieceMost : T <= 2048 ? 8 : T <= 8192 ? 16 : kPieceMost; }
 
 hipError_t launch_embed_order(const int64_t *tokens, int64_t T, int64_t V, const Order &o, bf16_t *fill, int64_t fill_n,
                               hipStream_t s) {
