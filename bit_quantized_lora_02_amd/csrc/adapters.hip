@@ -7,16 +7,15 @@
 // ("QLoRA: fine-tuning a large model on one GPU" (learn.pranaymahendrakar.com), Researcher level, "LoRA, stated once" and
 // "The variants worth knowing": one base model in memory, requests for different adapters batched together.)
 // At ranks up to 128 every product has far fewer operations per byte than the matrix units need to be the bound: the
-// floor is the traffic of X, Y and the adapters in use.  So each product streams its long operand once, straight from
-// HBM into MFMA operands, and the rank-wide results u and du stay in binary32: where one of them is an operand it enters
-// as two bf16 parts (16 bits of it), which costs a second MFMA on idle units and leaves the outputs with the one rounding
-// of their type.
+// floor is the traffic of X, Y and the adapters in use.  So each product streams its long operand once, and the rank-wide
+// results u and du stay in binary32: where one of them is an operand it enters as two bf16 parts (16 bits of it), which
+// costs a second MFMA on idle units and leaves the outputs with the one rounding of their type.
 //   1. k_adapt_plan    one workgroup groups the tokens by adapter (stably); the others transpose the pools for the backward.
 //                      Up to kAdaptSmall tokens in the forward, the next kernels find their tokens themselves.
 //   2. k_adapt_shrink  u or du: 16 tokens of one adapter against its r rows, the long axis over 8 waves (and ranges of it
 //                      over workgroups where there are few tokens).
-//   3. k_adapt_expand  base + u B^T (or du A): 16 or 32 tokens of one adapter, 64 columns per wave.
-//   4. k_adapt_grads   dA and dB: a piece of an adapter's tokens, 256 columns; transposed operands through LDS.
+//   3. k_adapt_expand  base + u B^T (or du A): 16 or 32 tokens of one adapter, 128 columns at a time.
+//   4. k_adapt_grads   dA and dB: a piece of an adapter's tokens, 64 columns; transposed operands through LDS.
 //   5. k_adapt_reduce  sums of the pieces, in order.
 // No kernel writes a value in more than one place or adds atomically: results repeat bit by bit.
 #include "step.h"
@@ -285,7 +284,7 @@ __device__ __forceinline__ int chunk_at(int row, int chunk) { return row * 128 +
 // RT: rank tiles of 16.  Eight waves take 64-value steps of the long axis in turn.  A step's rows come in whole lines
 // (eight lanes each) and go through a part of LDS that is the wave's own: no barriers.  Straight into the MFMA's layout,
 // where neighbouring lanes are neighbouring rows, each lane is a cache access of its own, which alone took 15 of 20 us
-// (4096 x 4096, rank up to 64; now 9).  What stands in a row that is none (past the rank) stays in that row's sums,
+// (4096 tokens x 4096, ranks to 64; now 12, 2.8 TB/s of X beside the adapters' rows from the L2).  What stands in a row that is none (past the rank) stays in that row's sums,
 // which are not stored.  (Tiles of 32 tokens, which read the adapter half as often: 12.4 -> 16.4 us.)
 constexpr int kShrinkWaves = 8;
 template <int RT>
@@ -858,10 +857,14 @@ namespace {
 ExpandArgs expand_args(const AdaptRows &a, bool wide, const float *U, int ranges, const bf16_t *Q, int64_t N, bool scaled,
                        const bf16_t *base, bf16_t *out, float *U_out, int64_t *grid) {
   const int64_t tiles = most_tiles(a, wide ? 32 : 16), cols = (N + kExpandCols - 1) / kExpandCols;
-  // Column blocks: enough workgroups for the GPU, few enough that their lookups and u are shared by several steps (up to
-  // 8, which suffice: 1000 tokens, 4096 x 4096 8.4 us with one step each, 6.3 with two; 4096 x 14336 56 us with 7, 60 with
-  // 14).  A multiple of 8, so that a block's rows of Q stay in the L2 of one XCD (workgroups go round the eight).
+  // Column blocks: enough workgroups for the GPU, few enough that their lookups and u are shared by several steps (1000
+  // tokens, 4096 x 4096 8.4 us with one step each, 6.3 with two; 4096 tokens x 14336 62 us with 4, 56 with 7, 60 with 14;
+  // 8000 x 4096 30.0 with two, 32.5 with four).  A multiple of 8, so that a block's rows of Q stay in the L2 of one XCD
+  // (workgroups go round the eight).  Above rank 64 u costs a block more: 8000 x 4096, rank 128 55 us with four steps, 63
+  // with two.
+  const int64_t least = a.r > 64 ? 8 : 16;
   int64_t want = (1024 / tiles + 8) / 8 * 8;
+  if (want < least) want = least;
   if (want * 8 < cols) want = (cols + 63) / 64 * 8;
   const int64_t per = cols <= want ? 1 : (cols + want - 1) / want;
   int64_t blocks = (cols + per - 1) / per;
