@@ -1002,7 +1002,10 @@ class HeadDistillFn(torch.autograd.Function):
 
 
 class EmbedFn(torch.autograd.Function):
-    """Autograd wrapper of ``embed``: forward(tokens, W, scale) -> Y; the gradient of W is dense."""
+    """Autograd wrapper of ``embed``: forward(tokens, W, scale) -> Y; the gradient of W is dense.
+
+    This and the next two can be captured into a HIP graph, forward and backward, where no eager graph of the same leaves is
+    alive."""
 
     @classmethod
     def apply(cls, tokens, W, scale=1.0):
