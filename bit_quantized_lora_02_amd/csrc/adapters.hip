@@ -10,8 +10,9 @@
 // floor is the traffic of X, Y and the adapters in use.  So each product streams its long operand once, and the rank-wide
 // results u and du stay in binary32: where one of them is an operand it enters as two bf16 parts (16 bits of it), which
 // costs a second MFMA on idle units and leaves the outputs with the one rounding of their type.
-//   1. k_adapt_plan    one workgroup groups the tokens by adapter (stably); the others transpose the pools for the backward.
-//                      Up to kAdaptSmall tokens in the forward, the next kernels find their tokens themselves.
+//   1. k_adapt_plan    groups the tokens by adapter (stably), a workgroup for 8192 of them (more, which k_adapt_count counts
+//                      before); other workgroups transpose the pools for the backward.  Up to kAdaptSmall tokens in the
+//                      forward, the next kernels find their tokens themselves.
 //   2. k_adapt_shrink  u or du: 16 tokens of one adapter against its r rows, the long axis over 8 waves (and ranges of it
 //                      over workgroups where there are few tokens).
 //   3. k_adapt_expand  base + u B^T (or du A): 16 or 32 tokens of one adapter, 128 columns at a time.
@@ -54,6 +55,14 @@ __device__ __forceinline__ int rank_of(const AdaptRows &a, int group) {
   if (!a.rank) return a.r;
   const int k = a.rank[group];
   return k < 0 ? 0 : k > a.r ? a.r : k;
+}
+
+// A wave's stores to its own part of LDS, then its other lanes' loads from it (or the other way round): the LDS serves a
+// wave in order, so this only keeps the compiler to it.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Lanes whose number is this lane's, by a vote on each of its bits.
@@ -169,51 +178,68 @@ struct PlanShared {
   int at[kPlanWaves][1024];  // tokens of a wave's share in each group, then where the next of them goes
   int wave[kPlanWaves];
 };
-// The tokens are shared out to 16 waves in order.  A lane finds the lanes with its own group by a vote per bit of the
-// group's number; the first of them adds their count to the wave's, and a lane's place is the group's start, plus the
-// counts of earlier waves and steps, plus the equal lanes before it: the order of the batch is kept.
-constexpr int kPlanSteps = 8;  // of 64 tokens, whose groups a wave holds at once (all of its share up to 8192 tokens)
-__device__ __forceinline__ void plan_tokens(const AdaptRows &a, PlanShared &sh) {
+// A chunk of 8192 tokens is shared out to 16 waves in order.  A lane finds the lanes with its own group by a vote per bit of
+// the group's number; the first of them adds their count to the wave's, and a lane's place is the group's start, plus the
+// counts of earlier chunks, waves and steps, plus the equal lanes before it: the order of the batch is kept.  Of several
+// chunks a first launch writes the counts (COUNT), and each one adds up what it needs of them (65536 tokens 16 us for both,
+// in one workgroup 85).
+constexpr int kPlanSteps = 8;  // of 64 tokens, whose groups a wave holds at once
+static_assert(kPlanWaves * 64 * kPlanSteps == kAdaptChunk, "a wave holds its share of a chunk");
+template <bool COUNT>
+__device__ __forceinline__ void plan_tokens(const AdaptRows &a, int chunk, PlanShared &sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), groups = a.n_pool + 1;
   const int bits = 32 - __builtin_clz(groups);
-  const int64_t per = ((a.T + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64, first = wave * per;
-  const int64_t end = first + per < a.T ? first + per : a.T;
+  const int64_t c0 = chunk * kAdaptChunk, c1 = c0 + kAdaptChunk < a.T ? c0 + kAdaptChunk : a.T;
+  const int64_t per = ((c1 - c0 + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64, first = c0 + wave * per;
+  const int64_t end = first + per < c1 ? first + per : c1;
   int group[kPlanSteps];
   uint64_t same[kPlanSteps];
-  auto load = [&](int64_t t0) {
 #pragma unroll
-    for (int i = 0; i < kPlanSteps; ++i) {
-      const int64_t t = t0 + i * 64 + lane;
-      group[i] = t < end ? group_of(a, t) : groups;  // (no token: a group of its own)
-    }
+  for (int i = 0; i < kPlanSteps; ++i) {
+    const int64_t t = first + i * 64 + lane;
+    group[i] = t < end ? group_of(a, t) : groups;  // (no token: a group of its own)
+  }
 #pragma unroll
-    for (int i = 0; i < kPlanSteps; ++i) same[i] = same_lanes(group[i], bits);
-  };
+  for (int i = 0; i < kPlanSteps; ++i) same[i] = same_lanes(group[i], bits);
   const uint64_t before = ((uint64_t)1 << lane) - 1;
-  load(first);
   if (tid < groups)
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) sh.at[w][tid] = 0;
   __syncthreads();
-  for (int64_t t0 = first; t0 < end; t0 += 64 * kPlanSteps) {
-    if (t0 > first) load(t0);
 #pragma unroll
-    for (int i = 0; i < kPlanSteps; ++i)
-      if (group[i] < groups && (same[i] & before) == 0) atomicAdd(&sh.at[wave][group[i]], __popcll(same[i]));
-  }
+  for (int i = 0; i < kPlanSteps; ++i)
+    if (group[i] < groups && (same[i] & before) == 0) atomicAdd(&sh.at[wave][group[i]], __popcll(same[i]));
   __syncthreads();
   int n = 0;  // thread k: tokens of group k
   if (tid < groups)
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) n += sh.at[w][tid];
+  if (COUNT) {
+    if (tid < groups) a.counts[(int64_t)chunk * groups + tid] = n;
+    return;
+  }
+  int earlier = 0;  // those in earlier chunks
+  if (a.counts && tid < groups) {
+    const int chunks = (int)adapt_chunks(a.T);
+    n = 0;
+#pragma unroll 8
+    for (int c = 0; c < chunks; ++c) {
+      const int k = a.counts[(int64_t)c * groups + tid];
+      earlier += c < chunk ? k : 0;
+      n += k;
+    }
+  }
   const int sum = scan_dpp(n);
   if (lane == 63) sh.wave[wave] = sum;
   __syncthreads();
   int at = sum - n;
   for (int w = 0; w < wave; ++w) at += sh.wave[w];
   if (tid < groups) {
-    a.start[tid] = at;
-    if (tid == a.n_pool) a.start[groups] = at + n;
+    if (chunk == 0) {
+      a.start[tid] = at;
+      if (tid == a.n_pool) a.start[groups] = at + n;
+    }
+    at += earlier;
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) {
       const int c = sh.at[w][tid];
@@ -222,19 +248,16 @@ __device__ __forceinline__ void plan_tokens(const AdaptRows &a, PlanShared &sh) 
     }
   }
   __syncthreads();
-  const bool whole = per <= 64 * kPlanSteps;
-  if (!whole) load(first);
-  for (int64_t t0 = first; t0 < end; t0 += 64 * kPlanSteps) {
-    if (t0 > first) load(t0);
 #pragma unroll
-    for (int i = 0; i < kPlanSteps; ++i) {
-      if (group[i] < groups) {
-        int *const at_ = &sh.at[wave][group[i]];
-        const int base = *at_;
-        a.order[base + __popcll(same[i] & before)] = (int32_t)(t0 + i * 64 + lane);
-        if ((same[i] & before) == 0) *at_ = base + __popcll(same[i]);  // (after all lanes have read it: one wave, in order)
-      }
+  for (int i = 0; i < kPlanSteps; ++i) {
+    if (group[i] < groups) {
+      int *const at_ = &sh.at[wave][group[i]];
+      const int base = *at_;
+      a.order[base + __popcll(same[i] & before)] = (int32_t)(first + i * 64 + lane);
+      wave_order();
+      if ((same[i] & before) == 0) *at_ = base + __popcll(same[i]);
     }
+    wave_order();
   }
 }
 
@@ -268,12 +291,23 @@ int64_t turn_blocks(const AdaptTurn &t, int n_pool) {
   return t.to ? n_pool * ((t.rows + kTurn - 1) / kTurn) * ((t.cols + 127) / 128) : 0;
 }
 
-__global__ __launch_bounds__(1024) void k_adapt_plan(AdaptRows a, AdaptTurn t0, AdaptTurn t1, int64_t blocks0) {
+// The first workgroups group the tokens, a chunk each; the others transpose.
+__global__ __launch_bounds__(1024) void k_adapt_plan(AdaptRows a, int chunks, AdaptTurn t0, AdaptTurn t1, int64_t blocks0,
+                                                     int64_t blocks) {
   __shared__ __attribute__((aligned(16))) char shared[sizeof(PlanShared)];
   static_assert(sizeof(TurnShared) <= sizeof(PlanShared), "one piece of LDS for both");
-  if (blockIdx.x == 0) plan_tokens(a, *reinterpret_cast<PlanShared *>(shared));
-  else if (blockIdx.x - 1 < blocks0) turn_pool(t0, blockIdx.x - 1, *reinterpret_cast<TurnShared *>(shared));
-  else turn_pool(t1, blockIdx.x - 1 - blocks0, *reinterpret_cast<TurnShared *>(shared));
+  if ((int)blockIdx.x < chunks) {
+    plan_tokens<false>(a, blockIdx.x, *reinterpret_cast<PlanShared *>(shared));
+    return;
+  }
+  for (int64_t id = (int)blockIdx.x - chunks; id < blocks; id += (int)gridDim.x - chunks) {
+    turn_pool(id < blocks0 ? t0 : t1, id < blocks0 ? id : id - blocks0, *reinterpret_cast<TurnShared *>(shared));
+    __syncthreads();
+  }
+}
+__global__ __launch_bounds__(1024) void k_adapt_count(AdaptRows a) {
+  __shared__ PlanShared shared;
+  plan_tokens<true>(a, blockIdx.x, shared);
 }
 
 // A 16-byte chunk of a row of 64 values in LDS: the eight chunks of rows in turn, so that the 16 rows that an MFMA operand
@@ -284,13 +318,14 @@ __device__ __forceinline__ int chunk_at(int row, int chunk) { return row * 128 +
 // RT: rank tiles of 16.  Eight waves take 64-value steps of the long axis in turn.  A step's rows come in whole lines
 // (eight lanes each) and go through a part of LDS that is the wave's own: no barriers.  Straight into the MFMA's layout,
 // where neighbouring lanes are neighbouring rows, each lane is a cache access of its own, which alone took 15 of 20 us
-// (4096 tokens x 4096, ranks to 64; now 12, 2.8 TB/s of X beside the adapters' rows from the L2).  What stands in a row that is none (past the rank) stays in that row's sums,
-// which are not stored.  (Tiles of 32 tokens, which read the adapter half as often: 12.4 -> 16.4 us.)
+// (4096 tokens x 4096, ranks to 64; now 12, 2.8 TB/s of X beside the adapters' rows from the L2).  What stands in a row
+// that is none (past the rank) stays in that row's sums, which are not stored.  (Tiles of 32 tokens, which read the adapter
+// half as often: 12.4 -> 16.4 us.)
 constexpr int kShrinkWaves = 8;
 template <int RT>
-__global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_shrink(AdaptRows a, const bf16_t *__restrict__ P, int64_t K,
-                                                                    const bf16_t *__restrict__ Q, bool scaled, int ranges,
-                                                                    float *__restrict__ U) {
+__global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_shrink(
+    AdaptRows a, const bf16_t *__restrict__ P, int64_t K, const bf16_t *__restrict__ Q, bool scaled, int ranges,
+    float *__restrict__ U) {
   constexpr int LD = RT * 16 + 4, PART = RT < 2 ? RT : 2;  // rank tiles that are in LDS at once
   constexpr int kOwn = 2048 * (1 + PART), kAll = kShrinkWaves * kOwn, kSums = kShrinkWaves * 16 * LD * 4;
   __shared__ __attribute__((aligned(128))) char shared[kAll > kSums ? kAll : kSums];
@@ -369,7 +404,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_sh
           next();
           if (i + kShrinkWaves < n) load((first + at) * 64);
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_order();
         if (j0 == 0)
 #pragma unroll
           for (int h = 0; h < 2; ++h) pf[h] = *reinterpret_cast<const u32x4_t *>(own + chunk_at(l, 4 * h + g));
@@ -379,7 +414,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_sh
           for (int h = 0; h < 2; ++h)
             acc[j0 + j] = mfma16(*reinterpret_cast<const u32x4_t *>(own + 2048 * (1 + j) + chunk_at(l, 4 * h + g)), pf[h],
                                  acc[j0 + j]);
-        __builtin_amdgcn_wave_barrier();
+        wave_order();
       }
     }
   }
@@ -498,7 +533,8 @@ __device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       bv[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (base && row0 + 16 * i < tile.n && n0 + col0 < end) bv[i] = ONCE ? load16_once(base + at[i] + n0) : load16(base + at[i] + n0);
+      if (base && row0 + 16 * i < tile.n && n0 + col0 < end)
+        bv[i] = ONCE ? load16_once(base + at[i] + n0) : load16(base + at[i] + n0);
     }
     if (rank)
 #pragma unroll
@@ -555,7 +591,7 @@ __device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs
       }
     if (n0 + kExpandCols < end) load(n0 + kExpandCols);
     if (rank) {
-      __builtin_amdgcn_wave_barrier();
+      wave_order();
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         u32x4_t qf[KQ];
@@ -612,7 +648,8 @@ __device__ __forceinline__ u32x4_t turned(const bf16_t *base, int ld, int row, i
   return u32x4_t{l2.x, l2.y, h2.x, h2.y};
 }
 
-constexpr int kGradCols = 64;  // per workgroup (128 take more registers for the sums: rank 64 23 us, else 17; rank 16 9.4, 8.8)
+// Columns of a workgroup (128 take more registers for the sums: rank 64 23 us, else 17; rank 16 9.4, else 8.8).
+constexpr int kGradCols = 64;
 template <int RT>
 struct GradShape {
   static constexpr int CW = kGradCols, LX = CW + 16, LV = RT * 16 + (RT > 1 ? 16 : 0);
@@ -625,8 +662,9 @@ struct GradShape {
 // BY_J: the output is [n][r] (dB), else [r][n] (dA).  The ranks from jb on, 16 RT of them.
 template <int RT, bool BY_J>
 __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile, int rank, int jb,
-                                           const float *__restrict__ V, int ranges, float scale, const bf16_t *__restrict__ X, int64_t N, int64_t c0,
-                                           float *__restrict__ part, bf16_t *__restrict__ grad, char *shared) {
+                                           const float *__restrict__ V, int ranges, float scale,
+                                           const bf16_t *__restrict__ X, int64_t N, int64_t c0, float *__restrict__ part,
+                                           bf16_t *__restrict__ grad, char *shared) {
   using S = GradShape<RT>;
   constexpr int CW = S::CW, LX = S::LX, LV = S::LV, XL = CW / 16, PT = CW / 16;  // XL: 16-byte loads of X per lane
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l = lane & 15;
@@ -694,7 +732,7 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
       load(tokens);
       tokens = tokens_of(t0 + 256);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
     const int row = 8 * g + (l >> 2), at = 4 * (l & 3);
     u32x4_t xv[PT];
 #pragma unroll
@@ -713,7 +751,7 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
         }
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
   }
   // the sums of two waves at a time, in the output's layout: [rank][column] or [column][rank]
   constexpr int LD = BY_J ? S::LD_B : S::LD_A;
@@ -813,7 +851,8 @@ __global__ __launch_bounds__(256) void k_adapt_reduce(AdaptRows a, AdaptGrads g,
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int q = 0; q < pieces; ++q) {
-    const float4 x = reinterpret_cast<const float4 *>(p + q * size)[0], y = reinterpret_cast<const float4 *>(p + q * size)[1];
+    const float4 *const at = reinterpret_cast<const float4 *>(p + q * size);
+    const float4 x = at[0], y = at[1];
     sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w, sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
   }
   store16((of_a ? g.dA : g.dB) + group * size + e, pack8(sum));
@@ -828,8 +867,16 @@ int64_t most_tiles(const AdaptRows &a, int M) {
 }  // namespace
 
 hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const AdaptTurn &t1, hipStream_t s) {
-  const int64_t b0 = turn_blocks(t0, a.n_pool), b1 = turn_blocks(t1, a.n_pool);
-  launch(k_adapt_plan, dim3((uint32_t)(1 + b0 + b1)), dim3(1024), 0, s, a, t0, t1, b0);
+  const int64_t b0 = turn_blocks(t0, a.n_pool), blocks = b0 + turn_blocks(t1, a.n_pool);
+  // (the largest pools have more blocks than a launch may have threads)
+  const int64_t chunks = a.T > 0 ? adapt_chunks(a.T) : 1;
+  launch(k_adapt_plan, dim3((uint32_t)(chunks + (blocks < 65536 ? blocks : 65536))), dim3(1024), 0, s, a, (int)chunks, t0, t1,
+         b0, blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_count(const AdaptRows &a, hipStream_t s) {
+  launch(k_adapt_count, dim3((uint32_t)adapt_chunks(a.T)), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

@@ -10,8 +10,9 @@
 // pieces at fixed places, so results repeat bit by bit.
 //   1. k_embed_order  ranks the positions against each other; the workgroups that have no positions to rank fill dW with
 //                     zeros, which takes longer, so the sort costs no time of its own where dW is large.
-//   2. k_embed_merge  (more than kOrderChunk positions) merges the sorted chunks.
-//   3. k_embed_sum    a wave adds a piece of the sorted list over 512 columns; a row that lies in one piece is written at once.
+//   2. k_embed_merge  (more than kOrderChunk positions) merges the sorted chunks, four at a time.
+//   3. k_embed_sum    a wave adds a piece of the sorted list over 512 columns; a row that lies in one piece is written at
+//                     once.
 //   4. k_embed_join   rows that were cut at the pieces' borders.
 #include "step.h"
 #include "step_device.h"
@@ -43,15 +44,14 @@ __global__ __launch_bounds__(256) void k_embed(const int64_t *__restrict__ token
 // the number of equal ones before it.  16 threads count for each position, a sixteenth of 2048 keys at a time, which all
 // read from LDS, two vector instructions per pair (8192 positions: 67 million pairs over the whole GPU, 6 us).
 constexpr int kRankItems = 16, kRankParts = 16, kRankKeys = 2048, kRankPart = kRankKeys / kRankParts;
-__device__ __forceinline__ void rank_chunk(const int64_t *__restrict__ tokens, int64_t T, int64_t V, int64_t block,
+__device__ __forceinline__ void rank_chunk(const int64_t *__restrict__ tokens, int64_t T, int64_t V, int64_t block, int chunk,
                                            int32_t *__restrict__ order, int32_t *__restrict__ key) {
   __shared__ __attribute__((aligned(16))) uint32_t s_key[kRankParts][kRankPart + 4];
   __shared__ uint32_t s_rank[kRankParts][kRankItems];
-  constexpr int64_t kBlocks = kOrderChunk / kRankItems;
-  const int64_t base = block / kBlocks * kOrderChunk;
-  const int n = (int)(T - base < kOrderChunk ? T - base : kOrderChunk);
+  const int64_t first = block * kRankItems, base = first & -(int64_t)chunk;  // (a power of two)
+  const int n = (int)(T - base < chunk ? T - base : chunk);
   const int tid = threadIdx.x, item = tid % kRankItems, part = tid / kRankItems;
-  const int i0 = (int)(block % kBlocks) * kRankItems, i = i0 + item;
+  const int i0 = (int)(first - base), i = i0 + item;
   auto key_of = [&](int at, int64_t v) {  // (behind the end: above every key)
     return at >= n ? 0xffffffffu : (uint64_t)v < (uint64_t)V ? (uint32_t)v : (uint32_t)V;
   };
@@ -70,7 +70,7 @@ __device__ __forceinline__ void rank_chunk(const int64_t *__restrict__ tokens, i
   for (int j0 = 0; j0 < n; j0 += kRankKeys) {
     if (j0) __syncthreads();
 #pragma unroll
-    for (int p = 0; p < kRankKeys / 256; ++p) 
+    for (int p = 0; p < kRankKeys / 256; ++p)
       s_key[(p * 256 + tid) / kRankPart][tid % kRankPart] = key_of(j0 + p * 256 + tid, next[p]);
     if (j0 + kRankKeys < n) load(j0 + kRankKeys);
     __syncthreads();
@@ -106,45 +106,47 @@ static_assert(kRankItems * kRankParts == 256 && 256 % kRankPart == 0 && kRankPar
 // The rest of the workgroups fill: one store per thread, which reaches 6.8 TB/s (1.05 GB in 154 us; workgroups that stay
 // for several stores 4.4 to 6.2, nontemporal stores 4.4).
 __global__ __launch_bounds__(256) void k_embed_order(const int64_t *__restrict__ tokens, int64_t T, int64_t V,
-                                                     int32_t *__restrict__ order, int32_t *__restrict__ key, int64_t blocks,
-                                                     bf16_t *__restrict__ fill, int64_t fill_n) {
+                                                     int chunk, int32_t *__restrict__ order, int32_t *__restrict__ key,
+                                                     int64_t blocks, bf16_t *__restrict__ fill, int64_t fill_n) {
   if (blockIdx.x < blocks) {
-    rank_chunk(tokens, T, V, blockIdx.x, order, key);
+    rank_chunk(tokens, T, V, blockIdx.x, chunk, order, key);
     return;
   }
   const int64_t e = ((int64_t)(blockIdx.x - blocks) * 256 + threadIdx.x) * 8;
   if (e < fill_n) store16(fill + e, u32x4_t{0u, 0u, 0u, 0u});
 }
 
-// First place in [0, n) whose key is not below k (UPPER: above k).
-template <bool UPPER>
-__device__ __forceinline__ int bound(const int32_t *__restrict__ key, int n, int k) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (UPPER ? key[mid] <= k : key[mid] < k) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
-
-// A place of a sorted chunk among all chunks: its place there plus, in each earlier chunk, the keys not above its own
-// and, in each later one, those below.
-__global__ __launch_bounds__(256) void k_embed_merge(int64_t T, const int32_t *__restrict__ order,
+// Merges sorted runs of `run` places (a power of two), four at a time: a place goes behind, in each earlier run of the
+// four, the keys not above its own and, in each later one, those below.  The four searches go in step, so that a step waits
+// for memory once.
+constexpr int kMergeRuns = 4;
+__global__ __launch_bounds__(256) void k_embed_merge(int64_t T, int64_t run, const int32_t *__restrict__ order,
                                                      const int32_t *__restrict__ key, int32_t *__restrict__ order_out,
                                                      int32_t *__restrict__ key_out) {
   const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (p >= T) return;
-  const int64_t own = p / kOrderChunk;
-  const int k = key[p];
-  int64_t at = p - own * kOrderChunk;
-  for (int64_t c = 0; c * kOrderChunk < T; ++c) {
-    const int64_t base = c * kOrderChunk;
-    const int n = (int)(T - base < kOrderChunk ? T - base : kOrderChunk);
-    if (c < own) at += bound<true>(key + base, n, k);
-    else if (c > own) at += bound<false>(key + base, n, k);
+  const int64_t own = p / run, first = own / kMergeRuns * kMergeRuns;
+  const int k = key[p], position = order[p];
+  const int32_t *from[kMergeRuns];
+  int n[kMergeRuns], limit[kMergeRuns], below[kMergeRuns];
+#pragma unroll
+  for (int c = 0; c < kMergeRuns; ++c) {
+    const int64_t base = (first + c) * run, left = T - base;
+    n[c] = first + c == own || left <= 0 ? 0 : (int)(left < run ? left : run);
+    from[c] = key + (n[c] ? base : p);
+    limit[c] = first + c < own ? k + 1 : k;
+    below[c] = 0;
   }
-  order_out[at] = order[p];
+  for (int step = (int)run; step; step >>= 1)
+#pragma unroll
+    for (int c = 0; c < kMergeRuns; ++c) {  // (the keys below the limit are the first of the run)
+      const int m = below[c] + step;
+      if (from[c][m <= n[c] ? m - 1 : 0] < limit[c] && m <= n[c]) below[c] = m;
+    }
+  int64_t at = first * run + (p - own * run);
+#pragma unroll
+  for (int c = 0; c < kMergeRuns; ++c) at += below[c];
+  order_out[at] = position;
   key_out[at] = k;
 }
 
@@ -298,18 +300,32 @@ hipError_t launch_embed(const int64_t *tokens, int64_t T, const bf16_t *W, int64
 // (Up to 32 tokens one piece, without a join; then enough pieces to fill the GPU.)
 int embed_piece(int64_t T) { return T <= kPieceMost ? kPieceMost : T <= 2048 ? 8 : T <= 8192 ? 16 : kPieceMost; }
 
+// Positions that are ranked against each other: ranking costs T x chunk, and up to four chunks take one pass of the merge
+// (131072 positions: ranked in 87 us 8192 at a time, in 29 us 2048 at a time with one pass more, which takes 7).
+static int64_t order_chunk(int64_t T) { return T <= kMergeRuns * kOrderChunk ? kOrderChunk : kOrderChunk / 4; }
+int embed_passes(int64_t T) {
+  int n = 0;
+  for (int64_t run = order_chunk(T); run < T; run *= kMergeRuns) ++n;
+  return n;
+}
+
+// (each pass goes from one pair of lists to the other, the last one to order and key)
 hipError_t launch_embed_order(const int64_t *tokens, int64_t T, int64_t V, const Order &o, bf16_t *fill, int64_t fill_n,
                               hipStream_t s) {
   const int64_t blocks = (T + kRankItems - 1) / kRankItems, fills = (fill_n + 2047) / 2048;
-  const bool merged = T > kOrderChunk;
-  launch(k_embed_order, dim3((uint32_t)(blocks + fills)), dim3(256), 0, s, tokens, T, V,
-         merged ? o.order2 : o.order, merged ? o.key2 : o.key, blocks, fill, fill_n);
+  const bool second = embed_passes(T) & 1;
+  launch(k_embed_order, dim3((uint32_t)(blocks + fills)), dim3(256), 0, s, tokens, T, V, (int)order_chunk(T),
+         second ? o.order2 : o.order, second ? o.key2 : o.key, blocks, fill, fill_n);
   return hipGetLastError();
 }
 
-hipError_t launch_embed_merge(int64_t T, const Order &o, hipStream_t s) {
-  launch(k_embed_merge, dim3((uint32_t)((T + 255) / 256)), dim3(256), 0, s, T, (const int32_t *)o.order2,
-         (const int32_t *)o.key2, o.order, o.key);
+hipError_t launch_embed_merge(int64_t T, int pass, const Order &o, hipStream_t s) {
+  int64_t run = order_chunk(T);
+  for (int i = 0; i < pass; ++i) run *= kMergeRuns;
+  const bool second = (embed_passes(T) - pass) & 1;
+  launch(k_embed_merge, dim3((uint32_t)((T + 255) / 256)), dim3(256), 0, s, T, run,
+         (const int32_t *)(second ? o.order2 : o.order), (const int32_t *)(second ? o.key2 : o.key),
+         second ? o.order : o.order2, second ? o.key : o.key2);
   return hipGetLastError();
 }
 

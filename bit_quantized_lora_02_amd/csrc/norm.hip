@@ -42,11 +42,11 @@ __device__ __forceinline__ float row_sum(float x, float *at, int wave) {
   return s;
 }
 
-// A workgroup of NT threads takes rows blockIdx.x, + gridDim.x, ..; a thread holds C chunks of 8 columns.
+// A workgroup of NT threads takes rows blockIdx.x, + gridDim.x, ..; a thread holds C chunks of 8 columns.  Y may be X.
 template <int NT, int C, bool F32>
-__global__ __launch_bounds__(NT) void k_norm(const bf16_t *__restrict__ X, int64_t T, int64_t D,
-                                             const void *__restrict__ w, const void *__restrict__ b, float eps,
-                                             bf16_t *__restrict__ Y, float *__restrict__ mean, float *__restrict__ rstd) {
+__global__ __launch_bounds__(NT) void k_norm(const bf16_t *X, int64_t T, int64_t D, const void *__restrict__ w,
+                                             const void *__restrict__ b, float eps, bf16_t *Y, float *__restrict__ mean,
+                                             float *__restrict__ rstd) {
   __shared__ float s_sum[4][NT / 64];
   const int tid = threadIdx.x, wave = tid >> 6;
   bool in[C];

@@ -10,10 +10,10 @@ namespace qlora {
 
 // Rows by key: order[p] is the row at place p of the rows sorted by key, equal keys by row; key[p] its key.  A key
 // outside [0, n_keys) counts as n_keys and comes last.
-constexpr int64_t kOrderChunk = 8192;  // rows that are ranked against each other; longer lists merge such chunks
+constexpr int64_t kOrderChunk = 8192;  // rows that are ranked against each other at most; longer lists merge sorted chunks
 struct Order {
   int32_t *order = nullptr, *key = nullptr;    // [T]
-  int32_t *order2 = nullptr, *key2 = nullptr;  // [T], of the chunks before they are merged (T > kOrderChunk only)
+  int32_t *order2 = nullptr, *key2 = nullptr;  // [T], others between passes of the merge (T > kOrderChunk only)
 };
 
 // Embedding.
@@ -23,7 +23,8 @@ hipError_t launch_embed(const int64_t *tokens, int64_t T, const bf16_t *W, int64
 int embed_piece(int64_t T);
 hipError_t launch_embed_order(const int64_t *tokens, int64_t T, int64_t V, const Order &o, bf16_t *fill, int64_t fill_n,
                               hipStream_t s);
-hipError_t launch_embed_merge(int64_t T, const Order &o, hipStream_t s);
+int embed_passes(int64_t T);  // of the merge
+hipError_t launch_embed_merge(int64_t T, int pass, const Order &o, hipStream_t s);
 hipError_t launch_embed_sum(const Order &o, int64_t T, const bf16_t *dY, int64_t V, int64_t D, float scale, bool add,
                             bf16_t *dW, float *part, hipStream_t s);
 hipError_t launch_embed_join(const Order &o, int64_t T, int64_t V, int64_t D, float scale, bool add, bf16_t *dW,
@@ -46,6 +47,8 @@ hipError_t launch_norm_reduce(const float *part, int groups, int64_t D, bool f32
 constexpr int kPoolMax = 1000;
 constexpr int64_t kAdaptSmall = 64;  // up to so many tokens the forward's workgroups group them by themselves
 constexpr int64_t kAdaptFew = 128;   // tokens of a backward whose last two products are one launch
+constexpr int64_t kAdaptChunk = 8192;  // tokens that one workgroup groups
+__host__ __device__ inline int64_t adapt_chunks(int64_t T) { return (T + kAdaptChunk - 1) / kAdaptChunk; }
 struct AdaptRows {
   const int32_t *index = nullptr;  // [T] adapter of each token
   int64_t T = 0;
@@ -53,6 +56,7 @@ struct AdaptRows {
   const int32_t *rank = nullptr;   // [n_pool] or null (r)
   const float *scale = nullptr;    // [n_pool]
   int32_t *order = nullptr, *start = nullptr;  // [T], [n_pool + 2]; null: at most kAdaptSmall tokens
+  int32_t *counts = nullptr;                   // [chunks][n_pool + 1]; null: one chunk
 };
 // Groups the tokens and, for each non-null `to`, transposes a pool: from [n_pool][rows][cols] to [n_pool][cols][rows].
 struct AdaptTurn {
@@ -60,6 +64,7 @@ struct AdaptTurn {
   bf16_t *to = nullptr;
   int64_t rows = 0, cols = 0;
 };
+hipError_t launch_adapt_count(const AdaptRows &a, hipStream_t s);  // the counts, before the plan
 hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const AdaptTurn &t1, hipStream_t s);
 // U[split][t][j] = (scale) P[t] . Q_a[j] over a range of K, Q [n_pool][r][K]: ranges of K (their sums come apart).
 int adapt_ranges(int64_t T, int n_pool, int64_t K);

@@ -68,7 +68,8 @@ int check_norm(int64_t T, int64_t D, int weights) {
   if (int rc = check_tokens(T)) return rc;
   if (D < 8 || D > kNormMax || D % 8 != 0)
     return fail(QLORA_EINVAL, "n_in must be a multiple of 8 in [8, %d] (got %lld)", (int)kNormMax, (long long)D);
-  if (T * D >= (int64_t)1 << 32) return fail(QLORA_EINVAL, "T x n_in must be below 2^32 (got %lld x %lld)", (long long)T, (long long)D);
+  if (T * D >= (int64_t)1 << 32)
+    return fail(QLORA_EINVAL, "T x n_in must be below 2^32 (got %lld x %lld)", (long long)T, (long long)D);
   if (weights != QLORA_WEIGHT_BF16 && weights != QLORA_WEIGHT_F32)
     return fail(QLORA_EINVAL, "weight_type must be QLORA_WEIGHT_BF16 or QLORA_WEIGHT_F32 (got %d)", weights);
   return QLORA_OK;
@@ -78,9 +79,10 @@ int check_norm(int64_t T, int64_t D, int weights) {
 int check_adapters(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32_t r) {
   if (int rc = check_tokens(T)) return rc;
   if (n_in < 8 || n_in > kMaxDim || n_in % 8 || n_out < 8 || n_out > kMaxDim || n_out % 8)
-    return fail(QLORA_EINVAL, "n_in and n_out must be positive multiples of 8, at most 2^22 (got %lld, %lld)", (long long)n_in,
-                (long long)n_out);
-  if (n_pool < 1 || n_pool > kPoolMax) return fail(QLORA_EINVAL, "n_pool must be in [1, %d] (got %d)", kPoolMax, (int)n_pool);
+    return fail(QLORA_EINVAL, "n_in and n_out must be positive multiples of 8, at most 2^22 (got %lld, %lld)",
+                (long long)n_in, (long long)n_out);
+  if (n_pool < 1 || n_pool > kPoolMax)
+    return fail(QLORA_EINVAL, "n_pool must be in [1, %d] (got %d)", kPoolMax, (int)n_pool);
   if (r < 8 || r > QLORA_MAX_RANK || r % 8)
     return fail(QLORA_EINVAL, "r must be a multiple of 8 in [8, %d] (got %d)", QLORA_MAX_RANK, (int)r);
   if (n_pool * n_in > (int64_t)1 << 27 || n_pool * n_out > (int64_t)1 << 27)
@@ -92,7 +94,7 @@ int check_adapters(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32
 
 struct AdaptPlan {
   int ranges_u = 1, ranges_du = 1, piece = 0;
-  size_t order = 0, start = 0, u = 0, du = 0, du_sum = 0, at = 0, bt = 0, part_a = 0, part_b = 0, total = 0;
+  size_t order = 0, start = 0, counts = 0, u = 0, du = 0, du_sum = 0, at = 0, bt = 0, part_a = 0, part_b = 0, total = 0;
 };
 
 AdaptPlan adapt_plan(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int32_t r, bool backward) {
@@ -100,6 +102,7 @@ AdaptPlan adapt_plan(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int
   Parts w;
   p.order = w.take((size_t)T * 4);
   p.start = w.take((size_t)(n_pool + 2) * 4);
+  if (T > kAdaptChunk) p.counts = w.take((size_t)adapt_chunks(T) * (n_pool + 1) * 4);
   p.ranges_u = adapt_ranges(T, n_pool, n_in);
   p.u = w.take((size_t)p.ranges_u * T * r * 4);
   if (backward) {
@@ -121,7 +124,8 @@ int check_pool(const void *X, const void *A, const void *B, const int32_t *rank,
                int64_t T) {
   if (!A || !B || !scale) return fail(QLORA_EINVAL, "A_pool, B_pool and scale must not be NULL");
   if (T > 0 && (!X || !index)) return fail(QLORA_EINVAL, "X and index must not be NULL");
-  if (!aligned16(X) || !aligned16(A) || !aligned16(B)) return fail(QLORA_EINVAL, "X, A_pool and B_pool must be 16-byte aligned");
+  if (!aligned16(X) || !aligned16(A) || !aligned16(B))
+    return fail(QLORA_EINVAL, "X, A_pool and B_pool must be 16-byte aligned");
   if (!aligned_to(rank, 4) || !aligned_to(scale, 4) || !aligned_to(index, 4))
     return fail(QLORA_EINVAL, "rank, scale and index must be 4-byte aligned");
   return QLORA_OK;
@@ -165,6 +169,10 @@ int qlora_adapters_fwd(const qlora_bf16 *X, int64_t T, int64_t n_in, const qlora
   if (T > kAdaptSmall) {
     a.order = (int32_t *)(w + p.order);
     a.start = (int32_t *)(w + p.start);
+    if (T > kAdaptChunk) {
+      a.counts = (int32_t *)(w + p.counts);
+      LAUNCH("adapters_count", launch_adapt_count(a, s));
+    }
     LAUNCH("adapters_plan", launch_adapt_plan(a, AdaptTurn(), AdaptTurn(), s));
   }
   const bool direct = U_out && p.ranges_u == 1;
@@ -213,6 +221,10 @@ int qlora_adapters_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, int
     tb.to = (bf16_t *)(w + p.bt);
     tb.rows = n_out;
     tb.cols = r;
+  }
+  if (T > kAdaptChunk) {
+    a.counts = (int32_t *)(w + p.counts);
+    LAUNCH("adapters_count", launch_adapt_count(a, s));
   }
   LAUNCH("adapters_plan", launch_adapt_plan(a, ta, tb, s));
   AdaptGrads g;
@@ -299,7 +311,7 @@ int qlora_embed_bwd(const int64_t *tokens, const qlora_bf16 *dY, int64_t T, int6
   if (T > 0 || !add)
     LAUNCH("embed_order", launch_embed_order(tokens, T, n_vocab, o, dW, add ? 0 : n_vocab * n_in, s));
   if (T == 0) return QLORA_OK;
-  if (T > kOrderChunk) LAUNCH("embed_merge", launch_embed_merge(T, o, s));
+  for (int pass = 0; pass < embed_passes(T); ++pass) LAUNCH("embed_merge", launch_embed_merge(T, pass, o, s));
   LAUNCH("embed_sum", launch_embed_sum(o, T, dY, n_vocab, n_in, scale, add, dW, part, s));
   if (T > embed_piece(T)) LAUNCH("embed_join", launch_embed_join(o, T, n_vocab, n_in, scale, add, dW, part, s));
   return QLORA_OK;

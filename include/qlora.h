@@ -511,7 +511,7 @@ int qlora_adapters_fwd(const qlora_bf16 *X, int64_t T, int64_t n_in, const qlora
  * completely, with zeros past the ranks and for adapters without tokens (T = 0: everywhere).  Each of dX, dA and dB may be
  * NULL (not formed).  u and du stay binary32 and enter the products as two bf16 parts; sums run in a fixed order.
  * ws: qlora_adapters_workspace_bytes(..., 1): the tokens in groups, u and du, both pools transposed, and binary32 sums of
- * pieces of 64 to 1024 tokens.
+ * pieces of 128 to 1024 tokens.
  */
 int qlora_adapters_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, int64_t n_in, const qlora_bf16 *A_pool,
                        const qlora_bf16 *B_pool, int64_t n_out, int32_t n_pool, int32_t r, const int32_t *rank,

@@ -317,3 +317,50 @@ def test_graph_replays(T):
         got = [t.clone() for t in out]
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, step())), f"replay {i}"
+
+
+def test_rows_beyond_four_gib():
+    """Offsets past 2^32 bytes of Y, dY, X and dX: rows at the ends against a call on those rows alone."""
+    T, N, K, r = 66000, 32776, 64, 8
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").to(bf)  # noqa: E731
+    X, A, Bp = rn(T, K), rn(2, r, K), rn(2, N, r)
+    scale = torch.tensor([0.5, 2.0], device="cuda")
+    index = (torch.arange(T, device="cuda", dtype=torch.int32) // 7) % 3 - 1
+    at = torch.tensor([0, 1, 65000, 65534, 65535, 65536, T - 9, T - 1], device="cuda")
+    Y, u = B.adapters_fwd(X, A, Bp, scale, index)
+    few, u_few = B.adapters_fwd(X[at], A, Bp, scale, index[at])
+    assert torch.equal(u[at], u_few) and torch.equal(Y[at], few)
+    dX, dA, dB = B.adapters_bwd(X, Y, A, Bp, scale, index, U=u)
+    few = B.adapters_bwd(X[at], Y[at].contiguous(), A, Bp, scale, index[at])[0]
+    # (both round dX once, each by at most BF of it; du of few tokens is added from ranges of n_out, binary32 sums in
+    # another order, which move dX by less than a tenth of that)
+    rel = float((dX[at].double() - few.double()).norm() / few.double().norm())
+    assert rel <= 2.1 * BF and torch.isfinite(dA.float()).all() and torch.isfinite(dB.float()).all()
+    # the same adapters the other way round: the wide side is the input
+    del dX, dA, dB
+    A2, B2 = rn(2, r, N), rn(2, K, r)
+    Z, v = B.adapters_fwd(Y, A2, B2, scale, index)
+    few, v_few = B.adapters_fwd(Y[at].contiguous(), A2, B2, scale, index[at])
+    assert float((v[at].double() - v_few.double()).norm() / v_few.double().norm()) <= depth(N) and Z.shape == (T, K)
+    dX = B.adapters_bwd(Y, Z, A2, B2, scale, index, U=v, need_dw=False)[0]
+    few = B.adapters_bwd(torch.zeros(len(at), N, dtype=bf, device="cuda"), Z[at], A2, B2, scale, index[at])[0]
+    assert torch.equal(dX[at], few)
+
+
+def test_pools_of_many_blocks():
+    """Pools that are transposed in more blocks than one launch has workgroups."""
+    T, K, N, pool, r = 200, 8192, 8192, 1000, 8
+    assert pool * (K // 128 + N // 64) > 65536
+    s = make(T, K, N, pool, r, "any", False, 3)
+    want, bounds = reference(s, "cuda")
+    g = {k: s[k].cuda() for k in ("X", "dY", "A", "B", "scale", "index", "dbase")}
+    got = B.adapters_bwd(g["X"], g["dY"], g["A"], g["B"], g["scale"], g["index"], U=want[1].float(), base=g["dbase"])
+    for name, x, y, b in zip(("dX", "dA", "dB"), got, want[2:], bounds[2:]):
+        check(name, x, y, b)
+
+
+@pytest.mark.parametrize("T,pool,kind", [(8192, 5, "any"), (8193, 1000, "any"), (40000, 1000, "any"), (70001, 3, "runs")])
+def test_many_tokens(T, pool, kind):
+    """Tokens that one workgroup, and several, bring into groups."""
+    test_adapters(T, 16, 8, pool, 8, kind, True)

@@ -118,6 +118,13 @@ def test_embedding(T, V, D, kind):
     assert torch.isnan(got[~named]).all()
 
 
+@pytest.mark.parametrize("T,V,D,kind", [(32768, 700, 16, "any"), (32769, 9000, 16, "any"), (131072, 40, 8, "runs"),
+                                        (140001, 30000, 16, "any")])
+def test_embedding_of_many_tokens(T, V, D, kind):
+    """Lists that are merged in one, three and four passes."""
+    test_embedding(T, V, D, kind)
+
+
 def test_embedding_of_no_tokens():
     t = torch.zeros(0, dtype=torch.int64, device="cuda")
     dY = torch.zeros(0, 64, dtype=bf, device="cuda")
@@ -337,3 +344,26 @@ def test_graph_replays():
         got = [t.clone() for t in out]
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, step())), f"replay {i}"
+
+
+def test_rows_beyond_four_gib():
+    """Offsets past 2^32 bytes of looked up and normed rows and of their gradients; the last rows against the definitions."""
+    T, D, V = 70000, 32768, 100
+    g = torch.Generator(device="cuda").manual_seed(0)
+    W = torch.randn(V, D, generator=g, device="cuda").to(bf)
+    tokens = torch.arange(T, device="cuda") % V
+    E = B.embed(tokens, W)
+    at = torch.tensor([0, 1, 65535, 65536, 65537, T - 2, T - 1], device="cuda")
+    assert torch.equal(E[at], W[tokens[at]])
+    w, b = 1 + 0.1 * torch.randn(D, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda")
+    Y, mean, rstd = B.layer_norm(E, w, b)
+    y, m, r, e_y, e_m, e_r = norm_reference(E[at].cpu(), w.cpu(), b.cpu(), 1e-5)
+    check("Y", Y[at], y, e_y)
+    check("rstd", rstd[at], r, e_r)
+    dY = Y[at].cpu()
+    dX, _, _ = B.layer_norm_bwd(E, Y, w, mean, rstd, outs=(Y, None, None))
+    want, bounds = norm_bwd_reference(E[at].cpu(), dY, w.cpu(), mean[at].cpu(), rstd[at].cpu(), True)
+    check("dX", dX[at], want[0], bounds[0])
+    dW = B.embed_bwd(tokens, E, V)
+    n = torch.bincount(tokens, minlength=V).double()[:, None]
+    check("dW", dW, n * W.double(), (n + 2) * U * n * W.double().abs() + BF * n * W.double().abs())
