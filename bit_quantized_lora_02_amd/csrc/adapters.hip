@@ -471,14 +471,16 @@ __device__ __forceinline__ void load_u(const AdaptRows &a, const float *__restri
 // and output are read and written 256 bytes of a row at a time: from the MFMA's layout (64 bytes of 16 tokens each)
 // a copy alone reached 3.9 to 4.9 TB/s, in such pieces 5.8.
 constexpr int kExpandCols = 128;
-// ONCE: the base goes past the caches.
+// ONCE: the base goes past the caches.  LINES: output and base in whole lines of memory where rows do not begin with one: a
+// row goes `back` columns behind the products, to where a line begins, and what is left of a step's products waits in
+// registers for the next one (4096 tokens x 14344, rank 64 66 us, else 89; x 14336 56).
 struct ExpandArgs {
   const float *U;
   int ranges;
   const bf16_t *Q;
   int64_t N;
   bool scaled;
-  int64_t per;  // columns of a block
+  int64_t per;  // columns of a block, a multiple of 128
   int blocks;
   const bf16_t *base;
   bf16_t *out;
@@ -492,7 +494,7 @@ struct ExpandShared {
   char mem[kOut > kParts ? kOut : kParts];
   int token[TOKENS];
 };
-template <int KS, int MT, bool ONCE>
+template <int KS, int MT, bool ONCE, bool LINES>
 __device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs &x, int at_block, char *shared) {
   using S = ExpandShared<KS, MT>;
   constexpr int CP = S::CP, KQ = KS ? KS : 1, TOKENS = S::TOKENS;
@@ -523,9 +525,19 @@ __device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs
   // rows as they lie in memory: a thread's 8 columns of every 16th token; its chunks of the wave's 32 rows of Q.  The first
   // step's are on their way before u is, and each next step's before the present one is stored.
   const int row0 = tid >> 4, col0 = (tid & 15) * 8;
+  const int64_t stop = LINES ? end + kExpandCols : end;
   int64_t at[MT];
+  int back[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) at[i] = (int64_t)s_token[row0 + 16 * i] * N + col0;
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = (int64_t)s_token[row0 + 16 * i] * N;
+    back[i] = LINES ? (int)((uintptr_t)(out + row) >> 4 & 7) * 8 : 0;
+    at[i] = row + col0 - back[i];
+  }
+  auto mine = [&](int i, int64_t n0) {
+    const int64_t n = n0 + col0 - back[i];
+    return row0 + 16 * i < tile.n && (!LINES || n >= first) && n < end;
+  };
   const char *const q = (const char *)(x.Q + (int64_t)(rank ? tile.group : 0) * N * a.r);
   char *const own = sh.q[wave];
   u32x4_t bv[MT], qv[CP / 2];
@@ -533,10 +545,10 @@ __device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       bv[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (base && row0 + 16 * i < tile.n && n0 + col0 < end)
+      if (base && mine(i, n0))
         bv[i] = ONCE ? load16_once(base + at[i] + n0) : load16(base + at[i] + n0);
     }
-    if (rank)
+    if (rank && n0 < end)
 #pragma unroll
       for (int i = 0; i < CP / 2; ++i) {  // (behind the last row: any row, whose products are not stored)
         const int r = i * (64 / CP) + lane / CP, c = lane % CP;
@@ -579,18 +591,20 @@ __device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs
     }
   __syncthreads();
   const bool full = rank == CP * 8;
-  for (int64_t n0 = first; n0 < end; n0 += kExpandCols) {
+  f32x4_t left[MT][2] = {};
+  for (int64_t n0 = first; n0 < stop; n0 += kExpandCols) {
     u32x4_t now[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) now[i] = bv[i];
-    if (rank)
+    const bool products = rank && (!LINES || n0 < end);
+    if (products)
 #pragma unroll
       for (int i = 0; i < CP / 2; ++i) {
         const int r = i * (64 / CP) + lane / CP, c = lane % CP;
         *reinterpret_cast<u32x4_t *>(own + swizzled(r, c)) = full ? qv[i] : below_rank(qv[i], rank - c * 8);
       }
-    if (n0 + kExpandCols < end) load(n0 + kExpandCols);
-    if (rank) {
+    if (n0 + kExpandCols < stop) load(n0 + kExpandCols);
+    if (products) {
       wave_order();
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -612,27 +626,34 @@ __device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs
       __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-      if (row0 + 16 * i < tile.n && n0 + col0 < end) {
+    for (int i = 0; i < MT; ++i) {
+      const f32x4_t *d = reinterpret_cast<const f32x4_t *>(&s_out[row0 + 16 * i][(col0 - back[i]) & (kExpandCols - 1)]);
+      f32x4_t d0, d1;
+      if (LINES) {
+        const f32x4_t v0 = d[0], v1 = d[1];  // (behind the last step nothing new, which nothing takes)
+        d0 = col0 < back[i] ? left[i][0] : v0, d1 = col0 < back[i] ? left[i][1] : v1;
+        left[i][0] = v0, left[i][1] = v1;
+      }
+      if (mine(i, n0)) {
         if (rank) {
+          if (!LINES) d0 = d[0], d1 = d[1];
           float y[8];
           unpack8(now[i], y);
-          const f32x4_t *d = reinterpret_cast<const f32x4_t *>(&s_out[row0 + 16 * i][col0]);
-          const f32x4_t d0 = d[0], d1 = d[1];
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] += d0[e], y[4 + e] += d1[e];
           now[i] = pack8(y);
         }
         store16_once(out + at[i] + n0, now[i]);
       }
-    if (rank) __syncthreads();
+    }
+    if (products) __syncthreads();
   }
 }
 
-template <int KS, int MT, bool ONCE>
+template <int KS, int MT, bool ONCE, bool LINES>
 __global__ __launch_bounds__(256, KS * MT <= 4 ? 4 : 2) void k_adapt_expand(AdaptRows a, ExpandArgs x) {
   __shared__ __attribute__((aligned(128))) char shared[sizeof(ExpandShared<KS, MT>)];
-  expand_tile<KS, MT, ONCE>(a, x, blockIdx.x, shared);
+  expand_tile<KS, MT, ONCE, LINES>(a, x, blockIdx.x, shared);
 }
 
 // ---------------------------------------------------------------------- grads
@@ -800,12 +821,15 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
 // all of them in one, and one workgroup per CU, 95 us; so 80).
 struct GradArgs {
   AdaptGrads g;
-  int piece, parts, blocks_a, blocks;  // blocks: of a piece, parts for each 64 columns, of X first
+  int piece, parts, blocks_a, columns, blocks;  // columns: blocks of 64, of X first; blocks: of a piece, in all
 };
 template <int RT>
 __device__ __forceinline__ void grads_tile(const AdaptRows &a, const GradArgs &q, int at_block, char *shared) {
   const int id = at_block / q.blocks, rest = at_block - id * q.blocks;
-  const int block = rest / q.parts, jb = (rest - block * q.parts) * 64;
+  // (the parts of a block of columns come eight workgroups apart, on one XCD: the columns are then in its L2)
+  const int eights = rest / (8 * q.parts), in = rest - eights * 8 * q.parts;
+  const int block = q.parts == 1 ? rest : eights * 8 + (in & 7), jb = q.parts == 1 ? 0 : (in >> 3) * 64;
+  if (block >= q.columns) return;
   Tile tile;
   if (!find_tile<true>(a, q.piece, id, &tile)) return;
   const int rank = rank_of(a, tile.group);
@@ -828,7 +852,7 @@ template <int KS, int RT>
 __global__ __launch_bounds__(256) void k_adapt_back(AdaptRows a, ExpandArgs x, GradArgs q, int expand_blocks) {
   constexpr int kExpand = sizeof(ExpandShared<KS, 1>), kGrads = GradShape<RT>::kAll;
   __shared__ __attribute__((aligned(128))) char shared[kExpand > kGrads ? kExpand : kGrads];
-  if ((int)blockIdx.x < expand_blocks) expand_tile<KS, 1, false>(a, x, blockIdx.x, shared);
+  if ((int)blockIdx.x < expand_blocks) expand_tile<KS, 1, false, false>(a, x, blockIdx.x, shared);
   else grads_tile<RT>(a, q, blockIdx.x - expand_blocks, shared);
 }
 
@@ -880,9 +904,14 @@ hipError_t launch_adapt_count(const AdaptRows &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-int adapt_ranges(int64_t T, int n_pool, int64_t K) {
+// Enough workgroups for the GPU, but no more partial sums than that takes, which the next product adds for each of its
+// blocks of columns (4096 x 4096: 1200 tokens, rank 64 22.7 us with three ranges, 25.5 with nine; 2048 29.3 with
+// two, 32.6 with five; 4096 42.9 with two, 44.2 with one).  Above rank 64 a CU holds one workgroup of the shrinking product,
+// and a second round of them costs as much as the first (4000 tokens, rank 128 49 us with one range, 61 with two).
+int adapt_ranges(int64_t T, int n_pool, int r, int64_t K) {
   const int64_t tiles = (T + 15) / 16 + (n_pool < T ? n_pool : T) / 2, most = (K + 511) / 512;
-  int64_t n = tiles < 1 ? 1 : 768 / tiles;
+  int64_t n = tiles < 1 ? 1 : (r > 32 ? 256 : 512) / tiles;
+  if (n < 2 && r <= 64 && tiles <= 384) n = 2;
   n = n < 1 ? 1 : n > 8 ? 8 : n;
   return (int)(n < most ? n : most);
 }
@@ -923,8 +952,9 @@ ExpandArgs expand_args(const AdaptRows &a, bool wide, const float *U, int ranges
 GradArgs grad_args(const AdaptRows &a, const AdaptGrads &g, int piece, int64_t *grid) {
   const int64_t ba = g.dA ? (g.n_in + kGradCols - 1) / kGradCols : 0, bb = g.dB ? (g.n_out + kGradCols - 1) / kGradCols : 0;
   const int parts = (a.r + 63) / 64;
-  *grid = (ba + bb) * parts * (a.T / piece + a.n_pool);
-  return GradArgs{g, piece, parts, (int)ba, (int)(ba + bb) * parts};
+  const int64_t blocks = parts > 1 ? (ba + bb + 7) / 8 * 8 * parts : ba + bb;
+  *grid = blocks * (a.T / piece + a.n_pool);
+  return GradArgs{g, piece, parts, (int)ba, (int)(ba + bb), (int)blocks};
 }
 }  // namespace
 
@@ -936,18 +966,26 @@ hipError_t launch_adapt_expand(const AdaptRows &a, const float *U, int ranges, c
   // A base that the caches cannot hold beside the rest goes past them (4096 x 14336, 117 MB: the call 79 us, else 84; of
   // 25 MB, just written, 19 us of the kernel, else 14).
   const bool once = a.T * N * 2 > (int64_t)64 << 20;
+  // (what the L2s hold is put together there: 5703 x 2704 takes 17.6 us either way, 3001 x 1000 13.4, with LINES 15.0)
+  const bool lines = (N % 64 != 0 || ((uintptr_t)out & 127) != 0) && a.T * N * 2 > (int64_t)32 << 20;
   const dim3 grid((uint32_t)blocks), block(256);
-#define EXPAND(KS_)                                                                   \
-  do {                                                                                \
-    if (wide && once) launch(k_adapt_expand<KS_, 2, true>, grid, block, 0, s, a, x);  \
-    else if (wide) launch(k_adapt_expand<KS_, 2, false>, grid, block, 0, s, a, x);    \
-    else launch(k_adapt_expand<KS_, 1, false>, grid, block, 0, s, a, x);              \
+#define EXPAND_(KS_, MT_, ONCE_)                                                               \
+  do {                                                                                         \
+    if (lines) launch(k_adapt_expand<KS_, MT_, ONCE_, true>, grid, block, 0, s, a, x);         \
+    else launch(k_adapt_expand<KS_, MT_, ONCE_, false>, grid, block, 0, s, a, x);              \
+  } while (0)
+#define EXPAND(KS_)                            \
+  do {                                         \
+    if (wide && once) EXPAND_(KS_, 2, true);   \
+    else if (wide) EXPAND_(KS_, 2, false);     \
+    else EXPAND_(KS_, 1, false);               \
   } while (0)
   if (a.r <= 16) EXPAND(0);
   else if (a.r <= 32) EXPAND(1);
   else if (a.r <= 64) EXPAND(2);
   else EXPAND(4);
 #undef EXPAND
+#undef EXPAND_
   return hipGetLastError();
 }
 

@@ -67,7 +67,7 @@ struct AdaptTurn {
 hipError_t launch_adapt_count(const AdaptRows &a, hipStream_t s);  // the counts, before the plan
 hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const AdaptTurn &t1, hipStream_t s);
 // U[split][t][j] = (scale) P[t] . Q_a[j] over a range of K, Q [n_pool][r][K]: ranges of K (their sums come apart).
-int adapt_ranges(int64_t T, int n_pool, int64_t K);
+int adapt_ranges(int64_t T, int n_pool, int r, int64_t K);
 hipError_t launch_adapt_shrink(const AdaptRows &a, const bf16_t *P, int64_t K, const bf16_t *Q, bool scaled, int ranges,
                                float *U, hipStream_t s);
 // out[t] = bf16(base[t] + (scale) U[t] . Q_a^T), Q [n_pool][N][r], U the sum of its ranges (also to U_out unless null).

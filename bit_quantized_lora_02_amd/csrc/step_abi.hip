@@ -103,10 +103,10 @@ AdaptPlan adapt_plan(int64_t T, int64_t n_in, int64_t n_out, int32_t n_pool, int
   p.order = w.take((size_t)T * 4);
   p.start = w.take((size_t)(n_pool + 2) * 4);
   if (T > kAdaptChunk) p.counts = w.take((size_t)adapt_chunks(T) * (n_pool + 1) * 4);
-  p.ranges_u = adapt_ranges(T, n_pool, n_in);
+  p.ranges_u = adapt_ranges(T, n_pool, r, n_in);
   p.u = w.take((size_t)p.ranges_u * T * r * 4);
   if (backward) {
-    p.ranges_du = adapt_ranges(T, n_pool, n_out);
+    p.ranges_du = adapt_ranges(T, n_pool, r, n_out);
     p.du = w.take((size_t)p.ranges_du * T * r * 4);
     p.du_sum = p.ranges_du > 1 ? w.take((size_t)T * r * 4) : p.du;
     p.at = w.take((size_t)n_pool * r * n_in * 2);

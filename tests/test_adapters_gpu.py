@@ -364,3 +364,33 @@ def test_pools_of_many_blocks():
 def test_many_tokens(T, pool, kind):
     """Tokens that one workgroup, and several, bring into groups."""
     test_adapters(T, 16, 8, pool, 8, kind, True)
+
+
+@pytest.mark.parametrize("T,N,r,off", [(1500, 12008, 16, 0), (2500, 8072, 40, 0), (2100, 16200, 24, 0), (2100, 16384, 128, 8),
+                                       (3000, 6008, 72, 24), (1200, 14400, 8, 40)])
+def test_large_outputs_of_odd_widths(T, N, r, off):
+    """Outputs past the caches whose rows do not begin with a line of memory, with and without a base, and over it."""
+    print(f"adapters T={T} N={N} r={r} output {2 * off} bytes off a line", flush=True)
+    K = 72
+    s = make(T, K, N, 3, r, "any", True, N + r)
+    want, bounds = reference(s, "cuda")
+    g = {k: s[k].cuda() for k in ("X", "dY", "A", "B", "scale", "index", "rank", "base")}
+    pools = (g["A"], g["B"], g["scale"], g["index"], g["rank"])
+    plain = want[0] - g["base"].double()
+    for base in (None, g["base"]):
+        whole = torch.full((off + T * N + 64,), 7.0, dtype=bf, device="cuda")
+        out = whole[off:off + T * N].view(T, N)
+        B.adapters_fwd(g["X"], *pools, base=base, out=out)
+        torch.cuda.synchronize()
+        assert (whole[:off] == 7).all() and (whole[off + T * N:] == 7).all()
+        check("Y", out, plain if base is None else want[0], bounds[0] + (BF * plain.abs() if base is None else 0))
+    whole[off:off + T * N] = g["base"].view(-1)
+    B.adapters_fwd(g["X"], *pools, base=out, out=out)
+    check("Y over base", out, want[0], bounds[0])
+    # the same as dX, whose wide side is n_in
+    s2 = make(T, N, K, 3, r, "runs", True, N)
+    want, bounds = reference(s2, "cuda")
+    g = {k: s2[k].cuda() for k in ("X", "dY", "A", "B", "scale", "index", "rank", "dbase")}
+    got = B.adapters_bwd(g["X"], g["dY"], g["A"], g["B"], g["scale"], g["index"], g["rank"], U=want[1].float(), base=g["dbase"])
+    for name, x, y, b in zip(("dX", "dA", "dB"), got, want[2:], bounds[2:]):
+        check(name, x, y, b)
