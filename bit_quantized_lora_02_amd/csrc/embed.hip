@@ -302,7 +302,10 @@ int embed_piece(int64_t T) { return T <= kPieceMost ? kPieceMost : T <= 2048 ? 8
 
 // Positions that are ranked against each other: ranking costs T x chunk, and up to four chunks take one pass of the merge
 // (131072 positions: ranked in 87 us 8192 at a time, in 29 us 2048 at a time with one pass more, which takes 7).
-static int64_t order_chunk(int64_t T) { return T <= kMergeRuns * kOrderChunk ? kOrderChunk : kOrderChunk / 4; }
+static int64_t order_chunk(int64_t T) {
+  const int64_t c = T <= kOrderChunk || T > 2 * kOrderChunk ? kOrderChunk : kOrderChunk / 2;
+  return T <= kMergeRuns * c ? c : kOrderChunk / 4;
+}
 int embed_passes(int64_t T) {
   int n = 0;
   for (int64_t run = order_chunk(T); run < T; run *= kMergeRuns) ++n;

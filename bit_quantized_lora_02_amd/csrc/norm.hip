@@ -9,7 +9,7 @@
 // sums).  The variance is taken from the centred row (no difference of large sums).  All sums are binary32 in
 // a fixed order; bf16 outputs are rounded once.  Workgroups are persistent: they hold the weights (and, backward, the
 // running sums of dw and db) of their columns in registers over all of their rows, and load the next row while the
-// present one is reduced.
+// present one is reduced.  Of few rows the backward reads X and dY twice, from the caches, and is one launch.
 #include "step.h"
 #include "step_device.h"
 
@@ -120,14 +120,33 @@ __device__ __forceinline__ void store_sums(float *__restrict__ out, int64_t D, i
 // the workgroup's rows; then the groups add theirs in LDS, one after the other, and the workgroup's go to part[block].
 // (C = 4, the longest rows: the sums do not fit the registers beside a row and come from k_norm_columns; 1024 x 32768 so
 // 86 us in all, with spilled registers 191.)
-template <int NT, int C, bool F32>
-__global__ __launch_bounds__(1024) void k_norm_bwd(const bf16_t *__restrict__ X, const bf16_t *dY, int64_t T, int64_t D,
-                                                   const void *__restrict__ w, const float *__restrict__ mean,
-                                                   const float *__restrict__ rstd, bf16_t *dX, float *__restrict__ part) {
+struct NormBwd {
+  const bf16_t *X, *dY;
+  int64_t T, D;
+  const void *w;
+  const float *mean, *rstd;
+  bf16_t *dX;
+  float *part;
+};
+template <int NT, int C, bool SUMS>
+struct BwdShared {
+  static constexpr int G = 1024 / NT;
+  float sum[2][G][2][NT / 64];
+  __attribute__((aligned(16))) float part[SUMS && G > 1 ? NT * C * 16 : 4];
+};
+template <int NT, int C, bool F32, bool SUMS>
+__device__ __forceinline__ void norm_bwd_rows(const NormBwd &p, int64_t block, int64_t blocks, char *shared) {
   constexpr int G = 1024 / NT, WAVES = NT / 64;
-  constexpr bool SUMS = C <= 2;
-  __shared__ float s_sum[2][G][2][WAVES];
-  __shared__ __attribute__((aligned(16))) float s_part[G > 1 ? NT * C * 16 : 1];
+  const bf16_t *__restrict__ const X = p.X;
+  const bf16_t *const dY = p.dY;
+  const int64_t T = p.T, D = p.D;
+  const void *__restrict__ const w = p.w;
+  const float *__restrict__ const mean = p.mean, *__restrict__ const rstd = p.rstd;
+  bf16_t *const dX = p.dX;
+  float *__restrict__ const part = p.part;
+  auto &sh = *reinterpret_cast<BwdShared<NT, C, SUMS> *>(shared);
+  auto &s_sum = sh.sum;
+  float *const s_part = sh.part;
   const int g = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   bool in[C];
@@ -160,7 +179,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const bf16_t *__restrict__ X,
       }
     }
   };
-  const int64_t first = (int64_t)blockIdx.x * G, step = (int64_t)gridDim.x * G;
+  const int64_t first = block * G, step = blocks * G;
   // row t of this group (behind the last one a row of zeros: every thread meets the barriers)
   auto work = [&](const Row &row, int64_t t, int turn) {
     float a = 0.f, b = 0.f;
@@ -245,10 +264,67 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const bf16_t *__restrict__ X,
     }
     if (g != G - 1) return;
   }
-  float *out = part + (int64_t)blockIdx.x * 2 * D;
+  float *out = part + block * 2 * D;
 #pragma unroll
   for (int c = 0; c < (SUMS ? C : 0); ++c)
     if (in[c]) store_sums(out, D, d[c], dw[c], db[c]);
+}
+template <int NT, int C, bool F32>
+__global__ __launch_bounds__(1024) void k_norm_bwd(NormBwd p) {
+  __shared__ __attribute__((aligned(16))) char shared[sizeof(BwdShared<NT, C, C <= 2>)];
+  norm_bwd_rows<NT, C, F32, C <= 2>(p, blockIdx.x, gridDim.x, shared);
+}
+
+// Few rows: dX in the first workgroups and, from the statistics that the forward left, dw and db in the others: 64 columns
+// each, the rows to 128 teams of eight lanes in turn, whose sums are added in a fixed order (17 x 1808 4.1 us, else 4.2 and
+// 4.0 in two launches; 512 x 16384 17 us, else 24).
+struct ColumnShared {
+  float sum[128][8][17];
+};
+__device__ __forceinline__ void norm_columns_few(const NormBwd &p, int64_t block, bool f32, void *__restrict__ dw,
+                                                 void *__restrict__ db, char *shared) {
+  auto &s_sum = reinterpret_cast<ColumnShared *>(shared)->sum;
+  const int tid = threadIdx.x, lane = tid & 7, team = tid >> 3;
+  const int64_t d = block * 64 + lane * 8;
+  float sum[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+  if (d < p.D)
+#pragma unroll 4
+    for (int64_t t = team; t < p.T; t += 128) {
+      const float m = p.mean[t], r = p.rstd[t];
+      float x[8], y[8];
+      unpack8(load16(p.X + t * p.D + d), x);
+      unpack8(load16(p.dY + t * p.D + d), y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum[i] = fmaf(y[i], (x[i] - m) * r, sum[i]);
+        sum[8 + i] += y[i];
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s_sum[team][lane][i] = sum[i];
+  __syncthreads();
+  const int of_db = tid >> 6, col = tid & 63;
+  const int64_t at = block * 64 + col;
+  void *const to = of_db ? db : dw;
+  if (of_db > 1 || !to || at >= p.D) return;
+  float four[4] = {0.f, 0.f, 0.f, 0.f};  // (teams 0, 4, ..; 1, 5, ..; and so on)
+#pragma unroll 16
+  for (int q = 0; q < 128; q += 4)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) four[i] += s_sum[q + i][col >> 3][of_db * 8 + (col & 7)];
+  const float all = (four[0] + four[1]) + (four[2] + four[3]);
+  if (f32) ((float *)to)[at] = all;
+  else ((bf16_t *)to)[at] = f32_to_bf16(all);
+}
+template <int NT, int C, bool F32>
+__global__ __launch_bounds__(1024) void k_norm_few(NormBwd p, int64_t row_blocks, void *__restrict__ dw,
+                                                   void *__restrict__ db) {
+  constexpr int kRows = sizeof(BwdShared<NT, C, false>), kColumns = sizeof(ColumnShared);
+  __shared__ __attribute__((aligned(16))) char shared[kRows > kColumns ? kRows : kColumns];
+  if (blockIdx.x < row_blocks) norm_bwd_rows<NT, C, F32, false>(p, blockIdx.x, row_blocks, shared);
+  else norm_columns_few(p, blockIdx.x - row_blocks, F32, dw, db, shared);
 }
 
 // The sums alone: 2048 columns, every gridDim.y-th row.
@@ -343,20 +419,33 @@ hipError_t launch_norm_bwd(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t
                            const float *mean, const float *rstd, bf16_t *dX, float *part, hipStream_t s) {
   const int nt = bwd_threads(D), c = (int)((D + nt * 8 - 1) / (nt * 8));
   const dim3 grid((uint32_t)norm_bwd_groups(T, D)), block(1024);
-#define NORM_ARGS grid, block, 0, s, X, dY, T, D, w, mean, rstd, dX, part
-#define NORM_NT(NT_)                                           \
-  do {                                                         \
-    if (c <= 1) NORM_CASE(NT_, 1, k_norm_bwd, NORM_ARGS);      \
-    else NORM_CASE(NT_, 2, k_norm_bwd, NORM_ARGS);             \
+  const NormBwd p{X, dY, T, D, w, mean, rstd, dX, part};
+#define NORM_NT(kern, ...)                                             \
+  do {                                                                 \
+    if (nt == 64 && c <= 1) NORM_CASE(64, 1, kern, __VA_ARGS__);       \
+    else if (nt == 64) NORM_CASE(64, 2, kern, __VA_ARGS__);            \
+    else if (nt == 256 && c <= 1) NORM_CASE(256, 1, kern, __VA_ARGS__); \
+    else if (nt == 256) NORM_CASE(256, 2, kern, __VA_ARGS__);          \
+    else if (c <= 1) NORM_CASE(1024, 1, kern, __VA_ARGS__);            \
+    else if (c <= 2) NORM_CASE(1024, 2, kern, __VA_ARGS__);            \
+    else NORM_CASE(1024, 4, kern, __VA_ARGS__);                        \
   } while (0)
-  if (nt == 64) NORM_NT(64);
-  else if (nt == 256) NORM_NT(256);
-  else if (c <= 2) NORM_NT(1024);
-  else {
-    NORM_CASE(1024, 4, k_norm_bwd, NORM_ARGS);
-  }
+  NORM_NT(k_norm_bwd, grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+// 1024 x 4096 11.6 us so, else 14.0, but 1001 x 5992, whose rows do not begin with a line of memory, 18.5 and 17.1; 768 x
+// 4096 10.6 and 13.5.  2048 x 32768 115 us, with k_norm_columns 146; 8192 x 24576 390 and 376.
+bool norm_bwd_few(int64_t T, int64_t D) { return T <= (norm_bwd_columns(D) ? 2048 : 768); }
+
+hipError_t launch_norm_few(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t D, const void *w, bool f32,
+                           const float *mean, const float *rstd, bf16_t *dX, void *dw, void *db, hipStream_t s) {
+  const int nt = bwd_threads(D), c = (int)((D + nt * 8 - 1) / (nt * 8));
+  const int64_t rows = dX ? norm_bwd_groups(T, D) : 0;
+  const dim3 grid((uint32_t)(rows + (D + 63) / 64)), block(1024);
+  const NormBwd p{X, dY, T, D, w, mean, rstd, dX, nullptr};
+  NORM_NT(k_norm_few, grid, block, 0, s, p, rows, dw, db);
 #undef NORM_NT
-#undef NORM_ARGS
   return hipGetLastError();
 }
 

@@ -37,6 +37,9 @@ hipError_t launch_norm(const bf16_t *X, int64_t T, int64_t D, const void *w, con
 int norm_bwd_groups(int64_t T, int64_t D);  // workgroups, each with binary32 sums [2][D] in `part`
 hipError_t launch_norm_bwd(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t D, const void *w, bool f32,
                            const float *mean, const float *rstd, bf16_t *dX, float *part, hipStream_t s);
+bool norm_bwd_few(int64_t T, int64_t D);  // few rows: all of the backward in one launch (unless dX is dY itself)
+hipError_t launch_norm_few(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t D, const void *w, bool f32,
+                           const float *mean, const float *rstd, bf16_t *dX, void *dw, void *db, hipStream_t s);
 bool norm_bwd_columns(int64_t D);  // the sums come from a kernel of their own, which goes first (dX may be dY itself)
 hipError_t launch_norm_columns(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t D, const float *mean, const float *rstd,
                                float *part, hipStream_t s);

@@ -359,6 +359,10 @@ int qlora_layer_norm_bwd(const qlora_bf16 *X, const qlora_bf16 *dY, int64_t T, i
   hipStream_t s = (hipStream_t)stream;
   const bool f32 = weight_type == QLORA_WEIGHT_F32;
   float *part = sums ? (float *)ws : nullptr;
+  if (sums && norm_bwd_few(T, n_in) && dX != dY) {
+    LAUNCH("layer_norm_bwd", launch_norm_few(X, dY, T, n_in, weight, f32, mean, rstd, dX, dweight, dbias, s));
+    return QLORA_OK;
+  }
   // (without rows: the sums are zero)
   const bool columns = norm_bwd_columns(n_in);
   if (sums && columns) LAUNCH("layer_norm_columns", launch_norm_columns(X, dY, T, n_in, mean, rstd, part, s));

@@ -27,7 +27,7 @@ static int g_fail = 0;
 // Of one size: the plans' choices and their bytes, against what the parts must hold.
 static void plan(int64_t T, int64_t K, int64_t N, int32_t pool, int32_t r) {
   for (int64_t n : {K, N}) {
-    const int s = qlora::adapt_ranges(T, pool, n);
+    const int s = qlora::adapt_ranges(T, pool, r, n);
     HOLDS(s >= 1 && s <= 8 && s <= (n + 511) / 512);
     size_t e = 0;
     EXPECT(qlora_embed_workspace_bytes(T, n, &e), QLORA_OK);

@@ -239,6 +239,20 @@ def test_layer_norm(T, D, f32):
     assert torch.equal(X2, B.layer_norm(Xg, wg, bg)[0]), "Y over X"
 
 
+@pytest.mark.parametrize("T,D", [(31, 200), (256, 4096), (768, 5992), (769, 5992), (700, 16392), (2048, 16392),
+                                 (2049, 16392), (129, 32768)])
+def test_layer_norm_of_few_and_more_rows(T, D):
+    """Both sides of where the backward becomes one launch; dX over dY with the sums."""
+    test_layer_norm(T, D, T % 2 == 0)
+    X, dY, w, _ = norm_inputs(T, D, False, T)
+    Xg, dYg, wg = X.cuda(), dY.cuda(), w.cuda()
+    _, mean, rstd = B.layer_norm(Xg, wg)
+    want, bounds = norm_bwd_reference(X, dY, w, mean.cpu(), rstd.cpu(), False)
+    got = B.layer_norm_bwd(Xg, dYg, wg, mean, rstd, outs=(dYg, torch.empty_like(wg), torch.empty_like(wg)))
+    for name, x, y, e in zip(("dX", "dweight", "dbias"), got, want, bounds):
+        check(name, x, y, e)
+
+
 def test_layer_norm_of_special_rows():
     """No rows; equal values (variance 0); a row of large values of one sign; a NaN and an infinity stay in their rows."""
     w, b = torch.full((512,), 2.0, device="cuda"), torch.full((512,), 0.5, device="cuda")
