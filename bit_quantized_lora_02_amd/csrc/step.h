@@ -19,7 +19,11 @@ struct Order {
 // Embedding.
 hipError_t launch_embed(const int64_t *tokens, int64_t T, const bf16_t *W, int64_t V, int64_t D, float scale, bf16_t *Y,
                         hipStream_t s);
-// Entries of the sorted list that one wave adds up, and the bytes of the sums that cross from one such piece to the next.
+// The gradient of up to kEmbedFew tokens.
+constexpr int64_t kEmbedFew = 64;
+hipError_t launch_embed_few(const int64_t *tokens, int64_t T, const bf16_t *dY, int64_t V, int64_t D, float scale, bool add,
+                            bf16_t *dW, hipStream_t s);
+// Of more: entries of the sorted list that one wave adds up.
 int embed_piece(int64_t T);
 hipError_t launch_embed_order(const int64_t *tokens, int64_t T, int64_t V, const Order &o, bf16_t *fill, int64_t fill_n,
                               hipStream_t s);

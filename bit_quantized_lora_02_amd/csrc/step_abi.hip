@@ -308,8 +308,12 @@ int qlora_embed_bwd(const int64_t *tokens, const qlora_bf16 *dY, int64_t T, int6
   o.key2 = (int32_t *)(w + p.key2);
   float *part = (float *)(w + p.part);
   const bool add = accumulate != 0;
-  if (T > 0 || !add)
-    LAUNCH("embed_order", launch_embed_order(tokens, T, n_vocab, o, dW, add ? 0 : n_vocab * n_in, s));
+  if (T == 0 && add) return QLORA_OK;
+  if (T > 0 && T <= kEmbedFew) {
+    LAUNCH("embed_few", launch_embed_few(tokens, T, dY, n_vocab, n_in, scale, add, dW, s));
+    return QLORA_OK;
+  }
+  LAUNCH("embed_order", launch_embed_order(tokens, T, n_vocab, o, dW, add ? 0 : n_vocab * n_in, s));
   if (T == 0) return QLORA_OK;
   for (int pass = 0; pass < embed_passes(T); ++pass) LAUNCH("embed_merge", launch_embed_merge(T, pass, o, s));
   LAUNCH("embed_sum", launch_embed_sum(o, T, dY, n_vocab, n_in, scale, add, dW, part, s));
