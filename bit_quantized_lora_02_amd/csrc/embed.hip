@@ -286,26 +286,39 @@ __global__ __launch_bounds__(256) void k_embed_join(const int32_t *__restrict__ 
   }
 }
 
-// Few tokens, one launch: each lane of a wave holds a token.  A thread fills 8 columns with zeros, as above, or adds them up
+// Few tokens, one launch: each lane of a wave holds L of them, 64 apart.  A thread fills 8 columns with zeros, as above, or adds them up
 // where a token names their row; with ADD a workgroup takes 2048 columns of the row of token blockIdx.x / slices, unless an
-// earlier token names it too.  (16 tokens of 50000 x 1024 16.3 us, with
-// the sort 20.6.)
-template <bool ADD>
+// earlier token names it too.  (16 tokens of 50000 x 1024 16.3 us, with the sort 20.6; 128 of 1000 x 1024 8 and 13.  256
+// tokens that are all the same would take 26, with the sort 14: they are added eight at a time.)
+template <int L, bool ADD>
 __global__ __launch_bounds__(256) void k_embed_few(const int64_t *__restrict__ tokens, int T, const bf16_t *__restrict__ dY,
                                                    int64_t V, int64_t D, float scale, bf16_t *__restrict__ dW,
                                                    uint32_t slices) {
   const int lane = threadIdx.x & 63;
-  const int64_t v = tokens[lane < T ? lane : T - 1];
-  const int key = lane < T && (uint64_t)v < (uint64_t)V ? (int)v : -1;
+  int64_t v[L];
+  int key[L];
+#pragma unroll
+  for (int l = 0; l < L; ++l) v[l] = tokens[l * 64 + lane < T ? l * 64 + lane : T - 1];
+#pragma unroll
+  for (int l = 0; l < L; ++l) key[l] = l * 64 + lane < T && (uint64_t)v[l] < (uint64_t)V ? (int)v[l] : -1;
   const uint32_t per = (uint32_t)(D / 8), chunks = per * (uint32_t)V;  // (at most 2^31)
   int row, first, last;  // of this thread; of the workgroup
   uint32_t c;            // 16-byte chunk of the row
   bool in;               // (behind the end a thread stays, whose lane holds a token)
   if (ADD) {
     const int t = blockIdx.x / slices;
-    row = first = last = __builtin_amdgcn_readlane(key, t);
+    row = -1;
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+      if (t >> 6 == l) row = __builtin_amdgcn_readlane(key[l], t & 63);
+    first = last = row;
     c = (blockIdx.x - t * slices) * 256 + threadIdx.x;
-    if (row < 0 || __builtin_ctzll(__ballot(key == row)) != t) return;
+    if (row < 0) return;
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      const uint64_t same = __ballot(key[l] == row);
+      if (l < t >> 6 ? same != 0 : l == t >> 6 && (same & (((uint64_t)1 << (t & 63)) - 1)) != 0) return;
+    }
     in = c < per;
   } else {
     const uint32_t c0 = blockIdx.x * 256u, c1 = chunks - c0 > 255 ? c0 + 255 : chunks - 1;
@@ -318,30 +331,34 @@ __global__ __launch_bounds__(256) void k_embed_few(const int64_t *__restrict__ t
   if (!in) c = 0;
   bf16_t *const to = dW + ((int64_t)row * D + c * 8);
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  uint64_t left = __ballot(key >= first && key <= last);
-  if (!ADD && left == 0) {
+  uint64_t named[L], any = 0;
+#pragma unroll
+  for (int l = 0; l < L; ++l) any |= named[l] = __ballot(key[l] >= first && key[l] <= last);
+  if (!ADD && any == 0) {
     if (in) store16(to, u32x4_t{0u, 0u, 0u, 0u});
     return;
   }
   constexpr int N = 8;  // rows in flight
-  while (left) {
-    u32x4_t x[N];
-    int of[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {  // (behind the last: its row again, not added)
-      const int t = left ? __builtin_ctzll(left) : 0;
-      of[i] = left ? __builtin_amdgcn_readlane(key, t) : -1;
-      x[i] = load16(dY + (int64_t)t * D + c * 8);
-      left &= left - 1;
+  for (int l = 0; l < L; ++l)
+    for (uint64_t left = named[l]; left;) {
+      u32x4_t x[N];
+      int of[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {  // (behind the last: some row, not added)
+        const int t = left ? __builtin_ctzll(left) : 0;
+        of[i] = left ? __builtin_amdgcn_readlane(key[l], t) : -1;
+        x[i] = load16(dY + (int64_t)(l * 64 + t) * D + c * 8);
+        left &= left - 1;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float y[8];
+        unpack8(x[i], y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = of[i] == row ? sum[e] + y[e] : sum[e];
+      }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float y[8];
-      unpack8(x[i], y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] = of[i] == row ? sum[e] + y[e] : sum[e];
-    }
-  }
   if (in) write_row(to, sum, scale, ADD);
 }
 
@@ -362,8 +379,15 @@ int embed_piece(int64_t T) { return T <= 2048 ? 8 : T <= 8192 ? 16 : kPieceMost;
 hipError_t launch_embed_few(const int64_t *tokens, int64_t T, const bf16_t *dY, int64_t V, int64_t D, float scale, bool add,
                             bf16_t *dW, hipStream_t s) {
   const int64_t slices = (D + 2047) / 2048, blocks = add ? T * slices : (V * (D / 8) + 255) / 256;
-  if (add) launch(k_embed_few<true>, dim3((uint32_t)blocks), dim3(256), 0, s, tokens, (int)T, dY, V, D, scale, dW, (uint32_t)slices);
-  else launch(k_embed_few<false>, dim3((uint32_t)blocks), dim3(256), 0, s, tokens, (int)T, dY, V, D, scale, dW, (uint32_t)slices);
+#define FEW(L_)                                                                                                       \
+  do {                                                                                                                \
+    if (add) launch(k_embed_few<L_, true>, grid, block, 0, s, tokens, (int)T, dY, V, D, scale, dW, (uint32_t)slices); \
+    else launch(k_embed_few<L_, false>, grid, block, 0, s, tokens, (int)T, dY, V, D, scale, dW, (uint32_t)slices);    \
+  } while (0)
+  const dim3 grid((uint32_t)blocks), block(256);
+  if (T <= 64) FEW(1);
+  else FEW(2);
+#undef FEW
   return hipGetLastError();
 }
 

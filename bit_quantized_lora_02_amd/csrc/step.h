@@ -20,7 +20,7 @@ struct Order {
 hipError_t launch_embed(const int64_t *tokens, int64_t T, const bf16_t *W, int64_t V, int64_t D, float scale, bf16_t *Y,
                         hipStream_t s);
 // The gradient of up to kEmbedFew tokens.
-constexpr int64_t kEmbedFew = 64;
+constexpr int64_t kEmbedFew = 128;
 hipError_t launch_embed_few(const int64_t *tokens, int64_t T, const bf16_t *dY, int64_t V, int64_t D, float scale, bool add,
                             bf16_t *dW, hipStream_t s);
 // Of more: entries of the sorted list that one wave adds up.

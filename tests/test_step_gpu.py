@@ -125,6 +125,13 @@ def test_embedding_of_many_tokens(T, V, D, kind):
     test_embedding(T, V, D, kind)
 
 
+@pytest.mark.parametrize("T", [1, 8, 63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("V,D,kind", [(40, 72, "runs"), (3, 2056, "one"), (1000, 16, "any"), (7, 8, "none")])
+def test_embedding_of_few_tokens(T, V, D, kind):
+    """Both sides of where the gradient becomes one launch."""
+    test_embedding(T, V, D, kind)
+
+
 def test_embedding_of_no_tokens():
     t = torch.zeros(0, dtype=torch.int64, device="cuda")
     dY = torch.zeros(0, 64, dtype=bf, device="cuda")
