@@ -692,11 +692,6 @@ def _at(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _shaped(out, shape: tuple, dtype: torch.dtype, device: torch.device, name: str) -> torch.Tensor:
-    """The caller's buffer, checked, or a new one."""
-    return torch.empty(shape, dtype=dtype, device=device) if out is None else _want(out, shape, dtype, device, name)
-
-
 def _scratch(ws, nb: int, device: torch.device):
     """(workspace, its bytes): the caller's, or a new one of nb bytes."""
     if ws is not None:
@@ -785,7 +780,7 @@ def layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
         _norm_weight(bias, n_in, dev, "bias", weight.dtype)
     if outs is None:
         Y = torch.empty_like(X)
-        mean, rstd = torch.empty((2, T), dtype=torch.float32, device=dev).unbind(0)
+        mean, rstd = X.new_empty(T, dtype=torch.float32), X.new_empty(T, dtype=torch.float32)
     else:
         Y, mean, rstd = outs
         _want(Y, (T, n_in), torch.bfloat16, dev, "Y")
@@ -869,8 +864,11 @@ def adapters_fwd(X: torch.Tensor, A_pool: torch.Tensor, B_pool: torch.Tensor, sc
     dev, bf = X.device, torch.bfloat16
     if base is not None:
         base = _want(_bits(base), (T, n_out), bf, dev, "base")
-    Y = _shaped(out, (T, n_out), bf, dev, "out")
-    U = _shaped(u_out, (T, r), torch.float32, dev, "u_out") if save_u or u_out is not None else None
+    Y = X.new_empty((T, n_out)) if out is None else _want(out, (T, n_out), bf, dev, "out")
+    if u_out is not None:
+        U = _want(u_out, (T, r), torch.float32, dev, "u_out")
+    else:
+        U = X.new_empty((T, r), dtype=torch.float32) if save_u else None
     ws, nb = _scratch(ws, adapters_workspace_bytes(T, n_in, n_out, n_pool, r), dev)
     _run("qlora_adapters_fwd", dev, X.data_ptr(), T, n_in, A_pool.data_ptr(), B_pool.data_ptr(), n_out, n_pool, r, _at(rank),
          scale.data_ptr(), index.data_ptr(), _at(base), Y.data_ptr(), _at(U), ws.data_ptr(), nb)
