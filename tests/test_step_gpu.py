@@ -247,7 +247,7 @@ def test_layer_norm(T, D, f32):
 
 
 @pytest.mark.parametrize("T,D", [(31, 200), (256, 4096), (768, 5992), (769, 5992), (700, 16392), (2048, 16392),
-                                 (2049, 16392), (129, 32768)])
+                                 (2049, 16392), (129, 32768), (900, 9000), (800, 12288), (520, 24576), (700, 1288)])
 def test_layer_norm_of_few_and_more_rows(T, D):
     """Both sides of where the backward becomes one launch; dX over dY with the sums."""
     test_layer_norm(T, D, T % 2 == 0)
