@@ -817,8 +817,8 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
   }
 }
 
-// A workgroup takes at most 64 ranks, as their sums then leave room for others (8000 tokens, 4096 x 4096, rank 128: with
-// all of them in one, and one workgroup per CU, 95 us; so 80).
+// A workgroup takes at most 64 ranks, an equal part of them, as their sums then leave room for others (8000 tokens, 4096 x
+// 4096, rank 128: with all of them in one, and one workgroup per CU, 95 us; so 78).
 struct GradArgs {
   AdaptGrads g;
   int piece, parts, blocks_a, columns, blocks;  // columns: blocks of 64, of X first; blocks: of a piece, in all
@@ -828,7 +828,7 @@ __device__ __forceinline__ void grads_tile(const AdaptRows &a, const GradArgs &q
   const int id = at_block / q.blocks, rest = at_block - id * q.blocks;
   // (the parts of a block of columns come eight workgroups apart, on one XCD: the columns are then in its L2)
   const int eights = rest / (8 * q.parts), in = rest - eights * 8 * q.parts;
-  const int block = q.parts == 1 ? rest : eights * 8 + (in & 7), jb = q.parts == 1 ? 0 : (in >> 3) * 64;
+  const int block = q.parts == 1 ? rest : eights * 8 + (in & 7), jb = q.parts == 1 ? 0 : (in >> 3) * 16 * RT;
   if (block >= q.columns) return;
   Tile tile;
   if (!find_tile<true>(a, q.piece, id, &tile)) return;
@@ -933,18 +933,24 @@ namespace {
 ExpandArgs expand_args(const AdaptRows &a, bool wide, const float *U, int ranges, const bf16_t *Q, int64_t N, bool scaled,
                        const bf16_t *base, bf16_t *out, float *U_out, int64_t *grid) {
   const int64_t tiles = most_tiles(a, wide ? 32 : 16), cols = (N + kExpandCols - 1) / kExpandCols;
-  // Column blocks: enough workgroups for the GPU, few enough that their lookups and u are shared by several steps (1000
-  // tokens, 4096 x 4096 8.4 us with one step each, 6.3 with two; 4096 tokens x 14336 62 us with 4, 56 with 7, 60 with 14;
-  // 8000 x 4096 30.0 with two, 32.5 with four).  A multiple of 8, so that a block's rows of Q stay in the L2 of one XCD
-  // (workgroups go round the eight).  Above rank 64 u costs a block more: 8000 x 4096, rank 128 55 us with four steps, 63
-  // with two.
-  const int64_t least = a.r > 64 ? 8 : 16;
-  int64_t want = (1024 / tiles + 8) / 8 * 8;
-  if (want < least) want = least;
-  if (want * 8 < cols) want = (cols + 63) / 64 * 8;
-  const int64_t per = cols <= want ? 1 : (cols + want - 1) / want;
+  // Column blocks, so many that the workgroups which the GPU holds at once (`slots`) are used up in whole rounds, and each
+  // has several steps to share its lookups and u, which cost about one: of the numbers of rounds the one that takes least
+  // (4096 x 4096: 8000 tokens, rank 64 32.3 us so, 37.8 with 16 blocks in all cases; 3000 x 6000, rank 96 26.5 us, with 8
+  // blocks 32).  Adapters past the L2s take a multiple of 8 blocks, so that a block's rows of Q stay in the L2 of one XCD
+  // (workgroups go round the eight: 4096 x 14336, 8 of rank 64 62 us, else 67); above rank 64 that is no gain (2000 x
+  // 9000, 5 of rank 128 33 us, else 29.5).
+  const int64_t slots = a.r > 64 ? (wide ? 512 : 768) : a.r > 32 && wide ? 1024 : 1280;
+  const int64_t adapters = a.n_pool < a.T ? a.n_pool : a.T, likely = a.T / (wide ? 32 : 16) + adapters / 2 + 1;
+  const bool eights = a.r <= 64 && adapters * N * a.r * 2 > (int64_t)8 << 20;
+  int64_t least = INT64_MAX, per = 1;
+  for (int k = 1; k <= 6; ++k) {
+    int64_t b = eights ? 8 * k : k * slots / likely;
+    if (b < 1) b = 1;
+    const int64_t steps = (cols + b - 1) / b, rounds = (b * likely + slots - 1) / slots;
+    if (rounds * (steps + 1) < least) least = rounds * (steps + 1), per = steps;
+  }
   int64_t blocks = (cols + per - 1) / per;
-  if (blocks > 8) blocks = (blocks + 7) / 8 * 8;
+  if (eights && blocks > 8) blocks = (blocks + 7) / 8 * 8;
   *grid = blocks * tiles;
   return ExpandArgs{U, ranges, Q, N, scaled, per * kExpandCols, (int)blocks, base, out, U_out};
 }
@@ -1001,8 +1007,10 @@ hipError_t launch_adapt_grads(const AdaptRows &a, const AdaptGrads &g, int piece
   int64_t blocks;
   const GradArgs q = grad_args(a, g, piece, &blocks);
   const dim3 grid((uint32_t)blocks), block(256);
-  if (a.r <= 16) launch(k_adapt_grads<1>, grid, block, 0, s, a, q);
-  else if (a.r <= 32) launch(k_adapt_grads<2>, grid, block, 0, s, a, q);
+  const int ranks = (a.r + q.parts - 1) / q.parts;  // of a part
+  if (ranks <= 16) launch(k_adapt_grads<1>, grid, block, 0, s, a, q);
+  else if (ranks <= 32) launch(k_adapt_grads<2>, grid, block, 0, s, a, q);
+  else if (ranks <= 48) launch(k_adapt_grads<3>, grid, block, 0, s, a, q);
   else launch(k_adapt_grads<4>, grid, block, 0, s, a, q);
   return hipGetLastError();
 }
