@@ -894,8 +894,8 @@ hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const Adap
   const int64_t b0 = turn_blocks(t0, a.n_pool), blocks = b0 + turn_blocks(t1, a.n_pool);
   // (the largest pools have more blocks than a launch may have threads)
   const int64_t chunks = a.T > 0 ? adapt_chunks(a.T) : 1;
-  launch(k_adapt_plan, dim3((uint32_t)(chunks + (blocks < 65536 ? blocks : 65536))), dim3(1024), 0, s, a, (int)chunks, t0, t1,
-         b0, blocks);
+  const dim3 grid((uint32_t)(chunks + (blocks < 65536 ? blocks : 65536)));
+  launch(k_adapt_plan, grid, dim3(1024), 0, s, a, (int)chunks, t0, t1, b0, blocks);
   return hipGetLastError();
 }
 

@@ -14,6 +14,7 @@
 //   3. k_embed_sum    a wave adds a piece of the sorted list over 512 columns; a row that lies in one piece is written at
 //                     once.
 //   4. k_embed_join   rows that were cut at the pieces' borders.
+// Up to kEmbedFew tokens k_embed_few does all of it.
 #include "step.h"
 #include "step_device.h"
 
@@ -44,8 +45,8 @@ __global__ __launch_bounds__(256) void k_embed(const int64_t *__restrict__ token
 // the number of equal ones before it.  16 threads count for each position, a sixteenth of 2048 keys at a time, which all
 // read from LDS, two vector instructions per pair (8192 positions: 67 million pairs over the whole GPU, 6 us).
 constexpr int kRankItems = 16, kRankParts = 16, kRankKeys = 2048, kRankPart = kRankKeys / kRankParts;
-__device__ __forceinline__ void rank_chunk(const int64_t *__restrict__ tokens, int64_t T, int64_t V, int64_t block, int chunk,
-                                           int32_t *__restrict__ order, int32_t *__restrict__ key) {
+__device__ __forceinline__ void rank_chunk(const int64_t *__restrict__ tokens, int64_t T, int64_t V, int64_t block,
+                                           int chunk, int32_t *__restrict__ order, int32_t *__restrict__ key) {
   __shared__ __attribute__((aligned(16))) uint32_t s_key[kRankParts][kRankPart + 4];
   __shared__ uint32_t s_rank[kRankParts][kRankItems];
   const int64_t first = block * kRankItems, base = first & -(int64_t)chunk;  // (a power of two)
@@ -286,10 +287,10 @@ __global__ __launch_bounds__(256) void k_embed_join(const int32_t *__restrict__ 
   }
 }
 
-// Few tokens, one launch: each lane of a wave holds L of them, 64 apart.  A thread fills 8 columns with zeros, as above, or adds them up
-// where a token names their row; with ADD a workgroup takes 2048 columns of the row of token blockIdx.x / slices, unless an
-// earlier token names it too.  (16 tokens of 50000 x 1024 16.3 us, with the sort 20.6; 128 of 1000 x 1024 8 and 13.  256
-// tokens that are all the same would take 26, with the sort 14: they are added eight at a time.)
+// Few tokens, one launch: each lane of a wave holds L of them, 64 apart.  A thread fills 8 columns with zeros, as above, or
+// adds them up where a token names their row; with ADD a workgroup takes 2048 columns of the row of token blockIdx.x /
+// slices, unless an earlier token names it too.  (16 tokens of 50000 x 1024 16.3 us, with the sort 20.6; 128 of 1000 x
+// 1024 8 and 13.  256 tokens that are all the same would take 26, with the sort 14: they are added eight at a time.)
 template <int L, bool ADD>
 __global__ __launch_bounds__(256) void k_embed_few(const int64_t *__restrict__ tokens, int T, const bf16_t *__restrict__ dY,
                                                    int64_t V, int64_t D, float scale, bf16_t *__restrict__ dW,
@@ -343,10 +344,10 @@ __global__ __launch_bounds__(256) void k_embed_few(const int64_t *__restrict__ t
   for (int l = 0; l < L; ++l)
     for (uint64_t left = named[l]; left;) {
       u32x4_t x[N];
-      int of[N];
+      int of[N], t = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {  // (behind the last: some row, not added)
-        const int t = left ? __builtin_ctzll(left) : 0;
+      for (int i = 0; i < N; ++i) {  // (behind the last: its row again, not added)
+        if (left) t = __builtin_ctzll(left);
         of[i] = left ? __builtin_amdgcn_readlane(key[l], t) : -1;
         x[i] = load16(dY + (int64_t)(l * 64 + t) * D + c * 8);
         left &= left - 1;

@@ -424,8 +424,8 @@ hipError_t launch_norm_bwd(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t
   const int nt = bwd_threads(D), c = (int)((D + nt * 8 - 1) / (nt * 8));
   const dim3 grid((uint32_t)norm_bwd_groups(T, D));
   const NormBwd p{X, dY, T, D, w, mean, rstd, dX, part};
-  // (where 1024 threads would be half idle: 4096 x 4104 23.6 us, so 22.0.  Few rows stay with the threads that norm_few has, so
-  // that dX does not depend on what else is asked for.)
+  // (where 1024 threads would be half idle: 4096 x 4104 23.6 us, so 22.0.  Few rows stay with the threads that k_norm_few
+  // has, so that dX does not depend on what else is asked for.)
   const bool many = !norm_bwd_few(T, D);
   if (many && D > 4096 && D <= 6144) {
     NORM_CASE(768, 1, k_norm_bwd, grid, dim3(768), 0, s, p);
