@@ -923,6 +923,7 @@ hipError_t launch_adapt_shrink(const AdaptRows &a, const bf16_t *P, int64_t K, c
   if (a.r <= 16) SHRINK(1);
   else if (a.r <= 32) SHRINK(2);
   else if (a.r <= 64) SHRINK(4);
+  else if (a.r <= 96) SHRINK(6);
   else SHRINK(8);
 #undef SHRINK
   return hipGetLastError();
