@@ -394,3 +394,9 @@ def test_large_outputs_of_odd_widths(T, N, r, off):
     got = B.adapters_bwd(g["X"], g["dY"], g["A"], g["B"], g["scale"], g["index"], g["rank"], U=want[1].float(), base=g["dbase"])
     for name, x, y, b in zip(("dX", "dA", "dB"), got, want[2:], bounds[2:]):
         check(name, x, y, b)
+
+
+@pytest.mark.parametrize("T", [90, 700, 2100])
+@pytest.mark.parametrize("r", range(8, 129, 8))
+def test_every_rank(T, r):
+    test_adapters(T, 328, 264, 3, r, "any", True)
