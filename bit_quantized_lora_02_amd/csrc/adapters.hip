@@ -261,46 +261,50 @@ __device__ __forceinline__ void plan_tokens(const AdaptRows &a, int chunk, PlanS
   }
 }
 
-constexpr int kTurn = 64;  // a workgroup turns 64 rows x 128 columns
+// A workgroup turns all r ranks of 8 (1024 / r) rows or columns, a chunk of 16 bytes per thread: what it reads or writes is
+// one piece of memory (with the plan, four of rank 72, 12600 and 13256 long 8.7 us, in tiles of 64 x 128 14.7; 16 of rank
+// 32, 4096 and 4096 long 6.1 and 9.7).
+// In LDS eight rows are followed by one word, so that a wave's reads down a column meet different banks.
 struct TurnShared {
-  bf16_t tile[kTurn][136];
+  uint32_t tile[4096 + 128];
 };
-__device__ __forceinline__ void turn_pool(const AdaptTurn &t, int64_t id, TurnShared &sh) {
-  auto &s_tile = sh.tile;
-  const int64_t rb = (t.rows + kTurn - 1) / kTurn, cb = (t.cols + 127) / 128;
-  const int64_t pool = id / (rb * cb), rest = id - pool * rb * cb;
-  const int64_t r0 = rest % rb * kTurn, c0 = rest / rb * 128;
+__device__ __forceinline__ void turn_pool(const AdaptTurn &t, uint32_t id, TurnShared &sh) {
+  const uint32_t pool = id / t.blocks, rest = id - pool * t.blocks;
+  const int64_t r0 = t.rows == t.tile_rows ? 0 : (int64_t)rest * t.tile_rows;
+  const int64_t c0 = t.rows == t.tile_rows ? (int64_t)rest * t.tile_cols : 0;
   const bf16_t *from = t.from + pool * t.rows * t.cols;
   bf16_t *to = t.to + pool * t.rows * t.cols;
-  const int tid = threadIdx.x;
+  const uint32_t tid = threadIdx.x, across = t.tile_cols / 8, down = t.tile_rows / 8;  // (all sizes are multiples of 8)
+  const uint32_t ld = t.tile_cols / 2;  // words of a row
   {
-    const int row = tid >> 4, col = (tid & 15) * 8;
-    if (r0 + row < t.rows && c0 + col < t.cols)
-      *reinterpret_cast<u32x4_t *>(&s_tile[row][col]) = load16(from + (r0 + row) * t.cols + c0 + col);
+    const uint32_t row = tid / across, col = (tid - row * across) * 8;
+    if (row < (uint32_t)t.tile_rows && r0 + row < t.rows && c0 + col < t.cols) {
+      const u32x4_t v = load16(from + (r0 + row) * t.cols + c0 + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sh.tile[row * ld + (row >> 3) + col / 2 + i] = v[i];
+    }
   }
   __syncthreads();
-  const int col = tid >> 3, row = (tid & 7) * 8;  // (both sizes are multiples of 8)
-  if (c0 + col < t.cols && r0 + row < t.rows) {
+  const uint32_t col = tid / down, row = (tid - col * down) * 8;
+  if (col < (uint32_t)t.tile_cols && c0 + col < t.cols && r0 + row < t.rows) {
+    const bf16_t *const at = reinterpret_cast<const bf16_t *>(&sh.tile[row * ld + (row >> 3)]) + col;
     u32x4_t v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = s_tile[row + 2 * i][col] | (uint32_t)s_tile[row + 2 * i + 1][col] << 16;
+    for (int i = 0; i < 4; ++i) v[i] = at[4 * i * ld] | (uint32_t)at[(4 * i + 2) * ld] << 16;
     store16(to + (c0 + col) * t.rows + r0 + row, v);
   }
 }
-int64_t turn_blocks(const AdaptTurn &t, int n_pool) {
-  return t.to ? n_pool * ((t.rows + kTurn - 1) / kTurn) * ((t.cols + 127) / 128) : 0;
-}
 
 // The first workgroups group the tokens, a chunk each; the others transpose.
-__global__ __launch_bounds__(1024) void k_adapt_plan(AdaptRows a, int chunks, AdaptTurn t0, AdaptTurn t1, int64_t blocks0,
-                                                     int64_t blocks) {
+__global__ __launch_bounds__(1024) void k_adapt_plan(AdaptRows a, int chunks, AdaptTurn t0, AdaptTurn t1, uint32_t blocks0,
+                                                     uint32_t blocks) {
   __shared__ __attribute__((aligned(16))) char shared[sizeof(PlanShared)];
   static_assert(sizeof(TurnShared) <= sizeof(PlanShared), "one piece of LDS for both");
   if ((int)blockIdx.x < chunks) {
     plan_tokens<false>(a, blockIdx.x, *reinterpret_cast<PlanShared *>(shared));
     return;
   }
-  for (int64_t id = (int)blockIdx.x - chunks; id < blocks; id += (int)gridDim.x - chunks) {
+  for (uint32_t id = blockIdx.x - chunks; id < blocks; id += gridDim.x - chunks) {
     turn_pool(id < blocks0 ? t0 : t1, id < blocks0 ? id : id - blocks0, *reinterpret_cast<TurnShared *>(shared));
     __syncthreads();
   }
@@ -890,11 +894,16 @@ int64_t most_tiles(const AdaptRows &a, int M) {
 
 }  // namespace
 
-hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const AdaptTurn &t1, hipStream_t s) {
-  const int64_t b0 = turn_blocks(t0, a.n_pool), blocks = b0 + turn_blocks(t1, a.n_pool);
+hipError_t launch_adapt_plan(const AdaptRows &a, AdaptTurn t0, AdaptTurn t1, hipStream_t s) {
+  // (at most 2^27 / 64 + 1000 workgroups for a pool)
+  const int side = 1024 / a.r * 8;
+  t0.tile_rows = t1.tile_cols = a.r;
+  t0.tile_cols = t1.tile_rows = side;
+  t0.blocks = (uint32_t)((t0.cols + side - 1) / side), t1.blocks = (uint32_t)((t1.rows + side - 1) / side);
+  const uint32_t b0 = t0.to ? a.n_pool * t0.blocks : 0, blocks = b0 + (t1.to ? a.n_pool * t1.blocks : 0);
   // (the largest pools have more blocks than a launch may have threads)
   const int64_t chunks = a.T > 0 ? adapt_chunks(a.T) : 1;
-  const dim3 grid((uint32_t)(chunks + (blocks < 65536 ? blocks : 65536)));
+  const dim3 grid((uint32_t)chunks + (blocks < 8192 ? blocks : 8192));
   launch(k_adapt_plan, grid, dim3(1024), 0, s, a, (int)chunks, t0, t1, b0, blocks);
   return hipGetLastError();
 }

@@ -65,14 +65,17 @@ struct AdaptRows {
   int32_t *order = nullptr, *start = nullptr;  // [T], [n_pool + 2]; null: at most kAdaptSmall tokens
   int32_t *counts = nullptr;                   // [chunks][n_pool + 1]; null: one chunk
 };
-// Groups the tokens and, for each non-null `to`, transposes a pool: from [n_pool][rows][cols] to [n_pool][cols][rows].
+// Groups the tokens and, for each non-null `to`, transposes a pool: from [n_pool][rows][cols] to [n_pool][cols][rows]; the
+// ranks are t0's rows and t1's columns.
 struct AdaptTurn {
   const bf16_t *from = nullptr;
   bf16_t *to = nullptr;
   int64_t rows = 0, cols = 0;
+  int tile_rows = 0, tile_cols = 0;  // of a workgroup (this and the workgroups of a pool are set at the launch)
+  uint32_t blocks = 0;
 };
 hipError_t launch_adapt_count(const AdaptRows &a, hipStream_t s);  // the counts, before the plan
-hipError_t launch_adapt_plan(const AdaptRows &a, const AdaptTurn &t0, const AdaptTurn &t1, hipStream_t s);
+hipError_t launch_adapt_plan(const AdaptRows &a, AdaptTurn t0, AdaptTurn t1, hipStream_t s);
 // U[split][t][j] = (scale) P[t] . Q_a[j] over a range of K, Q [n_pool][r][K]: ranges of K (their sums come apart).
 int adapt_ranges(int64_t T, int n_pool, int r, int64_t K);
 hipError_t launch_adapt_shrink(const AdaptRows &a, const bf16_t *P, int64_t K, const bf16_t *Q, bool scaled, int ranges,
