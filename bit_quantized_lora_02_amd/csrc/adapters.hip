@@ -13,8 +13,8 @@
 //   1. k_adapt_plan    groups the tokens by adapter (stably), a workgroup for 8192 of them (more, which k_adapt_count counts
 //                      before); other workgroups transpose the pools for the backward.  Up to kAdaptSmall tokens in the
 //                      forward, the next kernels find their tokens themselves.
-//   2. k_adapt_shrink  u or du: 16 tokens of one adapter against its r rows, the long axis over 8 waves (and ranges of it
-//                      over workgroups where there are few tokens).
+//   2. k_adapt_shrink  u or du: 16 or 32 tokens of one adapter against its r rows, the long axis over 8 waves (and ranges
+//                      of it over workgroups where there are few tokens).
 //   3. k_adapt_expand  base + u B^T (or du A): 16 or 32 tokens of one adapter, 128 columns at a time.
 //   4. k_adapt_grads   dA and dB: a piece of an adapter's tokens, 64 columns; transposed operands through LDS.
 //   5. k_adapt_reduce  sums of the pieces, in order.
@@ -319,41 +319,45 @@ __global__ __launch_bounds__(1024) void k_adapt_count(AdaptRows a) {
 __device__ __forceinline__ int chunk_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
 // --------------------------------------------------------------------- shrink
-// RT: rank tiles of 16.  Eight waves take 64-value steps of the long axis in turn.  A step's rows come in whole lines
-// (eight lanes each) and go through a part of LDS that is the wave's own: no barriers.  Straight into the MFMA's layout,
-// where neighbouring lanes are neighbouring rows, each lane is a cache access of its own, which alone took 15 of 20 us
-// (4096 tokens x 4096, ranks to 64; now 12, 2.8 TB/s of X beside the adapters' rows from the L2).  What stands in a row
-// that is none (past the rank) stays in that row's sums, which are not stored.  (Tiles of 32 tokens, which read the adapter
-// half as often: 12.4 -> 16.4 us.)
+// RT: rank tiles of 16, MT: token tiles of 16.  Eight waves take 64-value steps of the long axis in turn.  A step's rows
+// come in whole lines (eight lanes each) and go through a part of LDS that is the wave's own: no barriers.  Straight into
+// the MFMA's layout, where neighbouring lanes are neighbouring rows, each lane is a cache access of its own, which alone
+// took 15 of 20 us (4096 tokens x 4096, ranks to 64; now 12, 2.8 TB/s of X beside the adapters' rows from the L2).  What
+// stands in a row that is none (past the rank) stays in that row's sums, which are not stored.  (MT = 2 at these ranks:
+// 12.4 -> 16.4 us.)
 constexpr int kShrinkWaves = 8;
-template <int RT>
-__global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_shrink(
+template <int RT, int MT>
+__global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : MT == 1 ? 3 : 2) void k_adapt_shrink(
     AdaptRows a, const bf16_t *__restrict__ P, int64_t K, const bf16_t *__restrict__ Q, bool scaled, int ranges,
     float *__restrict__ U) {
   constexpr int LD = RT * 16 + 4, PART = RT < 2 ? RT : 2;  // rank tiles that are in LDS at once
-  constexpr int kOwn = 2048 * (1 + PART), kAll = kShrinkWaves * kOwn, kSums = kShrinkWaves * 16 * LD * 4;
+  constexpr int kOwn = 2048 * (MT + PART), kAll = kShrinkWaves * kOwn, kSums = kShrinkWaves * 16 * LD * 4;
   __shared__ __attribute__((aligned(128))) char shared[kAll > kSums ? kAll : kSums];
-  __shared__ int s_token[16];
+  __shared__ int s_token[16 * MT];
   float(*const s_sum)[16][LD] = reinterpret_cast<float(*)[16][LD]>(shared);
   const int id = blockIdx.x / ranges, range = blockIdx.x - id * ranges;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l = lane & 15;
   Tile tile;
-  int token[1];
-  if (!find_tokens<16>(a, id, &tile, token)) return;
+  int token[MT];
+  if (!find_tokens<16 * MT>(a, id, &tile, token)) return;
   const int rank = rank_of(a, tile.group);
-  if (wave == 0 && lane < 16) s_token[lane] = token[0];
-  f32x4_t acc[RT];
+  if (wave == 0 && lane < 16)
 #pragma unroll
-  for (int j = 0; j < RT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MT; ++m) s_token[16 * m + lane] = token[m];
+  f32x4_t acc[MT][RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < RT; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (rank > 0) {
     char *const own = shared + wave * kOwn;
     const int row0 = lane >> 3, chunk = lane & 7;  // of this lane's loads: rows row0 and row0 + 8 of 16
-    const bf16_t *p[2];
-    bool there[2];
+    const bf16_t *p[2 * MT];
+    bool there[2 * MT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2 * MT; ++h) {
       there[h] = row0 + 8 * h < tile.n;
-      p[h] = P + (int64_t)__builtin_amdgcn_ds_bpermute((row0 + 8 * h) * 4, token[0]) * K + chunk * 8;
+      p[h] = P + (int64_t)__builtin_amdgcn_ds_bpermute((row0 + 8 * (h & 1)) * 4, token[h >> 1]) * K + chunk * 8;
     }
     const char *q = (const char *)(Q + (int64_t)tile.group * a.r * K);
     uint32_t row[RT][2];  // bytes from the adapter's first (r K <= 2^29)
@@ -367,11 +371,11 @@ __global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_sh
     const int64_t steps = (K + 63) / 64, per = (steps + ranges - 1) / ranges;
     const int64_t first = range * per, end = first + per < steps ? first + per : steps;
     const u32x4_t zero = {0u, 0u, 0u, 0u};
-    u32x4_t pv[2], qv[RT][2];
+    u32x4_t pv[2 * MT], qv[RT][2];
     auto load = [&](int64_t k) {
       const bool in = k + chunk * 8 < K;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) pv[h] = in && there[h] ? load16(p[h] + k) : zero;
+      for (int h = 0; h < 2 * MT; ++h) pv[h] = in && there[h] ? load16(p[h] + k) : zero;
       if (k + 64 <= K) {
 #pragma unroll
         for (int j = 0; j < RT; ++j)
@@ -394,16 +398,16 @@ __global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_sh
     };
     if (wave < n) load((first + at) * 64);
     for (int i = wave; i < n; i += kShrinkWaves) {
-      u32x4_t pf[2];
+      u32x4_t pf[MT][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4_t *>(own + chunk_at(row0 + 8 * h, chunk)) = pv[h];
+      for (int h = 0; h < 2 * MT; ++h) *reinterpret_cast<u32x4_t *>(own + chunk_at(row0 + 8 * h, chunk)) = pv[h];
 #pragma unroll
       for (int j0 = 0; j0 < RT; j0 += PART) {
 #pragma unroll
         for (int j = 0; j < PART; ++j)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<u32x4_t *>(own + 2048 * (1 + j) + chunk_at(row0 + 8 * h, chunk)) = qv[j0 + j][h];
+            *reinterpret_cast<u32x4_t *>(own + 2048 * (MT + j) + chunk_at(row0 + 8 * h, chunk)) = qv[j0 + j][h];
         if (j0 + PART == RT) {  // (all of this step is on its way)
           next();
           if (i + kShrinkWaves < n) load((first + at) * 64);
@@ -411,32 +415,40 @@ __global__ __launch_bounds__(64 * kShrinkWaves, RT <= 4 ? 4 : 3) void k_adapt_sh
         wave_order();
         if (j0 == 0)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) pf[h] = *reinterpret_cast<const u32x4_t *>(own + chunk_at(l, 4 * h + g));
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              pf[m][h] = *reinterpret_cast<const u32x4_t *>(own + 2048 * m + chunk_at(l, 4 * h + g));
 #pragma unroll
         for (int j = 0; j < PART; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            acc[j0 + j] = mfma16(*reinterpret_cast<const u32x4_t *>(own + 2048 * (1 + j) + chunk_at(l, 4 * h + g)), pf[h],
-                                 acc[j0 + j]);
+          for (int h = 0; h < 2; ++h) {
+            const u32x4_t qf = *reinterpret_cast<const u32x4_t *>(own + 2048 * (MT + j) + chunk_at(l, 4 * h + g));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m][j0 + j] = mfma16(qf, pf[m][h], acc[m][j0 + j]);
+          }
         wave_order();
       }
     }
   }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < RT; ++j) *reinterpret_cast<f32x4_t *>(&s_sum[wave][l][j * 16 + 4 * g]) = acc[j];
-  __syncthreads();
   const float scale = scaled && tile.group < a.n_pool ? a.scale[tile.group] : 1.f;
-  for (int e = threadIdx.x; e < 16 * RT * 16; e += 64 * kShrinkWaves) {
-    const int n = e / (RT * 16), j = e % (RT * 16);
-    if (n >= tile.n || j >= a.r) continue;
-    float sum = 0.f;
-    if (j < rank) {
 #pragma unroll
-      for (int w = 0; w < kShrinkWaves; ++w) sum += s_sum[w][n][j];
-      sum *= scale;
+  for (int m = 0; m < MT; ++m) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < RT; ++j) *reinterpret_cast<f32x4_t *>(&s_sum[wave][l][j * 16 + 4 * g]) = acc[m][j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < 16 * RT * 16; e += 64 * kShrinkWaves) {
+      const int n = e / (RT * 16), j = e % (RT * 16);
+      if (16 * m + n >= tile.n || j >= a.r) continue;
+      float sum = 0.f;
+      if (j < rank) {
+#pragma unroll
+        for (int w = 0; w < kShrinkWaves; ++w) sum += s_sum[w][n][j];
+        sum *= scale;
+      }
+      U[((int64_t)range * a.T + s_token[16 * m + n]) * a.r + j] = sum;
     }
-    U[((int64_t)range * a.T + s_token[n]) * a.r + j] = sum;
   }
 }
 
@@ -913,12 +925,17 @@ hipError_t launch_adapt_count(const AdaptRows &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Tiles of 32 tokens, which read the adapter half as often: above rank 64, where a CU holds one workgroup either way, and
+// where there are tiles enough (8000 x 4096, rank 128 44.4 -> 29.5 us; 300 x 4096, rank 72 6.0 -> 7.2).
+static bool shrink_wide(int64_t T, int r) { return r > 64 && T >= 2048; }
+
 // Enough workgroups for the GPU, but no more partial sums than that takes, which the next product adds for each of its
 // blocks of columns (4096 x 4096: 1200 tokens, rank 64 22.7 us with three ranges, 25.5 with nine; 2048 29.3 with
 // two, 32.6 with five; 4096 42.9 with two, 44.2 with one).  Above rank 64 a CU holds one workgroup of the shrinking product,
 // and a second round of them costs as much as the first (4000 tokens, rank 128 49 us with one range, 61 with two).
 int adapt_ranges(int64_t T, int n_pool, int r, int64_t K) {
-  const int64_t tiles = (T + 15) / 16 + (n_pool < T ? n_pool : T) / 2, most = (K + 511) / 512;
+  const int m = shrink_wide(T, r) ? 32 : 16;
+  const int64_t tiles = (T + m - 1) / m + (n_pool < T ? n_pool : T) / 2, most = (K + 511) / 512;
   int64_t n = tiles < 1 ? 1 : (r > 32 ? 256 : 512) / tiles;
   if (n < 2 && r <= 64 && tiles <= 384) n = 2;
   n = n < 1 ? 1 : n > 8 ? 8 : n;
@@ -927,13 +944,16 @@ int adapt_ranges(int64_t T, int n_pool, int r, int64_t K) {
 
 hipError_t launch_adapt_shrink(const AdaptRows &a, const bf16_t *P, int64_t K, const bf16_t *Q, bool scaled, int ranges,
                                float *U, hipStream_t s) {
-  const dim3 grid((uint32_t)(most_tiles(a, 16) * ranges)), block(64 * kShrinkWaves);
-#define SHRINK(RT_) launch(k_adapt_shrink<RT_>, grid, block, 0, s, a, P, K, Q, scaled, ranges, U)
-  if (a.r <= 16) SHRINK(1);
-  else if (a.r <= 32) SHRINK(2);
-  else if (a.r <= 64) SHRINK(4);
-  else if (a.r <= 96) SHRINK(6);
-  else SHRINK(8);
+  const bool wide = shrink_wide(a.T, a.r);
+  const dim3 grid((uint32_t)(most_tiles(a, wide ? 32 : 16) * ranges)), block(64 * kShrinkWaves);
+#define SHRINK(RT_, MT_) launch(k_adapt_shrink<RT_, MT_>, grid, block, 0, s, a, P, K, Q, scaled, ranges, U)
+  if (a.r <= 16) SHRINK(1, 1);
+  else if (a.r <= 32) SHRINK(2, 1);
+  else if (a.r <= 64) SHRINK(4, 1);
+  else if (a.r <= 96 && wide) SHRINK(6, 2);
+  else if (a.r <= 96) SHRINK(6, 1);
+  else if (wide) SHRINK(8, 2);
+  else SHRINK(8, 1);
 #undef SHRINK
   return hipGetLastError();
 }
