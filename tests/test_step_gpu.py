@@ -388,3 +388,22 @@ def test_rows_beyond_four_gib():
     dW = B.embed_bwd(tokens, E, V)
     n = torch.bincount(tokens, minlength=V).double()[:, None]
     check("dW", dW, n * W.double(), (n + 2) * U * n * W.double().abs() + BF * n * W.double().abs())
+
+
+def test_few_tokens_of_a_vocabulary_beyond_eight_gib():
+    """Offsets past 2^32 elements of dW where the gradient is one launch: written with zeros, and added to."""
+    V, D = 140000, 32768
+    tokens = torch.tensor([0, V - 1, 131072, V - 1, V, 70001], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dY = torch.randn(6, D, generator=g, device="cuda").to(bf)
+    dW = torch.full((V, D), 3.0, dtype=bf, device="cuda")
+    B.embed_bwd(tokens, dY, V, dW=dW, accumulate=True)
+    rows = torch.tensor([0, V - 1, 131072, 70001], device="cuda")
+    want = torch.stack((dY[0].float(), dY[1].float() + dY[3].float(), dY[2].float(), dY[5].float()))
+    assert torch.equal(dW[rows], (3.0 + want.double()).to(bf))
+    dW[rows] = 3.0
+    assert all(bool((part == 3).all()) for part in dW.split(20000))
+    B.embed_bwd(tokens, dY, V, dW=dW)
+    assert torch.equal(dW[rows], want.to(bf))
+    dW[rows] = 0
+    assert not any(bool(part.any()) for part in dW.split(20000))
