@@ -118,8 +118,8 @@ __device__ __forceinline__ void store_sums(float *__restrict__ out, int64_t D, i
 
 // A workgroup of 1024 threads in groups of NT, each with a row at a time.  The sums of dw and db stay in registers over
 // the workgroup's rows; then the groups add theirs in LDS, one after the other, and the workgroup's go to part[block].
-// (C = 4, the longest rows: the sums do not fit the registers beside a row and come from k_norm_columns; 1024 x 32768 so
-// 86 us in all, with spilled registers 191.)
+// (C = 4, the longest rows: the sums do not fit the registers beside a row and come from k_norm_columns; 8192 x 32768
+// 515 us in all; of 1024 rows it took 86, with spilled registers 191.)
 struct NormBwd {
   const bf16_t *X, *dY;
   int64_t T, D;
