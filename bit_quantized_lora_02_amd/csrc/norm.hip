@@ -116,10 +116,6 @@ __device__ __forceinline__ void store_sums(float *__restrict__ out, int64_t D, i
   pb[1] = make_float4(db[4], db[5], db[6], db[7]);
 }
 
-// A workgroup of 1024 threads in groups of NT, each with a row at a time.  The sums of dw and db stay in registers over
-// the workgroup's rows; then the groups add theirs in LDS, one after the other, and the workgroup's go to part[block].
-// (C = 4, the longest rows: the sums do not fit the registers beside a row and come from k_norm_columns; 8192 x 32768
-// 515 us in all; of 1024 rows it took 86, with spilled registers 191.)
 struct NormBwd {
   const bf16_t *X, *dY;
   int64_t T, D;
@@ -134,6 +130,10 @@ struct BwdShared {
   float sum[2][G][2][NT / 64];
   __attribute__((aligned(16))) float part[SUMS && G > 1 ? NT * C * 16 : 4];
 };
+// A workgroup of up to 1024 threads in groups of NT, each with a row at a time.  The sums of dw and db stay in registers over
+// the workgroup's rows; then the groups add theirs in LDS, one after the other, and the workgroup's go to part[block].
+// (C = 4, the longest rows: the sums do not fit the registers beside a row and come from k_norm_columns; 8192 x 32768
+// 515 us in all; of 1024 rows it took 86, with spilled registers 191.)
 template <int NT, int C, bool F32, bool SUMS>
 __device__ __forceinline__ void norm_bwd_rows(const NormBwd &p, int64_t block, int64_t blocks, char *shared) {
   constexpr int G = 1024 / NT, WAVES = NT / 64;
@@ -269,6 +269,7 @@ __device__ __forceinline__ void norm_bwd_rows(const NormBwd &p, int64_t block, i
   for (int c = 0; c < (SUMS ? C : 0); ++c)
     if (in[c]) store_sums(out, D, d[c], dw[c], db[c]);
 }
+
 template <int NT, int C, bool F32>
 __global__ __launch_bounds__(1024 / NT * NT) void k_norm_bwd(NormBwd p) {
   __shared__ __attribute__((aligned(16))) char shared[sizeof(BwdShared<NT, C, C <= 2>)];
