@@ -848,7 +848,7 @@ __device__ __forceinline__ void grads_tile(const AdaptRows &a, const GradArgs &q
   if (block >= q.columns) return;
   Tile tile;
   if (!find_tile<true>(a, q.piece, id, &tile)) return;
-  const int rank = rank_of(a, tile.group);
+  const int rank = tile.n > 0 ? rank_of(a, tile.group) : 0;  // (without tokens: zeros, whatever the scale holds)
   const AdaptGrads &g = q.g;
   if (block < q.blocks_a)
     grad_piece<RT, false>(a, tile, rank, jb, g.dU, g.dU_ranges, 1.f, g.X, g.n_in, (int64_t)block * kGradCols, g.part_a, g.dA,

@@ -400,3 +400,23 @@ def test_large_outputs_of_odd_widths(T, N, r, off):
 @pytest.mark.parametrize("r", range(8, 129, 8))
 def test_every_rank(T, r):
     test_adapters(T, 328, 264, 3, r, "any", True)
+
+
+@pytest.mark.parametrize("T,r", [(0, 16), (40, 24), (100, 128), (700, 72), (2500, 16)])
+def test_scales_of_adapters_without_tokens(T, r):
+    """An adapter that no token names has gradients of zeros, whatever its scale holds."""
+    print(f"adapters T={T} r={r}, scales that are not finite", flush=True)
+    pool, K, N = 5, 72, 136
+    s = make(T, K, N, pool, r, "any", False, T + r)
+    s["index"] = torch.tensor([1, 3, -1], dtype=torch.int32)[torch.arange(T) % 3]
+    g = {k: v.cuda() for k, v in s.items() if v is not None}
+    call = lambda scale: B.adapters_bwd(g["X"], g["dY"], g["A"], g["B"], scale, g["index"])  # noqa: E731
+    want = call(g["scale"])
+    odd = g["scale"].clone()
+    odd[0], odd[2], odd[4] = float("nan"), float("inf"), float("-inf")
+    got = call(odd)
+    for name, x, y in zip(("dX", "dA", "dB"), got, want):
+        assert torch.equal(x, y), name
+    for a in range(pool):
+        if T == 0 or a not in (1, 3):
+            assert (got[1][a] == 0).all() and (got[2][a] == 0).all()
