@@ -151,10 +151,14 @@ __device__ __forceinline__ bool find_tokens(const AdaptRows &a, int id, Tile *ti
   return true;
 }
 
-// u as two bf16 parts, hi + lo (16 bits of it).
+// u as two bf16 parts, hi + lo (16 bits of it).  The high part stays in bf16's range, so that an infinite u is a finite part
+// and an infinite one, not two infinities of different signs.
 __device__ __forceinline__ void split8(const float u[8], u32x4_t *hi, u32x4_t *lo) {
+  constexpr float kMost = 0x1.fep127f;  // the largest bf16
   float rest[8];
-  u32x4_t h = pack8(u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rest[i] = __builtin_amdgcn_fmed3f(u[i], -kMost, kMost);
+  const u32x4_t h = pack8(rest);
   unpack8(h, rest);
 #pragma unroll
   for (int i = 0; i < 8; ++i) rest[i] = u[i] - rest[i];
@@ -762,6 +766,7 @@ __device__ __forceinline__ void grad_piece(const AdaptRows &a, const Tile &tile,
       const float u[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
       u32x4_t hi, lo;
       split8(u, &hi, &lo);
+      if (left < 32 && row >= left) hi = lo = u32x4_t{0u, 0u, 0u, 0u};  // (an infinite u times that zero row of X)
       *reinterpret_cast<u32x4_t *>(s_hi + row * LV + j0) = hi;
       *reinterpret_cast<u32x4_t *>(s_lo + row * LV + j0) = lo;
     }

@@ -490,7 +490,8 @@ int qlora_layer_norm_workspace_bytes(int64_t T, int64_t n_in, size_t *bytes);
  * binary32 (alpha_a / rank_a, say).  base [T, n_out] bf16, or NULL for zeros; Y may be base itself.  U_out [T, r]
  * binary32 receives u (zeros past the rank and where there is no adapter) for the backward, or NULL.  All device memory;
  * rank, scale and index are read by the kernels.  u is binary32 and enters its second product as two bf16 parts (off by
- * at most 2^-16 of it); the products accumulate in binary32 in a fixed order and Y is rounded once.
+ * at most 2^-16 of it; an infinite u gives what the product does, but an infinite value of B may give NaN in place of an
+ * infinity, as the parts differ in sign); the products accumulate in binary32 in a fixed order and Y is rounded once.
  * n_in, n_out % 8 == 0, 8 <= r <= QLORA_MAX_RANK with r % 8 == 0, 1 <= n_pool <= QLORA_MAX_POOL, n_pool * n_in and
  * n_pool * n_out <= 2^27, T <= 2^22, T * n_in and T * n_out < 2^32.  X, A_pool, B_pool, base, Y, U_out 16-byte aligned,
  * rank, scale, index 4-byte; outputs overlap no input except Y base.
@@ -509,7 +510,8 @@ int qlora_adapters_fwd(const qlora_bf16 *X, int64_t T, int64_t n_in, const qlora
  * U [T, r] binary32 as written by the forward, or NULL to recompute it.  base [T, n_in] bf16: the shared projection's
  * part of dX, or NULL for zeros; dX may be base itself.  dA [n_pool, r, n_in], dB [n_pool, n_out, r] bf16 are written
  * completely, with zeros past the ranks and for adapters without tokens (T = 0: everywhere).  Each of dX, dA and dB may be
- * NULL (not formed).  u and du stay binary32 and enter the products as two bf16 parts; sums run in a fixed order.
+ * NULL (not formed).  u and du stay binary32 and enter the products as two bf16 parts, as above (where an infinite value of
+ * A, X or dY may give NaN); sums run in a fixed order.
  * ws: qlora_adapters_workspace_bytes(..., 1): the tokens in groups, u and du, both pools transposed, and binary32 sums of
  * pieces of 128 to 1024 tokens.
  */

@@ -420,3 +420,78 @@ def test_scales_of_adapters_without_tokens(T, r):
     for a in range(pool):
         if T == 0 or a not in (1, 3):
             assert (got[1][a] == 0).all() and (got[2][a] == 0).all()
+
+
+def kinds(t):
+    """0: finite, 1: +inf, 2: -inf, 3: NaN."""
+    t = t.double().cpu()
+    return torch.isposinf(t) * 1 + torch.isneginf(t) * 2 + torch.isnan(t) * 3
+
+
+@pytest.mark.parametrize("T,r", [(40, 8), (60, 72), (100, 16), (128, 128), (300, 40), (700, 16), (900, 120), (2500, 32), (2600, 104)])
+def test_infinities(T, r):
+    """An infinite u or du gives what the formulas give: infinities, NaN where both signs meet, in that token's rows and
+    that adapter's gradients alone.  The tokens are the last of their groups, behind which a tile has more places."""
+    print(f"adapters T={T} r={r} infinite", flush=True)
+    pool, K, N = 4, 72, 136
+    s = make(T, K, N, pool, r, "any", False, T + r)
+    s["A"][:, :, ::2] = s["A"][:, :, ::2].abs() + 0.125
+    s["B"][:, ::2] = s["B"][:, ::2].abs() + 0.125
+    last = [int((s["index"] == a).nonzero()[-1]) for a in range(pool)]
+    g = {k: v.cuda() for k, v in s.items() if v is not None}
+    pools = (g["A"], g["B"], g["scale"], g["index"])
+    A, Bp = s["A"].double(), s["B"].double()
+    inf = float("inf")
+
+    # X of two tokens: u, Y and, with u formed again, dB
+    X, clean = g["X"].clone(), g["X"].clone()
+    for a, value in ((1, inf), (2, -inf), (3, float("nan"))):
+        X[last[a], 4], clean[last[a]] = value, 0
+    Y, u = B.adapters_fwd(X, *pools, base=g["base"])
+    want_Y, want_u = (t.clone() for t in B.adapters_fwd(clean, *pools, base=g["base"]))
+    dB = B.adapters_bwd(X, g["dY"], *pools, outs=(None, None, torch.empty_like(g["B"])))[2]
+    want_dB = B.adapters_bwd(clean, g["dY"], *pools, outs=(None, None, torch.empty_like(g["B"])))[2]
+    for a in (1, 2, 3):
+        t = last[a]
+        u_t = X[t].double().cpu() @ A[a].t().contiguous()
+        assert (kinds(u_t) == a).all() and torch.equal(kinds(u[t]), kinds(u_t))
+        assert torch.equal(kinds(Y[t]), kinds(u_t @ Bp[a].t().contiguous())), f"Y of an infinite u, adapter {a}"
+        assert (kinds(Y[t])[::2] == a).all()
+        assert torch.equal(kinds(dB[a]), kinds(s["dY"][t].double()[:, None] * u_t)), f"dB of an infinite u, adapter {a}"
+        Y[t], u[t], dB[a] = want_Y[t], want_u[t], want_dB[a]
+    assert torch.equal(Y, want_Y) and torch.equal(u, want_u) and torch.equal(dB, want_dB)
+
+    # dY of a token: du, dX and dA; a given u: dB
+    dY, clean = g["dY"].clone(), g["dY"].clone()
+    dY[last[0], 6], clean[last[0]] = -inf, 0
+    U, clean_U = want_u.clone(), want_u.clone()
+    U[last[3]], clean_U[last[3]] = inf, 0
+    got = B.adapters_bwd(g["X"], dY, *pools, U=U, base=g["dbase"])
+    want = B.adapters_bwd(g["X"], clean, *pools, U=clean_U, base=g["dbase"])
+    t = last[0]
+    du = dY[t].double().cpu() @ Bp[0]
+    assert torch.isneginf(du).all()
+    assert torch.equal(kinds(got[0][t]), kinds(du @ A[0])), "dX of an infinite du"
+    assert (kinds(got[0][t])[::2] == 2).all()
+    assert torch.equal(kinds(got[1][0]), kinds(du[:, None] * s["X"][t].double())), "dA of an infinite du"
+    t3 = last[3]
+    assert torch.equal(kinds(got[2][3]), kinds((s["dY"][t3].double() * inf)[:, None].expand(N, r))), "dB of an infinite u"
+    got[0][t], got[1][0], got[2][3], got[2][0] = want[0][t], want[1][0], want[2][3], want[2][0]
+    for name, x, y in zip(("dX", "dA", "dB"), got, want):
+        assert torch.equal(x, y), name
+
+
+@pytest.mark.parametrize("T", [3, 200, 2100])
+def test_largest_values(T):
+    """u finite and past bf16's range: 2^128 - 2^118, cancelled by the base to what its low part alone gives."""
+    K, N, r = 72, 264, 8
+    X = torch.zeros(T, K, dtype=bf, device="cuda")
+    X[:, 0], X[:, 1] = 2.0 ** 127 * (2 - 2.0 ** -7), 0.75 * 2.0 ** 120
+    A = torch.zeros(1, r, K, dtype=bf, device="cuda")
+    A[:, :, :2] = 1
+    Bp = torch.full((1, N, r), 2.0 ** -100, dtype=bf, device="cuda")
+    base = torch.full((T, N), -8 * 2.0 ** 27 * (2 - 2.0 ** -7), dtype=bf, device="cuda")
+    scale, index = torch.ones(1, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    Y, u = B.adapters_fwd(X, A, Bp, scale, index, base=base)
+    assert (u.double() == 2.0 ** 128 - 2.0 ** 118).all()
+    assert (Y == 6 * 2.0 ** 20).all()
