@@ -589,7 +589,7 @@ __device__ __forceinline__ void expand_tile(const AdaptRows &a, const ExpandArgs
       to[1] = make_float4(u[4], u[5], u[6], u[7]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] *= scale;
+    for (int i = 0; i < 8; ++i) u[i] = c * 8 + i < rank ? u[i] * scale : 0.f;  // (an infinite scale times no column)
     u32x4_t h, o;
     split8(u, &h, &o);
     *reinterpret_cast<u32x4_t *>(s_mem + swizzled(n, c)) = h;

@@ -495,3 +495,18 @@ def test_largest_values(T):
     Y, u = B.adapters_fwd(X, A, Bp, scale, index, base=base)
     assert (u.double() == 2.0 ** 128 - 2.0 ** 118).all()
     assert (Y == 6 * 2.0 ** 20).all()
+
+
+@pytest.mark.parametrize("T,r,rank", [(20, 8, 8), (200, 24, 24), (2100, 40, 3)])
+def test_infinite_scale(T, r, rank):
+    """What lies past the rank takes no part in a product with an infinite scale either."""
+    K, N = 72, 136
+    s = make(T, K, N, 2, r, "any", False, T)
+    g = {k: v.cuda() for k, v in s.items() if v is not None}
+    X, A, Bp = (g[k].abs() for k in ("X", "A", "B"))
+    ranks = torch.full((2,), rank, dtype=torch.int32, device="cuda")
+    want, _ = B.adapters_fwd(X, A, Bp, g["scale"], g["index"], rank=ranks, base=g["base"])
+    g["scale"][1] = float("inf")
+    Y, _ = B.adapters_fwd(X, A, Bp, g["scale"], g["index"], rank=ranks, base=g["base"])
+    mine = g["index"] == 1
+    assert torch.isposinf(Y[mine]).all() and torch.equal(Y[~mine], want[~mine])
