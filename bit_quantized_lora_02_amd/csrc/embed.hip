@@ -340,6 +340,7 @@ __global__ __launch_bounds__(256) void k_embed_few(const int64_t *__restrict__ t
     return;
   }
   constexpr int N = 8;  // rows in flight
+  bool mine = ADD;      // a token names this thread's row
 #pragma unroll
   for (int l = 0; l < L; ++l)
     for (uint64_t left = named[l]; left;) {
@@ -358,9 +359,10 @@ __global__ __launch_bounds__(256) void k_embed_few(const int64_t *__restrict__ t
         unpack8(x[i], y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] = of[i] == row ? sum[e] + y[e] : sum[e];
+        mine |= of[i] == row;
       }
     }
-  if (in) write_row(to, sum, scale, ADD);
+  if (in) write_row(to, sum, mine ? scale : 0.f, ADD);
 }
 
 int64_t slices_of(int64_t D) { return (D + kWaveCols - 1) / kWaveCols; }

@@ -407,3 +407,17 @@ def test_few_tokens_of_a_vocabulary_beyond_eight_gib():
     assert torch.equal(dW[rows], want.to(bf))
     dW[rows] = 0
     assert not any(bool(part.any()) for part in dW.split(20000))
+
+
+@pytest.mark.parametrize("T", [1, 64, 65, 128, 129, 3000])
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -2.0])
+def test_rows_that_no_token_names(T, scale):
+    """They are zeros of the positive sign, whatever the scale; the others are the products with it."""
+    V, D = 50, 24
+    tokens = torch.tensor([7, 20, -1, V])[torch.arange(T) % 4].cuda()
+    dY = torch.ones(T, D, dtype=bf, device="cuda")
+    dW = B.embed_bwd(tokens, dY, V, scale)
+    n = torch.bincount(tokens.cpu().clamp(-1, V) + 1, minlength=V + 2)[1:V + 1]
+    assert (dW.cpu()[n == 0].view(torch.int16) == 0).all()
+    want = (n.float() * scale).to(bf)[:, None].expand(V, D)
+    assert torch.equal(torch.nan_to_num(dW.cpu()[n > 0], nan=7.0), torch.nan_to_num(want[n > 0], nan=7.0))
