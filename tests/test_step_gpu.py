@@ -421,3 +421,23 @@ def test_rows_that_no_token_names(T, scale):
     assert (dW.cpu()[n == 0].view(torch.int16) == 0).all()
     want = (n.float() * scale).to(bf)[:, None].expand(V, D)
     assert torch.equal(torch.nan_to_num(dW.cpu()[n > 0], nan=7.0), torch.nan_to_num(want[n > 0], nan=7.0))
+
+
+@pytest.mark.parametrize("T,D,power,eps", [(5, 8, 120, 1e-5), (1000, 8, 120, 1e-5), (2100, 72, 120, 1e-5), (5, 200, 120, 1e-5),
+                                           (900, 200, 120, 1e-5), (5, 8200, 112, 1e-12), (800, 8200, 112, 1e-12),
+                                           (5, 16392, 110, 1e-12)])
+def test_layer_norm_gradient_of_large_equal_values(T, D, power, eps):
+    """Rows of one large value: mean times rstd is past binary32, the centred values are 0 and dX is finite."""
+    X = torch.full((T, D), 2.0 ** power).to(bf)
+    X[::2] *= -1
+    g = torch.Generator().manual_seed(T + D)
+    dY = torch.randn(T, D, generator=g).to(bf)
+    w = 1 + 0.3 * torch.randn(D, generator=g)
+    _, mean, rstd = B.layer_norm(X.cuda(), w.cuda(), eps=eps)
+    assert torch.equal(mean.cpu(), X[:, 0].float()) and torch.isinf(mean * rstd).all()
+    want, bounds = norm_bwd_reference(X, dY, w, mean.cpu(), rstd.cpu(), True)
+    for need in ((True, True, True), (True, False, False)):
+        got = B.layer_norm_bwd(X.cuda(), dY.cuda(), w.cuda(), mean, rstd, *need)
+        for name, x, y, e in zip(("dX", "dweight", "dbias"), got, want, bounds):
+            if x is not None:
+                check(name, x, y, e)
