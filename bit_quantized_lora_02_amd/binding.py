@@ -1007,6 +1007,8 @@ class EmbedFn(torch.autograd.Function):
 
     @classmethod
     def apply(cls, tokens, W, scale=1.0):
+        if isinstance(scale, torch.Tensor) and scale.requires_grad and torch.is_grad_enabled():
+            raise ValueError("the scale gets no gradient: detach it")
         return super().apply(tokens, W, scale)
 
     @staticmethod

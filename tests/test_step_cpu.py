@@ -134,3 +134,13 @@ def test_functions_ask_for_the_gradients_that_are_needed(monkeypatch):
     w = W.clone().requires_grad_(True)
     B.EmbedFn.apply(TOKENS, w, 2.0).sum().backward()
     assert asked.pop() == (100, 2.0) and (w.grad == 1).all()
+
+
+def test_embed_function_refuses_a_scale_that_asks_for_a_gradient(monkeypatch):
+    monkeypatch.setattr(B, "embed", lambda tokens, W, scale: W[tokens] * float(scale))
+    w, scale = W.clone().requires_grad_(True), torch.tensor(2.0, requires_grad=True)
+    with pytest.raises(ValueError, match="scale gets no gradient"):
+        B.EmbedFn.apply(TOKENS, w, scale)
+    assert B.EmbedFn.apply(TOKENS, w, scale.detach()).requires_grad
+    with torch.no_grad():
+        assert not B.EmbedFn.apply(TOKENS, w, scale).requires_grad
