@@ -1013,6 +1013,7 @@ class EmbedFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, tokens, W, scale):
+        scale = float(scale)  # (a tensor may change before the backward)
         Y = embed(tokens, W, scale)
         ctx.save_for_backward(tokens)
         ctx.n_vocab, ctx.scale = W.shape[0], scale

@@ -144,3 +144,14 @@ def test_embed_function_refuses_a_scale_that_asks_for_a_gradient(monkeypatch):
     assert B.EmbedFn.apply(TOKENS, w, scale.detach()).requires_grad
     with torch.no_grad():
         assert not B.EmbedFn.apply(TOKENS, w, scale).requires_grad
+
+
+def test_embed_function_keeps_the_forwards_scale(monkeypatch):
+    asked = []
+    monkeypatch.setattr(B, "embed", lambda tokens, W, scale: W[tokens] * float(scale))
+    monkeypatch.setattr(B, "embed_bwd", lambda tokens, dY, V, scale: asked.append(float(scale)) or torch.ones(V, 64, dtype=bf))
+    scale = torch.tensor(2.0)
+    Y = B.EmbedFn.apply(TOKENS, W.clone().requires_grad_(True), scale)
+    scale.fill_(5.0)
+    Y.sum().backward()
+    assert asked == [2.0]
