@@ -144,3 +144,28 @@ def test_function_asks_for_the_gradients_that_are_needed(monkeypatch):
     a["scale"].requires_grad_(True)
     with pytest.raises(ValueError, match="scales get no gradient"):
         B.AdaptersFn.apply(*a.values())
+
+
+@pytest.mark.parametrize("T,K,N,pool,r,kind,ranks", [(90, 72, 136, 4, 24, "any", True), (60, 40, 8, 2, 8, "runs", False)])
+def test_references_are_the_definitions_gradients(T, K, N, pool, r, kind, ranks):
+    """The formulas that the kernels are held against, entry by entry against torch's gradients of the definition in
+    binary64; values a fiftieth off are past the bounds."""
+    from test_adapters_gpu import make, reference
+    s = make(T, K, N, pool, r, kind, ranks, T)
+    # (multiples of powers of two: u is a binary32 value, as the backward takes it)
+    s["X"], s["A"] = ((s[k].float() * n).round() / n for k, n in (("X", 4), ("A", 64)))
+    want, bounds = reference(s)
+    leaves = {k: s[k].double().requires_grad_(True) for k in ("X", "A", "B")}
+    rank = s["rank"] if ranks else torch.full((pool,), r)
+    on = (torch.arange(r)[None, :] < rank[:, None]).double()
+    mine = (s["index"].long()[:, None] == torch.arange(pool)[None, :]).double()
+    u = torch.einsum("tk,ajk->taj", leaves["X"], leaves["A"]) * on * mine[:, :, None]
+    Y = torch.einsum("taj,anj->tn", u * s["scale"].double()[:, None], leaves["B"])
+    Y.backward(s["dY"].double())
+    grads = {"Y": Y + s["base"].double(), "u": u.sum(1), "dX": leaves["X"].grad + s["dbase"].double(), "dA": leaves["A"].grad,
+             "dB": leaves["B"].grad}
+    assert torch.equal(want[1], want[1].float().double())
+    for (name, x), y in zip(grads.items(), want):
+        assert (x - y).abs().max() <= 1e-11 * x.abs().max(), name
+    for x, b in ((leaves["X"].grad, bounds[2]), (leaves["A"].grad, bounds[3]), (leaves["B"].grad, bounds[4])):
+        assert ((0.02 * x).abs() > 1.1 * b)[x != 0].double().mean() > 0.5

@@ -510,3 +510,25 @@ def test_infinite_scale(T, r, rank):
     Y, _ = B.adapters_fwd(X, A, Bp, g["scale"], g["index"], rank=ranks, base=g["base"])
     mine = g["index"] == 1
     assert torch.isposinf(Y[mine]).all() and torch.equal(Y[~mine], want[~mine])
+
+
+@pytest.mark.parametrize("T,r,ranks", [(90, 24, True), (700, 72, True), (2500, 16, False)])
+def test_gradients_entry_by_entry(T, r, ranks):
+    """The gradients against torch's of the definition in binary64, u formed again by the backward."""
+    K, N, pool = 72, 136, 4
+    s = make(T, K, N, pool, r, "any", ranks, T + r)
+    leaves = {k: s[k].double().requires_grad_(True) for k in ("X", "A", "B")}
+    rank = s["rank"] if ranks else torch.full((pool,), r)
+    Y = s["base"].double()
+    for a in range(pool):
+        t, k = (s["index"] == a).nonzero()[:, 0], int(rank[a])
+        u = leaves["X"][t] @ leaves["A"][a, :k].t()
+        Y = Y.index_add(0, t, s["scale"][a].double() * (u @ leaves["B"][a, :, :k].t()))
+    Y.backward(s["dY"].double())
+    bounds = reference(s)[1]
+    g = {k: None if v is None else v.cuda() for k, v in s.items() if k != "e_dB"}
+    got = B.adapters_bwd(g["X"], g["dY"], g["A"], g["B"], g["scale"], g["index"], g["rank"], base=g["dbase"])
+    check("dX", got[0], leaves["X"].grad + s["dbase"].double(), bounds[2])
+    check("dA", got[1], leaves["A"].grad, bounds[3])
+    # (the bound of dB is that of a given u, rounded from the exact one, and what a recomputed one is off it)
+    check("dB", got[2], leaves["B"].grad, bounds[4] + 1.01 * s["e_dB"])

@@ -155,3 +155,38 @@ def test_embed_function_keeps_the_forwards_scale(monkeypatch):
     scale.fill_(5.0)
     Y.sum().backward()
     assert asked == [2.0]
+
+
+@pytest.mark.parametrize("T,D,f32", [(1, 8, True), (37, 264, True), (90, 72, False)])
+def test_norm_references_are_the_definitions_gradients(T, D, f32):
+    """The formulas that the kernels are held against, entry by entry against torch's gradients of the definition in
+    binary64; a term that is left out, or has the other sign, is past the bounds."""
+    from test_step_gpu import norm_bwd_reference, norm_inputs, norm_reference
+    X, dY, w, b = norm_inputs(T, D, f32, T + D)
+    leaves = [t.double().requires_grad_(True) for t in (X, w, b)]
+    Y = torch.nn.functional.layer_norm(leaves[0], (D,), leaves[1], leaves[2], 1e-5)
+    Y.backward(dY.double())
+    y, mean, rstd, *_ = norm_reference(X, w, b, 1e-5)
+    assert (y - Y).abs().max() <= 1e-11 * Y.abs().max()
+    want, bounds = norm_bwd_reference(X, dY, w, mean, rstd, f32)
+    for x, t in zip(want, leaves):
+        assert (x - t.grad).abs().max() <= 1e-10 * t.grad.abs().max()
+    xh = (X.double() - mean[:, None]) * rstd[:, None]
+    g, r, bound = dY.double() * w.double(), rstd[:, None], 1.1 * bounds[0]
+    one, two = r * g.mean(1, keepdim=True), r * xh * (g * xh).mean(1, keepdim=True)
+    for off in (one, two, 2 * one, 2 * two):
+        assert (off.abs() > bound).double().mean() > 0.5
+    assert ((0.02 * want[1]).abs() > 1.1 * bounds[1]).double().mean() > 0.5
+    assert ((0.02 * want[2]).abs() > 1.1 * bounds[2]).double().mean() > 0.5
+
+
+@pytest.mark.parametrize("T,V,D,kind", [(37, 50, 264, "any"), (200, 7, 8, "runs")])
+def test_embedding_reference_is_the_definitions_gradient(T, V, D, kind):
+    from test_step_gpu import embed_bwd_reference, tokens_of
+    tokens, dY = tokens_of(kind, T, V, T), torch.randn(T, D, generator=torch.Generator().manual_seed(T)).to(bf)
+    w = torch.zeros(V, D, dtype=torch.float64, requires_grad=True)
+    rows = torch.cat([w, torch.zeros(1, D, dtype=torch.float64)])[torch.where((tokens >= 0) & (tokens < V), tokens, V)]
+    (rows * 1.5).backward(dY.double())
+    dW, bound, named = embed_bwd_reference(tokens, dY, V, 1.5)
+    assert (dW - w.grad).abs().max() <= 1e-12 * w.grad.abs().max()
+    assert ((0.02 * dW).abs() > 1.1 * bound)[named].double().mean() > 0.5

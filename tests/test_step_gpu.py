@@ -441,3 +441,28 @@ def test_layer_norm_gradient_of_large_equal_values(T, D, power, eps):
         for name, x, y, e in zip(("dX", "dweight", "dbias"), got, want, bounds):
             if x is not None:
                 check(name, x, y, e)
+
+
+@pytest.mark.parametrize("T,D,f32", [(37, 264, True), (800, 1032, False), (1500, 4104, True)])
+def test_gradients_entry_by_entry(T, D, f32):
+    """The kernels' gradients against torch's of the definition in binary64.  The statistics that the kernel takes are off
+    by e_m and rel_r: xh by d = r e_m + |xh| rel_r, mean(g xh) by mean(|g| d), and dX and dweight follow."""
+    X, dY, w, b = norm_inputs(T, D, f32, T)
+    leaves = [t.double().requires_grad_(True) for t in (X, w, b)]
+    torch.nn.functional.layer_norm(leaves[0], (D,), leaves[1], leaves[2], 1e-5).backward(dY.double())
+    _, mean, rstd = B.layer_norm(X.cuda(), w.cuda(), b.cuda())
+    got = B.layer_norm_bwd(X.cuda(), dY.cuda(), w.cuda(), mean, rstd)
+    _, m, r, _, e_m, e_r = norm_reference(X, w, b, 1e-5)
+    _, bounds = norm_bwd_reference(X, dY, w, m, r, f32)
+    m, r, e_m, rel = m[:, None], r[:, None], e_m[:, None], (e_r / r + U)[:, None]
+    xh, g = (X.double() - m) * r, dY.double() * w.double()
+    d = r * e_m + xh.abs() * rel
+    more = r * (d * (g * xh).mean(1, keepdim=True).abs() + (xh.abs() + d) * (g.abs() * d).mean(1, keepdim=True))
+    more = (more + rel * leaves[0].grad.abs()) * 1.01, (dY.double().abs() * d).sum(0), 0.0
+    for name, x, t, e, f in zip(("dX", "dweight", "dbias"), got, leaves, bounds, more):
+        check(name, x, t.grad, e + f)
+    V = 50
+    tokens = tokens_of("runs", T, V, T)
+    W = torch.zeros(V + 1, D, dtype=torch.float64, requires_grad=True)
+    (W[torch.where((tokens >= 0) & (tokens < V), tokens, V)] * 1.5).backward(dY.double())
+    check("dW", B.embed_bwd(tokens.cuda(), dY.cuda(), V, 1.5), W.grad[:V], embed_bwd_reference(tokens, dY, V, 1.5)[1])
