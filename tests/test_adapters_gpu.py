@@ -532,3 +532,37 @@ def test_gradients_entry_by_entry(T, r, ranks):
     check("dA", got[1], leaves["A"].grad, bounds[3])
     # (the bound of dB is that of a given u, rounded from the exact one, and what a recomputed one is off it)
     check("dB", got[2], leaves["B"].grad, bounds[4] + 1.01 * s["e_dB"])
+
+
+@pytest.mark.parametrize("T", [48, 700])
+def test_function_captured(T):
+    """Forward and backward of AdaptersFn in one graph, replayed on new inputs with eager work between."""
+    s = make(T, 264, 520, 6, 32, "any", True, 12)
+    c = {k: v.cuda() for k, v in s.items() if v is not None}
+    leaves = [c[k].requires_grad_(True) for k in ("X", "A", "B", "base")]
+
+    def step(X, A, Bp, base):
+        Y = B.AdaptersFn.apply(X, A, Bp, c["scale"], c["index"], c["rank"], base)
+        return (Y.detach(), *torch.autograd.grad(Y, (X, A, Bp, base), c["dY"]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*leaves)
+    for i in range(4):
+        with torch.no_grad():
+            for t in (c["dY"], *leaves):
+                t.normal_()
+        c["index"].random_(-1, 6)
+        c["rank"].random_(0, 33)
+        want = step(*(t.detach().clone().requires_grad_(True) for t in leaves))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, p, q in zip(("Y", "dX", "dA", "dB", "dbase"), out, want):
+            assert torch.equal(p, q), f"{name} of replay {i}"

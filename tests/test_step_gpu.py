@@ -466,3 +466,37 @@ def test_gradients_entry_by_entry(T, D, f32):
     W = torch.zeros(V + 1, D, dtype=torch.float64, requires_grad=True)
     (W[torch.where((tokens >= 0) & (tokens < V), tokens, V)] * 1.5).backward(dY.double())
     check("dW", B.embed_bwd(tokens.cuda(), dY.cuda(), V, 1.5), W.grad[:V], embed_bwd_reference(tokens, dY, V, 1.5)[1])
+
+
+def test_functions_captured():
+    """Forward and backward of EmbedFn and LayerNormFn in one graph, replayed on new inputs with eager work between."""
+    T, D, V = 900, 520, 700
+    X, dY, w, b = (t.cuda() for t in norm_inputs(T, D, True, 2))
+    tokens = torch.randint(-5, V, (T,), device="cuda")
+    table = torch.randn(V, D, device="cuda").to(bf)
+    leaves = [t.requires_grad_(True) for t in (table, w, b)]
+
+    def step(table, w, b):
+        Y = B.LayerNormFn.apply(B.EmbedFn.apply(tokens, table, 2.0), w, b)
+        return (Y.detach(), *torch.autograd.grad(Y, (table, w, b), dY))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*leaves)
+    for i in range(4):
+        with torch.no_grad():
+            for t in (dY, *leaves):
+                t.normal_()
+        tokens.random_(-5, V)
+        want = step(*(t.detach().clone().requires_grad_(True) for t in leaves))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, p, q in zip(("Y", "dW", "dweight", "dbias"), out, want):
+            assert torch.equal(p, q), f"{name} of replay {i}"
