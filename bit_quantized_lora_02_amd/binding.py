@@ -1002,6 +1002,9 @@ class HeadDistillFn(torch.autograd.Function):
 class EmbedFn(torch.autograd.Function):
     """Autograd wrapper of ``embed``: forward(tokens, W, scale) -> Y; the gradient of W is dense.
 
+    Of a W that is the output layer too, autograd adds the two dense gradients in bf16, one more pass and rounding;
+    ``embed_bwd`` with ``accumulate``, after the loss has written its dW, has neither.
+
     This and the next two can be captured into a HIP graph, forward and backward, where no eager graph of the same leaves is
     alive."""
 

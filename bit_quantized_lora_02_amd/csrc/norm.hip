@@ -6,7 +6,8 @@
 //
 // Each kernel reads its rows once and keeps a row in registers between the two sums and the output, so both directions
 // are bound by HBM (forward 8192 x 8192 50 us, 5.4 TB/s; backward 4096 x 4096 20 us, 5.0 TB/s, and 4 us for the weights'
-// sums).  The variance is taken from the centred row (no difference of large sums).  All sums are binary32 in
+// sums).  (The forward of more than 24576 columns has no registers for all of its weights and bias: 68 bytes a thread of
+// binary32 ones, 52 of bf16, are in scratch memory; 4096 x 32768 122 and 112 us, 4.4 and 4.8 TB/s, 4096 x 24576 76, 5.3.)  The variance is taken from the centred row (no difference of large sums).  All sums are binary32 in
 // a fixed order; bf16 outputs are rounded once.  Workgroups are persistent: they hold the weights (and, backward, the
 // running sums of dw and db) of their columns in registers over all of their rows, and load the next row while the
 // present one is reduced.  Of few rows the backward reads X and dY twice, from the caches, and is one launch.
@@ -456,8 +457,10 @@ hipError_t launch_norm_bwd(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t
   return hipGetLastError();
 }
 
-// 1024 x 4096 11.6 us so, else 14.0, but 1001 x 5992, whose rows do not begin with a line of memory, 18.5 and 17.1; 768 x
-// 4096 10.6 and 13.5.  2048 x 32768 115 us, with k_norm_columns 146; 8192 x 24576 390 and 376.
+// Up to 768 rows one launch gains at every width (768 x 4096 10.5 us, else 13.3; x 5992 14.2 and 16.3; x 16384 24.9 and
+// 26.5).  At 1024 rows the second reads cost more than the launches where rows do not begin with a line of memory or are long
+// (x 5992 17.8 and 17.0, x 8192 18.5 and 18.4, x 16384 32.0 and 30.9); rows of up to 4096 columns would still gain (12.0 and
+// 14.1).  2048 x 32768 117 us, with k_norm_columns 146; 8192 x 24576 390 and 379.
 bool norm_bwd_few(int64_t T, int64_t D) { return T <= (norm_bwd_columns(D) ? 2048 : 768); }
 
 hipError_t launch_norm_few(const bf16_t *X, const bf16_t *dY, int64_t T, int64_t D, const void *w, bool f32,
